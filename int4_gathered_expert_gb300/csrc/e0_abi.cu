@@ -51,6 +51,35 @@ int check_head(const e0_prerouter* h) {
     return E0_OK;
 }
 
+inline bool float_type(int t) { return t == E0_F32 || t == E0_F16 || t == E0_BF16; }
+inline int elem_bytes(int t) { return t == E0_F32 ? 4 : t == E0_E4M3 ? 1 : 2; }
+// Whether every pointer (NULL counts) is aligned to `a` bytes.
+template <typename... P>
+bool aligned(size_t a, const P*... p) {
+    return (((uintptr_t)p | ...) & (a - 1)) == 0;
+}
+
+inline bool block_tokens_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+
+int check_kv_cache(const e0_kv_cache* c) {
+    if (!c) return E0_ERR_NULL;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return E0_ERR_NULL;
+    if (c->n_blocks < 1 || c->Hkv < 1) return E0_ERR_ARG;
+    if (!block_tokens_ok(c->block_tokens) || (c->D != 64 && c->D != 128 && c->D != 256)) return E0_ERR_UNSUPPORTED;
+    if (!aligned(16, c->k, c->v) || !aligned(4, c->k_scale, c->v_scale)) return E0_ERR_ARG;
+    return E0_OK;
+}
+
+int check_kv_state(const e0_kv_state* s, const int32_t* ctx_out, const int32_t* free_out) {
+    if (!s) return E0_ERR_NULL;
+    if (s->B < 0 || s->max_blocks < 1 || s->n_blocks < 1 || !block_tokens_ok(s->block_tokens)) return E0_ERR_ARG;
+    if (s->B > E0_MAX_SEQS) return E0_ERR_UNSUPPORTED;
+    if (!s->free_list || !s->free_count || !free_out) return E0_ERR_NULL;
+    if (s->B > 0 && (!s->block_table || !s->ctx_len || !ctx_out)) return E0_ERR_NULL;
+    if (!aligned(4, s->block_table, s->ctx_len, s->free_list, s->free_count, ctx_out, free_out)) return E0_ERR_ARG;
+    return E0_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -304,6 +333,108 @@ int e0_stack_prefetch_experts_cached(void* ws, int layer, int t_next, const e0_s
         (cache->capacity > 0 && !cache->data))
         return E0_ERR_NULL;
     return e0::stack_prefetch_experts_cached(ws, layer, t_next, pool, bank, cache, d_status, cs(stream));
+}
+
+int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, int dtype, float eps, int64_t r_ld,
+                  int64_t d_ld, void* r_out, void* h, uint8_t* q, float* q_scale, uint32_t* d_status,
+                  e0_stream_t stream) {
+    if (T < 0 || H < 1 || !float_type(dtype) || !(eps >= 0.f)) return E0_ERR_ARG;
+    if (H > E0_MAX_NORM_H) return E0_ERR_UNSUPPORTED;
+    if (T == 0) return E0_OK;
+    if (!r || (!r_out && !h && !q) || (q == nullptr) != (q_scale == nullptr)) return E0_ERR_NULL;
+    if (r_ld < H || (d && d_ld < H)) return E0_ERR_ARG;
+    if (!aligned(elem_bytes(dtype), r, d, r_out, h) || !aligned(4, w, q_scale)) return E0_ERR_ARG;
+    // in place only where a thread's own elements stay its own
+    if (h && (h == r_out || h == r || h == d)) return E0_ERR_ARG;
+    if ((r_out == r && r_ld != H) || (r_out && r_out == d && d_ld != H)) return E0_ERR_ARG;
+    return e0::rmsnorm_q8(r, d, w, T, H, dtype, eps, r_ld, d_ld, r_out, h, q, q_scale, d_status, cs(stream));
+}
+
+size_t e0_linear_bytes(int N, int K) {
+    if (N < 1 || K < 1 || K % 64 != 0) return 0;
+    return e0::linear_bytes(N, K);
+}
+
+int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_t stream) {
+    if (!src || !src->codes || !src->scale || !src->bias || !dst) return E0_ERR_NULL;
+    if (N < 1 || K < 1 || K % 64 != 0) return E0_ERR_ARG;
+    if (!aligned(16, dst) || !aligned(2, src->scale, src->bias)) return E0_ERR_ARG;
+    return e0::pack_linear(src, N, K, dst, cs(stream));
+}
+
+int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type, int64_t x_ld, const float* x_scale,
+                      int T, const void* add, int64_t add_ld, void* y, int y_type, int64_t y_ld, e0_stream_t stream) {
+    if (T < 0 || N < 1 || K < 1 || K % 64 != 0) return E0_ERR_ARG;
+    if (!(float_type(x_type) || x_type == E0_E4M3) || !float_type(y_type)) return E0_ERR_ARG;
+    if (T > E0_MAX_T_LINEAR) return E0_ERR_UNSUPPORTED;
+    if (T == 0) return E0_OK;
+    if (!w || !x || !y || (x_type == E0_E4M3 && !x_scale)) return E0_ERR_NULL;
+    if (x_ld < K || y_ld < N || (add && add_ld < N)) return E0_ERR_ARG;
+    if (!aligned(16, w) || !aligned(elem_bytes(x_type), x) || !aligned(elem_bytes(y_type), y, add) ||
+        !aligned(4, x_scale))
+        return E0_ERR_ARG;
+    if (add == y && add_ld != y_ld) return E0_ERR_ARG;
+    return e0::linear_forward(w, N, K, x, x_type, x_ld, x_scale, T, add, add_ld, y, y_type, y_ld, cs(stream));
+}
+
+int e0_kv_plan(const e0_kv_state* state, const int32_t* new_len, int T_cap, int32_t* ctx_out, int32_t* free_out,
+               int32_t* cu_q, int64_t* slots, int32_t* positions, int32_t* seq_ids, uint32_t* d_status,
+               e0_stream_t stream) {
+    const int rc = check_kv_state(state, ctx_out, free_out);
+    if (rc) return rc;
+    if (T_cap < 0) return E0_ERR_ARG;
+    if (!cu_q || (state->B > 0 && !new_len) || (T_cap > 0 && !slots)) return E0_ERR_NULL;
+    if (!aligned(4, new_len, cu_q, positions, seq_ids) || !aligned(8, slots)) return E0_ERR_ARG;
+    return e0::kv_plan(state, new_len, T_cap, ctx_out, free_out, cu_q, slots, positions, seq_ids, d_status, cs(stream));
+}
+
+int e0_kv_release(const e0_kv_state* state, const uint8_t* mask, int32_t* ctx_out, int32_t* free_out,
+                  uint32_t* d_status, e0_stream_t stream) {
+    const int rc = check_kv_state(state, ctx_out, free_out);
+    if (rc) return rc;
+    if (state->B > 0 && !mask) return E0_ERR_NULL;
+    return e0::kv_release(state, mask, ctx_out, free_out, d_status, cs(stream));
+}
+
+int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dtype, int64_t k_ld, int64_t v_ld,
+                 const int64_t* slots, int T, uint32_t* d_status, e0_stream_t stream) {
+    const int rc = check_kv_cache(cache);
+    if (rc) return rc;
+    if (T < 0 || !float_type(dtype)) return E0_ERR_ARG;
+    if ((int64_t)T * 2 * cache->Hkv > (int64_t)1 << 33) return E0_ERR_UNSUPPORTED;  // the grid of warps
+    if (T == 0) return E0_OK;
+    if (!k || !v || !slots) return E0_ERR_NULL;
+    const int64_t row = (int64_t)cache->Hkv * cache->D;
+    if (k_ld < row || v_ld < row) return E0_ERR_ARG;
+    if (!aligned(elem_bytes(dtype), k, v) || !aligned(8, slots)) return E0_ERR_ARG;
+    return e0::kv_append(cache, k, v, dtype, k_ld, v_ld, slots, T, d_status, cs(stream));
+}
+
+size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q) {
+    if (B < 1 || B > E0_MAX_SEQS || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || max_q < 1) return 0;
+    if (D != 64 && D != 128 && D != 256) return 0;
+    return e0::attn_ws_bytes(D);
+}
+
+int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
+                   const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
+                   int window, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes, uint32_t* d_status,
+                   e0_stream_t stream) {
+    const int rc = check_kv_cache(cache);
+    if (rc) return rc;
+    if (B < 0 || max_blocks < 1 || max_q < 1 || !float_type(dtype) || window < 0) return E0_ERR_ARG;
+    if (Hq < cache->Hkv || Hq % cache->Hkv != 0 || !(scale == scale)) return E0_ERR_ARG;
+    if (!cu_q && max_q != 1) return E0_ERR_ARG;
+    if (B > E0_MAX_SEQS || (int64_t)max_q * Hq > (int64_t)1 << 30) return E0_ERR_UNSUPPORTED;
+    if (B == 0) return E0_OK;
+    if (!block_table || !ctx_len || !q || !out || !ws) return E0_ERR_NULL;
+    const int64_t row = (int64_t)Hq * cache->D;
+    if (q_ld < row || out_ld < row) return E0_ERR_ARG;
+    if (!aligned(16, q) || (q_ld * elem_bytes(dtype)) % 16 != 0 || !aligned(elem_bytes(dtype), out)) return E0_ERR_ARG;
+    if (!aligned(4, block_table, ctx_len, cu_q, lse) || !aligned(256, ws)) return E0_ERR_ARG;
+    if (ws_bytes < e0::attn_ws_bytes(cache->D)) return E0_ERR_ARG;
+    return e0::attn_decode(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale, window,
+                           out, out_ld, lse, ws, d_status, cs(stream));
 }
 
 int e0_selftest_bounded_wait(const uint32_t* flag, uint32_t limit_us, uint32_t* d_status, e0_stream_t stream) {

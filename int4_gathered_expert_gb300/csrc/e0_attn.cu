@@ -1,0 +1,474 @@
+// Attention of decode queries over the paged 8-bit KV cache (e0_attn_decode).
+#include <cuda_runtime.h>
+
+#include "e0_internal.h"
+#include "e0_types.cuh"
+
+namespace e0 {
+namespace {
+
+// out = softmax(scale q K^T) V in one pass over the context with the running
+// maximum and sum.  A job is one (sequence, KV head, 8 query rows): the rows are
+// the query heads of the group and the sequence's new tokens, token major.  A
+// job's context is cut into units of 64 positions, and the units of all jobs,
+// one after another, are dealt out evenly to the thread blocks: every block
+// reads the same number of bytes whatever the lengths are.  A job that ends up on
+// several blocks leaves one partial result (maximum, sum, unscaled output) on
+// each, at most two a block, and k_attn_join adds them in order.
+//
+// In a block, warp w takes positions 16w..16w+15 of every unit.  Products run
+// on the tensor cores (16 x 8 x 16, fp16 operands, fp32 accumulation).  e4m3
+// codes widen to fp16 exactly.  The 16 operand rows hold the 8 query rows twice:
+// rows 0..7 the fp16 part, rows 8..15 the rest of the value, so neither q nor the
+// probabilities lose bits that matter (22 significant bits), at no cost: a
+// decode step has few rows and the kernel is bound by reading the cache.
+// Operand layouts are chosen so that every lane loads 16 bytes at a time straight
+// from the cache: the order of D inside the first product and of the output
+// columns in the second are permuted (the same permutation on both operands).
+// The scale of a block of keys multiplies the scores; that of the values goes into
+// the probabilities relative to the largest one seen (a running reference
+// like the maximum's), so that they stay in fp16's range.
+
+constexpr int UNIT = 64;
+constexpr int ROWS = 8;
+constexpr int AT_WARPS = 4;
+
+struct AttnArgs {
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* ks;
+    const float* vs;
+    const int32_t* table;
+    const int32_t* ctx;
+    const int32_t* cu;
+    const void* q;
+    void* out;
+    float* lse;
+    float* part_o;    // [2 * blocks][ROWS][D]
+    float2* part_ml;  // [2 * blocks][ROWS]
+    uint32_t* st;
+    int64_t q_ld, out_ld;
+    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks;
+    float scale;
+};
+
+// One sequence as the schedule sees it.
+struct Seq {
+    int row0, n, ctx, first;  // first query row, queries, cached tokens, first unit that anyone sees
+    int units, tiles;         // units of context, tiles of 8 rows per KV head
+};
+
+E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
+    Seq s;
+    s.row0 = A.cu ? A.cu[b] : b;
+    s.n = A.cu ? A.cu[b + 1] - s.row0 : 1;
+    s.ctx = A.ctx[b];
+    bool bad = false;
+    if (s.row0 < 0 || s.n < 0 || s.n > A.max_q) bad = true, s.n = 0;
+    if (s.ctx < 0 || (long long)s.ctx > ((long long)A.max_blocks << A.shift)) bad = true, s.ctx = 0;
+    if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
+    const int low = s.ctx - s.n + 1 - A.window;  // the first position that the first query sees
+    s.first = A.window > 0 && low > 0 ? low / UNIT : 0;
+    s.units = (s.ctx + UNIT - 1) / UNIT - s.first;
+    if (s.units < 1) s.units = 1;  // a job without context still writes its rows
+    const int G = A.Hq / A.Hkv;
+    s.tiles = (int)(((long long)s.n * G + ROWS - 1) / ROWS);
+    return s;
+}
+
+// First unit of every sequence's jobs, in shared memory; the total.
+E0_DEV long long schedule(const AttnArgs& A, long long* first, long long* red, bool tell) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int per = (A.B + blockDim.x - 1) / blockDim.x, b0 = threadIdx.x * per;
+    long long sum = 0;
+    for (int i = 0; i < per && b0 + i < A.B; ++i) {
+        const Seq s = seq_of(A, b0 + i, tell);
+        sum += (long long)s.units * s.tiles * A.Hkv;
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) red[warp] = inc;
+    __syncthreads();
+    long long base = 0, total = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i < warp) base += red[i];
+        total += red[i];
+    }
+    long long at = base + inc - sum;
+    for (int i = 0; i < per && b0 + i < A.B; ++i) {
+        const Seq s = seq_of(A, b0 + i, false);
+        first[b0 + i] = at;
+        at += (long long)s.units * s.tiles * A.Hkv;
+    }
+    if (threadIdx.x == 0) first[A.B] = total;
+    __syncthreads();
+    return total;
+}
+
+// Units of a block: the same for all, at least 2 (a join costs more than a unit).
+E0_DEV long long units_per_block(const AttnArgs& A, long long total) {
+    const long long per = (total + A.blocks - 1) / A.blocks;
+    return per < 2 ? 2 : per;
+}
+
+struct Job {
+    Seq s;
+    int head, tile;
+    long long first;  // its first unit among all
+    int seq;
+};
+
+E0_DEV Job job_at(const AttnArgs& A, const long long* first, long long unit) {
+    int lo = 0, hi = A.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= unit) lo = mid; else hi = mid;
+    }
+    Job j;
+    j.seq = lo;
+    j.s = seq_of(A, lo, false);
+    const int k = (int)((unit - first[lo]) / j.s.units);
+    j.head = k / j.s.tiles;
+    j.tile = k % j.s.tiles;
+    j.first = first[lo] + (long long)k * j.s.units;
+    return j;
+}
+
+// Two e4m3 codes -> an fp16 pair times 2^-8, exact (NaN codes read as +-480 *
+// 2^-8, so what a masked place holds cannot spread): sel picks each code's byte and
+// eight copies of its sign, the shift moves exponent and mantissa to where fp16
+// has them, and the mask leaves one sign.
+E0_DEV uint32_t widen(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t p;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(a), "r"(b), "r"(sel));
+    return (p << 7) & 0xBF80BF80u;
+}
+
+E0_DEV void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+E0_DEV uint32_t half2_of(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The fp16 part of a pair and what it leaves.
+E0_DEV void split_half(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    const float2 f = __half22float2(h);
+    lo = half2_of(a - f.x, b - f.y);
+}
+
+E0_DEV float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+E0_DEV float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+template <int D>
+struct AttnSmem {
+    float o[AT_WARPS][ROWS][D + 4];
+    float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS], r[AT_WARPS];
+    uint32_t q[D / 16][32][4];
+    float f[ROWS];
+    long long red[AT_WARPS];
+};
+
+template <int TY>
+E0_DEV void store_out(const AttnArgs& A, size_t row, int i, float v) {
+    typedef typename Elem<TY>::T T;
+    reinterpret_cast<T*>(A.out)[row * A.out_ld + i] = Elem<TY>::put(v);
+}
+
+template <int D, int TY>
+__global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
+    typedef typename Elem<TY>::T T;
+    extern __shared__ __align__(16) char attn_sm[];
+    AttnSmem<D>& S = *reinterpret_cast<AttnSmem<D>*>(attn_sm);
+    long long* first = reinterpret_cast<long long*>(attn_sm + sizeof(AttnSmem<D>));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t4 = lane & 3;
+    const long long total = schedule(A, first, S.red, blockIdx.x == 0);
+    const long long per = units_per_block(A, total);
+    long long u = blockIdx.x * per;
+    const long long u1 = u + per < total ? u + per : total;
+    const int G = A.Hq / A.Hkv, bs = 1 << A.shift;
+    constexpr int KC = D / 64;          // 16-byte chunks of a key row a lane reads
+    constexpr int NT = D / 8;           // output tiles
+    constexpr int VC = D >= 128 ? D / 128 : 1;  // 16-byte chunks of a value row
+
+    while (u < u1) {
+        const Job j = job_at(A, first, u);
+        const int c0 = (int)(u - j.first);
+        const int c1 = (int)(min(j.first + j.s.units, u1) - j.first);
+        // ---- the job's queries as operand fragments: warps share them through shared memory
+        const int rr = j.tile * ROWS + gid;  // this lane's query row
+        const bool row_ok = rr < j.s.n * G;
+        const int qi = rr / G;
+        const int hq = j.head * G + rr % G;
+        const int last = j.s.ctx - j.s.n + qi;  // the last position that the row sees
+        const int low = A.window > 0 ? last - A.window + 1 : 0;
+        __syncthreads();  // the former job's shared memory has been read
+        if (warp == 0) {
+            float x[KC][16];
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                if (row_ok) {
+                    load_vec<TY, 16>(reinterpret_cast<const T*>(A.q) + (size_t)(j.s.row0 + qi) * A.q_ld + (size_t)hq * D +
+                                         64 * c + 16 * t4, x[c]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[c][i]) & 0x7FFFFFFFu);
+            }
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // rows go in times a power of two that brings the largest near 1
+            int e = (int)(m >> 23);
+            e = e < 27 ? 27 : e > 253 ? 253 : e;
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a[4];
+                    split_half(x[c][4 * i] * down, x[c][4 * i + 1] * down, a[0], a[1]);
+                    split_half(x[c][4 * i + 2] * down, x[c][4 * i + 3] * down, a[2], a[3]);
+                    *reinterpret_cast<uint4*>(S.q[4 * c + i][lane]) = make_uint4(a[0], a[1], a[2], a[3]);
+                }
+            // what the product lacks: the power of two, the codes' 2^8, the scale, log2 e
+            if (t4 == 0)
+                S.f[gid] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                            : __uint_as_float((uint32_t)e << 23) * 256.f * A.scale * LOG2E;
+        }
+        __syncthreads();
+        const float f = S.f[gid];
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        float mx = -INFINITY, sum = 0.f, ref = 0.f;  // ref: the largest value scale so far
+
+        for (int c = c0; c < c1; ++c) {
+            const int pos = (j.s.first + c) * UNIT + 16 * warp;
+            if (pos >= j.s.ctx) continue;
+            const int id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
+            if (id < 0 || id >= A.n_blocks) {
+                if (lane == 0) set_status(A.st, E0_ST_BAD_BLOCK);
+                continue;
+            }
+            const size_t at = (((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1));
+            const uint8_t* kp = A.k + at * D;
+            const uint8_t* vp = A.v + at * D;
+            const float ksc = A.ks[(size_t)id * A.Hkv + j.head], vsc = A.vs[(size_t)id * A.Hkv + j.head];
+            uint4 kw[2][KC];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < KC; ++i)
+                    kw[h][i] = ldg_stream(kp + (size_t)(8 * h + gid) * D + 64 * i + 16 * t4);
+            uint4 vw[VC][4];  // tokens 2t, 2t+1, 8+2t, 9+2t
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* p = vp + (size_t)(2 * t4 + (i & 1) + 8 * (i >> 1)) * D;
+                if constexpr (D == 64) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p + 8 * gid));
+                    vw[0][i] = make_uint4(x.x, x.y, 0, 0);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < VC; ++h) vw[h][i] = ldg_stream(p + 128 * h + 16 * gid);
+                }
+            }
+            float s[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KC; ++i) {
+                    const uint32_t w[4] = {kw[h][i].x, kw[h][i].y, kw[h][i].z, kw[h][i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 a = *reinterpret_cast<const uint4*>(S.q[4 * i + k][lane]);
+                        mma(s[h], a.x, a.y, a.z, a.w, widen(w[k], 0, 0x9180), widen(w[k], 0, 0xB3A2));
+                    }
+                }
+            }
+            // scores in units of log2, masked; this lane: row gid, tokens 8h + 2t, + 1
+            float p[2][2], top = -INFINITY;
+            const float fk = f * ksc;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at_pos = pos + 8 * h + 2 * t4 + i;
+                    const bool seen = row_ok && at_pos <= last && at_pos >= low;
+                    p[h][i] = seen ? (s[h][i] + s[h][2 + i]) * fk : -INFINITY;
+                    top = fmaxf(top, p[h][i]);
+                }
+            top = fmaxf(mx, quad_max(top));
+            const float base = top == -INFINITY ? 0.f : top;
+            const float shrink = exp2f(mx - base);
+            mx = top;
+            const float ref1 = fmaxf(ref, vsc);
+            const float keep = ref1 > 0.f ? shrink * (ref / ref1) : shrink;
+            const float vrel = ref1 > 0.f ? vsc / ref1 : 0.f;
+            ref = ref1;
+            sum *= shrink;
+            uint32_t ph[2], pl[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                p[h][0] = exp2f(p[h][0] - base);
+                p[h][1] = exp2f(p[h][1] - base);
+                sum += p[h][0] + p[h][1];
+                split_half(p[h][0] * vrel, p[h][1] * vrel, ph[h], pl[h]);
+            }
+            if (__any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][0] *= keep, acc[n][1] *= keep, acc[n][2] *= keep, acc[n][3] *= keep;
+            }
+#pragma unroll
+            for (int h = 0; h < VC; ++h) {
+                const uint32_t w[4][4] = {{vw[h][0].x, vw[h][0].y, vw[h][0].z, vw[h][0].w},
+                                          {vw[h][1].x, vw[h][1].y, vw[h][1].z, vw[h][1].w},
+                                          {vw[h][2].x, vw[h][2].y, vw[h][2].z, vw[h][2].w},
+                                          {vw[h][3].x, vw[h][3].y, vw[h][3].z, vw[h][3].w}};
+#pragma unroll
+                for (int n = 0; n < (D == 64 ? 8 : 16); ++n) {
+                    const uint32_t sel = 0xC480u + 0x1111u * (n & 3);  // byte and sign of a's and b's n-th code
+                    mma(acc[16 * h + n], ph[0], pl[0], ph[1], pl[1], widen(w[0][n / 4], w[1][n / 4], sel),
+                        widen(w[2][n / 4], w[3][n / 4], sel));
+                }
+            }
+        }
+        // ---- the warps' results together
+        sum = quad_sum(sum);
+        if (t4 == 0) S.m[warp][gid] = mx, S.l[warp][gid] = sum;
+        if (lane == 0) S.r[warp] = ref * 256.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            // tile n, columns 2t and 2t+1: elements 16 * column + n % 16 of its 128 (8 * column + n of 64)
+            const int d0 = D == 64 ? 16 * t4 + n : 128 * (n / 16) + 32 * t4 + n % 16;
+            S.o[warp][gid][d0] = acc[n][0] + acc[n][2];
+            S.o[warp][gid][d0 + (D == 64 ? 8 : 16)] = acc[n][1] + acc[n][3];
+        }
+        __syncthreads();
+        const bool whole = c0 == 0 && c1 == j.s.units;
+        const int slot = 2 * blockIdx.x + (c0 == 0 ? 1 : 0);  // a job that began before this block: its first slot
+        for (int e = threadIdx.x; e < ROWS * D; e += AT_WARPS * 32) {
+            const int r = e / D, d = e % D, row = j.tile * ROWS + r;
+            if (row >= j.s.n * G) break;
+            float m = S.m[0][r];
+#pragma unroll
+            for (int w = 1; w < AT_WARPS; ++w) m = fmaxf(m, S.m[w][r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            float o = 0.f, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < AT_WARPS; ++w) {
+                const float k = exp2f(S.m[w][r] - base);
+                l += k * S.l[w][r];
+                o += k * S.r[w] * S.o[w][r][d];
+            }
+            if (whole) {
+                const size_t tok = (size_t)j.s.row0 + row / G;
+                const int head = j.head * G + row % G;
+                store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
+                if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * LN2 : -INFINITY;
+            } else {
+                A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
+                if (d == 0) A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
+            }
+        }
+        u = j.first + c1;
+    }
+}
+
+// A block boundary that falls inside a job, the first one in it: join the job's
+// partial results, one row a block (y).
+template <int D, int TY>
+__global__ void __launch_bounds__(D) k_attn_join(AttnArgs A) {
+    extern __shared__ __align__(16) char join_sm[];
+    long long* first = reinterpret_cast<long long*>(join_sm);
+    __shared__ long long red[D / 32];
+    const long long total = schedule(A, first, red, false);
+    const long long per = units_per_block(A, total);
+    const long long edge = (blockIdx.x + 1) * per;
+    if (edge >= total) return;
+    const Job j = job_at(A, first, edge);
+    const int G = A.Hq / A.Hkv, r = blockIdx.y, row = j.tile * ROWS + r;
+    if (j.first == edge || j.first < edge - per || row >= j.s.n * G) return;
+    const int b1 = (int)((j.first + j.s.units - 1) / per);
+    float m = -INFINITY;
+    for (int b = blockIdx.x; b <= b1; ++b) m = fmaxf(m, A.part_ml[(size_t)(2 * b + (b == blockIdx.x)) * ROWS + r].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float o = 0.f, l = 0.f;
+    for (int b = blockIdx.x; b <= b1; ++b) {
+        const size_t at = (size_t)(2 * b + (b == blockIdx.x)) * ROWS + r;
+        const float2 ml = A.part_ml[at];
+        const float k = exp2f(ml.x - base);
+        l += k * ml.y;
+        o += k * A.part_o[at * D + threadIdx.x];
+    }
+    const size_t tok = (size_t)j.s.row0 + row / G;
+    const int head = j.head * G + row % G;
+    store_out<TY>(A, tok, head * D + threadIdx.x, l > 0.f || l != l ? o / l : 0.f);
+    if (A.lse && threadIdx.x == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * LN2 : -INFINITY;
+}
+
+constexpr int BLOCKS_PER_SM = 2;
+
+template <int D, int TY>
+int launch(AttnArgs a, cudaStream_t s) {
+    const size_t sched = (size_t)(a.B + 1) * sizeof(long long);
+    const size_t sm = sizeof(AttnSmem<D>) + sched;
+    if (cudaFuncSetAttribute(k_attn<D, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
+        return E0_ERR_CUDA;
+    k_attn<D, TY><<<a.blocks, AT_WARPS * 32, sm, s>>>(a);
+    k_attn_join<D, TY><<<dim3(a.blocks - 1, ROWS), D, sched, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+template <int TY>
+int launch_d(const AttnArgs& a, int D, cudaStream_t s) {
+    return D == 64 ? launch<64, TY>(a, s) : D == 128 ? launch<128, TY>(a, s) : launch<256, TY>(a, s);
+}
+
+}  // namespace
+
+size_t attn_ws_bytes(int D) {
+    const size_t slots = 2 * (size_t)num_sms() * BLOCKS_PER_SM;
+    return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2);
+}
+
+int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
+                int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale, int window, void* out,
+                int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
+    AttnArgs a = {};
+    a.k = c->k, a.v = c->v, a.ks = c->k_scale, a.vs = c->v_scale;
+    a.table = table, a.ctx = ctx, a.cu = cu, a.q = q, a.out = out, a.lse = lse;
+    a.blocks = num_sms() * BLOCKS_PER_SM;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2 * (size_t)a.blocks * ROWS * c->D);
+    a.st = st, a.q_ld = q_ld, a.out_ld = out_ld;
+    a.B = B, a.max_blocks = max_blocks, a.n_blocks = c->n_blocks, a.Hq = Hq, a.Hkv = c->Hkv, a.max_q = max_q;
+    a.window = window, a.scale = scale;
+    while ((1 << a.shift) < c->block_tokens) ++a.shift;
+    return dtype == E0_F32   ? launch_d<E0_F32>(a, c->D, s)
+           : dtype == E0_F16 ? launch_d<E0_F16>(a, c->D, s)
+                             : launch_d<E0_BF16>(a, c->D, s);
+}
+
+}  // namespace e0

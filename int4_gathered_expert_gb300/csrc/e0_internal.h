@@ -50,6 +50,23 @@ bool stack_known(const void* ws);
 int stack_step(const float* x, float* r_out, void* ws, const e0_stack_trace* trace, int impl, uint32_t* st,
                cudaStream_t s);
 
+int rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, int dtype, float eps, int64_t r_ld,
+               int64_t d_ld, void* r_out, void* h, uint8_t* q, float* q_scale, uint32_t* st, cudaStream_t s);
+size_t linear_bytes(int N, int K);
+int pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, cudaStream_t s);
+int linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type, int64_t x_ld, const float* x_scale, int T,
+                   const void* add, int64_t add_ld, void* y, int y_type, int64_t y_ld, cudaStream_t s);
+int kv_plan(const e0_kv_state* k, const int32_t* new_len, int T_cap, int32_t* ctx_out, int32_t* free_out,
+            int32_t* cu_q, int64_t* slots, int32_t* positions, int32_t* seq_ids, uint32_t* st, cudaStream_t s);
+int kv_release(const e0_kv_state* k, const uint8_t* mask, int32_t* ctx_out, int32_t* free_out, uint32_t* st,
+               cudaStream_t s);
+int kv_append(const e0_kv_cache* c, const void* k, const void* v, int dtype, int64_t k_ld, int64_t v_ld,
+              const int64_t* slots, int T, uint32_t* st, cudaStream_t s);
+size_t attn_ws_bytes(int D);
+int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
+                int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale, int window, void* out,
+                int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s);
+
 size_t prefill_ws_bytes(int T, int H, int I, int E, int K);
 int prefill_sort(const int32_t* inds, int T, int K, int E, int32_t* counts, int32_t* offsets, int32_t* perm,
                  void* ws, cudaStream_t s);

@@ -1,0 +1,419 @@
+// The paged 8-bit KV cache: block tables and slot maps from sequence lengths
+// (e0_kv_plan, e0_kv_release) and writing keys and values (e0_kv_append).
+#include <cuda_runtime.h>
+
+#include "e0_internal.h"
+#include "e0_types.cuh"
+
+namespace e0 {
+namespace {
+
+// ------------------------------------------------------------------ plan and release
+//
+// Both are a prefix sum over the sequences and then independent work on every
+// new token or block.  Every thread block computes the whole prefix sum by
+// itself (B lengths, a few KB out of L2) and takes its share of the rest, so
+// one launch does it without blocks waiting on one another.  Only new lengths
+// and stack height written over the old ones must come after every block has
+// read those: in the same block where there is one, else in a second launch.
+
+constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_ONE_BLOCK = 4096;  // tokens (blocks, for a release) that one thread block takes
+
+// What the lengths come to: sequence b's first token and first block, in
+// shared memory, and the totals; ok false where the request cannot be met.
+struct PlanSums {
+    int32_t* tok;   // [B + 1]
+    int32_t* blk;   // [B + 1]
+    int32_t* ctx;   // [B]
+    int total_tok, total_blk, height;
+    bool ok;
+};
+
+// Inclusive sums over the block's threads of two values.
+E0_DEV void block_scan2(long long& a, long long& b, long long (*red)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) a += x, b += y;
+    }
+    if (lane == 31) red[warp][0] = a, red[warp][1] = b;
+    __syncthreads();
+    long long sa = 0, sb = 0;
+    for (int i = 0; i < warp; ++i) sa += red[i][0], sb += red[i][1];
+    a += sa, b += sb;
+}
+
+struct PlanArgs {
+    int32_t* table;
+    const int32_t* ctx;
+    int32_t* free_list;
+    const int32_t* free_count;
+    const int32_t* new_len;   // plan
+    const uint8_t* mask;      // release
+    int32_t* ctx_out;
+    int32_t* free_out;
+    int32_t* cu_q;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* seq_ids;
+    uint32_t* st;
+    int B, max_blocks, shift, n_blocks, T_cap;
+    bool fill, commit;        // write slots and tables; write ctx_out and free_out
+};
+
+template <bool RELEASE>
+E0_DEV PlanSums plan_sums(const PlanArgs& A, int32_t* sm) {
+    __shared__ long long red[PLAN_THREADS / 32][2];
+    PlanSums S;
+    S.tok = sm, S.blk = sm + A.B + 1, S.ctx = sm + 2 * (A.B + 1);
+    const int per = (A.B + blockDim.x - 1) / blockDim.x, b0 = threadIdx.x * per;
+    const long long bs = 1ll << A.shift, room = (long long)A.max_blocks << A.shift;
+    long long nt = 0, nb = 0;
+    bool bad_len = false, full = false;
+    for (int i = 0; i < per; ++i) {
+        const int b = b0 + i;
+        if (b >= A.B) break;
+        const int c = A.ctx[b], n = RELEASE ? 0 : A.new_len[b];
+        const bool on = RELEASE ? A.mask[b] != 0 : true;
+        bad_len |= on && (c < 0 || n < 0 || (long long)c + n > room);
+        if (on) {
+            nt += n;
+            nb += RELEASE ? ((c + bs - 1) >> A.shift) : ((c + n + bs - 1) >> A.shift) - ((c + bs - 1) >> A.shift);
+        }
+    }
+    long long it = nt, ib = nb;
+    block_scan2(it, ib, red);
+    __shared__ long long tot[2];
+    if (threadIdx.x == blockDim.x - 1) tot[0] = it, tot[1] = ib;
+    __syncthreads();
+    S.height = *A.free_count;
+    full = tot[0] > A.T_cap;
+    if (RELEASE) {
+        bad_len |= S.height < 0 || S.height + tot[1] > A.n_blocks;
+        full = false;
+    } else {
+        bad_len |= S.height < 0 || S.height > A.n_blocks;
+        full |= tot[1] > S.height;
+    }
+    bad_len = __syncthreads_or(bad_len);
+    S.ok = !bad_len && !full;
+    if (!S.ok && blockIdx.x == 0 && threadIdx.x == 0)
+        set_status(A.st, bad_len ? E0_ST_BAD_LENGTH : E0_ST_POOL_FULL);
+    S.total_tok = S.ok ? (int)tot[0] : 0;
+    S.total_blk = S.ok ? (int)tot[1] : 0;
+    long long t = it - nt, k = ib - nb;
+    for (int i = 0; i < per; ++i) {
+        const int b = b0 + i;
+        if (b >= A.B) break;
+        const int c = A.ctx[b], n = RELEASE ? 0 : A.new_len[b];
+        S.ctx[b] = c;
+        S.tok[b] = S.ok ? (int)t : 0;
+        S.blk[b] = S.ok ? (int)k : 0;
+        if (S.ok && (!RELEASE || A.mask[b])) {
+            t += n;
+            k += RELEASE ? ((c + bs - 1) >> A.shift) : ((c + n + bs - 1) >> A.shift) - ((c + bs - 1) >> A.shift);
+        }
+    }
+    if (threadIdx.x == 0) S.tok[A.B] = S.total_tok, S.blk[A.B] = S.total_blk;
+    __syncthreads();
+    return S;
+}
+
+// The last b < B with first[b] <= i.
+E0_DEV int find_seq(const int32_t* first, int B, int i) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= i) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(PlanArgs A) {
+    extern __shared__ int32_t plan_sm[];
+    const PlanSums S = plan_sums<false>(A, plan_sm);
+    const int bs = 1 << A.shift;
+    if (A.fill) {
+        const int n = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + threadIdx.x;
+        for (int i = at; i < S.total_blk; i += n) {
+            const int b = find_seq(S.blk, A.B, i);
+            const int id = A.free_list[S.height - 1 - i];
+            const int j = ((S.ctx[b] + bs - 1) >> A.shift) + i - S.blk[b];
+            A.table[(size_t)b * A.max_blocks + j] = id;
+            if (id < 0 || id >= A.n_blocks) set_status(A.st, E0_ST_BAD_BLOCK);
+        }
+        for (int t = at; t < A.T_cap; t += n) {
+            int64_t slot = -1;
+            int pos = -1, b = -1;
+            if (t < S.total_tok) {
+                b = find_seq(S.tok, A.B, t);
+                pos = S.ctx[b] + t - S.tok[b];
+                const int held = (S.ctx[b] + bs - 1) >> A.shift, j = pos >> A.shift;
+                const int id = j < held ? A.table[(size_t)b * A.max_blocks + j]
+                                        : A.free_list[S.height - 1 - (S.blk[b] + j - held)];
+                if (id >= 0 && id < A.n_blocks)
+                    slot = ((int64_t)id << A.shift) + (pos & (bs - 1));
+                else
+                    set_status(A.st, E0_ST_BAD_BLOCK);
+            }
+            A.slots[t] = slot;
+            if (A.positions) A.positions[t] = pos;
+            if (A.seq_ids) A.seq_ids[t] = b;
+        }
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b <= A.B; b += blockDim.x) A.cu_q[b] = S.tok[b];
+    }
+    // block 0 alone writes these; where they lie over the inputs it is the only block
+    if (A.commit && blockIdx.x == 0) {
+        for (int b = threadIdx.x; b < A.B; b += blockDim.x) A.ctx_out[b] = S.ctx[b] + (S.tok[b + 1] - S.tok[b]);
+        if (threadIdx.x == 0) *A.free_out = S.height - S.total_blk;
+    }
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) k_kv_release(PlanArgs A) {
+    extern __shared__ int32_t plan_sm[];
+    const PlanSums S = plan_sums<true>(A, plan_sm);
+    if (A.fill) {
+        const int n = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + threadIdx.x;
+        for (int i = at; i < S.total_blk; i += n) {
+            const int b = find_seq(S.blk, A.B, i);
+            int32_t* p = A.table + (size_t)b * A.max_blocks + (i - S.blk[b]);
+            const int id = *p;
+            if (id < 0 || id >= A.n_blocks) set_status(A.st, E0_ST_BAD_BLOCK);
+            A.free_list[S.height + i] = id;
+            *p = -1;
+        }
+    }
+    if (A.commit && blockIdx.x == 0) {
+        for (int b = threadIdx.x; b < A.B; b += blockDim.x) A.ctx_out[b] = S.ok && A.mask[b] ? 0 : S.ctx[b];
+        if (threadIdx.x == 0) *A.free_out = S.height + S.total_blk;
+    }
+}
+
+// The launches of either: fill and commit in one where the outputs lie apart
+// from the inputs or one thread block does it all, else one after the other.
+template <typename K>
+int plan_launch(K kernel, PlanArgs a, long long work, cudaStream_t s) {
+    long long g = work <= PLAN_ONE_BLOCK ? 1 : (work + PLAN_THREADS - 1) / PLAN_THREADS;
+    if (g > num_sms()) g = num_sms();
+    const bool apart = a.ctx_out != a.ctx && a.free_out != a.free_count;
+    const int threads = work <= 256 && a.B <= 256 ? 256 : PLAN_THREADS;
+    const size_t sm = (3 * (size_t)a.B + 2) * sizeof(int32_t);
+    a.fill = true;
+    a.commit = g == 1 || apart;
+    if (sm > 40 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
+        return E0_ERR_CUDA;
+    kernel<<<(int)g, threads, sm, s>>>(a);
+    if (!a.commit) {
+        a.fill = false, a.commit = true;
+        a.st = nullptr;  // said already
+        kernel<<<1, PLAN_THREADS, sm, s>>>(a);
+    }
+    return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+PlanArgs plan_args(const e0_kv_state* k, int32_t* ctx_out, int32_t* free_out, uint32_t* st) {
+    PlanArgs a = {};
+    a.table = k->block_table, a.ctx = k->ctx_len, a.free_list = k->free_list, a.free_count = k->free_count;
+    a.ctx_out = ctx_out, a.free_out = free_out, a.st = st;
+    a.B = k->B, a.max_blocks = k->max_blocks, a.n_blocks = k->n_blocks;
+    while ((1 << a.shift) < k->block_tokens) ++a.shift;
+    return a;
+}
+
+// ------------------------------------------------------------------ append
+//
+// A warp takes one run of tokens of one block, for one head, for keys or
+// values: it finds the largest magnitude of the run, settles the block's
+// scale, rounds the older codes again if the scale grew, and writes the new
+// ones.  Warps are laid out by token; the warp of a run's first token does the
+// run, the others leave after reading two slots.  Scales are powers of two:
+// x / s and code * old / new are then exact, so the only rounding is that to
+// e4m3, and a scale that grows costs nothing but the codes that fall into e4m3's
+// subnormals.  (A scale of max / 448 would round every older code again at each
+// new maximum, and e4m3's relative precision gains nothing from it.)
+
+struct AppendArgs {
+    const void* x[2];
+    int64_t ld[2];
+    uint8_t* codes[2];
+    float* scale[2];
+    const int64_t* slots;
+    uint32_t* st;
+    int T, Hkv, shift, n_blocks;
+};
+
+E0_DEV float pow2_scale(float m) {  // smallest 2^e >= 2^-100 with m / 448 (rounded) <= 2^e
+    const uint32_t b = __float_as_uint(__fdiv_rn(m, 448.f));
+    uint32_t e = (b >> 23) + ((b & 0x7FFFFFu) != 0);
+    if (e < 27) e = 27;
+    return __uint_as_float(e << 23);
+}
+
+// A warp's row of one token and head: lane l holds elements l*D/32 ...
+template <int TY, int D>
+E0_DEV void row_load(const typename Elem<TY>::T* p, float (&v)[D / 32], bool vec) {
+    constexpr int N = D / 32;
+    if (vec) {
+        if constexpr (TY == E0_F32) {
+            if constexpr (N == 2) {
+                const float2 f = __ldg(reinterpret_cast<const float2*>(p));
+                v[0] = f.x, v[1] = f.y;
+            } else {
+                load_vec<TY, N>(p, v);
+            }
+        } else if constexpr (N == 2) {
+            const float2 f = unpack16<TY>(__ldg(reinterpret_cast<const uint32_t*>(p)));
+            v[0] = f.x, v[1] = f.y;
+        } else {
+            load_vec<TY, N>(p, v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = Elem<TY>::get(p[i]);
+    }
+}
+
+template <int TY, int D>
+__global__ void __launch_bounds__(256) k_kv_append(AppendArgs A, bool vec) {
+    typedef typename Elem<TY>::T T;
+    constexpr int N = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long id = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    const int per = 2 * A.Hkv;
+    const long long t0 = id / per;
+    if (t0 >= A.T) return;
+    const int which = (int)(id % per) / A.Hkv, head = (int)(id % per) % A.Hkv;
+    const int bs = 1 << A.shift;
+    const int64_t slot = A.slots[t0];
+    if (slot < 0) return;
+    const int off = (int)(slot & (bs - 1));
+    if (off != 0 && t0 > 0 && A.slots[t0 - 1] == slot - 1) return;  // inside a run
+    const int64_t blk = slot >> A.shift;
+    if (blk >= A.n_blocks) {
+        if (lane == 0) set_status(A.st, E0_ST_BAD_BLOCK);
+        return;
+    }
+    // the run's length: tokens that follow with consecutive slots inside the block
+    int n = 0;
+    for (;;) {
+        const int i = n + lane;
+        const bool in = off + i < bs && t0 + i < A.T && A.slots[t0 + i] == slot + i;
+        const uint32_t out = ~__ballot_sync(0xffffffffu, in);
+        n += out ? __ffs(out) - 1 : 32;
+        if (out) break;
+    }
+    const int64_t ld = which ? A.ld[1] : A.ld[0];
+    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + t0 * ld + (size_t)head * D + lane * N;
+    uint32_t m = 0;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        float v[N];
+        row_load<TY, D>(x + (size_t)i * ld, v, vec);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+            if (a < 0x7F800000u) m = max(m, a); else bad = true;
+        }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(A.st, E0_ST_NONFINITE);
+
+    float* scale = (which ? A.scale[1] : A.scale[0]) + (size_t)blk * A.Hkv + head;
+    uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
+    float s = pow2_scale(__uint_as_float(m));
+    if (off > 0) {
+        float old = *scale;
+        if (!(old > 0.f && old < 3.0e38f)) old = s;  // nothing a call of ours wrote: the codes stay as they are
+        s = fmaxf(s, old);
+        if (s > old) {
+            const float ratio = old / s;
+            uint4* c = reinterpret_cast<uint4*>(codes);
+            const int words = off * D / 16;
+#pragma unroll 4
+            for (int i = lane; i < words; i += 32) {
+                uint4 u = c[i];
+                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t r = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 f = unpack16<E0_F16>(e4m3x2_to_half2((uint16_t)(w[k] >> (16 * h))));
+                        r |= e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+                    }
+                    w[k] = r;
+                }
+                c[i] = u;
+            }
+        }
+    }
+    __syncwarp();
+    if (lane == 0) *scale = s;
+    const float inv = 1.f / s;  // a power of two
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        float v[N];
+        row_load<TY, D>(x + (size_t)i * ld, v, vec);
+        uint32_t c[(N + 3) / 4] = {};
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float a = fabsf(v[j]) < INFINITY ? v[j] * inv : 0.f, b = fabsf(v[j + 1]) < INFINITY ? v[j + 1] * inv : 0.f;
+            c[j / 4] |= e4m3x2(a, b) << (8 * (j & 2));
+        }
+        uint8_t* p = codes + (size_t)(off + i) * D + lane * N;
+        if constexpr (N == 2)
+            *reinterpret_cast<uint16_t*>(p) = (uint16_t)c[0];
+        else if constexpr (N == 4)
+            *reinterpret_cast<uint32_t*>(p) = c[0];
+        else
+            *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+    }
+}
+
+template <int TY, int D>
+int append_launch(const AppendArgs& a, cudaStream_t s) {
+    const int sz = type_size(TY);
+    const uintptr_t need = D / 32 * sz < 16 ? D / 32 * sz : 16;
+    const uintptr_t bits = (uintptr_t)a.x[0] | (uintptr_t)a.x[1] | (uintptr_t)(a.ld[0] * sz) | (uintptr_t)(a.ld[1] * sz);
+    const long long warps = (long long)a.T * 2 * a.Hkv;
+    k_kv_append<TY, D><<<(int)((warps + 7) / 8), 256, 0, s>>>(a, !(bits & (need - 1)));
+    return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+template <int TY>
+int append_d(const AppendArgs& a, int D, cudaStream_t s) {
+    return D == 64 ? append_launch<TY, 64>(a, s) : D == 128 ? append_launch<TY, 128>(a, s) : append_launch<TY, 256>(a, s);
+}
+
+}  // namespace
+
+int kv_plan(const e0_kv_state* k, const int32_t* new_len, int T_cap, int32_t* ctx_out, int32_t* free_out,
+            int32_t* cu_q, int64_t* slots, int32_t* positions, int32_t* seq_ids, uint32_t* st, cudaStream_t s) {
+    PlanArgs a = plan_args(k, ctx_out, free_out, st);
+    a.new_len = new_len, a.T_cap = T_cap, a.cu_q = cu_q, a.slots = slots, a.positions = positions, a.seq_ids = seq_ids;
+    return plan_launch(k_kv_plan, a, T_cap, s);
+}
+
+int kv_release(const e0_kv_state* k, const uint8_t* mask, int32_t* ctx_out, int32_t* free_out, uint32_t* st,
+               cudaStream_t s) {
+    PlanArgs a = plan_args(k, ctx_out, free_out, st);
+    a.mask = mask;
+    const long long most = (long long)k->B * k->max_blocks;
+    return plan_launch(k_kv_release, a, most < k->n_blocks ? most : k->n_blocks, s);
+}
+
+int kv_append(const e0_kv_cache* c, const void* k, const void* v, int dtype, int64_t k_ld, int64_t v_ld,
+              const int64_t* slots, int T, uint32_t* st, cudaStream_t s) {
+    AppendArgs a = {{k, v}, {k_ld, v_ld}, {c->k, c->v}, {c->k_scale, c->v_scale}, slots, st, T, c->Hkv, 0, c->n_blocks};
+    while ((1 << a.shift) < c->block_tokens) ++a.shift;
+    return dtype == E0_F32   ? append_d<E0_F32>(a, c->D, s)
+           : dtype == E0_F16 ? append_d<E0_F16>(a, c->D, s)
+                             : append_d<E0_BF16>(a, c->D, s);
+}
+
+}  // namespace e0

@@ -17,11 +17,15 @@ LIB_PATH = os.path.join(_HERE, "libe0moe.so")
 
 E0_OK, E0_ERR_ARG, E0_ERR_NULL, E0_ERR_UNSUPPORTED, E0_ERR_CUDA = 0, -1, -2, -3, -4
 E0_ST_SLOT_MISS, E0_ST_BAD_EXPERT, E0_ST_NONFINITE, E0_ST_TIMEOUT, E0_ST_POOL_FULL, E0_ST_INTERNAL = 1, 2, 4, 8, 16, 32
+E0_ST_BAD_BLOCK, E0_ST_BAD_LENGTH = 64, 128
+E0_F32, E0_F16, E0_BF16, E0_E4M3 = 0, 1, 2, 3
 E0_ROUTE_SOFTMAX_TOPK, E0_ROUTE_SIGMOID_GROUP = 0, 1
 E0_MAX_E, E0_MAX_K, E0_MAX_T_DECODE, E0_MAX_LORA_RANK = 1024, 32, 64, 64
+E0_MAX_NORM_H, E0_MAX_SEQS, E0_MAX_T_LINEAR = 16384, 4096, 524280
 
 vp = C.c_void_p
 i32 = C.c_int32
+i64 = C.c_int64
 
 
 class QTensor(C.Structure):
@@ -64,6 +68,16 @@ class StackLayer(C.Structure):
 
 class StackTrace(C.Structure):
     _fields_ = [("r", vp), ("inds", vp), ("w", vp), ("head_logits", vp), ("pred_inds", vp)]
+
+
+class KvCache(C.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("k_scale", vp), ("v_scale", vp),
+                ("n_blocks", i32), ("Hkv", i32), ("block_tokens", i32), ("D", i32)]
+
+
+class KvState(C.Structure):
+    _fields_ = [("block_table", vp), ("ctx_len", vp), ("free_list", vp), ("free_count", vp),
+                ("B", i32), ("max_blocks", i32), ("block_tokens", i32), ("n_blocks", i32)]
 
 
 _lib = None
@@ -109,6 +123,17 @@ def load() -> C.CDLL:
         "e0_prefill_sort": (C.c_int, [vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, sz, vp]),
         "e0_moe_prefill_forward": (C.c_int, [vp, C.c_int, P(SlotPool), vp, P(RouteParams), vp, vp, vp,
                                              vp, sz, vp, vp]),
+        "e0_rmsnorm_q8": (C.c_int, [vp, vp, vp, C.c_int, C.c_int, C.c_int, C.c_float, i64, i64, vp, vp, vp, vp, vp, vp]),
+        "e0_linear_bytes": (sz, [C.c_int, C.c_int]),
+        "e0_pack_linear": (C.c_int, [P(QTensor), C.c_int, C.c_int, vp, vp]),
+        "e0_linear_forward": (C.c_int, [vp, C.c_int, C.c_int, vp, C.c_int, i64, vp, C.c_int, vp, i64, vp, C.c_int, i64,
+                                        vp]),
+        "e0_kv_plan": (C.c_int, [P(KvState), vp, C.c_int, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "e0_kv_release": (C.c_int, [P(KvState), vp, vp, vp, vp, vp]),
+        "e0_kv_append": (C.c_int, [P(KvCache), vp, vp, C.c_int, i64, i64, vp, C.c_int, vp, vp]),
+        "e0_attn_workspace_size": (sz, [C.c_int] * 5),
+        "e0_attn_decode": (C.c_int, [P(KvCache), vp, C.c_int, vp, vp, C.c_int, C.c_int, vp, C.c_int, i64, C.c_int,
+                                     C.c_float, C.c_int, vp, i64, vp, vp, sz, vp, vp]),
         "e0_selftest_bounded_wait": (C.c_int, [vp, C.c_uint32, vp, vp]),
         "e0_read_status": (C.c_int, [vp, P(C.c_uint32), vp]),
         "e0_status_string": (C.c_char_p, [C.c_int]),
@@ -130,7 +155,10 @@ def exported_symbols():
             "e0_stack_update_layers", "e0_stack_prefetch_experts", "e0_stack_prefetch_experts_batch",
             "e0_stack_prefetch_experts_cached", "e0_stack_prefetch_experts_cached_batch",
             "e0_prefill_sort",
-            "e0_moe_prefill_forward", "e0_selftest_bounded_wait", "e0_read_status", "e0_status_string"]
+            "e0_moe_prefill_forward",
+            "e0_rmsnorm_q8", "e0_linear_bytes", "e0_pack_linear", "e0_linear_forward", "e0_kv_plan", "e0_kv_release",
+            "e0_kv_append", "e0_attn_workspace_size", "e0_attn_decode",
+            "e0_selftest_bounded_wait", "e0_read_status", "e0_status_string"]
 
 
 # ---------------------------------------------------------------- marshalling
@@ -323,6 +351,60 @@ def e0_moe_prefill_forward(X, T, bank: SlotPool, W_router, rp: RouteParams, Y, i
                                        ptr(inds_out), ptr(w_out), ptr(ws), ws_bytes, ptr(status),
                                        stream_handle(stream))
     return _check("e0_moe_prefill_forward", rc, raise_on_error)
+
+
+def e0_rmsnorm_q8(r, d, w, T, H, dtype, eps, r_ld, d_ld, r_out, h, q, q_scale, status=None, stream=None,
+                  raise_on_error=True):
+    rc = load().e0_rmsnorm_q8(ptr(r), ptr(d), ptr(w), T, H, dtype, eps, r_ld, d_ld, ptr(r_out), ptr(h), ptr(q),
+                              ptr(q_scale), ptr(status), stream_handle(stream))
+    return _check("e0_rmsnorm_q8", rc, raise_on_error)
+
+
+def e0_linear_bytes(N, K):
+    return load().e0_linear_bytes(N, K)
+
+
+def e0_pack_linear(src: QTensor, N, K, dst, stream=None, raise_on_error=True):
+    rc = load().e0_pack_linear(C.byref(src), N, K, ptr(dst), stream_handle(stream))
+    return _check("e0_pack_linear", rc, raise_on_error)
+
+
+def e0_linear_forward(w, N, K, x, x_type, x_ld, x_scale, T, add, add_ld, y, y_type, y_ld, stream=None,
+                      raise_on_error=True):
+    rc = load().e0_linear_forward(ptr(w), N, K, ptr(x), x_type, x_ld, ptr(x_scale), T, ptr(add), add_ld, ptr(y),
+                                  y_type, y_ld, stream_handle(stream))
+    return _check("e0_linear_forward", rc, raise_on_error)
+
+
+def e0_kv_plan(state: KvState, new_len, T_cap, ctx_out, free_out, cu_q, slots, positions=None, seq_ids=None,
+               status=None, stream=None, raise_on_error=True):
+    rc = load().e0_kv_plan(C.byref(state), ptr(new_len), T_cap, ptr(ctx_out), ptr(free_out), ptr(cu_q), ptr(slots),
+                           ptr(positions), ptr(seq_ids), ptr(status), stream_handle(stream))
+    return _check("e0_kv_plan", rc, raise_on_error)
+
+
+def e0_kv_release(state: KvState, mask, ctx_out, free_out, status=None, stream=None, raise_on_error=True):
+    rc = load().e0_kv_release(C.byref(state), ptr(mask), ptr(ctx_out), ptr(free_out), ptr(status),
+                              stream_handle(stream))
+    return _check("e0_kv_release", rc, raise_on_error)
+
+
+def e0_kv_append(cache: KvCache, k, v, dtype, k_ld, v_ld, slots, T, status=None, stream=None, raise_on_error=True):
+    rc = load().e0_kv_append(C.byref(cache), ptr(k), ptr(v), dtype, k_ld, v_ld, ptr(slots), T, ptr(status),
+                             stream_handle(stream))
+    return _check("e0_kv_append", rc, raise_on_error)
+
+
+def e0_attn_workspace_size(B, Hq, Hkv, D, max_q):
+    return load().e0_attn_workspace_size(B, Hq, Hkv, D, max_q)
+
+
+def e0_attn_decode(cache: KvCache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale,
+                   window, out, out_ld, lse, ws, ws_bytes, status=None, stream=None, raise_on_error=True):
+    rc = load().e0_attn_decode(C.byref(cache), ptr(block_table), max_blocks, ptr(ctx_len), ptr(cu_q), B, max_q,
+                               ptr(q), dtype, q_ld, Hq, scale, window, ptr(out), out_ld, ptr(lse), ptr(ws), ws_bytes,
+                               ptr(status), stream_handle(stream))
+    return _check("e0_attn_decode", rc, raise_on_error)
 
 
 E0_SELFTEST_MAX_WAIT_US = 2000000
