@@ -22,9 +22,11 @@ namespace {
 // rows 0..7 the fp16 part, rows 8..15 the rest of the value, so neither q nor the
 // probabilities lose bits that matter (22 significant bits), at no cost: a
 // decode step has few rows and the kernel is bound by reading the cache.
-// Operand layouts are chosen so that every lane loads 16 bytes at a time straight
-// from the cache: the order of D inside the first product and of the output
-// columns in the second are permuted (the same permutation on both operands).
+// A warp's codes come through its own ring in shared memory, copied some steps
+// ahead, so warps never wait for one another inside a job.  Operand layouts are
+// chosen so that every lane reads 16 bytes at a time: the order of D inside the
+// first product and of the output columns in the second are permuted (the same
+// permutation on both operands).
 // The scale of a block of keys multiplies the scores; that of the values goes into
 // the probabilities relative to the largest one seen (a running reference
 // like the maximum's), so that they stay in fp16's range.
@@ -32,6 +34,15 @@ namespace {
 constexpr int UNIT = 64;
 constexpr int ROWS = 8;
 constexpr int AT_WARPS = 4;
+constexpr int STEP = 16;  // positions a warp takes at once
+static_assert(UNIT == AT_WARPS * STEP, "a warp takes one step of each unit");
+
+// Steps whose copies a warp has under way (its ring in shared memory).
+template <int D>
+struct Ring {
+    static constexpr int STAGES = D == 256 ? 3 : D == 128 ? 6 : 8;
+    static constexpr int BYTES = 2 * STEP * D;  // keys, then values
+};
 
 struct AttnArgs {
     const uint8_t* k;
@@ -56,6 +67,7 @@ struct AttnArgs {
 struct Seq {
     int row0, n, ctx, first;  // first query row, queries, cached tokens, first unit that anyone sees
     int units, tiles;         // units of context, tiles of 8 rows per KV head
+    int low;                  // the first position that the first query sees
 };
 
 E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
@@ -67,8 +79,8 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     if (s.row0 < 0 || s.n < 0 || s.n > A.max_q) bad = true, s.n = 0;
     if (s.ctx < 0 || (long long)s.ctx > ((long long)A.max_blocks << A.shift)) bad = true, s.ctx = 0;
     if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
-    const int low = s.ctx - s.n + 1 - A.window;  // the first position that the first query sees
-    s.first = A.window > 0 && low > 0 ? low / UNIT : 0;
+    s.low = A.window > 0 ? max(s.ctx - s.n + 1 - A.window, 0) : 0;
+    s.first = s.low / UNIT;
     s.units = (s.ctx + UNIT - 1) / UNIT - s.first;
     if (s.units < 1) s.units = 1;  // a job without context still writes its rows
     const int G = A.Hq / A.Hkv;
@@ -180,12 +192,42 @@ constexpr float LN2 = 0.6931471805599453f;
 
 template <int D>
 struct AttnSmem {
-    float o[AT_WARPS][ROWS][D + 4];
-    float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS], r[AT_WARPS];
+    uint8_t ring[AT_WARPS][Ring<D>::STAGES][Ring<D>::BYTES];  // a warp's output at the end of a job
     uint32_t q[D / 16][32][4];
+    float2 scales[AT_WARPS][Ring<D>::STAGES];  // of the step's keys and values; x < 0: the step is not seen
+    float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS], r[AT_WARPS];
     float f[ROWS];
     long long red[AT_WARPS];
 };
+
+template <int D>
+E0_DEV float* warp_out(AttnSmem<D>& S, int w) {  // [ROWS][D + 4]
+    static_assert(sizeof(S.ring[0]) >= ROWS * (D + 4) * sizeof(float), "the ring holds a warp's output");
+    return reinterpret_cast<float*>(S.ring[w]);
+}
+
+// Where the 16-byte chunk c of row r of a step's keys or values stands: chunks
+// are permuted inside 128 bytes so that the eight lanes of a load's phase, which
+// read four chunks of two key rows, or two chunks of four value rows, find
+// eight different ones.
+template <int D>
+E0_DEV int key_chunk(int r, int c) {
+    return D == 64 ? r * 4 + c : r * (D / 16) + (c ^ (((r & 1) << 2) | ((r >> 1) & 3)));
+}
+template <int D>
+E0_DEV int value_chunk(int r, int c) {
+    return D == 64 ? ((r * 4 + c) ^ (r & 6)) : r * (D / 16) + (c ^ (r & 6));
+}
+
+E0_DEV void copy16(uint8_t* dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+E0_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+E0_DEV void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <int TY>
 E0_DEV void store_out(const AttnArgs& A, size_t row, int i, float v) {
@@ -200,6 +242,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     AttnSmem<D>& S = *reinterpret_cast<AttnSmem<D>*>(attn_sm);
     long long* first = reinterpret_cast<long long*>(attn_sm + sizeof(AttnSmem<D>));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t4 = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long total = schedule(A, first, S.red, blockIdx.x == 0);
     const long long per = units_per_block(A, total);
     long long u = blockIdx.x * per;
@@ -207,6 +250,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     const int G = A.Hq / A.Hkv, bs = 1 << A.shift;
     constexpr int KC = D / 64;          // 16-byte chunks of a key row a lane reads
     constexpr int NT = D / 8;           // output tiles
+    constexpr int STAGES = Ring<D>::STAGES;
     constexpr int VC = D >= 128 ? D / 128 : 1;  // 16-byte chunks of a value row
 
     while (u < u1) {
@@ -258,58 +302,94 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         }
         __syncthreads();
         const float f = S.f[gid];
+        uint32_t qf[D <= 128 ? D / 16 : 1][4];  // registers hold them where there are enough
+        if constexpr (D <= 128) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint4 a = *reinterpret_cast<const uint4*>(S.q[i][lane]);
+                qf[i][0] = a.x, qf[i][1] = a.y, qf[i][2] = a.z, qf[i][3] = a.w;
+            }
+        }
         float acc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
         float mx = -INFINITY, sum = 0.f, ref = 0.f;  // ref: the largest value scale so far
 
-        for (int c = c0; c < c1; ++c) {
-            const int pos = (j.s.first + c) * UNIT + 16 * warp;
-            if (pos >= j.s.ctx) continue;
-            const int id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
-            if (id < 0 || id >= A.n_blocks) {
-                if (lane == 0) set_status(A.st, E0_ST_BAD_BLOCK);
-                continue;
-            }
-            const size_t at = (((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1));
-            const uint8_t* kp = A.k + at * D;
-            const uint8_t* vp = A.v + at * D;
-            const float ksc = A.ks[(size_t)id * A.Hkv + j.head], vsc = A.vs[(size_t)id * A.Hkv + j.head];
-            uint4 kw[2][KC];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < KC; ++i)
-                    kw[h][i] = ldg_stream(kp + (size_t)(8 * h + gid) * D + 64 * i + 16 * t4);
-            uint4 vw[VC][4];  // tokens 2t, 2t+1, 8+2t, 9+2t
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* p = vp + (size_t)(2 * t4 + (i & 1) + 8 * (i >> 1)) * D;
-                if constexpr (D == 64) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p + 8 * gid));
-                    vw[0][i] = make_uint4(x.x, x.y, 0, 0);
+        // block ids and scales of 32 steps at a time, one a lane
+        int my_id = -1;
+        float2 my_sc = make_float2(-1.f, 0.f);
+        const auto look_up = [&](int c) {
+            const int pos = (j.s.first + c + lane) * UNIT + STEP * warp;
+            my_id = -1;
+            my_sc = make_float2(-1.f, 0.f);
+            if (c + lane < c1 && pos < j.s.ctx && pos + STEP > j.s.low) {
+                my_id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
+                if (my_id >= 0 && my_id < A.n_blocks) {
+                    const size_t i = (size_t)my_id * A.Hkv + j.head;
+                    my_sc = make_float2(A.ks[i], A.vs[i]);
                 } else {
-#pragma unroll
-                    for (int h = 0; h < VC; ++h) vw[h][i] = ldg_stream(p + 128 * h + 16 * gid);
+                    my_id = -1;
+                    set_status(A.st, E0_ST_BAD_BLOCK);
                 }
             }
+        };
+        const auto issue = [&](int c) {
+            if (c < c1) {
+                const int from = (c - c0) & 31, stage = (c - c0) % STAGES;
+                if (from == 0) look_up(c);
+                const int id = __shfl_sync(0xffffffffu, my_id, from);
+                const float kx = __shfl_sync(0xffffffffu, my_sc.x, from), vx = __shfl_sync(0xffffffffu, my_sc.y, from);
+                if (lane == 0) S.scales[warp][stage] = make_float2(id < 0 ? -1.f : kx, vx);
+                if (id >= 0) {
+                    const int pos = (j.s.first + c) * UNIT + STEP * warp;
+                    const size_t at = ((((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1))) * D + 16 * lane;
+                    uint8_t* dst = S.ring[warp][stage];
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const int r = (i * 32 + lane) / (D / 16), ch = (i * 32 + lane) % (D / 16);
+                        copy16(dst + 16 * key_chunk<D>(r, ch), A.k + at + 512 * i);
+                        copy16(dst + STEP * D + 16 * value_chunk<D>(r, ch), A.v + at + 512 * i);
+                    }
+                }
+            }
+            copy_commit();
+        };
+        for (int i = 0; i < STAGES - 1; ++i) issue(c0 + i);
+
+        for (int c = c0; c < c1; ++c) {
+            copy_wait<STAGES - 2>();
+            __syncwarp();  // the step has arrived for all lanes, and all have read the one before it
+            const int stage = (c - c0) % STAGES;
+            const float2 sc = S.scales[warp][stage];
+            issue(c + STAGES - 1);
+            if (sc.x < 0.f) continue;
+            const int pos = (j.s.first + c) * UNIT + STEP * warp;
+            const uint8_t* kp = S.ring[warp][stage];
+            const uint8_t* vp = kp + STEP * D;
             float s[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
 #pragma unroll
                 for (int i = 0; i < KC; ++i) {
-                    const uint32_t w[4] = {kw[h][i].x, kw[h][i].y, kw[h][i].z, kw[h][i].w};
+                    const uint4 kw = *reinterpret_cast<const uint4*>(kp + 16 * key_chunk<D>(8 * h + gid, 4 * i + t4));
+                    const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint4 a = *reinterpret_cast<const uint4*>(S.q[4 * i + k][lane]);
-                        mma(s[h], a.x, a.y, a.z, a.w, widen(w[k], 0, 0x9180), widen(w[k], 0, 0xB3A2));
+                        const uint32_t b0 = widen(w[k], 0, 0x9180), b1 = widen(w[k], 0, 0xB3A2);
+                        if constexpr (D <= 128) {
+                            const uint32_t(&a)[4] = qf[4 * i + k];
+                            mma(s[h], a[0], a[1], a[2], a[3], b0, b1);
+                        } else {
+                            const uint4 a = *reinterpret_cast<const uint4*>(S.q[4 * i + k][lane]);
+                            mma(s[h], a.x, a.y, a.z, a.w, b0, b1);
+                        }
                     }
                 }
             }
             // scores in units of log2, masked; this lane: row gid, tokens 8h + 2t, + 1
             float p[2][2], top = -INFINITY;
-            const float fk = f * ksc;
+            const float fk = f * sc.x;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -323,9 +403,9 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             const float base = top == -INFINITY ? 0.f : top;
             const float shrink = exp2f(mx - base);
             mx = top;
-            const float ref1 = fmaxf(ref, vsc);
+            const float ref1 = fmaxf(ref, sc.y);
             const float keep = ref1 > 0.f ? shrink * (ref / ref1) : shrink;
-            const float vrel = ref1 > 0.f ? vsc / ref1 : 0.f;
+            const float vrel = ref1 > 0.f ? sc.y / ref1 : 0.f;
             ref = ref1;
             sum *= shrink;
             uint32_t ph[2], pl[2];
@@ -342,10 +422,18 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             }
 #pragma unroll
             for (int h = 0; h < VC; ++h) {
-                const uint32_t w[4][4] = {{vw[h][0].x, vw[h][0].y, vw[h][0].z, vw[h][0].w},
-                                          {vw[h][1].x, vw[h][1].y, vw[h][1].z, vw[h][1].w},
-                                          {vw[h][2].x, vw[h][2].y, vw[h][2].z, vw[h][2].w},
-                                          {vw[h][3].x, vw[h][3].y, vw[h][3].z, vw[h][3].w}};
+                uint32_t w[4][4];  // tokens 2t, 2t+1, 8+2t, 9+2t
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 2 * t4 + (i & 1) + 8 * (i >> 1);
+                    if constexpr (D == 64) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(vp + 16 * value_chunk<D>(r, gid >> 1) + 8 * (gid & 1));
+                        w[i][0] = x.x, w[i][1] = x.y;
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4*>(vp + 16 * value_chunk<D>(r, 8 * h + gid));
+                        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < (D == 64 ? 8 : 16); ++n) {
                     const uint32_t sel = 0xC480u + 0x1111u * (n & 3);  // byte and sign of a's and b's n-th code
@@ -354,6 +442,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                 }
             }
         }
+        copy_wait<0>();
         // ---- the warps' results together
         sum = quad_sum(sum);
         if (t4 == 0) S.m[warp][gid] = mx, S.l[warp][gid] = sum;
@@ -362,8 +451,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         for (int n = 0; n < NT; ++n) {
             // tile n, columns 2t and 2t+1: elements 16 * column + n % 16 of its 128 (8 * column + n of 64)
             const int d0 = D == 64 ? 16 * t4 + n : 128 * (n / 16) + 32 * t4 + n % 16;
-            S.o[warp][gid][d0] = acc[n][0] + acc[n][2];
-            S.o[warp][gid][d0 + (D == 64 ? 8 : 16)] = acc[n][1] + acc[n][3];
+            warp_out<D>(S, warp)[gid * (D + 4) + d0] = acc[n][0] + acc[n][2];
+            warp_out<D>(S, warp)[gid * (D + 4) + d0 + (D == 64 ? 8 : 16)] = acc[n][1] + acc[n][3];
         }
         __syncthreads();
         const bool whole = c0 == 0 && c1 == j.s.units;
@@ -380,7 +469,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             for (int w = 0; w < AT_WARPS; ++w) {
                 const float k = exp2f(S.m[w][r] - base);
                 l += k * S.l[w][r];
-                o += k * S.r[w] * S.o[w][r][d];
+                o += k * S.r[w] * warp_out<D>(S, w)[r * (D + 4) + d];
             }
             if (whole) {
                 const size_t tok = (size_t)j.s.row0 + row / G;
@@ -397,38 +486,79 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 }
 
 // A block boundary that falls inside a job, the first one in it: join the job's
-// partial results, one row a block (y).
+// partial results, one row a block (y).  A thread adds four columns of every
+// JOIN_GROUPS-th partial result, then the groups' sums are added.
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_PARTS = 512;  // partial results a job can have: the thread blocks
+
 template <int D, int TY>
-__global__ void __launch_bounds__(D) k_attn_join(AttnArgs A) {
+__global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
+    constexpr int GROUPS = JOIN_THREADS / (D / 4);
     extern __shared__ __align__(16) char join_sm[];
     long long* first = reinterpret_cast<long long*>(join_sm);
-    __shared__ long long red[D / 32];
+    __shared__ long long red[JOIN_THREADS / 32];
+    __shared__ float weight[JOIN_PARTS];
+    __shared__ float part[GROUPS][D + 4];
+    __shared__ float wm[JOIN_THREADS / 32], wl[JOIN_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long total = schedule(A, first, red, false);
     const long long per = units_per_block(A, total);
     const long long edge = (blockIdx.x + 1) * per;
-    if (edge >= total) return;
-    const Job j = job_at(A, first, edge);
+    Job j = {};
+    if (edge < total) j = job_at(A, first, edge);
     const int G = A.Hq / A.Hkv, r = blockIdx.y, row = j.tile * ROWS + r;
-    if (j.first == edge || j.first < edge - per || row >= j.s.n * G) return;
-    const int b1 = (int)((j.first + j.s.units - 1) / per);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
+    if (edge >= total || j.first == edge || j.first < edge - per || row >= j.s.n * G) return;
+    const int b0 = blockIdx.x, n = (int)((j.first + j.s.units - 1) / per) - b0 + 1;
+    // the first block left its part in its second slot, the others in their first
+    const auto slot = [&](int i) { return ((size_t)2 * (b0 + i) + (i == 0)) * ROWS + r; };
     float m = -INFINITY;
-    for (int b = blockIdx.x; b <= b1; ++b) m = fmaxf(m, A.part_ml[(size_t)(2 * b + (b == blockIdx.x)) * ROWS + r].x);
+    for (int i = tid; i < n; i += JOIN_THREADS) m = fmaxf(m, A.part_ml[slot(i)].x);
+    m = warp_max(m);
+    if (lane == 0) wm[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < JOIN_THREADS / 32; ++w) m = fmaxf(m, wm[w]);
     const float base = m == -INFINITY ? 0.f : m;
-    float o = 0.f, l = 0.f;
-    for (int b = blockIdx.x; b <= b1; ++b) {
-        const size_t at = (size_t)(2 * b + (b == blockIdx.x)) * ROWS + r;
-        const float2 ml = A.part_ml[at];
-        const float k = exp2f(ml.x - base);
-        l += k * ml.y;
-        o += k * A.part_o[at * D + threadIdx.x];
+    float l = 0.f;
+    for (int i = tid; i < n; i += JOIN_THREADS) {
+        const float2 ml = A.part_ml[slot(i)];
+        weight[i] = exp2f(ml.x - base);
+        l += weight[i] * ml.y;
     }
+    l = warp_sum(l);
+    if (lane == 0) wl[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < JOIN_THREADS / 32; ++w) l += wl[w];
+    const int g = tid / (D / 4), d4 = tid % (D / 4) * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = g; i < n; i += GROUPS) {
+        const float4 x = *reinterpret_cast<const float4*>(A.part_o + slot(i) * D + d4);
+        const float k = weight[i];
+        o.x += k * x.x, o.y += k * x.y, o.z += k * x.z, o.w += k * x.w;
+    }
+    *reinterpret_cast<float4*>(&part[g][d4]) = o;
+    __syncthreads();
     const size_t tok = (size_t)j.s.row0 + row / G;
     const int head = j.head * G + row % G;
-    store_out<TY>(A, tok, head * D + threadIdx.x, l > 0.f || l != l ? o / l : 0.f);
-    if (A.lse && threadIdx.x == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * LN2 : -INFINITY;
+    if (tid < D) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) v += part[k][tid];
+        store_out<TY>(A, tok, head * D + tid, l > 0.f || l != l ? v / l : 0.f);
+    }
+    if (A.lse && tid == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * LN2 : -INFINITY;
 }
 
 constexpr int BLOCKS_PER_SM = 2;
+
+int attn_blocks() {
+    const int n = num_sms() * BLOCKS_PER_SM;
+    return n < JOIN_PARTS ? n : JOIN_PARTS;
+}
 
 template <int D, int TY>
 int launch(AttnArgs a, cudaStream_t s) {
@@ -437,8 +567,20 @@ int launch(AttnArgs a, cudaStream_t s) {
     if (cudaFuncSetAttribute(k_attn<D, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
         return E0_ERR_CUDA;
     k_attn<D, TY><<<a.blocks, AT_WARPS * 32, sm, s>>>(a);
-    k_attn_join<D, TY><<<dim3(a.blocks - 1, ROWS), D, sched, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
+    // the join starts while the blocks above still run, works out its schedule
+    // and then waits for all of them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.blocks - 1, ROWS);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.dynamicSmemBytes = sched;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_join<D, TY>, a) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
 
 template <int TY>
@@ -449,7 +591,7 @@ int launch_d(const AttnArgs& a, int D, cudaStream_t s) {
 }  // namespace
 
 size_t attn_ws_bytes(int D) {
-    const size_t slots = 2 * (size_t)num_sms() * BLOCKS_PER_SM;
+    const size_t slots = 2 * (size_t)attn_blocks();
     return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2);
 }
 
@@ -459,7 +601,7 @@ int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
     AttnArgs a = {};
     a.k = c->k, a.v = c->v, a.ks = c->k_scale, a.vs = c->v_scale;
     a.table = table, a.ctx = ctx, a.cu = cu, a.q = q, a.out = out, a.lse = lse;
-    a.blocks = num_sms() * BLOCKS_PER_SM;
+    a.blocks = attn_blocks();
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + 2 * (size_t)a.blocks * ROWS * c->D);
     a.st = st, a.q_ld = q_ld, a.out_ld = out_ld;

@@ -651,6 +651,27 @@ def test_attention_rows_that_see_nothing(L):
     assert st & L.E0_ST_BAD_LENGTH
 
 
+@pytest.mark.parametrize("bs", [16, 64])
+def test_attention_window_over_released_blocks(L, bs):
+    """Blocks that lie wholly before the window may be gone: ids out of range, scales that are not numbers."""
+    rng = np.random.default_rng(bs)
+    Hq, Hkv, D, window = 4, 2, 64, 70
+    ctx, cu = [500, 130, 69], np.array([0, 1, 4, 6])
+    c, t, desc, table = filled_cache(L, 3, bs, Hkv, D, ctx, rng)
+    q = dev(rng.standard_normal((6, Hq, D)), torch.float32)
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, F32, window)
+    check_attention(c, table, ctx, cu, q, out, lse, F32, window)
+    for b in range(3):
+        first = max(0, ctx[b] - (cu[b + 1] - cu[b]) + 1 - window)
+        for j in range(first // bs):
+            blk = int(table[b, j])
+            t[2][blk], t[3][blk], t[0][blk], t[1][blk] = float("nan"), float("inf"), 127, 127
+            if j % 2:
+                table[b, j] = -1
+    again, lse2, st = attend(L, c, desc, table, ctx, cu, q, F32, window)
+    assert st == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_masked_garbage_and_non_finite_queries(L):
     """What stands behind a sequence's end (NaN codes and scales) or outside a window does not matter; a query that is not
     finite spoils its own head only."""
