@@ -518,7 +518,8 @@ int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type,
  * block and head one contiguous run of e4m3 codes and one fp32 scale; an
  * element stands for code * scale.  block_tokens is 16, 32, 64 or 128; D is
  * 64, 128 or 256.  The codes 0x7F and 0xFF (NaN) are never written by
- * e0_kv_append; e0_attn_decode reads them as +-480. */
+ * e0_kv_append; what a query gets that sees a token with such a code is not
+ * specified. */
 typedef struct e0_kv_cache {
     uint8_t* k;              /* device [n_blocks][Hkv][block_tokens][D], 16-byte aligned */
     uint8_t* v;              /* the same for the values                                  */
@@ -604,7 +605,7 @@ size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * negative or needs more than max_blocks blocks raises E0_ST_BAD_LENGTH and its
  * queries see nothing; a cu_q that is negative, falls or gives more than max_q
  * queries raises it too and that sequence's rows are left as they were.  A block id out of range raises E0_ST_BAD_BLOCK and its tokens are
- * not seen.  The result does not depend on how blocks are laid out in the pool, and equal calls
+ * not seen.  A scale of values below 2^-100 counts as 2^-100.  The result does not depend on how blocks are laid out in the pool, and equal calls
  * give equal bits.  Any max_q; the call is made for decode steps and short
  * runs of tokens (every 8 query rows of a KV head read the sequence once more).  Errors: NULL
  * pointers -> E0_ERR_NULL; sizes not positive, Hq no multiple of Hkv,

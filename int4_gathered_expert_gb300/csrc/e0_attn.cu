@@ -10,38 +10,50 @@ namespace {
 // out = softmax(scale q K^T) V in one pass over the context with the running
 // maximum and sum.  A job is one (sequence, KV head, 8 query rows): the rows are
 // the query heads of the group and the sequence's new tokens, token major.  A
-// job's context is cut into units of 64 positions, and the units of all jobs,
-// one after another, are dealt out evenly to the thread blocks: every block
-// reads the same number of bytes whatever the lengths are.  A job that ends up on
-// several blocks leaves one partial result (maximum, sum, unscaled output) on
-// each, at most two a block, and k_attn_join adds them in order.
+// job's context is cut into units, and the units of all jobs, one after another,
+// are dealt out evenly to the thread blocks: every block reads the same number
+// of bytes whatever the lengths are.  A job that ends up on several blocks
+// leaves one partial result (maximum, sum, unscaled output) on each, at most two
+// a block, and k_attn_join adds them in order.
 //
-// In a block, warp w takes positions 16w..16w+15 of every unit.  Products run
-// on the tensor cores (16 x 8 x 16, fp16 operands, fp32 accumulation).  e4m3
-// codes widen to fp16 exactly.  The 16 operand rows hold the 8 query rows twice:
-// rows 0..7 the fp16 part, rows 8..15 the rest of the value, so neither q nor the
-// probabilities lose bits that matter (22 significant bits), at no cost: a
-// decode step has few rows and the kernel is bound by reading the cache.
+// A unit is one step of each of a block's warps.  Products run on the tensor
+// cores (16 x 8 x 16, fp16 operands, fp32 accumulation); e4m3 codes widen to fp16
+// exactly.  The 16 operand rows hold the 8 query rows twice: rows 0..7 the fp16
+// part, rows 8..15 the rest of the value, so neither q nor the probabilities
+// lose bits that matter (22 significant bits), at no cost: a decode step has few
+// rows and the kernel is bound by reading the cache.
 // A warp's codes come through its own ring in shared memory, copied some steps
 // ahead, so warps never wait for one another inside a job.  Operand layouts are
 // chosen so that every lane reads 16 bytes at a time: the order of D inside the
 // first product and of the output columns in the second are permuted (the same
 // permutation on both operands).
 // The scale of a block of keys multiplies the scores; that of the values goes into
-// the probabilities relative to the largest one seen (a running reference
-// like the maximum's), so that they stay in fp16's range.
+// the exponent: with t_j = score_j + log2(scale_j) and m the running maximum of
+// t, the weights of the codes are 2^(t_j - m + 15), which fills fp16's range
+// whatever the scales are (the rest of a weight goes in times 2^12, so weights down
+// to 2^-51 of the largest count), and the softmax's sum is that of the weights
+// over their scales.
 
-constexpr int UNIT = 64;
 constexpr int ROWS = 8;
 constexpr int AT_WARPS = 4;
-constexpr int STEP = 16;  // positions a warp takes at once
-static_assert(UNIT == AT_WARPS * STEP, "a warp takes one step of each unit");
 
-// Steps whose copies a warp has under way (its ring in shared memory).
+// SUBS: 16-position pieces (the smallest block) of a warp's step.  A step costs a
+// chain of dependent instructions (products, maximum, exponentials, products)
+// whatever its length, so it is as long as registers and the ring allow.
+// STAGES: steps a warp's ring holds; all but one are under way.
 template <int D>
-struct Ring {
-    static constexpr int STAGES = D == 256 ? 3 : D == 128 ? 6 : 8;
+struct Tile {
+    static constexpr int SUBS = D == 256 ? 1 : 2;
+    static constexpr int STEP = 16 * SUBS;
+    static constexpr int UNIT = AT_WARPS * STEP;
+    static constexpr int STAGES = D == 64 ? 5 : 3;
     static constexpr int BYTES = 2 * STEP * D;  // keys, then values
+};
+
+// What a block that starts a job which goes on in the next ones leaves for the join.
+struct Cut {
+    int parts;  // 0: nothing
+    int row0, tile, head, rows;
 };
 
 struct AttnArgs {
@@ -57,9 +69,10 @@ struct AttnArgs {
     float* lse;
     float* part_o;    // [2 * blocks][ROWS][D]
     float2* part_ml;  // [2 * blocks][ROWS]
+    Cut* cuts;        // [blocks]
     uint32_t* st;
     int64_t q_ld, out_ld;
-    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks;
+    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks, unit;
     float scale;
 };
 
@@ -80,8 +93,8 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     if (s.ctx < 0 || (long long)s.ctx > ((long long)A.max_blocks << A.shift)) bad = true, s.ctx = 0;
     if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
     s.low = A.window > 0 ? max(s.ctx - s.n + 1 - A.window, 0) : 0;
-    s.first = s.low / UNIT;
-    s.units = (s.ctx + UNIT - 1) / UNIT - s.first;
+    s.first = s.low / A.unit;
+    s.units = (int)(((long long)s.ctx + A.unit - 1) / A.unit) - s.first;
     if (s.units < 1) s.units = 1;  // a job without context still writes its rows
     const int G = A.Hq / A.Hkv;
     s.tiles = (int)(((long long)s.n * G + ROWS - 1) / ROWS);
@@ -95,6 +108,7 @@ E0_DEV long long schedule(const AttnArgs& A, long long* first, long long* red, b
     long long sum = 0;
     for (int i = 0; i < per && b0 + i < A.B; ++i) {
         const Seq s = seq_of(A, b0 + i, tell);
+        first[b0 + i] = sum;  // from the thread's own first sequence on, for now
         sum += (long long)s.units * s.tiles * A.Hkv;
     }
     long long inc = sum;
@@ -110,12 +124,7 @@ E0_DEV long long schedule(const AttnArgs& A, long long* first, long long* red, b
         if (i < warp) base += red[i];
         total += red[i];
     }
-    long long at = base + inc - sum;
-    for (int i = 0; i < per && b0 + i < A.B; ++i) {
-        const Seq s = seq_of(A, b0 + i, false);
-        first[b0 + i] = at;
-        at += (long long)s.units * s.tiles * A.Hkv;
-    }
+    for (int i = 0; i < per && b0 + i < A.B; ++i) first[b0 + i] += base + inc - sum;
     if (threadIdx.x == 0) first[A.B] = total;
     __syncthreads();
     return total;
@@ -150,14 +159,21 @@ E0_DEV Job job_at(const AttnArgs& A, const long long* first, long long unit) {
     return j;
 }
 
-// Two e4m3 codes -> an fp16 pair times 2^-8, exact (NaN codes read as +-480 *
-// 2^-8, so what a masked place holds cannot spread): sel picks each code's byte and
-// eight copies of its sign, the shift moves exponent and mantissa to where fp16
-// has them, and the mask leaves one sign.
-E0_DEV uint32_t widen(uint32_t a, uint32_t b, uint32_t sel) {
+// a's and b's codes at byte (sel & 3) as an fp16 pair: interleave, widen.
+E0_DEV uint32_t widen_pair(uint32_t a, uint32_t b, int byte) {
     uint32_t p;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(a), "r"(b), "r"(sel));
-    return (p << 7) & 0xBF80BF80u;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(a), "r"(b), "r"(0x40u + 0x11u * byte));
+    return e4m3x2_to_half2((uint16_t)p);
+}
+// NaN codes (0x7F, 0xFF) of a word -> 0.
+E0_DEV uint32_t without_nan(uint32_t w) {
+    const uint32_t m = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bit 7 where the code is NaN
+    return w & ~(m | (m - (m >> 7)));
+}
+E0_DEV float exp2_of(float x) {  // 2 ulp; results below 2^-126 are 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 E0_DEV void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -170,12 +186,12 @@ E0_DEV uint32_t half2_of(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// The fp16 part of a pair and what it leaves.
-E0_DEV void split_half(float a, float b, uint32_t& hi, uint32_t& lo) {
+// The fp16 part of a pair and what it leaves, times `up`.
+E0_DEV void split_half(float a, float b, uint32_t& hi, uint32_t& lo, float up = 1.f) {
     const __half2 h = __floats2half2_rn(a, b);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     const float2 f = __half22float2(h);
-    lo = half2_of(a - f.x, b - f.y);
+    lo = half2_of((a - f.x) * up, (b - f.y) * up);
 }
 
 E0_DEV float quad_sum(float v) {
@@ -189,13 +205,16 @@ E0_DEV float quad_max(float v) {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr float LEAST_SCALE = 7.8886090522101181e-31f;  // 2^-100, the least that e0_kv_append writes
+constexpr float LIFT = 15.f;                            // the largest weight is 2^LIFT
+constexpr float REST = 4096.f;                          // what the rests of the weights go in times
 
 template <int D>
 struct AttnSmem {
-    uint8_t ring[AT_WARPS][Ring<D>::STAGES][Ring<D>::BYTES];  // a warp's output at the end of a job
+    uint8_t ring[AT_WARPS][Tile<D>::STAGES][Tile<D>::BYTES];  // a warp's output at the end of a job
     uint32_t q[D / 16][32][4];
-    float2 scales[AT_WARPS][Ring<D>::STAGES];  // of the step's keys and values; x < 0: the step is not seen
-    float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS], r[AT_WARPS];
+    float4 scales[AT_WARPS][Tile<D>::STAGES][2];  // of a piece: keys' scale (< 0: not seen), values' log2 and inverse
+    float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS];
     float f[ROWS];
     long long red[AT_WARPS];
 };
@@ -250,21 +269,74 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     const int G = A.Hq / A.Hkv, bs = 1 << A.shift;
     constexpr int KC = D / 64;          // 16-byte chunks of a key row a lane reads
     constexpr int NT = D / 8;           // output tiles
-    constexpr int STAGES = Ring<D>::STAGES;
     constexpr int VC = D >= 128 ? D / 128 : 1;  // 16-byte chunks of a value row
+    constexpr int SUBS = Tile<D>::SUBS, STEP = Tile<D>::STEP, UNIT = Tile<D>::UNIT, STAGES = Tile<D>::STAGES;
+    constexpr int AHEAD = 32 / SUBS;    // steps whose block ids the lanes hold
+    Cut cut = {0, 0, 0, 0, 0};
 
     while (u < u1) {
         const Job j = job_at(A, first, u);
         const int c0 = (int)(u - j.first);
         const int c1 = (int)(min(j.first + j.s.units, u1) - j.first);
-        // ---- the job's queries as operand fragments: warps share them through shared memory
         const int rr = j.tile * ROWS + gid;  // this lane's query row
         const bool row_ok = rr < j.s.n * G;
         const int qi = rr / G;
         const int hq = j.head * G + rr % G;
         const int last = j.s.ctx - j.s.n + qi;  // the last position that the row sees
         const int low = A.window > 0 ? last - A.window + 1 : 0;
+        // what every row of the tile sees
+        const int last_all = j.s.ctx - j.s.n + j.tile * ROWS / G;
+        const int low_all = A.window > 0 ? j.s.ctx - A.window : 0;
         __syncthreads();  // the former job's shared memory has been read
+
+        // block ids and scales of the next pieces, one a lane
+        int my_id = -1;
+        float4 my_sc = make_float4(-1.f, 0.f, 0.f, 0.f);
+        const auto look_up = [&](int c) {
+            const int cc = c + lane / SUBS, pos = (j.s.first + cc) * UNIT + STEP * warp + 16 * (lane % SUBS);
+            my_id = -1;
+            my_sc = make_float4(-1.f, 0.f, 0.f, 0.f);
+            if (cc < c1 && pos < j.s.ctx && pos + 16 > j.s.low) {
+                my_id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
+                if (my_id >= 0 && my_id < A.n_blocks) {
+                    const size_t i = (size_t)my_id * A.Hkv + j.head;
+                    const float v = fmaxf(A.vs[i], LEAST_SCALE);
+                    my_sc = make_float4(A.ks[i], log2f(v), 1.f / v, 0.f);
+                } else {
+                    my_id = -1;
+                    set_status(A.st, E0_ST_BAD_BLOCK);
+                }
+            }
+        };
+        int in_stage = 0, in_at = 0;  // where the next copy goes; its place among the lanes' ids
+        const auto issue = [&](int c) {
+            if (c < c1) {
+                if (in_at == 0) look_up(c);
+#pragma unroll
+                for (int h = 0; h < SUBS; ++h) {
+                    const int from = in_at * SUBS + h;
+                    const int id = __shfl_sync(0xffffffffu, my_id, from);
+                    if (lane == from) S.scales[warp][in_stage][h] = my_sc;
+                    if (id >= 0) {
+                        const int pos = (j.s.first + c) * UNIT + STEP * warp + 16 * h;
+                        const size_t at = ((((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1))) * D + 16 * lane;
+                        uint8_t* dst = S.ring[warp][in_stage] + h * 16 * D;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            const int r = (i * 32 + lane) / (D / 16), ch = (i * 32 + lane) % (D / 16);
+                            copy16(dst + 16 * key_chunk<D>(r, ch), A.k + at + 512 * i);
+                            copy16(dst + STEP * D + 16 * value_chunk<D>(r, ch), A.v + at + 512 * i);
+                        }
+                    }
+                }
+                if (++in_at == AHEAD) in_at = 0;
+                if (++in_stage == STAGES) in_stage = 0;
+            }
+            copy_commit();
+        };
+        for (int i = 0; i < STAGES - 1; ++i) issue(c0 + i);
+
+        // ---- the job's queries as operand fragments: warps share them through shared memory
         if (warp == 0) {
             float x[KC][16];
             uint32_t m = 0;
@@ -295,10 +367,10 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     split_half(x[c][4 * i + 2] * down, x[c][4 * i + 3] * down, a[2], a[3]);
                     *reinterpret_cast<uint4*>(S.q[4 * c + i][lane]) = make_uint4(a[0], a[1], a[2], a[3]);
                 }
-            // what the product lacks: the power of two, the codes' 2^8, the scale, log2 e
+            // what the product lacks: the power of two, the scale, log2 e
             if (t4 == 0)
                 S.f[gid] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                                            : __uint_as_float((uint32_t)e << 23) * 256.f * A.scale * LOG2E;
+                                            : __uint_as_float((uint32_t)e << 23) * A.scale * LOG2E;
         }
         __syncthreads();
         const float f = S.f[gid];
@@ -313,146 +385,126 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         float acc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        float mx = -INFINITY, sum = 0.f, ref = 0.f;  // ref: the largest value scale so far
+        float mx = -INFINITY, sum = 0.f;
 
-        // block ids and scales of 32 steps at a time, one a lane
-        int my_id = -1;
-        float2 my_sc = make_float2(-1.f, 0.f);
-        const auto look_up = [&](int c) {
-            const int pos = (j.s.first + c + lane) * UNIT + STEP * warp;
-            my_id = -1;
-            my_sc = make_float2(-1.f, 0.f);
-            if (c + lane < c1 && pos < j.s.ctx && pos + STEP > j.s.low) {
-                my_id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
-                if (my_id >= 0 && my_id < A.n_blocks) {
-                    const size_t i = (size_t)my_id * A.Hkv + j.head;
-                    my_sc = make_float2(A.ks[i], A.vs[i]);
-                } else {
-                    my_id = -1;
-                    set_status(A.st, E0_ST_BAD_BLOCK);
-                }
-            }
-        };
-        const auto issue = [&](int c) {
-            if (c < c1) {
-                const int from = (c - c0) & 31, stage = (c - c0) % STAGES;
-                if (from == 0) look_up(c);
-                const int id = __shfl_sync(0xffffffffu, my_id, from);
-                const float kx = __shfl_sync(0xffffffffu, my_sc.x, from), vx = __shfl_sync(0xffffffffu, my_sc.y, from);
-                if (lane == 0) S.scales[warp][stage] = make_float2(id < 0 ? -1.f : kx, vx);
-                if (id >= 0) {
-                    const int pos = (j.s.first + c) * UNIT + STEP * warp;
-                    const size_t at = ((((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1))) * D + 16 * lane;
-                    uint8_t* dst = S.ring[warp][stage];
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const int r = (i * 32 + lane) / (D / 16), ch = (i * 32 + lane) % (D / 16);
-                        copy16(dst + 16 * key_chunk<D>(r, ch), A.k + at + 512 * i);
-                        copy16(dst + STEP * D + 16 * value_chunk<D>(r, ch), A.v + at + 512 * i);
-                    }
-                }
-            }
-            copy_commit();
-        };
-        for (int i = 0; i < STAGES - 1; ++i) issue(c0 + i);
-
+        int stage = 0;
         for (int c = c0; c < c1; ++c) {
             copy_wait<STAGES - 2>();
             __syncwarp();  // the step has arrived for all lanes, and all have read the one before it
-            const int stage = (c - c0) % STAGES;
-            const float2 sc = S.scales[warp][stage];
-            issue(c + STAGES - 1);
-            if (sc.x < 0.f) continue;
-            const int pos = (j.s.first + c) * UNIT + STEP * warp;
+            float4 sc[SUBS];
+#pragma unroll
+            for (int h = 0; h < SUBS; ++h) sc[h] = S.scales[warp][stage][h];
             const uint8_t* kp = S.ring[warp][stage];
+            if (++stage == STAGES) stage = 0;
+            issue(c + STAGES - 1);
+            if (sc[0].x < 0.f && sc[SUBS - 1].x < 0.f) continue;
+            const int pos = (j.s.first + c) * UNIT + STEP * warp;
+            // whether some row does not see all of the step: masks, and codes that may be anything
+            const bool edge = pos + STEP - 1 > last_all || pos < low_all || sc[0].x < 0.f || sc[SUBS - 1].x < 0.f;
             const uint8_t* vp = kp + STEP * D;
-            float s[2][4];
+            float s[2 * SUBS][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+            for (int h = 0; h < 2 * SUBS; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
 #pragma unroll
-                for (int i = 0; i < KC; ++i) {
-                    const uint4 kw = *reinterpret_cast<const uint4*>(kp + 16 * key_chunk<D>(8 * h + gid, 4 * i + t4));
-                    const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+            for (int i = 0; i < KC; ++i) {
+                uint4 kw[2 * SUBS];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t b0 = widen(w[k], 0, 0x9180), b1 = widen(w[k], 0, 0xB3A2);
-                        if constexpr (D <= 128) {
-                            const uint32_t(&a)[4] = qf[4 * i + k];
-                            mma(s[h], a[0], a[1], a[2], a[3], b0, b1);
-                        } else {
-                            const uint4 a = *reinterpret_cast<const uint4*>(S.q[4 * i + k][lane]);
-                            mma(s[h], a.x, a.y, a.z, a.w, b0, b1);
-                        }
+                for (int h = 0; h < 2 * SUBS; ++h)
+                    kw[h] = *reinterpret_cast<const uint4*>(kp + 16 * key_chunk<D>(8 * h + gid, 4 * i + t4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t a[4];
+                    if constexpr (D <= 128) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) a[x] = qf[4 * i + k][x];
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4*>(S.q[4 * i + k][lane]);
+                        a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2 * SUBS; ++h) {
+                        const uint32_t w = k == 0 ? kw[h].x : k == 1 ? kw[h].y : k == 2 ? kw[h].z : kw[h].w;
+                        mma(s[h], a[0], a[1], a[2], a[3], e4m3x2_to_half2((uint16_t)w), e4m3x2_to_half2((uint16_t)(w >> 16)));
                     }
                 }
             }
-            // scores in units of log2, masked; this lane: row gid, tokens 8h + 2t, + 1
-            float p[2][2], top = -INFINITY;
-            const float fk = f * sc.x;
+            // t (in units of log2); this lane: row gid, positions 8h + 2t, + 1
+            float p[2 * SUBS][2], top = mx;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2 * SUBS; ++h) {
+                const float fk = f * sc[h / 2].x;
+                p[h][0] = fmaf(s[h][0] + s[h][2], fk, sc[h / 2].y);
+                p[h][1] = fmaf(s[h][1] + s[h][3], fk, sc[h / 2].y);
+            }
+            if (edge) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int at_pos = pos + 8 * h + 2 * t4 + i;
-                    const bool seen = row_ok && at_pos <= last && at_pos >= low;
-                    p[h][i] = seen ? (s[h][i] + s[h][2 + i]) * fk : -INFINITY;
-                    top = fmaxf(top, p[h][i]);
-                }
-            top = fmaxf(mx, quad_max(top));
+                for (int h = 0; h < 2 * SUBS; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = pos + 8 * h + 2 * t4 + i;
+                        const bool seen = row_ok && at <= last && at >= low && !(sc[h / 2].x < 0.f);
+                        if (!seen) p[h][i] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2 * SUBS; ++h) top = fmaxf(top, fmaxf(p[h][0], p[h][1]));
+            top = quad_max(top);
             const float base = top == -INFINITY ? 0.f : top;
-            const float shrink = exp2f(mx - base);
+            const float keep = exp2_of(mx - base);
             mx = top;
-            const float ref1 = fmaxf(ref, sc.y);
-            const float keep = ref1 > 0.f ? shrink * (ref / ref1) : shrink;
-            const float vrel = ref1 > 0.f ? sc.y / ref1 : 0.f;
-            ref = ref1;
-            sum *= shrink;
-            uint32_t ph[2], pl[2];
+            sum *= keep;
+            uint32_t ph[2 * SUBS], pl[2 * SUBS];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                p[h][0] = exp2f(p[h][0] - base);
-                p[h][1] = exp2f(p[h][1] - base);
-                sum += p[h][0] + p[h][1];
-                split_half(p[h][0] * vrel, p[h][1] * vrel, ph[h], pl[h]);
+            for (int h = 0; h < 2 * SUBS; ++h) {
+                p[h][0] = exp2_of(p[h][0] - (base - LIFT));
+                p[h][1] = exp2_of(p[h][1] - (base - LIFT));
+                sum = fmaf(p[h][0] + p[h][1], sc[h / 2].z, sum);
+                split_half(p[h][0], p[h][1], ph[h], pl[h], REST);
             }
             if (__any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[n][0] *= keep, acc[n][1] *= keep, acc[n][2] *= keep, acc[n][3] *= keep;
             }
 #pragma unroll
-            for (int h = 0; h < VC; ++h) {
-                uint32_t w[4][4];  // tokens 2t, 2t+1, 8+2t, 9+2t
+            for (int b = 0; b < SUBS; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 2 * t4 + (i & 1) + 8 * (i >> 1);
-                    if constexpr (D == 64) {
-                        const uint2 x = *reinterpret_cast<const uint2*>(vp + 16 * value_chunk<D>(r, gid >> 1) + 8 * (gid & 1));
-                        w[i][0] = x.x, w[i][1] = x.y;
-                    } else {
-                        const uint4 x = *reinterpret_cast<const uint4*>(vp + 16 * value_chunk<D>(r, 8 * h + gid));
-                        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                for (int h = 0; h < VC; ++h) {
+                    uint32_t w[4][4];  // tokens 2t, 2t+1, 8+2t, 9+2t
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * b + 2 * t4 + (i & 1) + 8 * (i >> 1);
+                        if constexpr (D == 64) {
+                            const uint2 x =
+                                *reinterpret_cast<const uint2*>(vp + 16 * value_chunk<D>(r, gid >> 1) + 8 * (gid & 1));
+                            w[i][0] = x.x, w[i][1] = x.y;
+                        } else {
+                            const uint4 x = *reinterpret_cast<const uint4*>(vp + 16 * value_chunk<D>(r, 8 * h + gid));
+                            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                        }
                     }
-                }
+                    if (edge) {  // a probability of 0 must not meet a NaN
 #pragma unroll
-                for (int n = 0; n < (D == 64 ? 8 : 16); ++n) {
-                    const uint32_t sel = 0xC480u + 0x1111u * (n & 3);  // byte and sign of a's and b's n-th code
-                    mma(acc[16 * h + n], ph[0], pl[0], ph[1], pl[1], widen(w[0][n / 4], w[1][n / 4], sel),
-                        widen(w[2][n / 4], w[3][n / 4], sel));
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < (D == 64 ? 2 : 4); ++k) w[i][k] = without_nan(w[i][k]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < (D == 64 ? 8 : 16); ++n)
+                        mma(acc[16 * h + n], ph[2 * b], pl[2 * b], ph[2 * b + 1], pl[2 * b + 1],
+                            widen_pair(w[0][n / 4], w[1][n / 4], n & 3), widen_pair(w[2][n / 4], w[3][n / 4], n & 3));
                 }
-            }
         }
         copy_wait<0>();
+        __syncwarp();
         // ---- the warps' results together
         sum = quad_sum(sum);
         if (t4 == 0) S.m[warp][gid] = mx, S.l[warp][gid] = sum;
-        if (lane == 0) S.r[warp] = ref * 256.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             // tile n, columns 2t and 2t+1: elements 16 * column + n % 16 of its 128 (8 * column + n of 64)
             const int d0 = D == 64 ? 16 * t4 + n : 128 * (n / 16) + 32 * t4 + n % 16;
-            warp_out<D>(S, warp)[gid * (D + 4) + d0] = acc[n][0] + acc[n][2];
-            warp_out<D>(S, warp)[gid * (D + 4) + d0 + (D == 64 ? 8 : 16)] = acc[n][1] + acc[n][3];
+            warp_out<D>(S, warp)[gid * (D + 4) + d0] = fmaf(acc[n][2], 1.f / REST, acc[n][0]);
+            warp_out<D>(S, warp)[gid * (D + 4) + d0 + (D == 64 ? 8 : 16)] = fmaf(acc[n][3], 1.f / REST, acc[n][1]);
         }
         __syncthreads();
         const bool whole = c0 == 0 && c1 == j.s.units;
@@ -469,47 +521,83 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             for (int w = 0; w < AT_WARPS; ++w) {
                 const float k = exp2f(S.m[w][r] - base);
                 l += k * S.l[w][r];
-                o += k * S.r[w] * warp_out<D>(S, w)[r * (D + 4) + d];
+                o += k * warp_out<D>(S, w)[r * (D + 4) + d];
             }
             if (whole) {
                 const size_t tok = (size_t)j.s.row0 + row / G;
                 const int head = j.head * G + row % G;
                 store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
-                if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * LN2 : -INFINITY;
+                if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
             } else {
                 A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
                 if (d == 0) A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
             }
         }
+        if (!whole && c0 == 0)
+            cut = {(int)((j.first + j.s.units - 1) / per) - (int)blockIdx.x + 1, j.s.row0, j.tile, j.head,
+                   min(ROWS, j.s.n * G - j.tile * ROWS)};
         u = j.first + c1;
     }
+    if (threadIdx.x == 0) A.cuts[blockIdx.x] = cut;
 }
 
-// A block boundary that falls inside a job, the first one in it: join the job's
-// partial results, one row a block (y).  A thread adds four columns of every
-// JOIN_GROUPS-th partial result, then the groups' sums are added.
+// Join the partial results of the job that block x started and did not end.
+// Few parts: one thread block takes all rows, a thread four columns of a row.
+// Many: one row a thread block (y), a thread adds four columns of every
+// GROUPS-th part, then the groups' sums are added.
 constexpr int JOIN_THREADS = 256;
-constexpr int JOIN_PARTS = 512;  // partial results a job can have: the thread blocks
+constexpr int JOIN_PARTS = 512;  // parts a job can have: the thread blocks
+constexpr int JOIN_FEW = 8;
 
 template <int D, int TY>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
     constexpr int GROUPS = JOIN_THREADS / (D / 4);
-    extern __shared__ __align__(16) char join_sm[];
-    long long* first = reinterpret_cast<long long*>(join_sm);
-    __shared__ long long red[JOIN_THREADS / 32];
     __shared__ float weight[JOIN_PARTS];
     __shared__ float part[GROUPS][D + 4];
     __shared__ float wm[JOIN_THREADS / 32], wl[JOIN_THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long total = schedule(A, first, red, false);
-    const long long per = units_per_block(A, total);
-    const long long edge = (blockIdx.x + 1) * per;
-    Job j = {};
-    if (edge < total) j = job_at(A, first, edge);
-    const int G = A.Hq / A.Hkv, r = blockIdx.y, row = j.tile * ROWS + r;
+    const int g = tid / (D / 4), d4 = tid % (D / 4) * 4, G = A.Hq / A.Hkv, b0 = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
-    if (edge >= total || j.first == edge || j.first < edge - per || row >= j.s.n * G) return;
-    const int b0 = blockIdx.x, n = (int)((j.first + j.s.units - 1) / per) - b0 + 1;
+    const Cut cut = A.cuts[b0];
+    const int n = cut.parts;
+    const auto write = [&](int r, int d, float o, float m, float l) {
+        const int row = cut.tile * ROWS + r, head = cut.head * G + row % G;
+        const size_t tok = (size_t)cut.row0 + row / G;
+        store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
+        if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
+    };
+    if (n <= JOIN_FEW) {
+        if (blockIdx.y != 0) return;
+        for (int r = g; r < cut.rows && n > 0; r += GROUPS) {
+            const auto slot = [&](int i) { return ((size_t)2 * (b0 + i) + (i == 0)) * ROWS + r; };
+            float2 ml[JOIN_FEW];
+            float4 x[JOIN_FEW];
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < JOIN_FEW; ++i)
+                if (i < n) {
+                    ml[i] = A.part_ml[slot(i)];
+                    x[i] = *reinterpret_cast<const float4*>(A.part_o + slot(i) * D + d4);
+                    m = fmaxf(m, ml[i].x);
+                }
+            const float base = m == -INFINITY ? 0.f : m;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < JOIN_FEW; ++i)
+                if (i < n) {
+                    const float k = exp2f(ml[i].x - base);
+                    l += k * ml[i].y;
+                    o.x += k * x[i].x, o.y += k * x[i].y, o.z += k * x[i].z, o.w += k * x[i].w;
+                }
+            write(r, d4, o.x, m, l);
+            write(r, d4 + 1, o.y, m, l);
+            write(r, d4 + 2, o.z, m, l);
+            write(r, d4 + 3, o.w, m, l);
+        }
+        return;
+    }
+    const int r = blockIdx.y;
+    if (r >= cut.rows) return;
     // the first block left its part in its second slot, the others in their first
     const auto slot = [&](int i) { return ((size_t)2 * (b0 + i) + (i == 0)) * ROWS + r; };
     float m = -INFINITY;
@@ -532,9 +620,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
     l = 0.f;
 #pragma unroll
     for (int w = 0; w < JOIN_THREADS / 32; ++w) l += wl[w];
-    const int g = tid / (D / 4), d4 = tid % (D / 4) * 4;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = g; i < n; i += GROUPS) {
         const float4 x = *reinterpret_cast<const float4*>(A.part_o + slot(i) * D + d4);
         const float k = weight[i];
@@ -542,15 +629,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
     }
     *reinterpret_cast<float4*>(&part[g][d4]) = o;
     __syncthreads();
-    const size_t tok = (size_t)j.s.row0 + row / G;
-    const int head = j.head * G + row % G;
     if (tid < D) {
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < GROUPS; ++k) v += part[k][tid];
-        store_out<TY>(A, tok, head * D + tid, l > 0.f || l != l ? v / l : 0.f);
+        write(r, tid, v, m, l);
     }
-    if (A.lse && tid == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * LN2 : -INFINITY;
 }
 
 constexpr int BLOCKS_PER_SM = 2;
@@ -562,18 +646,17 @@ int attn_blocks() {
 
 template <int D, int TY>
 int launch(AttnArgs a, cudaStream_t s) {
+    a.unit = Tile<D>::UNIT;
     const size_t sched = (size_t)(a.B + 1) * sizeof(long long);
     const size_t sm = sizeof(AttnSmem<D>) + sched;
     if (cudaFuncSetAttribute(k_attn<D, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
         return E0_ERR_CUDA;
     k_attn<D, TY><<<a.blocks, AT_WARPS * 32, sm, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
-    // the join starts while the blocks above still run, works out its schedule
-    // and then waits for all of them
+    // the join's blocks start while those above still run and wait for all of them
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.blocks - 1, ROWS);
+    cfg.gridDim = dim3(a.blocks, ROWS);
     cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.dynamicSmemBytes = sched;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -592,7 +675,7 @@ int launch_d(const AttnArgs& a, int D, cudaStream_t s) {
 
 size_t attn_ws_bytes(int D) {
     const size_t slots = 2 * (size_t)attn_blocks();
-    return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2);
+    return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2) + slots / 2 * sizeof(Cut);
 }
 
 int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
@@ -604,6 +687,7 @@ int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
     a.blocks = attn_blocks();
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + 2 * (size_t)a.blocks * ROWS * c->D);
+    a.cuts = reinterpret_cast<Cut*>(a.part_ml + 2 * (size_t)a.blocks * ROWS);
     a.st = st, a.q_ld = q_ld, a.out_ld = out_ld;
     a.B = B, a.max_blocks = max_blocks, a.n_blocks = c->n_blocks, a.Hq = Hq, a.Hkv = c->Hkv, a.max_q = max_q;
     a.window = window, a.scale = scale;
