@@ -604,7 +604,8 @@ size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * on are left as they were.  Statistics and sums are fp32.  A ctx_len that is
  * negative or needs more than max_blocks blocks raises E0_ST_BAD_LENGTH and its
  * queries see nothing; a cu_q that is negative, falls or gives more than max_q
- * queries raises it too and that sequence's rows are left as they were.  A block id out of range raises E0_ST_BAD_BLOCK and its tokens are
+ * queries raises it too and that sequence's rows are left as they were; so does a
+ * call whose (query tile, KV head, 64 positions) are more than 2^31, and writes nothing.  A block id out of range raises E0_ST_BAD_BLOCK and its tokens are
  * not seen.  A scale of values below 2^-100 counts as 2^-100.  The result does not depend on how blocks are laid out in the pool, and equal calls
  * give equal bits.  Any max_q; the call is made for decode steps and short
  * runs of tokens (every 8 query rows of a KV head read the sequence once more).  Errors: NULL

@@ -29,10 +29,12 @@ namespace {
 // permutation on both operands).
 // The scale of a block of keys multiplies the scores; that of the values goes into
 // the exponent: with t_j = score_j + log2(scale_j) and m the running maximum of
-// t, the weights of the codes are 2^(t_j - m + 15), which fills fp16's range
-// whatever the scales are (the rest of a weight goes in times 2^12, so weights down
-// to 2^-51 of the largest count), and the softmax's sum is that of the weights
-// over their scales.
+// t, the weights of the codes are 2^(t_j - m + 7), at most 2^15 because m follows
+// only where t has grown by more than 8 (a row's output is then scaled once or
+// twice in a job, not at every new maximum).  That fills fp16's range whatever the
+// scales are: the rest of a weight goes in times 2^12, so weights down to 2^-43
+// of the largest count.  The softmax's sum is that of the weights over their
+// scales.
 
 constexpr int ROWS = 8;
 constexpr int AT_WARPS = 4;
@@ -48,11 +50,15 @@ struct Tile {
     static constexpr int UNIT = AT_WARPS * STEP;
     static constexpr int STAGES = D == 64 ? 5 : 3;
     static constexpr int BYTES = 2 * STEP * D;  // keys, then values
+    // what a job costs beside its units (block ids, queries, result: 3 us, in which
+    // the block's share of the memory's rate reads 64 KB), in units
+    static constexpr int JOB_COST = 65536 / (AT_WARPS * BYTES);
 };
 
-// What a block that starts a job which goes on in the next ones leaves for the join.
+// What a block leaves for the join: the job that it started and did not end, and
+// the one that it went on with.
 struct Cut {
-    int parts;  // 0: nothing
+    int parts, block;  // blocks that have a part (0: no job), the first of them
     int row0, tile, head, rows;
 };
 
@@ -69,10 +75,10 @@ struct AttnArgs {
     float* lse;
     float* part_o;    // [2 * blocks][ROWS][D]
     float2* part_ml;  // [2 * blocks][ROWS]
-    Cut* cuts;        // [blocks]
+    Cut* cuts;        // [blocks][2]
     uint32_t* st;
     int64_t q_ld, out_ld;
-    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks, unit;
+    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks, unit, job_cost;
     float scale;
 };
 
@@ -101,61 +107,74 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     return s;
 }
 
-// First unit of every sequence's jobs, in shared memory; the total.
-E0_DEV long long schedule(const AttnArgs& A, long long* first, long long* red, bool tell) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+// A schedule longer than this is not run (it would read for seconds).
+constexpr uint32_t MOST_UNITS = 0x7FFFFFFFu;
+
+E0_DEV uint32_t add_units(uint32_t a, uint32_t b) { return min(a + b, MOST_UNITS); }
+
+// Every sequence's first place in the schedule, in shared memory; its length.
+E0_DEV uint32_t schedule(const AttnArgs& A, uint32_t* first, uint32_t* red, bool tell) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (A.B + blockDim.x - 1) / blockDim.x, b0 = threadIdx.x * per;
-    long long sum = 0;
+    uint32_t sum = 0;
     for (int i = 0; i < per && b0 + i < A.B; ++i) {
         const Seq s = seq_of(A, b0 + i, tell);
         first[b0 + i] = sum;  // from the thread's own first sequence on, for now
-        sum += (long long)s.units * s.tiles * A.Hkv;
+        const unsigned long long n = (unsigned long long)(s.units + A.job_cost) * s.tiles * A.Hkv;
+        sum = add_units(sum, n < MOST_UNITS ? (uint32_t)n : MOST_UNITS);
     }
-    long long inc = sum;
+    uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc = add_units(inc, x);
     }
     if (lane == 31) red[warp] = inc;
     __syncthreads();
-    long long base = 0, total = 0;
-    for (int i = 0; i < nw; ++i) {
-        if (i < warp) base += red[i];
-        total += red[i];
+    uint32_t base = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < AT_WARPS; ++i) {
+        if (i < warp) base = add_units(base, red[i]);
+        total = add_units(total, red[i]);
     }
-    for (int i = 0; i < per && b0 + i < A.B; ++i) first[b0 + i] += base + inc - sum;
-    if (threadIdx.x == 0) first[A.B] = total;
+    for (int i = 0; i < per && b0 + i < A.B; ++i) first[b0 + i] = add_units(first[b0 + i], base + inc - sum);
+    if (total >= MOST_UNITS) {
+        if (tell && threadIdx.x == 0) set_status(A.st, E0_ST_BAD_LENGTH);
+        total = 0;
+    }
     __syncthreads();
     return total;
 }
 
-// Units of a block: the same for all, at least 2 (a join costs more than a unit).
-E0_DEV long long units_per_block(const AttnArgs& A, long long total) {
-    const long long per = (total + A.blocks - 1) / A.blocks;
-    return per < 2 ? 2 : per;
+// What of the schedule a block takes: the same for all, and at least a short job.
+E0_DEV uint32_t block_share(const AttnArgs& A, uint32_t total) {
+    const uint32_t per = (total + A.blocks - 1) / A.blocks;
+    return per < A.job_cost + 2 ? A.job_cost + 2 : per;
 }
 
-struct Job {
+// A block's part of a job: units c0..c1-1 of it (none where c1 <= c0).
+struct Span {
     Seq s;
-    int head, tile;
-    long long first;  // its first unit among all
-    int seq;
+    int seq, head, tile, c0, c1;
+    uint32_t first, end;  // the job's place in the schedule; where the part ends there
 };
 
-E0_DEV Job job_at(const AttnArgs& A, const long long* first, long long unit) {
+E0_DEV Span span_at(const AttnArgs& A, const uint32_t* first, uint32_t u, uint32_t u1) {
     int lo = 0, hi = A.B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (first[mid] <= unit) lo = mid; else hi = mid;
+        if (first[mid] <= u) lo = mid; else hi = mid;
     }
-    Job j;
+    Span j;
     j.seq = lo;
     j.s = seq_of(A, lo, false);
-    const int k = (int)((unit - first[lo]) / j.s.units);
+    const uint32_t len = j.s.units + A.job_cost, k = (u - first[lo]) / len;
     j.head = k / j.s.tiles;
     j.tile = k % j.s.tiles;
-    j.first = first[lo] + (long long)k * j.s.units;
+    j.first = first[lo] + k * len;
+    j.end = min(j.first + len, u1);
+    j.c0 = max((int)(u - j.first) - A.job_cost, 0);
+    j.c1 = (int)(j.end - j.first) - A.job_cost;
     return j;
 }
 
@@ -206,7 +225,7 @@ E0_DEV float quad_max(float v) {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LEAST_SCALE = 7.8886090522101181e-31f;  // 2^-100, the least that e0_kv_append writes
-constexpr float LIFT = 15.f;                            // the largest weight is 2^LIFT
+constexpr float LIFT = 7.f, SLACK = 8.f;                // weights are 2^(t - m + LIFT), t at most m + SLACK
 constexpr float REST = 4096.f;                          // what the rests of the weights go in times
 
 template <int D>
@@ -216,13 +235,16 @@ struct AttnSmem {
     float4 scales[AT_WARPS][Tile<D>::STAGES][2];  // of a piece: keys' scale (< 0: not seen), values' log2 and inverse
     float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS];
     float f[ROWS];
-    long long red[AT_WARPS];
+    uint32_t red[AT_WARPS];
 };
 
+// Element d of row r of a warp's output, in its ring's first stage; columns are
+// permuted inside 32 so that what the lanes write at once has 32 banks.
 template <int D>
-E0_DEV float* warp_out(AttnSmem<D>& S, int w) {  // [ROWS][D + 4]
-    static_assert(sizeof(S.ring[0]) >= ROWS * (D + 4) * sizeof(float), "the ring holds a warp's output");
-    return reinterpret_cast<float*>(S.ring[w]);
+E0_DEV float& warp_out(AttnSmem<D>& S, int w, int r, int d) {
+    static_assert(Tile<D>::BYTES >= ROWS * D * sizeof(float), "a stage holds a warp's output");
+    const int key = D == 64 ? 4 * r + (d >> 4) : 4 * r + (d >> 5);
+    return reinterpret_cast<float*>(S.ring[w])[r * D + (d ^ (key & 31))];
 }
 
 // Where the 16-byte chunk c of row r of a step's keys or values stands: chunks
@@ -257,114 +279,141 @@ E0_DEV void store_out(const AttnArgs& A, size_t row, int i, float v) {
 template <int D, int TY>
 __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     typedef typename Elem<TY>::T T;
-    extern __shared__ __align__(16) char attn_sm[];
+    extern __shared__ __align__(128) char attn_sm[];
     AttnSmem<D>& S = *reinterpret_cast<AttnSmem<D>*>(attn_sm);
-    long long* first = reinterpret_cast<long long*>(attn_sm + sizeof(AttnSmem<D>));
+    uint32_t* first = reinterpret_cast<uint32_t*>(attn_sm + sizeof(AttnSmem<D>));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t4 = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long total = schedule(A, first, S.red, blockIdx.x == 0);
-    const long long per = units_per_block(A, total);
-    long long u = blockIdx.x * per;
-    const long long u1 = u + per < total ? u + per : total;
+    const uint32_t total = schedule(A, first, S.red, blockIdx.x == 0);
+    const uint32_t per = block_share(A, total);
+    uint32_t u = blockIdx.x * per;
+    const uint32_t u1 = min(u + per, total);
     const int G = A.Hq / A.Hkv, bs = 1 << A.shift;
     constexpr int KC = D / 64;          // 16-byte chunks of a key row a lane reads
     constexpr int NT = D / 8;           // output tiles
     constexpr int VC = D >= 128 ? D / 128 : 1;  // 16-byte chunks of a value row
     constexpr int SUBS = Tile<D>::SUBS, STEP = Tile<D>::STEP, UNIT = Tile<D>::UNIT, STAGES = Tile<D>::STAGES;
     constexpr int AHEAD = 32 / SUBS;    // steps whose block ids the lanes hold
-    Cut cut = {0, 0, 0, 0, 0};
+    Cut begun = {0, 0, 0, 0, 0, 0}, went_on = {0, 0, 0, 0, 0, 0};
 
-    while (u < u1) {
-        const Job j = job_at(A, first, u);
-        const int c0 = (int)(u - j.first);
-        const int c1 = (int)(min(j.first + j.s.units, u1) - j.first);
-        const int rr = j.tile * ROWS + gid;  // this lane's query row
-        const bool row_ok = rr < j.s.n * G;
-        const int qi = rr / G;
-        const int hq = j.head * G + rr % G;
-        const int last = j.s.ctx - j.s.n + qi;  // the last position that the row sees
-        const int low = A.window > 0 ? last - A.window + 1 : 0;
-        // what every row of the tile sees
-        const int last_all = j.s.ctx - j.s.n + j.tile * ROWS / G;
-        const int low_all = A.window > 0 ? j.s.ctx - A.window : 0;
-        __syncthreads();  // the former job's shared memory has been read
-
-        // block ids and scales of the next pieces, one a lane
-        int my_id = -1;
-        float4 my_sc = make_float4(-1.f, 0.f, 0.f, 0.f);
-        const auto look_up = [&](int c) {
-            const int cc = c + lane / SUBS, pos = (j.s.first + cc) * UNIT + STEP * warp + 16 * (lane % SUBS);
-            my_id = -1;
-            my_sc = make_float4(-1.f, 0.f, 0.f, 0.f);
-            if (cc < c1 && pos < j.s.ctx && pos + 16 > j.s.low) {
-                my_id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
-                if (my_id >= 0 && my_id < A.n_blocks) {
-                    const size_t i = (size_t)my_id * A.Hkv + j.head;
-                    const float v = fmaxf(A.vs[i], LEAST_SCALE);
-                    my_sc = make_float4(A.ks[i], log2f(v), 1.f / v, 0.f);
-                } else {
-                    my_id = -1;
-                    set_status(A.st, E0_ST_BAD_BLOCK);
-                }
+    // the next part that has units
+    Span j;
+    const auto next = [&]() {
+        while (u < u1) {
+            j = span_at(A, first, u, u1);
+            u = j.end;
+            if (j.c1 > j.c0) return true;
+        }
+        return false;
+    };
+    // block ids and scales of the next pieces, one a lane
+    int my_id = -1;
+    float4 my_sc;
+    const auto look_up = [&](int c) {
+        const int cc = c + lane / SUBS, pos = (j.s.first + cc) * UNIT + STEP * warp + 16 * (lane % SUBS);
+        my_id = -1;
+        my_sc = make_float4(-1.f, 0.f, 0.f, 0.f);
+        if (cc < j.c1 && pos < j.s.ctx && pos + 16 > j.s.low) {
+            my_id = A.table[(size_t)j.seq * A.max_blocks + (pos >> A.shift)];
+            if (my_id >= 0 && my_id < A.n_blocks) {
+                const size_t i = (size_t)my_id * A.Hkv + j.head;
+                const float v = fmaxf(A.vs[i], LEAST_SCALE);
+                my_sc = make_float4(A.ks[i], log2f(v), 1.f / v, 0.f);
+            } else {
+                my_id = -1;
+                set_status(A.st, E0_ST_BAD_BLOCK);
             }
-        };
-        int in_stage = 0, in_at = 0;  // where the next copy goes; its place among the lanes' ids
-        const auto issue = [&](int c) {
-            if (c < c1) {
-                if (in_at == 0) look_up(c);
+        }
+    };
+    int in_stage = 0, in_at = 0;  // where the next copy goes; its place among the lanes' ids
+    const auto issue = [&](int c) {
+        if (c < j.c1) {
+            if (in_at == AHEAD) {
+                look_up(c);
+                in_at = 0;
+            }
 #pragma unroll
-                for (int h = 0; h < SUBS; ++h) {
-                    const int from = in_at * SUBS + h;
-                    const int id = __shfl_sync(0xffffffffu, my_id, from);
-                    if (lane == from) S.scales[warp][in_stage][h] = my_sc;
-                    if (id >= 0) {
-                        const int pos = (j.s.first + c) * UNIT + STEP * warp + 16 * h;
-                        const size_t at = ((((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1))) * D + 16 * lane;
-                        uint8_t* dst = S.ring[warp][in_stage] + h * 16 * D;
+            for (int h = 0; h < SUBS; ++h) {
+                const int from = in_at * SUBS + h;
+                const int id = __shfl_sync(0xffffffffu, my_id, from);
+                if (lane == from) S.scales[warp][in_stage][h] = my_sc;
+                if (id >= 0) {
+                    const int pos = (j.s.first + c) * UNIT + STEP * warp + 16 * h;
+                    const size_t at = ((((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1))) * D + 16 * lane;
+                    uint8_t* dst = S.ring[warp][in_stage] + h * 16 * D;
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            const int r = (i * 32 + lane) / (D / 16), ch = (i * 32 + lane) % (D / 16);
-                            copy16(dst + 16 * key_chunk<D>(r, ch), A.k + at + 512 * i);
-                            copy16(dst + STEP * D + 16 * value_chunk<D>(r, ch), A.v + at + 512 * i);
-                        }
+                    for (int i = 0; i < D / 32; ++i) {
+                        const int r = (i * 32 + lane) / (D / 16), ch = (i * 32 + lane) % (D / 16);
+                        copy16(dst + 16 * key_chunk<D>(r, ch), A.k + at + 512 * i);
+                        copy16(dst + STEP * D + 16 * value_chunk<D>(r, ch), A.v + at + 512 * i);
                     }
                 }
-                if (++in_at == AHEAD) in_at = 0;
-                if (++in_stage == STAGES) in_stage = 0;
             }
-            copy_commit();
-        };
-        for (int i = 0; i < STAGES - 1; ++i) issue(c0 + i);
+            ++in_at;
+            if (++in_stage == STAGES) in_stage = 0;
+        }
+        copy_commit();
+    };
+    // the first steps of a part go to the stages but the first, which holds the
+    // former part's output until it has been written
+    const auto begin = [&]() {
+        in_stage = 1, in_at = 0;
+#pragma unroll 1
+        for (int i = 0; i < STAGES - 1; ++i) issue(j.c0 + i);
+    };
+    // this lane's query row: 16 elements of each 64, as they are in memory; a row
+    // beyond the tile's reads the tile's first and counts as zeros
+    constexpr int RAW = TY == E0_F32 ? 4 : 2;
+    uint4 raw[KC][RAW];
+    const auto load_q = [&]() {
+        const int row = j.tile * ROWS + (j.tile * ROWS + gid < j.s.n * G ? gid : 0);
+        const T* p = reinterpret_cast<const T*>(A.q) + (size_t)(j.s.row0 + row / G) * A.q_ld +
+                     (size_t)(j.head * G + row % G) * D + 16 * t4;
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int i = 0; i < RAW; ++i) raw[c][i] = __ldg(reinterpret_cast<const uint4*>(p + 64 * c) + i);
+    };
+    const auto q_of = [&](int c, int i) {  // element i of 16
+        const uint4 u = raw[c][TY == E0_F32 ? i / 4 : i / 8];
+        if constexpr (TY == E0_F32) {
+            const uint32_t w = i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w;
+            return __uint_as_float(w);
+        } else {
+            const uint32_t w = i % 8 < 2 ? u.x : i % 8 < 4 ? u.y : i % 8 < 6 ? u.z : u.w;
+            const float2 f = unpack16<TY>(w);
+            return i % 2 ? f.y : f.x;
+        }
+    };
 
+    bool more = next();
+    if (more) {
+        look_up(j.c0);
+        if (warp == 0) load_q();
+        begin();
+    }
+    while (more) {
         // ---- the job's queries as operand fragments: warps share them through shared memory
         if (warp == 0) {
-            float x[KC][16];
             uint32_t m = 0;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                if (row_ok) {
-                    load_vec<TY, 16>(reinterpret_cast<const T*>(A.q) + (size_t)(j.s.row0 + qi) * A.q_ld + (size_t)hq * D +
-                                         64 * c + 16 * t4, x[c]);
-                } else {
+            for (int c = 0; c < KC; ++c)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[c][i]) & 0x7FFFFFFFu);
-            }
+                for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(q_of(c, i)) & 0x7FFFFFFFu);
+            if (j.tile * ROWS + gid >= j.s.n * G) m = 0;
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             // rows go in times a power of two that brings the largest near 1
             int e = (int)(m >> 23);
             e = e < 27 ? 27 : e > 253 ? 253 : e;
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+            const float down = m == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t a[4];
-                    split_half(x[c][4 * i] * down, x[c][4 * i + 1] * down, a[0], a[1]);
-                    split_half(x[c][4 * i + 2] * down, x[c][4 * i + 3] * down, a[2], a[3]);
+                    split_half(q_of(c, 4 * i) * down, q_of(c, 4 * i + 1) * down, a[0], a[1]);
+                    split_half(q_of(c, 4 * i + 2) * down, q_of(c, 4 * i + 3) * down, a[2], a[3]);
                     *reinterpret_cast<uint4*>(S.q[4 * c + i][lane]) = make_uint4(a[0], a[1], a[2], a[3]);
                 }
             // what the product lacks: the power of two, the scale, log2 e
@@ -372,7 +421,14 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                 S.f[gid] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
                                             : __uint_as_float((uint32_t)e << 23) * A.scale * LOG2E;
         }
-        __syncthreads();
+        __syncthreads();  // and the former part's output and statistics have been read
+        const Span cur = j;
+        const bool row_ok = cur.tile * ROWS + gid < cur.s.n * G;
+        const int last = cur.s.ctx - cur.s.n + (cur.tile * ROWS + gid) / G;  // the last position that the row sees
+        const int low = A.window > 0 ? last - A.window + 1 : 0;
+        // what every row of the tile sees
+        const int last_all = cur.s.ctx - cur.s.n + cur.tile * ROWS / G;
+        const int low_all = A.window > 0 ? cur.s.ctx - A.window : 0;
         const float f = S.f[gid];
         uint32_t qf[D <= 128 ? D / 16 : 1][4];  // registers hold them where there are enough
         if constexpr (D <= 128) {
@@ -387,8 +443,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
         float mx = -INFINITY, sum = 0.f;
 
-        int stage = 0;
-        for (int c = c0; c < c1; ++c) {
+        int stage = 1;
+        for (int c = cur.c0; c < cur.c1; ++c) {
             copy_wait<STAGES - 2>();
             __syncwarp();  // the step has arrived for all lanes, and all have read the one before it
             float4 sc[SUBS];
@@ -398,13 +454,17 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             if (++stage == STAGES) stage = 0;
             issue(c + STAGES - 1);
             if (sc[0].x < 0.f && sc[SUBS - 1].x < 0.f) continue;
-            const int pos = (j.s.first + c) * UNIT + STEP * warp;
+            const int pos = (cur.s.first + c) * UNIT + STEP * warp;
             // whether some row does not see all of the step: masks, and codes that may be anything
             const bool edge = pos + STEP - 1 > last_all || pos < low_all || sc[0].x < 0.f || sc[SUBS - 1].x < 0.f;
             const uint8_t* vp = kp + STEP * D;
-            float s[2 * SUBS][4];
+            // four chains of products: pieces of 8 positions, or for few pieces also halves of D
+            constexpr int CH = 2 / SUBS;
+            float s[2 * SUBS][4], s2[CH == 2 ? 2 * SUBS : 1][4];
 #pragma unroll
             for (int h = 0; h < 2 * SUBS; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+#pragma unroll
+            for (int h = 0; h < (CH == 2 ? 2 * SUBS : 1); ++h) s2[h][0] = s2[h][1] = s2[h][2] = s2[h][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < KC; ++i) {
                 uint4 kw[2 * SUBS];
@@ -424,7 +484,11 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 #pragma unroll
                     for (int h = 0; h < 2 * SUBS; ++h) {
                         const uint32_t w = k == 0 ? kw[h].x : k == 1 ? kw[h].y : k == 2 ? kw[h].z : kw[h].w;
-                        mma(s[h], a[0], a[1], a[2], a[3], e4m3x2_to_half2((uint16_t)w), e4m3x2_to_half2((uint16_t)(w >> 16)));
+                        const uint32_t b0 = e4m3x2_to_half2((uint16_t)w), b1 = e4m3x2_to_half2((uint16_t)(w >> 16));
+                        if (CH == 2 && (k & 1))
+                            mma(s2[CH == 2 ? h : 0], a[0], a[1], a[2], a[3], b0, b1);
+                        else
+                            mma(s[h], a[0], a[1], a[2], a[3], b0, b1);
                     }
                 }
             }
@@ -433,6 +497,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 #pragma unroll
             for (int h = 0; h < 2 * SUBS; ++h) {
                 const float fk = f * sc[h / 2].x;
+                if constexpr (CH == 2) s[h][0] += s2[h][0], s[h][1] += s2[h][1], s[h][2] += s2[h][2], s[h][3] += s2[h][3];
                 p[h][0] = fmaf(s[h][0] + s[h][2], fk, sc[h / 2].y);
                 p[h][1] = fmaf(s[h][1] + s[h][3], fk, sc[h / 2].y);
             }
@@ -449,21 +514,22 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 #pragma unroll
             for (int h = 0; h < 2 * SUBS; ++h) top = fmaxf(top, fmaxf(p[h][0], p[h][1]));
             top = quad_max(top);
-            const float base = top == -INFINITY ? 0.f : top;
-            const float keep = exp2_of(mx - base);
-            mx = top;
-            sum *= keep;
+            if (__any_sync(0xffffffffu, top > mx + SLACK)) {
+                if (!(top > mx + SLACK)) top = mx;
+                const float keep = mx == top ? 1.f : exp2_of(mx - top);
+                mx = top;
+                sum *= keep;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][0] *= keep, acc[n][1] *= keep, acc[n][2] *= keep, acc[n][3] *= keep;
+            }
+            const float base = (mx == -INFINITY ? 0.f : mx) - LIFT;
             uint32_t ph[2 * SUBS], pl[2 * SUBS];
 #pragma unroll
             for (int h = 0; h < 2 * SUBS; ++h) {
-                p[h][0] = exp2_of(p[h][0] - (base - LIFT));
-                p[h][1] = exp2_of(p[h][1] - (base - LIFT));
+                p[h][0] = exp2_of(p[h][0] - base);
+                p[h][1] = exp2_of(p[h][1] - base);
                 sum = fmaf(p[h][0] + p[h][1], sc[h / 2].z, sum);
                 split_half(p[h][0], p[h][1], ph[h], pl[h], REST);
-            }
-            if (__any_sync(0xffffffffu, keep != 1.f)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] *= keep, acc[n][1] *= keep, acc[n][2] *= keep, acc[n][3] *= keep;
             }
 #pragma unroll
             for (int b = 0; b < SUBS; ++b)
@@ -496,158 +562,190 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         }
         copy_wait<0>();
         __syncwarp();
-        // ---- the warps' results together
+        // ---- the next part's copies start, then the warps' results come together
+        more = next();
+        if (more) {
+            look_up(j.c0);
+            if (warp == 0) load_q();
+        }
         sum = quad_sum(sum);
         if (t4 == 0) S.m[warp][gid] = mx, S.l[warp][gid] = sum;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             // tile n, columns 2t and 2t+1: elements 16 * column + n % 16 of its 128 (8 * column + n of 64)
             const int d0 = D == 64 ? 16 * t4 + n : 128 * (n / 16) + 32 * t4 + n % 16;
-            warp_out<D>(S, warp)[gid * (D + 4) + d0] = fmaf(acc[n][2], 1.f / REST, acc[n][0]);
-            warp_out<D>(S, warp)[gid * (D + 4) + d0 + (D == 64 ? 8 : 16)] = fmaf(acc[n][3], 1.f / REST, acc[n][1]);
+            warp_out<D>(S, warp, gid, d0) = fmaf(acc[n][2], 1.f / REST, acc[n][0]);
+            warp_out<D>(S, warp, gid, d0 + (D == 64 ? 8 : 16)) = fmaf(acc[n][3], 1.f / REST, acc[n][1]);
         }
+        if (more) begin();
         __syncthreads();
-        const bool whole = c0 == 0 && c1 == j.s.units;
-        const int slot = 2 * blockIdx.x + (c0 == 0 ? 1 : 0);  // a job that began before this block: its first slot
-        for (int e = threadIdx.x; e < ROWS * D; e += AT_WARPS * 32) {
-            const int r = e / D, d = e % D, row = j.tile * ROWS + r;
-            if (row >= j.s.n * G) break;
-            float m = S.m[0][r];
+        const bool whole = cur.c0 == 0 && cur.c1 == cur.s.units;
+        const int slot = 2 * blockIdx.x + (cur.c0 == 0 ? 1 : 0);  // a job that began in a former block: the first slot
+        const int rows = min(ROWS, cur.s.n * G - cur.tile * ROWS);
+#pragma unroll 1
+        for (int r = warp; r < rows; r += AT_WARPS) {
+            float m = S.m[0][r], l = 0.f, k[AT_WARPS];
 #pragma unroll
             for (int w = 1; w < AT_WARPS; ++w) m = fmaxf(m, S.m[w][r]);
             const float base = m == -INFINITY ? 0.f : m;
-            float o = 0.f, l = 0.f;
 #pragma unroll
             for (int w = 0; w < AT_WARPS; ++w) {
-                const float k = exp2f(S.m[w][r] - base);
-                l += k * S.l[w][r];
-                o += k * warp_out<D>(S, w)[r * (D + 4) + d];
+                k[w] = exp2_of(S.m[w][r] - base);
+                l += k[w] * S.l[w][r];
             }
-            if (whole) {
-                const size_t tok = (size_t)j.s.row0 + row / G;
-                const int head = j.head * G + row % G;
-                store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
-                if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
-            } else {
-                A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
-                if (d == 0) A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            const int row = cur.tile * ROWS + r, head = cur.head * G + row % G;
+            const size_t tok = (size_t)cur.s.row0 + row / G;
+#pragma unroll
+            for (int d = lane; d < D; d += 32) {
+                float o = 0.f;
+#pragma unroll
+                for (int w = 0; w < AT_WARPS; ++w) o += k[w] * warp_out<D>(S, w, r, d);
+                if (whole)
+                    store_out<TY>(A, tok, head * D + d, o * inv);
+                else
+                    A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
+            }
+            if (lane == 0) {
+                if (!whole)
+                    A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
+                else if (A.lse)
+                    A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
             }
         }
-        if (!whole && c0 == 0)
-            cut = {(int)((j.first + j.s.units - 1) / per) - (int)blockIdx.x + 1, j.s.row0, j.tile, j.head,
-                   min(ROWS, j.s.n * G - j.tile * ROWS)};
-        u = j.first + c1;
+        if (!whole) {
+            const int b0 = (int)((cur.first + A.job_cost) / per);
+            const int b1 = (int)((cur.first + A.job_cost + cur.s.units - 1) / per);
+            (cur.c0 == 0 ? begun : went_on) = {b1 - b0 + 1, b0, cur.s.row0, cur.tile, cur.head, rows};
+        }
     }
-    if (threadIdx.x == 0) A.cuts[blockIdx.x] = cut;
+    if (threadIdx.x == 0) A.cuts[2 * blockIdx.x] = begun, A.cuts[2 * blockIdx.x + 1] = went_on;
 }
 
-// Join the partial results of the job that block x started and did not end.
-// Few parts: one thread block takes all rows, a thread four columns of a row.
-// Many: one row a thread block (y), a thread adds four columns of every
-// GROUPS-th part, then the groups' sums are added.
+// Join the parts of the jobs that several blocks have.  Few parts: the thread
+// block that started the job takes all of it, a thread four columns of a row.
+// Many: the thread blocks that have a part share its rows and quarters of rows; a
+// thread adds four columns of every GROUPS-th part, then the groups' sums are
+// added.  Either way in the same order in every run.
 constexpr int JOIN_THREADS = 256;
-constexpr int JOIN_PARTS = 512;  // parts a job can have: the thread blocks
 constexpr int JOIN_FEW = 8;
 
 template <int D, int TY>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
-    constexpr int GROUPS = JOIN_THREADS / (D / 4);
-    __shared__ float weight[JOIN_PARTS];
-    __shared__ float part[GROUPS][D + 4];
-    __shared__ float wm[JOIN_THREADS / 32], wl[JOIN_THREADS / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = tid / (D / 4), d4 = tid % (D / 4) * 4, G = A.Hq / A.Hkv, b0 = blockIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are there
-    const Cut cut = A.cuts[b0];
-    const int n = cut.parts;
-    const auto write = [&](int r, int d, float o, float m, float l) {
+    constexpr int COLS = D / 4;                     // a quarter of a row
+    constexpr int GROUPS = JOIN_THREADS / (COLS / 4);
+    constexpr int BATCH = 8;
+    __shared__ float part[GROUPS][COLS + 4];
+    __shared__ float gm[GROUPS], gl[GROUPS];
+    const int tid = threadIdx.x, G = A.Hq / A.Hkv;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+    const Cut begun = A.cuts[2 * blockIdx.x], went_on = A.cuts[2 * blockIdx.x + 1];
+    const auto write = [&](const Cut& cut, int r, int d, float o, float m, float l) {
         const int row = cut.tile * ROWS + r, head = cut.head * G + row % G;
         const size_t tok = (size_t)cut.row0 + row / G;
         store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
         if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
     };
-    if (n <= JOIN_FEW) {
-        if (blockIdx.y != 0) return;
-        for (int r = g; r < cut.rows && n > 0; r += GROUPS) {
-            const auto slot = [&](int i) { return ((size_t)2 * (b0 + i) + (i == 0)) * ROWS + r; };
+    // the first block left its part in its second slot, the others in their first
+    const auto slot_of = [](const Cut& cut, int r, int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * ROWS + r; };
+    if (begun.parts > 0 && begun.parts <= JOIN_FEW) {
+        const int n = begun.parts, d4 = tid % (D / 4) * 4;
+        for (int r = tid / (D / 4); r < begun.rows; r += JOIN_THREADS / (D / 4)) {
             float2 ml[JOIN_FEW];
             float4 x[JOIN_FEW];
             float m = -INFINITY, l = 0.f;
 #pragma unroll
             for (int i = 0; i < JOIN_FEW; ++i)
                 if (i < n) {
-                    ml[i] = A.part_ml[slot(i)];
-                    x[i] = *reinterpret_cast<const float4*>(A.part_o + slot(i) * D + d4);
-                    m = fmaxf(m, ml[i].x);
+                    ml[i] = A.part_ml[slot_of(begun, r, i)];
+                    x[i] = *reinterpret_cast<const float4*>(A.part_o + slot_of(begun, r, i) * D + d4);
                 }
+#pragma unroll
+            for (int i = 0; i < JOIN_FEW; ++i)
+                if (i < n) m = fmaxf(m, ml[i].x);
             const float base = m == -INFINITY ? 0.f : m;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < JOIN_FEW; ++i)
                 if (i < n) {
-                    const float k = exp2f(ml[i].x - base);
+                    const float k = exp2_of(ml[i].x - base);
                     l += k * ml[i].y;
                     o.x += k * x[i].x, o.y += k * x[i].y, o.z += k * x[i].z, o.w += k * x[i].w;
                 }
-            write(r, d4, o.x, m, l);
-            write(r, d4 + 1, o.y, m, l);
-            write(r, d4 + 2, o.z, m, l);
-            write(r, d4 + 3, o.w, m, l);
+            write(begun, r, d4, o.x, m, l);
+            write(begun, r, d4 + 1, o.y, m, l);
+            write(begun, r, d4 + 2, o.z, m, l);
+            write(begun, r, d4 + 3, o.w, m, l);
         }
-        return;
     }
-    const int r = blockIdx.y;
-    if (r >= cut.rows) return;
-    // the first block left its part in its second slot, the others in their first
-    const auto slot = [&](int i) { return ((size_t)2 * (b0 + i) + (i == 0)) * ROWS + r; };
-    float m = -INFINITY;
-    for (int i = tid; i < n; i += JOIN_THREADS) m = fmaxf(m, A.part_ml[slot(i)].x);
-    m = warp_max(m);
-    if (lane == 0) wm[warp] = m;
-    __syncthreads();
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const Cut cut = side ? went_on : begun;
+        if (cut.parts <= JOIN_FEW) continue;
+        const int n = cut.parts, g = tid / (COLS / 4), d4 = tid % (COLS / 4) * 4;
+        for (int item = (int)blockIdx.x - cut.block; item < 4 * cut.rows; item += n) {
+            const int r = item >> 2, col = (item & 3) * COLS;
+            // BATCH parts a thread at a time, with the running maximum
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = g; i0 < n; i0 += BATCH * GROUPS) {
+                float2 ml[BATCH];
+                float4 x[BATCH];
 #pragma unroll
-    for (int w = 0; w < JOIN_THREADS / 32; ++w) m = fmaxf(m, wm[w]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int i = tid; i < n; i += JOIN_THREADS) {
-        const float2 ml = A.part_ml[slot(i)];
-        weight[i] = exp2f(ml.x - base);
-        l += weight[i] * ml.y;
-    }
-    l = warp_sum(l);
-    if (lane == 0) wl[warp] = l;
-    __syncthreads();
-    l = 0.f;
+                for (int k = 0; k < BATCH; ++k) {
+                    const int i = i0 + k * GROUPS;
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < n) {
+                        ml[k] = A.part_ml[slot_of(cut, r, i)];
+                        x[k] = *reinterpret_cast<const float4*>(A.part_o + slot_of(cut, r, i) * D + col + d4);
+                    }
+                }
+                float top = m;
 #pragma unroll
-    for (int w = 0; w < JOIN_THREADS / 32; ++w) l += wl[w];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = g; i < n; i += GROUPS) {
-        const float4 x = *reinterpret_cast<const float4*>(A.part_o + slot(i) * D + d4);
-        const float k = weight[i];
-        o.x += k * x.x, o.y += k * x.y, o.z += k * x.z, o.w += k * x.w;
-    }
-    *reinterpret_cast<float4*>(&part[g][d4]) = o;
-    __syncthreads();
-    if (tid < D) {
-        float v = 0.f;
+                for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+                const float base = top == -INFINITY ? 0.f : top, keep = exp2_of(m - base);
+                m = top;
+                l *= keep;
+                o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
 #pragma unroll
-        for (int k = 0; k < GROUPS; ++k) v += part[k][tid];
-        write(r, tid, v, m, l);
+                for (int k = 0; k < BATCH; ++k) {
+                    const float w = exp2_of(ml[k].x - base);
+                    l += w * ml[k].y;
+                    o.x += w * x[k].x, o.y += w * x[k].y, o.z += w * x[k].z, o.w += w * x[k].w;
+                }
+            }
+            *reinterpret_cast<float4*>(&part[g][d4]) = o;
+            if (d4 == 0) gm[g] = m, gl[g] = l;
+            __syncthreads();
+            if (tid < COLS) {
+                float M = -INFINITY, v = 0.f;
+                l = 0.f;
+#pragma unroll
+                for (int k = 0; k < GROUPS; ++k) M = fmaxf(M, gm[k]);
+                const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int k = 0; k < GROUPS; ++k) {
+                    const float w = exp2_of(gm[k] - base);
+                    l += w * gl[k];
+                    v += w * part[k][tid];
+                }
+                write(cut, r, col + tid, v, M, l);
+            }
+            __syncthreads();
+        }
     }
 }
 
 constexpr int BLOCKS_PER_SM = 2;
 
-int attn_blocks() {
-    const int n = num_sms() * BLOCKS_PER_SM;
-    return n < JOIN_PARTS ? n : JOIN_PARTS;
-}
+int attn_blocks() { return num_sms() * BLOCKS_PER_SM; }
 
 template <int D, int TY>
 int launch(AttnArgs a, cudaStream_t s) {
     a.unit = Tile<D>::UNIT;
-    const size_t sched = (size_t)(a.B + 1) * sizeof(long long);
+    a.job_cost = Tile<D>::JOB_COST;
+    const size_t sched = (size_t)a.B * sizeof(uint32_t);
     const size_t sm = sizeof(AttnSmem<D>) + sched;
     if (cudaFuncSetAttribute(k_attn<D, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
         return E0_ERR_CUDA;
@@ -655,7 +753,7 @@ int launch(AttnArgs a, cudaStream_t s) {
     if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
     // the join's blocks start while those above still run and wait for all of them
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.blocks, ROWS);
+    cfg.gridDim = dim3(a.blocks);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -675,7 +773,7 @@ int launch_d(const AttnArgs& a, int D, cudaStream_t s) {
 
 size_t attn_ws_bytes(int D) {
     const size_t slots = 2 * (size_t)attn_blocks();
-    return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2) + slots / 2 * sizeof(Cut);
+    return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2) + slots * sizeof(Cut);
 }
 
 int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
