@@ -489,7 +489,7 @@ size_t e0_linear_bytes(int N, int K);
  * i and i + 8, i = 0..7.  Lane l holds rows l/4 and l/4 + 8 and the inputs
  * 16*(l%4) .. + 15; its word i holds the inputs 4i..4i+3 of those, nibbles
  * 0, 4 = row l/4 inputs 0, 1; 1, 5 = row l/4 + 8 inputs 0, 1; 2, 6 and 3, 7
- * the same for inputs 2, 3.  src is a host descriptor of device pointers, dst
+ * the same for inputs 2, 3; the word is then rotated left by 3 bits.  src is a host descriptor of device pointers, dst
  * device memory of e0_linear_bytes(N, K) bytes, 16-byte aligned.
  * Asynchronous. */
 int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_t stream);

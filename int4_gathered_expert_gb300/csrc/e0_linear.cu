@@ -20,9 +20,12 @@ namespace {
 // Decode is bound by reading the weights: 4.5 bits each, once.  The layout gives a
 // lane its 16 x 64 tile's fragment with one 16-byte load.
 //
-// Codes as operands.  fp16: the bits 0..15 of a code are the subnormal number
-// code * 2^-24, exact, so a code pair costs a mask (and a shift for three of
-// four); the scale takes the 2^24.  bf16: 0x4300 | code is 128 + code, less 128.
+// Codes as operands cost a mask (and a rotation for three of four): they stand
+// in the bits 3..6 of a half.  As fp16 that is the subnormal number code * 2^-21,
+// exact; the scale takes the 2^21.  As bf16, with the exponent of 16 set, it is 16 +
+// code; the product is then too large by 16 sum x, which goes into the bias.  (With
+// codes in the bits 0..3 it would be 128 + code, and the sums' rounding 5 times as
+// large; subtracting the 128 again took a third of the instructions.)
 // Activations: fp16 and bf16 as they are; e4m3 widened to fp16 (exact), its
 // scale applied to the group's sums; fp32 as three bf16 parts (8 significant bits
 // each, cut off, the sum exact), three products a step.
@@ -58,74 +61,90 @@ template <bool BF>
 E0_DEV void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t q = (w >> (4 * i)) & 0x000F000Fu;
-        if (BF) {
-            q |= 0x43004300u;
-            const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&q), __float2bfloat162_rn(128.f));
-            q = *reinterpret_cast<const uint32_t*>(&v);
-        }
-        a[i] = q;
+        const uint32_t q = __funnelshift_r(w, w, 4 * i) & 0x00780078u;
+        a[i] = BF ? q | 0x41804180u : q;
     }
 }
+// What a group's (scale, bias) word turns the sums with: fp16 codes stand for code
+// * 2^-21, bf16 ones for code + 16.
+template <bool BF>
+E0_DEV float2 scale_bias(uint32_t w) {
+    float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    if (BF)
+        f.y = fmaf(-16.f, f.x, f.y);
+    else
+        f.x *= 2097152.f;
+    return f;
+}
 
-// A lane's 16 consecutive inputs of one token and group as B fragments:
-// b[p][2i], b[p][2i+1] for step i and part p (fp32 has three, the others one).
+// A lane's 16 consecutive inputs of one token and group, as they are in memory ...
 template <int XT>
-E0_DEV void load_x(const LinArgs& A, int tok, int g, int t4, uint32_t (&b)[XT == E0_F32 ? 3 : 1][8]) {
-    constexpr int P = XT == E0_F32 ? 3 : 1;
+struct RawX {
+    static constexpr int WORDS = XT == E0_F32 ? 16 : XT == E0_E4M3 ? 4 : 8;
+    static constexpr int PARTS = XT == E0_F32 ? 3 : 1;
+    uint32_t w[WORDS];
+};
+template <int XT>
+E0_DEV void load_x(const LinArgs& A, int tok, int g, int t4, RawX<XT>& r) {
+    constexpr int SZ = XT == E0_F32 ? 4 : XT == E0_E4M3 ? 1 : 2, W = RawX<XT>::WORDS;
     if (tok >= A.T) {
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[p][i] = 0;
+        for (int i = 0; i < W; ++i) r.w[i] = 0;
         return;
     }
-    const size_t at = (size_t)tok * A.x_ld + g * GROUP + 16 * t4;
-    if constexpr (XT == E0_E4M3) {
-        const uint8_t* x = reinterpret_cast<const uint8_t*>(A.x) + at;
-        uint32_t w[4];
-        if (A.vec) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(x));
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        } else {
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(A.x) + ((size_t)tok * A.x_ld + g * GROUP + 16 * t4) * SZ;
+    if (A.vec) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = x[4 * i] | (x[4 * i + 1] << 8) | (x[4 * i + 2] << 16) | ((uint32_t)x[4 * i + 3] << 24);
+        for (int i = 0; i < W / 4; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(x) + i);
+            r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
         }
+    } else if constexpr (SZ == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) r.w[i] = reinterpret_cast<const uint32_t*>(x)[i];
+    } else if constexpr (SZ == 2) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+        for (int i = 0; i < W; ++i) r.w[i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            r.w[i] = x[4 * i] | (x[4 * i + 1] << 8) | (x[4 * i + 2] << 16) | ((uint32_t)x[4 * i + 3] << 24);
+    }
+}
+// ... and as B fragments: b[p][2i], b[p][2i+1] for step i and part p.
+template <int XT>
+E0_DEV void fragments(RawX<XT> r, uint32_t (&b)[RawX<XT>::PARTS][8]) {
+    if constexpr (XT == E0_E4M3) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            b[0][2 * i] = e4m3x2_to_half2((uint16_t)w[i]);
-            b[0][2 * i + 1] = e4m3x2_to_half2((uint16_t)(w[i] >> 16));
+            b[0][2 * i] = e4m3x2_to_half2((uint16_t)r.w[i]);
+            b[0][2 * i + 1] = e4m3x2_to_half2((uint16_t)(r.w[i] >> 16));
         }
     } else if constexpr (XT == E0_F32) {
-        const float* x = reinterpret_cast<const float*>(A.x) + at;
-        float v[16];
-        if (A.vec) {
-            load_vec<E0_F32, 16>(x, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = x[i];
-        }
 #pragma unroll
         for (int p = 0; p < 3; ++p)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t lo = __float_as_uint(v[2 * i]), hi = __float_as_uint(v[2 * i + 1]);
+                const uint32_t lo = r.w[2 * i], hi = r.w[2 * i + 1];
                 b[p][i] = __byte_perm(lo, hi, 0x7632);
-                v[2 * i] -= __uint_as_float(lo & 0xFFFF0000u);
-                v[2 * i + 1] -= __uint_as_float(hi & 0xFFFF0000u);
+                r.w[2 * i] = __float_as_uint(__uint_as_float(lo) - __uint_as_float(lo & 0xFFFF0000u));
+                r.w[2 * i + 1] = __float_as_uint(__uint_as_float(hi) - __uint_as_float(hi & 0xFFFF0000u));
             }
     } else {
-        const uint16_t* x = reinterpret_cast<const uint16_t*>(A.x) + at;
-        if (A.vec) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(x)), v = __ldg(reinterpret_cast<const uint4*>(x) + 1);
-            b[0][0] = u.x, b[0][1] = u.y, b[0][2] = u.z, b[0][3] = u.w;
-            b[0][4] = v.x, b[0][5] = v.y, b[0][6] = v.z, b[0][7] = v.w;
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[0][i] = x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
-        }
+        for (int i = 0; i < 8; ++i) b[0][i] = r.w[i];
     }
+}
+
+E0_DEV void copy16(uint8_t* dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+E0_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+E0_DEV void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 E0_DEV float get_any(const void* p, int type, size_t i) {
@@ -142,160 +161,419 @@ E0_DEV void put_any(void* p, int type, size_t i, float v) {
         reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// One block: 16*RM rows, 8*NT tokens, the groups of its share of K (the blocks
-// of a cluster share a row tile and split K); its warps take the groups in
-// turn.  The warps' sums meet in shared memory and the cluster's in distributed
-// shared memory, always in the same order.
-template <int XT, int RM, int NT>
-__global__ void __launch_bounds__(LIN_WARPS * 32, RM* NT >= 8 ? 1 : 2) k_linear(LinArgs A) {
+// y[t][n] = v (+ add[t][n]), where there is such a row and token.
+E0_DEV void store_y(const LinArgs& A, int n, int t, float v) {
+    if (n >= A.N || t >= A.T) return;
+    if (A.add) v += get_any(A.add, A.y_type, (size_t)t * A.add_ld + n);
+    put_any(A.y, A.y_type, (size_t)t * A.y_ld + n, v);
+}
+
+// A group's share of rows i and i + 8, tokens 2t and 2t + 1: s * sum q x + b * sum x.
+template <bool SCALED>
+E0_DEV void add_group(float (&tot)[4], const float (&d)[4], float s0, float b0, float s1, float b1, const float* sx,
+                      const float* xs) {
+    if (SCALED) {
+        tot[0] = fmaf(xs[0], fmaf(s0, d[0], b0 * sx[0]), tot[0]);
+        tot[1] = fmaf(xs[1], fmaf(s0, d[1], b0 * sx[1]), tot[1]);
+        tot[2] = fmaf(xs[0], fmaf(s1, d[2], b1 * sx[0]), tot[2]);
+        tot[3] = fmaf(xs[1], fmaf(s1, d[3], b1 * sx[1]), tot[3]);
+    } else {
+        tot[0] = fmaf(s0, d[0], fmaf(b0, sx[0], tot[0]));
+        tot[1] = fmaf(s0, d[1], fmaf(b0, sx[1], tot[1]));
+        tot[2] = fmaf(s1, d[2], fmaf(b1, sx[0], tot[2]));
+        tot[3] = fmaf(s1, d[3], fmaf(b1, sx[1], tot[3]));
+    }
+}
+
+// The sums of the cluster's blocks: element e of a block's N sums belongs to block
+// e / (N / S), and every block writes it there, [its rank][e % (N / S)].
+struct Spread {
+    float* to;  // this block's own [S][N / S]
+    int S, rank, share;
+    E0_DEV Spread(float* buf, int n) : to(buf), S(gridDim.y), rank(blockIdx.y), share(n / S) {}
+    E0_DEV void put(int e, float v) {
+        cg::this_cluster().map_shared_rank(to, e / share)[rank * share + e % share] = v;
+    }
+    E0_DEV float get(int i) const {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < S) v += to[k * share + i];
+        return v;
+    }
+};
+
+// Up to 8 rows of x.  A tile is 16*RM rows of W; the blocks of a cluster share a
+// tile and split K, the warps of a block take the groups of its share in turn,
+// and a block goes through tiles blockIdx.x, + gridDim.x, ...  A warp's records
+// come through its own ring in shared memory, copied STAGES - 1 groups ahead and
+// on into the next tile, so the memory is kept busy while a tile's sums meet.
+// The warps' sums meet in shared memory and the cluster's in distributed shared
+// memory, always in the same order.
+template <int RM>
+struct VecRing {
+    static constexpr int STAGES = RM == 4 ? 4 : 8;
+    static constexpr int BYTES = RM * REC;
+    static constexpr int SMEM = LIN_WARPS * STAGES * BYTES;
+};
+
+template <int XT, int RM>
+__global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
     constexpr bool BF = XT == E0_F32 || XT == E0_BF16;
-    constexpr int P = XT == E0_F32 ? 3 : 1;
-    constexpr int COLS = NT * 8, ROWS = RM * 16;
-    __shared__ float part[LIN_WARPS][ROWS][COLS + 1];
-    __shared__ float sums[ROWS][COLS + 1];
+    constexpr int P = RawX<XT>::PARTS, ROWS = RM * 16, STAGES = VecRing<RM>::STAGES;
+    extern __shared__ __align__(128) uint8_t lin_sm[];
+    __shared__ float part[LIN_WARPS][ROWS][9];
+    __shared__ float sums[RM == 1 ? ROWS * 8 : 1];  // one block of rows is all that a cluster has
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t4 = lane & 3;
-    const int G = A.K / GROUP, S = gridDim.y;
-    const int g0 = (int)((long long)blockIdx.y * G / S), g1 = (int)((long long)(blockIdx.y + 1) * G / S);
-    const int nb = (A.N + 15) / 16, rb0 = blockIdx.x * RM, tok0 = blockIdx.z * COLS;
+    uint8_t* ring = lin_sm + warp * STAGES * VecRing<RM>::BYTES;
+    const int G = A.K / GROUP, S = gridDim.y, rank = blockIdx.y;
+    const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);
+    const int nb = (A.N + 15) / 16, tiles = (nb + RM - 1) / RM;
     const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
     const uint32_t ones[4] = {one, one, one, one};
-    const float up = BF ? 1.f : 16777216.f;  // fp16 codes stand for code * 2^-24
+
+    // where the next copy comes from and goes to
+    int in_tile = blockIdx.x, in_g = g0 + warp, in_stage = 0;
+    constexpr int PIECES = (RM * 36 + 31) / 32;  // 16-byte pieces of a step that a lane copies
+    const auto issue = [&]() {
+        if (in_tile < tiles && in_g < g1) {
+            uint8_t* dst = ring + in_stage * VecRing<RM>::BYTES + lane * 16;
+            const uint8_t* src = A.w + ((size_t)in_tile * RM * G + in_g) * REC;
+            const int left = (nb - in_tile * RM) * 36;  // rows beyond the last block are not stored
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int c = i * 32 + lane, r = c / 36;
+                if (c < min(RM * 36, left)) copy16(dst + i * 512, src + (size_t)(r * (G - 1) * REC) + c * 16);
+            }
+            if (++in_stage == STAGES) in_stage = 0;
+            in_g += LIN_WARPS;
+            if (in_g >= g1) in_g = g0 + warp, in_tile += gridDim.x;
+        }
+        copy_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+
+    int stage = 0;
+    RawX<XT> raw;  // of the next group
+    float nxt[2] = {0.f, 0.f};
+    const auto fetch_x = [&](int g) {
+        load_x<XT>(A, gid, g, t4, raw);
+        if constexpr (XT == E0_E4M3) {
+            nxt[0] = 2 * t4 < A.T ? __ldg(A.xs + (size_t)(2 * t4) * G + g) : 0.f;
+            nxt[1] = 2 * t4 + 1 < A.T ? __ldg(A.xs + (size_t)(2 * t4 + 1) * G + g) : 0.f;
+        }
+    };
+    if (g0 + warp < g1) fetch_x(g0 + warp);
+#pragma unroll 1
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        float tot[RM][4];
+#pragma unroll
+        for (int r = 0; r < RM; ++r) tot[r][0] = tot[r][1] = tot[r][2] = tot[r][3] = 0.f;
+#pragma unroll 1
+        for (int g = g0 + warp; g < g1; g += LIN_WARPS) {
+            uint32_t b[P][8];
+            fragments<XT>(raw, b);
+            const float xs[2] = {nxt[0], nxt[1]};
+            fetch_x(g + LIN_WARPS < g1 ? g + LIN_WARPS : g0 + warp);
+            copy_wait<STAGES - 2>();
+            __syncwarp();  // the group has arrived for all lanes, and all have read the one before it
+            const uint8_t* rec = ring + stage * VecRing<RM>::BYTES;
+            if (++stage == STAGES) stage = 0;
+            issue();
+            float sx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int p = 0; p < P; ++p) mma16(sx, ones, b[p][2 * i], b[p][2 * i + 1], BF);
+#pragma unroll
+            for (int r = 0; r < RM; ++r) {
+                const uint4 c = *reinterpret_cast<const uint4*>(rec + r * REC + lane * 16);
+                const uint2 sb = *reinterpret_cast<const uint2*>(rec + r * REC + 512 + gid * 8);
+                const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a[4];
+                    unpack_codes<BF>(cw[i], a);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) mma16(d, a, b[p][2 * i], b[p][2 * i + 1], BF);
+                }
+                const float2 lo = scale_bias<BF>(sb.x), hi = scale_bias<BF>(sb.y);
+                add_group<XT == E0_E4M3>(tot[r], d, lo.x, lo.y, hi.x, hi.y, sx, xs);
+            }
+        }
+        if (tile != blockIdx.x) __syncthreads();  // the former tile's sums have been read
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+            part[warp][16 * r + gid][2 * t4] = tot[r][0];
+            part[warp][16 * r + gid][2 * t4 + 1] = tot[r][1];
+            part[warp][16 * r + gid + 8][2 * t4] = tot[r][2];
+            part[warp][16 * r + gid + 8][2 * t4 + 1] = tot[r][3];
+        }
+        __syncthreads();
+        // rows run along neighbouring threads, so stores to one token's row are coalesced
+        if (S == 1) {
+            for (int e = threadIdx.x; e < ROWS * min(A.T, 8); e += LIN_WARPS * 32) {
+                const int row = e % ROWS, col = e / ROWS;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < LIN_WARPS; ++w) v += part[w][row][col];
+                store_y(A, tile * ROWS + row, col, v);
+            }
+        } else if constexpr (RM == 1) {  // one tile a cluster
+            Spread sp(sums, ROWS * 8);
+            cg::this_cluster().sync();  // all blocks run
+            for (int e = threadIdx.x; e < ROWS * 8; e += LIN_WARPS * 32) {
+                const int row = e % ROWS, col = e / ROWS;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < LIN_WARPS; ++w) v += part[w][row][col];
+                sp.put(e, v);
+            }
+            cg::this_cluster().sync();  // all sums are where they belong
+            for (int i = threadIdx.x; i < sp.share; i += LIN_WARPS * 32) {
+                const int e = rank * sp.share + i;
+                store_y(A, tile * ROWS + e % ROWS, e / ROWS, sp.get(i));
+            }
+        }
+    }
+}
+
+// More than 8 rows of x: 32 of them (TOK) and 128*RM rows of W a block; a warp has
+// 16*RM rows and all warps go through the groups of the block's share of K
+// together.  x comes through shared memory once for the block, its sums over
+// groups are formed there by all warps one group ahead; a warp's records
+// come through its ring as above.  The blocks of a cluster split K.
+constexpr int TOK = 32;
+constexpr int BATCH_RM = 1;
+
+template <int XT>
+struct BatchSmem {
+    static constexpr int STAGES = 4, ROWS = LIN_WARPS * 16 * BATCH_RM;
+    static constexpr int XROW = GROUP * (XT == E0_F32 ? 4 : XT == E0_E4M3 ? 1 : 2);  // bytes
+    uint8_t rec[STAGES][LIN_WARPS][BATCH_RM * REC];
+    uint8_t x[STAGES][TOK * XROW];
+    float sx[2][TOK], xs[2][TOK];
+    float sums[ROWS * (TOK + 1)];  // over the tile, or the cluster's share of it
+};
+
+// 16-byte chunk c of token t's group: chunks of odd tokens change places in pairs,
+// so that the eight lanes of a load's phase (two tokens, every second chunk)
+// find eight different ones.
+template <int XT>
+E0_DEV int x_chunk(int t, int c) {
+    constexpr int PER = BatchSmem<XT>::XROW / 16;
+    return XT == E0_E4M3 ? t * PER + c : t * PER + (c ^ (t & 1));
+}
+
+template <int XT>
+__global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
+    constexpr bool BF = XT == E0_F32 || XT == E0_BF16;
+    constexpr int P = RawX<XT>::PARTS, RM = BATCH_RM, NT = TOK / 8;
+    typedef BatchSmem<XT> SM;
+    constexpr int STAGES = SM::STAGES, PER = SM::XROW / 16, SZ = SM::XROW / GROUP;
+    extern __shared__ __align__(128) uint8_t lin_sm[];
+    SM& M = *reinterpret_cast<SM*>(lin_sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, t4 = lane & 3;
+    const int G = A.K / GROUP, S = gridDim.y, rank = blockIdx.y;
+    const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);
+    const int nb = (A.N + 15) / 16, rb0 = (blockIdx.x * LIN_WARPS + warp) * RM, tok0 = blockIdx.z * TOK;
+
+    const auto issue = [&](int g) {
+        if (g < g1) {
+            const int stage = (g - g0) % STAGES;
+            uint8_t* dst = M.rec[stage][warp] + lane * 16;
+            const uint8_t* src = A.w + ((size_t)rb0 * G + g) * REC;
+            const int left = (nb - rb0) * 36;
+#pragma unroll
+            for (int i = 0; i < (RM * 36 + 31) / 32; ++i) {
+                const int c = i * 32 + lane, r = c / 36;
+                if (c < min(RM * 36, left)) copy16(dst + i * 512, src + (size_t)(r * (G - 1) * REC) + c * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < (TOK * PER + LIN_WARPS * 32 - 1) / (LIN_WARPS * 32); ++i) {
+                const int e = i * LIN_WARPS * 32 + tid, t = e / PER, c = e % PER;
+                if (t < TOK) {
+                    const uint8_t* src = reinterpret_cast<const uint8_t*>(A.x) +
+                                         ((size_t)(tok0 + t) * A.x_ld + g * GROUP) * SZ + c * 16;
+                    uint8_t* to = M.x[stage] + 16 * x_chunk<XT>(t, c);
+                    if (tok0 + t >= A.T)
+                        *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+                    else if (A.vec)
+                        copy16(to, src);
+                    else
+#pragma unroll
+                        for (int k = 0; k < 16; k += SZ) {
+                            if (SZ == 4) *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(src + k);
+                            if (SZ == 2) *reinterpret_cast<uint16_t*>(to + k) = *reinterpret_cast<const uint16_t*>(src + k);
+                            if (SZ == 1) to[k] = src[k];
+                        }
+                }
+            }
+        }
+        copy_commit();
+    };
+    const auto fragments_of = [&](int stage, int n, uint32_t (&b)[P][8]) {
+        RawX<XT> r;
+#pragma unroll
+        for (int i = 0; i < RawX<XT>::WORDS / 4; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(M.x[stage] + 16 * x_chunk<XT>(8 * n + gid, RawX<XT>::WORDS / 4 * t4 + i));
+            r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
+        }
+        fragments<XT>(r, b);
+    };
+    // sums over one group of 8 tokens' inputs: warps 0..3 have one tile each
+    const auto sum_x = [&](int g) {
+        if (g >= g1 || warp >= NT) return;
+        const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
+        const uint32_t ones[4] = {one, one, one, one};
+        uint32_t b[P][8];
+        fragments_of((g - g0) % STAGES, warp, b);
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p) mma16(d, ones, b[p][2 * i], b[p][2 * i + 1], BF);
+        if (gid == 0) {
+            const int t = 8 * warp + 2 * t4;
+            M.sx[g & 1][t] = d[0], M.sx[g & 1][t + 1] = d[1];
+            if constexpr (XT == E0_E4M3) {
+                M.xs[g & 1][t] = tok0 + t < A.T ? __ldg(A.xs + (size_t)(tok0 + t) * G + g) : 0.f;
+                M.xs[g & 1][t + 1] = tok0 + t + 1 < A.T ? __ldg(A.xs + (size_t)(tok0 + t + 1) * G + g) : 0.f;
+            }
+        }
+    };
 
     float tot[RM][NT][4];
 #pragma unroll
     for (int r = 0; r < RM; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[r][n][i] = 0.f;
-
-    for (int g = g0 + warp; g < g1; g += LIN_WARPS) {
+        for (int n = 0; n < NT; ++n) tot[r][n][0] = tot[r][n][1] = tot[r][n][2] = tot[r][n][3] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) issue(g0 + i);
+    copy_wait<STAGES - 2>();
+    __syncthreads();
+    sum_x(g0);
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+        copy_wait<STAGES - 3>();
+        __syncthreads();  // groups g and g + 1 and the sums of g are there; g - 1 has been read
+        issue(g + STAGES - 1);
+        sum_x(g + 1);
+        const int stage = (g - g0) % STAGES;
         uint4 c[RM];
         uint2 sb[RM];
 #pragma unroll
         for (int r = 0; r < RM; ++r) {
-            const int rb = min(rb0 + r, nb - 1);  // rows beyond the last block are not stored
-            const uint8_t* p = A.w + ((size_t)rb * G + g) * REC;
-            c[r] = ldg_stream(p + lane * 16);
-            sb[r] = __ldg(reinterpret_cast<const uint2*>(p + 512) + gid);
+            c[r] = *reinterpret_cast<const uint4*>(M.rec[stage][warp] + r * REC + lane * 16);
+            sb[r] = *reinterpret_cast<const uint2*>(M.rec[stage][warp] + r * REC + 512 + gid * 8);
         }
-        uint32_t b[NT][P][8];
-        float xs[NT][2];
+        float d[RM][NT][4];
+#pragma unroll
+        for (int r = 0; r < RM; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) d[r][n][0] = d[r][n][1] = d[r][n][2] = d[r][n][3] = 0.f;
+        uint32_t a[RM][4][4];
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+            const uint32_t cw[4] = {c[r].x, c[r].y, c[r].z, c[r].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack_codes<BF>(cw[i], a[r][i]);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            load_x<XT>(A, tok0 + n * 8 + gid, g, t4, b[n]);
-            if constexpr (XT == E0_E4M3) {
-                const int ta = tok0 + n * 8 + 2 * t4;
-                xs[n][0] = ta < A.T ? __ldg(A.xs + (size_t)ta * G + g) : 0.f;
-                xs[n][1] = ta + 1 < A.T ? __ldg(A.xs + (size_t)(ta + 1) * G + g) : 0.f;
-            }
-        }
-        float sx[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t b[P][8];
+            fragments_of(stage, n, b);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int p = 0; p < P; ++p) mma16(d, ones, b[n][p][2 * i], b[n][p][2 * i + 1], BF);
-            sx[n][0] = d[0], sx[n][1] = d[1];
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int r = 0; r < RM; ++r) mma16(d[r][n], a[r][i], b[p][2 * i], b[p][2 * i + 1], BF);
         }
 #pragma unroll
-        for (int r = 0; r < RM; ++r) {
-            float d[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-            const uint32_t cw[4] = {c[r].x, c[r].y, c[r].z, c[r].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a[4];
-                unpack_codes<BF>(cw[i], a);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int p = 0; p < P; ++p) mma16(d[n], a, b[n][p][2 * i], b[n][p][2 * i + 1], BF);
+        for (int n = 0; n < NT; ++n) {
+            const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[g & 1][8 * n + 2 * t4]);
+            const float sx[2] = {sx2.x, sx2.y};
+            float xs[2] = {1.f, 1.f};
+            if constexpr (XT == E0_E4M3) {
+                const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[g & 1][8 * n + 2 * t4]);
+                xs[0] = x2.x, xs[1] = x2.y;
             }
-            const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&sb[r].x));
-            const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&sb[r].y));
-            const float s0 = lo.x * up, s1 = hi.x * up;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (XT == E0_E4M3) {
-                    tot[r][n][0] = fmaf(xs[n][0], fmaf(s0, d[n][0], lo.y * sx[n][0]), tot[r][n][0]);
-                    tot[r][n][1] = fmaf(xs[n][1], fmaf(s0, d[n][1], lo.y * sx[n][1]), tot[r][n][1]);
-                    tot[r][n][2] = fmaf(xs[n][0], fmaf(s1, d[n][2], hi.y * sx[n][0]), tot[r][n][2]);
-                    tot[r][n][3] = fmaf(xs[n][1], fmaf(s1, d[n][3], hi.y * sx[n][1]), tot[r][n][3]);
-                } else {
-                    tot[r][n][0] += fmaf(s0, d[n][0], lo.y * sx[n][0]);
-                    tot[r][n][1] += fmaf(s0, d[n][1], lo.y * sx[n][1]);
-                    tot[r][n][2] += fmaf(s1, d[n][2], hi.y * sx[n][0]);
-                    tot[r][n][3] += fmaf(s1, d[n][3], hi.y * sx[n][1]);
-                }
+            for (int r = 0; r < RM; ++r) {
+                const float2 lo = scale_bias<BF>(sb[r].x), hi = scale_bias<BF>(sb[r].y);
+                add_group<XT == E0_E4M3>(tot[r][n], d[r][n], lo.x, lo.y, hi.x, hi.y, sx, xs);
             }
         }
     }
+    copy_wait<0>();
+    const int cols = min(A.T - tok0, TOK);
+    if (S == 1) {
+        constexpr int LD = TOK + 1;
+#pragma unroll
+        for (int r = 0; r < RM; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float* o = M.sums + ((warp * RM + r) * 16 + gid) * LD + 8 * n + 2 * t4;
+                o[0] = tot[r][n][0], o[1] = tot[r][n][1], o[8 * LD] = tot[r][n][2], o[8 * LD + 1] = tot[r][n][3];
+            }
+        __syncthreads();
+        for (int e = tid; e < SM::ROWS * cols; e += LIN_WARPS * 32)
+            store_y(A, blockIdx.x * SM::ROWS + e % SM::ROWS, tok0 + e / SM::ROWS, M.sums[e % SM::ROWS * LD + e / SM::ROWS]);
+        return;
+    }
+    Spread sp(M.sums, SM::ROWS * TOK);
+    cg::this_cluster().sync();  // all blocks run
 #pragma unroll
     for (int r = 0; r < RM; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            part[warp][16 * r + gid][8 * n + 2 * t4] = tot[r][n][0];
-            part[warp][16 * r + gid][8 * n + 2 * t4 + 1] = tot[r][n][1];
-            part[warp][16 * r + gid + 8][8 * n + 2 * t4] = tot[r][n][2];
-            part[warp][16 * r + gid + 8][8 * n + 2 * t4 + 1] = tot[r][n][3];
+            const int e = (8 * n + 2 * t4) * SM::ROWS + (warp * RM + r) * 16 + gid;
+            sp.put(e, tot[r][n][0]), sp.put(e + SM::ROWS, tot[r][n][1]);
+            sp.put(e + 8, tot[r][n][2]), sp.put(e + SM::ROWS + 8, tot[r][n][3]);
         }
-    __syncthreads();
-    const int rank = blockIdx.y;
-    for (int e = threadIdx.x; e < ROWS * COLS; e += LIN_WARPS * 32) {
-        const int row = e % ROWS, col = e / ROWS;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < LIN_WARPS; ++w) v += part[w][row][col];
-        sums[row][col] = v;
+    cg::this_cluster().sync();  // all sums are where they belong
+    for (int i = tid; i < sp.share; i += LIN_WARPS * 32) {
+        const int e = rank * sp.share + i;
+        store_y(A, blockIdx.x * SM::ROWS + e % SM::ROWS, tok0 + e / SM::ROWS, sp.get(i));
     }
-    if (S > 1) cg::this_cluster().sync(); else __syncthreads();
-    // the blocks of the cluster finish a share of the tile each; rows run
-    // along neighbouring threads, so stores to one token's row are coalesced
-    for (int e = threadIdx.x + rank * LIN_WARPS * 32; e < ROWS * COLS; e += S * LIN_WARPS * 32) {
-        const int row = e % ROWS, col = e / ROWS;
-        const int n = rb0 * 16 + row, t = tok0 + col;
-        if (n >= A.N || t >= A.T) continue;
-        float v = 0.f;
-        if (S > 1) {
-            for (int k = 0; k < S; ++k) v += cg::this_cluster().map_shared_rank(&sums[0][0], k)[row * (COLS + 1) + col];
-        } else {
-            v = sums[row][col];
-        }
-        if (A.add) v += get_any(A.add, A.y_type, (size_t)t * A.add_ld + n);
-        put_any(A.y, A.y_type, (size_t)t * A.y_ld + n, v);
-    }
-    if (S > 1) cg::this_cluster().sync();  // a block's sums are read until here
 }
 
-template <int XT, int RM, int NT>
-int launch(const LinArgs& a, int S, cudaStream_t s) {
+template <typename K>
+int launch(K kernel, const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return E0_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.N + 16 * RM - 1) / (16 * RM), S, (a.T + 8 * NT - 1) / (8 * NT));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(LIN_WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1, at[0].val.clusterDim.y = S, at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.x = 1, at[0].val.clusterDim.y = grid.y, at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = S > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_linear<XT, RM, NT>, a) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+    cfg.numAttrs = grid.y > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
 
 template <int XT>
 int linear_type(const LinArgs& a, cudaStream_t s) {
-    const int sms = num_sms(), G = a.K / GROUP;
-    const long long tiles16 = (a.N + 15) / 16;
-    const bool wide = tiles16 >= 8LL * sms;
-    const int rows = a.T > 8 ? 32 : wide ? 64 : 16;
-    const long long tiles = (a.N + rows - 1) / rows;
+    const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
+    if (a.T > 8) {
+        const int tiles = (nb + LIN_WARPS * BATCH_RM - 1) / (LIN_WARPS * BATCH_RM), zs = (a.T + TOK - 1) / TOK;
+        int S = 1;
+        while (S < 8 && (long long)tiles * zs * S < 2LL * sms && G / (2 * S) >= 4) S *= 2;
+        return launch(k_linear_batch<XT>, a, dim3(tiles, S, zs), sizeof(BatchSmem<XT>), s);
+    }
+    if (nb >= 8 * sms) {
+        const int tiles = (nb + 3) / 4;
+        return launch(k_linear_vec<XT, 4>, a, dim3(tiles < 2 * sms ? tiles : 2 * sms, 1), VecRing<4>::SMEM, s);
+    }
     int S = 1;
-    while (S < 8 && tiles * S < 2LL * sms && G / (2 * S) >= LIN_WARPS / 2) S *= 2;
-    if (a.T > 8) return launch<XT, 2, 4>(a, S, s);
-    return wide ? launch<XT, 4, 1>(a, S, s) : launch<XT, 1, 1>(a, S, s);
+    while (S < 8 && (long long)nb * S < 2LL * sms && G / (2 * S) >= LIN_WARPS / 2) S *= 2;
+    return launch(k_linear_vec<XT, 1>, a, dim3(nb, S), VecRing<1>::SMEM, s);
 }
 
 // A thread writes one lane's 16 bytes of codes of one record; lanes 0..7 also
@@ -318,6 +596,7 @@ __global__ void k_pack_linear(e0_qtensor src, int N, int K, uint8_t* dst) {
             w[i] |= v << (4 * h);
         }
     }
+    for (int i = 0; i < 4; ++i) w[i] = (w[i] << 3) | (w[i] >> 29);
     *reinterpret_cast<uint4*>(out + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     if (lane < 8) {
         uint32_t p[2];
