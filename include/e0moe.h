@@ -102,7 +102,7 @@ enum { E0_ROUTE_SOFTMAX_TOPK = 0, E0_ROUTE_SIGMOID_GROUP = 1 };
 
 /* Limits of the kernels (E0_ERR_UNSUPPORTED beyond them). */
 enum { E0_MAX_E = 1024, E0_MAX_K = 32, E0_MAX_T_DECODE = 64, E0_MAX_LORA_RANK = 64 };
-enum { E0_MAX_NORM_H = 16384, E0_MAX_SEQS = 4096, E0_MAX_T_LINEAR = 524280 };
+enum { E0_MAX_NORM_H = 16384, E0_MAX_SEQS = 4096, E0_MAX_T_LINEAR = 524280, E0_MAX_K_LINEAR = 1 << 20 };
 
 /* ---- element types of the calls that take one -------------------------
  * E0_E4M3 is the 8-bit float with 4 exponent and 3 mantissa bits, no infinity
@@ -489,7 +489,7 @@ size_t e0_linear_bytes(int N, int K);
  * i and i + 8, i = 0..7.  Lane l holds rows l/4 and l/4 + 8 and the inputs
  * 16*(l%4) .. + 15; its word i holds the inputs 4i..4i+3 of those, nibbles
  * 0, 4 = row l/4 inputs 0, 1; 1, 5 = row l/4 + 8 inputs 0, 1; 2, 6 and 3, 7
- * the same for inputs 2, 3; the word is then rotated left by 3 bits.  src is a host descriptor of device pointers, dst
+ * the same for inputs 2, 3.  src is a host descriptor of device pointers, dst
  * device memory of e0_linear_bytes(N, K) bytes, 16-byte aligned.
  * Asynchronous. */
 int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_t stream);
@@ -504,7 +504,7 @@ int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_
  * equal bits.  A row of x that holds a NaN or infinity gives a row of y that
  * is not finite; other rows are not touched by it.  Any T: the weights are
  * read once for every 8 to 32 rows, so the call is made for decode batches, not
- * for long prompts (T > E0_MAX_T_LINEAR -> E0_ERR_UNSUPPORTED).  Errors: a NULL x, y or w, or no x_scale where x_type
+ * for long prompts (T > E0_MAX_T_LINEAR, K > E0_MAX_K_LINEAR -> E0_ERR_UNSUPPORTED).  Errors: a NULL x, y or w, or no x_scale where x_type
  * wants one -> E0_ERR_NULL; sizes not positive, K no multiple of 64, an
  * unknown type, a row stride below the row, a w that is not 16-byte aligned,
  * or a pointer that its element type does not align -> E0_ERR_ARG. */

@@ -366,7 +366,7 @@ int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type,
                       int T, const void* add, int64_t add_ld, void* y, int y_type, int64_t y_ld, e0_stream_t stream) {
     if (T < 0 || N < 1 || K < 1 || K % 64 != 0) return E0_ERR_ARG;
     if (!(float_type(x_type) || x_type == E0_E4M3) || !float_type(y_type)) return E0_ERR_ARG;
-    if (T > E0_MAX_T_LINEAR) return E0_ERR_UNSUPPORTED;
+    if (T > E0_MAX_T_LINEAR || K > E0_MAX_K_LINEAR) return E0_ERR_UNSUPPORTED;
     if (T == 0) return E0_OK;
     if (!w || !x || !y || (x_type == E0_E4M3 && !x_scale)) return E0_ERR_NULL;
     if (x_ld < K || y_ld < N || (add && add_ld < N)) return E0_ERR_ARG;

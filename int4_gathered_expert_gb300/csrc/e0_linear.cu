@@ -20,12 +20,14 @@ namespace {
 // Decode is bound by reading the weights: 4.5 bits each, once.  The layout gives a
 // lane its 16 x 64 tile's fragment with one 16-byte load.
 //
-// Codes as operands cost a mask (and a rotation for three of four): they stand
-// in the bits 3..6 of a half.  As fp16 that is the subnormal number code * 2^-21,
-// exact; the scale takes the 2^21.  As bf16, with the exponent of 16 set, it is 16 +
-// code; the product is then too large by 16 sum x, which goes into the bias.  (With
-// codes in the bits 0..3 it would be 128 + code, and the sums' rounding 5 times as
-// large; subtracting the 128 again took a third of the instructions.)
+// Codes as operands cost a mask and a shift for some.  fp16: a code in the bits
+// 0..3 of a half is the subnormal number code * 2^-24, exact, in the bits 4..7 code *
+// 2^-20; the layout gives all codes of the lower row the first place and of the
+// upper row the second, and the rows' scales take the factors.  bf16: in the bits
+// 3..6, with the exponent of 16 set, it is 16 + code; the product is then too large
+// by 16 sum x, which goes into the bias.  (In the bits 0..3 it would be 128 + code
+// and the sums' rounding 5 times as large; subtracting the 128 again took a
+// third of the instructions.)
 // Activations: fp16 and bf16 as they are; e4m3 widened to fp16 (exact), its
 // scale applied to the group's sums; fp32 as three bf16 parts (8 significant bits
 // each, cut off, the sum exact), three products a step.
@@ -59,21 +61,27 @@ E0_DEV void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
 // One word of a lane's codes -> its A fragment of one step.
 template <bool BF>
 E0_DEV void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t q = __funnelshift_r(w, w, 4 * i) & 0x00780078u;
-        a[i] = BF ? q | 0x41804180u : q;
+    if (BF) {
+        a[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+        a[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+        a[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+        a[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    } else {
+        a[0] = w & 0x000F000Fu;
+        a[1] = w & 0x00F000F0u;
+        a[2] = (w >> 8) & 0x000F000Fu;
+        a[3] = (w >> 8) & 0x00F000F0u;
     }
 }
-// What a group's (scale, bias) word turns the sums with: fp16 codes stand for code
-// * 2^-21, bf16 ones for code + 16.
-template <bool BF>
+// What the sums are turned with, from the (scale, bias) word of a lower (i) or
+// upper (i + 8) row.
+template <bool BF, bool UPPER>
 E0_DEV float2 scale_bias(uint32_t w) {
     float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
     if (BF)
         f.y = fmaf(-16.f, f.x, f.y);
     else
-        f.x *= 2097152.f;
+        f.x *= UPPER ? 1048576.f : 16777216.f;
     return f;
 }
 
@@ -232,22 +240,30 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
     const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
     const uint32_t ones[4] = {one, one, one, one};
 
-    // where the next copy comes from and goes to
+    // where the next copy comes from and goes to; the lane's 16-byte pieces of a step
+    constexpr int PIECES = (RM * 36 + 31) / 32;
+    uint32_t piece[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int c = i * 32 + lane;
+        piece[i] = (uint32_t)(c / 36) * (uint32_t)(G - 1) * REC + c * 16;
+    }
     int in_tile = blockIdx.x, in_g = g0 + warp, in_stage = 0;
-    constexpr int PIECES = (RM * 36 + 31) / 32;  // 16-byte pieces of a step that a lane copies
+    const uint8_t* src = A.w + ((size_t)in_tile * RM * G + in_g) * REC;
     const auto issue = [&]() {
         if (in_tile < tiles && in_g < g1) {
             uint8_t* dst = ring + in_stage * VecRing<RM>::BYTES + lane * 16;
-            const uint8_t* src = A.w + ((size_t)in_tile * RM * G + in_g) * REC;
-            const int left = (nb - in_tile * RM) * 36;  // rows beyond the last block are not stored
+            const int mine = min(RM, nb - in_tile * RM) * 36 - lane;  // rows beyond the last block are not stored
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                const int c = i * 32 + lane, r = c / 36;
-                if (c < min(RM * 36, left)) copy16(dst + i * 512, src + (size_t)(r * (G - 1) * REC) + c * 16);
-            }
+            for (int i = 0; i < PIECES; ++i)
+                if (i * 32 < mine) copy16(dst + i * 512, src + piece[i]);
             if (++in_stage == STAGES) in_stage = 0;
             in_g += LIN_WARPS;
-            if (in_g >= g1) in_g = g0 + warp, in_tile += gridDim.x;
+            src += LIN_WARPS * REC;
+            if (in_g >= g1) {
+                in_g = g0 + warp, in_tile += gridDim.x;
+                src = A.w + ((size_t)in_tile * RM * G + in_g) * REC;
+            }
         }
         copy_commit();
     };
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
 #pragma unroll
                     for (int p = 0; p < P; ++p) mma16(d, a, b[p][2 * i], b[p][2 * i + 1], BF);
                 }
-                const float2 lo = scale_bias<BF>(sb.x), hi = scale_bias<BF>(sb.y);
+                const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
                 add_group<XT == E0_E4M3>(tot[r], d, lo.x, lo.y, hi.x, hi.y, sx, xs);
             }
         }
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
 // groups are formed there by all warps one group ahead; a warp's records
 // come through its ring as above.  The blocks of a cluster split K.
 constexpr int TOK = 32;
-constexpr int BATCH_RM = 1;
+constexpr int BATCH_RM = 2;
 
 template <int XT>
 struct BatchSmem {
@@ -380,37 +396,52 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);
     const int nb = (A.N + 15) / 16, rb0 = (blockIdx.x * LIN_WARPS + warp) * RM, tok0 = blockIdx.z * TOK;
 
+    // the thread's 16-byte pieces of a group of its warp's records and of x
+    constexpr int PIECES = (RM * 36 + 31) / 32, XPIECES = (TOK * PER + LIN_WARPS * 32 - 1) / (LIN_WARPS * 32);
+    uint32_t piece[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int c = i * 32 + lane;
+        piece[i] = (uint32_t)(c / 36) * (uint32_t)(G - 1) * REC + c * 16;
+    }
+    const int mine = min(RM, nb - rb0) * 36 - lane;
+    const uint8_t* src = A.w + ((size_t)rb0 * G + g0) * REC;
+    const uint8_t* xsrc[XPIECES];
+    uint32_t xdst[XPIECES];
+#pragma unroll
+    for (int i = 0; i < XPIECES; ++i) {
+        const int e = i * LIN_WARPS * 32 + tid, t = e / PER, c = e % PER;
+        xdst[i] = 16 * x_chunk<XT>(t, c);
+        xsrc[i] = t < TOK && tok0 + t < A.T
+                      ? reinterpret_cast<const uint8_t*>(A.x) + ((size_t)(tok0 + t) * A.x_ld + g0 * GROUP) * SZ + c * 16
+                      : nullptr;
+        if (t < TOK && !xsrc[i])  // tokens that are not there: zeros in all stages
+            for (int k = 0; k < STAGES; ++k) *reinterpret_cast<uint4*>(M.x[k] + xdst[i]) = make_uint4(0, 0, 0, 0);
+    }
+    int in_stage = 0;
     const auto issue = [&](int g) {
         if (g < g1) {
-            const int stage = (g - g0) % STAGES;
-            uint8_t* dst = M.rec[stage][warp] + lane * 16;
-            const uint8_t* src = A.w + ((size_t)rb0 * G + g) * REC;
-            const int left = (nb - rb0) * 36;
+            uint8_t* dst = M.rec[in_stage][warp] + lane * 16;
 #pragma unroll
-            for (int i = 0; i < (RM * 36 + 31) / 32; ++i) {
-                const int c = i * 32 + lane, r = c / 36;
-                if (c < min(RM * 36, left)) copy16(dst + i * 512, src + (size_t)(r * (G - 1) * REC) + c * 16);
-            }
+            for (int i = 0; i < PIECES; ++i)
+                if (i * 32 < mine) copy16(dst + i * 512, src + piece[i]);
+            src += REC;
 #pragma unroll
-            for (int i = 0; i < (TOK * PER + LIN_WARPS * 32 - 1) / (LIN_WARPS * 32); ++i) {
-                const int e = i * LIN_WARPS * 32 + tid, t = e / PER, c = e % PER;
-                if (t < TOK) {
-                    const uint8_t* src = reinterpret_cast<const uint8_t*>(A.x) +
-                                         ((size_t)(tok0 + t) * A.x_ld + g * GROUP) * SZ + c * 16;
-                    uint8_t* to = M.x[stage] + 16 * x_chunk<XT>(t, c);
-                    if (tok0 + t >= A.T)
-                        *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
-                    else if (A.vec)
-                        copy16(to, src);
-                    else
-#pragma unroll
+            for (int i = 0; i < XPIECES; ++i)
+                if (xsrc[i]) {
+                    uint8_t* to = M.x[in_stage] + xdst[i];
+                    if (A.vec) {
+                        copy16(to, xsrc[i]);
+                    } else {
                         for (int k = 0; k < 16; k += SZ) {
-                            if (SZ == 4) *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(src + k);
-                            if (SZ == 2) *reinterpret_cast<uint16_t*>(to + k) = *reinterpret_cast<const uint16_t*>(src + k);
-                            if (SZ == 1) to[k] = src[k];
+                            if (SZ == 4) *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(xsrc[i] + k);
+                            if (SZ == 2) *reinterpret_cast<uint16_t*>(to + k) = *reinterpret_cast<const uint16_t*>(xsrc[i] + k);
+                            if (SZ == 1) to[k] = xsrc[i][k];
                         }
+                    }
+                    xsrc[i] += GROUP * SZ;
                 }
-            }
+            if (++in_stage == STAGES) in_stage = 0;
         }
         copy_commit();
     };
@@ -462,49 +493,38 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
         issue(g + STAGES - 1);
         sum_x(g + 1);
         const int stage = (g - g0) % STAGES;
-        uint4 c[RM];
-        uint2 sb[RM];
+        uint32_t b[P == 1 ? NT : 1][P][8];  // one part: all tiles' operands stay for the rows to come
+        if constexpr (P == 1) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) fragments_of(stage, n, b[n]);
+        }
 #pragma unroll
         for (int r = 0; r < RM; ++r) {
-            c[r] = *reinterpret_cast<const uint4*>(M.rec[stage][warp] + r * REC + lane * 16);
-            sb[r] = *reinterpret_cast<const uint2*>(M.rec[stage][warp] + r * REC + 512 + gid * 8);
-        }
-        float d[RM][NT][4];
+            const uint8_t* rec = M.rec[stage][warp] + r * REC;
+            const uint4 c = *reinterpret_cast<const uint4*>(rec + lane * 16);
+            const uint2 sb = *reinterpret_cast<const uint2*>(rec + 512 + gid * 8);
+            const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
+            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+            uint32_t a[4][4];
 #pragma unroll
-        for (int r = 0; r < RM; ++r)
+            for (int i = 0; i < 4; ++i) unpack_codes<BF>(cw[i], a[i]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) d[r][n][0] = d[r][n][1] = d[r][n][2] = d[r][n][3] = 0.f;
-        uint32_t a[RM][4][4];
+            for (int n = 0; n < NT; ++n) {
+                if constexpr (P > 1) fragments_of(stage, n, b[0]);
+                const uint32_t(&bn)[P][8] = b[P == 1 ? n : 0];
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < RM; ++r) {
-            const uint32_t cw[4] = {c[r].x, c[r].y, c[r].z, c[r].w};
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack_codes<BF>(cw[i], a[r][i]);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            uint32_t b[P][8];
-            fragments_of(stage, n, b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-#pragma unroll
-                    for (int r = 0; r < RM; ++r) mma16(d[r][n], a[r][i], b[p][2 * i], b[p][2 * i + 1], BF);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[g & 1][8 * n + 2 * t4]);
-            const float sx[2] = {sx2.x, sx2.y};
-            float xs[2] = {1.f, 1.f};
-            if constexpr (XT == E0_E4M3) {
-                const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[g & 1][8 * n + 2 * t4]);
-                xs[0] = x2.x, xs[1] = x2.y;
-            }
-#pragma unroll
-            for (int r = 0; r < RM; ++r) {
-                const float2 lo = scale_bias<BF>(sb[r].x), hi = scale_bias<BF>(sb[r].y);
-                add_group<XT == E0_E4M3>(tot[r][n], d[r][n], lo.x, lo.y, hi.x, hi.y, sx, xs);
+                    for (int p = 0; p < P; ++p) mma16(d, a[i], bn[p][2 * i], bn[p][2 * i + 1], BF);
+                const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[g & 1][8 * n + 2 * t4]);
+                const float sx[2] = {sx2.x, sx2.y};
+                float xs[2] = {1.f, 1.f};
+                if constexpr (XT == E0_E4M3) {
+                    const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[g & 1][8 * n + 2 * t4]);
+                    xs[0] = x2.x, xs[1] = x2.y;
+                }
+                add_group<XT == E0_E4M3>(tot[r][n], d, lo.x, lo.y, hi.x, hi.y, sx, xs);
             }
         }
     }
@@ -596,7 +616,6 @@ __global__ void k_pack_linear(e0_qtensor src, int N, int K, uint8_t* dst) {
             w[i] |= v << (4 * h);
         }
     }
-    for (int i = 0; i < 4; ++i) w[i] = (w[i] << 3) | (w[i] >> 29);
     *reinterpret_cast<uint4*>(out + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     if (lane < 8) {
         uint32_t p[2];

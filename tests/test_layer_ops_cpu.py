@@ -54,7 +54,8 @@ LIN = dict(w=P, N=64, K=128, x=P, x_type=0, x_ld=128, x_scale=None, T=1, add=Non
     (dict(y_type=3), "ARG"), (dict(w=None), "NULL"), (dict(x=None), "NULL"), (dict(y=None), "NULL"),
     (dict(x_type=3), "NULL"), (dict(x_ld=127), "ARG"), (dict(y_ld=63), "ARG"), (dict(add=P, add_ld=63), "ARG"),
     (dict(w=P + 8), "ARG"), (dict(x=P + 2), "ARG"), (dict(y=P + 2), "ARG"), (dict(add=2 * P, add_ld=65), "ARG"),
-    (dict(x_type=3, x_scale=P + 1), "ARG"), (dict(T=524281), "UNSUPPORTED"), (dict(T=0, x=None), "OK")])
+    (dict(x_type=3, x_scale=P + 1), "ARG"), (dict(T=524281), "UNSUPPORTED"),
+    (dict(K=(1 << 20) + 64, x_ld=1 << 21), "UNSUPPORTED"), (dict(T=0, x=None), "OK")])
 def test_linear_refusals(L, change, code):
     want = L.E0_OK if code == "OK" else getattr(L, "E0_ERR_" + code)
     assert call(L.e0_linear_forward, LIN, **change) == want
