@@ -483,8 +483,9 @@ int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, in
 size_t e0_linear_bytes(int N, int K);
 
 /* Lay out a canonical Q-tensor ([N] rows of K inputs) for e0_linear_forward:
- * for each block of 16 rows (the last one filled up with zero rows) and each
- * group of 64 inputs one record of 576 bytes, [row block][group]: 512 bytes of
+ * for each block of 16 rows and each group of 64 inputs one record of 576 bytes,
+ * [row block / 8][group][row block % 8], filled up with zero rows to a
+ * multiple of 128: 512 bytes of
  * codes, 16 for each of 32 lanes, then 8 (scale, bias) fp16 pairs of the rows
  * i and i + 8, i = 0..7.  Lane l holds rows l/4 and l/4 + 8 and the inputs
  * 16*(l%4) .. + 15; its word i holds the inputs 4i..4i+3 of those, nibbles

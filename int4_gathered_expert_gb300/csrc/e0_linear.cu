@@ -34,6 +34,8 @@ namespace {
 // Rounding: products are exact in fp32, sums and the scaling are fp32.
 
 constexpr int REC = 576;          // bytes of one 16-row, 64-input record
+constexpr int SUPER = 8;          // row blocks whose records of a group stand together
+constexpr int SREC = SUPER * REC;
 constexpr int LIN_WARPS = 8;
 
 struct LinArgs {
@@ -62,10 +64,10 @@ E0_DEV void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
 template <bool BF>
 E0_DEV void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
     if (BF) {
-        a[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-        a[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-        a[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-        a[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+        const uint32_t v[4] = {w << 3, w >> 1, w >> 5, w >> 9};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // (v & mask) | exponents in one instruction
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(v[i]), "r"(0x00780078u), "r"(0x41804180u));
     } else {
         a[0] = w & 0x000F000Fu;
         a[1] = w & 0x00F000F0u;
@@ -220,9 +222,13 @@ struct Spread {
 // memory, always in the same order.
 template <int RM>
 struct VecRing {
-    static constexpr int STAGES = RM == 4 ? 4 : 8;
+    static constexpr int STAGES = RM == 8 ? 2 : RM == 4 ? 3 : 8;
     static constexpr int BYTES = RM * REC;
     static constexpr int SMEM = LIN_WARPS * STAGES * BYTES;
+    // the warps' sums, [warp][row][T | 1], and the cluster's
+    static int smem(int T, int S) {
+        return SMEM + LIN_WARPS * RM * 16 * (T | 1) * 4 + (S > 1 ? RM * 16 * 8 * 4 : 0);
+    }
 };
 
 template <int XT, int RM>
@@ -230,39 +236,36 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
     constexpr bool BF = XT == E0_F32 || XT == E0_BF16;
     constexpr int P = RawX<XT>::PARTS, ROWS = RM * 16, STAGES = VecRing<RM>::STAGES;
     extern __shared__ __align__(128) uint8_t lin_sm[];
-    __shared__ float part[LIN_WARPS][ROWS][9];
-    __shared__ float sums[RM == 1 ? ROWS * 8 : 1];  // one block of rows is all that a cluster has
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t4 = lane & 3;
     uint8_t* ring = lin_sm + warp * STAGES * VecRing<RM>::BYTES;
+    float* part = reinterpret_cast<float*>(lin_sm + VecRing<RM>::SMEM);
+    const int LD = A.T | 1;
     const int G = A.K / GROUP, S = gridDim.y, rank = blockIdx.y;
     const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);
     const int nb = (A.N + 15) / 16, tiles = (nb + RM - 1) / RM;
     const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
     const uint32_t ones[4] = {one, one, one, one};
 
-    // where the next copy comes from and goes to; the lane's 16-byte pieces of a step
-    constexpr int PIECES = (RM * 36 + 31) / 32;
-    uint32_t piece[PIECES];
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const int c = i * 32 + lane;
-        piece[i] = (uint32_t)(c / 36) * (uint32_t)(G - 1) * REC + c * 16;
-    }
+    // where the next copy comes from and goes to
+    constexpr int PIECES = (RM * 36 + 31) / 32;  // 16-byte pieces of a step that a lane copies
     int in_tile = blockIdx.x, in_g = g0 + warp, in_stage = 0;
-    const uint8_t* src = A.w + ((size_t)in_tile * RM * G + in_g) * REC;
+    const auto src_of = [&](int tile) {
+        const int rb = tile * RM;
+        return A.w + ((size_t)(rb / SUPER) * G + g0 + warp) * SREC + (rb % SUPER) * REC + lane * 16;
+    };
+    const uint8_t* src = src_of(in_tile);
     const auto issue = [&]() {
         if (in_tile < tiles && in_g < g1) {
             uint8_t* dst = ring + in_stage * VecRing<RM>::BYTES + lane * 16;
-            const int mine = min(RM, nb - in_tile * RM) * 36 - lane;  // rows beyond the last block are not stored
 #pragma unroll
             for (int i = 0; i < PIECES; ++i)
-                if (i * 32 < mine) copy16(dst + i * 512, src + piece[i]);
+                if (i * 32 + 31 < RM * 36 || i * 32 + lane < RM * 36) copy16(dst + i * 512, src + i * 512);
             if (++in_stage == STAGES) in_stage = 0;
             in_g += LIN_WARPS;
-            src += LIN_WARPS * REC;
+            src += LIN_WARPS * SREC;
             if (in_g >= g1) {
                 in_g = g0 + warp, in_tile += gridDim.x;
-                src = A.w + ((size_t)in_tile * RM * G + in_g) * REC;
+                src = src_of(in_tile);
             }
         }
         copy_commit();
@@ -322,35 +325,29 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
         if (tile != blockIdx.x) __syncthreads();  // the former tile's sums have been read
 #pragma unroll
         for (int r = 0; r < RM; ++r) {
-            part[warp][16 * r + gid][2 * t4] = tot[r][0];
-            part[warp][16 * r + gid][2 * t4 + 1] = tot[r][1];
-            part[warp][16 * r + gid + 8][2 * t4] = tot[r][2];
-            part[warp][16 * r + gid + 8][2 * t4 + 1] = tot[r][3];
+            float* o = part + (warp * ROWS + 16 * r + gid) * LD + 2 * t4;
+            if (2 * t4 < A.T) o[0] = tot[r][0], o[8 * LD] = tot[r][2];
+            if (2 * t4 + 1 < A.T) o[1] = tot[r][1], o[8 * LD + 1] = tot[r][3];
         }
         __syncthreads();
+        const auto sum = [&](int row, int col) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < LIN_WARPS; ++w) v += part[(w * ROWS + row) * LD + col];
+            return v;
+        };
         // rows run along neighbouring threads, so stores to one token's row are coalesced
         if (S == 1) {
-            for (int e = threadIdx.x; e < ROWS * min(A.T, 8); e += LIN_WARPS * 32) {
-                const int row = e % ROWS, col = e / ROWS;
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < LIN_WARPS; ++w) v += part[w][row][col];
-                store_y(A, tile * ROWS + row, col, v);
-            }
-        } else if constexpr (RM == 1) {  // one tile a cluster
-            Spread sp(sums, ROWS * 8);
+            for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32)
+                store_y(A, tile * ROWS + e % ROWS, e / ROWS, sum(e % ROWS, e / ROWS));
+        } else {  // one tile a cluster
+            Spread sp(part + LIN_WARPS * ROWS * LD, ROWS * 8);
             cg::this_cluster().sync();  // all blocks run
-            for (int e = threadIdx.x; e < ROWS * 8; e += LIN_WARPS * 32) {
-                const int row = e % ROWS, col = e / ROWS;
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < LIN_WARPS; ++w) v += part[w][row][col];
-                sp.put(e, v);
-            }
+            for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32) sp.put(e, sum(e % ROWS, e / ROWS));
             cg::this_cluster().sync();  // all sums are where they belong
             for (int i = threadIdx.x; i < sp.share; i += LIN_WARPS * 32) {
                 const int e = rank * sp.share + i;
-                store_y(A, tile * ROWS + e % ROWS, e / ROWS, sp.get(i));
+                if (e < ROWS * A.T) store_y(A, tile * ROWS + e % ROWS, e / ROWS, sp.get(i));
             }
         }
     }
@@ -358,20 +355,27 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
 
 // More than 8 rows of x: 32 of them (TOK) and 128*RM rows of W a block; a warp has
 // 16*RM rows and all warps go through the groups of the block's share of K
-// together.  x comes through shared memory once for the block, its sums over
-// groups are formed there by all warps one group ahead; a warp's records
-// come through its ring as above.  The blocks of a cluster split K.
+// together, PAIR at a time.  x comes through shared memory once for the block,
+// its sums over groups are formed there one step ahead, a tile of 8 tokens
+// and a group by each warp; a warp's records come through its ring as above.  The
+// blocks of a cluster split K.
 constexpr int TOK = 32;
 constexpr int BATCH_RM = 2;
+constexpr int PAIR = 2;
+static_assert(LIN_WARPS == PAIR * TOK / 8, "every warp sums one tile of x and group");
 
 template <int XT>
 struct BatchSmem {
-    static constexpr int STAGES = 4, ROWS = LIN_WARPS * 16 * BATCH_RM;
+    static constexpr int STAGES = 3, ROWS = LIN_WARPS * 16 * BATCH_RM;
     static constexpr int XROW = GROUP * (XT == E0_F32 ? 4 : XT == E0_E4M3 ? 1 : 2);  // bytes
-    uint8_t rec[STAGES][LIN_WARPS][BATCH_RM * REC];
-    uint8_t x[STAGES][TOK * XROW];
-    float sx[2][TOK], xs[2][TOK];
-    float sums[ROWS * (TOK + 1)];  // over the tile, or the cluster's share of it
+    union {
+        struct {
+            uint8_t rec[STAGES][LIN_WARPS][PAIR][BATCH_RM * REC];
+            uint8_t x[STAGES][PAIR][TOK * XROW];
+            float sx[2][PAIR][TOK], xs[2][PAIR][TOK];
+        };
+        float sums[ROWS * (TOK + 1)];  // at the end: over the tile, or the cluster's share of it
+    };
 };
 
 // 16-byte chunk c of token t's group: chunks of odd tokens change places in pairs,
@@ -398,14 +402,9 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
 
     // the thread's 16-byte pieces of a group of its warp's records and of x
     constexpr int PIECES = (RM * 36 + 31) / 32, XPIECES = (TOK * PER + LIN_WARPS * 32 - 1) / (LIN_WARPS * 32);
-    uint32_t piece[PIECES];
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const int c = i * 32 + lane;
-        piece[i] = (uint32_t)(c / 36) * (uint32_t)(G - 1) * REC + c * 16;
-    }
-    const int mine = min(RM, nb - rb0) * 36 - lane;
-    const uint8_t* src = A.w + ((size_t)rb0 * G + g0) * REC;
+    static_assert(SUPER % RM == 0, "a warp's records of a group stand together");
+    const uint8_t* src = A.w + ((size_t)(rb0 / SUPER) * G + g0) * SREC + (rb0 % SUPER) * REC + lane * 16;
+    const bool mine = rb0 < nb;
     const uint8_t* xsrc[XPIECES];
     uint32_t xdst[XPIECES];
 #pragma unroll
@@ -416,62 +415,66 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
                       ? reinterpret_cast<const uint8_t*>(A.x) + ((size_t)(tok0 + t) * A.x_ld + g0 * GROUP) * SZ + c * 16
                       : nullptr;
         if (t < TOK && !xsrc[i])  // tokens that are not there: zeros in all stages
-            for (int k = 0; k < STAGES; ++k) *reinterpret_cast<uint4*>(M.x[k] + xdst[i]) = make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < STAGES * PAIR; ++k)
+                *reinterpret_cast<uint4*>(M.x[k / PAIR][k % PAIR] + xdst[i]) = make_uint4(0, 0, 0, 0);
     }
     int in_stage = 0;
     const auto issue = [&](int g) {
-        if (g < g1) {
-            uint8_t* dst = M.rec[in_stage][warp] + lane * 16;
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-                if (i * 32 < mine) copy16(dst + i * 512, src + piece[i]);
-            src += REC;
+        for (int h = 0; h < PAIR; ++h)
+            if (g + h < g1) {
+                uint8_t* dst = M.rec[in_stage][warp][h] + lane * 16;
 #pragma unroll
-            for (int i = 0; i < XPIECES; ++i)
-                if (xsrc[i]) {
-                    uint8_t* to = M.x[in_stage] + xdst[i];
-                    if (A.vec) {
-                        copy16(to, xsrc[i]);
-                    } else {
-                        for (int k = 0; k < 16; k += SZ) {
-                            if (SZ == 4) *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(xsrc[i] + k);
-                            if (SZ == 2) *reinterpret_cast<uint16_t*>(to + k) = *reinterpret_cast<const uint16_t*>(xsrc[i] + k);
-                            if (SZ == 1) to[k] = xsrc[i][k];
+                for (int i = 0; i < PIECES; ++i)
+                    if (mine && i * 32 + lane < RM * 36) copy16(dst + i * 512, src + i * 512);
+                src += SREC;
+#pragma unroll
+                for (int i = 0; i < XPIECES; ++i)
+                    if (xsrc[i]) {
+                        uint8_t* to = M.x[in_stage][h] + xdst[i];
+                        if (A.vec) {
+                            copy16(to, xsrc[i]);
+                        } else {
+                            for (int k = 0; k < 16; k += SZ) {
+                                if (SZ == 4) *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(xsrc[i] + k);
+                                if (SZ == 2) *reinterpret_cast<uint16_t*>(to + k) = *reinterpret_cast<const uint16_t*>(xsrc[i] + k);
+                                if (SZ == 1) to[k] = xsrc[i][k];
+                            }
                         }
+                        xsrc[i] += GROUP * SZ;
                     }
-                    xsrc[i] += GROUP * SZ;
-                }
-            if (++in_stage == STAGES) in_stage = 0;
-        }
+            }
+        if (++in_stage == STAGES) in_stage = 0;
         copy_commit();
     };
-    const auto fragments_of = [&](int stage, int n, uint32_t (&b)[P][8]) {
+    const auto fragments_of = [&](const uint8_t* x, int n, uint32_t (&b)[P][8]) {
         RawX<XT> r;
 #pragma unroll
         for (int i = 0; i < RawX<XT>::WORDS / 4; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4*>(M.x[stage] + 16 * x_chunk<XT>(8 * n + gid, RawX<XT>::WORDS / 4 * t4 + i));
+            const uint4 u = *reinterpret_cast<const uint4*>(x + 16 * x_chunk<XT>(8 * n + gid, RawX<XT>::WORDS / 4 * t4 + i));
             r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
         }
         fragments<XT>(r, b);
     };
-    // sums over one group of 8 tokens' inputs: warps 0..3 have one tile each
-    const auto sum_x = [&](int g) {
-        if (g >= g1 || warp >= NT) return;
+    // sums over a group of 8 tokens' inputs: the warp's tile and group of a step
+    const auto sum_x = [&](int step, int stage, int g) {
+        const int h = warp / NT, n = warp % NT;
+        if (g + h >= g1) return;
         const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
         const uint32_t ones[4] = {one, one, one, one};
         uint32_t b[P][8];
-        fragments_of((g - g0) % STAGES, warp, b);
+        fragments_of(M.x[stage][h], n, b);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int p = 0; p < P; ++p) mma16(d, ones, b[p][2 * i], b[p][2 * i + 1], BF);
         if (gid == 0) {
-            const int t = 8 * warp + 2 * t4;
-            M.sx[g & 1][t] = d[0], M.sx[g & 1][t + 1] = d[1];
+            const int t = 8 * n + 2 * t4;
+            *reinterpret_cast<float2*>(&M.sx[step & 1][h][t]) = make_float2(d[0], d[1]);
             if constexpr (XT == E0_E4M3) {
-                M.xs[g & 1][t] = tok0 + t < A.T ? __ldg(A.xs + (size_t)(tok0 + t) * G + g) : 0.f;
-                M.xs[g & 1][t + 1] = tok0 + t + 1 < A.T ? __ldg(A.xs + (size_t)(tok0 + t + 1) * G + g) : 0.f;
+                M.xs[step & 1][h][t] = tok0 + t < A.T ? __ldg(A.xs + (size_t)(tok0 + t) * G + g + h) : 0.f;
+                M.xs[step & 1][h][t + 1] = tok0 + t + 1 < A.T ? __ldg(A.xs + (size_t)(tok0 + t + 1) * G + g + h) : 0.f;
             }
         }
     };
@@ -482,56 +485,78 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) tot[r][n][0] = tot[r][n][1] = tot[r][n][2] = tot[r][n][3] = 0.f;
 #pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) issue(g0 + i);
+    for (int i = 0; i < STAGES - 1; ++i) issue(g0 + i * PAIR);
     copy_wait<STAGES - 2>();
     __syncthreads();
-    sum_x(g0);
+    sum_x(0, 0, g0);
+    int stage = 0, step = 0;
 #pragma unroll 1
-    for (int g = g0; g < g1; ++g) {
+    for (int g = g0; g < g1; g += PAIR, ++step) {
         copy_wait<STAGES - 3>();
-        __syncthreads();  // groups g and g + 1 and the sums of g are there; g - 1 has been read
-        issue(g + STAGES - 1);
-        sum_x(g + 1);
-        const int stage = (g - g0) % STAGES;
-        uint32_t b[P == 1 ? NT : 1][P][8];  // one part: all tiles' operands stay for the rows to come
-        if constexpr (P == 1) {
+        __syncthreads();  // this step and the next and this one's sums are there; the last one has been read
+        issue(g + (STAGES - 1) * PAIR);
+        const int ahead = stage + 1 == STAGES ? 0 : stage + 1;
+        sum_x(step + 1, ahead, g + PAIR);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) fragments_of(stage, n, b[n]);
-        }
+        for (int h = 0; h < PAIR; ++h) {
+            if (g + h >= g1) break;
+            const uint8_t* x = M.x[stage][h];
+            uint32_t b[P == 1 ? NT : 1][P][8];  // one part: all tiles' operands stay for the rows to come
+            if constexpr (P == 1) {
 #pragma unroll
-        for (int r = 0; r < RM; ++r) {
-            const uint8_t* rec = M.rec[stage][warp] + r * REC;
-            const uint4 c = *reinterpret_cast<const uint4*>(rec + lane * 16);
-            const uint2 sb = *reinterpret_cast<const uint2*>(rec + 512 + gid * 8);
-            const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-            uint32_t a[4][4];
+                for (int n = 0; n < NT; ++n) fragments_of(x, n, b[n]);
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack_codes<BF>(cw[i], a[i]);
+            for (int r = 0; r < RM; ++r) {
+                const uint8_t* rec = M.rec[stage][warp][h] + r * REC;
+                const uint4 c = *reinterpret_cast<const uint4*>(rec + lane * 16);
+                const uint2 sb = *reinterpret_cast<const uint2*>(rec + 512 + gid * 8);
+                const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
+                const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+                float d[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (P > 1) fragments_of(stage, n, b[0]);
-                const uint32_t(&bn)[P][8] = b[P == 1 ? n : 0];
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+                if constexpr (P == 1) {  // NT chains of products at once
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a[4];
+                        unpack_codes<BF>(cw[i], a);
 #pragma unroll
-                    for (int p = 0; p < P; ++p) mma16(d, a[i], bn[p][2 * i], bn[p][2 * i + 1], BF);
-                const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[g & 1][8 * n + 2 * t4]);
-                const float sx[2] = {sx2.x, sx2.y};
-                float xs[2] = {1.f, 1.f};
-                if constexpr (XT == E0_E4M3) {
-                    const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[g & 1][8 * n + 2 * t4]);
-                    xs[0] = x2.x, xs[1] = x2.y;
+                        for (int n = 0; n < NT; ++n) mma16(d[n], a, b[n][0][2 * i], b[n][0][2 * i + 1], BF);
+                    }
+                } else {
+                    uint32_t a[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) unpack_codes<BF>(cw[i], a[i]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        fragments_of(x, n, b[0]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int p = 0; p < P; ++p) mma16(d[n], a[i], b[0][p][2 * i], b[0][p][2 * i + 1], BF);
+                    }
                 }
-                add_group<XT == E0_E4M3>(tot[r][n], d, lo.x, lo.y, hi.x, hi.y, sx, xs);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[step & 1][h][8 * n + 2 * t4]);
+                    const float sx[2] = {sx2.x, sx2.y};
+                    float xs[2] = {1.f, 1.f};
+                    if constexpr (XT == E0_E4M3) {
+                        const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[step & 1][h][8 * n + 2 * t4]);
+                        xs[0] = x2.x, xs[1] = x2.y;
+                    }
+                    add_group<XT == E0_E4M3>(tot[r][n], d[n], lo.x, lo.y, hi.x, hi.y, sx, xs);
+                }
             }
         }
+        stage = ahead;
     }
     copy_wait<0>();
     const int cols = min(A.T - tok0, TOK);
     if (S == 1) {
         constexpr int LD = TOK + 1;
+        __syncthreads();  // all warps are through: the sums stand where x and the records were
 #pragma unroll
         for (int r = 0; r < RM; ++r)
 #pragma unroll
@@ -545,7 +570,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
         return;
     }
     Spread sp(M.sums, SM::ROWS * TOK);
-    cg::this_cluster().sync();  // all blocks run
+    cg::this_cluster().sync();  // all warps of all blocks are through
 #pragma unroll
     for (int r = 0; r < RM; ++r)
 #pragma unroll
@@ -587,13 +612,24 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
         while (S < 8 && (long long)tiles * zs * S < 2LL * sms && G / (2 * S) >= 4) S *= 2;
         return launch(k_linear_batch<XT>, a, dim3(tiles, S, zs), sizeof(BatchSmem<XT>), s);
     }
-    if (nb >= 8 * sms) {
-        const int tiles = (nb + 3) / 4;
-        return launch(k_linear_vec<XT, 4>, a, dim3(tiles < 2 * sms ? tiles : 2 * sms, 1), VecRing<4>::SMEM, s);
-    }
-    int S = 1;
-    while (S < 8 && (long long)nb * S < 2LL * sms && G / (2 * S) >= LIN_WARPS / 2) S *= 2;
-    return launch(k_linear_vec<XT, 1>, a, dim3(nb, S), VecRing<1>::SMEM, s);
+    // The more row blocks a warp has, the less the operands of x cost; but there
+    // have to be blocks for the whole machine, with K split over up to 8 of
+    // them and at least two groups a warp.
+    const int most = G / (2 * LIN_WARPS) < 1 ? 1 : G / (2 * LIN_WARPS) > 8 ? 8 : G / (2 * LIN_WARPS);
+    const auto split = [&](int rm) {
+        const int tiles = (nb + rm - 1) / rm;
+        int S = 1;
+        while (2 * S <= most && (long long)tiles * 2 * S <= 2LL * sms) S *= 2;
+        return S;
+    };
+    const auto fills = [&](int rm) { return (long long)((nb + rm - 1) / rm) * split(rm) * 4 >= 5LL * sms; };
+    const auto grid = [&](int rm) {
+        const int tiles = (nb + rm - 1) / rm, S = split(rm);
+        return dim3(S == 1 && tiles > 2 * sms ? 2 * sms : tiles, S);
+    };
+    if (fills(8)) return launch(k_linear_vec<XT, 8>, a, grid(8), VecRing<8>::smem(a.T, split(8)), s);
+    if (fills(4)) return launch(k_linear_vec<XT, 4>, a, grid(4), VecRing<4>::smem(a.T, split(4)), s);
+    return launch(k_linear_vec<XT, 1>, a, grid(1), VecRing<1>::smem(a.T, split(1)), s);
 }
 
 // A thread writes one lane's 16 bytes of codes of one record; lanes 0..7 also
@@ -601,9 +637,9 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
 __global__ void k_pack_linear(e0_qtensor src, int N, int K, uint8_t* dst) {
     const int G = K / GROUP, lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
     const long long rec = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-    const long long recs = (long long)((N + 15) / 16) * G;
+    const long long recs = (long long)((N + 16 * SUPER - 1) / (16 * SUPER)) * SUPER * G;
     if (rec >= recs) return;
-    const int rb = (int)(rec / G), g = (int)(rec % G);
+    const int g = (int)(rec / SUPER % G), rb = (int)(rec / SUPER / G) * SUPER + (int)(rec % SUPER);
     uint8_t* out = dst + rec * REC;
     uint32_t w[4] = {0, 0, 0, 0};
     for (int h = 0; h < 2; ++h) {
@@ -629,10 +665,10 @@ __global__ void k_pack_linear(e0_qtensor src, int N, int K, uint8_t* dst) {
 
 }  // namespace
 
-size_t linear_bytes(int N, int K) { return (size_t)((N + 15) / 16) * (K / GROUP) * REC; }
+size_t linear_bytes(int N, int K) { return (size_t)((N + 16 * SUPER - 1) / (16 * SUPER)) * (K / GROUP) * SREC; }
 
 int pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, cudaStream_t s) {
-    const long long recs = (long long)((N + 15) / 16) * (K / GROUP);
+    const long long recs = (long long)(linear_bytes(N, K) / REC);
     k_pack_linear<<<(int)((recs + 7) / 8), 256, 0, s>>>(*src, N, K, dst);
     return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }

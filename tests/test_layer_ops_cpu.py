@@ -62,8 +62,8 @@ def test_linear_refusals(L, change, code):
 
 
 def test_pack_linear_refusals_and_sizes(L):
-    assert L.e0_linear_bytes(16, 64) == 576
-    assert L.e0_linear_bytes(17, 128) == 2 * 2 * 576
+    assert L.e0_linear_bytes(1, 64) == L.e0_linear_bytes(128, 64) == 8 * 576
+    assert L.e0_linear_bytes(129, 128) == 2 * 2 * 8 * 576
     assert L.e0_linear_bytes(131072, 8192) == 8192 * 128 * 576
     for n, k in ((0, 64), (1, 0), (1, 63), (-1, 64)):
         assert L.e0_linear_bytes(n, k) == 0
