@@ -65,6 +65,7 @@ int check_kv_cache(const e0_kv_cache* c) {
     if (!c) return E0_ERR_NULL;
     if (!c->k || !c->v || !c->k_scale || !c->v_scale) return E0_ERR_NULL;
     if (c->n_blocks < 1 || c->Hkv < 1) return E0_ERR_ARG;
+    if (c->Hkv > 32767) return E0_ERR_UNSUPPORTED;  // the grid of e0_kv_append
     if (!block_tokens_ok(c->block_tokens) || (c->D != 64 && c->D != 128 && c->D != 256)) return E0_ERR_UNSUPPORTED;
     if (!aligned(16, c->k, c->v) || !aligned(4, c->k_scale, c->v_scale)) return E0_ERR_ARG;
     return E0_OK;
@@ -401,7 +402,6 @@ int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dty
     const int rc = check_kv_cache(cache);
     if (rc) return rc;
     if (T < 0 || !float_type(dtype)) return E0_ERR_ARG;
-    if ((int64_t)T * 2 * cache->Hkv > (int64_t)1 << 33) return E0_ERR_UNSUPPORTED;  // the grid of warps
     if (T == 0) return E0_OK;
     if (!k || !v || !slots) return E0_ERR_NULL;
     const int64_t row = (int64_t)cache->Hkv * cache->D;

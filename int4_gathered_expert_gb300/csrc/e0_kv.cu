@@ -226,15 +226,19 @@ PlanArgs plan_args(const e0_kv_state* k, int32_t* ctx_out, int32_t* free_out, ui
 
 // ------------------------------------------------------------------ append
 //
-// A warp takes one run of tokens of one block, for one head, for keys or
-// values: it finds the largest magnitude of the run, settles the block's
-// scale, rounds the older codes again if the scale grew, and writes the new
-// ones.  Warps are laid out by token; the warp of a run's first token does the
-// run, the others leave after reading two slots.  Scales are powers of two:
-// x / s and code * old / new are then exact, so the only rounding is that to
-// e4m3, and a scale that grows costs nothing but the codes that fall into e4m3's
-// subnormals.  (A scale of max / 448 would round every older code again at each
-// new maximum, and e4m3's relative precision gains nothing from it.)
+// A run is the consecutive new tokens of one block of the cache; for a run, a head and
+// keys or values the kernel finds the largest magnitude, settles the scale, rounds
+// the older codes again if the scale grew, and writes the new ones.  A thread block
+// finds the runs that begin among `per` tokens; it takes each with all its warps,
+// or, where there are many (single tokens), one with each warp.  A few tokens a warp
+// stay in registers between the maximum and the codes, so a run of up to 64 tokens
+// (32 of D = 256) is read once.  Scales are powers of two: x / s and code * old / new are then
+// exact, so the only rounding is that to e4m3, and a scale that grows costs nothing
+// but the codes that fall into e4m3's subnormals.  (A scale of max / 448 would round
+// every older code again at each new maximum, and e4m3's relative precision gains
+// nothing from it.)
+
+constexpr int APP_WARPS = 8;
 
 struct AppendArgs {
     const void* x[2];
@@ -253,50 +257,67 @@ E0_DEV float pow2_scale(float m) {  // smallest 2^e >= 2^-100 with m / 448 (roun
     return __uint_as_float(e << 23);
 }
 
-// A warp's row of one token and head: lane l holds elements l*D/32 ...
+// A lane's D / 32 elements of one token's head, as they are in memory.
 template <int TY, int D>
-E0_DEV void row_load(const typename Elem<TY>::T* p, float (&v)[D / 32], bool vec) {
-    constexpr int N = D / 32;
-    if (vec) {
-        if constexpr (TY == E0_F32) {
-            if constexpr (N == 2) {
-                const float2 f = __ldg(reinterpret_cast<const float2*>(p));
-                v[0] = f.x, v[1] = f.y;
+struct AppRaw {
+    static constexpr int N = D / 32, WORDS = N * (TY == E0_F32 ? 4 : 2) / 4;
+    uint32_t w[WORDS];
+    E0_DEV void load(const typename Elem<TY>::T* p, bool vec) {
+        if (vec) {
+            if constexpr (WORDS == 1) {
+                w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            } else if constexpr (WORDS == 2) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+                w[0] = u.x, w[1] = u.y;
             } else {
-                load_vec<TY, N>(p, v);
-            }
-        } else if constexpr (N == 2) {
-            const float2 f = unpack16<TY>(__ldg(reinterpret_cast<const uint32_t*>(p)));
-            v[0] = f.x, v[1] = f.y;
-        } else {
-            load_vec<TY, N>(p, v);
-        }
-    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = Elem<TY>::get(p[i]);
+                for (int i = 0; i < WORDS / 4; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+                }
+            }
+        } else if constexpr (TY == E0_F32) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+        }
     }
-}
+    E0_DEV void get(float (&v)[N]) const {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (TY == E0_F32) {
+                v[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = unpack16<TY>(w[i]);
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
 
-template <int TY, int D>
-__global__ void __launch_bounds__(256) k_kv_append(AppendArgs A, bool vec) {
+// The run that begins with token t0, by the calling warp (TEAM 1) or by all warps
+// of the thread block together.
+template <int TY, int D, int TEAM>
+E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t0, uint32_t* most) {
     typedef typename Elem<TY>::T T;
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long id = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-    const int per = 2 * A.Hkv;
-    const long long t0 = id / per;
-    if (t0 >= A.T) return;
-    const int which = (int)(id % per) / A.Hkv, head = (int)(id % per) % A.Hkv;
+    constexpr int N = D / 32, HOLD = D == 256 ? 4 : 8;
+    const int lane = threadIdx.x & 31, member = TEAM == 1 ? 0 : threadIdx.x >> 5;
     const int bs = 1 << A.shift;
     const int64_t slot = A.slots[t0];
-    if (slot < 0) return;
     const int off = (int)(slot & (bs - 1));
-    if (off != 0 && t0 > 0 && A.slots[t0 - 1] == slot - 1) return;  // inside a run
     const int64_t blk = slot >> A.shift;
     if (blk >= A.n_blocks) {
-        if (lane == 0) set_status(A.st, E0_ST_BAD_BLOCK);
+        if (member == 0 && lane == 0) set_status(A.st, E0_ST_BAD_BLOCK);
         return;
     }
+    const int64_t ld = which ? A.ld[1] : A.ld[0];
+    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + t0 * ld + (size_t)head * D + lane * N;
+    float* scale = (which ? A.scale[1] : A.scale[0]) + (size_t)blk * A.Hkv + head;
+    uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
+    float old = off > 0 ? *scale : 0.f;
     // the run's length: tokens that follow with consecutive slots inside the block
     int n = 0;
     for (;;) {
@@ -306,28 +327,42 @@ __global__ void __launch_bounds__(256) k_kv_append(AppendArgs A, bool vec) {
         n += out ? __ffs(out) - 1 : 32;
         if (out) break;
     }
-    const int64_t ld = which ? A.ld[1] : A.ld[0];
-    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + t0 * ld + (size_t)head * D + lane * N;
-    uint32_t m = 0;
-    bool bad = false;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    // member w has the tokens w, w + TEAM, ...; beyond the last it reads the last again
+    AppRaw<TY, D> held[HOLD];
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) held[k].load(x + (size_t)min(member + k * TEAM, n - 1) * ld, vec);
+    uint32_t m = 0, all = 0;
+    const auto look = [&](const AppRaw<TY, D>& r) {
         float v[N];
-        row_load<TY, D>(x + (size_t)i * ld, v, vec);
+        r.get(v);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-            if (a < 0x7F800000u) m = max(m, a); else bad = true;
+            all = max(all, a);
+            m = max(m, a < 0x7F800000u ? a : 0u);
         }
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) look(held[k]);
+#pragma unroll 1
+    for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
+        AppRaw<TY, D> r;
+        r.load(x + (size_t)i * ld, vec);
+        look(r);
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(A.st, E0_ST_NONFINITE);
-
-    float* scale = (which ? A.scale[1] : A.scale[0]) + (size_t)blk * A.Hkv + head;
-    uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
+    if (__any_sync(0xffffffffu, all >= 0x7F800000u) && lane == 0) set_status(A.st, E0_ST_NONFINITE);
+    if constexpr (TEAM > 1) {
+        if (lane == 0) most[member] = m;
+        __syncthreads();  // and the old scale has been read
+#pragma unroll
+        for (int w = 0; w < TEAM; ++w) m = max(m, most[w]);
+        __syncthreads();  // most has been read
+    } else {
+        __syncwarp();
+    }
     float s = pow2_scale(__uint_as_float(m));
     if (off > 0) {
-        float old = *scale;
         if (!(old > 0.f && old < 3.0e38f)) old = s;  // nothing a call of ours wrote: the codes stay as they are
         s = fmaxf(s, old);
         if (s > old) {
@@ -335,9 +370,9 @@ __global__ void __launch_bounds__(256) k_kv_append(AppendArgs A, bool vec) {
             uint4* c = reinterpret_cast<uint4*>(codes);
             const int words = off * D / 16;
 #pragma unroll 4
-            for (int i = lane; i < words; i += 32) {
-                uint4 u = c[i];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+            for (int i = member * 32 + lane; i < words; i += TEAM * 32) {
+                const uint4 u = c[i];
+                uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t r = 0;
@@ -348,17 +383,15 @@ __global__ void __launch_bounds__(256) k_kv_append(AppendArgs A, bool vec) {
                     }
                     w[k] = r;
                 }
-                c[i] = u;
+                c[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
     }
-    __syncwarp();
-    if (lane == 0) *scale = s;
+    if (member == 0 && lane == 0) *scale = s;
     const float inv = 1.f / s;  // a power of two
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    const auto write = [&](int i, const AppRaw<TY, D>& r) {
         float v[N];
-        row_load<TY, D>(x + (size_t)i * ld, v, vec);
+        r.get(v);
         uint32_t c[(N + 3) / 4] = {};
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
@@ -372,6 +405,38 @@ __global__ void __launch_bounds__(256) k_kv_append(AppendArgs A, bool vec) {
             *reinterpret_cast<uint32_t*>(p) = c[0];
         else
             *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+    };
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+        if (member + k * TEAM < n) write(member + k * TEAM, held[k]);
+#pragma unroll 1
+    for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
+        AppRaw<TY, D> r;
+        r.load(x + (size_t)i * ld, vec);
+        write(i, r);
+    }
+}
+
+// per: 8 or 16 (the smallest block: two runs of a prompt can begin among as many tokens).
+template <int TY, int D>
+__global__ void __launch_bounds__(APP_WARPS * 32, 4) k_kv_append(AppendArgs A, bool vec, int per) {
+    __shared__ uint32_t most[APP_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head = blockIdx.y >> 1, which = blockIdx.y & 1;
+    // the tokens that begin a run, the same for every warp
+    const long long t = (long long)blockIdx.x * per + lane;
+    bool begins = false;
+    if (lane < per && t < A.T) {
+        const int64_t slot = A.slots[t], before = t > 0 ? A.slots[t - 1] : -2;
+        begins = slot >= 0 && ((slot & ((1 << A.shift) - 1)) == 0 || before != slot - 1);
+    }
+    uint32_t left = __ballot_sync(0xffffffffu, begins);
+    const int base = blockIdx.x * per;
+    if (__popc(left) > 2) {
+        for (int k = 0; left; left &= left - 1, ++k)
+            if (k % APP_WARPS == warp) append_run<TY, D, 1>(A, vec, which, head, base + __ffs(left) - 1, most);
+    } else {
+        for (; left; left &= left - 1) append_run<TY, D, APP_WARPS>(A, vec, which, head, base + __ffs(left) - 1, most);
     }
 }
 
@@ -380,8 +445,9 @@ int append_launch(const AppendArgs& a, cudaStream_t s) {
     const int sz = type_size(TY);
     const uintptr_t need = D / 32 * sz < 16 ? D / 32 * sz : 16;
     const uintptr_t bits = (uintptr_t)a.x[0] | (uintptr_t)a.x[1] | (uintptr_t)(a.ld[0] * sz) | (uintptr_t)(a.ld[1] * sz);
-    const long long warps = (long long)a.T * 2 * a.Hkv;
-    k_kv_append<TY, D><<<(int)((warps + 7) / 8), 256, 0, s>>>(a, !(bits & (need - 1)));
+    // 8 tokens a thread block where 16 would leave SMs without one
+    const int per = (long long)a.T * 2 * a.Hkv >= 16LL * 4 * num_sms() ? 16 : 8;
+    k_kv_append<TY, D><<<dim3((a.T + per - 1) / per, 2 * a.Hkv), APP_WARPS * 32, 0, s>>>(a, !(bits & (need - 1)), per);
     return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
 

@@ -195,20 +195,22 @@ E0_DEV void add_group(float (&tot)[4], const float (&d)[4], float s0, float b0, 
     }
 }
 
-// The sums of the cluster's blocks: element e of a block's N sums belongs to block
-// e / (N / S), and every block writes it there, [its rank][e % (N / S)].
+// The sums of the cluster's blocks (a power of two): element e of a block's n sums
+// belongs to block e / (n / S), and every block writes it there, [its rank][e % (n / S)].
 struct Spread {
-    float* to;  // this block's own [S][N / S]
-    int S, rank, share;
-    E0_DEV Spread(float* buf, int n) : to(buf), S(gridDim.y), rank(blockIdx.y), share(n / S) {}
-    E0_DEV void put(int e, float v) {
-        cg::this_cluster().map_shared_rank(to, e / share)[rank * share + e % share] = v;
+    float* to;  // this block's own [S][n / S]
+    int S, rank, share, bits;
+    E0_DEV Spread(float* buf, int n) : to(buf), S(gridDim.y), rank(blockIdx.y), share(n / S), bits(0) {
+        while ((1 << bits) < share) ++bits;
+    }
+    E0_DEV void put(int e, float v) const {
+        cg::this_cluster().map_shared_rank(to, e >> bits)[(rank << bits) + (e & (share - 1))] = v;
     }
     E0_DEV float get(int i) const {
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < S) v += to[k * share + i];
+            if (k < S) v += to[(k << bits) + i];
         return v;
     }
 };

@@ -8,13 +8,15 @@
 namespace e0 {
 namespace {
 
-// One block per row.  A thread keeps its elements in registers between the
-// two uses of a row (the sum of squares, then the outputs), so a row is read
-// once: bytes moved are the algorithmic ones and the kernel is bound by them.
-// Thread i owns the 8 consecutive elements 8(i + j * blockDim): 8 neighbouring
-// threads hold one group of 64, whose maximum is three shuffles.
-// VEC: H is a multiple of 8 and every row starts on a 16-byte boundary, so the
-// 8 elements are whole vector accesses; otherwise they are checked one by one.
+// A row's elements stay in registers between their two uses (the sum of squares,
+// then the outputs), so a row is read once: bytes moved are the algorithmic ones
+// and the kernel is bound by them.  Chunk c of a row is the 8 consecutive elements
+// 8c...; neighbouring lanes hold neighbouring chunks, so a group of 64 is 8 lanes
+// and its maximum three shuffles.  Two shapes: a block per row (few rows: the
+// latency of one row counts), and a warp per row (many rows: what a row costs
+// beside its elements is shared by 8 times as many).
+// VEC: H is a multiple of 8 and every row starts on a 16-byte boundary, so a chunk
+// is whole vector accesses; otherwise elements are checked one by one.
 struct NormArgs {
     const void* r;
     const void* d;
@@ -25,9 +27,155 @@ struct NormArgs {
     float* qs;
     uint32_t* st;
     int64_t r_ld, d_ld;
-    int H;
-    float eps;
+    int T, H;
+    float eps, inv_h;
 };
+
+// A chunk as it is in memory: the 8 elements from e on (VEC: a place beyond the row
+// reads the row's first chunk instead, so that no branch stands between the loads of
+// several chunks; what it read counts as zeros).  Plain loads, not the read-only path:
+// r_out may be r or d.
+template <int TY, bool VEC>
+struct Chunk {
+    typedef typename Elem<TY>::T T;
+    static constexpr int WORDS = VEC ? (TY == E0_F32 ? 8 : 4) : 8;
+    uint32_t w[WORDS];
+    E0_DEV void load(const T* p, int e, int H) {
+        if constexpr (VEC) {
+            const uint4* q = reinterpret_cast<const uint4*>(p + (e < H ? e : 0));
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 u = q[i];
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = e + i < H ? __float_as_uint(Elem<TY>::get(p[e + i])) : 0u;
+        }
+    }
+    E0_DEV void get(int e, int H, float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (!VEC || TY == E0_F32) {
+                v[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = unpack16<TY>(w[i / 2]);
+                v[i] = i % 2 ? f.y : f.x;
+            }
+            if (VEC && e >= H) v[i] = 0.f;
+        }
+    }
+};
+// s = r + d, rounded to the type.
+template <int TY>
+E0_DEV void add_rounded(float (&v)[8], const float (&w)[8]) {
+    if constexpr (TY == E0_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack16<TY>(pack16<TY>(v[2 * i] + w[2 * i], v[2 * i + 1] + w[2 * i + 1]));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+    }
+}
+// All chunks of a thread: loads first, then the sums and their squares.
+template <int TY, bool VEC, int CH>
+E0_DEV float load_row(const NormArgs& A, size_t row, int c0, int step, float (&v)[CH][8]) {
+    typedef typename Elem<TY>::T T;
+    const T* r = reinterpret_cast<const T*>(A.r) + row * A.r_ld;
+    const T* d = A.d ? reinterpret_cast<const T*>(A.d) + row * A.d_ld : nullptr;
+    Chunk<TY, VEC> a[CH], b[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) a[j].load(r, 8 * (c0 + j * step), A.H);
+    if (d) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) b[j].load(d, 8 * (c0 + j * step), A.H);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int e = 8 * (c0 + j * step);
+        a[j].get(e, A.H, v[j]);
+        if (d) {
+            float w[8];
+            b[j].get(e, A.H, w);
+            add_rounded<TY>(v[j], w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+    }
+    return ss;
+}
+
+template <int TY, bool VEC>
+E0_DEV void store_chunk(typename Elem<TY>::T* p, int e, int H, const float (&v)[8]) {
+    if constexpr (VEC) {
+        if (e < H) store_vec<TY>(p + e, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < H) p[e + i] = Elem<TY>::put(v[i]);
+    }
+}
+
+// A chunk's outputs; all lanes of a warp call it.  Returns whether its group holds a
+// value that is not finite.  rcp.approx and the product with 1 / 448 are an ulp
+// off the divisions, of no account beside the scale's own rounding.
+template <int TY, bool VEC>
+E0_DEV bool finish_chunk(const NormArgs& A, size_t row, int e, float rstd, float (&v)[8]) {
+    typedef typename Elem<TY>::T T;
+    const int H = A.H;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = rstd;
+    if (A.w) {
+        if constexpr (VEC) {
+            if (e < H) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(A.w + e)), g = __ldg(reinterpret_cast<const float4*>(A.w + e) + 1);
+                const float u[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= rstd, w[i] = u[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (e + i < H) v[i] *= rstd, w[i] = __ldg(A.w + e + i);
+        }
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] *= w[i];
+        if (e + i < H) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // ordered as |v|, NaN above infinity
+    }
+    if (A.h) store_chunk<TY, VEC>(reinterpret_cast<T*>(A.h) + row * H, e, H, v);
+    if (!A.q) return false;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool bad = m >= 0x7F800000u;
+    const float mx = __uint_as_float(m);
+    const bool zero = bad || mx < 7.7037198e-34f;  // 2^-110: 448 / mx and mx / 448 stay normal numbers
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(mx));
+    inv = zero ? 0.f : 448.f * inv;
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    if (zero) c[0] = c[1] = c[2] = c[3] = 0;
+    uint8_t* q = A.q + row * H;
+    if constexpr (VEC) {
+        if (e < H) *reinterpret_cast<uint2*>(q + e) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < H) q[e + i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
+    }
+    if ((threadIdx.x & 7) == 0 && e < H)
+        A.qs[row * ((H + GROUP - 1) / GROUP) + e / GROUP] = zero ? 0.f : mx * (1.f / 448.f);
+    return bad;
+}
 
 template <int TY, bool VEC, int CH>
 __global__ void __launch_bounds__(512) k_rmsnorm_q8(NormArgs A) {
@@ -35,122 +183,65 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(NormArgs A) {
     __shared__ float red[16];
     const int H = A.H, tid = threadIdx.x, nt = blockDim.x;
     const size_t row = blockIdx.x;
-    const T* r = reinterpret_cast<const T*>(A.r) + row * A.r_ld;
-    const T* d = A.d ? reinterpret_cast<const T*>(A.d) + row * A.d_ld : nullptr;
-    T* r_out = A.r_out ? reinterpret_cast<T*>(A.r_out) + row * H : nullptr;
     float v[CH][8];
-    float ss = 0.f;
+    float ss = warp_sum(load_row<TY, VEC, CH>(A, row, tid, nt, v));
+    if (A.r_out) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        const int e = 8 * (tid + j * nt);
-        float dv[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.f, dv[i] = 0.f;
-        if (VEC) {
-            if (e < H) {
-                // plain loads, not the read-only path: r_out may be r or d
-                if constexpr (TY == E0_F32) {
-                    const float4 a = *reinterpret_cast<const float4*>(r + e), b = *reinterpret_cast<const float4*>(r + e + 4);
-                    v[j][0] = a.x, v[j][1] = a.y, v[j][2] = a.z, v[j][3] = a.w;
-                    v[j][4] = b.x, v[j][5] = b.y, v[j][6] = b.z, v[j][7] = b.w;
-                    if (d) {
-                        const float4 f = *reinterpret_cast<const float4*>(d + e), g = *reinterpret_cast<const float4*>(d + e + 4);
-                        dv[0] = f.x, dv[1] = f.y, dv[2] = f.z, dv[3] = f.w;
-                        dv[4] = g.x, dv[5] = g.y, dv[6] = g.z, dv[7] = g.w;
-                    }
-                } else {
-                    const uint4 a = *reinterpret_cast<const uint4*>(r + e);
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    if (d) b = *reinterpret_cast<const uint4*>(d + e);
-                    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = unpack16<TY>(wa[i]), g = unpack16<TY>(wb[i]);
-                        v[j][2 * i] = f.x, v[j][2 * i + 1] = f.y, dv[2 * i] = g.x, dv[2 * i + 1] = g.y;
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e + i < H) {
-                    v[j][i] = Elem<TY>::get(r[e + i]);
-                    if (d) dv[i] = Elem<TY>::get(d[e + i]);
-                }
-        }
-        if (d) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = Elem<TY>::get(Elem<TY>::put(v[j][i] + dv[i]));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-        if (r_out) {
-            if (VEC) {
-                if (e < H) store_vec<TY>(r_out + e, v[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (e + i < H) r_out[e + i] = Elem<TY>::put(v[j][i]);
-            }
-        }
+        for (int j = 0; j < CH; ++j) store_chunk<TY, VEC>(reinterpret_cast<T*>(A.r_out) + row * H, 8 * (tid + j * nt), H, v[j]);
     }
-    ss = warp_sum(ss);
     if ((tid & 31) == 0) red[tid >> 5] = ss;
     __syncthreads();
     ss = 0.f;
     for (int i = 0; i < nt / 32; ++i) ss += red[i];
-    const float rstd = 1.f / sqrtf(ss / (float)H + A.eps);
+    const float rstd = rsqrtf(fmaf(ss, A.inv_h, A.eps));
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) bad |= finish_chunk<TY, VEC>(A, row, 8 * (tid + j * nt), rstd, v[j]);
+    if (bad && (tid & 7) == 0) set_status(A.st, E0_ST_NONFINITE);
+}
 
-    T* h = A.h ? reinterpret_cast<T*>(A.h) + row * H : nullptr;
-    uint8_t* q = A.q ? A.q + row * H : nullptr;
-    const int ng = (H + GROUP - 1) / GROUP;
-    bool bad_any = false;
+constexpr int NORM_WARPS = 8;
+
+template <int TY, int CH>
+__global__ void __launch_bounds__(NORM_WARPS * 32, CH >= 8 ? 2 : 3) k_rmsnorm_q8_rows(NormArgs A) {
+    typedef typename Elem<TY>::T T;
+    const int H = A.H, lane = threadIdx.x & 31;
+    const size_t row = (size_t)blockIdx.x * NORM_WARPS + (threadIdx.x >> 5);
+    if (row >= (size_t)A.T) return;
+    float v[CH][8];
+    const float ss = load_row<TY, true, CH>(A, row, lane, 32, v);
+    if (A.r_out) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        const int e = 8 * (tid + j * nt);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float x = v[j][i] * rstd;
-            if (A.w && e + i < H) x *= __ldg(A.w + e + i);
-            v[j][i] = x;
-            if (e + i < H) m = max(m, __float_as_uint(x) & 0x7FFFFFFFu);  // ordered as |x|, NaN above infinity
-        }
-        if (h) {
-            if (VEC) {
-                if (e < H) store_vec<TY>(h + e, v[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (e + i < H) h[e + i] = Elem<TY>::put(v[j][i]);
-            }
-        }
-        if (!q) continue;
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const bool bad = m >= 0x7F800000u;
-        bad_any |= bad;
-        const float mx = __uint_as_float(m);
-        const bool zero = bad || mx < 7.7037198e-34f;  // 2^-110: 448 / mx and mx / 448 stay normal numbers
-        const float inv = zero ? 0.f : 448.f / mx;
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            c[i] = zero ? 0u : e4m3x2(v[j][2 * i] * inv, v[j][2 * i + 1] * inv);
-        if (VEC) {
-            if (e < H) *reinterpret_cast<uint2*>(q + e) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e + i < H) q[e + i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
-        }
-        if ((tid & 7) == 0 && e < H) A.qs[row * ng + e / GROUP] = zero ? 0.f : mx / 448.f;
+        for (int j = 0; j < CH; ++j) store_chunk<TY, true>(reinterpret_cast<T*>(A.r_out) + row * H, 8 * (lane + j * 32), H, v[j]);
     }
-    if (bad_any && (tid & 7) == 0) set_status(A.st, E0_ST_NONFINITE);
+    const float rstd = rsqrtf(fmaf(warp_sum(ss), A.inv_h, A.eps));
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) bad |= finish_chunk<TY, true>(A, row, 8 * (lane + j * 32), rstd, v[j]);
+    if (bad && (lane & 7) == 0) set_status(A.st, E0_ST_NONFINITE);
+}
+
+template <int TY>
+void launch_rows(const NormArgs& a, cudaStream_t s) {
+    const int grid = (a.T + NORM_WARPS - 1) / NORM_WARPS, nt = NORM_WARPS * 32;
+    if (a.H <= 512)
+        k_rmsnorm_q8_rows<TY, 2><<<grid, nt, 0, s>>>(a);
+    else if (a.H <= 1024)
+        k_rmsnorm_q8_rows<TY, 4><<<grid, nt, 0, s>>>(a);
+    else if (a.H <= 1536)
+        k_rmsnorm_q8_rows<TY, 6><<<grid, nt, 0, s>>>(a);
+    else
+        k_rmsnorm_q8_rows<TY, 8><<<grid, nt, 0, s>>>(a);
 }
 
 template <int TY, bool VEC>
-int launch(const NormArgs& a, int T, cudaStream_t s) {
+int launch(const NormArgs& a, cudaStream_t s) {
+    const int T = a.T;
+    // a warp a row from where the rows give every SM two blocks of warps
+    if (VEC && a.H <= 2048 && T >= 2 * NORM_WARPS * num_sms()) {
+        launch_rows<TY>(a, s);
+        return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+    }
     const int chunks = (a.H + 7) / 8;
     int nt = (chunks + 31) / 32 * 32;
     if (nt > 512) nt = 512;
@@ -167,15 +258,15 @@ int launch(const NormArgs& a, int T, cudaStream_t s) {
 
 int rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, int dtype, float eps, int64_t r_ld,
                int64_t d_ld, void* r_out, void* h, uint8_t* q, float* qs, uint32_t* st, cudaStream_t s) {
-    NormArgs a = {r, d, w, r_out, h, q, qs, st, r_ld, d_ld, H, eps};
+    NormArgs a = {r, d, w, r_out, h, q, qs, st, r_ld, d_ld, T, H, eps, (float)(1.0 / H)};
     const int sz = type_size(dtype);
-    uintptr_t bits = (uintptr_t)r | (uintptr_t)d | (uintptr_t)r_out | (uintptr_t)h | (uintptr_t)(r_ld * sz);
+    uintptr_t bits = (uintptr_t)r | (uintptr_t)d | (uintptr_t)r_out | (uintptr_t)h | (uintptr_t)w | (uintptr_t)(r_ld * sz);
     if (d) bits |= (uintptr_t)(d_ld * sz);
     const bool vec = H % 8 == 0 && !(bits & 15) && !((uintptr_t)q & 7);
     switch (dtype) {
-        case E0_F32: return vec ? launch<E0_F32, true>(a, T, s) : launch<E0_F32, false>(a, T, s);
-        case E0_F16: return vec ? launch<E0_F16, true>(a, T, s) : launch<E0_F16, false>(a, T, s);
-        default: return vec ? launch<E0_BF16, true>(a, T, s) : launch<E0_BF16, false>(a, T, s);
+        case E0_F32: return vec ? launch<E0_F32, true>(a, s) : launch<E0_F32, false>(a, s);
+        case E0_F16: return vec ? launch<E0_F16, true>(a, s) : launch<E0_F16, false>(a, s);
+        default: return vec ? launch<E0_BF16, true>(a, s) : launch<E0_BF16, false>(a, s);
     }
 }
 
