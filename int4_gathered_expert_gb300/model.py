@@ -312,3 +312,122 @@ class StreamedStack:
         self.ev2.record(ps)
         self.t = t + 1
         return out
+
+
+class LinearDev:
+    """A canonical int4 Q-tensor [N, K] laid out for e0_linear_forward."""
+
+    def __init__(self, q_np: Dict[str, np.ndarray], device="cuda", stream=None):
+        self.N, self.K = q_np["codes"].shape[0], q_np["codes"].shape[1] * 2
+        src = {k: _dev(v, device) for k, v in q_np.items()}
+        self.data = torch.empty(L.e0_linear_bytes(self.N, self.K), dtype=torch.uint8, device=device)
+        L.e0_pack_linear(L.QTensor(src["codes"].data_ptr(), src["scale"].data_ptr(), src["bias"].data_ptr()),
+                         self.N, self.K, self.data, stream=stream)
+        torch.cuda.synchronize()  # the source tensors go
+
+
+class KvCacheDev:
+    """A paged 8-bit KV cache of n_layers layers for B sequences: n_blocks blocks
+    a layer, one block table, one stack of free blocks (all blocks free, all
+    sequences empty).  A block id means the same block of every layer."""
+
+    def __init__(self, n_layers: int, B: int, n_blocks: int, max_blocks: int, Hkv: int, D: int, block_tokens: int = 64,
+                 device="cuda"):
+        self.B, self.n_blocks, self.max_blocks, self.block_tokens = B, n_blocks, max_blocks, block_tokens
+        shape = (n_layers, n_blocks, Hkv, block_tokens, D)
+        self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.k_scale = torch.ones(shape[:3], device=device)
+        self.v_scale = torch.ones(shape[:3], device=device)
+        self.descs = [L.KvCache(self.k[l].data_ptr(), self.v[l].data_ptr(), self.k_scale[l].data_ptr(),
+                                self.v_scale[l].data_ptr(), n_blocks, Hkv, block_tokens, D) for l in range(n_layers)]
+        self.table = torch.full((B, max_blocks), -1, dtype=torch.int32, device=device)
+        self.ctx = torch.zeros(B, dtype=torch.int32, device=device)
+        self.free = torch.arange(n_blocks - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = torch.full((1,), n_blocks, dtype=torch.int32, device=device)
+        self.state = L.KvState(self.table.data_ptr(), self.ctx.data_ptr(), self.free.data_ptr(),
+                               self.free_count.data_ptr(), B, max_blocks, block_tokens, n_blocks)
+
+    def plan(self, new_len, T_cap, cu_q, slots, positions=None, seq_ids=None, status=None, stream=None):
+        """Room for new_len more tokens of each sequence; lengths and stack move in place."""
+        L.e0_kv_plan(self.state, new_len, T_cap, self.ctx, self.free_count, cu_q, slots, positions, seq_ids, status,
+                     stream=stream)
+
+    def release(self, mask, status=None, stream=None):
+        """Empty the sequences whose mask byte is set; their blocks are free again."""
+        L.e0_kv_release(self.state, mask, self.ctx, self.free_count, status, stream=stream)
+
+
+class BatchDecoder:
+    """Decode steps of a batch of sequences through whole layers, attention and
+    MoE, on a StackDev's weights.  For each layer:
+
+        r += MoE of the layer before; h = norm(r) * w in 8 bits
+        q, k, v = W_qkv h (fp16); k, v into the cache
+        r += W_out attention(q)
+        MoE(rmsnorm(r)), with the layer's own routing (batches do not predict)
+
+    attn: one ``synth.attention`` dict a layer.  A step takes up to T tokens, new_len[b]
+    of each sequence in order, as rows of x (T <= 64, the MoE block's limit).  All
+    of a step's work is on one stream and allocates nothing, so a step can be
+    captured into a CUDA graph."""
+
+    def __init__(self, sd: StackDev, attn: List[dict], shape, cache: KvCacheDev, T: int, device="cuda"):
+        if len(attn) != sd.L:
+            raise ValueError("one attention half a layer")
+        if not 1 <= T <= L.E0_MAX_T_DECODE:
+            raise ValueError("T is 1..%d" % L.E0_MAX_T_DECODE)
+        self.sd, self.a, self.cache, self.T = sd, shape, cache, T
+        self.qkv = [LinearDev(w["qkv"], device) for w in attn]
+        self.out = [LinearDev(w["out"], device) for w in attn]
+        self.norm = [_dev(w["norm"], device) for w in attn]
+        H, a = sd.H, shape
+        self.row = (a.Hq + 2 * a.Hkv) * a.D
+
+        def buf(*s, dtype=torch.float32):
+            return torch.zeros(s, dtype=dtype, device=device)
+
+        self.r, self.h, self.y = buf(T, H), buf(T, H), buf(T, H)
+        self.q8, self.q8_scale = buf(T, H, dtype=torch.uint8), buf(T, -(-H // 64))
+        self.x_qkv = buf(T, self.row, dtype=torch.float16)
+        self.o = buf(T, a.Hq * a.D, dtype=torch.float16)
+        self.cu_q = buf(cache.B + 1, dtype=torch.int32)
+        self.slots = buf(T, dtype=torch.int64)
+        self.inds, self.w = buf(T, sd.K, dtype=torch.int32), buf(T, sd.K)
+        self.ws_bytes = L.e0_workspace_size(0, T, sd.H, sd.I, sd.E, sd.K)
+        self.ws = buf(self.ws_bytes, dtype=torch.uint8)
+        self.aws_bytes = L.e0_attn_workspace_size(cache.B, a.Hq, a.Hkv, a.D, T)
+        self.aws = buf(self.aws_bytes, dtype=torch.uint8)
+        self.status = buf(1, dtype=torch.int32)
+        self.r_out = buf(T, H)
+
+    def step(self, x: torch.Tensor, new_len: torch.Tensor, window: int = 0, stream=None) -> torch.Tensor:
+        """x fp32 [T, H], new_len int32 [B] on the device; the rows after the
+        last new token hold nothing of use.  Where a step finds no room
+        (E0_ST_POOL_FULL in ``status``), no token is cached."""
+        sd, a, c, T, H = self.sd, self.a, self.cache, self.T, self.sd.H
+        kw = dict(stream=stream)
+        c.plan(new_len, T, self.cu_q, self.slots, status=self.status, **kw)
+        src, delta = x, None
+        for l in range(sd.L):
+            L.e0_rmsnorm_q8(src, delta, self.norm[l], T, H, L.E0_F32, 1e-6, H, H, self.r, None, self.q8, self.q8_scale,
+                            self.status, **kw)
+            p = self.qkv[l]
+            L.e0_linear_forward(p.data, p.N, p.K, self.q8, L.E0_E4M3, H, self.q8_scale, T, None, 0, self.x_qkv, L.E0_F16,
+                                self.row, **kw)
+            k = self.x_qkv.data_ptr() + 2 * a.Hq * a.D
+            v = k + 2 * a.Hkv * a.D
+            L.e0_kv_append(c.descs[l], k, v, L.E0_F16, self.row, self.row, self.slots, T, self.status, **kw)
+            L.e0_attn_decode(c.descs[l], c.table, c.max_blocks, c.ctx, self.cu_q, c.B, T, self.x_qkv, L.E0_F16, self.row,
+                             a.Hq, a.D ** -0.5, window, self.o, a.Hq * a.D, None, self.aws, self.aws_bytes, self.status,
+                             **kw)
+            p = self.out[l]
+            L.e0_linear_forward(p.data, p.N, p.K, self.o, L.E0_F16, a.Hq * a.D, None, T, self.r, H, self.r, L.E0_F32, H,
+                                **kw)
+            L.e0_rmsnorm(self.r, T, H, 1e-6, self.h, **kw)
+            sh = sd.shared[l].desc if sd.shared[l] is not None else None
+            L.e0_moe_block_forward(self.h, T, sd.pools[l].desc, sd.routers[l], sd.rp, None, None, sh, self.y, self.inds,
+                                   self.w, self.ws, self.ws_bytes, self.status, **kw)
+            src, delta = self.r, self.y
+        L.e0_rmsnorm_q8(self.r, self.y, None, T, H, L.E0_F32, 1e-6, H, H, self.r_out, None, None, None, self.status, **kw)
+        return self.r_out

@@ -72,6 +72,15 @@ class StackShape:
         return tuple(o + 1 for o in self.owners)
 
 
+@dataclass(frozen=True)
+class AttnShape:
+    """The attention half of a layer: Hq query heads over Hkv KV heads of D."""
+    Hq: int
+    Hkv: int
+    D: int
+    block_tokens: int = 64
+
+
 TINY = LayerShape(H=256, I=128, E=16, K=4)
 L35B = LayerShape(H=2048, I=512, E=256, K=4)
 L8B = LayerShape(H=1536, I=384, E=128, K=8, route="sigmoid_group",
@@ -182,6 +191,15 @@ def shared_expert(seed: int, layer: int, shape: LayerShape, rank: int = 16,
     for p, (out, inn) in (("gate", (I, H)), ("up", (I, H)), ("down", (H, I))):
         lora[p] = {"A": fp16_normal(g, (rank, inn), 0.01), "B": fp16_normal(g, (out, rank), 0.0125)}
     return {"q": expert_view(q, 0), "lora": lora, "rank": rank, "alpha": alpha}
+
+
+def attention(seed: int, layer: int, H: int, a: AttnShape) -> dict:
+    """The attention half of one layer: the projection to queries, keys and
+    values [(Hq + 2 Hkv) D, H] and the one back [H, Hq D] as Q-tensors, and the
+    norm's weight fp32 [H] ~ 1 + N(0, 0.1)."""
+    g = _rng(seed, 11, layer)
+    return {"qkv": qtensor(g, (a.Hq + 2 * a.Hkv) * a.D, H), "out": qtensor(g, H, a.Hq * a.D),
+            "norm": (1 + 0.1 * g.standard_normal(H)).astype(np.float32)}
 
 
 def normal_rows(seed: int, T: int, H: int, tag: int = 5) -> np.ndarray:

@@ -1,0 +1,179 @@
+"""The attention half and the MoE half of layers together (BatchDecoder): every
+stage against a 64-bit reference fed with what the stage before left, sequences
+that come, grow, end and come again, a captured step, a pool that runs out."""
+import os
+
+import numpy as np
+import pytest
+
+from int4_gathered_expert_gb300 import synth
+from oracle import e0_oracle as O
+from tests import layer_ref as R
+from tests.parity import REL_L2, rel_l2
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+EPS = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from int4_gathered_expert_gb300 import build, lib
+    if not os.path.exists(lib.LIB_PATH):
+        build.build()
+    lib.load()
+    return lib
+
+
+def decoder(n_layers, B, T, n_blocks, max_blocks, a, seed=21, shared=True):
+    from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev, StackDev
+    shape = synth.StackShape(layer=synth.TINY, n_layers=n_layers, owners=(), shared_expert=shared, seed=seed)
+    m = synth.stack_model(shape, n_tokens=1, threads=2)
+    attn = [synth.attention(seed, l, synth.TINY.H, a) for l in range(n_layers)]
+    cache = KvCacheDev(n_layers, B, n_blocks, max_blocks, a.Hkv, a.D, a.block_tokens)
+    return m, attn, BatchDecoder(StackDev(m), attn, a, cache, T)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def codes_of(t):
+    return R.decode(t.cpu().numpy())
+
+
+def test_one_layer_stage_by_stage(L):
+    a = synth.AttnShape(Hq=6, Hkv=2, D=64, block_tokens=16)
+    B, T, H = 3, 12, synth.TINY.H
+    m, attn, bd = decoder(1, B, T, 24, 12, a)
+    c = bd.cache
+    ref = R.Cache(24, a.Hkv, 16, a.D)
+    ref.k, ref.v = c.k[0].cpu().numpy(), c.v[0].cpu().numpy()
+    rng = np.random.default_rng(3)
+    ctx = np.zeros(B, int)
+    for new in ([7, 3, 0], [1, 1, 1], [0, 1, 9], [1, 1, 1], [5, 0, 1]):
+        x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).cuda()
+        out = bd.step(x, torch.tensor(new, dtype=torch.int32, device="cuda"))
+        assert L.e0_read_status(bd.status) == 0
+        n = sum(new)
+        ctx += new
+        assert c.ctx.tolist() == list(ctx)
+        # the norm's codes and scales give h back to half a step
+        xv = f64(x)
+        h = xv / np.sqrt((xv ** 2).mean(1, keepdims=True) + 1e-6) * attn[0]["norm"].astype(np.float64)
+        hq = (codes_of(bd.q8).reshape(T, -1, 64) * f64(bd.q8_scale)[:, :, None]).reshape(T, H)
+        step = np.maximum(np.abs(h) * 2.0 ** -4, np.repeat(f64(bd.q8_scale), 64, 1) * 2.0 ** -10)
+        assert (np.abs(hq - h) <= step * (1 + 1e-4) + 1e-5 * np.abs(h)).all()
+        # queries, keys, values: fp32 sums of exact products, one rounding to fp16
+        W = O.dequant(attn[0]["qkv"])
+        want = hq @ W.T
+        mag = np.abs(hq) @ (15 * np.repeat(attn[0]["qkv"]["scale"].astype(np.float64), 64, 1)
+                            + np.abs(np.repeat(attn[0]["qkv"]["bias"].astype(np.float64), 64, 1))).T
+        qkv = f64(bd.x_qkv)
+        assert (np.abs(qkv - want) <= 90 * EPS * mag + 2.0 ** -11 * np.abs(want) * 1.001 + 2.0 ** -25).all()
+        # the cache holds them
+        slots = bd.slots.cpu().numpy()
+        assert (slots[n:] == -1).all()
+        k = qkv[:, a.Hq * a.D:(a.Hq + a.Hkv) * a.D].reshape(T, a.Hkv, a.D)
+        v = qkv[:, (a.Hq + a.Hkv) * a.D:].reshape(T, a.Hkv, a.D)
+        ref.append(k, v, slots)
+        used = np.unique(slots[:n] // 16)
+        assert np.array_equal(codes_of(c.k[0]), R.decode(ref.k)) and np.array_equal(codes_of(c.v[0]), R.decode(ref.v))
+        assert np.array_equal(c.k_scale[0].cpu().numpy()[used], ref.ks[used])
+        # attention over it
+        table, cu = c.table.cpu().numpy(), bd.cu_q.cpu().numpy()
+        o = f64(bd.o).reshape(T, a.Hq, a.D)
+        for b in range(B):
+            if new[b]:
+                kk, vv = ref.row(table[b], ctx[b])
+                q = qkv[cu[b]:cu[b + 1], :a.Hq * a.D].reshape(-1, a.Hq, a.D)
+                wo, _, tol, _ = R.attention(q, kk, vv, float(np.float32(a.D ** -0.5)), ctx[b], 0)
+                assert (np.abs(o[cu[b]:cu[b + 1]] - wo) <= tol + 2.0 ** -11 * np.abs(wo) * 1.001 + 2.0 ** -25).all()
+        # back onto the stream, and the MoE half
+        r = xv + f64(bd.o) @ O.dequant(attn[0]["out"]).T
+        assert rel_l2(f64(bd.r)[:n], r[:n]) <= 1e-5
+        hh = O.rmsnorm(f64(bd.r)[:n])
+        y = O.moe_block(hh, O.BankExperts(m.banks[0]), bd.inds.cpu().numpy()[:n], f64(bd.w)[:n], m.shared[0])
+        assert rel_l2(f64(bd.y)[:n], y) <= REL_L2
+        assert torch.equal(out, bd.r + bd.y)
+
+
+def test_layers_follow_one_another(L):
+    """Two layers equal the second layer alone fed with the first one's output."""
+    a = synth.AttnShape(Hq=4, Hkv=1, D=64, block_tokens=16)
+    B, T = 4, 4
+    m, attn, two = decoder(2, B, T, 16, 4, a)
+    from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev
+    halves = []
+    for l in range(2):
+        sd = two.sd
+        import copy
+        one = copy.copy(sd)
+        one.L, one.pools, one.routers, one.shared = 1, [sd.pools[l]], [sd.routers[l]], [sd.shared[l]]
+        halves.append(BatchDecoder(one, [attn[l]], a, KvCacheDev(1, B, 16, 4, 1, 64, 16), T))
+    rng = np.random.default_rng(5)
+    new = torch.ones(B, dtype=torch.int32, device="cuda")
+    for _ in range(20):
+        x = torch.from_numpy(rng.standard_normal((T, 256)).astype(np.float32)).cuda()
+        got = two.step(x, new).clone()
+        mid = halves[0].step(x, new)
+        assert torch.equal(got, halves[1].step(mid, new))
+    assert L.e0_read_status(two.status) == 0
+    assert torch.equal(two.cache.k[1], halves[1].cache.k[0])
+
+
+def test_a_captured_step_replays(L):
+    a = synth.AttnShape(Hq=8, Hkv=2, D=128, block_tokens=16)
+    B, T = 5, 8
+    _, _, eager = decoder(2, B, T, 40, 8, a)
+    _, _, graph = decoder(2, B, T, 40, 8, a)
+    x = torch.zeros((T, 256), device="cuda")
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    graph.step(x, new)  # nothing joins: the first call of everything
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        graph.step(x, new)
+    rng = np.random.default_rng(6)
+    for i in range(25):
+        x.copy_(torch.from_numpy(rng.standard_normal((T, 256)).astype(np.float32)))
+        lens = rng.multinomial(T, np.ones(B) / B) if i % 3 == 0 else np.ones(B, int)
+        new.copy_(torch.from_numpy(lens.astype(np.int32)))
+        if i == 15:  # two sequences end; others come in their place
+            for d in (eager, graph):
+                d.cache.release(torch.tensor([1, 0, 0, 1, 0], dtype=torch.uint8, device="cuda"), d.status)
+        g.replay()
+        n = int(lens.sum())
+        assert torch.equal(graph.r_out[:n], eager.step(x, new)[:n])
+    assert L.e0_read_status(graph.status) == 0
+    assert torch.equal(graph.cache.table, eager.cache.table) and torch.equal(graph.cache.ctx, eager.cache.ctx)
+
+
+def test_a_full_pool_caches_nothing(L):
+    a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
+    m, attn, bd = decoder(1, 2, 40, 4, 8, a)
+    x = torch.randn((40, 256), generator=torch.Generator().manual_seed(1)).cuda()
+    bd.step(x, torch.tensor([20, 18], dtype=torch.int32, device="cuda"))
+    assert L.e0_read_status(bd.status) == 0 and bd.cache.free_count.item() == 0
+    before = [t.clone() for t in (bd.cache.k, bd.cache.v, bd.cache.table, bd.cache.ctx, bd.cache.k_scale)]
+    bd.step(x, torch.tensor([1, 20], dtype=torch.int32, device="cuda"))
+    assert L.e0_read_status(bd.status) == L.E0_ST_POOL_FULL
+    for t, w in zip((bd.cache.k, bd.cache.v, bd.cache.table, bd.cache.ctx, bd.cache.k_scale), before):
+        assert torch.equal(t, w)
+    bd.status.zero_()
+    bd.cache.release(torch.tensor([1, 0], dtype=torch.uint8, device="cuda"), bd.status)
+    bd.step(x, torch.tensor([1, 14], dtype=torch.int32, device="cuda"))
+    assert L.e0_read_status(bd.status) == 0 and bd.cache.ctx.tolist() == [1, 32]
+
+
+def test_decoder_refuses(L):
+    from int4_gathered_expert_gb300.model import BatchDecoder
+    a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
+    _, attn, bd = decoder(1, 2, 4, 4, 8, a)
+    with pytest.raises(ValueError):
+        BatchDecoder(bd.sd, attn + attn, a, bd.cache, 4)
+    with pytest.raises(ValueError):
+        BatchDecoder(bd.sd, attn, a, bd.cache, 65)
