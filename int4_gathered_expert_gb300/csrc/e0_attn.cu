@@ -326,7 +326,10 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         }
     };
     int in_stage = 0, in_at = 0;  // where the next copy goes; its place among the lanes' ids
-    const auto issue = [&](int c) {
+    const auto put_scales = [&](int at, int stage) {
+        if (lane / SUBS == at) S.scales[warp][stage][lane % SUBS] = my_sc;
+    };
+    const auto issue = [&](int c, bool scales) {
         if (c < j.c1) {
             if (in_at == AHEAD) {
                 look_up(c);
@@ -336,7 +339,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             for (int h = 0; h < SUBS; ++h) {
                 const int from = in_at * SUBS + h;
                 const int id = __shfl_sync(0xffffffffu, my_id, from);
-                if (lane == from) S.scales[warp][in_stage][h] = my_sc;
                 if (id >= 0) {
                     const int pos = (j.s.first + c) * UNIT + STEP * warp + 16 * h;
                     const size_t at = ((((size_t)id * A.Hkv + j.head) << A.shift) + (pos & (bs - 1))) * D + 16 * lane;
@@ -349,17 +351,21 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     }
                 }
             }
+            if (scales) put_scales(in_at, in_stage);
             ++in_at;
             if (++in_stage == STAGES) in_stage = 0;
         }
         copy_commit();
     };
     // the first steps of a part go to the stages but the first, which holds the
-    // former part's output until it has been written
+    // former part's output until it has been written; the codes' copies need the
+    // block ids only and go ahead of the scales
     const auto begin = [&]() {
         in_stage = 1, in_at = 0;
 #pragma unroll 1
-        for (int i = 0; i < STAGES - 1; ++i) issue(j.c0 + i);
+        for (int i = 0; i < STAGES - 1; ++i) issue(j.c0 + i, false);
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) put_scales(i, i + 1);
     };
     // this lane's query row: 16 elements of each 64, as they are in memory; a row
     // beyond the tile's reads the tile's first and counts as zeros
@@ -389,12 +395,13 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     bool more = next();
     if (more) {
         look_up(j.c0);
-        if (warp == 0) load_q();
+        load_q();
         begin();
     }
     while (more) {
-        // ---- the job's queries as operand fragments: warps share them through shared memory
-        if (warp == 0) {
+        // ---- the job's queries as operand fragments: every warp reads them all for the
+        // rows' maxima and leaves its share of the fragments in shared memory
+        {
             uint32_t m = 0;
 #pragma unroll
             for (int c = 0; c < KC; ++c)
@@ -411,13 +418,14 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             for (int c = 0; c < KC; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if ((4 * c + i) / KC != warp) continue;
                     uint32_t a[4];
                     split_half(q_of(c, 4 * i) * down, q_of(c, 4 * i + 1) * down, a[0], a[1]);
                     split_half(q_of(c, 4 * i + 2) * down, q_of(c, 4 * i + 3) * down, a[2], a[3]);
                     *reinterpret_cast<uint4*>(S.q[4 * c + i][lane]) = make_uint4(a[0], a[1], a[2], a[3]);
                 }
             // what the product lacks: the power of two, the scale, log2 e
-            if (t4 == 0)
+            if (warp == 0 && t4 == 0)
                 S.f[gid] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
                                             : __uint_as_float((uint32_t)e << 23) * A.scale * LOG2E;
         }
@@ -452,7 +460,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             for (int h = 0; h < SUBS; ++h) sc[h] = S.scales[warp][stage][h];
             const uint8_t* kp = S.ring[warp][stage];
             if (++stage == STAGES) stage = 0;
-            issue(c + STAGES - 1);
+            issue(c + STAGES - 1, true);
             if (sc[0].x < 0.f && sc[SUBS - 1].x < 0.f) continue;
             const int pos = (cur.s.first + c) * UNIT + STEP * warp;
             // whether some row does not see all of the step: masks, and codes that may be anything
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         more = next();
         if (more) {
             look_up(j.c0);
-            if (warp == 0) load_q();
+            load_q();
         }
         sum = quad_sum(sum);
         if (t4 == 0) S.m[warp][gid] = mx, S.l[warp][gid] = sum;
@@ -747,7 +755,8 @@ int launch(AttnArgs a, cudaStream_t s) {
     a.job_cost = Tile<D>::JOB_COST;
     const size_t sched = (size_t)a.B * sizeof(uint32_t);
     const size_t sm = sizeof(AttnSmem<D>) + sched;
-    if (cudaFuncSetAttribute(k_attn<D, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
+    static std::atomic<uint64_t> asked{0};
+    if (!allow_smem((const void*)k_attn<D, TY>, sizeof(AttnSmem<D>) + E0_MAX_SEQS * sizeof(uint32_t), asked))
         return E0_ERR_CUDA;
     k_attn<D, TY><<<a.blocks, AT_WARPS * 32, sm, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;

@@ -60,6 +60,18 @@ E0_DEV void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum.
+E0_DEV void mma16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool bf) {
+    if (bf)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // One word of a lane's codes -> its A fragment of one step.
 template <bool BF>
 E0_DEV void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
@@ -302,23 +314,31 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
             const uint8_t* rec = ring + stage * VecRing<RM>::BYTES;
             if (++stage == STAGES) stage = 0;
             issue();
-            float sx[4] = {0.f, 0.f, 0.f, 0.f};
+            float sx[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int p = 0; p < P; ++p) mma16(sx, ones, b[p][2 * i], b[p][2 * i + 1], BF);
+                for (int p = 0; p < P; ++p)
+                    if (i + p == 0)
+                        mma16_first(sx, ones, b[0][0], b[0][1], BF);
+                    else
+                        mma16(sx, ones, b[p][2 * i], b[p][2 * i + 1], BF);
 #pragma unroll
             for (int r = 0; r < RM; ++r) {
                 const uint4 c = *reinterpret_cast<const uint4*>(rec + r * REC + lane * 16);
                 const uint2 sb = *reinterpret_cast<const uint2*>(rec + r * REC + 512 + gid * 8);
                 const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                float d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t a[4];
                     unpack_codes<BF>(cw[i], a);
 #pragma unroll
-                    for (int p = 0; p < P; ++p) mma16(d, a, b[p][2 * i], b[p][2 * i + 1], BF);
+                    for (int p = 0; p < P; ++p)
+                        if (i + p == 0)
+                            mma16_first(d, a, b[0][0], b[0][1], BF);
+                        else
+                            mma16(d, a, b[p][2 * i], b[p][2 * i + 1], BF);
                 }
                 const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
                 add_group<XT == E0_E4M3>(tot[r], d, lo.x, lo.y, hi.x, hi.y, sx, xs);
@@ -516,15 +536,17 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
                 const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
                 const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
                 float d[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
                 if constexpr (P == 1) {  // NT chains of products at once
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t a[4];
                         unpack_codes<BF>(cw[i], a);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16(d[n], a, b[n][0][2 * i], b[n][0][2 * i + 1], BF);
+                        for (int n = 0; n < NT; ++n)
+                            if (i == 0)
+                                mma16_first(d[n], a, b[n][0][0], b[n][0][1], BF);
+                            else
+                                mma16(d[n], a, b[n][0][2 * i], b[n][0][2 * i + 1], BF);
                     }
                 } else {
                     uint32_t a[4][4];
@@ -536,7 +558,11 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int p = 0; p < P; ++p) mma16(d[n], a[i], b[0][p][2 * i], b[0][p][2 * i + 1], BF);
+                            for (int p = 0; p < P; ++p)
+                                if (i + p == 0)
+                                    mma16_first(d[n], a[0], b[0][0][0], b[0][0][1], BF);
+                                else
+                                    mma16(d[n], a[i], b[0][p][2 * i], b[0][p][2 * i + 1], BF);
                     }
                 }
 #pragma unroll
@@ -588,10 +614,11 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     }
 }
 
-template <typename K>
-int launch(K kernel, const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return E0_ERR_CUDA;
+// most: the most dynamic shared memory that any launch of the kernel wants.
+template <void (*kernel)(LinArgs)>
+int launch(const LinArgs& a, dim3 grid, size_t smem, size_t most, cudaStream_t s) {
+    static std::atomic<uint64_t> asked{0};
+    if (!allow_smem((const void*)kernel, most, asked)) return E0_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(LIN_WARPS * 32);
@@ -612,7 +639,7 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
         const int tiles = (nb + LIN_WARPS * BATCH_RM - 1) / (LIN_WARPS * BATCH_RM), zs = (a.T + TOK - 1) / TOK;
         int S = 1;
         while (S < 8 && (long long)tiles * zs * S < 2LL * sms && G / (2 * S) >= 4) S *= 2;
-        return launch(k_linear_batch<XT>, a, dim3(tiles, S, zs), sizeof(BatchSmem<XT>), s);
+        return launch<k_linear_batch<XT>>(a, dim3(tiles, S, zs), sizeof(BatchSmem<XT>), sizeof(BatchSmem<XT>), s);
     }
     // The more row blocks a warp has, the less the operands of x cost; but there
     // have to be blocks for the whole machine, with K split over up to 8 of
@@ -629,9 +656,9 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
         const int tiles = (nb + rm - 1) / rm, S = split(rm);
         return dim3(S == 1 && tiles > 2 * sms ? 2 * sms : tiles, S);
     };
-    if (fills(8)) return launch(k_linear_vec<XT, 8>, a, grid(8), VecRing<8>::smem(a.T, split(8)), s);
-    if (fills(4)) return launch(k_linear_vec<XT, 4>, a, grid(4), VecRing<4>::smem(a.T, split(4)), s);
-    return launch(k_linear_vec<XT, 1>, a, grid(1), VecRing<1>::smem(a.T, split(1)), s);
+    if (fills(8)) return launch<k_linear_vec<XT, 8>>(a, grid(8), VecRing<8>::smem(a.T, split(8)), VecRing<8>::smem(8, 2), s);
+    if (fills(4)) return launch<k_linear_vec<XT, 4>>(a, grid(4), VecRing<4>::smem(a.T, split(4)), VecRing<4>::smem(8, 2), s);
+    return launch<k_linear_vec<XT, 1>>(a, grid(1), VecRing<1>::smem(a.T, split(1)), VecRing<1>::smem(8, 2), s);
 }
 
 // A thread writes one lane's 16 bytes of codes of one record; lanes 0..7 also

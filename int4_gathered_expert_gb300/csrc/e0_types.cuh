@@ -4,11 +4,25 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "e0_common.cuh"
 
 namespace e0 {
 
-__host__ inline int type_size(int t) { return t == E0_F32 ? 4 : t == E0_E4M3 ? 1 : 2; }
+// Let kernel f have `bytes` of dynamic shared memory on the current device: asked
+// for once a device (`bytes` is the most that any launch of f wants).
+inline bool allow_smem(const void* f, size_t bytes, std::atomic<uint64_t>& asked) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (asked.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    if (dev < 64) asked.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+inline int type_size(int t) { return t == E0_F32 ? 4 : t == E0_E4M3 ? 1 : 2; }
 
 template <int TY>
 struct Elem;
