@@ -8,8 +8,8 @@ namespace e0 {
 namespace {
 
 // out = softmax(scale q K^T) V in one pass over the context with the running
-// maximum and sum.  A job is one (sequence, KV head, 8 query rows): the rows are
-// the query heads of the group and the sequence's new tokens, token major.  A
+// maximum and sum.  A job is one (sequence, KV head, tile of query rows): the rows
+// are the query heads of the group and the sequence's new tokens, token major.  A
 // job's context is cut into units, and the units of all jobs, one after another,
 // are dealt out evenly to the thread blocks: every block reads the same number
 // of bytes whatever the lengths are.  A job that ends up on several blocks
@@ -18,10 +18,14 @@ namespace {
 //
 // A unit is one step of each of a block's warps.  Products run on the tensor
 // cores (16 x 8 x 16, fp16 operands, fp32 accumulation); e4m3 codes widen to fp16
-// exactly.  The 16 operand rows hold the 8 query rows twice: rows 0..7 the fp16
-// part, rows 8..15 the rest of the value, so neither q nor the probabilities
-// lose bits that matter (22 significant bits), at no cost: a decode step has few
-// rows and the kernel is bound by reading the cache.
+// exactly.  The 16 operand rows hold 8 query rows twice: rows 0..7 the fp16 part,
+// rows 8..15 the rest of the value, so neither q nor the probabilities lose bits
+// that matter (22 significant bits), at no cost: a decode step has few rows and
+// the kernel is bound by reading the cache.  Where there are more than 8 rows and the
+// outputs are bf16, the tile is WIDE: 16 query rows, q exact (8 bits of each row's
+// power of two), probabilities rounded to fp16, an eighth of what the output's
+// rounding is; a sequence is then read half as often.  (fp16 outputs would be 1.4
+// times as far off with it, so they keep the rests.)
 // A warp's codes come through its own ring in shared memory, copied some steps
 // ahead, so warps never wait for one another inside a job.  Operand layouts are
 // chosen so that every lane reads 16 bytes at a time: the order of D inside the
@@ -36,8 +40,8 @@ namespace {
 // of the largest count.  The softmax's sum is that of the weights over their
 // scales.
 
-constexpr int ROWS = 8;
 constexpr int AT_WARPS = 4;
+constexpr int MOST_ROWS = 16;
 
 // SUBS: 16-position pieces (the smallest block) of a warp's step.  A step costs a
 // chain of dependent instructions (products, maximum, exponentials, products)
@@ -73,19 +77,19 @@ struct AttnArgs {
     const void* q;
     void* out;
     float* lse;
-    float* part_o;    // [2 * blocks][ROWS][D]
-    float2* part_ml;  // [2 * blocks][ROWS]
+    float* part_o;    // [2 * blocks][rows][D]
+    float2* part_ml;  // [2 * blocks][rows]
     Cut* cuts;        // [blocks][2]
     uint32_t* st;
     int64_t q_ld, out_ld;
-    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks, unit, job_cost;
+    int B, max_blocks, n_blocks, shift, Hq, Hkv, max_q, window, blocks, unit, job_cost, rows;
     float scale;
 };
 
 // One sequence as the schedule sees it.
 struct Seq {
     int row0, n, ctx, first;  // first query row, queries, cached tokens, first unit that anyone sees
-    int units, tiles;         // units of context, tiles of 8 rows per KV head
+    int units, tiles;         // units of context, tiles of query rows per KV head
     int low;                  // the first position that the first query sees
 };
 
@@ -103,7 +107,7 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     s.units = (int)(((long long)s.ctx + A.unit - 1) / A.unit) - s.first;
     if (s.units < 1) s.units = 1;  // a job without context still writes its rows
     const int G = A.Hq / A.Hkv;
-    s.tiles = (int)(((long long)s.n * G + ROWS - 1) / ROWS);
+    s.tiles = (int)(((long long)s.n * G + A.rows - 1) / A.rows);
     return s;
 }
 
@@ -233,16 +237,16 @@ struct AttnSmem {
     uint8_t ring[AT_WARPS][Tile<D>::STAGES][Tile<D>::BYTES];  // a warp's output at the end of a job
     uint32_t q[D / 16][32][4];
     float4 scales[AT_WARPS][Tile<D>::STAGES][2];  // of a piece: keys' scale (< 0: not seen), values' log2 and inverse
-    float m[AT_WARPS][ROWS], l[AT_WARPS][ROWS];
-    float f[ROWS];
+    float m[AT_WARPS][MOST_ROWS], l[AT_WARPS][MOST_ROWS];
+    float f[MOST_ROWS];
     uint32_t red[AT_WARPS];
 };
 
-// Element d of row r of a warp's output, in its ring's first stage; columns are
+// Element d of row r (of 8) of a warp's output, in its ring's first stage; columns are
 // permuted inside 32 so that what the lanes write at once has 32 banks.
 template <int D>
 E0_DEV float& warp_out(AttnSmem<D>& S, int w, int r, int d) {
-    static_assert(Tile<D>::BYTES >= ROWS * D * sizeof(float), "a stage holds a warp's output");
+    static_assert(Tile<D>::BYTES >= 8 * D * sizeof(float), "a stage holds a warp's output");
     const int key = D == 64 ? 4 * r + (d >> 4) : 4 * r + (d >> 5);
     return reinterpret_cast<float*>(S.ring[w])[r * D + (d ^ (key & 31))];
 }
@@ -276,7 +280,7 @@ E0_DEV void store_out(const AttnArgs& A, size_t row, int i, float v) {
     reinterpret_cast<T*>(A.out)[row * A.out_ld + i] = Elem<TY>::put(v);
 }
 
-template <int D, int TY>
+template <int D, int TY, bool WIDE>
 __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     typedef typename Elem<TY>::T T;
     extern __shared__ __align__(128) char attn_sm[];
@@ -289,6 +293,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     uint32_t u = blockIdx.x * per;
     const uint32_t u1 = min(u + per, total);
     const int G = A.Hq / A.Hkv, bs = 1 << A.shift;
+    constexpr int RW = WIDE ? 2 : 1, ROWS = 8 * RW;  // rows of a lane (gid, gid + 8); of a tile
     constexpr int KC = D / 64;          // 16-byte chunks of a key row a lane reads
     constexpr int NT = D / 8;           // output tiles
     constexpr int VC = D >= 128 ? D / 128 : 1;  // 16-byte chunks of a value row
@@ -371,8 +376,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     // beyond the tile's reads the tile's first and counts as zeros
     constexpr int RAW = TY == E0_F32 ? 4 : 2;
     uint4 raw[KC][RAW];
-    const auto load_q = [&]() {
-        const int row = j.tile * ROWS + (j.tile * ROWS + gid < j.s.n * G ? gid : 0);
+    const auto load_q = [&](int at) {  // row at of the tile
+        const int row = j.tile * ROWS + (j.tile * ROWS + at < j.s.n * G ? at : 0);
         const T* p = reinterpret_cast<const T*>(A.q) + (size_t)(j.s.row0 + row / G) * A.q_ld +
                      (size_t)(j.head * G + row % G) * D + 16 * t4;
 #pragma unroll
@@ -395,19 +400,21 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
     bool more = next();
     if (more) {
         look_up(j.c0);
-        load_q();
+        load_q(gid);
         begin();
     }
     while (more) {
         // ---- the job's queries as operand fragments: every warp reads them all for the
         // rows' maxima and leaves its share of the fragments in shared memory
-        {
+#pragma unroll
+        for (int w = 0; w < RW; ++w) {
+            if (w == 1) load_q(gid + 8);
             uint32_t m = 0;
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(q_of(c, i)) & 0x7FFFFFFFu);
-            if (j.tile * ROWS + gid >= j.s.n * G) m = 0;
+            if (j.tile * ROWS + gid + 8 * w >= j.s.n * G) m = 0;
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             // rows go in times a power of two that brings the largest near 1
@@ -422,22 +429,33 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     uint32_t a[4];
                     split_half(q_of(c, 4 * i) * down, q_of(c, 4 * i + 1) * down, a[0], a[1]);
                     split_half(q_of(c, 4 * i + 2) * down, q_of(c, 4 * i + 3) * down, a[2], a[3]);
-                    *reinterpret_cast<uint4*>(S.q[4 * c + i][lane]) = make_uint4(a[0], a[1], a[2], a[3]);
+                    uint32_t* to = S.q[4 * c + i][lane];
+                    if constexpr (WIDE)
+                        to[w] = a[0], to[2 + w] = a[2];
+                    else
+                        *reinterpret_cast<uint4*>(to) = make_uint4(a[0], a[1], a[2], a[3]);
                 }
             // what the product lacks: the power of two, the scale, log2 e
             if (warp == 0 && t4 == 0)
-                S.f[gid] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                                            : __uint_as_float((uint32_t)e << 23) * A.scale * LOG2E;
+                S.f[gid + 8 * w] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                                    : __uint_as_float((uint32_t)e << 23) * A.scale * LOG2E;
         }
         __syncthreads();  // and the former part's output and statistics have been read
         const Span cur = j;
-        const bool row_ok = cur.tile * ROWS + gid < cur.s.n * G;
-        const int last = cur.s.ctx - cur.s.n + (cur.tile * ROWS + gid) / G;  // the last position that the row sees
-        const int low = A.window > 0 ? last - A.window + 1 : 0;
+        bool row_ok[RW];
+        int last[RW], low[RW];  // the last and first positions that the row sees
+        float f[RW];
+#pragma unroll
+        for (int w = 0; w < RW; ++w) {
+            const int row = cur.tile * ROWS + gid + 8 * w;
+            row_ok[w] = row < cur.s.n * G;
+            last[w] = cur.s.ctx - cur.s.n + row / G;
+            low[w] = A.window > 0 ? last[w] - A.window + 1 : 0;
+            f[w] = S.f[gid + 8 * w];
+        }
         // what every row of the tile sees
         const int last_all = cur.s.ctx - cur.s.n + cur.tile * ROWS / G;
         const int low_all = A.window > 0 ? cur.s.ctx - A.window : 0;
-        const float f = S.f[gid];
         uint32_t qf[D <= 128 ? D / 16 : 1][4];  // registers hold them where there are enough
         if constexpr (D <= 128) {
 #pragma unroll
@@ -449,7 +467,9 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         float acc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        float mx = -INFINITY, sum = 0.f;
+        float mx[RW], sum[RW];
+#pragma unroll
+        for (int w = 0; w < RW; ++w) mx[w] = -INFINITY, sum[w] = 0.f;
 
         int stage = 1;
         for (int c = cur.c0; c < cur.c1; ++c) {
@@ -500,44 +520,68 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     }
                 }
             }
-            // t (in units of log2); this lane: row gid, positions 8h + 2t, + 1
-            float p[2 * SUBS][2], top = mx;
+            // t (in units of log2); this lane: rows gid (+ 8), positions 8h + 2t, + 1
+            float p[RW][2 * SUBS][2], top[RW];
 #pragma unroll
             for (int h = 0; h < 2 * SUBS; ++h) {
-                const float fk = f * sc[h / 2].x;
                 if constexpr (CH == 2) s[h][0] += s2[h][0], s[h][1] += s2[h][1], s[h][2] += s2[h][2], s[h][3] += s2[h][3];
-                p[h][0] = fmaf(s[h][0] + s[h][2], fk, sc[h / 2].y);
-                p[h][1] = fmaf(s[h][1] + s[h][3], fk, sc[h / 2].y);
+                const float fk = f[0] * sc[h / 2].x;
+                if constexpr (WIDE) {
+                    const float fk1 = f[RW - 1] * sc[h / 2].x;
+                    p[0][h][0] = fmaf(s[h][0], fk, sc[h / 2].y), p[0][h][1] = fmaf(s[h][1], fk, sc[h / 2].y);
+                    p[RW - 1][h][0] = fmaf(s[h][2], fk1, sc[h / 2].y), p[RW - 1][h][1] = fmaf(s[h][3], fk1, sc[h / 2].y);
+                } else {
+                    p[0][h][0] = fmaf(s[h][0] + s[h][2], fk, sc[h / 2].y);
+                    p[0][h][1] = fmaf(s[h][1] + s[h][3], fk, sc[h / 2].y);
+                }
             }
             if (edge) {
 #pragma unroll
-                for (int h = 0; h < 2 * SUBS; ++h)
+                for (int w = 0; w < RW; ++w)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int at = pos + 8 * h + 2 * t4 + i;
-                        const bool seen = row_ok && at <= last && at >= low && !(sc[h / 2].x < 0.f);
-                        if (!seen) p[h][i] = -INFINITY;
-                    }
+                    for (int h = 0; h < 2 * SUBS; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = pos + 8 * h + 2 * t4 + i;
+                            const bool seen = row_ok[w] && at <= last[w] && at >= low[w] && !(sc[h / 2].x < 0.f);
+                            if (!seen) p[w][h][i] = -INFINITY;
+                        }
             }
+            bool grows = false;
 #pragma unroll
-            for (int h = 0; h < 2 * SUBS; ++h) top = fmaxf(top, fmaxf(p[h][0], p[h][1]));
-            top = quad_max(top);
-            if (__any_sync(0xffffffffu, top > mx + SLACK)) {
-                if (!(top > mx + SLACK)) top = mx;
-                const float keep = mx == top ? 1.f : exp2_of(mx - top);
-                mx = top;
-                sum *= keep;
+            for (int w = 0; w < RW; ++w) {
+                top[w] = mx[w];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] *= keep, acc[n][1] *= keep, acc[n][2] *= keep, acc[n][3] *= keep;
+                for (int h = 0; h < 2 * SUBS; ++h) top[w] = fmaxf(top[w], fmaxf(p[w][h][0], p[w][h][1]));
+                top[w] = quad_max(top[w]);
+                grows |= top[w] > mx[w] + SLACK;
             }
-            const float base = (mx == -INFINITY ? 0.f : mx) - LIFT;
-            uint32_t ph[2 * SUBS], pl[2 * SUBS];
+            if (__any_sync(0xffffffffu, grows)) {
+                float keep[RW];
 #pragma unroll
-            for (int h = 0; h < 2 * SUBS; ++h) {
-                p[h][0] = exp2_of(p[h][0] - base);
-                p[h][1] = exp2_of(p[h][1] - base);
-                sum = fmaf(p[h][0] + p[h][1], sc[h / 2].z, sum);
-                split_half(p[h][0], p[h][1], ph[h], pl[h], REST);
+                for (int w = 0; w < RW; ++w) {
+                    if (!(top[w] > mx[w] + SLACK)) top[w] = mx[w];
+                    keep[w] = mx[w] == top[w] ? 1.f : exp2_of(mx[w] - top[w]);
+                    mx[w] = top[w];
+                    sum[w] *= keep[w];
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[n][0] *= keep[0], acc[n][1] *= keep[0], acc[n][2] *= keep[RW - 1], acc[n][3] *= keep[RW - 1];
+            }
+            uint32_t ph[2 * SUBS], pl[2 * SUBS];  // the operand's rows 0..7 and 8..15
+#pragma unroll
+            for (int w = 0; w < RW; ++w) {
+                const float base = (mx[w] == -INFINITY ? 0.f : mx[w]) - LIFT;
+#pragma unroll
+                for (int h = 0; h < 2 * SUBS; ++h) {
+                    const float a = exp2_of(p[w][h][0] - base), b = exp2_of(p[w][h][1] - base);
+                    sum[w] = fmaf(a + b, sc[h / 2].z, sum[w]);
+                    if constexpr (WIDE)
+                        (w ? pl : ph)[h] = half2_of(a, b);
+                    else
+                        split_half(a, b, ph[h], pl[h], REST);
+                }
             }
 #pragma unroll
             for (int b = 0; b < SUBS; ++b)
@@ -574,24 +618,40 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         more = next();
         if (more) {
             look_up(j.c0);
-            load_q();
+            load_q(gid);
         }
-        sum = quad_sum(sum);
-        if (t4 == 0) S.m[warp][gid] = mx, S.l[warp][gid] = sum;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            // tile n, columns 2t and 2t+1: elements 16 * column + n % 16 of its 128 (8 * column + n of 64)
-            const int d0 = D == 64 ? 16 * t4 + n : 128 * (n / 16) + 32 * t4 + n % 16;
-            warp_out<D>(S, warp, gid, d0) = fmaf(acc[n][2], 1.f / REST, acc[n][0]);
-            warp_out<D>(S, warp, gid, d0 + (D == 64 ? 8 : 16)) = fmaf(acc[n][3], 1.f / REST, acc[n][1]);
+        for (int w = 0; w < RW; ++w) {
+            sum[w] = quad_sum(sum[w]);
+            if (t4 == 0) S.m[warp][gid + 8 * w] = mx[w], S.l[warp][gid + 8 * w] = sum[w];
         }
+        // rows 0..7, then 8..15 of a wide tile, through the ring's first stage
+        const auto put_out = [&](int w) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                // tile n, columns 2t and 2t+1: elements 16 * column + n % 16 of its 128 (8 * column + n of 64)
+                const int d0 = D == 64 ? 16 * t4 + n : 128 * (n / 16) + 32 * t4 + n % 16;
+                const float a = WIDE ? acc[n][2 * w] : fmaf(acc[n][2], 1.f / REST, acc[n][0]);
+                const float b = WIDE ? acc[n][2 * w + 1] : fmaf(acc[n][3], 1.f / REST, acc[n][1]);
+                warp_out<D>(S, warp, gid, d0) = a;
+                warp_out<D>(S, warp, gid, d0 + (D == 64 ? 8 : 16)) = b;
+            }
+        };
+        put_out(0);
         if (more) begin();
         __syncthreads();
         const bool whole = cur.c0 == 0 && cur.c1 == cur.s.units;
         const int slot = 2 * blockIdx.x + (cur.c0 == 0 ? 1 : 0);  // a job that began in a former block: the first slot
         const int rows = min(ROWS, cur.s.n * G - cur.tile * ROWS);
+#pragma unroll
+        for (int half = 0; half < RW; ++half) {
+        if (half == 1) {
+            __syncthreads();  // the first rows have been read
+            put_out(1);
+            __syncthreads();
+        }
 #pragma unroll 1
-        for (int r = warp; r < rows; r += AT_WARPS) {
+        for (int r = 8 * half + warp; r < min(rows, 8 * half + 8); r += AT_WARPS) {
             float m = S.m[0][r], l = 0.f, k[AT_WARPS];
 #pragma unroll
             for (int w = 1; w < AT_WARPS; ++w) m = fmaxf(m, S.m[w][r]);
@@ -608,7 +668,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             for (int d = lane; d < D; d += 32) {
                 float o = 0.f;
 #pragma unroll
-                for (int w = 0; w < AT_WARPS; ++w) o += k[w] * warp_out<D>(S, w, r, d);
+                for (int w = 0; w < AT_WARPS; ++w) o += k[w] * warp_out<D>(S, w, r & 7, d);
                 if (whole)
                     store_out<TY>(A, tok, head * D + d, o * inv);
                 else
@@ -620,6 +680,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                 else if (A.lse)
                     A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
             }
+        }
         }
         if (!whole) {
             const int b0 = (int)((cur.first + A.job_cost) / per);
@@ -649,13 +710,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
     const Cut begun = A.cuts[2 * blockIdx.x], went_on = A.cuts[2 * blockIdx.x + 1];
     const auto write = [&](const Cut& cut, int r, int d, float o, float m, float l) {
-        const int row = cut.tile * ROWS + r, head = cut.head * G + row % G;
+        const int row = cut.tile * A.rows + r, head = cut.head * G + row % G;
         const size_t tok = (size_t)cut.row0 + row / G;
         store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
         if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
     };
     // the first block left its part in its second slot, the others in their first
-    const auto slot_of = [](const Cut& cut, int r, int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * ROWS + r; };
+    const auto slot_of = [&](const Cut& cut, int r, int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * A.rows + r; };
     if (begun.parts > 0 && begun.parts <= JOIN_FEW) {
         const int n = begun.parts, d4 = tid % (D / 4) * 4;
         for (int r = tid / (D / 4); r < begun.rows; r += JOIN_THREADS / (D / 4)) {
@@ -749,16 +810,17 @@ constexpr int BLOCKS_PER_SM = 2;
 
 int attn_blocks() { return num_sms() * BLOCKS_PER_SM; }
 
-template <int D, int TY>
+template <int D, int TY, bool WIDE>
 int launch(AttnArgs a, cudaStream_t s) {
+    a.rows = WIDE ? 16 : 8;
     a.unit = Tile<D>::UNIT;
     a.job_cost = Tile<D>::JOB_COST;
     const size_t sched = (size_t)a.B * sizeof(uint32_t);
     const size_t sm = sizeof(AttnSmem<D>) + sched;
     static std::atomic<uint64_t> asked{0};
-    if (!allow_smem((const void*)k_attn<D, TY>, sizeof(AttnSmem<D>) + E0_MAX_SEQS * sizeof(uint32_t), asked))
+    if (!allow_smem((const void*)k_attn<D, TY, WIDE>, sizeof(AttnSmem<D>) + E0_MAX_SEQS * sizeof(uint32_t), asked))
         return E0_ERR_CUDA;
-    k_attn<D, TY><<<a.blocks, AT_WARPS * 32, sm, s>>>(a);
+    k_attn<D, TY, WIDE><<<a.blocks, AT_WARPS * 32, sm, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
     // the join's blocks start while those above still run and wait for all of them
     cudaLaunchConfig_t cfg = {};
@@ -773,16 +835,16 @@ int launch(AttnArgs a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k_attn_join<D, TY>, a) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
 
-template <int TY>
+template <int TY, bool WIDE>
 int launch_d(const AttnArgs& a, int D, cudaStream_t s) {
-    return D == 64 ? launch<64, TY>(a, s) : D == 128 ? launch<128, TY>(a, s) : launch<256, TY>(a, s);
+    return D == 64 ? launch<64, TY, WIDE>(a, s) : D == 128 ? launch<128, TY, WIDE>(a, s) : launch<256, TY, WIDE>(a, s);
 }
 
 }  // namespace
 
 size_t attn_ws_bytes(int D) {
     const size_t slots = 2 * (size_t)attn_blocks();
-    return slots * ROWS * D * sizeof(float) + slots * ROWS * sizeof(float2) + slots * sizeof(Cut);
+    return slots * MOST_ROWS * D * sizeof(float) + slots * MOST_ROWS * sizeof(float2) + slots * sizeof(Cut);
 }
 
 int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
@@ -793,15 +855,16 @@ int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
     a.table = table, a.ctx = ctx, a.cu = cu, a.q = q, a.out = out, a.lse = lse;
     a.blocks = attn_blocks();
     a.part_o = reinterpret_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2 * (size_t)a.blocks * ROWS * c->D);
-    a.cuts = reinterpret_cast<Cut*>(a.part_ml + 2 * (size_t)a.blocks * ROWS);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2 * (size_t)a.blocks * MOST_ROWS * c->D);
+    a.cuts = reinterpret_cast<Cut*>(a.part_ml + 2 * (size_t)a.blocks * MOST_ROWS);
     a.st = st, a.q_ld = q_ld, a.out_ld = out_ld;
     a.B = B, a.max_blocks = max_blocks, a.n_blocks = c->n_blocks, a.Hq = Hq, a.Hkv = c->Hkv, a.max_q = max_q;
     a.window = window, a.scale = scale;
     while ((1 << a.shift) < c->block_tokens) ++a.shift;
-    return dtype == E0_F32   ? launch_d<E0_F32>(a, c->D, s)
-           : dtype == E0_F16 ? launch_d<E0_F16>(a, c->D, s)
-                             : launch_d<E0_BF16>(a, c->D, s);
+    if (dtype == E0_F32) return launch_d<E0_F32, false>(a, c->D, s);
+    if (dtype == E0_F16) return launch_d<E0_F16, false>(a, c->D, s);
+    const bool wide = (int64_t)max_q * (Hq / c->Hkv) > 8;
+    return wide ? launch_d<E0_BF16, true>(a, c->D, s) : launch_d<E0_BF16, false>(a, c->D, s);
 }
 
 }  // namespace e0

@@ -96,10 +96,11 @@ class Cache:
         return k, v
 
 
-def attention(q, k, v, scale, ctx, window):
+def attention(q, k, v, scale, ctx, window, weight_err=0.0):
     """q [n][Hq][D], the last n of ctx positions; k, v [ctx][Hkv][D] (NaN
     positions are not seen).  Returns out, lse and, for each output, a bound on what
-    fp32 sums and 22-bit operands may be off by."""
+    fp32 sums, 22-bit operands and weights that are weight_err (relative) off may
+    be off by."""
     n, Hq, D = q.shape
     Hkv = k.shape[1] if k.ndim == 3 else 1
     G = Hq // Hkv
@@ -126,6 +127,6 @@ def attention(q, k, v, scale, ctx, window):
             # exp2's argument and result; sums over the positions; the operands of the second product
             ds = (D + 16) * eps * mag.max() + 4 * eps * np.abs(x).max()
             rel = 2 * ds + (seen.sum() / 4 + 64) * eps
-            tol[i, h] = rel * ((e / z) @ np.abs(vv))
+            tol[i, h] = (rel + weight_err) * ((e / z) @ np.abs(vv))
             ltol[i, h] = rel + 4 * eps * abs(lse[i, h])
     return out, lse, tol, ltol

@@ -543,7 +543,10 @@ def check_attention(c, table, ctx, cu, q, out, lse, dtype, window=0, scale=None)
         if n == 0:
             continue
         k, v = c.row(table[b], int(ctx[b]))
-        o, l, tol, ltol = R.attention(qv[cu[b]:cu[b + 1]], k, v, scale, int(ctx[b]), window)
+        # bf16 with more than 8 query rows a KV head: weights rounded to fp16, half a step at most
+        wide = dtype == BF16 and int(np.diff(cu).max()) * (Hq // c.H) > 8
+        o, l, tol, ltol = R.attention(qv[cu[b]:cu[b + 1]], k, v, scale, int(ctx[b]), window,
+                                      2.0 ** -11 if wide else 0.0)
         g = got[cu[b]:cu[b + 1]]
         assert (np.abs(g - o) <= tol + H[dtype] * np.abs(o) * 1.0001 + TINY16[dtype]).all(), b
         if gl is not None:
@@ -584,7 +587,25 @@ def test_attention_heads_and_runs_of_queries(L, Hq, Hkv, window):
     check_attention(c, table, ctx, cu, q, out, lse, F16, window)
 
 
-@pytest.mark.parametrize("B,longest,Hq,Hkv,D", [(1, 9000, 8, 1, 128), (1, 20000, 4, 2, 64), (3, 5000, 16, 2, 256),
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 1, 64), (24, 1, 128), (32, 2, 256), (9, 1, 128)])
+@pytest.mark.parametrize("window", [0, 60])
+def test_attention_many_rows_bf16(L, Hq, Hkv, D, window):
+    """More than 8 query rows a KV head: tiles of 16, the last one part empty; sequences on one and on several blocks."""
+    rng = np.random.default_rng(Hq + D)
+    new = [1, 3, 0, 5, 1]
+    ctx = [1, 700, 9, 64, 3000]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    c, t, desc, table = filled_cache(L, len(ctx), 16, Hkv, D, ctx, rng)
+    q = dev(rng.standard_normal((int(cu[-1]), Hq, D)) * 1.5, torch.bfloat16)
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, BF16, window)
+    assert st == 0
+    check_attention(c, table, ctx, cu, q, out, lse, BF16, window)
+    q[0, 8] = float("nan")  # one head of the upper rows
+    out2, lse2, _ = attend(L, c, desc, table, ctx, cu, q, BF16, window)
+    assert out2[0, 8].isnan().all() and torch.equal(out2[1:], out[1:]) and torch.equal(out2[0, :8], out[0, :8])
+
+
+@pytest.mark.parametrize("B,longest,Hq,Hkv,D", [(1, 9000, 8, 1, 128), (1, 20000, 4, 2, 64), (3, 5000, 16, 2, 256), (1, 12000, 32, 2, 128),
                                                 (40, 900, 8, 4, 64), (300, 60, 2, 2, 64)])
 def test_attention_splits(L, B, longest, Hq, Hkv, D):
     """Long sequences split over many blocks, many short ones packed into each."""
