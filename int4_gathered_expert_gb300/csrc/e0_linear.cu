@@ -382,17 +382,16 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
 // and a group by each warp; a warp's records come through its ring as above.  The
 // blocks of a cluster split K.
 constexpr int TOK = 32;
-constexpr int BATCH_RM = 2;
 constexpr int PAIR = 2;
 static_assert(LIN_WARPS == PAIR * TOK / 8, "every warp sums one tile of x and group");
 
-template <int XT>
+template <int XT, int RM>
 struct BatchSmem {
-    static constexpr int STAGES = 3, ROWS = LIN_WARPS * 16 * BATCH_RM;
+    static constexpr int STAGES = 3, ROWS = LIN_WARPS * 16 * RM;
     static constexpr int XROW = GROUP * (XT == E0_F32 ? 4 : XT == E0_E4M3 ? 1 : 2);  // bytes
     union {
         struct {
-            uint8_t rec[STAGES][LIN_WARPS][PAIR][BATCH_RM * REC];
+            uint8_t rec[STAGES][LIN_WARPS][PAIR][RM * REC];
             uint8_t x[STAGES][PAIR][TOK * XROW];
             float sx[2][PAIR][TOK], xs[2][PAIR][TOK];
         };
@@ -405,15 +404,15 @@ struct BatchSmem {
 // find eight different ones.
 template <int XT>
 E0_DEV int x_chunk(int t, int c) {
-    constexpr int PER = BatchSmem<XT>::XROW / 16;
+    constexpr int PER = BatchSmem<XT, 1>::XROW / 16;
     return XT == E0_E4M3 ? t * PER + c : t * PER + (c ^ (t & 1));
 }
 
-template <int XT>
+template <int XT, int RM>
 __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     constexpr bool BF = XT == E0_F32 || XT == E0_BF16;
-    constexpr int P = RawX<XT>::PARTS, RM = BATCH_RM, NT = TOK / 8;
-    typedef BatchSmem<XT> SM;
+    constexpr int P = RawX<XT>::PARTS, NT = TOK / 8;
+    typedef BatchSmem<XT, RM> SM;
     constexpr int STAGES = SM::STAGES, PER = SM::XROW / 16, SZ = SM::XROW / GROUP;
     extern __shared__ __align__(128) uint8_t lin_sm[];
     SM& M = *reinterpret_cast<SM*>(lin_sm);
@@ -636,10 +635,20 @@ template <int XT>
 int linear_type(const LinArgs& a, cudaStream_t s) {
     const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
     if (a.T > 8) {
-        const int tiles = (nb + LIN_WARPS * BATCH_RM - 1) / (LIN_WARPS * BATCH_RM), zs = (a.T + TOK - 1) / TOK;
-        int S = 1;
-        while (S < 8 && (long long)tiles * zs * S < 2LL * sms && G / (2 * S) >= 4) S *= 2;
-        return launch<k_linear_batch<XT>>(a, dim3(tiles, S, zs), sizeof(BatchSmem<XT>), sizeof(BatchSmem<XT>), s);
+        // two row blocks a warp share the operands of x; one where two would
+        // leave SMs without a block
+        const int zs = (a.T + TOK - 1) / TOK;
+        const auto tiles = [&](int rm) { return (nb + LIN_WARPS * rm - 1) / (LIN_WARPS * rm); };
+        const auto split = [&](int rm) {
+            int S = 1;
+            while (S < 8 && (long long)tiles(rm) * zs * S < 2LL * sms && G / (2 * S) >= 4) S *= 2;
+            return S;
+        };
+        if ((long long)tiles(2) * zs * split(2) >= sms)
+            return launch<k_linear_batch<XT, 2>>(a, dim3(tiles(2), split(2), zs), sizeof(BatchSmem<XT, 2>),
+                                                 sizeof(BatchSmem<XT, 2>), s);
+        return launch<k_linear_batch<XT, 1>>(a, dim3(tiles(1), split(1), zs), sizeof(BatchSmem<XT, 1>),
+                                             sizeof(BatchSmem<XT, 1>), s);
     }
     // The more row blocks a warp has, the less the operands of x cost; but there
     // have to be blocks for the whole machine, with K split over up to 8 of
