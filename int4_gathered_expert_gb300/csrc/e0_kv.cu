@@ -194,8 +194,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_release(PlanArgs A) {
 
 // The launches of either: fill and commit in one where the outputs lie apart
 // from the inputs or one thread block does it all, else one after the other.
-template <typename K>
-int plan_launch(K kernel, PlanArgs a, long long work, cudaStream_t s) {
+template <bool RELEASE>
+int plan_launch(PlanArgs a, long long work, cudaStream_t s) {
+    void (*const kernel)(PlanArgs) = RELEASE ? k_kv_release : k_kv_plan;
+    static std::atomic<uint64_t> asked{0};
     long long g = work <= PLAN_ONE_BLOCK ? 1 : (work + PLAN_THREADS - 1) / PLAN_THREADS;
     if (g > num_sms()) g = num_sms();
     const bool apart = a.ctx_out != a.ctx && a.free_out != a.free_count;
@@ -203,9 +205,7 @@ int plan_launch(K kernel, PlanArgs a, long long work, cudaStream_t s) {
     const size_t sm = (3 * (size_t)a.B + 2) * sizeof(int32_t);
     a.fill = true;
     a.commit = g == 1 || apart;
-    if (sm > 40 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
-        return E0_ERR_CUDA;
+    if (!allow_smem((const void*)kernel, (3 * (size_t)E0_MAX_SEQS + 2) * sizeof(int32_t), asked)) return E0_ERR_CUDA;
     kernel<<<(int)g, threads, sm, s>>>(a);
     if (!a.commit) {
         a.fill = false, a.commit = true;
@@ -285,6 +285,19 @@ struct AppRaw {
             for (int i = 0; i < WORDS; ++i) w[i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
         }
     }
+    // The largest magnitude's bits with those of m: 16-bit types two at a time, each
+    // half for itself until fp32_bits.
+    E0_DEV uint32_t max_bits(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            m = TY == E0_F32 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        return m;
+    }
+    static E0_DEV uint32_t fp32_bits(uint32_t m) {
+        if constexpr (TY == E0_F32) return m;
+        const float2 f = unpack16<TY>(max(m & 0xFFFFu, m >> 16));
+        return __float_as_uint(f.x);
+    }
     E0_DEV void get(float (&v)[N]) const {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
@@ -318,6 +331,15 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
     float* scale = (which ? A.scale[1] : A.scale[0]) + (size_t)blk * A.Hkv + head;
     uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
     float old = off > 0 ? *scale : 0.f;
+    // member w has the tokens w, w + TEAM, ...  A team reads what the rest of the block
+    // would hold before it knows the run's length, a single warp the first only.
+    AppRaw<TY, D> held[HOLD];
+    if constexpr (TEAM > 1) {
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) held[k].load(x + (size_t)min(member + k * TEAM, A.T - 1 - t0) * ld, vec);
+    } else {
+        held[0].load(x, vec);
+    }
     // the run's length: tokens that follow with consecutive slots inside the block
     int n = 0;
     for (;;) {
@@ -327,31 +349,48 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
         n += out ? __ffs(out) - 1 : 32;
         if (out) break;
     }
-    // member w has the tokens w, w + TEAM, ...; beyond the last it reads the last again
-    AppRaw<TY, D> held[HOLD];
+    // largest magnitude as bits: of the values, and of those that are finite
+    uint32_t all = 0, m = 0;
+    if constexpr (TEAM == 1) {
 #pragma unroll
-    for (int k = 0; k < HOLD; ++k) held[k].load(x + (size_t)min(member + k * TEAM, n - 1) * ld, vec);
-    uint32_t m = 0, all = 0;
-    const auto look = [&](const AppRaw<TY, D>& r) {
-        float v[N];
-        r.get(v);
+        for (int k = 1; k < HOLD; ++k)
+            if (k < n) held[k].load(x + (size_t)k * ld, vec);
+    }
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-            all = max(all, a);
-            m = max(m, a < 0x7F800000u ? a : 0u);
-        }
-    };
-#pragma unroll
-    for (int k = 0; k < HOLD; ++k) look(held[k]);
+    for (int k = 0; k < HOLD; ++k)
+        if (member + k * TEAM < n) all = held[k].max_bits(all);
 #pragma unroll 1
     for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
         AppRaw<TY, D> r;
         r.load(x + (size_t)i * ld, vec);
-        look(r);
+        all = r.max_bits(all);
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (__any_sync(0xffffffffu, all >= 0x7F800000u) && lane == 0) set_status(A.st, E0_ST_NONFINITE);
+    all = __reduce_max_sync(0xffffffffu, AppRaw<TY, D>::fp32_bits(all));
+    const bool plain = all < 0x7F800000u;  // what this warp has is finite
+    if (plain) {
+        m = all;
+    } else {
+        if (lane == 0) set_status(A.st, E0_ST_NONFINITE);
+        const auto look = [&](const AppRaw<TY, D>& r) {
+            float v[N];
+            r.get(v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                m = max(m, a < 0x7F800000u ? a : 0u);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (member + k * TEAM < n) look(held[k]);
+#pragma unroll 1
+        for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
+            AppRaw<TY, D> r;
+            r.load(x + (size_t)i * ld, vec);
+            look(r);
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+    }
     if constexpr (TEAM > 1) {
         if (lane == 0) most[member] = m;
         __syncthreads();  // and the old scale has been read
@@ -395,7 +434,8 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
         uint32_t c[(N + 3) / 4] = {};
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
-            const float a = fabsf(v[j]) < INFINITY ? v[j] * inv : 0.f, b = fabsf(v[j + 1]) < INFINITY ? v[j + 1] * inv : 0.f;
+            float a = v[j] * inv, b = v[j + 1] * inv;
+            if (!plain) a = fabsf(v[j]) < INFINITY ? a : 0.f, b = fabsf(v[j + 1]) < INFINITY ? b : 0.f;
             c[j / 4] |= e4m3x2(a, b) << (8 * (j & 2));
         }
         uint8_t* p = codes + (size_t)(off + i) * D + lane * N;
@@ -462,7 +502,7 @@ int kv_plan(const e0_kv_state* k, const int32_t* new_len, int T_cap, int32_t* ct
             int32_t* cu_q, int64_t* slots, int32_t* positions, int32_t* seq_ids, uint32_t* st, cudaStream_t s) {
     PlanArgs a = plan_args(k, ctx_out, free_out, st);
     a.new_len = new_len, a.T_cap = T_cap, a.cu_q = cu_q, a.slots = slots, a.positions = positions, a.seq_ids = seq_ids;
-    return plan_launch(k_kv_plan, a, T_cap, s);
+    return plan_launch<false>(a, T_cap, s);
 }
 
 int kv_release(const e0_kv_state* k, const uint8_t* mask, int32_t* ctx_out, int32_t* free_out, uint32_t* st,
@@ -470,7 +510,7 @@ int kv_release(const e0_kv_state* k, const uint8_t* mask, int32_t* ctx_out, int3
     PlanArgs a = plan_args(k, ctx_out, free_out, st);
     a.mask = mask;
     const long long most = (long long)k->B * k->max_blocks;
-    return plan_launch(k_kv_release, a, most < k->n_blocks ? most : k->n_blocks, s);
+    return plan_launch<true>(a, most < k->n_blocks ? most : k->n_blocks, s);
 }
 
 int kv_append(const e0_kv_cache* c, const void* k, const void* v, int dtype, int64_t k_ld, int64_t v_ld,

@@ -120,6 +120,13 @@ E0_DEV void store_chunk(typename Elem<TY>::T* p, int e, int H, const float (&v)[
     }
 }
 
+// The larger magnitude (its sign says nothing); NaN where either is.
+E0_DEV float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A chunk's outputs; all lanes of a warp call it.  Returns whether its group holds a
 // value that is not finite.  rcp.approx and the product with 1 / 448 are an ulp
 // off the divisions, of no account beside the scale's own rounding.
@@ -144,18 +151,18 @@ E0_DEV bool finish_chunk(const NormArgs& A, size_t row, int e, float rstd, float
                 if (e + i < H) v[i] *= rstd, w[i] = __ldg(A.w + e + i);
         }
     }
-    uint32_t m = 0;
+    float mx = 0.f;  // NaN where a value is
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         v[i] *= w[i];
-        if (e + i < H) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // ordered as |v|, NaN above infinity
+        if (VEC || e + i < H) mx = max_abs(mx, v[i]);
     }
     if (A.h) store_chunk<TY, VEC>(reinterpret_cast<T*>(A.h) + row * H, e, H, v);
     if (!A.q) return false;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool bad = m >= 0x7F800000u;
-    const float mx = __uint_as_float(m);
+    for (int o = 1; o < 8; o <<= 1) mx = max_abs(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = fabsf(mx);
+    const bool bad = !(mx < INFINITY) && e < H;
     const bool zero = bad || mx < 7.7037198e-34f;  // 2^-110: 448 / mx and mx / 448 stay normal numbers
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(mx));
