@@ -102,7 +102,8 @@ enum { E0_ROUTE_SOFTMAX_TOPK = 0, E0_ROUTE_SIGMOID_GROUP = 1 };
 
 /* Limits of the kernels (E0_ERR_UNSUPPORTED beyond them). */
 enum { E0_MAX_E = 1024, E0_MAX_K = 32, E0_MAX_T_DECODE = 64, E0_MAX_LORA_RANK = 64 };
-enum { E0_MAX_NORM_H = 16384, E0_MAX_SEQS = 4096, E0_MAX_T_LINEAR = 524280, E0_MAX_K_LINEAR = 1 << 20 };
+enum { E0_MAX_NORM_H = 16384, E0_MAX_SEQS = 4096, E0_MAX_CONTEXT = 1 << 30,
+       E0_MAX_T_LINEAR = 524280, E0_MAX_N_LINEAR = 1 << 28, E0_MAX_K_LINEAR = 1 << 20 };
 
 /* ---- element types of the calls that take one -------------------------
  * E0_E4M3 is the 8-bit float with 4 exponent and 3 mantissa bits, no infinity
@@ -479,7 +480,8 @@ int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, in
                   uint32_t* d_status, e0_stream_t stream);
 
 /* Bytes of an N x K int4 matrix in the layout of e0_linear_forward, 0 where
- * K is no multiple of 64 or a size is not positive. */
+ * K is no multiple of 64 or a size is not positive or beyond E0_MAX_N_LINEAR /
+ * E0_MAX_K_LINEAR. */
 size_t e0_linear_bytes(int N, int K);
 
 /* Lay out a canonical Q-tensor ([N] rows of K inputs) for e0_linear_forward:
@@ -505,7 +507,8 @@ int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_
  * equal bits.  A row of x that holds a NaN or infinity gives a row of y that
  * is not finite; other rows are not touched by it.  Any T: the weights are
  * read once for every 8 to 32 rows, so the call is made for decode batches, not
- * for long prompts (T > E0_MAX_T_LINEAR, K > E0_MAX_K_LINEAR -> E0_ERR_UNSUPPORTED).  Errors: a NULL x, y or w, or no x_scale where x_type
+ * for long prompts (T, N or K beyond E0_MAX_*_LINEAR -> E0_ERR_UNSUPPORTED).
+ * y must not overlap x.  Errors: a NULL x, y or w, or no x_scale where x_type
  * wants one -> E0_ERR_NULL; sizes not positive, K no multiple of 64, an
  * unknown type, a row stride below the row, a w that is not 16-byte aligned,
  * or a pointer that its element type does not align -> E0_ERR_ARG. */
@@ -555,7 +558,8 @@ typedef struct e0_kv_state {
  * slots, positions and seq_ids -1.  An id on the free stack or in the table outside
  * [0, n_blocks) raises E0_ST_BAD_BLOCK and its tokens get slot -1.  Errors: NULL
  * pointers -> E0_ERR_NULL; sizes not positive (B = 0 and T_cap = 0 are allowed),
- * another block_tokens -> E0_ERR_ARG; B > E0_MAX_SEQS -> E0_ERR_UNSUPPORTED. */
+ * another block_tokens -> E0_ERR_ARG; B > E0_MAX_SEQS, max_blocks * block_tokens >
+ * E0_MAX_CONTEXT -> E0_ERR_UNSUPPORTED. */
 int e0_kv_plan(const e0_kv_state* state, const int32_t* new_len, int T_cap, int32_t* ctx_out,
                int32_t* free_out, int32_t* cu_q, int64_t* slots, int32_t* positions, int32_t* seq_ids,
                uint32_t* d_status, e0_stream_t stream);
@@ -589,7 +593,7 @@ int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dty
                  const int64_t* slots, int T, uint32_t* d_status, e0_stream_t stream);
 
 /* Workspace of e0_attn_decode (256-byte aligned; its contents need not be set
- * and are not kept).  0 where a size is not supported. */
+ * and are not kept; calls that may run at the same time need one each).  0 where a size is not supported. */
 size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
 
 /* Attention of the new tokens of B sequences over their cached tokens, the new
@@ -612,8 +616,8 @@ size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * runs of tokens (every 8 query rows of a KV head read the sequence once more).  Errors: NULL
  * pointers -> E0_ERR_NULL; sizes not positive, Hq no multiple of Hkv,
  * window < 0, a short workspace, bad types, strides or alignment (q and its rows 16 bytes),
- * max_q other than 1 without cu_q -> E0_ERR_ARG; D or block_tokens outside the cache's list, B > E0_MAX_SEQS ->
- * E0_ERR_UNSUPPORTED. */
+ * max_q other than 1 without cu_q -> E0_ERR_ARG; D or block_tokens outside the cache's list, B > E0_MAX_SEQS,
+ * max_blocks * block_tokens > E0_MAX_CONTEXT -> E0_ERR_UNSUPPORTED. */
 int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
                    const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq,
                    float scale, int window, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,

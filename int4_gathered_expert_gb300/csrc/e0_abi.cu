@@ -60,6 +60,8 @@ bool aligned(size_t a, const P*... p) {
 }
 
 inline bool block_tokens_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+// Positions of a sequence are 32-bit numbers, with room for sums of two.
+inline bool positions_ok(int max_blocks, int block_tokens) { return (int64_t)max_blocks * block_tokens <= E0_MAX_CONTEXT; }
 
 int check_kv_cache(const e0_kv_cache* c) {
     if (!c) return E0_ERR_NULL;
@@ -74,7 +76,7 @@ int check_kv_cache(const e0_kv_cache* c) {
 int check_kv_state(const e0_kv_state* s, const int32_t* ctx_out, const int32_t* free_out) {
     if (!s) return E0_ERR_NULL;
     if (s->B < 0 || s->max_blocks < 1 || s->n_blocks < 1 || !block_tokens_ok(s->block_tokens)) return E0_ERR_ARG;
-    if (s->B > E0_MAX_SEQS) return E0_ERR_UNSUPPORTED;
+    if (s->B > E0_MAX_SEQS || !positions_ok(s->max_blocks, s->block_tokens)) return E0_ERR_UNSUPPORTED;
     if (!s->free_list || !s->free_count || !free_out) return E0_ERR_NULL;
     if (s->B > 0 && (!s->block_table || !s->ctx_len || !ctx_out)) return E0_ERR_NULL;
     if (!aligned(4, s->block_table, s->ctx_len, s->free_list, s->free_count, ctx_out, free_out)) return E0_ERR_ARG;
@@ -352,13 +354,14 @@ int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, in
 }
 
 size_t e0_linear_bytes(int N, int K) {
-    if (N < 1 || K < 1 || K % 64 != 0) return 0;
+    if (N < 1 || K < 1 || K % 64 != 0 || N > E0_MAX_N_LINEAR || K > E0_MAX_K_LINEAR) return 0;
     return e0::linear_bytes(N, K);
 }
 
 int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_t stream) {
     if (!src || !src->codes || !src->scale || !src->bias || !dst) return E0_ERR_NULL;
     if (N < 1 || K < 1 || K % 64 != 0) return E0_ERR_ARG;
+    if (N > E0_MAX_N_LINEAR || K > E0_MAX_K_LINEAR) return E0_ERR_UNSUPPORTED;
     if (!aligned(16, dst) || !aligned(2, src->scale, src->bias)) return E0_ERR_ARG;
     return e0::pack_linear(src, N, K, dst, cs(stream));
 }
@@ -367,7 +370,7 @@ int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type,
                       int T, const void* add, int64_t add_ld, void* y, int y_type, int64_t y_ld, e0_stream_t stream) {
     if (T < 0 || N < 1 || K < 1 || K % 64 != 0) return E0_ERR_ARG;
     if (!(float_type(x_type) || x_type == E0_E4M3) || !float_type(y_type)) return E0_ERR_ARG;
-    if (T > E0_MAX_T_LINEAR || K > E0_MAX_K_LINEAR) return E0_ERR_UNSUPPORTED;
+    if (T > E0_MAX_T_LINEAR || N > E0_MAX_N_LINEAR || K > E0_MAX_K_LINEAR) return E0_ERR_UNSUPPORTED;
     if (T == 0) return E0_OK;
     if (!w || !x || !y || (x_type == E0_E4M3 && !x_scale)) return E0_ERR_NULL;
     if (x_ld < K || y_ld < N || (add && add_ld < N)) return E0_ERR_ARG;
@@ -425,7 +428,8 @@ int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max
     if (B < 0 || max_blocks < 1 || max_q < 1 || !float_type(dtype) || window < 0) return E0_ERR_ARG;
     if (Hq < cache->Hkv || Hq % cache->Hkv != 0 || !(scale == scale)) return E0_ERR_ARG;
     if (!cu_q && max_q != 1) return E0_ERR_ARG;
-    if (B > E0_MAX_SEQS || (int64_t)max_q * Hq > (int64_t)1 << 30) return E0_ERR_UNSUPPORTED;
+    if (B > E0_MAX_SEQS || (int64_t)max_q * Hq > (int64_t)1 << 30 || !positions_ok(max_blocks, cache->block_tokens))
+        return E0_ERR_UNSUPPORTED;
     if (B == 0) return E0_OK;
     if (!block_table || !ctx_len || !q || !out || !ws) return E0_ERR_NULL;
     const int64_t row = (int64_t)Hq * cache->D;
@@ -433,6 +437,8 @@ int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max
     if (!aligned(16, q) || (q_ld * elem_bytes(dtype)) % 16 != 0 || !aligned(elem_bytes(dtype), out)) return E0_ERR_ARG;
     if (!aligned(4, block_table, ctx_len, cu_q, lse) || !aligned(256, ws)) return E0_ERR_ARG;
     if (ws_bytes < e0::attn_ws_bytes(cache->D)) return E0_ERR_ARG;
+    // a window that no sequence can outgrow is none
+    if (window >= max_blocks * cache->block_tokens) window = 0;
     return e0::attn_decode(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale, window,
                            out, out_ld, lse, ws, d_status, cs(stream));
 }

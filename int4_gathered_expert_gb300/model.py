@@ -402,8 +402,8 @@ class BatchDecoder:
         self.r_out = buf(T, H)
 
     def step(self, x: torch.Tensor, new_len: torch.Tensor, window: int = 0, stream=None) -> torch.Tensor:
-        """x fp32 [T, H], new_len int32 [B] on the device; the rows after the
-        last new token hold nothing of use.  Where a step finds no room
+        """x fp32 [T, H], new_len int32 [B] on the device; the rows of x after the
+        last new token are any finite values, those of the result nothing of use.  Where a step finds no room
         (E0_ST_POOL_FULL in ``status``), no token is cached."""
         sd, a, c, T, H = self.sd, self.a, self.cache, self.T, self.sd.H
         kw = dict(stream=stream)

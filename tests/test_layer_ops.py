@@ -763,6 +763,60 @@ def test_attention_offsets_beyond_32_bits(L):
 # ------------------------------------------------------------------ all of them
 
 
+def test_attention_most_sequences_and_a_window_without_end(L):
+    """As many sequences as a call takes, most of them empty or one token long; a window that covers everything is none."""
+    rng = np.random.default_rng(16)
+    B, Hq, Hkv, D, bs = 4096, 2, 1, 64, 16
+    ctx = rng.integers(0, 3, B)
+    ctx[[0, 1000, 4095]] = [40, 300, 17]
+    new = np.minimum(ctx, 1)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    c, t, desc, table = filled_cache(L, B, bs, Hkv, D, ctx, rng)
+    q = dev(rng.standard_normal((int(cu[-1]), Hq, D)), torch.float32)
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, F32)
+    assert st == 0
+    check_attention(c, table, ctx, cu, q, out, lse, F32)
+    for window in (2 ** 31 - 1, table.shape[1] * bs):
+        again, _, _ = attend(L, c, desc, table, ctx, cu, q, F32, window)
+        assert torch.equal(out, again)
+
+
+def test_calls_at_once_on_two_streams(L):
+    """The same operators on two streams, workspaces of their own: what each leaves is what it leaves alone."""
+    rng = np.random.default_rng(17)
+    jobs = []
+    for ctx in ([2500, 64, 900], [70, 3100, 1]):
+        c, t, desc, table = filled_cache(L, 3, 64, 2, 128, ctx, rng)
+        w, *_, keep = make_linear(L, 3000, 1024, rng)
+        q = dev(rng.standard_normal((3, 8, 128)), torch.float16)
+        x = dev(rng.standard_normal((12, 1024)), torch.float16)
+        wsb = L.e0_attn_workspace_size(3, 8, 2, 128, 1)
+        jobs.append(dict(desc=desc, t=t, table=dev(table), M=table.shape[1], ctx=dev(np.array(ctx, np.int32)), q=q, x=x, w=w,
+                         keep=keep, ws=torch.empty(wsb, dtype=torch.uint8, device="cuda"), wsb=wsb, o=torch.empty_like(q),
+                         y=torch.empty((12, 3000), device="cuda"), n8=torch.empty((12, 1024), dtype=torch.uint8, device="cuda"),
+                         ns=torch.empty((12, 16), device="cuda")))
+
+    def run(j, stream=None):
+        L.e0_attn_decode(j["desc"], j["table"], j["M"], j["ctx"], None, 3, 1, j["q"], F16, 1024, 8, 0.1, 0, j["o"], 1024,
+                         None, j["ws"], j["wsb"], None, stream)
+        L.e0_rmsnorm_q8(j["x"], None, None, 12, 1024, F16, 1e-6, 1024, 0, None, None, j["n8"], j["ns"], None, stream)
+        L.e0_linear_forward(j["w"], 3000, 1024, j["n8"], E4M3, 1024, j["ns"], 12, None, 0, j["y"], F32, 3000, stream)
+
+    want = []
+    for j in jobs:
+        run(j)
+        want.append((j["o"].clone(), j["y"].clone()))
+        j["o"].zero_(), j["y"].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for j, s in zip(jobs, streams):
+            run(j, s)
+    torch.cuda.synchronize()
+    for j, (o, y) in zip(jobs, want):
+        assert torch.equal(j["o"], o) and torch.equal(j["y"], y)
+
+
 def test_streams_and_graphs_share_a_workspace(L):
     """Two captured attention steps over one workspace, replayed in turn, and the same on another stream, equal the eager calls."""
     rng = np.random.default_rng(15)

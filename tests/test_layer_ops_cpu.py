@@ -55,7 +55,7 @@ LIN = dict(w=P, N=64, K=128, x=P, x_type=0, x_ld=128, x_scale=None, T=1, add=Non
     (dict(x_type=3), "NULL"), (dict(x_ld=127), "ARG"), (dict(y_ld=63), "ARG"), (dict(add=P, add_ld=63), "ARG"),
     (dict(w=P + 8), "ARG"), (dict(x=P + 2), "ARG"), (dict(y=P + 2), "ARG"), (dict(add=2 * P, add_ld=65), "ARG"),
     (dict(x_type=3, x_scale=P + 1), "ARG"), (dict(T=524281), "UNSUPPORTED"),
-    (dict(K=(1 << 20) + 64, x_ld=1 << 21), "UNSUPPORTED"), (dict(T=0, x=None), "OK")])
+    (dict(K=(1 << 20) + 64, x_ld=1 << 21), "UNSUPPORTED"), (dict(N=(1 << 28) + 1, y_ld=1 << 29), "UNSUPPORTED"), (dict(T=0, x=None), "OK")])
 def test_linear_refusals(L, change, code):
     want = L.E0_OK if code == "OK" else getattr(L, "E0_ERR_" + code)
     assert call(L.e0_linear_forward, LIN, **change) == want
@@ -65,7 +65,7 @@ def test_pack_linear_refusals_and_sizes(L):
     assert L.e0_linear_bytes(1, 64) == L.e0_linear_bytes(128, 64) == 8 * 576
     assert L.e0_linear_bytes(129, 128) == 2 * 2 * 8 * 576
     assert L.e0_linear_bytes(131072, 8192) == 8192 * 128 * 576
-    for n, k in ((0, 64), (1, 0), (1, 63), (-1, 64)):
+    for n, k in ((0, 64), (1, 0), (1, 63), (-1, 64), ((1 << 28) + 1, 64), (1, (1 << 20) + 64)):
         assert L.e0_linear_bytes(n, k) == 0
     q = L.QTensor(P, P, P)
     no = dict(stream=0, raise_on_error=False)
@@ -74,6 +74,7 @@ def test_pack_linear_refusals_and_sizes(L):
     assert L.e0_pack_linear(q, 16, 64, None, **no) == L.E0_ERR_NULL
     assert L.e0_pack_linear(q, 0, 64, P, **no) == L.E0_ERR_ARG
     assert L.e0_pack_linear(q, 16, 65, P, **no) == L.E0_ERR_ARG
+    assert L.e0_pack_linear(q, (1 << 28) + 1, 64, P, **no) == L.E0_ERR_UNSUPPORTED
     assert L.e0_pack_linear(q, 16, 64, P + 8, **no) == L.E0_ERR_ARG
     assert L.e0_pack_linear(L.QTensor(P, P + 1, P), 16, 64, P, **no) == L.E0_ERR_ARG
 
@@ -87,7 +88,7 @@ def state(L, **c):
 @pytest.mark.parametrize("change,code", [
     (dict(B=-1), "ARG"), (dict(max_blocks=0), "ARG"), (dict(n_blocks=0), "ARG"), (dict(block_tokens=8), "ARG"),
     (dict(block_tokens=48), "ARG"), (dict(B=4097), "UNSUPPORTED"), (dict(block_table=None), "NULL"),
-    (dict(ctx_len=None), "NULL"), (dict(free_list=None), "NULL"), (dict(free_count=None), "NULL"),
+    (dict(max_blocks=(1 << 26) + 1), "UNSUPPORTED"), (dict(ctx_len=None), "NULL"), (dict(free_list=None), "NULL"), (dict(free_count=None), "NULL"),
     (dict(ctx_len=P + 2), "ARG")])
 def test_plan_and_release_refuse_a_bad_state(L, change, code):
     s = state(L, **change)
@@ -150,7 +151,7 @@ ATT = dict(cache=None, block_table=P, max_blocks=4, ctx_len=P, cu_q=P, B=2, max_
     (dict(B=-1), "ARG"), (dict(max_blocks=0), "ARG"), (dict(max_q=0), "ARG"), (dict(dtype=3), "ARG"),
     (dict(window=-1), "ARG"), (dict(Hq=3), "ARG"), (dict(Hq=1), "ARG"), (dict(scale=float("nan")), "ARG"),
     (dict(cu_q=None, max_q=2), "ARG"), (dict(B=4097), "UNSUPPORTED"), (dict(max_q=1 << 30), "UNSUPPORTED"),
-    (dict(block_table=None), "NULL"), (dict(ctx_len=None), "NULL"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
+    (dict(max_blocks=(1 << 26) + 1), "UNSUPPORTED"), (dict(block_table=None), "NULL"), (dict(ctx_len=None), "NULL"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
     (dict(ws=None), "NULL"), (dict(q_ld=255), "ARG"), (dict(q_ld=257), "ARG"), (dict(out_ld=255), "ARG"),
     (dict(q=P + 8), "ARG"), (dict(out=P + 1), "ARG"), (dict(lse=P + 2), "ARG"), (dict(ws=P + 128), "ARG"),
     (dict(ws_bytes=1), "ARG"), (dict(B=0, q=None), "OK")])
