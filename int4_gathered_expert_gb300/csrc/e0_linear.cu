@@ -376,24 +376,22 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
 }
 
 // More than 8 rows of x: 32 of them (TOK) and 128*RM rows of W a block; a warp has
-// 16*RM rows and all warps go through the groups of the block's share of K
-// together, PAIR at a time.  x comes through shared memory once for the block,
-// its sums over groups are formed there one step ahead, a tile of 8 tokens
-// and a group by each warp; a warp's records come through its ring as above.  The
-// blocks of a cluster split K.
+// 16*RM rows and goes through all groups of the block's share of K, its records
+// coming through its ring as above.  x comes through shared memory once for the
+// block, CHUNK groups at a time, and its sums over groups are formed there; inside
+// a chunk warps do not wait for one another.  The blocks of a cluster split K.
 constexpr int TOK = 32;
-constexpr int PAIR = 2;
-static_assert(LIN_WARPS == PAIR * TOK / 8, "every warp sums one tile of x and group");
 
 template <int XT, int RM>
 struct BatchSmem {
-    static constexpr int STAGES = 3, ROWS = LIN_WARPS * 16 * RM;
+    static constexpr int STAGES = 4, ROWS = LIN_WARPS * 16 * RM;
     static constexpr int XROW = GROUP * (XT == E0_F32 ? 4 : XT == E0_E4M3 ? 1 : 2);  // bytes
+    static constexpr int CHUNK = XT == E0_F32 ? 8 : 16;
     union {
         struct {
-            uint8_t rec[STAGES][LIN_WARPS][PAIR][RM * REC];
-            uint8_t x[STAGES][PAIR][TOK * XROW];
-            float sx[2][PAIR][TOK], xs[2][PAIR][TOK];
+            uint8_t rec[LIN_WARPS][STAGES][RM * REC];
+            uint8_t x[CHUNK][TOK * XROW];
+            float sx[CHUNK][TOK], xs[CHUNK][TOK];
         };
         float sums[ROWS * (TOK + 1)];  // at the end: over the tile, or the cluster's share of it
     };
@@ -413,7 +411,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     constexpr bool BF = XT == E0_F32 || XT == E0_BF16;
     constexpr int P = RawX<XT>::PARTS, NT = TOK / 8;
     typedef BatchSmem<XT, RM> SM;
-    constexpr int STAGES = SM::STAGES, PER = SM::XROW / 16, SZ = SM::XROW / GROUP;
+    constexpr int STAGES = SM::STAGES, PER = SM::XROW / 16, SZ = SM::XROW / GROUP, CHUNK = SM::CHUNK;
     extern __shared__ __align__(128) uint8_t lin_sm[];
     SM& M = *reinterpret_cast<SM*>(lin_sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, t4 = lane & 3;
@@ -421,50 +419,45 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);
     const int nb = (A.N + 15) / 16, rb0 = (blockIdx.x * LIN_WARPS + warp) * RM, tok0 = blockIdx.z * TOK;
 
-    // the thread's 16-byte pieces of a group of its warp's records and of x
-    constexpr int PIECES = (RM * 36 + 31) / 32, XPIECES = (TOK * PER + LIN_WARPS * 32 - 1) / (LIN_WARPS * 32);
+    // the thread's 16-byte pieces of a group of x
+    constexpr int XPIECES = (TOK * PER + LIN_WARPS * 32 - 1) / (LIN_WARPS * 32);
+    const auto stage_x = [&](int g, int n) {
+#pragma unroll
+        for (int i = 0; i < XPIECES; ++i) {
+            const int e = i * LIN_WARPS * 32 + tid, t = e / PER, c = e % PER;
+            if (t >= TOK) continue;
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(A.x) + ((size_t)(tok0 + t) * A.x_ld + g * GROUP) * SZ + c * 16;
+            uint8_t* to = M.x[0] + 16 * x_chunk<XT>(t, c);
+            for (int k = 0; k < n; ++k, src += GROUP * SZ, to += TOK * SM::XROW) {
+                if (tok0 + t >= A.T) {
+                    *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+                } else if (A.vec) {
+                    copy16(to, src);
+                } else {
+                    for (int b = 0; b < 16; b += SZ) {
+                        if (SZ == 4) *reinterpret_cast<uint32_t*>(to + b) = *reinterpret_cast<const uint32_t*>(src + b);
+                        if (SZ == 2) *reinterpret_cast<uint16_t*>(to + b) = *reinterpret_cast<const uint16_t*>(src + b);
+                        if (SZ == 1) to[b] = src[b];
+                    }
+                }
+            }
+        }
+        copy_commit();
+    };
+    // the lane's 16-byte pieces of a group of its warp's records
+    constexpr int PIECES = (RM * 36 + 31) / 32;
     static_assert(SUPER % RM == 0, "a warp's records of a group stand together");
     const uint8_t* src = A.w + ((size_t)(rb0 / SUPER) * G + g0) * SREC + (rb0 % SUPER) * REC + lane * 16;
     const bool mine = rb0 < nb;
-    const uint8_t* xsrc[XPIECES];
-    uint32_t xdst[XPIECES];
-#pragma unroll
-    for (int i = 0; i < XPIECES; ++i) {
-        const int e = i * LIN_WARPS * 32 + tid, t = e / PER, c = e % PER;
-        xdst[i] = 16 * x_chunk<XT>(t, c);
-        xsrc[i] = t < TOK && tok0 + t < A.T
-                      ? reinterpret_cast<const uint8_t*>(A.x) + ((size_t)(tok0 + t) * A.x_ld + g0 * GROUP) * SZ + c * 16
-                      : nullptr;
-        if (t < TOK && !xsrc[i])  // tokens that are not there: zeros in all stages
-            for (int k = 0; k < STAGES * PAIR; ++k)
-                *reinterpret_cast<uint4*>(M.x[k / PAIR][k % PAIR] + xdst[i]) = make_uint4(0, 0, 0, 0);
-    }
     int in_stage = 0;
     const auto issue = [&](int g) {
+        if (mine && g < g1) {
+            uint8_t* dst = M.rec[warp][in_stage] + lane * 16;
 #pragma unroll
-        for (int h = 0; h < PAIR; ++h)
-            if (g + h < g1) {
-                uint8_t* dst = M.rec[in_stage][warp][h] + lane * 16;
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-                    if (mine && i * 32 + lane < RM * 36) copy16(dst + i * 512, src + i * 512);
-                src += SREC;
-#pragma unroll
-                for (int i = 0; i < XPIECES; ++i)
-                    if (xsrc[i]) {
-                        uint8_t* to = M.x[in_stage][h] + xdst[i];
-                        if (A.vec) {
-                            copy16(to, xsrc[i]);
-                        } else {
-                            for (int k = 0; k < 16; k += SZ) {
-                                if (SZ == 4) *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(xsrc[i] + k);
-                                if (SZ == 2) *reinterpret_cast<uint16_t*>(to + k) = *reinterpret_cast<const uint16_t*>(xsrc[i] + k);
-                                if (SZ == 1) to[k] = xsrc[i][k];
-                            }
-                        }
-                        xsrc[i] += GROUP * SZ;
-                    }
-            }
+            for (int i = 0; i < PIECES; ++i)
+                if (i * 32 + 31 < RM * 36 || i * 32 + lane < RM * 36) copy16(dst + i * 512, src + i * 512);
+            src += SREC;
+        }
         if (++in_stage == STAGES) in_stage = 0;
         copy_commit();
     };
@@ -477,14 +470,12 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
         }
         fragments<XT>(r, b);
     };
-    // sums over a group of 8 tokens' inputs: the warp's tile and group of a step
-    const auto sum_x = [&](int step, int stage, int g) {
-        const int h = warp / NT, n = warp % NT;
-        if (g + h >= g1) return;
+    // sums over a group of 8 tokens' inputs
+    const auto sum_x = [&](int g, int k, int n) {
         const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
         const uint32_t ones[4] = {one, one, one, one};
         uint32_t b[P][8];
-        fragments_of(M.x[stage][h], n, b);
+        fragments_of(M.x[k], n, b);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -492,10 +483,10 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
             for (int p = 0; p < P; ++p) mma16(d, ones, b[p][2 * i], b[p][2 * i + 1], BF);
         if (gid == 0) {
             const int t = 8 * n + 2 * t4;
-            *reinterpret_cast<float2*>(&M.sx[step & 1][h][t]) = make_float2(d[0], d[1]);
+            *reinterpret_cast<float2*>(&M.sx[k][t]) = make_float2(d[0], d[1]);
             if constexpr (XT == E0_E4M3) {
-                M.xs[step & 1][h][t] = tok0 + t < A.T ? __ldg(A.xs + (size_t)(tok0 + t) * G + g + h) : 0.f;
-                M.xs[step & 1][h][t + 1] = tok0 + t + 1 < A.T ? __ldg(A.xs + (size_t)(tok0 + t + 1) * G + g + h) : 0.f;
+                M.xs[k][t] = tok0 + t < A.T ? __ldg(A.xs + (size_t)(tok0 + t) * G + g) : 0.f;
+                M.xs[k][t + 1] = tok0 + t + 1 < A.T ? __ldg(A.xs + (size_t)(tok0 + t + 1) * G + g) : 0.f;
             }
         }
     };
@@ -505,23 +496,31 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     for (int r = 0; r < RM; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) tot[r][n][0] = tot[r][n][1] = tot[r][n][2] = tot[r][n][3] = 0.f;
+    int stage = 0;
 #pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) issue(g0 + i * PAIR);
-    copy_wait<STAGES - 2>();
-    __syncthreads();
-    sum_x(0, 0, g0);
-    int stage = 0, step = 0;
+    for (int c0 = g0; c0 < g1; c0 += CHUNK) {
+        const int n_g = min(CHUNK, g1 - c0);
+        if (c0 > g0) __syncthreads();  // the last chunk has been read
+        stage_x(c0, n_g);
+        if (c0 == g0) {
 #pragma unroll 1
-    for (int g = g0; g < g1; g += PAIR, ++step) {
-        copy_wait<STAGES - 3>();
-        __syncthreads();  // this step and the next and this one's sums are there; the last one has been read
-        issue(g + (STAGES - 1) * PAIR);
-        const int ahead = stage + 1 == STAGES ? 0 : stage + 1;
-        sum_x(step + 1, ahead, g + PAIR);
-#pragma unroll
-        for (int h = 0; h < PAIR; ++h) {
-            if (g + h >= g1) break;
-            const uint8_t* x = M.x[stage][h];
+            for (int i = 0; i < STAGES - 1; ++i) issue(g0 + i);
+            copy_wait<STAGES - 1>();
+        } else {
+            copy_wait<0>();
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = warp; i < n_g * NT; i += LIN_WARPS) sum_x(c0 + i / NT, i / NT, i % NT);
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < n_g; ++k) {
+            copy_wait<STAGES - 2>();
+            __syncwarp();  // the group has arrived for all lanes, and all have read the one before it
+            const uint8_t* recs = M.rec[warp][stage];
+            if (++stage == STAGES) stage = 0;
+            issue(c0 + k + STAGES - 1);
+            const uint8_t* x = M.x[k];
             uint32_t b[P == 1 ? NT : 1][P][8];  // one part: all tiles' operands stay for the rows to come
             if constexpr (P == 1) {
 #pragma unroll
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
             }
 #pragma unroll
             for (int r = 0; r < RM; ++r) {
-                const uint8_t* rec = M.rec[stage][warp][h] + r * REC;
+                const uint8_t* rec = recs + r * REC;
                 const uint4 c = *reinterpret_cast<const uint4*>(rec + lane * 16);
                 const uint2 sb = *reinterpret_cast<const uint2*>(rec + 512 + gid * 8);
                 const float2 lo = scale_bias<BF, false>(sb.x), hi = scale_bias<BF, true>(sb.y);
@@ -566,18 +565,17 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[step & 1][h][8 * n + 2 * t4]);
+                    const float2 sx2 = *reinterpret_cast<const float2*>(&M.sx[k][8 * n + 2 * t4]);
                     const float sx[2] = {sx2.x, sx2.y};
                     float xs[2] = {1.f, 1.f};
                     if constexpr (XT == E0_E4M3) {
-                        const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[step & 1][h][8 * n + 2 * t4]);
+                        const float2 x2 = *reinterpret_cast<const float2*>(&M.xs[k][8 * n + 2 * t4]);
                         xs[0] = x2.x, xs[1] = x2.y;
                     }
                     add_group<XT == E0_E4M3>(tot[r][n], d[n], lo.x, lo.y, hi.x, hi.y, sx, xs);
                 }
             }
         }
-        stage = ahead;
     }
     copy_wait<0>();
     const int cols = min(A.T - tok0, TOK);
