@@ -39,6 +39,19 @@ namespace {
 // scales are: the rest of a weight goes in times 2^12, so weights down to 2^-43
 // of the largest count.  The softmax's sum is that of the weights over their
 // scales.
+//
+// Measured (device time, GB300): 64 sequences of up to 16000 tokens, 32 query on 4
+// KV heads of 128, 498 MB: 85.5 us, 5.8 TB/s, 86 % of the measured copy rate; what
+// is missing is the first steps' latency (4 us), jobs' ends and the join (3 us).  One
+// sequence of 32000, 16 on 2 heads of 256, 33 MB: 16.9 us, four steps a warp
+// between the schedule and the join.  16 sequences of 16000, 32 on 2 heads of 256:
+// 94.2 us in tiles of 8 rows, 73.8 in tiles of 16 (bf16); 32 of 8000, two queries
+// each, 32 on 4 of 128: 46.2 and 43.0.
+// What got it there, on the first of these: 166 us with loads straight into
+// registers; 155 with the ring; 110 with steps of 32 positions, the hardware's
+// widening of e4m3 (one instruction a pair; masks and shifts took three) and value
+// scales in the exponent; 93 with the next job's copies started before a job's end
+// and query loads without a branch between them; 86 with jobs' costs in the schedule.
 
 constexpr int AT_WARPS = 4;
 constexpr int MOST_ROWS = 16;

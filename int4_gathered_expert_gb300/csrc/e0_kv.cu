@@ -16,6 +16,9 @@ namespace {
 // one launch does it without blocks waiting on one another.  Only new lengths
 // and stack height written over the old ones must come after every block has
 // read those: in the same block where there is one, else in a second launch.
+// Bound by latency: a launch, the lengths' loads, two barriers, a search.  Measured
+// (device time, GB300): 64 sequences, a token each, 3.4 us; 300 sequences, 73739
+// tokens, 5.2 us.
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_ONE_BLOCK = 4096;  // tokens (blocks, for a release) that one thread block takes
@@ -237,6 +240,10 @@ PlanArgs plan_args(const e0_kv_state* k, int32_t* ctx_out, int32_t* free_out, ui
 // but the codes that fall into e4m3's subnormals.  (A scale of max / 448 would round
 // every older code again at each new maximum, and e4m3's relative precision gains
 // nothing from it.)
+// Measured (device time, GB300): 13013 tokens of 2 heads of 256 in fp16, 40 MB: 13.2 us,
+// 3.0 TB/s: a run is a chain of slots, rows, a barrier and stores of 4 us, and an
+// SM holds four at a time (one warp a run: 36.8 us); 64 single tokens of 8 heads of
+// 128: 3.2 us.
 
 constexpr int APP_WARPS = 8;
 

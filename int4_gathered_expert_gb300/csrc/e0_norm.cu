@@ -17,6 +17,11 @@ namespace {
 // beside its elements is shared by 8 times as many).
 // VEC: H is a multiple of 8 and every row starts on a 16-byte boundary, so a chunk
 // is whole vector accesses; otherwise elements are checked one by one.
+//
+// Measured (device time, GB300): 16384 x 1536 bf16, 178 MB: 31.6 us, 5.6 TB/s, 83 % of
+// the measured copy rate (a block per row: 43.1 us, the block's sum and the root once
+// for every 8 elements a thread); 16384 x 2048 fp32, 436 MB: 78 us, 5.6 TB/s; 8 x 2048:
+// 1.8 us, a launch.
 struct NormArgs {
     const void* r;
     const void* d;
@@ -244,7 +249,8 @@ void launch_rows(const NormArgs& a, cudaStream_t s) {
 template <int TY, bool VEC>
 int launch(const NormArgs& a, cudaStream_t s) {
     const int T = a.T;
-    // a warp a row from where the rows give every SM two blocks of warps
+    // a warp a row from where the rows give every SM two blocks of warps (16384 rows of
+    // 1536: 31.6 us against 43.1); below, a row's latency counts (8 rows: 1.8 us)
     if (VEC && a.H <= 2048 && T >= 2 * NORM_WARPS * num_sms()) {
         launch_rows<TY>(a, s);
         return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
