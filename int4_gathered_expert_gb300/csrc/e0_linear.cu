@@ -642,8 +642,8 @@ template <int XT>
 int linear_type(const LinArgs& a, cudaStream_t s) {
     const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
     if (a.T > 8) {
-        // two row blocks a warp share the operands of x; one where two would
-        // leave SMs without a block
+        // two row blocks a warp share the operands of x; one where two would leave SMs
+        // without a block (32 rows on 4096 x 4096: 11.5 us with one, 15.5 with two)
         const int zs = (a.T + TOK - 1) / TOK;
         const auto tiles = [&](int rm) { return (nb + LIN_WARPS * rm - 1) / (LIN_WARPS * rm); };
         const auto split = [&](int rm) {

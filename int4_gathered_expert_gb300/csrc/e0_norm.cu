@@ -12,16 +12,15 @@ namespace {
 // then the outputs), so a row is read once: bytes moved are the algorithmic ones
 // and the kernel is bound by them.  Chunk c of a row is the 8 consecutive elements
 // 8c...; neighbouring lanes hold neighbouring chunks, so a group of 64 is 8 lanes
-// and its maximum three shuffles.  Two shapes: a block per row (few rows: the
-// latency of one row counts), and a warp per row (many rows: what a row costs
-// beside its elements is shared by 8 times as many).
+// and its maximum three shuffles.  Two shapes: a block per row, and for many short
+// rows a warp per row, without the block's barrier.
 // VEC: H is a multiple of 8 and every row starts on a 16-byte boundary, so a chunk
 // is whole vector accesses; otherwise elements are checked one by one.
 //
-// Measured (device time, GB300): 16384 x 1536 bf16, 178 MB: 31.6 us, 5.6 TB/s, 83 % of
-// the measured copy rate (a block per row: 43.1 us, the block's sum and the root once
-// for every 8 elements a thread); 16384 x 2048 fp32, 436 MB: 78 us, 5.6 TB/s; 8 x 2048:
-// 1.8 us, a launch.
+// Measured (device time, GB300): 16384 x 2048 fp32, 436 MB: 64.1 us, 6.8 TB/s, the
+// measured copy rate; 16384 x 1536 bf16, 178 MB: 28.9 us, 6.1 TB/s, 91 % of it; 8 x 2048
+// fp32: 1.8 us, a launch.  What got the second there from 43.1 us: all loads before the
+// first use, approximate reciprocals in place of divisions, one-instruction maxima.
 struct NormArgs {
     const void* r;
     const void* d;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(NormArgs A) {
 constexpr int NORM_WARPS = 8;
 
 template <int TY, int CH>
-__global__ void __launch_bounds__(NORM_WARPS * 32, CH >= 8 ? 2 : 3) k_rmsnorm_q8_rows(NormArgs A) {
+__global__ void __launch_bounds__(NORM_WARPS * 32) k_rmsnorm_q8_rows(NormArgs A) {
     typedef typename Elem<TY>::T T;
     const int H = A.H, lane = threadIdx.x & 31;
     const size_t row = (size_t)blockIdx.x * NORM_WARPS + (threadIdx.x >> 5);
@@ -233,34 +232,25 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, CH >= 8 ? 2 : 3) k_rmsnorm_q8
     if (bad && (lane & 7) == 0) set_status(A.st, E0_ST_NONFINITE);
 }
 
-template <int TY>
-void launch_rows(const NormArgs& a, cudaStream_t s) {
-    const int grid = (a.T + NORM_WARPS - 1) / NORM_WARPS, nt = NORM_WARPS * 32;
-    if (a.H <= 512)
-        k_rmsnorm_q8_rows<TY, 2><<<grid, nt, 0, s>>>(a);
-    else if (a.H <= 1024)
-        k_rmsnorm_q8_rows<TY, 4><<<grid, nt, 0, s>>>(a);
-    else if (a.H <= 1536)
-        k_rmsnorm_q8_rows<TY, 6><<<grid, nt, 0, s>>>(a);
-    else
-        k_rmsnorm_q8_rows<TY, 8><<<grid, nt, 0, s>>>(a);
-}
-
 template <int TY, bool VEC>
 int launch(const NormArgs& a, cudaStream_t s) {
     const int T = a.T;
-    // a warp a row from where the rows give every SM two blocks of warps (16384 rows of
-    // 1536: 31.6 us against 43.1); below, a row's latency counts (8 rows: 1.8 us)
-    if (VEC && a.H <= 2048 && T >= 2 * NORM_WARPS * num_sms()) {
-        launch_rows<TY>(a, s);
+    // Short rows, many of them: a warp a row (4800 rows of 512 bf16: 3.7 us against 4.5
+    // with a block a row; 600 rows 2.4 against 2.3; rows of 1024 fp32: 14.8 against 12.5).
+    if (VEC && a.H <= 512 && T >= NORM_WARPS * num_sms()) {
+        k_rmsnorm_q8_rows<TY, 2><<<(T + NORM_WARPS - 1) / NORM_WARPS, NORM_WARPS * 32, 0, s>>>(a);
         return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
     }
     const int chunks = (a.H + 7) / 8;
-    int nt = (chunks + 31) / 32 * 32;
+    // A chunk a thread; two where there is work for the whole machine and a chunk is 16
+    // bytes (16384 rows of 1536 bf16: 28.9 us against 32.4, 2400 rows 4.8 against 5.6,
+    // 600 rows 3.0 against 2.7; fp32 gains nothing from it).
+    const int two = TY != E0_F32 && (long long)T * a.H >= 1 << 21 ? 2 : 1;
+    int nt = ((chunks + two - 1) / two + 31) / 32 * 32;
     if (nt > 512) nt = 512;
-    if (chunks <= 512)
+    if (chunks <= nt)
         k_rmsnorm_q8<TY, VEC, 1><<<T, nt, 0, s>>>(a);
-    else if (chunks <= 1024)
+    else if (chunks <= 2 * nt)
         k_rmsnorm_q8<TY, VEC, 2><<<T, nt, 0, s>>>(a);
     else
         k_rmsnorm_q8<TY, VEC, 4><<<T, nt, 0, s>>>(a);

@@ -47,7 +47,8 @@ def status():
 # ------------------------------------------------------------------ norm
 
 
-@pytest.mark.parametrize("T,H_", [(1, 64), (8, 2048), (3, 1536), (5, 100), (2, 1), (2, 63), (7, 65), (3, 4104),
+@pytest.mark.parametrize("T,H_", [(1, 64), (8, 2048), (3, 1536), (5, 100), (2, 1), (2, 63), (7, 65), (3, 4104), (1300, 512),
+                                  (1300, 136), (1400, 1544),
                                   (2, 8200), (1, 16384), (300, 256), (2, 5001)])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("with_d,with_w", [(True, True), (False, False)])
