@@ -232,7 +232,7 @@ PlanArgs plan_args(const e0_kv_state* k, int32_t* ctx_out, int32_t* free_out, ui
 // A run is the consecutive new tokens of one block of the cache; for a run, a head and
 // keys or values the kernel finds the largest magnitude, settles the scale, rounds
 // the older codes again if the scale grew, and writes the new ones.  A thread block
-// finds the runs that begin among `per` tokens; it takes each with all its warps,
+// finds the runs that begin among its `per` tokens; it takes each with all its warps,
 // or, where there are many (single tokens), one with each warp.  A few tokens a warp
 // stay in registers between the maximum and the codes, so a run of up to 64 tokens
 // (32 of D = 256) is read once.  Scales are powers of two: x / s and code * old / new are then
@@ -356,21 +356,22 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
         n += out ? __ffs(out) - 1 : 32;
         if (out) break;
     }
+    // batches of HOLD tokens a member; a longer run is read again for its codes
+    const bool once = n <= HOLD * TEAM;
+    const auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (i0 + member + k * TEAM < n) held[k].load(x + (size_t)(i0 + member + k * TEAM) * ld, vec);
+    };
+    if (TEAM == 1 && n > 1) load(0);
     // largest magnitude as bits: of the values, and of those that are finite
     uint32_t all = 0, m = 0;
-    if constexpr (TEAM == 1) {
-#pragma unroll
-        for (int k = 1; k < HOLD; ++k)
-            if (k < n) held[k].load(x + (size_t)k * ld, vec);
-    }
-#pragma unroll
-    for (int k = 0; k < HOLD; ++k)
-        if (member + k * TEAM < n) all = held[k].max_bits(all);
 #pragma unroll 1
-    for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
-        AppRaw<TY, D> r;
-        r.load(x + (size_t)i * ld, vec);
-        all = r.max_bits(all);
+    for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (i0 + member + k * TEAM < n) all = held[k].max_bits(all);
     }
     all = __reduce_max_sync(0xffffffffu, AppRaw<TY, D>::fp32_bits(all));
     const bool plain = all < 0x7F800000u;  // what this warp has is finite
@@ -378,7 +379,10 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
         m = all;
     } else {
         if (lane == 0) set_status(A.st, E0_ST_NONFINITE);
-        const auto look = [&](const AppRaw<TY, D>& r) {
+#pragma unroll 1
+        for (int i = member; i < n; i += TEAM) {
+            AppRaw<TY, D> r;
+            r.load(x + (size_t)i * ld, vec);
             float v[N];
             r.get(v);
 #pragma unroll
@@ -386,15 +390,6 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
                 const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
                 m = max(m, a < 0x7F800000u ? a : 0u);
             }
-        };
-#pragma unroll
-        for (int k = 0; k < HOLD; ++k)
-            if (member + k * TEAM < n) look(held[k]);
-#pragma unroll 1
-        for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
-            AppRaw<TY, D> r;
-            r.load(x + (size_t)i * ld, vec);
-            look(r);
         }
         m = __reduce_max_sync(0xffffffffu, m);
     }
@@ -453,18 +448,16 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
         else
             *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
     };
-#pragma unroll
-    for (int k = 0; k < HOLD; ++k)
-        if (member + k * TEAM < n) write(member + k * TEAM, held[k]);
 #pragma unroll 1
-    for (int i = member + HOLD * TEAM; i < n; i += TEAM) {
-        AppRaw<TY, D> r;
-        r.load(x + (size_t)i * ld, vec);
-        write(i, r);
+    for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
+        if (!once) load(i0);
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            if (i0 + member + k * TEAM < n) write(i0 + member + k * TEAM, held[k]);
     }
 }
 
-// per: 8 or 16 (the smallest block: two runs of a prompt can begin among as many tokens).
+// per: tokens that a thread block looks for runs among, at most 32.
 template <int TY, int D>
 __global__ void __launch_bounds__(APP_WARPS * 32, 4) k_kv_append(AppendArgs A, bool vec, int per) {
     __shared__ uint32_t most[APP_WARPS];
@@ -492,8 +485,11 @@ int append_launch(const AppendArgs& a, cudaStream_t s) {
     const int sz = type_size(TY);
     const uintptr_t need = D / 32 * sz < 16 ? D / 32 * sz : 16;
     const uintptr_t bits = (uintptr_t)a.x[0] | (uintptr_t)a.x[1] | (uintptr_t)(a.ld[0] * sz) | (uintptr_t)(a.ld[1] * sz);
-    // 8 tokens a thread block where 16 would leave SMs without one
-    const int per = (long long)a.T * 2 * a.Hkv >= 16LL * 4 * num_sms() ? 16 : 8;
+    // at most one run of a prompt a thread block (two wait for one another; thread blocks that find none cost
+    // as much as they take from the others: 8 heads, blocks of 128, 8000 tokens: 32 us
+    // with 16 tokens each, 27 with 32); 8 where more would leave SMs without one
+    const int most = a.shift > 5 ? 32 : 16;
+    const int per = (long long)a.T * 2 * a.Hkv >= 4LL * most * num_sms() ? most : 8;
     k_kv_append<TY, D><<<dim3((a.T + per - 1) / per, 2 * a.Hkv), APP_WARPS * 32, 0, s>>>(a, !(bits & (need - 1)), per);
     return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
