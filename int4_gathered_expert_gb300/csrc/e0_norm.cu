@@ -132,48 +132,59 @@ E0_DEV float max_abs(float a, float b) {
 }
 
 // A chunk's outputs; all lanes of a warp call it.  Returns whether its group holds a
-// value that is not finite.  rcp.approx and the product with 1 / 448 are an ulp
-// off the divisions, of no account beside the scale's own rounding.
+// value that is not finite.
+// h / c = 448 t / max|t| whatever the root is, so the codes come from t = s * w (times
+// the root's power of two, exact, which keeps t in h's range): their argument has two
+// or three roundings, and a code next to a rounding border hardly ever depends on the
+// order of the sum of squares.
 template <int TY, bool VEC>
 E0_DEV bool finish_chunk(const NormArgs& A, size_t row, int e, float rstd, float (&v)[8]) {
     typedef typename Elem<TY>::T T;
     const int H = A.H;
-    float w[8];
+    const uint32_t bits = __float_as_uint(rstd);
+    const float pow2 = rstd != rstd ? rstd : __uint_as_float(bits & 0x7F800000u);
+    const float rest = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);  // rstd = pow2 * rest
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = rstd;
+    for (int i = 0; i < 8; ++i) v[i] *= pow2;
     if (A.w) {
         if constexpr (VEC) {
             if (e < H) {
                 const float4 f = __ldg(reinterpret_cast<const float4*>(A.w + e)), g = __ldg(reinterpret_cast<const float4*>(A.w + e) + 1);
                 const float u[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= rstd, w[i] = u[i];
+                for (int i = 0; i < 8; ++i) v[i] *= u[i];
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (e + i < H) v[i] *= rstd, w[i] = __ldg(A.w + e + i);
+                if (e + i < H) v[i] *= __ldg(A.w + e + i);
         }
     }
+    if (A.h) {
+        float h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = v[i] * rest;
+        store_chunk<TY, VEC>(reinterpret_cast<T*>(A.h) + row * H, e, H, h);
+    }
+    if (!A.q) return false;
     float mx = 0.f;  // NaN where a value is
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] *= w[i];
+    for (int i = 0; i < 8; ++i)
         if (VEC || e + i < H) mx = max_abs(mx, v[i]);
-    }
-    if (A.h) store_chunk<TY, VEC>(reinterpret_cast<T*>(A.h) + row * H, e, H, v);
-    if (!A.q) return false;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) mx = max_abs(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mx = fabsf(mx);
-    const bool bad = !(mx < INFINITY) && e < H;
-    const bool zero = bad || mx < 7.7037198e-34f;  // 2^-110: 448 / mx and mx / 448 stay normal numbers
-    float inv;
+    const float most = mx * rest;  // max|h|
+    const bool bad = !(most < INFINITY) && e < H;
+    const bool zero = bad || most < 7.7037198e-34f;  // 2^-110: 448 / mx and most / 448 stay normal numbers
+    // 448 / mx: an approximate inverse and one step on the remainder
+    float inv, scale;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(mx));
-    inv = zero ? 0.f : 448.f * inv;
+    scale = 448.f * inv;
+    scale = fmaf(fmaf(-mx, scale, 448.f), inv, scale);
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * scale, v[2 * i + 1] * scale);
     if (zero) c[0] = c[1] = c[2] = c[3] = 0;
     uint8_t* q = A.q + row * H;
     if constexpr (VEC) {
@@ -184,7 +195,7 @@ E0_DEV bool finish_chunk(const NormArgs& A, size_t row, int e, float rstd, float
             if (e + i < H) q[e + i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
     }
     if ((threadIdx.x & 7) == 0 && e < H)
-        A.qs[row * ((H + GROUP - 1) / GROUP) + e / GROUP] = zero ? 0.f : mx * (1.f / 448.f);
+        A.qs[row * ((H + GROUP - 1) / GROUP) + e / GROUP] = zero ? 0.f : most * (1.f / 448.f);
     return bad;
 }
 
