@@ -102,7 +102,7 @@ enum { E0_ROUTE_SOFTMAX_TOPK = 0, E0_ROUTE_SIGMOID_GROUP = 1 };
 
 /* Limits of the kernels (E0_ERR_UNSUPPORTED beyond them). */
 enum { E0_MAX_E = 1024, E0_MAX_K = 32, E0_MAX_T_DECODE = 64, E0_MAX_LORA_RANK = 64 };
-enum { E0_MAX_NORM_H = 16384, E0_MAX_SEQS = 4096, E0_MAX_CONTEXT = 1 << 30,
+enum { E0_MAX_NORM_H = 16384, E0_MAX_ROWS = 1 << 30, E0_MAX_SEQS = 4096, E0_MAX_CONTEXT = 1 << 30,
        E0_MAX_T_LINEAR = 524280, E0_MAX_N_LINEAR = 1 << 28, E0_MAX_K_LINEAR = 1 << 20 };
 
 /* ---- element types of the calls that take one -------------------------
@@ -464,17 +464,18 @@ int e0_moe_prefill_forward(const uint16_t* X, int T, const e0_slot_pool* bank,
  *     h = s / sqrt(mean(s^2) + eps) * w            (w NULL: no weight)
  *     c = max|h| / 448 over each group of 64 values (the last may be short)
  *     q = e4m3(h / c)              nearest, ties to even; h ~ c * q
- * r, d: dtype (E0_F32, E0_F16 or E0_BF16) with rows r_ld / d_ld elements apart;
- * w fp32 [H].  Outputs, each NULL or contiguous: r_out dtype [T][H] receives
- * s, h dtype [T][H], q [T][H] with q_scale fp32 [T][ceil(H/64)] (both or
- * neither).  r_out may be r or d where their rows are contiguous; other
+ * r, d: dtype (E0_F32, E0_F16 or E0_BF16) with rows r_ld / d_ld elements
+ * apart; w fp32 [H].  Outputs, each NULL or contiguous: r_out dtype [T][H]
+ * receives s, h dtype [T][H], q [T][H] with q_scale fp32 [T][ceil(H/64)] (both
+ * or neither).  r_out may be r or d where their rows are contiguous; other
  * overlaps are not allowed.  Sums are fp32.  A NaN or infinity in h is kept in
  * the output h; in q its whole group is written as zeros with scale 0 and
  * E0_ST_NONFINITE is raised.  A group whose largest magnitude is below 2^-110
  * is written as zeros with scale 0.  Errors: no r, no output, or one of q and
  * q_scale alone -> E0_ERR_NULL; another dtype, a row stride below H, eps < 0,
- * h equal to r, d or r_out, r_out over rows that are not contiguous, or a pointer that its element type does not align ->
- * E0_ERR_ARG; H > E0_MAX_NORM_H -> E0_ERR_UNSUPPORTED. */
+ * h equal to r, d or r_out, r_out over rows that are not contiguous, or a
+ * pointer that its element type does not align -> E0_ERR_ARG; H >
+ * E0_MAX_NORM_H, T > E0_MAX_ROWS -> E0_ERR_UNSUPPORTED. */
 int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, int dtype, float eps,
                   int64_t r_ld, int64_t d_ld, void* r_out, void* h, uint8_t* q, float* q_scale,
                   uint32_t* d_status, e0_stream_t stream);
@@ -485,16 +486,15 @@ int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, in
 size_t e0_linear_bytes(int N, int K);
 
 /* Lay out a canonical Q-tensor ([N] rows of K inputs) for e0_linear_forward:
- * for each block of 16 rows and each group of 64 inputs one record of 576 bytes,
- * [row block / 8][group][row block % 8], filled up with zero rows to a
- * multiple of 128: 512 bytes of
- * codes, 16 for each of 32 lanes, then 8 (scale, bias) fp16 pairs of the rows
- * i and i + 8, i = 0..7.  Lane l holds rows l/4 and l/4 + 8 and the inputs
- * 16*(l%4) .. + 15; its word i holds the inputs 4i..4i+3 of those, nibbles
- * 0, 4 = row l/4 inputs 0, 1; 1, 5 = row l/4 + 8 inputs 0, 1; 2, 6 and 3, 7
- * the same for inputs 2, 3.  src is a host descriptor of device pointers, dst
- * device memory of e0_linear_bytes(N, K) bytes, 16-byte aligned.
- * Asynchronous. */
+ * for each block of 16 rows and each group of 64 inputs one record of 576
+ * bytes, [row block / 8][group][row block % 8], filled up with zero rows to a
+ * multiple of 128: 512 bytes of codes, 16 for each of 32 lanes, then 8 (scale,
+ * bias) fp16 pairs of the rows i and i + 8, i = 0..7.  Lane l holds rows l/4
+ * and l/4 + 8 and the inputs 16*(l%4) .. + 15; its word i holds the inputs
+ * 4i..4i+3 of those, nibbles 0, 4 = row l/4 inputs 0, 1; 1, 5 = row l/4 + 8
+ * inputs 0, 1; 2, 6 and 3, 7 the same for inputs 2, 3.  src is a host
+ * descriptor of device pointers, dst device memory of e0_linear_bytes(N, K)
+ * bytes, 16-byte aligned. Asynchronous. */
 int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_t stream);
 
 /* y[t][n] = sum_k w[n][k] x[t][k] (+ add[t][n]) for T rows, w in the layout of
@@ -506,12 +506,13 @@ int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_
  * sums are fp32 in an order that only the sizes decide, so equal calls give
  * equal bits.  A row of x that holds a NaN or infinity gives a row of y that
  * is not finite; other rows are not touched by it.  Any T: the weights are
- * read once for every 8 to 32 rows, so the call is made for decode batches, not
- * for long prompts (T, N or K beyond E0_MAX_*_LINEAR -> E0_ERR_UNSUPPORTED).
- * y must not overlap x.  Errors: a NULL x, y or w, or no x_scale where x_type
- * wants one -> E0_ERR_NULL; sizes not positive, K no multiple of 64, an
- * unknown type, a row stride below the row, a w that is not 16-byte aligned,
- * or a pointer that its element type does not align -> E0_ERR_ARG. */
+ * read once for every 8 to 32 rows, so the call is made for decode batches,
+ * not for long prompts (T, N or K beyond E0_MAX_*_LINEAR ->
+ * E0_ERR_UNSUPPORTED). y must not overlap x.  Errors: a NULL x, y or w, or no
+ * x_scale where x_type wants one -> E0_ERR_NULL; sizes not positive, K no
+ * multiple of 64, an unknown type, a row stride below the row, a w that is not
+ * 16-byte aligned, or a pointer that its element type does not align ->
+ * E0_ERR_ARG. */
 int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type, int64_t x_ld,
                       const float* x_scale, int T, const void* add, int64_t add_ld, void* y, int y_type,
                       int64_t y_ld, e0_stream_t stream);
@@ -541,54 +542,60 @@ typedef struct e0_kv_state {
     int32_t B, max_blocks, block_tokens, n_blocks;
 } e0_kv_state;
 
-/* Make room for new_len[b] (device, >= 0) more tokens of each sequence, and say
- * where they go.  With held_b = ceil(ctx_len[b] / block_tokens), a sequence
- * takes ceil((ctx_len[b] + new_len[b]) / block_tokens) - held_b blocks from the
- * top of the free stack, sequences in order; their ids are appended to its row of
- * the block table.  Outputs (device): cu_q [B+1] the prefix sums of new_len;
- * for the new token t of sequence b, in order of sequence and position:
- * positions[t] = ctx_len[b] + t - cu_q[b], seq_ids[t] = b and slots[t] = block id *
- * block_tokens + position % block_tokens; for t in [cu_q[B], T_cap) all three are -1.
- * positions and seq_ids may be NULL.  ctx_out [B] and free_out [1] receive the new
- * lengths and stack height; they may be state->ctx_len and state->free_count
- * themselves (one more launch where T_cap > 4096).  All or nothing: where a length
- * is negative or the sequence no longer fits max_blocks (E0_ST_BAD_LENGTH), or more
- * than T_cap tokens or than the free blocks are wanted (E0_ST_POOL_FULL), the table
- * stays as it was, ctx_out and free_out receive the old values, cu_q zeros and
- * slots, positions and seq_ids -1.  An id on the free stack or in the table outside
- * [0, n_blocks) raises E0_ST_BAD_BLOCK and its tokens get slot -1.  Errors: NULL
- * pointers -> E0_ERR_NULL; sizes not positive (B = 0 and T_cap = 0 are allowed),
- * another block_tokens -> E0_ERR_ARG; B > E0_MAX_SEQS, max_blocks * block_tokens >
- * E0_MAX_CONTEXT -> E0_ERR_UNSUPPORTED. */
+/* Make room for new_len[b] (device, >= 0) more tokens of each sequence, and
+ * say where they go.  With held_b = ceil(ctx_len[b] / block_tokens), a
+ * sequence takes ceil((ctx_len[b] + new_len[b]) / block_tokens) - held_b
+ * blocks from the top of the free stack, sequences in order; their ids are
+ * appended to its row of the block table.  Outputs (device): cu_q [B+1] the
+ * prefix sums of new_len; for the new token t of sequence b, in order of
+ * sequence and position: positions[t] = ctx_len[b] + t - cu_q[b], seq_ids[t] =
+ * b and slots[t] = block id * block_tokens + position % block_tokens; for t in
+ * [cu_q[B], T_cap) all three are -1. positions and seq_ids may be NULL.
+ * ctx_out [B] and free_out [1] receive the new lengths and stack height; they
+ * may be state->ctx_len and state->free_count themselves (one more launch
+ * where T_cap > 4096).  All or nothing: where a length is negative or the
+ * sequence no longer fits max_blocks (E0_ST_BAD_LENGTH), or more than T_cap
+ * tokens or than the free blocks are wanted (E0_ST_POOL_FULL), the table stays
+ * as it was, ctx_out and free_out receive the old values, cu_q zeros and
+ * slots, positions and seq_ids -1.  An id on the free stack or in the table
+ * outside [0, n_blocks) raises E0_ST_BAD_BLOCK and its tokens get slot -1.
+ * Errors: NULL pointers -> E0_ERR_NULL; sizes not positive (B = 0 and T_cap =
+ * 0 are allowed), another block_tokens -> E0_ERR_ARG; B > E0_MAX_SEQS,
+ * max_blocks * block_tokens > E0_MAX_CONTEXT, T_cap or n_blocks > E0_MAX_ROWS
+ * -> E0_ERR_UNSUPPORTED. */
 int e0_kv_plan(const e0_kv_state* state, const int32_t* new_len, int T_cap, int32_t* ctx_out,
                int32_t* free_out, int32_t* cu_q, int64_t* slots, int32_t* positions, int32_t* seq_ids,
                uint32_t* d_status, e0_stream_t stream);
 
-/* Give back the blocks of every sequence b with mask[b] != 0 (device bytes): its
- * block ids go onto the free stack, sequences in order, its row of the table
- * becomes -1 and its length 0.  A block belongs to one sequence: blocks that
- * several rows name are not counted.  ctx_out / free_out as for e0_kv_plan.  A length
- * that does not fit max_blocks, or a stack that would grow beyond n_blocks, raises
- * E0_ST_BAD_LENGTH and nothing is given back.  Errors as e0_kv_plan. */
+/* Give back the blocks of every sequence b with mask[b] != 0 (device bytes):
+ * its block ids go onto the free stack, sequences in order, its row of the
+ * table becomes -1 and its length 0.  A block belongs to one sequence: blocks
+ * that several rows name are not counted.  ctx_out / free_out as for
+ * e0_kv_plan.  A length that does not fit max_blocks, or a stack that would
+ * grow beyond n_blocks, raises E0_ST_BAD_LENGTH and nothing is given back.
+ * Errors as e0_kv_plan. */
 int e0_kv_release(const e0_kv_state* state, const uint8_t* mask, int32_t* ctx_out, int32_t* free_out,
                   uint32_t* d_status, e0_stream_t stream);
 
 /* Write T tokens' keys and values into the cache.  k and v: dtype (E0_F32,
  * E0_F16 or E0_BF16), token t's heads at k + t * k_ld elements, [Hkv][D]
  * contiguous there (so both may lie inside the rows of one projection).
- * slots[t] as e0_kv_plan writes them; a negative slot is skipped, one beyond the
- * cache raises E0_ST_BAD_BLOCK and is skipped.  For each block and head the scale
- * is the smallest power of two s >= 2^-100 with max|x| <= 448 s over the tokens
- * that the block holds (max|x| / 448 rounded to fp32 first); codes are e4m3(x / s),
- * nearest, ties to even.  A call that writes a block's first token starts the
- * block anew.  A call that adds tokens to a block keeps its scale where it is
- * large enough; otherwise the scale grows and the codes of the tokens before the
- * new ones are rounded again to the new scale.  A NaN or infinity is written as 0
- * and raises E0_ST_NONFINITE.  Tokens of one block must be consecutive, with
- * consecutive slots, and a call may name a slot once: otherwise what their block holds is not
- * specified (every access stays inside it).  Errors: NULL pointers ->
+ * slots[t] as e0_kv_plan writes them; a negative slot is skipped, one beyond
+ * the cache raises E0_ST_BAD_BLOCK and is skipped.  For each block and head
+ * the scale is the smallest power of two s >= 2^-100 with max|x| <= 448 s over
+ * the tokens that the block holds (max|x| / 448 rounded to fp32 first); codes
+ * are e4m3(x / s), nearest, ties to even.  A call that writes a block's first
+ * token starts the block anew.  A call that adds tokens to a block keeps its
+ * scale where it is large enough; otherwise the scale grows and the codes of
+ * the tokens before the new ones are rounded again to the new scale (what
+ * stands behind them is not touched: a sequence that was cut back ends with
+ * the new tokens).  A NaN or infinity is written as 0 and raises
+ * E0_ST_NONFINITE.  Tokens of one block must be consecutive, with consecutive
+ * slots, and a call may name a slot once: otherwise what their block holds is
+ * not specified (every access stays inside it).  Errors: NULL pointers ->
  * E0_ERR_NULL; bad sizes, types, strides or alignment -> E0_ERR_ARG; a D or
- * block_tokens other than the cache's list -> E0_ERR_UNSUPPORTED. */
+ * block_tokens other than the cache's list, T > E0_MAX_ROWS ->
+ * E0_ERR_UNSUPPORTED. */
 int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dtype, int64_t k_ld, int64_t v_ld,
                  const int64_t* slots, int T, uint32_t* d_status, e0_stream_t stream);
 
@@ -597,27 +604,31 @@ int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dty
 size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
 
 /* Attention of the new tokens of B sequences over their cached tokens, the new
- * ones included (append them first).  Sequence b has ctx_len[b] cached tokens, its
- * queries are the rows cu_q[b] .. cu_q[b+1]-1 of q (cu_q NULL: one each), at most
- * max_q; its i-th query stands at position p = ctx_len[b] - n_b + i and sees the
- * positions j <= p, with window > 0 only j > p - window.  For query head g and
- * its KV head g / (Hq / Hkv):
+ * ones included (append them first).  Sequence b has ctx_len[b] cached tokens,
+ * its queries are the rows cu_q[b] .. cu_q[b+1]-1 of q (cu_q NULL: one each),
+ * at most max_q; its i-th query stands at position p = ctx_len[b] - n_b + i
+ * and sees the positions j <= p, with window > 0 only j > p - window.  For
+ * query head g and its KV head g / (Hq / Hkv):
  *     out = sum_j softmax_j(scale q.k_j) v_j,   lse = ln sum_j exp(scale q.k_j)
- * q, out: dtype (E0_F32, E0_F16 or E0_BF16), rows q_ld / out_ld elements apart,
- * [Hq][D] contiguous; lse fp32 [rows][Hq] or NULL.  block_table [B][max_blocks].
- * A query that sees nothing gets out = 0 and lse = -infinity.  Rows from cu_q[B]
- * on are left as they were.  Statistics and sums are fp32.  A ctx_len that is
- * negative or needs more than max_blocks blocks raises E0_ST_BAD_LENGTH and its
- * queries see nothing; a cu_q that is negative, falls or gives more than max_q
- * queries raises it too and that sequence's rows are left as they were; so does a
- * call whose (query tile, KV head, 64 positions) are more than 2^31, and writes nothing.  A block id out of range raises E0_ST_BAD_BLOCK and its tokens are
- * not seen.  A scale of values below 2^-100 counts as 2^-100.  The result does not depend on how blocks are laid out in the pool, and equal calls
- * give equal bits.  Any max_q; the call is made for decode steps and short
- * runs of tokens (every 8 query rows of a KV head read the sequence once more).  Errors: NULL
- * pointers -> E0_ERR_NULL; sizes not positive, Hq no multiple of Hkv,
- * window < 0, a short workspace, bad types, strides or alignment (q and its rows 16 bytes),
- * max_q other than 1 without cu_q -> E0_ERR_ARG; D or block_tokens outside the cache's list, B > E0_MAX_SEQS,
- * max_blocks * block_tokens > E0_MAX_CONTEXT -> E0_ERR_UNSUPPORTED. */
+ * q, out: dtype (E0_F32, E0_F16 or E0_BF16), rows q_ld / out_ld elements
+ * apart, [Hq][D] contiguous; lse fp32 [rows][Hq] or NULL.  block_table
+ * [B][max_blocks]. A query that sees nothing gets out = 0 and lse = -infinity.
+ * Rows from cu_q[B] on are left as they were.  Statistics and sums are fp32.
+ * A ctx_len that is negative or needs more than max_blocks blocks raises
+ * E0_ST_BAD_LENGTH and its queries see nothing; a cu_q that is negative, falls
+ * or gives more than max_q queries raises it too and that sequence's rows are
+ * left as they were; a call of more than 2^31 pieces of work (query tile, KV
+ * head, 64 positions) raises it and writes nothing.  A block id out of range
+ * raises E0_ST_BAD_BLOCK and its tokens are not seen.  A scale of values below
+ * 2^-100 counts as 2^-100.  The result does not depend on how blocks are laid
+ * out in the pool, and equal calls give equal bits.  Any max_q; the call is
+ * made for decode steps and short runs of tokens (every 8 query rows of a KV
+ * head, or 16 with bf16, read the sequence once more).  Errors: NULL pointers
+ * -> E0_ERR_NULL; sizes not positive, Hq no multiple of Hkv, window < 0, a
+ * short workspace, bad types, strides or alignment (q and its rows 16 bytes),
+ * max_q other than 1 without cu_q -> E0_ERR_ARG; D or block_tokens outside the
+ * cache's list, B > E0_MAX_SEQS, max_blocks * block_tokens > E0_MAX_CONTEXT ->
+ * E0_ERR_UNSUPPORTED. */
 int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
                    const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq,
                    float scale, int window, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,

@@ -76,7 +76,8 @@ int check_kv_cache(const e0_kv_cache* c) {
 int check_kv_state(const e0_kv_state* s, const int32_t* ctx_out, const int32_t* free_out) {
     if (!s) return E0_ERR_NULL;
     if (s->B < 0 || s->max_blocks < 1 || s->n_blocks < 1 || !block_tokens_ok(s->block_tokens)) return E0_ERR_ARG;
-    if (s->B > E0_MAX_SEQS || !positions_ok(s->max_blocks, s->block_tokens)) return E0_ERR_UNSUPPORTED;
+    if (s->B > E0_MAX_SEQS || s->n_blocks > E0_MAX_ROWS || !positions_ok(s->max_blocks, s->block_tokens))
+        return E0_ERR_UNSUPPORTED;
     if (!s->free_list || !s->free_count || !free_out) return E0_ERR_NULL;
     if (s->B > 0 && (!s->block_table || !s->ctx_len || !ctx_out)) return E0_ERR_NULL;
     if (!aligned(4, s->block_table, s->ctx_len, s->free_list, s->free_count, ctx_out, free_out)) return E0_ERR_ARG;
@@ -342,7 +343,7 @@ int e0_rmsnorm_q8(const void* r, const void* d, const float* w, int T, int H, in
                   int64_t d_ld, void* r_out, void* h, uint8_t* q, float* q_scale, uint32_t* d_status,
                   e0_stream_t stream) {
     if (T < 0 || H < 1 || !float_type(dtype) || !(eps >= 0.f)) return E0_ERR_ARG;
-    if (H > E0_MAX_NORM_H) return E0_ERR_UNSUPPORTED;
+    if (H > E0_MAX_NORM_H || T > E0_MAX_ROWS) return E0_ERR_UNSUPPORTED;
     if (T == 0) return E0_OK;
     if (!r || (!r_out && !h && !q) || (q == nullptr) != (q_scale == nullptr)) return E0_ERR_NULL;
     if (r_ld < H || (d && d_ld < H)) return E0_ERR_ARG;
@@ -387,6 +388,7 @@ int e0_kv_plan(const e0_kv_state* state, const int32_t* new_len, int T_cap, int3
     const int rc = check_kv_state(state, ctx_out, free_out);
     if (rc) return rc;
     if (T_cap < 0) return E0_ERR_ARG;
+    if (T_cap > E0_MAX_ROWS) return E0_ERR_UNSUPPORTED;
     if (!cu_q || (state->B > 0 && !new_len) || (T_cap > 0 && !slots)) return E0_ERR_NULL;
     if (!aligned(4, new_len, cu_q, positions, seq_ids) || !aligned(8, slots)) return E0_ERR_ARG;
     return e0::kv_plan(state, new_len, T_cap, ctx_out, free_out, cu_q, slots, positions, seq_ids, d_status, cs(stream));
@@ -405,6 +407,7 @@ int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dty
     const int rc = check_kv_cache(cache);
     if (rc) return rc;
     if (T < 0 || !float_type(dtype)) return E0_ERR_ARG;
+    if (T > E0_MAX_ROWS) return E0_ERR_UNSUPPORTED;
     if (T == 0) return E0_OK;
     if (!k || !v || !slots) return E0_ERR_NULL;
     const int64_t row = (int64_t)cache->Hkv * cache->D;

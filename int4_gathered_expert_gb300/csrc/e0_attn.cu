@@ -681,42 +681,42 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         const int rows = min(ROWS, cur.s.n * G - cur.tile * ROWS);
 #pragma unroll
         for (int half = 0; half < RW; ++half) {
-        if (half == 1) {
-            __syncthreads();  // the first rows have been read
-            put_out(1);
-            __syncthreads();
-        }
+            if (half == 1) {
+                __syncthreads();  // the first rows have been read
+                put_out(1);
+                __syncthreads();
+            }
 #pragma unroll 1
-        for (int r = 8 * half + warp; r < min(rows, 8 * half + 8); r += AT_WARPS) {
-            float m = S.m[0][r], l = 0.f, k[AT_WARPS];
+            for (int r = 8 * half + warp; r < min(rows, 8 * half + 8); r += AT_WARPS) {
+                float m = S.m[0][r], l = 0.f, k[AT_WARPS];
 #pragma unroll
-            for (int w = 1; w < AT_WARPS; ++w) m = fmaxf(m, S.m[w][r]);
-            const float base = m == -INFINITY ? 0.f : m;
+                for (int w = 1; w < AT_WARPS; ++w) m = fmaxf(m, S.m[w][r]);
+                const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int w = 0; w < AT_WARPS; ++w) {
-                k[w] = exp2_of(S.m[w][r] - base);
-                l += k[w] * S.l[w][r];
+                for (int w = 0; w < AT_WARPS; ++w) {
+                    k[w] = exp2_of(S.m[w][r] - base);
+                    l += k[w] * S.l[w][r];
+                }
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const int row = cur.tile * ROWS + r, head = cur.head * G + row % G;
+                const size_t tok = (size_t)cur.s.row0 + row / G;
+#pragma unroll
+                for (int d = lane; d < D; d += 32) {
+                    float o = 0.f;
+#pragma unroll
+                    for (int w = 0; w < AT_WARPS; ++w) o += k[w] * warp_out<D>(S, w, r & 7, d);
+                    if (whole)
+                        store_out<TY>(A, tok, head * D + d, o * inv);
+                    else
+                        A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
+                }
+                if (lane == 0) {
+                    if (!whole)
+                        A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
+                    else if (A.lse)
+                        A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
+                }
             }
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            const int row = cur.tile * ROWS + r, head = cur.head * G + row % G;
-            const size_t tok = (size_t)cur.s.row0 + row / G;
-#pragma unroll
-            for (int d = lane; d < D; d += 32) {
-                float o = 0.f;
-#pragma unroll
-                for (int w = 0; w < AT_WARPS; ++w) o += k[w] * warp_out<D>(S, w, r & 7, d);
-                if (whole)
-                    store_out<TY>(A, tok, head * D + d, o * inv);
-                else
-                    A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
-            }
-            if (lane == 0) {
-                if (!whole)
-                    A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
-                else if (A.lse)
-                    A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
-            }
-        }
         }
         if (!whole) {
             const int b0 = (int)((cur.first + plan.cost) / plan.share);

@@ -21,7 +21,7 @@ E0_ST_BAD_BLOCK, E0_ST_BAD_LENGTH = 64, 128
 E0_F32, E0_F16, E0_BF16, E0_E4M3 = 0, 1, 2, 3
 E0_ROUTE_SOFTMAX_TOPK, E0_ROUTE_SIGMOID_GROUP = 0, 1
 E0_MAX_E, E0_MAX_K, E0_MAX_T_DECODE, E0_MAX_LORA_RANK = 1024, 32, 64, 64
-E0_MAX_NORM_H, E0_MAX_SEQS, E0_MAX_CONTEXT = 16384, 4096, 1 << 30
+E0_MAX_NORM_H, E0_MAX_ROWS, E0_MAX_SEQS, E0_MAX_CONTEXT = 16384, 1 << 30, 4096, 1 << 30
 E0_MAX_T_LINEAR, E0_MAX_N_LINEAR, E0_MAX_K_LINEAR = 524280, 1 << 28, 1 << 20
 
 vp = C.c_void_p

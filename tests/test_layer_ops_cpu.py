@@ -35,7 +35,8 @@ NORM = dict(r=P, d=None, w=None, T=1, H=64, dtype=0, eps=1e-6, r_ld=64, d_ld=0, 
 
 @pytest.mark.parametrize("change,code", [
     (dict(T=-1), "ARG"), (dict(H=0), "ARG"), (dict(dtype=3), "ARG"), (dict(dtype=-1), "ARG"), (dict(eps=-1.0), "ARG"),
-    (dict(eps=float("nan")), "ARG"), (dict(H=16385, r_ld=16385), "UNSUPPORTED"), (dict(r=None), "NULL"),
+    (dict(eps=float("nan")), "ARG"), (dict(H=16385, r_ld=16385), "UNSUPPORTED"), (dict(T=(1 << 30) + 1), "UNSUPPORTED"),
+    (dict(r=None), "NULL"),
     (dict(h=None), "NULL"), (dict(q=P), "NULL"), (dict(q_scale=P), "NULL"), (dict(r_ld=63), "ARG"),
     (dict(d=3 * P, d_ld=63), "ARG"), (dict(r=P + 2), "ARG"), (dict(dtype=1, r=P + 1), "ARG"), (dict(w=P + 2), "ARG"),
     (dict(h=P), "ARG"), (dict(d=2 * P, d_ld=64), "ARG"), (dict(r_out=2 * P), "ARG"),
@@ -55,7 +56,8 @@ LIN = dict(w=P, N=64, K=128, x=P, x_type=0, x_ld=128, x_scale=None, T=1, add=Non
     (dict(x_type=3), "NULL"), (dict(x_ld=127), "ARG"), (dict(y_ld=63), "ARG"), (dict(add=P, add_ld=63), "ARG"),
     (dict(w=P + 8), "ARG"), (dict(x=P + 2), "ARG"), (dict(y=P + 2), "ARG"), (dict(add=2 * P, add_ld=65), "ARG"),
     (dict(x_type=3, x_scale=P + 1), "ARG"), (dict(T=524281), "UNSUPPORTED"),
-    (dict(K=(1 << 20) + 64, x_ld=1 << 21), "UNSUPPORTED"), (dict(N=(1 << 28) + 1, y_ld=1 << 29), "UNSUPPORTED"), (dict(T=0, x=None), "OK")])
+    (dict(K=(1 << 20) + 64, x_ld=1 << 21), "UNSUPPORTED"), (dict(N=(1 << 28) + 1, y_ld=1 << 29), "UNSUPPORTED"),
+    (dict(T=0, x=None), "OK")])
 def test_linear_refusals(L, change, code):
     want = L.E0_OK if code == "OK" else getattr(L, "E0_ERR_" + code)
     assert call(L.e0_linear_forward, LIN, **change) == want
@@ -88,7 +90,8 @@ def state(L, **c):
 @pytest.mark.parametrize("change,code", [
     (dict(B=-1), "ARG"), (dict(max_blocks=0), "ARG"), (dict(n_blocks=0), "ARG"), (dict(block_tokens=8), "ARG"),
     (dict(block_tokens=48), "ARG"), (dict(B=4097), "UNSUPPORTED"), (dict(block_table=None), "NULL"),
-    (dict(max_blocks=(1 << 26) + 1), "UNSUPPORTED"), (dict(ctx_len=None), "NULL"), (dict(free_list=None), "NULL"), (dict(free_count=None), "NULL"),
+    (dict(max_blocks=(1 << 26) + 1), "UNSUPPORTED"), (dict(n_blocks=(1 << 30) + 1), "UNSUPPORTED"),
+    (dict(ctx_len=None), "NULL"), (dict(free_list=None), "NULL"), (dict(free_count=None), "NULL"),
     (dict(ctx_len=P + 2), "ARG")])
 def test_plan_and_release_refuse_a_bad_state(L, change, code):
     s = state(L, **change)
@@ -101,6 +104,7 @@ def test_plan_and_release_refusals(L):
     s = state(L)
     no = dict(stream=0, raise_on_error=False)
     assert L.e0_kv_plan(s, P, -1, P, P, P, P, **no) == L.E0_ERR_ARG
+    assert L.e0_kv_plan(s, P, (1 << 30) + 1, P, P, P, P, **no) == L.E0_ERR_UNSUPPORTED
     assert L.e0_kv_plan(s, None, 4, P, P, P, P, **no) == L.E0_ERR_NULL
     assert L.e0_kv_plan(s, P, 4, None, P, P, P, **no) == L.E0_ERR_NULL
     assert L.e0_kv_plan(s, P, 4, P, None, P, P, **no) == L.E0_ERR_NULL
@@ -121,7 +125,8 @@ def cache(L, **c):
 
 @pytest.mark.parametrize("change,code", [
     (dict(k=None), "NULL"), (dict(v_scale=None), "NULL"), (dict(n_blocks=0), "ARG"), (dict(Hkv=0), "ARG"),
-    (dict(Hkv=32768), "UNSUPPORTED"), (dict(block_tokens=24), "UNSUPPORTED"), (dict(D=96), "UNSUPPORTED"), (dict(D=512), "UNSUPPORTED"),
+    (dict(Hkv=32768), "UNSUPPORTED"), (dict(block_tokens=24), "UNSUPPORTED"), (dict(D=96), "UNSUPPORTED"),
+    (dict(D=512), "UNSUPPORTED"),
     (dict(v=P + 8), "ARG"), (dict(k_scale=P + 2), "ARG")])
 def test_append_and_attention_refuse_a_bad_cache(L, change, code):
     c = cache(L, **change)
@@ -136,7 +141,7 @@ APP = dict(k=P, v=P, dtype=0, k_ld=128, v_ld=128, slots=P, T=4)
 @pytest.mark.parametrize("change,code", [
     (dict(T=-1), "ARG"), (dict(dtype=3), "ARG"), (dict(k=None), "NULL"), (dict(v=None), "NULL"),
     (dict(slots=None), "NULL"), (dict(k_ld=127), "ARG"), (dict(v_ld=0), "ARG"), (dict(k=P + 2), "ARG"),
-    (dict(slots=P + 4), "ARG"), (dict(T=0, k=None), "OK")])
+    (dict(slots=P + 4), "ARG"), (dict(T=0, k=None), "OK"), (dict(T=(1 << 30) + 1), "UNSUPPORTED")])
 def test_append_refusals(L, change, code):
     want = L.E0_OK if code == "OK" else getattr(L, "E0_ERR_" + code)
     c = cache(L)
@@ -151,7 +156,8 @@ ATT = dict(cache=None, block_table=P, max_blocks=4, ctx_len=P, cu_q=P, B=2, max_
     (dict(B=-1), "ARG"), (dict(max_blocks=0), "ARG"), (dict(max_q=0), "ARG"), (dict(dtype=3), "ARG"),
     (dict(window=-1), "ARG"), (dict(Hq=3), "ARG"), (dict(Hq=1), "ARG"), (dict(scale=float("nan")), "ARG"),
     (dict(cu_q=None, max_q=2), "ARG"), (dict(B=4097), "UNSUPPORTED"), (dict(max_q=1 << 30), "UNSUPPORTED"),
-    (dict(max_blocks=(1 << 26) + 1), "UNSUPPORTED"), (dict(block_table=None), "NULL"), (dict(ctx_len=None), "NULL"), (dict(q=None), "NULL"), (dict(out=None), "NULL"),
+    (dict(max_blocks=(1 << 26) + 1), "UNSUPPORTED"), (dict(block_table=None), "NULL"), (dict(ctx_len=None), "NULL"),
+    (dict(q=None), "NULL"), (dict(out=None), "NULL"),
     (dict(ws=None), "NULL"), (dict(q_ld=255), "ARG"), (dict(q_ld=257), "ARG"), (dict(out_ld=255), "ARG"),
     (dict(q=P + 8), "ARG"), (dict(out=P + 1), "ARG"), (dict(lse=P + 2), "ARG"), (dict(ws=P + 128), "ARG"),
     (dict(ws_bytes=1), "ARG"), (dict(B=0, q=None), "OK")])
