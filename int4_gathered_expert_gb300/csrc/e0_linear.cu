@@ -402,7 +402,7 @@ struct BatchSmem {
             uint8_t x[CHUNK][TOK * XROW];
             float sx[CHUNK][TOK], xs[CHUNK][TOK];
         };
-        float sums[ROWS * (TOK + 1)];  // at the end: over the tile, or the cluster's share of it
+        float sums[TOK][ROWS + 4];  // at the end: the block's own; 4 more so that what the lanes write has 32 banks
     };
 };
 
@@ -587,37 +587,35 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
         }
     }
     copy_wait<0>();
-    const int cols = min(A.T - tok0, TOK);
-    if (S == 1) {
-        constexpr int LD = TOK + 1;
-        __syncthreads();  // all warps are through: the sums stand where x and the records were
-#pragma unroll
-        for (int r = 0; r < RM; ++r)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float* o = M.sums + ((warp * RM + r) * 16 + gid) * LD + 8 * n + 2 * t4;
-                o[0] = tot[r][n][0], o[1] = tot[r][n][1], o[8 * LD] = tot[r][n][2], o[8 * LD + 1] = tot[r][n][3];
-            }
-        __syncthreads();
-        for (int e = tid; e < SM::ROWS * cols; e += LIN_WARPS * 32)
-            store_y(A, blockIdx.x * SM::ROWS + e % SM::ROWS, tok0 + e / SM::ROWS, M.sums[e % SM::ROWS * LD + e / SM::ROWS]);
-        return;
-    }
-    Spread sp(M.sums, SM::ROWS * TOK);
-    cg::this_cluster().sync();  // all warps of all blocks are through
+    __syncthreads();  // all warps are through: the sums stand where x and the records were
 #pragma unroll
     for (int r = 0; r < RM; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int e = (8 * n + 2 * t4) * SM::ROWS + (warp * RM + r) * 16 + gid;
-            sp.put(e, tot[r][n][0]), sp.put(e + SM::ROWS, tot[r][n][1]);
-            sp.put(e + 8, tot[r][n][2]), sp.put(e + SM::ROWS + 8, tot[r][n][3]);
+            float* o = &M.sums[8 * n + 2 * t4][(warp * RM + r) * 16 + gid];
+            o[0] = tot[r][n][0], o[SM::ROWS + 4] = tot[r][n][1], o[8] = tot[r][n][2], o[SM::ROWS + 12] = tot[r][n][3];
         }
-    cg::this_cluster().sync();  // all sums are where they belong
-    for (int i = tid; i < sp.share; i += LIN_WARPS * 32) {
-        const int e = rank * sp.share + i;
-        store_y(A, blockIdx.x * SM::ROWS + e % SM::ROWS, tok0 + e / SM::ROWS, sp.get(i));
+    if (S > 1) cg::this_cluster().sync(); else __syncthreads();
+    // every block finishes some of the tokens; four rows a thread
+    const int toks = TOK / S;
+    for (int i = tid; i < toks * SM::ROWS / 4; i += LIN_WARPS * 32) {
+        const int t = rank * toks + i / (SM::ROWS / 4), row = i % (SM::ROWS / 4) * 4;
+        if (tok0 + t >= A.T) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < S) {
+                const float* from = S > 1 ? cg::this_cluster().map_shared_rank(&M.sums[0][0], k) : &M.sums[0][0];
+                const float4 x = *reinterpret_cast<const float4*>(from + t * (SM::ROWS + 4) + row);
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+        const int n = blockIdx.x * SM::ROWS + row;
+        store_y(A, n, tok0 + t, v.x);
+        store_y(A, n + 1, tok0 + t, v.y);
+        store_y(A, n + 2, tok0 + t, v.z);
+        store_y(A, n + 3, tok0 + t, v.w);
     }
+    if (S > 1) cg::this_cluster().sync();  // a block's sums are read until here
 }
 
 // most: the most dynamic shared memory that any launch of the kernel wants.
