@@ -216,26 +216,6 @@ E0_DEV void add_group(float (&tot)[4], const float (&d)[4], float s0, float b0, 
     }
 }
 
-// The sums of the cluster's blocks (a power of two): element e of a block's n sums
-// belongs to block e / (n / S), and every block writes it there, [its rank][e % (n / S)].
-struct Spread {
-    float* to;  // this block's own [S][n / S]
-    int S, rank, share, bits;
-    E0_DEV Spread(float* buf, int n) : to(buf), S(gridDim.y), rank(blockIdx.y), share(n / S), bits(0) {
-        while ((1 << bits) < share) ++bits;
-    }
-    E0_DEV void put(int e, float v) const {
-        cg::this_cluster().map_shared_rank(to, e >> bits)[(rank << bits) + (e & (share - 1))] = v;
-    }
-    E0_DEV float get(int i) const {
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < S) v += to[(k << bits) + i];
-        return v;
-    }
-};
-
 // Up to 8 rows of x.  A tile is 16*RM rows of W; the blocks of a cluster share a
 // tile and split K, the warps of a block take the groups of its share in turn,
 // and a block goes through tiles blockIdx.x, + gridDim.x, ...  A warp's records
@@ -372,14 +352,18 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
             for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32)
                 store_y(A, tile * ROWS + e % ROWS, e / ROWS, sum(e % ROWS, e / ROWS));
         } else {  // one tile a cluster
-            Spread sp(part + LIN_WARPS * ROWS * LD, ROWS * 8);
-            cg::this_cluster().sync();  // all blocks run
-            for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32) sp.put(e, sum(e % ROWS, e / ROWS));
-            cg::this_cluster().sync();  // all sums are where they belong
-            for (int i = threadIdx.x; i < sp.share; i += LIN_WARPS * 32) {
-                const int e = rank * sp.share + i;
-                if (e < ROWS * A.T) store_y(A, tile * ROWS + e % ROWS, e / ROWS, sp.get(i));
+            float* sums = part + LIN_WARPS * ROWS * LD;  // [T][ROWS]
+            for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32) sums[e] = sum(e % ROWS, e / ROWS);
+            cg::this_cluster().sync();
+            // every block finishes a share
+            for (int e = threadIdx.x + rank * LIN_WARPS * 32; e < ROWS * A.T; e += S * LIN_WARPS * 32) {
+                float v = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < S) v += cg::this_cluster().map_shared_rank(sums, k)[e];
+                store_y(A, tile * ROWS + e % ROWS, e / ROWS, v);
             }
+            cg::this_cluster().sync();  // a block's sums are read until here
         }
     }
 }
