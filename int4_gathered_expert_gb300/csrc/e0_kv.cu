@@ -2,6 +2,8 @@
 // (e0_kv_plan, e0_kv_release) and writing keys and values (e0_kv_append).
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "e0_internal.h"
 #include "e0_types.cuh"
 
@@ -257,11 +259,11 @@ struct AppendArgs {
     int T, Hkv, shift, n_blocks;
 };
 
-E0_DEV float pow2_scale(float m) {  // smallest 2^e >= 2^-100 with m / 448 (rounded) <= 2^e
-    const uint32_t b = __float_as_uint(__fdiv_rn(m, 448.f));
-    uint32_t e = (b >> 23) + ((b & 0x7FFFFFu) != 0);
-    if (e < 27) e = 27;
-    return __uint_as_float(e << 23);
+// The smallest 2^e >= 2^-100 with m / 448 (rounded) <= 2^e, for the bits of a finite m >= 0:
+// 448 = 1.75 * 2^8, and the fp32 number after 1.75 * 2^k rounds to more than 2^(k - 8).
+E0_DEV float pow2_scale(uint32_t m) {
+    const int e = (int)(m >> 23) - 8 + ((m & 0x7FFFFFu) > 0x600000u);
+    return __int_as_float(max(e, 27) << 23);
 }
 
 // A lane's D / 32 elements of one token's head, as they are in memory.
@@ -269,6 +271,10 @@ template <int TY, int D>
 struct AppRaw {
     static constexpr int N = D / 32, WORDS = N * (TY == E0_F32 ? 4 : 2) / 4;
     uint32_t w[WORDS];
+    E0_DEV void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
     E0_DEV void load(const typename Elem<TY>::T* p, bool vec) {
         if (vec) {
             if constexpr (WORDS == 1) {
@@ -318,60 +324,74 @@ struct AppRaw {
     }
 };
 
-// The run that begins with token t0, by the calling warp (TEAM 1) or by all warps
+// Slots of the 64 tokens from `base`, two a lane; -1 behind the last one.
+struct Slots {
+    int64_t lo, hi;
+    E0_DEV void load(const AppendArgs& A, long long base, int lane) {
+        lo = base + lane < A.T ? A.slots[base + lane] : -1;
+        hi = base + 32 + lane < A.T ? A.slots[base + 32 + lane] : -1;
+    }
+};
+
+// The run that begins with token base + j, by the calling warp (TEAM 1) or by all warps
 // of the thread block together.
 template <int TY, int D, int TEAM>
-E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t0, uint32_t* most) {
+E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int base, int j, const Slots& near,
+                       uint32_t* most) {
     typedef typename Elem<TY>::T T;
     constexpr int N = D / 32, HOLD = D == 256 ? 4 : 8;
     const int lane = threadIdx.x & 31, member = TEAM == 1 ? 0 : threadIdx.x >> 5;
-    const int bs = 1 << A.shift;
-    const int64_t slot = A.slots[t0];
+    const int bs = 1 << A.shift, t0 = base + j;
+    const int64_t slot = __shfl_sync(0xffffffffu, near.lo, j);
     const int off = (int)(slot & (bs - 1));
     const int64_t blk = slot >> A.shift;
     if (blk >= A.n_blocks) {
         if (member == 0 && lane == 0) set_status(A.st, E0_ST_BAD_BLOCK);
         return;
     }
-    const int64_t ld = which ? A.ld[1] : A.ld[0];
-    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + t0 * ld + (size_t)head * D + lane * N;
     float* scale = (which ? A.scale[1] : A.scale[0]) + (size_t)blk * A.Hkv + head;
-    uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
     float old = off > 0 ? *scale : 0.f;
-    // member w has the tokens w, w + TEAM, ...  A team reads what the rest of the block
-    // would hold before it knows the run's length, a single warp the first only.
-    AppRaw<TY, D> held[HOLD];
-    if constexpr (TEAM > 1) {
-#pragma unroll
-        for (int k = 0; k < HOLD; ++k) held[k].load(x + (size_t)min(member + k * TEAM, A.T - 1 - t0) * ld, vec);
-    } else {
-        held[0].load(x, vec);
-    }
     // the run's length: tokens that follow with consecutive slots inside the block
-    int n = 0;
-    for (;;) {
-        const int i = n + lane;
-        const bool in = off + i < bs && t0 + i < A.T && A.slots[t0 + i] == slot + i;
-        const uint32_t out = ~__ballot_sync(0xffffffffu, in);
-        n += out ? __ffs(out) - 1 : 32;
-        if (out) break;
+    int n;
+    {
+        const int64_t first = slot - j + lane;
+        const uint64_t follow = (uint64_t)__ballot_sync(0xffffffffu, near.hi == first + 32) << 32 |
+                                __ballot_sync(0xffffffffu, near.lo == first);
+        n = __ffsll(~(follow >> j)) - 1;  // j = 0 and all 64: -1
+        if (n < 0) n = 64;
+        if (n == 64 - j)
+            for (;;) {
+                const int i = n + lane;
+                const bool in = off + i < bs && t0 + i < A.T && A.slots[t0 + i] == slot + i;
+                const uint32_t out = ~__ballot_sync(0xffffffffu, in);
+                n += out ? __ffs(out) - 1 : 32;
+                if (out) break;
+            }
+        n = min(n, bs - off);
     }
+    // member w has the tokens w, w + TEAM, ...
+    const int64_t ld = which ? A.ld[1] : A.ld[0];
+    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + (t0 + member) * ld + (size_t)head * D + lane * N;
+    uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
+    AppRaw<TY, D> held[HOLD];
     // batches of HOLD tokens a member; a longer run is read again for its codes
     const bool once = n <= HOLD * TEAM;
     const auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
-            if (i0 + member + k * TEAM < n) held[k].load(x + (size_t)(i0 + member + k * TEAM) * ld, vec);
+            if (i0 + member + k * TEAM < n)
+                held[k].load(x + (i0 + k * TEAM) * ld, vec);
+            else
+                held[k].zero();
     };
-    if (TEAM == 1 && n > 1) load(0);
+    load(0);
     // largest magnitude as bits: of the values, and of those that are finite
     uint32_t all = 0, m = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
         if (i0 > 0) load(i0);
 #pragma unroll
-        for (int k = 0; k < HOLD; ++k)
-            if (i0 + member + k * TEAM < n) all = held[k].max_bits(all);
+        for (int k = 0; k < HOLD; ++k) all = held[k].max_bits(all);
     }
     all = __reduce_max_sync(0xffffffffu, AppRaw<TY, D>::fp32_bits(all));
     const bool plain = all < 0x7F800000u;  // what this warp has is finite
@@ -380,9 +400,9 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
     } else {
         if (lane == 0) set_status(A.st, E0_ST_NONFINITE);
 #pragma unroll 1
-        for (int i = member; i < n; i += TEAM) {
+        for (int i = 0; i < n - member; i += TEAM) {
             AppRaw<TY, D> r;
-            r.load(x + (size_t)i * ld, vec);
+            r.load(x + i * ld, vec);
             float v[N];
             r.get(v);
 #pragma unroll
@@ -402,7 +422,7 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
     } else {
         __syncwarp();
     }
-    float s = pow2_scale(__uint_as_float(m));
+    float s = pow2_scale(m);
     if (off > 0) {
         if (!(old > 0.f && old < 3.0e38f)) old = s;  // nothing a call of ours wrote: the codes stay as they are
         s = fmaxf(s, old);
@@ -430,17 +450,17 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
     }
     if (member == 0 && lane == 0) *scale = s;
     const float inv = 1.f / s;  // a power of two
-    const auto write = [&](int i, const AppRaw<TY, D>& r) {
+    uint8_t* to = codes + (size_t)(off + member) * D + lane * N;
+    const auto write = [&](auto finite, uint8_t* p, const AppRaw<TY, D>& r) {
         float v[N];
         r.get(v);
         uint32_t c[(N + 3) / 4] = {};
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
             float a = v[j] * inv, b = v[j + 1] * inv;
-            if (!plain) a = fabsf(v[j]) < INFINITY ? a : 0.f, b = fabsf(v[j + 1]) < INFINITY ? b : 0.f;
+            if (!finite) a = fabsf(v[j]) < INFINITY ? a : 0.f, b = fabsf(v[j + 1]) < INFINITY ? b : 0.f;
             c[j / 4] |= e4m3x2(a, b) << (8 * (j & 2));
         }
-        uint8_t* p = codes + (size_t)(off + i) * D + lane * N;
         if constexpr (N == 2)
             *reinterpret_cast<uint16_t*>(p) = (uint16_t)c[0];
         else if constexpr (N == 4)
@@ -448,13 +468,16 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int t
         else
             *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
     };
+    const auto write_all = [&](auto finite) {
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
-        if (!once) load(i0);
+        for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
+            if (!once) load(i0);
 #pragma unroll
-        for (int k = 0; k < HOLD; ++k)
-            if (i0 + member + k * TEAM < n) write(i0 + member + k * TEAM, held[k]);
-    }
+            for (int k = 0; k < HOLD; ++k)
+                if (i0 + member + k * TEAM < n) write(finite, to + (i0 + k * TEAM) * D, held[k]);
+        }
+    };
+    if (plain) write_all(std::true_type{}); else write_all(std::false_type{});
 }
 
 // per: tokens that a thread block looks for runs among, at most 32.
@@ -464,19 +487,21 @@ __global__ void __launch_bounds__(APP_WARPS * 32, 4) k_kv_append(AppendArgs A, b
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int head = blockIdx.y >> 1, which = blockIdx.y & 1;
     // the tokens that begin a run, the same for every warp
-    const long long t = (long long)blockIdx.x * per + lane;
-    bool begins = false;
-    if (lane < per && t < A.T) {
-        const int64_t slot = A.slots[t], before = t > 0 ? A.slots[t - 1] : -2;
-        begins = slot >= 0 && ((slot & ((1 << A.shift) - 1)) == 0 || before != slot - 1);
-    }
+    const long long base = (long long)blockIdx.x * per;
+    Slots near;
+    const int64_t before0 = base > 0 && base < A.T ? A.slots[base - 1] : -2;
+    near.load(A, base, lane);
+    int64_t before = __shfl_up_sync(0xffffffffu, near.lo, 1);
+    if (lane == 0) before = before0;
+    const bool begins = lane < per && near.lo >= 0 && ((near.lo & ((1 << A.shift) - 1)) == 0 || before != near.lo - 1);
     uint32_t left = __ballot_sync(0xffffffffu, begins);
-    const int base = blockIdx.x * per;
     if (__popc(left) > 2) {
         for (int k = 0; left; left &= left - 1, ++k)
-            if (k % APP_WARPS == warp) append_run<TY, D, 1>(A, vec, which, head, base + __ffs(left) - 1, most);
+            if (k % APP_WARPS == warp)
+                append_run<TY, D, 1>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
     } else {
-        for (; left; left &= left - 1) append_run<TY, D, APP_WARPS>(A, vec, which, head, base + __ffs(left) - 1, most);
+        for (; left; left &= left - 1)
+            append_run<TY, D, APP_WARPS>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
     }
 }
 
