@@ -234,18 +234,19 @@ PlanArgs plan_args(const e0_kv_state* k, int32_t* ctx_out, int32_t* free_out, ui
 // A run is the consecutive new tokens of one block of the cache; for a run, a head and
 // keys or values the kernel finds the largest magnitude, settles the scale, rounds
 // the older codes again if the scale grew, and writes the new ones.  A thread block
-// finds the runs that begin among its `per` tokens; it takes each with all its warps,
-// or, where there are many (single tokens), one with each warp.  A few tokens a warp
-// stay in registers between the maximum and the codes, so a run of up to 64 tokens
-// (32 of D = 256) is read once.  Scales are powers of two: x / s and code * old / new are then
+// finds the runs that begin among its `per` tokens.  Where a block of the cache is
+// small, it has eight heads' keys or values and a warp for each; else it has one's and
+// takes each run with all its warps or, where there are many (single tokens), one with
+// each warp.  A lane has eight elements of a token, and some tokens stay in registers
+// between the maximum and the codes, so most runs (up to 8192 elements by a thread
+// block) are read once.  Scales are powers of two: x / s and code * old / new are then
 // exact, so the only rounding is that to e4m3, and a scale that grows costs nothing
 // but the codes that fall into e4m3's subnormals.  (A scale of max / 448 would round
 // every older code again at each new maximum, and e4m3's relative precision gains
 // nothing from it.)
-// Measured (device time, GB300): 13013 tokens of 2 heads of 256 in fp16, 40 MB: 13.2 us,
-// 3.0 TB/s: a run is a chain of slots, rows, a barrier and stores of 4 us, and an
-// SM holds four at a time (one warp a run: 36.8 us); 64 single tokens of 8 heads of
-// 128: 3.2 us.
+// Measured (device time, GB300): 13013 tokens of 2 heads of 256 in fp16, 40 MB: 12.2 us,
+// 3.3 TB/s: a run is a chain of slots, rows, a barrier and stores of 4 us, and an
+// SM holds five thread blocks at a time; 64 single tokens of 8 heads of 128: 3.0 us.
 
 constexpr int APP_WARPS = 8;
 
@@ -266,10 +267,10 @@ E0_DEV float pow2_scale(uint32_t m) {
     return __int_as_float(max(e, 27) << 23);
 }
 
-// A lane's D / 32 elements of one token's head, as they are in memory.
-template <int TY, int D>
+// A lane's eight elements of one token's head, as they are in memory.
+template <int TY>
 struct AppRaw {
-    static constexpr int N = D / 32, WORDS = N * (TY == E0_F32 ? 4 : 2) / 4;
+    static constexpr int N = 8, WORDS = N * (TY == E0_F32 ? 4 : 2) / 4;
     uint32_t w[WORDS];
     E0_DEV void zero() {
 #pragma unroll
@@ -277,17 +278,10 @@ struct AppRaw {
     }
     E0_DEV void load(const typename Elem<TY>::T* p, bool vec) {
         if (vec) {
-            if constexpr (WORDS == 1) {
-                w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            } else if constexpr (WORDS == 2) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-                w[0] = u.x, w[1] = u.y;
-            } else {
 #pragma unroll
-                for (int i = 0; i < WORDS / 4; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-                    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-                }
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
             }
         } else if constexpr (TY == E0_F32) {
 #pragma unroll
@@ -334,14 +328,14 @@ struct Slots {
 };
 
 // The run that begins with token base + j, by the calling warp (TEAM 1) or by all warps
-// of the thread block together.
-template <int TY, int D, int TEAM>
+// of the thread block together.  HOLD: steps of the run that stay in registers.
+template <int TY, int D, int TEAM, int HOLD>
 E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int base, int j, const Slots& near,
                        uint32_t* most) {
     typedef typename Elem<TY>::T T;
-    constexpr int N = D / 32, HOLD = D == 256 ? 4 : 8;
+    constexpr int N = 8, LANES = D / N, AT_ONCE = TEAM * 32 / LANES;  // tokens that the team reads in a step
     const int lane = threadIdx.x & 31, member = TEAM == 1 ? 0 : threadIdx.x >> 5;
-    const int bs = 1 << A.shift, t0 = base + j;
+    const int bs = 1 << A.shift, t0 = base + j, mine = (member * 32 + lane) / LANES, at = lane % LANES * N;
     const int64_t slot = __shfl_sync(0xffffffffu, near.lo, j);
     const int off = (int)(slot & (bs - 1));
     const int64_t blk = slot >> A.shift;
@@ -369,18 +363,18 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int b
             }
         n = min(n, bs - off);
     }
-    // member w has the tokens w, w + TEAM, ...
+    // the lane has a part of the tokens mine, mine + AT_ONCE, ...
     const int64_t ld = which ? A.ld[1] : A.ld[0];
-    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + (t0 + member) * ld + (size_t)head * D + lane * N;
+    const T* x = reinterpret_cast<const T*>(which ? A.x[1] : A.x[0]) + (t0 + mine) * ld + (size_t)head * D + at;
     uint8_t* codes = (which ? A.codes[1] : A.codes[0]) + ((size_t)blk * A.Hkv + head) * ((size_t)D << A.shift);
-    AppRaw<TY, D> held[HOLD];
-    // batches of HOLD tokens a member; a longer run is read again for its codes
-    const bool once = n <= HOLD * TEAM;
+    AppRaw<TY> held[HOLD];
+    // batches of HOLD steps; a longer run is read again for its codes
+    const bool once = n <= HOLD * AT_ONCE;
     const auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k)
-            if (i0 + member + k * TEAM < n)
-                held[k].load(x + (i0 + k * TEAM) * ld, vec);
+            if (i0 + mine + k * AT_ONCE < n)
+                held[k].load(x + (i0 + k * AT_ONCE) * ld, vec);
             else
                 held[k].zero();
     };
@@ -388,20 +382,20 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int b
     // largest magnitude as bits: of the values, and of those that are finite
     uint32_t all = 0, m = 0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
+    for (int i0 = 0; i0 < n; i0 += HOLD * AT_ONCE) {
         if (i0 > 0) load(i0);
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) all = held[k].max_bits(all);
     }
-    all = __reduce_max_sync(0xffffffffu, AppRaw<TY, D>::fp32_bits(all));
+    all = __reduce_max_sync(0xffffffffu, AppRaw<TY>::fp32_bits(all));
     const bool plain = all < 0x7F800000u;  // what this warp has is finite
     if (plain) {
         m = all;
     } else {
         if (lane == 0) set_status(A.st, E0_ST_NONFINITE);
 #pragma unroll 1
-        for (int i = 0; i < n - member; i += TEAM) {
-            AppRaw<TY, D> r;
+        for (int i = 0; i < n - mine; i += AT_ONCE) {
+            AppRaw<TY> r;
             r.load(x + i * ld, vec);
             float v[N];
             r.get(v);
@@ -450,42 +444,40 @@ E0_DEV void append_run(const AppendArgs& A, bool vec, int which, int head, int b
     }
     if (member == 0 && lane == 0) *scale = s;
     const float inv = 1.f / s;  // a power of two
-    uint8_t* to = codes + (size_t)(off + member) * D + lane * N;
-    const auto write = [&](auto finite, uint8_t* p, const AppRaw<TY, D>& r) {
+    uint8_t* to = codes + (size_t)(off + mine) * D + at;
+    const auto write = [&](auto finite, uint8_t* p, const AppRaw<TY>& r) {
         float v[N];
         r.get(v);
-        uint32_t c[(N + 3) / 4] = {};
+        uint32_t c[2] = {};
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
             float a = v[j] * inv, b = v[j + 1] * inv;
             if (!finite) a = fabsf(v[j]) < INFINITY ? a : 0.f, b = fabsf(v[j + 1]) < INFINITY ? b : 0.f;
             c[j / 4] |= e4m3x2(a, b) << (8 * (j & 2));
         }
-        if constexpr (N == 2)
-            *reinterpret_cast<uint16_t*>(p) = (uint16_t)c[0];
-        else if constexpr (N == 4)
-            *reinterpret_cast<uint32_t*>(p) = c[0];
-        else
-            *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
     };
     const auto write_all = [&](auto finite) {
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += HOLD * TEAM) {
+        for (int i0 = 0; i0 < n; i0 += HOLD * AT_ONCE) {
             if (!once) load(i0);
 #pragma unroll
             for (int k = 0; k < HOLD; ++k)
-                if (i0 + member + k * TEAM < n) write(finite, to + (i0 + k * TEAM) * D, held[k]);
+                if (i0 + mine + k * AT_ONCE < n) write(finite, to + (i0 + k * AT_ONCE) * D, held[k]);
         }
     };
     if (plain) write_all(std::true_type{}); else write_all(std::false_type{});
 }
 
-// per: tokens that a thread block looks for runs among, at most 32.
-template <int TY, int D>
-__global__ void __launch_bounds__(APP_WARPS * 32, 4) k_kv_append(AppendArgs A, bool vec, int per) {
+// per: tokens that a thread block looks for runs among, at most 32.  SMALL: a warp takes
+// all runs among them for its keys or values of a head; else the thread block does.
+template <int TY, int D, bool SMALL>
+__global__ void __launch_bounds__(APP_WARPS * 32, SMALL || TY == E0_F32 ? 4 : 5)
+    k_kv_append(AppendArgs A, bool vec, int per) {
     __shared__ uint32_t most[APP_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int head = blockIdx.y >> 1, which = blockIdx.y & 1;
+    const int part = SMALL ? blockIdx.y * APP_WARPS + warp : blockIdx.y, head = part >> 1, which = part & 1;
+    if (SMALL && part >= 2 * A.Hkv) return;
     // the tokens that begin a run, the same for every warp
     const long long base = (long long)blockIdx.x * per;
     Slots near;
@@ -495,27 +487,43 @@ __global__ void __launch_bounds__(APP_WARPS * 32, 4) k_kv_append(AppendArgs A, b
     if (lane == 0) before = before0;
     const bool begins = lane < per && near.lo >= 0 && ((near.lo & ((1 << A.shift) - 1)) == 0 || before != near.lo - 1);
     uint32_t left = __ballot_sync(0xffffffffu, begins);
-    if (__popc(left) > 2) {
+    if constexpr (SMALL) {
+        // steps held: blocks of 16 x 128, 13.8 us with 8, 16.2 with 4; of 16 x 64, which
+        // are four steps, 8.5 and 7.4; 8 of fp32 are too many registers
+        constexpr int HOLD = TY == E0_F32 || D == 64 ? 4 : 8;
+        for (; left; left &= left - 1)
+            append_run<TY, D, 1, HOLD>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
+    } else if (__popc(left) > 2) {
         for (int k = 0; left; left &= left - 1, ++k)
             if (k % APP_WARPS == warp)
-                append_run<TY, D, 1>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
+                append_run<TY, D, 1, 4>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
     } else {
         for (; left; left &= left - 1)
-            append_run<TY, D, APP_WARPS>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
+            append_run<TY, D, APP_WARPS, 4>(A, vec, which, head, (int)base, __ffs(left) - 1, near, most);
     }
 }
 
 template <int TY, int D>
 int append_launch(const AppendArgs& a, cudaStream_t s) {
     const int sz = type_size(TY);
-    const uintptr_t need = D / 32 * sz < 16 ? D / 32 * sz : 16;
     const uintptr_t bits = (uintptr_t)a.x[0] | (uintptr_t)a.x[1] | (uintptr_t)(a.ld[0] * sz) | (uintptr_t)(a.ld[1] * sz);
-    // at most one run of a prompt a thread block (two wait for one another; thread blocks that find none cost
-    // as much as they take from the others: 8 heads, blocks of 128, 8000 tokens: 32 us
-    // with 16 tokens each, 27 with 32); 8 where more would leave SMs without one
+    // small: a thread block a run and head has too little to do (blocks of 16, 8 heads of 64,
+    // 9300 tokens: 29.9 us against 7.4; of 32 x 128: 21.2 against 13.4), but one warp a
+    // large run takes too long over it (32 x 256: 16.9 against 12.7).
+    // per: about one run of a prompt (of two, one waits for the other; thread blocks that
+    // find none are in the others' way: 16 tokens each against 32: blocks of 128, 22.4 us
+    // against 18.5; of 32 x 256, 12.8 against 16.2), fewer where that leaves SMs without
+    // a thread block, down to as many as there are warps for.
     const int most = a.shift > 5 ? 32 : 16;
-    const int per = (long long)a.T * 2 * a.Hkv >= 4LL * most * num_sms() ? most : 8;
-    k_kv_append<TY, D><<<dim3((a.T + per - 1) / per, 2 * a.Hkv), APP_WARPS * 32, 0, s>>>(a, !(bits & (need - 1)), per);
+    const bool small = D << a.shift <= 4096;
+    const int parts = small ? (2 * a.Hkv + APP_WARPS - 1) / APP_WARPS : 2 * a.Hkv;
+    int per = most;
+    while (per > (small ? 1 : APP_WARPS) && (long long)a.T * parts < 4LL * per * num_sms()) per /= 2;
+    const dim3 grid((a.T + per - 1) / per, parts);
+    if (small)
+        k_kv_append<TY, D, true><<<grid, APP_WARPS * 32, 0, s>>>(a, !(bits & 15), per);
+    else
+        k_kv_append<TY, D, false><<<grid, APP_WARPS * 32, 0, s>>>(a, !(bits & 15), per);
     return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
 
