@@ -622,6 +622,23 @@ def test_attention_splits(L, B, longest, Hq, Hkv, D):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("D,most", [(64, 1280), (128, 768), (256, 384)])
+@pytest.mark.parametrize("more", [-1, 0, 1, 40])
+@pytest.mark.parametrize("windowed", [False, True])
+def test_attention_few_short_jobs(L, D, most, more, windowed):
+    """A long sequence among short ones, around the longest that tables or windows may hold for calls without a join."""
+    rng = np.random.default_rng(D + more)
+    window = most + more - 1 - (128 if D < 256 else 64) if windowed else 0
+    ctx = [1, most + more + (5000 if windowed else 0), 3]
+    cu = np.arange(4)
+    c, t, desc, table = filled_cache(L, 3, 16, 2, D, ctx, rng)
+    table = np.ascontiguousarray(table[:, :-(-ctx[1] // 16)])
+    q = dev(rng.standard_normal((3, 4, D)), torch.float16)
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, F16, window)
+    assert st == 0
+    check_attention(c, table, ctx, cu, q, out, lse, F16, window)
+
+
 def test_attention_without_cu_q_or_lse_and_strided(L):
     rng = np.random.default_rng(6)
     B, Hq, Hkv, D, bs = 5, 4, 2, 64, 16
