@@ -130,12 +130,16 @@ constexpr uint32_t MOST_UNITS = 0x7FFFFFFFu;
 
 E0_DEV uint32_t add_units(uint32_t a, uint32_t b) { return min(a + b, MOST_UNITS); }
 
-// How the jobs are dealt out.  Even: every block the same share of the schedule.
-// Or, where there are no more jobs than blocks and the longest is not much longer
-// than a share, a job a block: nothing to join, no block with the ends of two jobs (16
-// sequences of up to 500, 8 heads of 64: 10.0 us against 11.8, the join launched in both).
+// How the jobs are dealt out.  Even: every block the same share of the schedule, as
+// many blocks as get one unit besides a job's cost.  Or, where there are no more jobs
+// than blocks and the longest is not much longer than a share, a job a block: nothing
+// to join, no block with the ends of two jobs (16 sequences of up to 500, 8 heads of
+// 64: 10.0 us against 11.8, the join launched in both).  Or, where there are no more
+// units than blocks, a unit a block (a sequence of 4096, 32 on 8 heads of 128: 10.0 us
+// against 11.7; with two units a block where there are up to twice as many, a sequence
+// of 8000, 8 heads of 64: 12.3 against 11.3).
 struct Plan {
-    uint32_t total;  // places in the schedule: units and jobs' costs, or jobs
+    uint32_t total;  // places in the schedule: units and jobs' costs, or jobs, or units
     uint32_t share;  // of a block
     uint32_t cost;   // places that a job takes beside its units
     bool whole;      // a job a block
@@ -171,16 +175,16 @@ E0_DEV Plan schedule(const AttnArgs& A, uint32_t* first, uint32_t (*red)[3], boo
         most = max(most, red[i][2]);
     }
     Plan p;
-    const uint32_t even = (total + A.blocks - 1) / A.blocks;
+    const uint32_t even = (total + A.blocks - 1) / A.blocks, units = total - total_jobs * A.job_cost;
+    p.whole = total_jobs <= (uint32_t)A.blocks && most <= max(even, (uint32_t)A.job_cost + 2) + A.job_cost;
     p.total = total;
-    p.share = max(even, (uint32_t)A.job_cost + 2);  // at least a short job
+    p.share = max(even, (uint32_t)A.job_cost + 1);
     p.cost = A.job_cost;
-    p.whole = total_jobs <= (uint32_t)A.blocks && most <= p.share + A.job_cost;
-    if (p.whole) {
-        p.total = total_jobs, p.share = 1, p.cost = 0;
-        uint32_t at = base_jobs + inc_jobs - jobs;
+    if (p.whole || (total < MOST_UNITS && units <= (uint32_t)A.blocks)) {
+        p.total = p.whole ? total_jobs : units, p.share = 1, p.cost = 0;
+        uint32_t at = base_jobs + inc_jobs - jobs;  // jobs before
         for (int i = 0; i < per && b0 + i < A.B; ++i) {
-            first[b0 + i] = at;
+            first[b0 + i] = p.whole ? at : first[b0 + i] + (base + inc - sum) - at * A.job_cost;
             at += (uint32_t)seq_of(A, b0 + i, false).tiles * A.Hkv;
         }
     } else {
@@ -740,7 +744,7 @@ template <int D, int TY>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
     constexpr int COLS = D / 4;                     // a quarter of a row
     constexpr int GROUPS = JOIN_THREADS / (COLS / 4);
-    constexpr int BATCH = 8;
+    constexpr int BATCH = 4;  // a sequence of 32000, 8 on 1 head of 128: 12.1 us, 12.4 with 8
     __shared__ float part[GROUPS][COLS + 4];
     __shared__ float gm[GROUPS], gl[GROUPS];
     const int tid = threadIdx.x, G = A.Hq / A.Hkv;

@@ -639,6 +639,24 @@ def test_attention_few_short_jobs(L, D, most, more, windowed):
     check_attention(c, table, ctx, cu, q, out, lse, F16, window)
 
 
+@pytest.mark.parametrize("D,unit", [(64, 128), (128, 128), (256, 64)])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_attention_a_unit_a_block(L, D, unit, more):
+    """Sequences that come to as many units as there are blocks, to one fewer and to one more."""
+    blocks = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(D + more)
+    units = blocks // 2 - 2  # of two heads, beside two sequences of one unit
+    ctx = [3, (units // 2 + more) * unit - 5, unit, (units - units // 2) * unit]
+    cu = np.array([0, 1, 2, 3, 4])
+    c, t, desc, table = filled_cache(L, 4, 64, 2, D, ctx, rng)
+    q = dev(rng.standard_normal((4, 16, D)) * 1.5, torch.float32)
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, F32)
+    assert st == 0
+    check_attention(c, table, ctx, cu, q, out, lse, F32)
+    again, _, _ = attend(L, c, desc, table, ctx, cu, q, F32)
+    assert torch.equal(out, again)
+
+
 def test_attention_without_cu_q_or_lse_and_strided(L):
     rng = np.random.default_rng(6)
     B, Hq, Hkv, D, bs = 5, 4, 2, 64, 16
