@@ -36,11 +36,11 @@ namespace {
 // Measured (device time, GB300): 131071 x 2048, 2 rows of bf16, 152 MB: 29.0 us, 5.2
 // TB/s, 77 % of the measured copy rate, bound by instructions (70 for a record of 16
 // x 64, 52 of them unpacking, products and scaling; the ALU pipe is busy 55 %).
-// 8192 x 8192, one row: 11.5 us; 2048 x 2048, one row of e4m3: 4.2 us (a launch,
-// two dependent loads and a cluster's sum).  32 rows of fp16 on 8192 x 8192: 27.3 us;
-// these products run at 0.5 a clock and SM and take 8 us by themselves, a block has
-// only 32 records a warp between its start and the cluster's sum, and 256 blocks
-// leave 24 SMs without one.
+// 8192 x 8192, one row: 11.1 us; 2048 x 2048, one row of e4m3: 4.2 us (a launch,
+// two dependent loads and a cluster's sum).  32 rows of fp16 on 8192 x 8192: 22.3 us,
+// of which 12 are 32 records a warp (these products run at 0.5 a clock and SM and
+// take 8 by themselves, and 256 blocks leave 24 SMs without a second one), 6.5 the start, 1
+// the sums of x and 2.7 the cluster's sum.
 
 constexpr int REC = 576;          // bytes of one 16-row, 64-input record
 constexpr int SUPER = 8;          // row blocks whose records of a group stand together
@@ -625,7 +625,7 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
     const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
     if (a.T > 8) {
         // two row blocks a warp share the operands of x; one where two would leave SMs
-        // without a block (32 rows on 4096 x 4096: 11.5 us with one, 15.5 with two)
+        // without a block (32 rows on 4096 x 4096: 10.5 us with one, 14.3 with two)
         const int zs = (a.T + TOK - 1) / TOK;
         const auto tiles = [&](int rm) { return (nb + LIN_WARPS * rm - 1) / (LIN_WARPS * rm); };
         const auto split = [&](int rm) {
@@ -640,7 +640,7 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
                                              sizeof(BatchSmem<XT, 1>), s);
     }
     // The more row blocks a warp has, the less the operands of x cost (131071 x 2048:
-    // 37 us with 4, 29 with 8; 8192 x 8192: 19.5 with 1, 11.5 with 8); but there
+    // 37 us with 4, 29 with 8; 8192 x 8192: 19.5 with 1, 11.1 with 8); but there
     // have to be blocks for the whole machine, with K split over up to 8 of
     // them and at least two groups a warp.
     const int most = G / (2 * LIN_WARPS) < 1 ? 1 : G / (2 * LIN_WARPS) > 8 ? 8 : G / (2 * LIN_WARPS);
