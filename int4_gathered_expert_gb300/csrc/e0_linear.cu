@@ -1,5 +1,6 @@
 // Dense int4 group-64 linear layer for decode batches (e0_linear_forward) and
 // its weight layout (e0_pack_linear).
+#include <climits>
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -581,9 +582,10 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
         }
     if (S > 1) cg::this_cluster().sync(); else __syncthreads();
     // every block finishes some of the tokens; four rows a thread
-    const int toks = TOK / S;
-    for (int i = tid; i < toks * SM::ROWS / 4; i += LIN_WARPS * 32) {
-        const int t = rank * toks + i / (SM::ROWS / 4), row = i % (SM::ROWS / 4) * 4;
+    const int t_end = (rank + 1) * TOK / S;
+    for (int i = tid;; i += LIN_WARPS * 32) {
+        const int t = rank * TOK / S + i / (SM::ROWS / 4), row = i % (SM::ROWS / 4) * 4;
+        if (t >= t_end) break;
         if (tok0 + t >= A.T) break;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -602,42 +604,86 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     if (S > 1) cg::this_cluster().sync();  // a block's sums are read until here
 }
 
-// most: the most dynamic shared memory that any launch of the kernel wants.
-template <void (*kernel)(LinArgs)>
-int launch(const LinArgs& a, dim3 grid, size_t smem, size_t most, cudaStream_t s) {
-    static std::atomic<uint64_t> asked{0};
-    if (!allow_smem((const void*)kernel, most, asked)) return E0_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
+void cluster_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, dim3 grid, size_t smem, cudaStream_t s) {
     cfg.gridDim = grid;
     cfg.blockDim = dim3(LIN_WARPS * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 1, at[0].val.clusterDim.y = grid.y, at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = grid.y > 1 ? 1 : 0;
+}
+
+// Clusters of S blocks that the GPU holds at once; asked for once.
+template <void (*kernel)(LinArgs)>
+int room(int S, size_t smem) {
+    static std::atomic<int> known[9];
+    int n = known[S].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cluster_launch(cfg, at, dim3(1, S), smem, 0);
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // not the call's
+        return 2 * num_sms() / S;
+    }
+    known[S].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// most: the most dynamic shared memory that any launch of the kernel wants.
+template <void (*kernel)(LinArgs)>
+bool prepare(size_t most) {
+    static std::atomic<uint64_t> asked{0};
+    return allow_smem((const void*)kernel, most, asked);
+}
+
+template <void (*kernel)(LinArgs)>
+int launch(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cluster_launch(cfg, at, grid, smem, s);
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+// Blocks of a cluster, which split K, for as many tiles: as few groups one after another
+// as can be, at least four a block.  Clusters that do not find room at once wait for
+// others to end (16 rows on 10240 x 2560, 40 tiles: 12.3 us with 3 blocks each, 14.7 with 8,
+// 16.1 with 7; 40 on 7168 x 2048: 13.2 with 5, 17.9 with 8).
+template <void (*kernel)(LinArgs)>
+int split_of(long long tiles, int G, size_t smem) {
+    int best = 1;
+    long long least = LLONG_MAX;
+    for (int S = 1; S <= 8 && (S == 1 || G / S >= 4); ++S) {
+        const long long n = room<kernel>(S, smem), groups = (tiles + n - 1) / n * ((G + S - 1) / S);
+        if (groups < least) least = groups, best = S;
+    }
+    return best;
+}
+
+template <int XT, int RM>
+int launch_vec(const LinArgs& a, dim3 grid, cudaStream_t s) {
+    if (!prepare<k_linear_vec<XT, RM>>(VecRing<RM>::smem(8, 2))) return E0_ERR_CUDA;
+    return launch<k_linear_vec<XT, RM>>(a, grid, VecRing<RM>::smem(a.T, grid.y), s);
 }
 
 template <int XT>
 int linear_type(const LinArgs& a, cudaStream_t s) {
     const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
     if (a.T > 8) {
-        // two row blocks a warp share the operands of x; one where two would leave SMs
-        // without a block (32 rows on 4096 x 4096: 10.5 us with one, 14.3 with two)
+        // two row blocks a warp share the operands of x (8192 x 8192: 22.3 us, 29.8 with
+        // one); one where two would leave SMs with no block or most of them with one (32
+        // rows on 4096 x 4096: 10.5 us with one, 14.3 with two; 5120 x 5120: 14.3 and 16.7)
         const int zs = (a.T + TOK - 1) / TOK;
         const auto tiles = [&](int rm) { return (nb + LIN_WARPS * rm - 1) / (LIN_WARPS * rm); };
-        const auto split = [&](int rm) {
-            int S = 1;
-            while (S < 8 && (long long)tiles(rm) * zs * S < 2LL * sms && G / (2 * S) >= 4) S *= 2;
-            return S;
-        };
-        if ((long long)tiles(2) * zs * split(2) >= sms)
-            return launch<k_linear_batch<XT, 2>>(a, dim3(tiles(2), split(2), zs), sizeof(BatchSmem<XT, 2>),
-                                                 sizeof(BatchSmem<XT, 2>), s);
-        return launch<k_linear_batch<XT, 1>>(a, dim3(tiles(1), split(1), zs), sizeof(BatchSmem<XT, 1>),
-                                             sizeof(BatchSmem<XT, 1>), s);
+        constexpr size_t sm1 = sizeof(BatchSmem<XT, 1>), sm2 = sizeof(BatchSmem<XT, 2>);
+        if (!prepare<k_linear_batch<XT, 1>>(sm1) || !prepare<k_linear_batch<XT, 2>>(sm2)) return E0_ERR_CUDA;
+        const int s2 = split_of<k_linear_batch<XT, 2>>((long long)tiles(2) * zs, G, sm2);
+        if ((long long)tiles(2) * zs * s2 * 4 >= 5LL * sms)
+            return launch<k_linear_batch<XT, 2>>(a, dim3(tiles(2), s2, zs), sm2, s);
+        const int s1 = split_of<k_linear_batch<XT, 1>>((long long)tiles(1) * zs, G, sm1);
+        return launch<k_linear_batch<XT, 1>>(a, dim3(tiles(1), s1, zs), sm1, s);
     }
     // The more row blocks a warp has, the less the operands of x cost (131071 x 2048:
     // 37 us with 4, 29 with 8; 8192 x 8192: 19.5 with 1, 11.1 with 8); but there
@@ -646,18 +692,16 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
     const int most = G / (2 * LIN_WARPS) < 1 ? 1 : G / (2 * LIN_WARPS) > 8 ? 8 : G / (2 * LIN_WARPS);
     const auto split = [&](int rm) {
         const int tiles = (nb + rm - 1) / rm;
-        int S = 1;
-        while (2 * S <= most && (long long)tiles * 2 * S <= 2LL * sms) S *= 2;
-        return S;
+        return max(1, min(most, 2 * sms / tiles));
     };
     const auto fills = [&](int rm) { return (long long)((nb + rm - 1) / rm) * split(rm) * 4 >= 5LL * sms; };
     const auto grid = [&](int rm) {
         const int tiles = (nb + rm - 1) / rm, S = split(rm);
         return dim3(S == 1 && tiles > 2 * sms ? 2 * sms : tiles, S);
     };
-    if (fills(8)) return launch<k_linear_vec<XT, 8>>(a, grid(8), VecRing<8>::smem(a.T, split(8)), VecRing<8>::smem(8, 2), s);
-    if (fills(4)) return launch<k_linear_vec<XT, 4>>(a, grid(4), VecRing<4>::smem(a.T, split(4)), VecRing<4>::smem(8, 2), s);
-    return launch<k_linear_vec<XT, 1>>(a, grid(1), VecRing<1>::smem(a.T, split(1)), VecRing<1>::smem(8, 2), s);
+    if (fills(8)) return launch_vec<XT, 8>(a, grid(8), s);
+    if (fills(4)) return launch_vec<XT, 4>(a, grid(4), s);
+    return launch_vec<XT, 1>(a, grid(1), s);
 }
 
 // A thread writes one lane's 16 bytes of codes of one record; lanes 0..7 also

@@ -189,6 +189,25 @@ def test_linear(L, T, N, K, xt):
         assert (np.abs(f64(y) - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("T,N,K", [(16, 10240, 2560), (40, 7168, 2048), (20, 11008, 1536), (64, 2500, 2048),
+                                   (1, 5120, 5120), (8, 4500, 7168), (2, 12500, 3200)])
+@pytest.mark.parametrize("xt", [F32, F16, E4M3])
+def test_linear_clusters(L, T, N, K, xt):
+    """K split over numbers of blocks that divide neither its groups nor the rows that they finish."""
+    rng = np.random.default_rng(N + K)
+    w, q, s, b, keep = make_linear(L, N, K, rng)
+    x, xs, xv = make_x(T, K, xt, rng)
+    want, mag = linear_ref(q, s, b, xv)
+    y = torch.full((T + 1, N), -7.0, device="cuda")
+    L.e0_linear_forward(w, N, K, x, xt, K, xs, T, None, 0, y, F32, N)
+    # as in test_linear
+    tol = (64 + 4 + K / 64 + 8 + 8 + 3) * EPS * mag + 2 * EPS * np.abs(want) * 1.0001
+    assert (np.abs(f64(y)[:T] - want) <= tol).all() and (y[T] == -7).all()
+    z = torch.empty((T, N), device="cuda")
+    L.e0_linear_forward(w, N, K, x, xt, K, xs, T, None, 0, z, F32, N)
+    assert torch.equal(z, y[:T])
+
+
 @pytest.mark.parametrize("xt", [F32, F16, BF16, E4M3])
 def test_linear_strides_alignment_and_untouched_rows(L, xt):
     rng = np.random.default_rng(9)
