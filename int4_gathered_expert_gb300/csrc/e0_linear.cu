@@ -37,11 +37,11 @@ namespace {
 // Measured (device time, GB300): 131071 x 2048, 2 rows of bf16, 152 MB: 29.0 us, 5.2
 // TB/s, 77 % of the measured copy rate, bound by instructions (70 for a record of 16
 // x 64, 52 of them unpacking, products and scaling; the ALU pipe is busy 55 %).
-// 8192 x 8192, one row: 11.1 us; 2048 x 2048, one row of e4m3: 4.2 us (a launch,
-// two dependent loads and a cluster's sum).  32 rows of fp16 on 8192 x 8192: 22.3 us,
-// of which 12 are 32 records a warp (these products run at 0.5 a clock and SM and
-// take 8 by themselves, and 256 blocks leave 24 SMs without a second one), 6.5 the start, 1
-// the sums of x and 2.7 the cluster's sum.
+// 8192 x 8192, one row: 11.1 us; 2048 x 2048, one row of e4m3: 3.5 us (a launch
+// and two dependent loads).  32 rows of fp16 on 8192 x 8192: 22.3 us, of which 12 are 32
+// records a warp (these products run at 0.5 a clock and SM and take 8 by themselves, and
+// 256 blocks, two a SM, leave 24 SMs idle), 6.5 the start, 1 the sums of x and 2.7 the
+// cluster's sum.
 
 constexpr int REC = 576;          // bytes of one 16-row, 64-input record
 constexpr int SUPER = 8;          // row blocks whose records of a group stand together
@@ -687,12 +687,14 @@ int linear_type(const LinArgs& a, cudaStream_t s) {
     }
     // The more row blocks a warp has, the less the operands of x cost (131071 x 2048:
     // 37 us with 4, 29 with 8; 8192 x 8192: 19.5 with 1, 11.1 with 8); but there
-    // have to be blocks for the whole machine, with K split over up to 8 of
-    // them and at least two groups a warp.
-    const int most = G / (2 * LIN_WARPS) < 1 ? 1 : G / (2 * LIN_WARPS) > 8 ? 8 : G / (2 * LIN_WARPS);
+    // have to be blocks for the whole machine, with K split over up to 8 of them.
+    // That costs a cluster's sum: single row blocks are split where a warp keeps four
+    // groups of K (2048 x 2048, one row: 3.5 us whole, 4.2 in halves; 512 x 8192: 5.3
+    // in halves, 4.3 in quarters), more of them from one and a half on (10240 x 2560: 6.5 us
+    // in threes of 8, 8.0 as single ones).
     const auto split = [&](int rm) {
-        const int tiles = (nb + rm - 1) / rm;
-        return max(1, min(most, 2 * sms / tiles));
+        const int tiles = (nb + rm - 1) / rm, most = rm == 1 ? G / (4 * LIN_WARPS) : G * 2 / (3 * LIN_WARPS);
+        return max(1, min(min(8, most), 2 * sms / tiles));
     };
     const auto fills = [&](int rm) { return (long long)((nb + rm - 1) / rm) * split(rm) * 4 >= 5LL * sms; };
     const auto grid = [&](int rm) {
