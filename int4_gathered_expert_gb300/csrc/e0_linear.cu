@@ -369,14 +369,12 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
     }
 }
 
-// More than 8 rows of x: 32 of them (TOK) and 128*RM rows of W a block; a warp has
+// More than 8 rows of x: 16 or 32 of them (TOK) and 128*RM rows of W a block; a warp has
 // 16*RM rows and goes through all groups of the block's share of K, its records
 // coming through its ring as above.  x comes through shared memory once for the
 // block, CHUNK groups at a time, and its sums over groups are formed there; inside
 // a chunk warps do not wait for one another.  The blocks of a cluster split K.
-constexpr int TOK = 32;
-
-template <int XT, int RM>
+template <int XT, int RM, int TOK>
 struct BatchSmem {
     static constexpr int STAGES = 4, ROWS = LIN_WARPS * 16 * RM;
     static constexpr int XROW = GROUP * (XT == E0_F32 ? 4 : XT == E0_E4M3 ? 1 : 2);  // bytes
@@ -396,15 +394,15 @@ struct BatchSmem {
 // find eight different ones.
 template <int XT>
 E0_DEV int x_chunk(int t, int c) {
-    constexpr int PER = BatchSmem<XT, 1>::XROW / 16;
+    constexpr int PER = BatchSmem<XT, 1, 16>::XROW / 16;
     return XT == E0_E4M3 ? t * PER + c : t * PER + (c ^ (t & 1));
 }
 
-template <int XT, int RM>
+template <int XT, int RM, int TOK>
 __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     constexpr bool BF = XT == E0_F32 || XT == E0_BF16;
     constexpr int P = RawX<XT>::PARTS, NT = TOK / 8;
-    typedef BatchSmem<XT, RM> SM;
+    typedef BatchSmem<XT, RM, TOK> SM;
     constexpr int STAGES = SM::STAGES, PER = SM::XROW / 16, SZ = SM::XROW / GROUP, CHUNK = SM::CHUNK;
     extern __shared__ __align__(128) uint8_t lin_sm[];
     SM& M = *reinterpret_cast<SM*>(lin_sm);
@@ -648,15 +646,18 @@ int launch(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
 }
 
 // Blocks of a cluster, which split K, for as many tiles: as few groups one after another
-// as can be, at least four a block.  Clusters that do not find room at once wait for
-// others to end (16 rows on 10240 x 2560, 40 tiles: 12.3 us with 3 blocks each, 14.7 with 8,
-// 16.1 with 7; 40 on 7168 x 2048: 13.2 with 5, 17.9 with 8).
+// as can be, with a block's start and end counted as START groups (a few microseconds;
+// without, 16 rows on 80000 x 2048, 313 tiles, take 72 us instead of 36), and at least
+// four groups a block. Clusters that do not find room at once wait for others to end (16
+// rows on 10240 x 2560, 40 tiles: 12.3 us with 3 blocks each, 14.7 with 8, 16.1 with 7; 40
+// on 7168 x 2048: 13.2 with 5, 17.9 with 8; both in tiles of 32 rows).
 template <void (*kernel)(LinArgs)>
 int split_of(long long tiles, int G, size_t smem) {
+    constexpr int START = 12;
     int best = 1;
     long long least = LLONG_MAX;
     for (int S = 1; S <= 8 && (S == 1 || G / S >= 4); ++S) {
-        const long long n = room<kernel>(S, smem), groups = (tiles + n - 1) / n * ((G + S - 1) / S);
+        const long long n = room<kernel>(S, smem), groups = (tiles + n - 1) / n * ((G + S - 1) / S + START);
         if (groups < least) least = groups, best = S;
     }
     return best;
@@ -668,23 +669,28 @@ int launch_vec(const LinArgs& a, dim3 grid, cudaStream_t s) {
     return launch<k_linear_vec<XT, RM>>(a, grid, VecRing<RM>::smem(a.T, grid.y), s);
 }
 
+template <int XT, int TOK>
+int linear_batch(const LinArgs& a, int nb, int G, int sms, cudaStream_t s) {
+    // two row blocks a warp share the operands of x (8192 x 8192: 22.3 us, 29.8 with
+    // one); one where two would leave SMs with no block or most of them with one (32
+    // rows on 4096 x 4096: 10.5 us with one, 14.3 with two; 5120 x 5120: 14.3 and 16.7)
+    const int zs = (a.T + TOK - 1) / TOK;
+    const auto tiles = [&](int rm) { return (nb + LIN_WARPS * rm - 1) / (LIN_WARPS * rm); };
+    constexpr size_t sm1 = sizeof(BatchSmem<XT, 1, TOK>), sm2 = sizeof(BatchSmem<XT, 2, TOK>);
+    if (!prepare<k_linear_batch<XT, 1, TOK>>(sm1) || !prepare<k_linear_batch<XT, 2, TOK>>(sm2)) return E0_ERR_CUDA;
+    const int s2 = split_of<k_linear_batch<XT, 2, TOK>>((long long)tiles(2) * zs, G, sm2);
+    if ((long long)tiles(2) * zs * s2 * 4 >= 5LL * sms)
+        return launch<k_linear_batch<XT, 2, TOK>>(a, dim3(tiles(2), s2, zs), sm2, s);
+    const int s1 = split_of<k_linear_batch<XT, 1, TOK>>((long long)tiles(1) * zs, G, sm1);
+    return launch<k_linear_batch<XT, 1, TOK>>(a, dim3(tiles(1), s1, zs), sm1, s);
+}
+
 template <int XT>
 int linear_type(const LinArgs& a, cudaStream_t s) {
     const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
-    if (a.T > 8) {
-        // two row blocks a warp share the operands of x (8192 x 8192: 22.3 us, 29.8 with
-        // one); one where two would leave SMs with no block or most of them with one (32
-        // rows on 4096 x 4096: 10.5 us with one, 14.3 with two; 5120 x 5120: 14.3 and 16.7)
-        const int zs = (a.T + TOK - 1) / TOK;
-        const auto tiles = [&](int rm) { return (nb + LIN_WARPS * rm - 1) / (LIN_WARPS * rm); };
-        constexpr size_t sm1 = sizeof(BatchSmem<XT, 1>), sm2 = sizeof(BatchSmem<XT, 2>);
-        if (!prepare<k_linear_batch<XT, 1>>(sm1) || !prepare<k_linear_batch<XT, 2>>(sm2)) return E0_ERR_CUDA;
-        const int s2 = split_of<k_linear_batch<XT, 2>>((long long)tiles(2) * zs, G, sm2);
-        if ((long long)tiles(2) * zs * s2 * 4 >= 5LL * sms)
-            return launch<k_linear_batch<XT, 2>>(a, dim3(tiles(2), s2, zs), sm2, s);
-        const int s1 = split_of<k_linear_batch<XT, 1>>((long long)tiles(1) * zs, G, sm1);
-        return launch<k_linear_batch<XT, 1>>(a, dim3(tiles(1), s1, zs), sm1, s);
-    }
+    // (16 rows of fp16 on 8192 x 8192: 14.9 us in a tile of 16, 20.6 in one of 32)
+    if (a.T > 16) return linear_batch<XT, 32>(a, nb, G, sms, s);
+    if (a.T > 8) return linear_batch<XT, 16>(a, nb, G, sms, s);
     // The more row blocks a warp has, the less the operands of x cost (131071 x 2048:
     // 37 us with 4, 29 with 8; 8192 x 8192: 19.5 with 1, 11.1 with 8); but there
     // have to be blocks for the whole machine, with K split over up to 8 of them.
