@@ -688,9 +688,13 @@ int linear_batch(const LinArgs& a, int nb, int G, int sms, cudaStream_t s) {
 template <int XT>
 int linear_type(const LinArgs& a, cudaStream_t s) {
     const int sms = num_sms(), G = a.K / GROUP, nb = (a.N + 15) / 16;
-    // (16 rows of fp16 on 8192 x 8192: 14.9 us in a tile of 16, 20.6 in one of 32)
-    if (a.T > 16) return linear_batch<XT, 32>(a, nb, G, sms, s);
-    if (a.T > 8) return linear_batch<XT, 16>(a, nb, G, sms, s);
+    // A tile of 16 rows takes two thirds of one of 32 (16 rows of fp16 on 8192 x 8192: 14.9 us
+    // and 20.6), so one of 16 is better than one of 32, and three than two (48 rows of
+    // bf16: 34.4 us and 40.3).
+    if (a.T > 8) {
+        const bool small = a.T <= 16 || (a.T > 32 && a.T <= 48);
+        return small ? linear_batch<XT, 16>(a, nb, G, sms, s) : linear_batch<XT, 32>(a, nb, G, sms, s);
+    }
     // The more row blocks a warp has, the less the operands of x cost (131071 x 2048:
     // 37 us with 4, 29 with 8; 8192 x 8192: 19.5 with 1, 11.1 with 8); but there
     // have to be blocks for the whole machine, with K split over up to 8 of them.

@@ -190,7 +190,7 @@ def test_linear(L, T, N, K, xt):
 
 
 @pytest.mark.parametrize("T,N,K", [(16, 10240, 2560), (40, 7168, 2048), (20, 11008, 1536), (64, 2500, 2048),
-                                   (16, 300, 640), (17, 300, 640), (12, 40000, 512), (15, 1000, 4160),
+                                   (16, 300, 640), (17, 300, 640), (48, 300, 640), (49, 300, 640), (12, 40000, 512), (15, 1000, 4160),
                                    (1, 5120, 5120), (8, 4500, 7168), (2, 12500, 3200)])
 @pytest.mark.parametrize("xt", [F32, F16, E4M3])
 def test_linear_clusters(L, T, N, K, xt):
