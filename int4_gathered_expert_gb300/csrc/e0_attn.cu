@@ -110,10 +110,11 @@ struct Seq {
 E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     Seq s;
     s.row0 = A.cu ? A.cu[b] : b;
-    s.n = A.cu ? A.cu[b + 1] - s.row0 : 1;
+    const long long n = A.cu ? (long long)A.cu[b + 1] - s.row0 : 1;  // of any two 32-bit numbers: not a 32-bit one
+    s.n = (int)n;
     s.ctx = A.ctx[b];
     bool bad = false;
-    if (s.row0 < 0 || s.n < 0 || s.n > A.max_q) bad = true, s.n = 0;
+    if (s.row0 < 0 || n < 0 || n > A.max_q) bad = true, s.n = 0;
     if (s.ctx < 0 || (long long)s.ctx > ((long long)A.max_blocks << A.shift)) bad = true, s.ctx = 0;
     if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
     s.low = A.window > 0 ? max(s.ctx - s.n + 1 - A.window, 0) : 0;

@@ -728,6 +728,23 @@ def test_attention_rows_that_see_nothing(L):
     assert st & L.E0_ST_BAD_LENGTH
 
 
+def test_attention_row_numbers_that_wrap(L):
+    """A cu_q whose neighbours differ by more than 32 bits hold: -2^31 - (2^31 - 1) is 1 in 32 bits, and 2^31 - 1 no row."""
+    rng = np.random.default_rng(18)
+    Hq, Hkv, D, bs = 4, 2, 64, 16
+    ctx, cu = [20, 33], np.array([0, 1, 2])
+    c, t, desc, table = filled_cache(L, 2, bs, Hkv, D, ctx, rng)
+    q = dev(rng.standard_normal((2, Hq, D)), torch.float32)
+    want, _, st = attend(L, c, desc, table, ctx, cu, q, F32)
+    assert st == 0
+    top = 2 ** 31 - 1
+    for bad in ([top, -top - 1, 2], [top - 1, -top, 1], [top, -top + 1, -top + 1], [1, -top, -top + 2]):
+        out, lse, st = attend(L, c, desc, table, ctx, np.array(bad), q, F32, max_q=3)
+        assert st == L.E0_ST_BAD_LENGTH and (out == -7).all() and (lse == -7).all()
+    out, _, st = attend(L, c, desc, table, ctx, np.array([-top - 1, 1, 2]), q, F32, max_q=3)
+    assert st == L.E0_ST_BAD_LENGTH and torch.equal(out[1], want[1]) and (out[0] == -7).all()
+
+
 @pytest.mark.parametrize("bs", [16, 64])
 def test_attention_window_over_released_blocks(L, bs):
     """Blocks that lie wholly before the window may be gone: ids out of range, scales that are not numbers."""
