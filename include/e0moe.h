@@ -568,12 +568,16 @@ int e0_kv_plan(const e0_kv_state* state, const int32_t* new_len, int T_cap, int3
                uint32_t* d_status, e0_stream_t stream);
 
 /* Give back the blocks of every sequence b with mask[b] != 0 (device bytes):
- * its block ids go onto the free stack, sequences in order, its row of the
- * table becomes -1 and its length 0.  A block belongs to one sequence: blocks
- * that several rows name are not counted.  ctx_out / free_out as for
- * e0_kv_plan.  A length that does not fit max_blocks, or a stack that would
- * grow beyond n_blocks, raises E0_ST_BAD_LENGTH and nothing is given back.
- * Errors as e0_kv_plan. */
+ * the block ids in the first ceil(ctx_len[b] / block_tokens) places of its row
+ * go onto the free stack, sequences in order, those places become -1 and its
+ * length 0.  A place that is -1 has no block (it was given back before, as one
+ * that lies wholly before a window may be) and is passed over; another id
+ * outside [0, n_blocks) raises E0_ST_BAD_BLOCK and is passed over too, so that
+ * only ids of the pool get onto the stack.  A block belongs to one sequence:
+ * blocks that several rows name are not counted.  ctx_out / free_out as for
+ * e0_kv_plan, in one launch.  A length that does not fit max_blocks, more than
+ * E0_MAX_ROWS places in all, or a stack that would grow beyond n_blocks raises
+ * E0_ST_BAD_LENGTH and nothing is given back.  Errors as e0_kv_plan. */
 int e0_kv_release(const e0_kv_state* state, const uint8_t* mask, int32_t* ctx_out, int32_t* free_out,
                   uint32_t* d_status, e0_stream_t stream);
 

@@ -434,6 +434,56 @@ def test_release_refuses_what_cannot_be(L):
         assert np.array_equal(kv.d_table.cpu().numpy(), kv.table)
 
 
+@pytest.mark.parametrize("B,bs,longest,wide", [(3, 16, 100, 0), (40, 16, 300, 0), (40, 16, 300, 300), (700, 16, 200, 0)])
+@pytest.mark.parametrize("bad", [False, True])
+@pytest.mark.parametrize("apart", [False, True])
+def test_release_passes_over_places_without_a_block(L, B, bs, longest, wide, bad, apart):
+    """Rows whose early blocks are gone (-1), or that hold ids that cannot be: what goes onto the stack are blocks of the
+    pool, in order, and a plan that takes them all gives every token a place.  wide: a table with many more places."""
+    rng = np.random.default_rng(B + wide)
+    held = rng.integers(1, longest + 1, B)
+    M = -(-longest // bs) + 2 + wide
+    kv = Kv(L, B, bs, M, int((-(-held // bs)).sum()) + 4, rng, held)
+    mask = rng.integers(0, 4, B).astype(np.uint8)
+    mask[0] = 1
+    gone = []
+    for b in range(B):
+        n = -(-int(kv.ctx[b]) // bs)
+        k = int(rng.integers(0, n + 1)) if mask[b] else 0
+        gone += list(kv.table[b, :k])  # given back by hand, in what order ever
+        kv.table[b, :k] = -1
+    kv.free = gone[::-1] + kv.free
+    junk = [kv.n, -2, 2 ** 31 - 1, -2 ** 31] if bad else []
+    at = [(b, j) for b in range(B) if mask[b] for j in range(-(-int(kv.ctx[b]) // bs)) if kv.table[b, j] == -1][:len(junk)]
+    dirty = kv.table.copy()
+    for (b, j), x in zip(at, junk):
+        dirty[b, j] = x
+    kv.d_table.copy_(dev(dirty))
+    kv.d_free[:len(kv.free)] = dev(np.array(kv.free, np.int32))
+    kv.d_count.fill_(len(kv.free))
+    ctx = torch.empty_like(kv.d_ctx) if apart else kv.d_ctx
+    count = torch.empty_like(kv.d_count) if apart else kv.d_count
+    st = status()
+    L.e0_kv_release(kv.desc, dev(mask), ctx, count, st)
+    kv.d_ctx.copy_(ctx), kv.d_count.copy_(count)
+    assert L.e0_read_status(st) == (L.E0_ST_BAD_BLOCK if at else 0)
+    for b in range(B):
+        if mask[b]:
+            kv.free += [int(x) for x in kv.table[b] if x >= 0]
+            kv.table[b] = -1
+            kv.ctx[b] = 0
+    kv.check()
+    new = np.zeros(B, int)  # all the blocks that there are, one sequence after another
+    left = len(kv.free)
+    for b in np.flatnonzero(mask):
+        k = min(left, M)
+        new[b], left = k * bs, left - k
+    o = plan(L, kv, new, int(new.sum()))
+    slots, _, _ = kv.plan_ref(new)
+    assert L.e0_read_status(o["st"]) == 0 and np.array_equal(o["slots"].cpu().numpy()[:len(slots)], np.array(slots))
+    kv.check()
+
+
 # ------------------------------------------------------------------ append
 
 
