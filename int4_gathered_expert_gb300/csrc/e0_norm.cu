@@ -177,11 +177,14 @@ E0_DEV bool finish_chunk(const NormArgs& A, size_t row, int e, float rstd, float
     const float most = mx * rest;  // max|h|
     const bool bad = !(most < INFINITY) && e < H;
     const bool zero = bad || most < 7.7037198e-34f;  // 2^-110: 448 / mx and most / 448 stay normal numbers
-    // 448 / mx: an approximate inverse and one step on the remainder
+    // 448 / mx as 112 / (mx / 4), whose inverse is a normal number up to the largest mx: an
+    // approximate inverse, a first quotient, and Newton's step on the quotient's remainder,
+    // which a fused multiply-add gives exactly (Markstein, IBM J. Res. Dev. 34, 1990)
+    const float quarter = 0.25f * mx;
     float inv, scale;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(mx));
-    scale = 448.f * inv;
-    scale = fmaf(fmaf(-mx, scale, 448.f), inv, scale);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(quarter));
+    scale = 112.f * inv;
+    scale = fmaf(fmaf(-quarter, scale, 112.f), inv, scale);
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * scale, v[2 * i + 1] * scale);

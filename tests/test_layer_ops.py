@@ -128,6 +128,37 @@ def test_norm_zero_tiny_and_non_finite_rows(L):
     L.e0_rmsnorm_q8(r, None, None, 0, 128, F32, 1e-6, 128, 0, None, h, None, None)
 
 
+@pytest.mark.parametrize("T,H_", [(4, 128), (3, 65), (1300, 64), (2, 4104)])
+def test_norm_up_to_the_largest_numbers(L, T, H_):
+    """Weights that bring h close to fp32's largest value: codes and scales as at any size."""
+    rng = np.random.default_rng(H_)
+    v = rng.uniform(-1, 1, (T, H_))
+    v[:, ::64] = 1  # every group's maximum
+    r = dev(v, torch.float32)
+    x = f64(r)
+    root = np.sqrt((x ** 2).mean(1, keepdims=True) + 1e-6)
+    w = dev(np.full(H_, 3.3e38 * root.min()), torch.float32)
+    want = x / root * f64(w)
+    assert 3e38 < np.abs(want).max() < 3.4e38
+    h, q = torch.empty_like(r), torch.empty((T, H_), dtype=torch.uint8, device="cuda")
+    ng = -(-H_ // 64)
+    qs, st = torch.empty((T, ng), device="cuda"), status()
+    L.e0_rmsnorm_q8(r, None, w, T, H_, F32, 1e-6, H_, 0, None, h, q, qs, st)
+    assert L.e0_read_status(st) == 0
+    rel = (32 + 21) / 2 * EPS + 5 * EPS  # as in test_norm
+    assert (np.abs(f64(h) - want) <= (rel + H[F32]) * np.abs(want) * 1.0001).all()
+    pad = np.zeros((T, ng * 64))
+    pad[:, :H_] = want
+    m = np.abs(pad.reshape(T, ng, 64)).max(2) / 448
+    assert (np.abs(f64(qs) - m) <= (rel + EPS) * m).all()
+    scaled = (pad.reshape(T, ng, 64) / m[:, :, None]).reshape(T, ng * 64)[:, :H_]
+    code = q.cpu().numpy()
+    sure = R.border_distance(scaled) > 2 * rel + 4 * EPS
+    assert sure.mean() > 0.99 and np.array_equal(code[sure], R.encode(scaled)[sure])
+    step = np.maximum(np.abs(scaled) * 2.0 ** -4, 2.0 ** -10)
+    assert (np.abs(R.decode(code) - scaled) <= step * (1 + 1e-5)).all()
+
+
 # ------------------------------------------------------------------ linear
 
 
