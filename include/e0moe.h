@@ -624,7 +624,11 @@ size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * left as they were; a call of more than 2^31 pieces of work (query tile, KV
  * head, 64 positions) raises it and writes nothing.  A block id out of range
  * raises E0_ST_BAD_BLOCK and its tokens are not seen.  A scale of values below
- * 2^-100 counts as 2^-100.  The result does not depend on how blocks are laid
+ * 2^-100 counts as 2^-100.  Where the scales of values that a query sees in one
+ * head lie up to 2^100 apart, tokens that are left out of its softmax's sum
+ * weigh less than 2^-26 of the heaviest; farther apart, tokens of the small
+ * scale may be left out.  lse is finite for all finite values up to 2^25
+ * positions.  The result does not depend on how blocks are laid
  * out in the pool, and equal calls give equal bits.  Any max_q; the call is
  * made for decode steps and short runs of tokens (every 8 query rows of a KV
  * head, or 16 with bf16, read the sequence once more).  Errors: NULL pointers

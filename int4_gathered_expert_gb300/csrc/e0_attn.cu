@@ -39,7 +39,10 @@ namespace {
 // twice in a job, not at every new maximum).  That fills fp16's range whatever the
 // scales are: the rest of a weight goes in times 2^12, so weights down to 2^-43
 // of the largest count.  The softmax's sum is that of the weights over their
-// scales.
+// scales, times 2^-12: the weights are at most 2^15 and the scales at least 2^-100, so 2^25
+// positions of zero values (2^30 with equal scores) stay inside fp32's range, and so
+// does the inverse of the sum where the scales are the largest ones of finite values,
+// 2^120, and the sum is 2^(7 - 120 - 12) or more.
 //
 // Measured (device time, GB300): 64 sequences of up to 16000 tokens, 32 query on 4
 // KV heads of 128, 498 MB: 85.5 us, 5.8 TB/s, 86 % of the measured copy rate; what
@@ -274,6 +277,12 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr float LEAST_SCALE = 7.8886090522101181e-31f;  // 2^-100, the least that e0_kv_append writes
 constexpr float LIFT = 7.f, SLACK = 8.f;                // weights are 2^(t - m + LIFT), t at most m + SLACK
 constexpr float REST = 4096.f;                          // what the rests of the weights go in times
+constexpr float SUM_LIFT = -12.f, SUM_UNIT = 1.f / 4096.f;  // sums are times 2^SUM_LIFT
+
+// ln of the softmax's sum from the running maximum and sum.
+E0_DEV float lse_of(float m, float l) {
+    return l > 0.f || l != l ? (m - (LIFT + SUM_LIFT) + log2f(l)) * LN2 : -INFINITY;
+}
 
 template <int D>
 struct AttnSmem {
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             if (my_id >= 0 && my_id < A.n_blocks) {
                 const size_t i = (size_t)my_id * A.Hkv + j.head;
                 const float v = fmaxf(A.vs[i], LEAST_SCALE);
-                my_sc = make_float4(A.ks[i], log2f(v), 1.f / v, 0.f);
+                my_sc = make_float4(A.ks[i], log2f(v), SUM_UNIT / v, 0.f);
             } else {
                 my_id = -1;
                 set_status(A.st, E0_ST_BAD_BLOCK);
@@ -712,7 +721,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 #pragma unroll
                     for (int w = 0; w < AT_WARPS; ++w) o += k[w] * warp_out<D>(S, w, r & 7, d);
                     if (whole)
-                        store_out<TY>(A, tok, head * D + d, o * inv);
+                        store_out<TY>(A, tok, head * D + d, o * SUM_UNIT * inv);
                     else
                         A.part_o[((size_t)slot * ROWS + r) * D + d] = o;
                 }
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     if (!whole)
                         A.part_ml[(size_t)slot * ROWS + r] = make_float2(m, l);
                     else if (A.lse)
-                        A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
+                        A.lse[tok * A.Hq + head] = lse_of(m, l);
                 }
             }
         }
@@ -754,8 +763,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(AttnArgs A) {
     const auto write = [&](const Cut& cut, int r, int d, float o, float m, float l) {
         const int row = cut.tile * A.rows + r, head = cut.head * G + row % G;
         const size_t tok = (size_t)cut.row0 + row / G;
-        store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o / l : 0.f);
-        if (A.lse && d == 0) A.lse[tok * A.Hq + head] = l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
+        store_out<TY>(A, tok, head * D + d, l > 0.f || l != l ? o * SUM_UNIT / l : 0.f);
+        if (A.lse && d == 0) A.lse[tok * A.Hq + head] = lse_of(m, l);
     };
     // the first block left its part in its second slot, the others in their first
     const auto slot_of = [&](const Cut& cut, int r, int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * A.rows + r; };

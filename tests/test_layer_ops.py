@@ -886,6 +886,50 @@ def test_attention_scores_and_scales_far_apart(L):
         check_attention(c, table, ctx, cu, q, out, lse, F32)
 
 
+@pytest.mark.parametrize("Hq,dtype", [(1, F32), (4, F16), (16, BF16)])
+def test_attention_lse_over_values_of_zero(L, Hq, dtype):
+    """A long context of zero values (scales of 2^-100): the softmax's sum stays in range, with scores that rise by almost
+    the running maximum's slack after each warp's first step, as with equal ones."""
+    B, n, D, bs = 300, 1 << 14, 64, 128
+    c = R.Cache(n // bs, 1, bs, D)
+    c.k[1:, :, :, 0] = 0x38  # 1.0; the first 128 positions have scores of 0
+    c.ks[:], c.vs[:] = 1, 2.0 ** -100
+    t, desc = cache_dev(L, c)
+    table = np.tile(np.arange(n // bs, dtype=np.int32), (B, 1))
+    q = torch.zeros((B, Hq, D), dtype=DT[dtype], device="cuda")
+    q[:, :, 0] = 43.75  # times 0.125: 7.89 in log2
+    ctx, cu = [n] * B, np.arange(B + 1)
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, dtype)
+    assert st == 0 and (out[:B] == 0).all()
+    want = np.log(128 + (n - 128) * np.exp(43.75 * 0.125))
+    # in log2: t, the maximum's part, log2 of the sum and their own sum are below 2^7, so half a step is 2^-18; log2f
+    # may be off by a step; exp2 by 2 ulp and n positive terms in 304 blocks of 4 warps of 8 lanes are summed in fp32
+    tol = (3 * 2.0 ** -18 + 2.0 ** -17) * np.log(2) + (2 + n / 32 + 64) * EPS + 4 * EPS * want
+    assert (np.abs(f64(lse)[:B] - want) <= tol).all()
+    # a sequence of 2^21 positions: the same blocks again and again, all scores equal
+    m = (1 << 21) + 1000
+    table = np.zeros((1, -(-m // bs)), np.int32)
+    out, lse, st = attend(L, c, desc, table, [m], np.arange(2), q[:1], dtype)
+    assert st == 0 and (out[:1] == 0).all()
+    tol = (3 * 2.0 ** -18 + 2.0 ** -17) * np.log(2) + (2 + m / 32 / 150 + 304 + 64) * EPS + 4 * EPS * np.log(m)
+    assert (np.abs(f64(lse)[:1] - np.log(m)) <= tol).all()
+
+
+@pytest.mark.parametrize("Hq,dtype", [(2, F32), (16, BF16)])
+def test_attention_values_of_the_largest_scales(L, Hq, dtype):
+    """Values up to fp32's end: the inverse of the softmax's sum stays in range."""
+    rng = np.random.default_rng(19)
+    ctx, cu = [1, 70, 900], np.arange(4)
+    c, t, desc, table = filled_cache(L, 3, 16, 1, 64, ctx, rng)
+    c.v &= 0xF7  # codes of at most 240
+    c.vs[:] = 2.0 ** 119
+    t, desc = cache_dev(L, c)
+    q = dev(rng.standard_normal((3, Hq, 64)) * 1.5, DT[dtype])
+    out, lse, st = attend(L, c, desc, table, ctx, cu, q, dtype)
+    assert st == 0 and torch.isfinite(out.float()).all()
+    check_attention(c, table, ctx, cu, q, out, lse, dtype)
+
+
 def test_attention_offsets_beyond_32_bits(L):
     """A pool of more than 2^31 code bytes: blocks at its end."""
     Hkv, D, bs = 8, 256, 128
