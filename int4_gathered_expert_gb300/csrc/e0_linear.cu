@@ -25,10 +25,12 @@ namespace {
 // 0..3 of a half is the subnormal number code * 2^-24, exact, in the bits 4..7 code *
 // 2^-20; the layout gives all codes of the lower row the first place and of the
 // upper row the second, and the rows' scales take the factors.  bf16: in the bits
-// 3..6, with the exponent of 16 set, it is 16 + code; the product is then too large
-// by 16 sum x, which goes into the bias.  (In the bits 0..3 it would be 128 + code
-// and the sums' rounding 5 times as large; subtracting the 128 again took a
-// third of the instructions.)
+// 3..6, with the exponent of 2^-7 set, it is (16 + code) * 2^-11; the product is then
+// too large by 16 sum x, which goes into the bias, and all sums stay times 2^-11 until
+// they are stored (sum x is formed with 2^-11 in place of ones), so that a group's
+// sums, up to 64 * 31 times a value of x, do not pass fp32's range where y does not.
+// (In the bits 0..3 it would be 128 + code and the sums' rounding 5 times as large;
+// subtracting the 128 again took a third of the instructions.)
 // Activations: fp16 and bf16 as they are; e4m3 widened to fp16 (exact), its
 // scale applied to the group's sums; fp32 as three bf16 parts (8 significant bits
 // each, cut off, the sum exact), three products a step.
@@ -89,7 +91,7 @@ E0_DEV void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
         const uint32_t v[4] = {w << 3, w >> 1, w >> 5, w >> 9};
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // (v & mask) | exponents in one instruction
-            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(v[i]), "r"(0x00780078u), "r"(0x41804180u));
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[i]) : "r"(v[i]), "r"(0x00780078u), "r"(0x3C003C00u));
     } else {
         a[0] = w & 0x000F000Fu;
         a[1] = w & 0x00F000F0u;
@@ -97,6 +99,11 @@ E0_DEV void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
         a[3] = (w >> 8) & 0x00F000F0u;
     }
 }
+// A pair of the values that sum x is the product with, and what sums are turned back with.
+template <bool BF>
+constexpr uint32_t ONE = BF ? 0x3A003A00u : 0x3C003C00u;  // 2^-11 in bf16, 1 in fp16
+template <bool BF>
+constexpr float UNIT = BF ? 2048.f : 1.f;
 // What the sums are turned with, from the (scale, bias) word of a lower (i) or
 // upper (i + 8) row.
 template <bool BF, bool UPPER>
@@ -193,9 +200,11 @@ E0_DEV void put_any(void* p, int type, size_t i, float v) {
         reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// y[t][n] = v (+ add[t][n]), where there is such a row and token.
+// y[t][n] = v (+ add[t][n]) from the sum in its unit, where there is such a row and token.
+template <bool BF>
 E0_DEV void store_y(const LinArgs& A, int n, int t, float v) {
     if (n >= A.N || t >= A.T) return;
+    v *= UNIT<BF>;
     if (A.add) v += get_any(A.add, A.y_type, (size_t)t * A.add_ld + n);
     put_any(A.y, A.y_type, (size_t)t * A.y_ld + n, v);
 }
@@ -247,8 +256,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
     const int G = A.K / GROUP, S = gridDim.y, rank = blockIdx.y;
     const int g0 = (int)((long long)rank * G / S), g1 = (int)((long long)(rank + 1) * G / S);
     const int nb = (A.N + 15) / 16, tiles = (nb + RM - 1) / RM;
-    const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
-    const uint32_t ones[4] = {one, one, one, one};
+    const uint32_t ones[4] = {ONE<BF>, ONE<BF>, ONE<BF>, ONE<BF>};
 
     // where the next copy comes from and goes to
     constexpr int PIECES = (RM * 36 + 31) / 32;  // 16-byte pieces of a step that a lane copies
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
         // rows run along neighbouring threads, so stores to one token's row are coalesced
         if (S == 1) {
             for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32)
-                store_y(A, tile * ROWS + e % ROWS, e / ROWS, sum(e % ROWS, e / ROWS));
+                store_y<BF>(A, tile * ROWS + e % ROWS, e / ROWS, sum(e % ROWS, e / ROWS));
         } else {  // one tile a cluster
             float* sums = part + LIN_WARPS * ROWS * LD;  // [T][ROWS]
             for (int e = threadIdx.x; e < ROWS * A.T; e += LIN_WARPS * 32) sums[e] = sum(e % ROWS, e / ROWS);
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_vec(LinArgs A) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (k < S) v += cg::this_cluster().map_shared_rank(sums, k)[e];
-                store_y(A, tile * ROWS + e % ROWS, e / ROWS, v);
+                store_y<BF>(A, tile * ROWS + e % ROWS, e / ROWS, v);
             }
             cg::this_cluster().sync();  // a block's sums are read until here
         }
@@ -464,8 +472,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
     };
     // sums over a group of 8 tokens' inputs
     const auto sum_x = [&](int g, int k, int n) {
-        const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
-        const uint32_t ones[4] = {one, one, one, one};
+        const uint32_t ones[4] = {ONE<BF>, ONE<BF>, ONE<BF>, ONE<BF>};
         uint32_t b[P][8];
         fragments_of(M.x[k], n, b);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -594,10 +601,10 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 2) k_linear_batch(LinArgs A) {
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
             }
         const int n = blockIdx.x * SM::ROWS + row;
-        store_y(A, n, tok0 + t, v.x);
-        store_y(A, n + 1, tok0 + t, v.y);
-        store_y(A, n + 2, tok0 + t, v.z);
-        store_y(A, n + 3, tok0 + t, v.w);
+        store_y<BF>(A, n, tok0 + t, v.x);
+        store_y<BF>(A, n + 1, tok0 + t, v.y);
+        store_y<BF>(A, n + 2, tok0 + t, v.z);
+        store_y<BF>(A, n + 3, tok0 + t, v.w);
     }
     if (S > 1) cg::this_cluster().sync();  // a block's sums are read until here
 }

@@ -281,6 +281,31 @@ def test_linear_extreme_and_non_finite_inputs(L, xt):
     assert not torch.isfinite(y[2:]).any()
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 40, 128), (8, 300, 4160), (12, 300, 640), (40, 130, 4096)])
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("add", [False, True])
+def test_linear_large_values_of_one_sign(L, T, N, K, xt, add):
+    """Values near fp32's end whose sums with the codes pass it, and y does not."""
+    rng = np.random.default_rng(N + K)
+    q = rng.integers(0, 16, (N, K)).astype(np.uint8)
+    scale = rng.uniform(1e-4, 2e-4, (N, K // 64)).astype(np.float16)
+    bias = (-7.5 * scale).astype(np.float16)
+    codes, s, b = dev(q[:, 0::2] | (q[:, 1::2] << 4)), dev(scale), dev(bias)
+    w = torch.empty(L.e0_linear_bytes(N, K), dtype=torch.uint8, device="cuda")
+    L.e0_pack_linear(L.QTensor(codes.data_ptr(), s.data_ptr(), b.data_ptr()), N, K, w)
+    x = dev(rng.uniform(1e38, 3.3e38, (T, K)), DT[xt])
+    a = dev(rng.uniform(-1e36, 1e36, (T, N)), torch.float32) if add else None
+    y = torch.empty((T, N), device="cuda")
+    L.e0_linear_forward(w, N, K, x, xt, K, None, T, a, N, y, F32, N)
+    want, mag = linear_ref(q.astype(np.float64), scale.astype(np.float64), bias.astype(np.float64), f64(x))
+    want = want + (f64(a) if add else 0)
+    assert np.isfinite(want.astype(np.float32)).all()
+    # as in test_linear; with codes as 16 + code a weight's part of the sums is up to 31 scales, and so is the bias's
+    big = np.abs(f64(x)).reshape(T, K // 64, 64).sum(2) @ (31 * scale.astype(np.float64).T)
+    tol = (64 + 4 + K / 64 + 8 + 8 + 3) * EPS * (mag + big) + 2 * EPS * np.abs(want) * 1.0001
+    assert (np.abs(f64(y) - want) <= tol).all()
+
+
 def test_linear_codes_reach_their_places(L):
     """Weights that single out one input each: every nibble of the layout is found."""
     rng = np.random.default_rng(5)
