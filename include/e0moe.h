@@ -503,8 +503,8 @@ int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_
  * add (NULL or given; may be y): y_type (E0_F32, E0_F16 or E0_BF16) with rows
  * y_ld / add_ld elements apart.  Every product and the sums over a group of 64
  * inputs are exact or fp32, whatever the types (an fp32 x is not rounded);
- * sums are fp32 in an order that only the sizes decide, so equal calls give
- * equal bits.  Rows of finite values give finite ones unless y or scale * |x|
+ * sums are fp32 in an order that only the sizes and the device decide, so equal
+ * calls give equal bits.  Rows of finite values give finite ones unless y or scale * |x|
  * passes fp32's range.  A row of x that holds a NaN or infinity gives a row of y that
  * is not finite; other rows are not touched by it.  Any T: the weights are
  * read once for every 8 to 32 rows, so the call is made for decode batches,

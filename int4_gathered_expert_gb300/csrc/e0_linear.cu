@@ -4,6 +4,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include "e0_first.h"
 #include "e0_internal.h"
 #include "e0_types.cuh"
 
@@ -620,21 +621,21 @@ void cluster_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, dim3 grid,
     cfg.numAttrs = grid.y > 1 ? 1 : 0;
 }
 
-// Clusters of S blocks that the GPU holds at once; asked for once.
+// Clusters of S blocks that the current device, dev, holds at once.  The order of y's
+// sums depends on it, so the first answer stays.
 template <void (*kernel)(LinArgs)>
-int room(int S, size_t smem) {
-    static std::atomic<int> known[9];
-    int n = known[S].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    cluster_launch(cfg, at, dim3(1, S), smem, 0);
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();  // not the call's
-        return 2 * num_sms() / S;
-    }
-    known[S].store(n, std::memory_order_relaxed);
-    return n;
+int room(int dev, int S, size_t smem) {
+    static FirstAnswer<9> known;
+    return known.get(dev, S, 2 * num_sms() / S, [&]() {
+        const cudaError_t before = cudaPeekAtLastError();
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        cluster_launch(cfg, at, dim3(1, S), smem, 0);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+        if (before == cudaSuccess) cudaGetLastError();  // an error of this question, not of the call
+        return 0;
+    });
 }
 
 // most: the most dynamic shared memory that any launch of the kernel wants.
@@ -661,10 +662,11 @@ int launch(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
 template <void (*kernel)(LinArgs)>
 int split_of(long long tiles, int G, size_t smem) {
     constexpr int START = 12;
-    int best = 1;
+    int best = 1, dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
     long long least = LLONG_MAX;
     for (int S = 1; S <= 8 && (S == 1 || G / S >= 4); ++S) {
-        const long long n = room<kernel>(S, smem), groups = (tiles + n - 1) / n * ((G + S - 1) / S + START);
+        const long long n = room<kernel>(dev, S, smem), groups = (tiles + n - 1) / n * ((G + S - 1) / S + START);
         if (groups < least) least = groups, best = S;
     }
     return best;

@@ -81,6 +81,40 @@ def test_pack_linear_refusals_and_sizes(L):
     assert L.e0_pack_linear(L.QTensor(P, P + 1, P), 16, 64, P, **no) == L.E0_ERR_ARG
 
 
+FIRST = r"""
+#include <cstdio>
+#include "e0_first.h"
+int main() {
+    e0::FirstAnswer<9> a;
+    int asked = 0;
+    const auto says = [&](int n) { return [&asked, n]() { ++asked; return n; }; };
+    printf("%d ", a.get(0, 3, 38, says(0)));    // no answer: the other number
+    printf("%d ", a.get(0, 3, 38, says(50)));   // ... and the same one ever after
+    printf("%d ", a.get(0, 4, 38, says(50)));   // another question
+    printf("%d ", a.get(1, 3, 38, says(44)));   // another device
+    printf("%d ", a.get(1, 3, 38, says(45)));
+    printf("%d %d ", a.get(-1, 3, 38, says(50)), a.get(64, 3, 38, says(50)));
+    printf("%d ", a.get(2, 3, 38, [&]() { return a.get(2, 3, 38, says(41)) + 1; }));  // the answer of a call in between
+    printf("%d\n", asked);
+}
+"""
+
+
+def test_the_first_answer_for_a_device_stays(tmp_path):
+    """How many parts K is split into, and so the order of the linear's sums, goes by what the runtime said first."""
+    import shutil
+    import subprocess
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    (tmp_path / "first.cpp").write_text(FIRST)
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "int4_gathered_expert_gb300", "csrc")
+    exe = str(tmp_path / "first")
+    subprocess.run([cxx, "-std=c++17", "-I", csrc, str(tmp_path / "first.cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, check=True).stdout
+    assert out.split() == ["38", "38", "50", "44", "44", "38", "38", "41", "4"]
+
+
 def state(L, **c):
     f = dict(block_table=P, ctx_len=P, free_list=P, free_count=P, B=2, max_blocks=4, block_tokens=16, n_blocks=8)
     f.update(c)
