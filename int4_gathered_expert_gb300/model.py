@@ -5,6 +5,7 @@ used for device memory and streams only; all arithmetic runs in libe0moe.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from typing import Dict, List, Optional
 
@@ -16,6 +17,15 @@ from . import lib as L
 
 def _dev(a: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a)).to(device, non_blocking=False)
+
+
+def _on(stream):
+    """torch's calls on the stream that a call takes (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 class DeviceQBank:
@@ -403,11 +413,14 @@ class BatchDecoder:
 
     def step(self, x: torch.Tensor, new_len: torch.Tensor, window: int = 0, stream=None) -> torch.Tensor:
         """x fp32 [T, H], new_len int32 [B] on the device; the rows of x after the
-        last new token are any finite values, those of the result nothing of use.  Where a step finds no room
-        (E0_ST_POOL_FULL in ``status``), no token is cached."""
+        last new token are any finite values, those of the result nothing of use.
+        The result is the decoder's own buffer: the next step writes over it.  Where a
+        step finds no room (E0_ST_POOL_FULL in ``status``), no token is cached."""
         sd, a, c, T, H = self.sd, self.a, self.cache, self.T, self.sd.H
         kw = dict(stream=stream)
         c.plan(new_len, T, self.cu_q, self.slots, status=self.status, **kw)
+        with _on(stream):
+            self.o.zero_()  # attention leaves the rows after the last new token, which an earlier step may have used
         src, delta = x, None
         for l in range(sd.L):
             L.e0_rmsnorm_q8(src, delta, self.norm[l], T, H, L.E0_F32, 1e-6, H, H, self.r, None, self.q8, self.q8_scale,

@@ -169,6 +169,43 @@ def test_a_full_pool_caches_nothing(L):
     assert L.e0_read_status(bd.status) == 0 and bd.cache.ctx.tolist() == [1, 32]
 
 
+@pytest.mark.parametrize("how", ["current", "stream", "handle"])
+def test_a_row_that_overflowed_does_not_stay(L, how):
+    """A query beyond fp16 spoils its own row; a step with fewer tokens after it raises nothing and is as it would be
+    without."""
+    a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
+    stream = {"current": None, "stream": torch.cuda.Stream(), "handle": torch.cuda.Stream()}[how]
+    arg = stream.cuda_stream if how == "handle" else stream
+    pair = []
+    for _ in range(2):
+        m, attn, bd = decoder(1, 2, 8, 8, 4, a)
+        bd.norm[0][0] = 1e9  # the first column, times this, passes fp16
+        pair.append(bd)
+    x = torch.randn((8, 256), generator=torch.Generator().manual_seed(2)).cuda()
+    x[:, 0] = 0
+    wild = x.clone()
+    wild[6, 0] = 1
+    torch.cuda.synchronize()
+
+    def step(bd, x, lens):
+        new = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        out = bd.step(x, new, stream=arg)
+        torch.cuda.synchronize()
+        st = L.e0_read_status(bd.status)
+        bd.status.zero_()
+        return out.clone(), st
+
+    _, st = step(pair[0], wild, [3, 5])
+    assert st & L.E0_ST_NONFINITE
+    assert step(pair[1], x, [3, 5])[1] == 0
+    for lens in ([2, 0], [1, 0]):
+        got, st = step(pair[0], x, lens)
+        want, _ = step(pair[1], x, lens)
+        n = sum(lens)
+        assert st == 0 and torch.isfinite(got).all() and torch.equal(got[:n], want[:n])
+
+
 def test_decoder_refuses(L):
     from int4_gathered_expert_gb300.model import BatchDecoder
     a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
