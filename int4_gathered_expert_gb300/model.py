@@ -387,12 +387,19 @@ class BatchDecoder:
             raise ValueError("one attention half a layer")
         if not 1 <= T <= L.E0_MAX_T_DECODE:
             raise ValueError("T is 1..%d" % L.E0_MAX_T_DECODE)
+        if len(cache.descs) < sd.L or any(c.Hkv != shape.Hkv or c.D != shape.D for c in cache.descs):
+            raise ValueError("the cache has other layers or heads than the attention")
+        row, back = (shape.Hq + 2 * shape.Hkv) * shape.D, shape.Hq * shape.D
+        for w in attn:
+            n, k = w["qkv"]["codes"].shape, w["out"]["codes"].shape
+            if n != (row, sd.H // 2) or k != (sd.H, back // 2) or w["norm"].shape != (sd.H,):
+                raise ValueError("an attention half of other sizes than its shape and the stack's H")
         self.sd, self.a, self.cache, self.T = sd, shape, cache, T
         self.qkv = [LinearDev(w["qkv"], device) for w in attn]
         self.out = [LinearDev(w["out"], device) for w in attn]
         self.norm = [_dev(w["norm"], device) for w in attn]
         H, a = sd.H, shape
-        self.row = (a.Hq + 2 * a.Hkv) * a.D
+        self.row = row
 
         def buf(*s, dtype=torch.float32):
             return torch.zeros(s, dtype=dtype, device=device)
@@ -417,6 +424,10 @@ class BatchDecoder:
         The result is the decoder's own buffer: the next step writes over it.  Where a
         step finds no room (E0_ST_POOL_FULL in ``status``), no token is cached."""
         sd, a, c, T, H = self.sd, self.a, self.cache, self.T, self.sd.H
+        if x.dtype != torch.float32 or x.shape != (T, H) or not x.is_cuda or not x.is_contiguous():
+            raise ValueError("x is contiguous fp32 [%d, %d] on the device" % (T, H))
+        if new_len.dtype != torch.int32 or new_len.shape != (c.B,) or not new_len.is_cuda or not new_len.is_contiguous():
+            raise ValueError("new_len is contiguous int32 [%d] on the device" % c.B)
         kw = dict(stream=stream)
         c.plan(new_len, T, self.cu_q, self.slots, status=self.status, **kw)
         with _on(stream):

@@ -214,3 +214,29 @@ def test_decoder_refuses(L):
         BatchDecoder(bd.sd, attn + attn, a, bd.cache, 4)
     with pytest.raises(ValueError):
         BatchDecoder(bd.sd, attn, a, bd.cache, 65)
+
+
+def test_decoder_refuses_what_does_not_fit(L):
+    """Caches, weights and inputs whose sizes the kernels would read past."""
+    from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev
+    a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
+    _, attn, bd = decoder(1, 2, 4, 4, 8, a)
+    for cache in (KvCacheDev(1, 2, 4, 8, 4, 64, 16), KvCacheDev(1, 2, 4, 8, 2, 128, 16), KvCacheDev(0, 2, 4, 8, 2, 64, 16)):
+        with pytest.raises(ValueError):
+            BatchDecoder(bd.sd, attn, a, cache, 4)
+    BatchDecoder(bd.sd, attn, a, KvCacheDev(2, 2, 4, 8, 2, 64, 16), 4)  # more layers than are used
+    other = synth.attention(1, 0, synth.TINY.H, synth.AttnShape(Hq=4, Hkv=2, D=64))
+    narrow = synth.attention(1, 0, 128, a)
+    for half in (other, narrow, dict(attn[0], out=other["out"]), dict(attn[0], norm=attn[0]["norm"][:-1])):
+        with pytest.raises(ValueError):
+            BatchDecoder(bd.sd, [half], a, bd.cache, 4)
+    x = torch.zeros((4, 256), device="cuda")
+    new = torch.ones(2, dtype=torch.int32, device="cuda")
+    for bad in (x[:3], x.half(), x[:, :128], x.cpu(), torch.zeros((256, 4), device="cuda").t(), x.view(-1)):
+        with pytest.raises(ValueError):
+            bd.step(bad, new)
+    for bad in (new.long(), new[:1], new.cpu(), torch.ones(4, dtype=torch.int32, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            bd.step(x, bad)
+    bd.step(x, new)
+    assert L.e0_read_status(bd.status) == 0 and bd.cache.ctx.tolist() == [1, 1]
