@@ -357,6 +357,7 @@ class KvCacheDev:
         self.free_count = torch.full((1,), n_blocks, dtype=torch.int32, device=device)
         self.state = L.KvState(self.table.data_ptr(), self.ctx.data_ptr(), self.free.data_ptr(),
                                self.free_count.data_ptr(), B, max_blocks, block_tokens, n_blocks)
+        torch.cuda.synchronize()  # any stream may use it from here on
 
     def plan(self, new_len, T_cap, cu_q, slots, positions=None, seq_ids=None, status=None, stream=None):
         """Room for new_len more tokens of each sequence; lengths and stack move in place."""
@@ -417,6 +418,7 @@ class BatchDecoder:
         self.aws = buf(self.aws_bytes, dtype=torch.uint8)
         self.status = buf(1, dtype=torch.int32)
         self.r_out = buf(T, H)
+        torch.cuda.synchronize()  # any stream may take the steps
 
     def step(self, x: torch.Tensor, new_len: torch.Tensor, window: int = 0, stream=None) -> torch.Tensor:
         """x fp32 [T, H], new_len int32 [B] on the device; the rows of x after the

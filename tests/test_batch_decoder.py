@@ -206,6 +206,24 @@ def test_a_row_that_overflowed_does_not_stay(L, how):
         assert st == 0 and torch.isfinite(got).all() and torch.equal(got[:n], want[:n])
 
 
+def test_a_new_cache_is_ready_for_any_stream(L):
+    """What fills it is not still waiting on the stream that was current."""
+    from int4_gathered_expert_gb300.model import KvCacheDev
+    other = torch.cuda.Stream()
+    new = torch.full((3,), 20, dtype=torch.int32, device="cuda")
+    cu, slots = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(60, dtype=torch.int64, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    keep = KvCacheDev(1, 3, 100, 8, 2, 64, 16)
+    keep.plan(new, 60, cu, slots, status=st, stream=other)  # the first call of everything
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a tenth of a second of work that the constructor's comes after
+    c = KvCacheDev(1, 3, 100, 8, 2, 64, 16)
+    c.plan(new, 60, cu, slots, status=st, stream=other)
+    torch.cuda.synchronize()
+    assert L.e0_read_status(st) == 0
+    assert c.ctx.tolist() == [20] * 3 and c.free_count.item() == 94 and c.table[:, :2].flatten().tolist() == list(range(6))
+
+
 def test_decoder_refuses(L):
     from int4_gathered_expert_gb300.model import BatchDecoder
     a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
