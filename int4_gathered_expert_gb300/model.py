@@ -7,7 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
-from typing import Dict, List, Optional
+from typing import Callable, Dict, List, Optional
 
 import numpy as np
 import torch
@@ -374,16 +374,20 @@ class BatchDecoder:
     MoE, on a StackDev's weights.  For each layer:
 
         r += MoE of the layer before; h = norm(r) * w in 8 bits
-        q, k, v = W_qkv h (fp16); k, v into the cache
+        q, k, v = W_qkv h (fp16); edit(layer, qkv, positions); k, v into the cache
         r += W_out attention(q)
         MoE(rmsnorm(r)), with the layer's own routing (batches do not predict)
 
     attn: one ``synth.attention`` dict a layer.  A step takes up to T tokens, new_len[b]
-    of each sequence in order, as rows of x (T <= 64, the MoE block's limit).  All
-    of a step's work is on one stream and allocates nothing, so a step can be
-    captured into a CUDA graph."""
+    of each sequence in order, as rows of x (T <= 64, the MoE block's limit).
+    edit: what a model does to queries and keys before they meet (rotary embeddings,
+    norms), or None: called on the step's stream with the layer, qkv fp16 [T, (Hq + 2
+    Hkv) D] (queries, keys, values; to be changed in place) and the rows' positions
+    int32 [T], -1 after the last new token.  All of a step's work is on one stream and
+    allocates nothing but what edit does, so a step can be captured into a CUDA graph."""
 
-    def __init__(self, sd: StackDev, attn: List[dict], shape, cache: KvCacheDev, T: int, device="cuda"):
+    def __init__(self, sd: StackDev, attn: List[dict], shape, cache: KvCacheDev, T: int, device="cuda",
+                 edit: Optional[Callable[[int, torch.Tensor, torch.Tensor], None]] = None):
         if len(attn) != sd.L:
             raise ValueError("one attention half a layer")
         if not 1 <= T <= L.E0_MAX_T_DECODE:
@@ -395,7 +399,7 @@ class BatchDecoder:
             n, k = w["qkv"]["codes"].shape, w["out"]["codes"].shape
             if n != (row, sd.H // 2) or k != (sd.H, back // 2) or w["norm"].shape != (sd.H,):
                 raise ValueError("an attention half of other sizes than its shape and the stack's H")
-        self.sd, self.a, self.cache, self.T = sd, shape, cache, T
+        self.sd, self.a, self.cache, self.T, self.edit = sd, shape, cache, T, edit
         self.qkv = [LinearDev(w["qkv"], device) for w in attn]
         self.out = [LinearDev(w["out"], device) for w in attn]
         self.norm = [_dev(w["norm"], device) for w in attn]
@@ -410,7 +414,7 @@ class BatchDecoder:
         self.x_qkv = buf(T, self.row, dtype=torch.float16)
         self.o = buf(T, a.Hq * a.D, dtype=torch.float16)
         self.cu_q = buf(cache.B + 1, dtype=torch.int32)
-        self.slots = buf(T, dtype=torch.int64)
+        self.slots, self.positions = buf(T, dtype=torch.int64), buf(T, dtype=torch.int32)
         self.inds, self.w = buf(T, sd.K, dtype=torch.int32), buf(T, sd.K)
         self.ws_bytes = L.e0_workspace_size(0, T, sd.H, sd.I, sd.E, sd.K)
         self.ws = buf(self.ws_bytes, dtype=torch.uint8)
@@ -431,7 +435,7 @@ class BatchDecoder:
         if new_len.dtype != torch.int32 or new_len.shape != (c.B,) or not new_len.is_cuda or not new_len.is_contiguous():
             raise ValueError("new_len is contiguous int32 [%d] on the device" % c.B)
         kw = dict(stream=stream)
-        c.plan(new_len, T, self.cu_q, self.slots, status=self.status, **kw)
+        c.plan(new_len, T, self.cu_q, self.slots, self.positions, status=self.status, **kw)
         with _on(stream):
             self.o.zero_()  # attention leaves the rows after the last new token, which an earlier step may have used
         src, delta = x, None
@@ -441,6 +445,9 @@ class BatchDecoder:
             p = self.qkv[l]
             L.e0_linear_forward(p.data, p.N, p.K, self.q8, L.E0_E4M3, H, self.q8_scale, T, None, 0, self.x_qkv, L.E0_F16,
                                 self.row, **kw)
+            if self.edit is not None:
+                with _on(stream):
+                    self.edit(l, self.x_qkv, self.positions)
             k = self.x_qkv.data_ptr() + 2 * a.Hq * a.D
             v = k + 2 * a.Hkv * a.D
             L.e0_kv_append(c.descs[l], k, v, L.E0_F16, self.row, self.row, self.slots, T, self.status, **kw)

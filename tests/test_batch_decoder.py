@@ -28,13 +28,13 @@ def L():
     return lib
 
 
-def decoder(n_layers, B, T, n_blocks, max_blocks, a, seed=21, shared=True):
+def decoder(n_layers, B, T, n_blocks, max_blocks, a, seed=21, shared=True, **kw):
     from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev, StackDev
     shape = synth.StackShape(layer=synth.TINY, n_layers=n_layers, owners=(), shared_expert=shared, seed=seed)
     m = synth.stack_model(shape, n_tokens=1, threads=2)
     attn = [synth.attention(seed, l, synth.TINY.H, a) for l in range(n_layers)]
     cache = KvCacheDev(n_layers, B, n_blocks, max_blocks, a.Hkv, a.D, a.block_tokens)
-    return m, attn, BatchDecoder(StackDev(m), attn, a, cache, T)
+    return m, attn, BatchDecoder(StackDev(m), attn, a, cache, T, **kw)
 
 
 def f64(t):
@@ -99,6 +99,94 @@ def test_one_layer_stage_by_stage(L):
         y = O.moe_block(hh, O.BankExperts(m.banks[0]), bd.inds.cpu().numpy()[:n], f64(bd.w)[:n], m.shared[0])
         assert rel_l2(f64(bd.y)[:n], y) <= REL_L2
         assert torch.equal(out, bd.r + bd.y)
+
+
+def rotary(a, base=100.0):
+    """Rotary embeddings of queries and keys, as an edit of BatchDecoder."""
+    freq = base ** (-torch.arange(a.D // 2, device="cuda", dtype=torch.float64) / (a.D // 2))
+
+    def edit(layer, qkv, positions):
+        angle = positions.clamp(min=0).double()[:, None, None] * freq * (layer + 1)
+        n = (a.Hq + a.Hkv) * a.D
+        x = qkv[:, :n].reshape(len(qkv), -1, 2, a.D // 2).double()
+        c, s = angle.cos(), angle.sin()
+        out = torch.stack([x[:, :, 0] * c - x[:, :, 1] * s, x[:, :, 1] * c + x[:, :, 0] * s], 2)
+        qkv[:, :n] = out.reshape(len(qkv), n).half()
+
+    return edit
+
+
+@pytest.mark.parametrize("how", ["current", "stream"])
+def test_rotary_embeddings_between_projection_and_cache(L, how):
+    """What the edit leaves is what is cached and asked with; it sees each row's position, and the step's stream."""
+    a = synth.AttnShape(Hq=4, Hkv=2, D=64, block_tokens=16)
+    B, T, H = 2, 9, synth.TINY.H
+    seen, rope = [], rotary(a)
+
+    def edit(layer, qkv, positions):
+        was = qkv.clone()
+        rope(layer, qkv, positions)
+        seen.append((layer, was, qkv.clone(), positions.clone(), torch.cuda.current_stream().cuda_stream))
+
+    stream = torch.cuda.Stream() if how == "stream" else None
+    m, attn, bd = decoder(2, B, T, 12, 6, a, edit=edit)
+    _, _, plain = decoder(2, B, T, 12, 6, a)
+    c = bd.cache
+    ref = [R.Cache(12, a.Hkv, 16, a.D) for _ in range(2)]
+    rng = np.random.default_rng(8)
+    ctx = np.zeros(B, int)
+    for new in ([5, 3], [1, 1], [8, 0], [0, 9], [1, 1]):
+        x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).cuda()
+        lens = torch.tensor(new, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        seen.clear()
+        bd.step(x, lens, stream=stream)
+        torch.cuda.synchronize()
+        assert L.e0_read_status(bd.status) == 0 and [e[0] for e in seen] == [0, 1]
+        n = sum(new)
+        want = [int(ctx[b]) + i for b in range(B) for i in range(new[b])] + [-1] * (T - n)
+        ctx += new
+        slots, table, cu = bd.slots.cpu().numpy(), c.table.cpu().numpy(), bd.cu_q.cpu().numpy()
+        for layer, was, qkv, pos, on in seen:
+            assert pos.tolist() == want
+            assert on == (stream or torch.cuda.current_stream()).cuda_stream
+            v = f64(qkv)
+            ref[layer].append(v[:, a.Hq * a.D:(a.Hq + a.Hkv) * a.D].reshape(T, a.Hkv, a.D),
+                              v[:, (a.Hq + a.Hkv) * a.D:].reshape(T, a.Hkv, a.D), slots)
+            assert np.array_equal(codes_of(c.k[layer]), R.decode(ref[layer].k))
+            assert np.array_equal(codes_of(c.v[layer]), R.decode(ref[layer].v))
+        o, q = f64(bd.o).reshape(T, a.Hq, a.D), f64(seen[1][2])[:, :a.Hq * a.D].reshape(T, a.Hq, a.D)
+        for b in range(B):
+            if new[b]:
+                kk, vv = ref[1].row(table[b], ctx[b])
+                wo, _, tol, _ = R.attention(q[cu[b]:cu[b + 1]], kk, vv, float(np.float32(a.D ** -0.5)), ctx[b], 0)
+                assert (np.abs(o[cu[b]:cu[b + 1]] - wo) <= tol + 2.0 ** -11 * np.abs(wo) * 1.001 + 2.0 ** -25).all()
+        plain.step(x, lens)
+        assert torch.equal(plain.positions, bd.positions)
+        moved = [p > 0 for p in want[:n]]
+        assert not np.array_equal(f64(seen[0][1])[:n][moved], f64(seen[0][2])[:n][moved])
+
+
+def test_a_captured_step_with_an_edit(L):
+    a = synth.AttnShape(Hq=4, Hkv=2, D=64, block_tokens=16)
+    B, T = 3, 4
+    _, _, eager = decoder(2, B, T, 20, 6, a, edit=rotary(a))
+    _, _, graph = decoder(2, B, T, 20, 6, a, edit=rotary(a))
+    x = torch.zeros((T, 256), device="cuda")
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    graph.step(x, new)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        graph.step(x, new)
+    rng = np.random.default_rng(9)
+    for _ in range(10):
+        x.copy_(torch.from_numpy(rng.standard_normal((T, 256)).astype(np.float32)))
+        lens = rng.multinomial(T, np.ones(B) / B)
+        new.copy_(torch.from_numpy(lens.astype(np.int32)))
+        g.replay()
+        assert torch.equal(graph.r_out, eager.step(x, new))
+    assert L.e0_read_status(graph.status) == 0 and torch.equal(graph.cache.ctx, eager.cache.ctx)
 
 
 def test_layers_follow_one_another(L):
