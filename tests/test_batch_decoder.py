@@ -240,6 +240,43 @@ def test_a_captured_step_replays(L):
     assert torch.equal(graph.cache.table, eager.cache.table) and torch.equal(graph.cache.ctx, eager.cache.ctx)
 
 
+def test_many_query_rows_over_a_long_context(L):
+    """Several new tokens of wide groups on contexts of thousands: more than a tile of query rows a KV head."""
+    a = synth.AttnShape(Hq=16, Hkv=2, D=64, block_tokens=64)
+    B, T = 3, 60
+    m, attn, bd = decoder(1, B, T, 130, 60, a)
+    c = bd.cache
+    ctx = np.array([3500, 40, 2000])
+    need = -(-ctx // 64)
+    rng = np.random.default_rng(11)
+    ref = R.Cache(130, 2, 64, 64)
+    for x, codes, dst, scale in ((ref.k, c.k, 0, ref.ks), (ref.v, c.v, 1, ref.vs)):  # what earlier steps left
+        x[:] = R.encode(rng.standard_normal(x.shape) * 100)
+        codes[0].copy_(torch.from_numpy(x))
+        scale[:] = 2.0 ** -7
+        (c.v_scale if dst else c.k_scale)[0].copy_(torch.from_numpy(scale))
+    ids = c.free.cpu().numpy()[::-1].copy()
+    at = 0
+    for b in range(B):
+        c.table[b, :need[b]] = torch.from_numpy(ids[at:at + need[b]]).cuda()
+        at += need[b]
+    c.free_count.fill_(130 - at)
+    c.ctx.copy_(torch.from_numpy(ctx.astype(np.int32)))
+    for new in ([20, 1, 30], [1, 1, 1]):
+        x = torch.from_numpy(rng.standard_normal((T, 256)).astype(np.float32)).cuda()
+        bd.step(x, torch.tensor(new, dtype=torch.int32, device="cuda"))
+        assert L.e0_read_status(bd.status) == 0
+        ctx = ctx + new
+        qkv, slots = f64(bd.x_qkv), bd.slots.cpu().numpy()
+        ref.append(qkv[:, 1024:1152].reshape(T, 2, 64), qkv[:, 1152:].reshape(T, 2, 64), slots)
+        table, cu, o = c.table.cpu().numpy(), bd.cu_q.cpu().numpy(), f64(bd.o).reshape(T, 16, 64)
+        for b in range(B):
+            kk, vv = ref.row(table[b], ctx[b])
+            q = qkv[cu[b]:cu[b + 1], :1024].reshape(-1, 16, 64)
+            wo, _, tol, _ = R.attention(q, kk, vv, 0.125, ctx[b], 0)
+            assert (np.abs(o[cu[b]:cu[b + 1]] - wo) <= tol + 2.0 ** -11 * np.abs(wo) * 1.001 + 2.0 ** -25).all()
+
+
 def test_a_full_pool_caches_nothing(L):
     a = synth.AttnShape(Hq=2, Hkv=2, D=64, block_tokens=16)
     m, attn, bd = decoder(1, 2, 40, 4, 8, a)

@@ -281,6 +281,42 @@ def test_linear_extreme_and_non_finite_inputs(L, xt):
     assert not torch.isfinite(y[2:]).any()
 
 
+@pytest.mark.parametrize("T", [5, 12, 33, 70])
+@pytest.mark.parametrize("xt", [F32, F16, BF16, E4M3])
+@pytest.mark.parametrize("more,skip", [(0, 0), (64, 0), (3, 1)])
+def test_linear_rows_of_any_kind(L, T, xt, more, skip):
+    """Strided and unaligned rows for few and for many of them, y over add in rows longer than N, K split over a cluster;
+    a row's values, a NaN or an infinity among them, do not reach the other rows."""
+    rng = np.random.default_rng(T + more)
+    N, K = 300, 1344
+    w, q, s, b, keep = make_linear(L, N, K, rng)
+    ld = K + more
+    x, xs, xv = make_x(T, K, xt, rng, ld, skip)
+    a = dev(rng.standard_normal((T + 2, N + 5)), torch.float32)
+    y = a.clone()
+    L.e0_linear_forward(w, N, K, x, xt, ld, xs, T, y, N + 5, y, F32, N + 5)
+    want, mag = linear_ref(q, s, b, xv)
+    want = want + f64(a)[:T, :N]
+    # as in test_linear
+    tol = (64 + 4 + K / 64 + 8 + 8 + 3) * EPS * mag + 2 * EPS * np.abs(want) * 1.0001
+    assert (np.abs(f64(y)[:T, :N] - want) <= tol).all()
+    assert torch.equal(y[:T, N:], a[:T, N:]) and torch.equal(y[T:], a[T:])
+    rows = torch.as_strided(x, (T, K), (ld, 1))
+    for row, value in ((0, 2.0), (T - 1, float("nan")), (T // 2, float("inf"))):
+        kept = rows[row].clone()
+        if xt != E4M3:
+            rows[row, 70] = value
+        else:
+            rows[row, 70] = 0x40 if value == 2 else 0x7F  # 2 and NaN; there is no infinity
+        z = a.clone()
+        L.e0_linear_forward(w, N, K, x, xt, ld, xs, T, z, N + 5, z, F32, N + 5)
+        others = torch.arange(T + 2, device="cuda") != row
+        assert torch.equal(z[others], y[others])
+        assert (torch.isfinite(z[row, :N]).all() and not torch.equal(z[row], y[row])) if value == 2 else \
+            not torch.isfinite(z[row, :N]).any()
+        rows[row] = kept
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 40, 128), (8, 300, 4160), (12, 300, 640), (40, 130, 4096)])
 @pytest.mark.parametrize("xt", [F32, BF16])
 @pytest.mark.parametrize("add", [False, True])
