@@ -468,9 +468,11 @@ int e0_moe_prefill_forward(const uint16_t* X, int T, const e0_slot_pool* bank,
  * apart; w fp32 [H].  Outputs, each NULL or contiguous: r_out dtype [T][H]
  * receives s, h dtype [T][H], q [T][H] with q_scale fp32 [T][ceil(H/64)] (both
  * or neither).  r_out may be r or d where their rows are contiguous; other
- * overlaps are not allowed.  Sums are fp32.  A NaN or infinity in h is kept in
- * the output h; in q its whole group is written as zeros with scale 0 and
- * E0_ST_NONFINITE is raised.  A group whose largest magnitude is below 2^-110
+ * overlaps are not allowed.  Sums are fp32: a row whose sum of squares passes
+ * their range (values around 2^64 and more) has an h of zeros, and
+ * E0_ST_NONFINITE is raised.  A NaN or infinity in h is kept in the output h; in
+ * q its whole group is written as zeros with scale 0 and E0_ST_NONFINITE is
+ * raised.  A group whose largest magnitude is below 2^-110
  * is written as zeros with scale 0.  Errors: no r, no output, or one of q and
  * q_scale alone -> E0_ERR_NULL; another dtype, a row stride below H, eps < 0,
  * h equal to r, d or r_out, r_out over rows that are not contiguous, or a

@@ -131,6 +131,10 @@ E0_DEV float max_abs(float a, float b) {
     return r;
 }
 
+// Whether the squares' sum has passed fp32's range: a root of infinity, whose inverse is 0
+// (that of the largest finite number is 2^-64).
+E0_DEV bool sum_overflowed(const NormArgs& A, float rstd) { return rstd == 0.f && (A.h || A.q); }
+
 // A chunk's outputs; all lanes of a warp call it.  Returns whether its group holds a
 // value that is not finite.
 // h / c = 448 t / max|t| whatever the root is, so the codes come from t = s * w (times
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_q8(NormArgs A) {
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < CH; ++j) bad |= finish_chunk<TY, VEC>(A, row, 8 * (tid + j * nt), rstd, v[j]);
-    if (bad && (tid & 7) == 0) set_status(A.st, E0_ST_NONFINITE);
+    if ((bad && (tid & 7) == 0) || (tid == 0 && sum_overflowed(A, rstd))) set_status(A.st, E0_ST_NONFINITE);
 }
 
 constexpr int NORM_WARPS = 8;
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) k_rmsnorm_q8_rows(NormArgs A)
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < CH; ++j) bad |= finish_chunk<TY, true>(A, row, 8 * (lane + j * 32), rstd, v[j]);
-    if (bad && (lane & 7) == 0) set_status(A.st, E0_ST_NONFINITE);
+    if ((bad && (lane & 7) == 0) || (lane == 0 && sum_overflowed(A, rstd))) set_status(A.st, E0_ST_NONFINITE);
 }
 
 template <int TY, bool VEC>

@@ -128,6 +128,28 @@ def test_norm_zero_tiny_and_non_finite_rows(L):
     L.e0_rmsnorm_q8(r, None, None, 0, 128, F32, 1e-6, 128, 0, None, h, None, None)
 
 
+@pytest.mark.parametrize("T,H_", [(3, 256), (3, 65), (1300, 64), (2, 8200)])
+def test_norm_says_where_the_sum_of_squares_overflows(L, T, H_):
+    """2^63.5 squared, twice, is 2^128; a row of 2^60 is still a row."""
+    r = torch.zeros((T, H_), device="cuda")
+    r[:, 0], r[:, 1] = 2.0 ** 60, -2.0 ** 60
+    h, q = torch.empty_like(r), torch.empty((T, H_), dtype=torch.uint8, device="cuda")
+    qs, st = torch.empty((T, -(-H_ // 64)), device="cuda"), status()
+    L.e0_rmsnorm_q8(r, None, None, T, H_, F32, 1e-6, H_, 0, None, h, q, qs, st)
+    assert L.e0_read_status(st) == 0
+    assert torch.allclose(h[:, 0], torch.full((T,), (H_ / 2) ** 0.5, device="cuda"), rtol=1e-6) and (q[:, 0] == 0x7E).all()
+    r[T - 1, :3] = 2.0 ** 64
+    for outs in ((h, None, None), (None, q, qs), (h, q, qs)):
+        st.zero_()
+        L.e0_rmsnorm_q8(r, None, None, T, H_, F32, 1e-6, H_, 0, None, *outs, st)
+        assert L.e0_read_status(st) == L.E0_ST_NONFINITE
+    assert (h[T - 1] == 0).all() and (q[T - 1] == 0).all() and (qs[T - 1] == 0).all()
+    assert (h[:T - 1, 0] > 1).all() and (q[:T - 1, 0] == 0x7E).all()
+    st.zero_()
+    L.e0_rmsnorm_q8(r, None, None, T, H_, F32, 1e-6, H_, 0, h, None, None, None, st)  # no norm is asked for
+    assert L.e0_read_status(st) == 0 and torch.equal(h, r)
+
+
 @pytest.mark.parametrize("T,H_", [(4, 128), (3, 65), (1300, 64), (2, 4104)])
 def test_norm_up_to_the_largest_numbers(L, T, H_):
     """Weights that bring h close to fp32's largest value: codes and scales as at any size."""
