@@ -598,6 +598,65 @@ def test_release_passes_over_places_without_a_block(L, B, bs, longest, wide, bad
     kv.check()
 
 
+def test_release_of_the_most_places(L):
+    """2^30 places without a block are passed over; more are refused."""
+    per = 1 << 26
+    table = torch.full((17, per), -1, dtype=torch.int32, device="cuda")
+    table[3, per - 1], table[15, 0], table[15, per - 1] = 5, 2, 7
+    ctx = torch.full((17,), 1 << 30, dtype=torch.int32, device="cuda")
+    free = torch.full((8,), -5, dtype=torch.int32, device="cuda")
+    free[:2] = torch.tensor([1, 6])
+    count = torch.full((1,), 2, dtype=torch.int32, device="cuda")
+    kv = L.KvState(table.data_ptr(), ctx.data_ptr(), free.data_ptr(), count.data_ptr(), 17, per, 16, 8)
+    mask, st = torch.ones(17, dtype=torch.uint8, device="cuda"), status()
+    L.e0_kv_release(kv, mask, ctx, count, st)
+    assert L.e0_read_status(st) == L.E0_ST_BAD_LENGTH
+    assert (ctx == 1 << 30).all() and count.item() == 2 and table[3, per - 1].item() == 5
+    mask[16] = 0
+    st.zero_()
+    L.e0_kv_release(kv, mask, ctx, count, st)
+    assert L.e0_read_status(st) == 0 and ctx.tolist() == [0] * 16 + [1 << 30]
+    assert count.item() == 5 and free.tolist() == [1, 6, 5, 2, 7, -5, -5, -5]
+    assert table[3, per - 1].item() == table[15, 0].item() == table[15, per - 1].item() == -1
+
+
+@pytest.mark.parametrize("B,M", [(3, 8), (200, 40)])
+def test_a_captured_plan_and_release(L, B, M):
+    """Sequences that come and go by the same graph, on a stream of its own, lengths and stack in place."""
+    rng = np.random.default_rng(M)
+    kv = Kv(L, B, 16, M, B * M // 2, rng, rng.integers(0, 30, B))
+    new, mask = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.uint8, device="cuda")
+    cap = 40 * B
+    cu, slots = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.zeros(cap, dtype=torch.int64, device="cuda")
+    st, stream = status(), torch.cuda.Stream()
+
+    def step(s=None):
+        L.e0_kv_release(kv.desc, mask, kv.d_ctx, kv.d_count, st, s)
+        L.e0_kv_plan(kv.desc, new, cap, kv.d_ctx, kv.d_count, cu, slots, status=st, stream=s)
+
+    torch.cuda.synchronize()
+    step(stream)  # the first call of everything: nothing comes, nothing goes
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step()
+    for _ in range(12):
+        gone = (rng.random(B) < 0.3) | (kv.ctx > 16 * M - 60)
+        for b in np.flatnonzero(gone):
+            kv.free += [int(x) for x in kv.table[b] if x >= 0]
+            kv.table[b], kv.ctx[b] = -1, 0
+        lens = rng.integers(0, 40, B)
+        lens[np.cumsum(lens // 16 + 2) > len(kv.free)] = 0
+        mask.copy_(dev(gone.astype(np.uint8)))
+        new.copy_(dev(lens.astype(np.int32)))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        want, _, _ = kv.plan_ref(lens)
+        assert L.e0_read_status(st) == 0 and slots[:len(want)].tolist() == want and (slots[len(want):] == -1).all()
+        kv.check()
+
+
 # ------------------------------------------------------------------ append
 
 
