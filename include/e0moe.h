@@ -463,7 +463,9 @@ int e0_moe_prefill_forward(const uint16_t* X, int T, const e0_slot_pool* bank,
  *     s = r + d                    rounded to dtype (d NULL: s = r)
  *     h = s / sqrt(mean(s^2) + eps) * w            (w NULL: no weight)
  *     c = max|h| / 448 over each group of 64 values (the last may be short)
- *     q = e4m3(h / c)              nearest, ties to even; h ~ c * q
+ *     q = e4m3(h / c)              nearest, ties to even; h ~ c * q (h / c is
+ *                                  formed in fp32: next to a border between two
+ *                                  codes either may come out)
  * r, d: dtype (E0_F32, E0_F16 or E0_BF16) with rows r_ld / d_ld elements
  * apart; w fp32 [H].  Outputs, each NULL or contiguous: r_out dtype [T][H]
  * receives s, h dtype [T][H], q [T][H] with q_scale fp32 [T][ceil(H/64)] (both
@@ -505,17 +507,17 @@ int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_
  * add (NULL or given; may be y): y_type (E0_F32, E0_F16 or E0_BF16) with rows
  * y_ld / add_ld elements apart.  Every product and the sums over a group of 64
  * inputs are exact or fp32, whatever the types (an fp32 x is not rounded);
- * sums are fp32 in an order that only the sizes and the device decide, so equal
- * calls give equal bits.  Rows of finite values give finite ones unless y or scale * |x|
- * passes fp32's range.  A row of x that holds a NaN or infinity gives a row of y that
- * is not finite; other rows are not touched by it.  Any T: the weights are
- * read once for every 8 to 32 rows, so the call is made for decode batches,
- * not for long prompts (T, N or K beyond E0_MAX_*_LINEAR ->
- * E0_ERR_UNSUPPORTED). y must not overlap x.  Errors: a NULL x, y or w, or no
- * x_scale where x_type wants one -> E0_ERR_NULL; sizes not positive, K no
- * multiple of 64, an unknown type, a row stride below the row, a w that is not
- * 16-byte aligned, or a pointer that its element type does not align ->
- * E0_ERR_ARG. */
+ * sums are fp32 in an order that only the sizes and the device decide, so
+ * equal calls give equal bits.  Rows of finite values give finite ones unless
+ * y or scale * |x| passes fp32's range.  A row of x that holds a NaN or
+ * infinity gives a row of y that is not finite; other rows are not touched by
+ * it.  Any T: the weights are read once for every 8 to 32 rows, so the call is
+ * made for decode batches, not for long prompts (T, N or K beyond
+ * E0_MAX_*_LINEAR -> E0_ERR_UNSUPPORTED).  y must not overlap x.  Errors: a
+ * NULL x, y or w, or no x_scale where x_type wants one -> E0_ERR_NULL; sizes
+ * not positive, K no multiple of 64, an unknown type, a row stride below the
+ * row, a w that is not 16-byte aligned, or a pointer that its element type does
+ * not align -> E0_ERR_ARG. */
 int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type, int64_t x_ld,
                       const float* x_scale, int T, const void* add, int64_t add_ld, void* y, int y_type,
                       int64_t y_ld, e0_stream_t stream);
@@ -607,7 +609,8 @@ int e0_kv_append(const e0_kv_cache* cache, const void* k, const void* v, int dty
                  const int64_t* slots, int T, uint32_t* d_status, e0_stream_t stream);
 
 /* Workspace of e0_attn_decode (256-byte aligned; its contents need not be set
- * and are not kept; calls that may run at the same time need one each).  0 where a size is not supported. */
+ * and are not kept; calls that may run at the same time need one each).  0
+ * where a size is not supported. */
 size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
 
 /* Attention of the new tokens of B sequences over their cached tokens, the new
@@ -618,8 +621,8 @@ size_t e0_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * query head g and its KV head g / (Hq / Hkv):
  *     out = sum_j softmax_j(scale q.k_j) v_j,   lse = ln sum_j exp(scale q.k_j)
  * q, out: dtype (E0_F32, E0_F16 or E0_BF16), rows q_ld / out_ld elements
- * apart, [Hq][D] contiguous; lse fp32 [rows][Hq] or NULL.  block_table
- * [B][max_blocks]. A query that sees nothing gets out = 0 and lse = -infinity.
+ * apart, [Hq][D] contiguous, and do not overlap; lse fp32 [rows][Hq] or NULL.
+ * block_table [B][max_blocks].  A query that sees nothing gets out = 0 and lse = -infinity.
  * Rows from cu_q[B] on are left as they were.  Statistics and sums are fp32.
  * A ctx_len that is negative or needs more than max_blocks blocks raises
  * E0_ST_BAD_LENGTH and its queries see nothing; a cu_q that is negative, falls
