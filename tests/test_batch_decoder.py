@@ -28,13 +28,13 @@ def L():
     return lib
 
 
-def decoder(n_layers, B, T, n_blocks, max_blocks, a, seed=21, shared=True, **kw):
+def decoder(n_layers, B, T, n_blocks, max_blocks, a, seed=21, shared=True):
     from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev, StackDev
     shape = synth.StackShape(layer=synth.TINY, n_layers=n_layers, owners=(), shared_expert=shared, seed=seed)
     m = synth.stack_model(shape, n_tokens=1, threads=2)
     attn = [synth.attention(seed, l, synth.TINY.H, a) for l in range(n_layers)]
     cache = KvCacheDev(n_layers, B, n_blocks, max_blocks, a.Hkv, a.D, a.block_tokens)
-    return m, attn, BatchDecoder(StackDev(m), attn, a, cache, T, **kw)
+    return m, attn, BatchDecoder(StackDev(m), attn, a, cache, T)
 
 
 def f64(t):
@@ -101,6 +101,14 @@ def test_one_layer_stage_by_stage(L):
         assert torch.equal(out, bd.r + bd.y)
 
 
+def decoder_with(edit, n_layers, B, T, n_blocks, max_blocks, a):
+    """The same as decoder's, with an edit."""
+    from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev
+    _, attn, bd = decoder(n_layers, B, T, n_blocks, max_blocks, a)
+    cache = KvCacheDev(n_layers, B, n_blocks, max_blocks, a.Hkv, a.D, a.block_tokens)
+    return BatchDecoder(bd.sd, attn, a, cache, T, edit=edit)
+
+
 def rotary(a, base=100.0):
     """Rotary embeddings of queries and keys, as an edit of BatchDecoder."""
     freq = base ** (-torch.arange(a.D // 2, device="cuda", dtype=torch.float64) / (a.D // 2))
@@ -129,7 +137,7 @@ def test_rotary_embeddings_between_projection_and_cache(L, how):
         seen.append((layer, was, qkv.clone(), positions.clone(), torch.cuda.current_stream().cuda_stream))
 
     stream = torch.cuda.Stream() if how == "stream" else None
-    m, attn, bd = decoder(2, B, T, 12, 6, a, edit=edit)
+    bd = decoder_with(edit, 2, B, T, 12, 6, a)
     _, _, plain = decoder(2, B, T, 12, 6, a)
     c = bd.cache
     ref = [R.Cache(12, a.Hkv, 16, a.D) for _ in range(2)]
@@ -170,8 +178,7 @@ def test_rotary_embeddings_between_projection_and_cache(L, how):
 def test_a_captured_step_with_an_edit(L):
     a = synth.AttnShape(Hq=4, Hkv=2, D=64, block_tokens=16)
     B, T = 3, 4
-    _, _, eager = decoder(2, B, T, 20, 6, a, edit=rotary(a))
-    _, _, graph = decoder(2, B, T, 20, 6, a, edit=rotary(a))
+    eager, graph = decoder_with(rotary(a), 2, B, T, 20, 6, a), decoder_with(rotary(a), 2, B, T, 20, 6, a)
     x = torch.zeros((T, 256), device="cuda")
     new = torch.zeros(B, dtype=torch.int32, device="cuda")
     graph.step(x, new)
