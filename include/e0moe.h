@@ -103,7 +103,8 @@ enum { E0_ROUTE_SOFTMAX_TOPK = 0, E0_ROUTE_SIGMOID_GROUP = 1 };
 /* Limits of the kernels (E0_ERR_UNSUPPORTED beyond them). */
 enum { E0_MAX_E = 1024, E0_MAX_K = 32, E0_MAX_T_DECODE = 64, E0_MAX_LORA_RANK = 64 };
 enum { E0_MAX_NORM_H = 16384, E0_MAX_ROWS = 1 << 30, E0_MAX_SEQS = 4096, E0_MAX_CONTEXT = 1 << 30,
-       E0_MAX_T_LINEAR = 524280, E0_MAX_N_LINEAR = 1 << 28, E0_MAX_K_LINEAR = 1 << 20 };
+       E0_MAX_T_LINEAR = 524280, E0_MAX_N_LINEAR = 1 << 28, E0_MAX_K_LINEAR = 1 << 20,
+       E0_MAX_ROPE_D = 256, E0_MAX_ROPE_AXES = 4, E0_MAX_VOCAB = 1 << 18 };
 
 /* ---- element types of the calls that take one -------------------------
  * E0_E4M3 is the 8-bit float with 4 exponent and 3 mantissa bits, no infinity
@@ -521,6 +522,78 @@ int e0_pack_linear(const e0_qtensor* src, int N, int K, uint8_t* dst, e0_stream_
 int e0_linear_forward(const uint8_t* w, int N, int K, const void* x, int x_type, int64_t x_ld,
                       const float* x_scale, int T, const void* add, int64_t add_ld, void* y, int y_type,
                       int64_t y_ld, e0_stream_t stream);
+
+/* ---- queries and keys: norms for each head, rotation by position -------- */
+
+/* e0_rope::flags */
+enum {
+    E0_ROPE_ADJACENT = 1, /* pair i is the elements 2i, 2i + 1; otherwise i, i + rot / 2 */
+    E0_QK_NORM = 2        /* a norm for each head before the rotation                   */
+};
+
+typedef struct e0_rope {
+    const float* freq;    /* device [rot / 2]: a pair's angle per position, in radians  */
+    const uint8_t* axis;  /* device [rot / 2] or NULL (all 0): the axis of positions that
+                             turns a pair; n_axes and beyond count as the last          */
+    const float* q_norm;  /* device [D] or NULL: the norm's weight for queries          */
+    const float* k_norm;  /* device [D] or NULL: ... for keys                           */
+    int32_t D, rot;       /* head dimension; its first rot elements turn                */
+    int32_t n_axes;       /* 1 (text) .. E0_MAX_ROPE_AXES (time, height, width, ...)    */
+    int32_t flags;
+    float eps;            /* of the norm                                                */
+} e0_rope;
+
+/* Norm and turn the queries and keys of T tokens in one pass.  Row t of x holds Hq + Hk
+ * heads of D, queries first (Hk = 0: queries alone, Hq = 0: keys alone).  For each head:
+ *     h = x / sqrt(mean(x^2) + eps) * w      with E0_QK_NORM; w NULL: no weight
+ *     a_i = positions[axis[i]][t] * freq[i]
+ *     (y_i0, y_i1) = (h_i0 cos a_i - h_i1 sin a_i, h_i1 cos a_i + h_i0 sin a_i)
+ * and the elements from rot on are h's.  x, y: dtype (E0_F32, E0_F16 or E0_BF16) with
+ * rows x_ld / y_ld elements apart; y may be x where the strides are equal, other overlaps
+ * are not allowed.  positions int32, pos_ld elements from axis to axis; a row whose
+ * position on the first axis is negative (as e0_kv_plan writes it where there is no token) is
+ * left as it was, other axes' may be negative.  Sums and products are fp32, rounded
+ * once at the end; an angle is off by less than 2^-22 of a radian at any position (and a
+ * freq of NaN or infinity turns nothing).  A head to be normed whose sum of squares is
+ * not finite raises E0_ST_NONFINITE: zeros where it overflowed, NaN where a value is.
+ * Errors: NULL x, y, rope, positions, or freq with rot > 0 -> E0_ERR_NULL; sizes negative,
+ * no head, D or rot odd, rot > D, unknown flags or dtype, eps < 0 or NaN, strides below a
+ * row, n_axes out of range, a pointer that its element type does not align, y = x with
+ * another stride -> E0_ERR_ARG; D > E0_MAX_ROPE_D, T > E0_MAX_ROWS, Hq + Hk > 65536 ->
+ * E0_ERR_UNSUPPORTED. */
+int e0_qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const e0_rope* rope,
+               const int32_t* positions, int64_t pos_ld, void* y, int64_t y_ld, uint32_t* d_status,
+               e0_stream_t stream);
+
+/* ---- the next tokens from the logits ------------------------------------ */
+
+/* A row's rules: device arrays of T values, each NULL for its default in all rows. */
+typedef struct e0_sampling {
+    const float* temperature; /* 1; 0 (or less than 2^-100): the largest logit's token   */
+    const int32_t* top_k;     /* 0 and less: no limit                                    */
+    const float* top_p;       /* 1 and more: no limit; 0 and less: the first token alone */
+    const float* min_p;       /* 0 and less: no limit; more than 1 counts as 1           */
+} e0_sampling;
+
+/* Draw a token for each of T rows of V logits x (dtype E0_F32, E0_F16 or E0_BF16, rows ld
+ * elements apart; -infinity: never drawn).  The row's tokens in order of falling x, of
+ * equal ones the lower first, have the weights w = exp((x - max) / temperature).  Kept are
+ * the first n of them, the least of
+ *     top_k,
+ *     the smallest n with w_1 + .. + w_n >= top_p (w_1 + .. + w_top_k),
+ *     the number of tokens with w >= min_p,
+ * but one at least.  token [T] is the first kept token, by number, whose running sum of
+ * kept weights exceeds u[t] times their total (u = 1: the last).  Optional outputs (or
+ * NULL): logp [T] = ln(w / total), kept [T] = n.  u: device fp32 [T] in [0, 1], the caller's
+ * random numbers.  Weights are integers, 2^44 w, off by 2^-29 of themselves at most, and their sums exact:
+ * equal calls give equal tokens; a weight below 2^-44 is never drawn.  A row that holds
+ * NaN or +infinity or nothing but -infinity, or whose temperature is negative, infinite or
+ * NaN, whose u is outside [0, 1], or top_p or min_p NaN, gets token -1, logp -infinity and
+ * kept 0, and raises E0_ST_NONFINITE.  rules NULL: all defaults.  Errors: NULL x, u or
+ * token -> E0_ERR_NULL; T negative, V < 1, another dtype, ld < V, a pointer that its element type
+ * does not align -> E0_ERR_ARG; V > E0_MAX_VOCAB, T > 2^24 -> E0_ERR_UNSUPPORTED. */
+int e0_sample(const void* x, int dtype, int64_t ld, int T, int V, const e0_sampling* rules, const float* u,
+              int32_t* token, float* logp, int32_t* kept, uint32_t* d_status, e0_stream_t stream);
 
 /* ---- the paged 8-bit KV cache ----------------------------------------- */
 

@@ -446,6 +446,37 @@ int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max
                            out, out_ld, lse, ws, d_status, cs(stream));
 }
 
+int e0_qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const e0_rope* rope,
+               const int32_t* positions, int64_t pos_ld, void* y, int64_t y_ld, uint32_t* d_status,
+               e0_stream_t stream) {
+    if (!rope) return E0_ERR_NULL;
+    const e0_rope& r = *rope;
+    if (T < 0 || Hq < 0 || Hk < 0 || Hq + (int64_t)Hk < 1 || !float_type(dtype)) return E0_ERR_ARG;
+    if (r.D < 2 || r.D % 2 || r.rot < 0 || r.rot % 2 || r.rot > r.D || r.n_axes < 1 || r.n_axes > E0_MAX_ROPE_AXES)
+        return E0_ERR_ARG;
+    if ((r.flags & ~(E0_ROPE_ADJACENT | E0_QK_NORM)) || !(r.eps >= 0.f)) return E0_ERR_ARG;
+    if (r.D > E0_MAX_ROPE_D || T > E0_MAX_ROWS || Hq + (int64_t)Hk > 65536) return E0_ERR_UNSUPPORTED;
+    if (T == 0) return E0_OK;
+    if (!x || !y || !positions || (r.rot > 0 && !r.freq)) return E0_ERR_NULL;
+    const int64_t row = (Hq + (int64_t)Hk) * r.D;
+    if (x_ld < row || y_ld < row || (r.n_axes > 1 && pos_ld < T)) return E0_ERR_ARG;
+    if (!aligned(elem_bytes(dtype), x, y) || !aligned(4, positions, r.freq, r.q_norm, r.k_norm)) return E0_ERR_ARG;
+    if (x == y && x_ld != y_ld) return E0_ERR_ARG;
+    return e0::qk_rope(x, dtype, x_ld, T, Hq, Hk, rope, positions, pos_ld, y, y_ld, d_status, cs(stream));
+}
+
+int e0_sample(const void* x, int dtype, int64_t ld, int T, int V, const e0_sampling* rules, const float* u,
+              int32_t* token, float* logp, int32_t* kept, uint32_t* d_status, e0_stream_t stream) {
+    if (T < 0 || V < 1 || !float_type(dtype)) return E0_ERR_ARG;
+    if (V > E0_MAX_VOCAB || T > 1 << 24) return E0_ERR_UNSUPPORTED;
+    if (T == 0) return E0_OK;
+    if (!x || !u || !token) return E0_ERR_NULL;
+    if (ld < V) return E0_ERR_ARG;
+    if (!aligned(elem_bytes(dtype), x) || !aligned(4, u, token, logp, kept)) return E0_ERR_ARG;
+    if (rules && !aligned(4, rules->temperature, rules->top_k, rules->top_p, rules->min_p)) return E0_ERR_ARG;
+    return e0::sample(x, dtype, ld, T, V, rules, u, token, logp, kept, d_status, cs(stream));
+}
+
 int e0_selftest_bounded_wait(const uint32_t* flag, uint32_t limit_us, uint32_t* d_status, e0_stream_t stream) {
     if (!flag || !d_status) return E0_ERR_NULL;
     if (limit_us == 0 || limit_us > E0_SELFTEST_MAX_WAIT_US) return E0_ERR_ARG;

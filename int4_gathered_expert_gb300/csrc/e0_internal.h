@@ -66,6 +66,10 @@ size_t attn_ws_bytes(int D);
 int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
                 int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale, int window, void* out,
                 int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s);
+int qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const e0_rope* r, const int32_t* pos,
+            int64_t pos_ld, void* y, int64_t y_ld, uint32_t* st, cudaStream_t s);
+int sample(const void* x, int dtype, int64_t ld, int T, int V, const e0_sampling* r, const float* u, int32_t* token,
+           float* logp, int32_t* kept, uint32_t* st, cudaStream_t s);
 
 size_t prefill_ws_bytes(int T, int H, int I, int E, int K);
 int prefill_sort(const int32_t* inds, int T, int K, int E, int32_t* counts, int32_t* offsets, int32_t* perm,

@@ -1,0 +1,259 @@
+// Norms of queries and keys for each head and their rotation by position, in one pass
+// (e0_qk_rope).
+#include <cuda_runtime.h>
+
+#include "e0_internal.h"
+#include "e0_types.cuh"
+
+namespace e0 {
+namespace {
+
+// Pair i of a head turns by the angle a = position * freq[i]:
+//     (x0, x1) -> (x0 cos a - x1 sin a, x1 cos a + x0 sin a),
+// after h = x / sqrt(mean(x^2) + eps) * w where there is a norm.  A row is read and
+// written once, and that bounds the kernel: a head's 16 values a lane (8 pairs) stay in
+// registers between the sum of squares and the rotation, the two halves of a lane's pairs
+// are a 16-byte vector each whichever way pairs stand, and the angles are found once a
+// token, not once a head.
+// An angle is needed modulo a turn only, and fp32 has lost it where position * freq is
+// large.  So freq / 2 pi is held as a 64-bit fraction of a turn, the product with the
+// position is an integer's modulo 2^64, which drops whole turns by itself, and its first
+// 32 bits go to the sine: off by less than 2^-22 of a radian at any position.
+// The fractions take 64-bit floating point, which this GPU has little of: once a thread
+// block, which handles many heads.
+constexpr int ROPE_WARPS = 8;
+constexpr int MOST_PAIRS = E0_MAX_ROPE_D / 2;
+
+struct RopeArgs {
+    const void* x;
+    void* y;
+    const float* freq;
+    const uint8_t* axis;
+    const float* wq;
+    const float* wk;
+    const int32_t* pos;
+    uint32_t* st;
+    int64_t x_ld, y_ld, pos_ld;
+    int T, Hq, heads, D, half, axes, per_token, lanes;  // half: pairs that turn; per_token: warps; lanes: of a head
+    bool adjacent, norm;
+    float eps, inv_d;
+};
+
+// Where the pairs 8 item .. 8 item + 7 stand: elements e0.. and e1.. of a head, 8 each.  Adjacent
+// pairs are (e0, e0 + 1), ..., then those from e1 on; others (e0, e1), (e0 + 1, e1 + 1), ...
+struct Place {
+    int e0, e1;
+    bool turns;
+};
+E0_DEV Place place_of(const RopeArgs& A, int item) {
+    const int p = 8 * item;
+    if (p >= A.half) return {2 * p, 2 * p + 8, false};
+    return A.adjacent ? Place{2 * p, 2 * p + 8, true} : Place{p, p + A.half, true};
+}
+
+// One pair's elements where vectors do not fit: pair p of D / 2.
+E0_DEV void pair_of(const RopeArgs& A, int p, int& a, int& b) {
+    const bool apart = p < A.half && !A.adjacent;
+    a = apart ? p : 2 * p;
+    b = apart ? p + A.half : 2 * p + 1;
+}
+
+// t modulo 1, times 2^64.
+E0_DEV unsigned long long fraction(double t) {
+    return (unsigned long long)(long long)((t - floor(t)) * 9223372036854775808.0) << 1;
+}
+
+template <int TY>
+struct Raw {
+    static constexpr int N = TY == E0_F32 ? 2 : 1;
+    uint4 v[N];  // 8 elements
+};
+
+// VEC: D and twice the pairs that turn are multiples of 16 and every row starts on a 16-byte
+// boundary; otherwise elements come one by one.
+template <int TY, bool VEC>
+__global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
+    typedef typename Elem<TY>::T T;
+    __shared__ unsigned long long turn[MOST_PAIRS];
+    __shared__ uint8_t axis[MOST_PAIRS];
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < A.half; i += ROPE_WARPS * 32) {
+        // 1 / 2 pi in two parts, the first of 29 bits: its product with 24 is exact
+        const double f = A.freq[i], t = f * 0.15915494272485375, rest = f * 3.6704158172530464e-10;
+        turn[i] = fraction(t) + fraction(rest);
+        axis[i] = A.axis ? (uint8_t)min((int)A.axis[i], A.axes - 1) : (uint8_t)0;
+    }
+    __syncthreads();
+    const long long w = (long long)blockIdx.x * ROPE_WARPS + (threadIdx.x >> 5);
+    const int t = (int)(w / A.per_token);
+    if (t >= A.T) return;
+    if (A.pos[t] < 0) return;  // no token: the row stays as it is
+    const int slots = 32 / A.lanes, item = lane & (A.lanes - 1), items = (A.D + 15) / 16;
+    const int first = (int)(w % A.per_token) * slots + lane / A.lanes, step = A.per_token * slots;
+    const bool live = item < items;
+    const Place at = place_of(A, item);
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int p = 8 * item + i;
+        cs[i] = 1.f, sn[i] = 0.f;
+        if (p < A.half) {
+            const long long pos = A.pos[(size_t)axis[p] * A.pos_ld + t];
+            const unsigned long long a = (unsigned long long)pos * turn[p];
+            // the nearest turn taken off: -1/2 .. 1/2 of a turn, as half turns
+            sincospif((float)(int)(a >> 32) * 4.6566128730773926e-10f, &sn[i], &cs[i]);
+        }
+    }
+    const T* x = reinterpret_cast<const T*>(A.x) + (size_t)t * A.x_ld;
+    T* y = reinterpret_cast<T*>(A.y) + (size_t)t * A.y_ld;
+    bool bad = false;
+    float wt[16];
+    int have = 0;  // whose weights wt holds: 1 the queries', 2 the keys'
+    const auto load = [&](int h, Raw<TY> (&r)[2]) {
+        if constexpr (VEC) {
+            if (h < A.heads && live) {
+                const uint4* a = reinterpret_cast<const uint4*>(x + (size_t)h * A.D + at.e0);
+                const uint4* b = reinterpret_cast<const uint4*>(x + (size_t)h * A.D + at.e1);
+#pragma unroll
+                for (int i = 0; i < Raw<TY>::N; ++i) r[0].v[i] = a[i], r[1].v[i] = b[i];
+            }
+        }
+    };
+    Raw<TY> now[2], next[2];
+    load(first, now);
+    for (int h0 = 0; h0 < A.heads; h0 += step) {  // all lanes of a warp take every turn
+        const int h = h0 + first;
+        const bool mine = h < A.heads && live;
+        load(h + step, next);
+        float a[8], b[8];  // pair i is (a[i], b[i])
+        if constexpr (VEC) {
+            float u[8], v[8];
+            if constexpr (TY == E0_F32) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 p = now[0].v[i / 4], q = now[1].v[i / 4];
+                    u[i] = __uint_as_float(i % 4 == 0 ? p.x : i % 4 == 1 ? p.y : i % 4 == 2 ? p.z : p.w);
+                    v[i] = __uint_as_float(i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 p = now[0].v[0], q = now[1].v[0];
+                    const float2 f = unpack16<TY>(i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w);
+                    const float2 g = unpack16<TY>(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
+                    u[2 * i] = f.x, u[2 * i + 1] = f.y, v[2 * i] = g.x, v[2 * i + 1] = g.y;
+                }
+            }
+            const bool side = A.adjacent || !at.turns;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                a[i] = side ? (i < 4 ? u[2 * i] : v[2 * (i & 3)]) : u[i];
+                b[i] = side ? (i < 4 ? u[2 * i + 1] : v[2 * (i & 3) + 1]) : v[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                int ea, eb;
+                pair_of(A, 8 * item + i, ea, eb);
+                const bool in = mine && 8 * item + i < A.D / 2;
+                a[i] = in ? Elem<TY>::get(x[(size_t)h * A.D + ea]) : 0.f;
+                b[i] = in ? Elem<TY>::get(x[(size_t)h * A.D + eb]) : 0.f;
+            }
+        }
+        if (A.norm) {
+            float ss = 0.f;
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+            }
+            for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float rstd = rsqrtf(fmaf(ss, A.inv_d, A.eps));
+            bad |= mine && !(ss < INFINITY);
+            const float* wp = h < A.Hq ? A.wq : A.wk;
+            const int kind = h < A.Hq ? 1 : 2;
+            if (wp && mine && have != kind) {
+                have = kind;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    int ea, eb;
+                    pair_of(A, 8 * item + i, ea, eb);
+                    const bool in = 8 * item + i < A.D / 2;
+                    wt[i] = in ? __ldg(wp + ea) : 0.f;
+                    wt[8 + i] = in ? __ldg(wp + eb) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                a[i] *= rstd, b[i] *= rstd;
+                if (wp) a[i] *= wt[i], b[i] *= wt[8 + i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p = a[i], q = b[i];
+            a[i] = fmaf(p, cs[i], -q * sn[i]);
+            b[i] = fmaf(q, cs[i], p * sn[i]);
+        }
+        if (mine) {
+            T* to = y + (size_t)h * A.D;
+            if constexpr (VEC) {
+                float u[8], v[8];
+                const bool side = A.adjacent || !at.turns;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u[2 * i] = side ? a[i] : a[2 * i], u[2 * i + 1] = side ? b[i] : a[2 * i + 1];
+                    v[2 * i] = side ? a[4 + i] : b[2 * i], v[2 * i + 1] = side ? b[4 + i] : b[2 * i + 1];
+                }
+                store_vec<TY>(to + at.e0, u);
+                store_vec<TY>(to + at.e1, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    int ea, eb;
+                    pair_of(A, 8 * item + i, ea, eb);
+                    if (8 * item + i < A.D / 2) to[ea] = Elem<TY>::put(a[i]), to[eb] = Elem<TY>::put(b[i]);
+                }
+            }
+        }
+        now[0] = next[0], now[1] = next[1];
+    }
+    if (bad && item == 0) set_status(A.st, E0_ST_NONFINITE);
+}
+
+template <int TY>
+int launch(const RopeArgs& a, bool vec, cudaStream_t s) {
+    const long long blocks = ((long long)a.T * a.per_token + ROPE_WARPS - 1) / ROPE_WARPS;
+    if (vec)
+        k_qk_rope<TY, true><<<(unsigned)blocks, ROPE_WARPS * 32, 0, s>>>(a);
+    else
+        k_qk_rope<TY, false><<<(unsigned)blocks, ROPE_WARPS * 32, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+}  // namespace
+
+int qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const e0_rope* r, const int32_t* pos,
+            int64_t pos_ld, void* y, int64_t y_ld, uint32_t* st, cudaStream_t s) {
+    RopeArgs a = {};
+    a.x = x, a.y = y, a.freq = r->freq, a.axis = r->axis, a.wq = r->q_norm, a.wk = r->k_norm, a.pos = pos, a.st = st;
+    a.x_ld = x_ld, a.y_ld = y_ld, a.pos_ld = pos_ld;
+    a.T = T, a.Hq = Hq, a.heads = Hq + Hk, a.D = r->D, a.half = r->rot / 2, a.axes = r->n_axes;
+    a.adjacent = r->flags & E0_ROPE_ADJACENT, a.norm = r->flags & E0_QK_NORM;
+    a.eps = r->eps, a.inv_d = (float)(1.0 / r->D);
+    a.lanes = 1;
+    while (16 * a.lanes < r->D) a.lanes *= 2;
+    // a warp a token; more of them, down to a head for each of a warp's places, where tokens are few
+    const int slots = 32 / a.lanes, most = (a.heads + slots - 1) / slots, want = 16 * num_sms();
+    a.per_token = T >= want ? 1 : (want + T - 1) / T;
+    if (a.per_token > most) a.per_token = most;
+    const int sz = type_size(dtype);
+    const uintptr_t bits = (uintptr_t)x | (uintptr_t)y | (uintptr_t)(x_ld * sz) | (uintptr_t)(y_ld * sz);
+    const bool vec = r->D % 16 == 0 && r->rot % 16 == 0 && !(bits & 15);
+    switch (dtype) {
+        case E0_F32: return launch<E0_F32>(a, vec, s);
+        case E0_F16: return launch<E0_F16>(a, vec, s);
+        default: return launch<E0_BF16>(a, vec, s);
+    }
+}
+
+}  // namespace e0

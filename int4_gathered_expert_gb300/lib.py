@@ -23,6 +23,8 @@ E0_ROUTE_SOFTMAX_TOPK, E0_ROUTE_SIGMOID_GROUP = 0, 1
 E0_MAX_E, E0_MAX_K, E0_MAX_T_DECODE, E0_MAX_LORA_RANK = 1024, 32, 64, 64
 E0_MAX_NORM_H, E0_MAX_ROWS, E0_MAX_SEQS, E0_MAX_CONTEXT = 16384, 1 << 30, 4096, 1 << 30
 E0_MAX_T_LINEAR, E0_MAX_N_LINEAR, E0_MAX_K_LINEAR = 524280, 1 << 28, 1 << 20
+E0_MAX_ROPE_D, E0_MAX_ROPE_AXES, E0_MAX_VOCAB = 256, 4, 1 << 18
+E0_ROPE_ADJACENT, E0_QK_NORM = 1, 2
 
 vp = C.c_void_p
 i32 = C.c_int32
@@ -81,6 +83,15 @@ class KvState(C.Structure):
                 ("B", i32), ("max_blocks", i32), ("block_tokens", i32), ("n_blocks", i32)]
 
 
+class Rope(C.Structure):
+    _fields_ = [("freq", vp), ("axis", vp), ("q_norm", vp), ("k_norm", vp), ("D", i32), ("rot", i32),
+                ("n_axes", i32), ("flags", i32), ("eps", C.c_float)]
+
+
+class Sampling(C.Structure):
+    _fields_ = [("temperature", vp), ("top_k", vp), ("top_p", vp), ("min_p", vp)]
+
+
 _lib = None
 
 
@@ -135,6 +146,8 @@ def load() -> C.CDLL:
         "e0_attn_workspace_size": (sz, [C.c_int] * 5),
         "e0_attn_decode": (C.c_int, [P(KvCache), vp, C.c_int, vp, vp, C.c_int, C.c_int, vp, C.c_int, i64, C.c_int,
                                      C.c_float, C.c_int, vp, i64, vp, vp, sz, vp, vp]),
+        "e0_qk_rope": (C.c_int, [vp, C.c_int, i64, C.c_int, C.c_int, C.c_int, P(Rope), vp, i64, vp, i64, vp, vp]),
+        "e0_sample": (C.c_int, [vp, C.c_int, i64, C.c_int, C.c_int, P(Sampling), vp, vp, vp, vp, vp, vp]),
         "e0_selftest_bounded_wait": (C.c_int, [vp, C.c_uint32, vp, vp]),
         "e0_read_status": (C.c_int, [vp, P(C.c_uint32), vp]),
         "e0_status_string": (C.c_char_p, [C.c_int]),
@@ -159,6 +172,7 @@ def exported_symbols():
             "e0_moe_prefill_forward",
             "e0_rmsnorm_q8", "e0_linear_bytes", "e0_pack_linear", "e0_linear_forward", "e0_kv_plan", "e0_kv_release",
             "e0_kv_append", "e0_attn_workspace_size", "e0_attn_decode",
+            "e0_qk_rope", "e0_sample",
             "e0_selftest_bounded_wait", "e0_read_status", "e0_status_string"]
 
 
@@ -422,6 +436,20 @@ def e0_attn_decode(cache: KvCache, block_table, max_blocks, ctx_len, cu_q, B, ma
                                ptr(q), dtype, q_ld, Hq, scale, window, ptr(out), out_ld, ptr(lse), ptr(ws), ws_bytes,
                                ptr(status), stream_handle(stream))
     return _check("e0_attn_decode", rc, raise_on_error)
+
+
+def e0_qk_rope(x, dtype, x_ld, T, Hq, Hk, rope: Rope, positions, pos_ld, y, y_ld, status=None, stream=None,
+               raise_on_error=True):
+    rc = load().e0_qk_rope(ptr(x), dtype, x_ld, T, Hq, Hk, C.byref(rope), ptr(positions), pos_ld, ptr(y), y_ld,
+                           ptr(status), stream_handle(stream))
+    return _check("e0_qk_rope", rc, raise_on_error)
+
+
+def e0_sample(x, dtype, ld, T, V, rules: Optional[Sampling], u, token, logp=None, kept=None, status=None, stream=None,
+              raise_on_error=True):
+    rc = load().e0_sample(ptr(x), dtype, ld, T, V, C.byref(rules) if rules is not None else None, ptr(u), ptr(token),
+                          ptr(logp), ptr(kept), ptr(status), stream_handle(stream))
+    return _check("e0_sample", rc, raise_on_error)
 
 
 E0_SELFTEST_MAX_WAIT_US = 2000000
