@@ -721,6 +721,60 @@ int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max
                    float scale, int window, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
                    uint32_t* d_status, e0_stream_t stream);
 
+/* What scores and masks e0_attn_scored and e0_attn_shared follow beside e0_attn_decode's. */
+typedef struct e0_attn_rules {
+    float cap;               /* > 0: a score s becomes cap * tanh(s / cap); 0: it does not  */
+    int32_t window;          /* as e0_attn_decode's                                         */
+    const float* slopes;     /* device [Hq] or NULL: slopes[g] * |p - j| is taken off the
+                                score (after the cap) of the query at p and the position j  */
+    const int32_t* first;    /* device [rows of q] or NULL: the first position that a row's
+                                query sees (where its document begins)                      */
+    const int32_t* open_len; /* device [B] or NULL: positions below it are seen by all
+                                queries of the sequence, earlier ones too (an open prefix)  */
+} e0_attn_rules;
+
+/* Workspace of e0_attn_scored, as e0_attn_workspace_size's. */
+size_t e0_attn_scored_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
+
+/* e0_attn_decode under the rules of `rules`, for single tokens and for prompts: the query at
+ * position p of sequence b, row t of q, sees the cached positions j with
+ *     (j <= p or j < open_len[b]) and j >= first[t] and (window = 0 or j > p - window),
+ * its scores are those of the rules, and lse is over them.  All else is e0_attn_decode's: the
+ * arguments, queries that see nothing, rows after the last sequence's, conditions found on the
+ * device, equal calls' bits.  A negative first[t] counts as 0, an open_len beyond the cached
+ * tokens as all of them.  Where max_q queries have 64 rows of a KV head and more and q is
+ * fp16 or bf16, the products run in tiles of 128 or 256 rows on the tensor cores:
+ * the weights are then rounded to 11 bits (bf16) or 22 (fp16).  fp32 queries take the path for
+ * few rows (every 8 of a KV head read the sequence once more).  rules NULL: none.  Errors as
+ * e0_attn_decode's; cap negative or not finite, window < 0, or a pointer of the rules that
+ * is not aligned to 4 bytes -> E0_ERR_ARG. */
+int e0_attn_scored(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
+                   const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
+                   const e0_attn_rules* rules, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
+                   uint32_t* d_status, e0_stream_t stream);
+
+/* Workspace of e0_attn_shared for at most T rows of q. */
+size_t e0_attn_shared_workspace_size(int B, int T, int Hq, int Hkv, int D, int max_q);
+
+/* Attention of a batch whose sequences begin alike: positions 0 .. P-1, P = *prefix_len
+ * (device), are tokens that all of them share, in the blocks prefix_table[0 ..
+ * prefix_blocks-1] (device) of the same cache, and are read once for the batch, not once a
+ * sequence.  block_table, ctx_len and cu_q are as e0_attn_decode's and say what each
+ * sequence has of its own, from position P on (ctx_len without the prefix; own tokens start in a
+ * block of their own, whatever P is); cu_q gives at most T rows.  A query sees the
+ * prefix and its own sequence up to itself, within the window.  rules: cap, window and slopes
+ * as e0_attn_scored's, or NULL; first and open_len -> E0_ERR_UNSUPPORTED.  A P that is
+ * negative or needs more than prefix_blocks blocks raises E0_ST_BAD_LENGTH, and nobody sees the
+ * prefix; a cu_q that gives more than T rows raises it, and that sequence's rows are left as they
+ * were.  All else is e0_attn_scored's.  Errors: as e0_attn_scored's, and NULL prefix_table or
+ * prefix_len -> E0_ERR_NULL; T < 1 or prefix_blocks < 1 -> E0_ERR_ARG; (prefix_blocks +
+ * max_blocks) * block_tokens > E0_MAX_CONTEXT, T * Hq > 2^30 -> E0_ERR_UNSUPPORTED. */
+int e0_attn_shared(const e0_kv_cache* cache, const int32_t* prefix_table, int prefix_blocks, const int32_t* prefix_len,
+                   const int32_t* block_table, int max_blocks, const int32_t* ctx_len, const int32_t* cu_q, int B,
+                   int T, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
+                   const e0_attn_rules* rules, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
+                   uint32_t* d_status, e0_stream_t stream);
+
 /* ---- status ------------------------------------------------------------- */
 
 /* Largest wait e0_selftest_bounded_wait accepts, in microseconds. */

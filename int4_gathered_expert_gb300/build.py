@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libe0moe.so")
 SOURCES = ["e0_decode.cu", "e0_prefill.cu", "e0_abi.cu", "e0_noalloc.cu", "e0_norm.cu", "e0_linear.cu", "e0_kv.cu",
-           "e0_attn.cu", "e0_rope.cu", "e0_sample.cu"]
+           "e0_attn.cu", "e0_attn_rules.cu", "e0_attn_tile.cu", "e0_rope.cu", "e0_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,6 +1,7 @@
 // extern "C" entry points of libe0moe: argument validation on the host, then
 // the launchers in namespace e0.  Nothing here allocates device memory.
 #include <cuda_runtime.h>
+#include <float.h>
 
 #include "e0_common.cuh"
 #include "e0_internal.h"
@@ -82,6 +83,39 @@ int check_kv_state(const e0_kv_state* s, const int32_t* ctx_out, const int32_t* 
     if (s->B > 0 && (!s->block_table || !s->ctx_len || !ctx_out)) return E0_ERR_NULL;
     if (!aligned(4, s->block_table, s->ctx_len, s->free_list, s->free_count, ctx_out, free_out)) return E0_ERR_ARG;
     return E0_OK;
+}
+
+// What the calls of attention over the cache have in common (B == 0: nothing more is read).
+int check_attn(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
+               const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
+               int window, const void* out, int64_t out_ld, const float* lse, const void* ws) {
+    const int rc = check_kv_cache(cache);
+    if (rc) return rc;
+    if (B < 0 || max_blocks < 1 || max_q < 1 || !float_type(dtype) || window < 0) return E0_ERR_ARG;
+    if (Hq < cache->Hkv || Hq % cache->Hkv != 0 || !(scale == scale)) return E0_ERR_ARG;
+    if (!cu_q && max_q != 1) return E0_ERR_ARG;
+    if (B > E0_MAX_SEQS || (int64_t)max_q * Hq > (int64_t)1 << 30 || !positions_ok(max_blocks, cache->block_tokens))
+        return E0_ERR_UNSUPPORTED;
+    if (B == 0) return E0_OK;
+    if (!block_table || !ctx_len || !q || !out || !ws) return E0_ERR_NULL;
+    const int64_t row = (int64_t)Hq * cache->D;
+    if (q_ld < row || out_ld < row) return E0_ERR_ARG;
+    if (!aligned(16, q) || (q_ld * elem_bytes(dtype)) % 16 != 0 || !aligned(elem_bytes(dtype), out)) return E0_ERR_ARG;
+    if (!aligned(4, block_table, ctx_len, cu_q, lse) || !aligned(256, ws)) return E0_ERR_ARG;
+    return E0_OK;
+}
+
+int check_rules(const e0_attn_rules* r) {
+    if (!r) return E0_OK;
+    if (!(r->cap >= 0.f && r->cap <= FLT_MAX)) return E0_ERR_ARG;
+    return aligned(4, r->slopes, r->first, r->open_len) ? E0_OK : E0_ERR_ARG;
+}
+
+// A copy of the rules whose window is none where no position can be beyond it.
+e0_attn_rules rules_of(const e0_attn_rules* r, int64_t positions) {
+    e0_attn_rules own = r ? *r : e0_attn_rules{};
+    if (own.window >= positions) own.window = 0;
+    return own;
 }
 
 }  // namespace
@@ -426,24 +460,61 @@ int e0_attn_decode(const e0_kv_cache* cache, const int32_t* block_table, int max
                    const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
                    int window, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes, uint32_t* d_status,
                    e0_stream_t stream) {
-    const int rc = check_kv_cache(cache);
-    if (rc) return rc;
-    if (B < 0 || max_blocks < 1 || max_q < 1 || !float_type(dtype) || window < 0) return E0_ERR_ARG;
-    if (Hq < cache->Hkv || Hq % cache->Hkv != 0 || !(scale == scale)) return E0_ERR_ARG;
-    if (!cu_q && max_q != 1) return E0_ERR_ARG;
-    if (B > E0_MAX_SEQS || (int64_t)max_q * Hq > (int64_t)1 << 30 || !positions_ok(max_blocks, cache->block_tokens))
-        return E0_ERR_UNSUPPORTED;
-    if (B == 0) return E0_OK;
-    if (!block_table || !ctx_len || !q || !out || !ws) return E0_ERR_NULL;
-    const int64_t row = (int64_t)Hq * cache->D;
-    if (q_ld < row || out_ld < row) return E0_ERR_ARG;
-    if (!aligned(16, q) || (q_ld * elem_bytes(dtype)) % 16 != 0 || !aligned(elem_bytes(dtype), out)) return E0_ERR_ARG;
-    if (!aligned(4, block_table, ctx_len, cu_q, lse) || !aligned(256, ws)) return E0_ERR_ARG;
+    const int rc = check_attn(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale, window, out,
+                              out_ld, lse, ws);
+    if (rc || B == 0) return rc;
     if (ws_bytes < e0::attn_ws_bytes(cache->D)) return E0_ERR_ARG;
     // a window that no sequence can outgrow is none
     if (window >= max_blocks * cache->block_tokens) window = 0;
     return e0::attn_decode(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale, window,
                            out, out_ld, lse, ws, d_status, cs(stream));
+}
+
+size_t e0_attn_scored_workspace_size(int B, int Hq, int Hkv, int D, int max_q) {
+    if (e0_attn_workspace_size(B, Hq, Hkv, D, max_q) == 0 || (int64_t)max_q * Hq > (int64_t)1 << 30) return 0;
+    return e0::attn_scored_ws_bytes(B, Hq, Hkv, D, max_q);
+}
+
+int e0_attn_scored(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
+                   const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
+                   const e0_attn_rules* rules, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
+                   uint32_t* d_status, e0_stream_t stream) {
+    int rc = check_attn(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale,
+                        rules ? rules->window : 0, out, out_ld, lse, ws);
+    if (!rc) rc = check_rules(rules);
+    if (rc || B == 0) return rc;
+    if (ws_bytes < e0::attn_scored_ws_bytes(B, Hq, cache->Hkv, cache->D, max_q)) return E0_ERR_ARG;
+    const e0_attn_rules own = rules_of(rules, (int64_t)max_blocks * cache->block_tokens);
+    return e0::attn_scored(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale, &own, out,
+                           out_ld, lse, ws, d_status, cs(stream));
+}
+
+size_t e0_attn_shared_workspace_size(int B, int T, int Hq, int Hkv, int D, int max_q) {
+    if (e0_attn_scored_workspace_size(B, Hq, Hkv, D, max_q) == 0 || T < 1 || (int64_t)T * Hq > (int64_t)1 << 30) return 0;
+    return e0::attn_shared_ws_bytes(B, T, Hq, Hkv, D, max_q);
+}
+
+int e0_attn_shared(const e0_kv_cache* cache, const int32_t* prefix_table, int prefix_blocks, const int32_t* prefix_len,
+                   const int32_t* block_table, int max_blocks, const int32_t* ctx_len, const int32_t* cu_q, int B,
+                   int T, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
+                   const e0_attn_rules* rules, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
+                   uint32_t* d_status, e0_stream_t stream) {
+    int rc = check_attn(cache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale,
+                        rules ? rules->window : 0, out, out_ld, lse, ws);
+    if (!rc) rc = check_rules(rules);
+    if (rc) return rc;
+    if (T < 1 || prefix_blocks < 1) return E0_ERR_ARG;
+    if ((int64_t)T * Hq > (int64_t)1 << 30 || prefix_blocks > E0_MAX_CONTEXT - max_blocks ||
+        !positions_ok(prefix_blocks + max_blocks, cache->block_tokens))
+        return E0_ERR_UNSUPPORTED;
+    if (rules && (rules->first || rules->open_len)) return E0_ERR_UNSUPPORTED;
+    if (B == 0) return E0_OK;
+    if (!prefix_table || !prefix_len) return E0_ERR_NULL;
+    if (!aligned(4, prefix_table, prefix_len)) return E0_ERR_ARG;
+    if (ws_bytes < e0::attn_shared_ws_bytes(B, T, Hq, cache->Hkv, cache->D, max_q)) return E0_ERR_ARG;
+    const e0_attn_rules own = rules_of(rules, (int64_t)(prefix_blocks + max_blocks) * cache->block_tokens);
+    return e0::attn_shared(cache, prefix_table, prefix_blocks, prefix_len, block_table, max_blocks, ctx_len, cu_q, B, T,
+                           max_q, q, dtype, q_ld, Hq, scale, &own, out, out_ld, lse, ws, d_status, cs(stream));
 }
 
 int e0_qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const e0_rope* rope,

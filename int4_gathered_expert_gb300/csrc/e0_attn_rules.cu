@@ -1,0 +1,134 @@
+// e0_attn_scored and e0_attn_shared: attention under score rules, and over a prefix that a
+// batch shares.
+#include "e0_attn.cuh"
+
+namespace e0 {
+namespace {
+
+// Whether many rows of a KV head go through the tensor cores' tiles (their products in fp16
+// are not enough for fp32 outputs) or through the kernel that is made for few.
+bool by_tiles(int dtype, int64_t rows) { return dtype != E0_F32 && rows >= 64; }
+
+void put_rules(AttnArgs& a, const e0_attn_rules* r) {
+    if (!r) return;
+    a.window = r->window, a.slopes = r->slopes, a.first = r->first, a.open = r->open_len;
+    if (r->cap > 0.f) {
+        a.cap = r->cap * LOG2E;
+        a.inv_cap = 1.f / a.cap;
+    }
+}
+
+// ---------------------------------------------------------------- the shared prefix
+
+// For each row its position behind the prefix, and {0, rows} as the bounds of one sequence
+// of them all.  `a` is of the sequences' own tokens.
+constexpr int ROWS_THREADS = 1024;
+__global__ void __launch_bounds__(ROWS_THREADS) k_shared_rows(AttnArgs a, const int32_t* prefix_len, int32_t* at, int32_t* cu) {
+    __shared__ int rows;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) rows = 0;
+    for (int t = threadIdx.x; t < a.limit; t += ROWS_THREADS) at[t] = 0;
+    __syncthreads();
+    const int before = max(*prefix_len, 0);
+    for (int b = threadIdx.x >> 5; b < a.B; b += ROWS_THREADS / 32) {
+        const Seq s = seq_of<true>(a, b, false);
+        for (int i = lane; i < s.n; i += 32) at[s.row0 + i] = before + s.ctx - s.n + i;
+        if (lane == 0 && s.n > 0) atomicMax(&rows, s.row0 + s.n);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) cu[0] = 0, cu[1] = rows;
+}
+
+// out = (e^(l1 - m) o1 + e^(l2 - m) o2) / (e^(l1 - m) + e^(l2 - m)) of two normed results
+// and their lse: a warp a row and head.
+constexpr int MERGE_WARPS = 8;
+template <int TY>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) k_shared_merge(AttnArgs a, const float* o1, const float* l1, const float* o2,
+                                                                   const float* l2) {
+    typedef typename Elem<TY>::T T;
+    const int lane = threadIdx.x & 31;
+    const Seq s = seq_of<true>(a, blockIdx.x, false);
+    for (int item = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5); item < s.n * a.Hq; item += gridDim.y * MERGE_WARPS) {
+        const size_t tok = (size_t)s.row0 + item / a.Hq, at = tok * a.Hq + item % a.Hq;
+        const float x = l1[at], y = l2[at];
+        const float m = x != x || y != y ? __uint_as_float(0x7FC00000u) : fmaxf(x, y), base = m == -INFINITY ? 0.f : m;
+        const float u = exp2_of((x - base) * LOG2E), v = exp2_of((y - base) * LOG2E), sum = u + v;
+        const float f1 = sum > 0.f || sum != sum ? u / sum : 0.f, f2 = sum > 0.f || sum != sum ? v / sum : 0.f;
+        T* to = reinterpret_cast<T*>(a.out) + tok * a.out_ld + (size_t)(item % a.Hq) * a.D;
+        for (int d = lane; d < a.D; d += 32)
+            to[d] = Elem<TY>::put(fmaf(f1, o1[at * a.D + d], f2 * o2[at * a.D + d]));
+        if (a.lse && lane == 0) a.lse[at] = base + log2f(sum) * LN2;
+    }
+}
+
+size_t parts_bytes(int T, int Hq, int D) {  // a normed fp32 result and its lse
+    return up256((size_t)T * Hq * D * sizeof(float)) + up256((size_t)T * Hq * sizeof(float));
+}
+
+}  // namespace
+
+size_t attn_scored_ws_bytes(int B, int Hq, int Hkv, int D, int max_q) {
+    const size_t few = attn_ws_bytes(D), many = attn_tile_ws_bytes(B, max_q, Hq / Hkv, D);
+    return by_tiles(E0_F16, (int64_t)max_q * (Hq / Hkv)) && many > few ? many : few;
+}
+
+int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu, int B,
+                int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale, const e0_attn_rules* rules,
+                void* out, int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
+    AttnArgs a = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, lse, ws, st);
+    put_rules(a, rules);
+    if (by_tiles(dtype, (int64_t)max_q * (Hq / c->Hkv))) return attn_tile(a, dtype, ws, s);
+    return launch_t<true>(a, dtype, c->D, s);
+}
+
+size_t attn_shared_ws_bytes(int B, int T, int Hq, int Hkv, int D, int max_q) {
+    const size_t own = attn_ws_bytes(D), tiles = attn_tile_ws_bytes(1, T, Hq / Hkv, D);
+    const size_t both = by_tiles(E0_F16, (int64_t)T * (Hq / Hkv)) && tiles > own ? tiles : own;
+    return up256((size_t)T * sizeof(int32_t)) + 256 + 2 * parts_bytes(T, Hq, D) + both;
+}
+
+int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_blocks, const int32_t* prefix_len,
+                const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu, int B, int T, int max_q,
+                const void* q, int dtype, int64_t q_ld, int Hq, float scale, const e0_attn_rules* rules, void* out,
+                int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
+    char* p = reinterpret_cast<char*>(ws);
+    const auto take = [&](size_t n) {
+        char* at = p;
+        p += up256(n);
+        return at;
+    };
+    int32_t* at = reinterpret_cast<int32_t*>(take((size_t)T * sizeof(int32_t)));
+    int32_t* cu2 = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+    float* o[2];
+    float* l[2];
+    for (int i = 0; i < 2; ++i) {
+        o[i] = reinterpret_cast<float*>(take((size_t)T * Hq * c->D * sizeof(float)));
+        l[i] = reinterpret_cast<float*>(take((size_t)T * Hq * sizeof(float)));
+    }
+    AttnArgs mine = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, l[1], p, st);
+    put_rules(mine, rules);
+    mine.raw = o[1], mine.limit = T;
+    mine.unit = 64;  // any: the kernels set their own
+    k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, prefix_len, at, cu2);
+    if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
+    // the prefix, as one sequence whose queries are all rows
+    AttnArgs front = args_of(c, prefix_table, prefix_blocks, prefix_len, cu2, 1, T, q, q_ld, Hq, scale, 0, out, out_ld, l[0], p, st);
+    put_rules(front, rules);
+    front.raw = o[0], front.limit = T, front.at = at;
+    int rc = by_tiles(dtype, (int64_t)T * (Hq / c->Hkv)) ? attn_tile(front, dtype, p, s) : launch_t<true>(front, dtype, c->D, s);
+    if (rc != E0_OK) return rc;
+    // what the sequences have of their own
+    rc = launch_t<true>(mine, dtype, c->D, s);
+    if (rc != E0_OK) return rc;
+    mine.lse = lse;
+    const long long items = (long long)max_q * Hq;
+    const dim3 grid(B, (unsigned)((items + MERGE_WARPS - 1) / MERGE_WARPS < 64 ? (items + MERGE_WARPS - 1) / MERGE_WARPS : 64));
+    switch (dtype) {
+        case E0_F32: k_shared_merge<E0_F32><<<grid, MERGE_WARPS * 32, 0, s>>>(mine, o[0], l[0], o[1], l[1]); break;
+        case E0_F16: k_shared_merge<E0_F16><<<grid, MERGE_WARPS * 32, 0, s>>>(mine, o[0], l[0], o[1], l[1]); break;
+        default: k_shared_merge<E0_BF16><<<grid, MERGE_WARPS * 32, 0, s>>>(mine, o[0], l[0], o[1], l[1]); break;
+    }
+    return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+}  // namespace e0

@@ -1,0 +1,882 @@
+// Attention of many query rows over the paged 8-bit KV cache on the 5th-generation tensor
+// cores: prompts of e0_attn_scored, and the shared prefix of e0_attn_shared.
+#pragma once
+#include "e0_attn.cuh"
+#include "e0_umma.cuh"
+
+namespace e0 {
+namespace {
+
+// One pass over the keys with the running maximum and sum, as in e0_attn.cuh, for tiles of
+// many query rows.  A job is a (sequence, KV head, tile of query rows); its context is cut
+// into units of KV positions, and the units of all jobs are dealt out evenly, one block an
+// SM.  Every row sees one range of positions, so a job's units are those that some row of it
+// sees, and masks are two comparisons.  Jobs that several blocks have are joined.
+//
+// A block's roles:
+//   - four warps turn a unit's codes into fp16 operands in shared memory (keys and values in
+//     the same order: 8 tokens x 8 elements are 128 bytes in a row, no swizzle; keys are then
+//     K-major, values MN-major), the next unit's codes already in registers;
+//   - one thread issues the products: S = Q K^T into tensor memory, O += P V with P from
+//     tensor memory;
+//   - four warps a half of the rows, a thread a row (so that maxima and sums need no
+//     exchange), turn S into P where S was.
+// With D up to 128 the tile has 256 rows in two halves, one half's products run under the other's
+// exponentials, and both read the same operands; with D = 256 tensor memory holds one half
+// and two S.
+// fp16 operands: codes widen exactly; bf16 queries go in times a power of two of the
+// row, fp16 ones as they are; the weights 2^(t - m + 7), at most 2^15, are rounded to fp16,
+// for bf16 outputs an eighth of what the output's rounding is; fp16 outputs get the weights'
+// rests, too, in a second product (SPLIT).
+template <int D>
+struct Geo {
+    static constexpr int HALVES = D == 256 ? 1 : 2;
+    static constexpr int ROWS = 128 * HALVES;
+    static constexpr int KV = D == 256 ? 64 : 128;
+    static constexpr int STAGES = D == 64 ? 3 : 2;
+    static constexpr int OPERAND = KV * D * 2;
+    static constexpr int SOFT = 4 * HALVES;  // softmax warps
+    static constexpr int THREADS = (SOFT + 4 + 1) * 32;
+    static constexpr int O_COL = 2 * KV;  // tensor memory: two S, then the halves' O
+    static constexpr int Q_BYTES = ROWS * D * 2;
+    static constexpr int LOADS = KV * D / (4 * 512);  // 16-byte loads of a converting lane for one operand
+};
+constexpr uint32_t TILE_TMEM = 512;
+constexpr uint64_t TILE_WAIT_NS = 2000000000ull;  // 2 s
+
+struct TileJob {
+    int seq, mtile, unit0, units;  // the first unit, how many
+    int k0[2], k1[2];              // of each half: its units, counted from unit0
+    int lo, hi, full_lo, full_hi;  // positions that some row sees; that all rows see
+    uint32_t start;                // place in the schedule of the first head's first unit
+    int row0, rows, p0;            // query rows: the sequence's first; of this tile (heads x tokens); position of its token 0
+};
+struct TileCut {
+    int parts, block, job, head;  // parts 0: none
+};
+struct TileHead {
+    uint32_t total, share;
+    int jobs, pad;
+};
+
+struct TileArgs {
+    AttnArgs a;               // parts and cuts unused
+    float* part_o;            // [2 * blocks][ROWS][D]
+    float2* part_ml;          // [2 * blocks][ROWS]
+    TileCut* cuts;            // [blocks][2]
+    TileJob* jobs;
+    int4* begin;              // [blocks]: job, head, unit
+    TileHead* head;
+    int blocks, most_jobs;
+    bool vec_out;
+};
+
+// The range of positions that a token of a sequence sees.
+E0_DEV void range_of(const TileArgs& A, int seq, int row0, int p0, int ctx, int i, int& p, int& lo, int& hi) {
+    p = A.a.at ? A.a.at[row0 + i] : p0 + i;
+    hi = A.a.at ? ctx : p + 1;
+    if (A.a.open) hi = max(hi, A.a.open[seq]);
+    hi = min(hi, ctx);
+    lo = A.a.window > 0 ? max(p - A.a.window + 1, 0) : 0;
+    if (A.a.first) lo = max(lo, A.a.first[row0 + i]);
+}
+
+// ---------------------------------------------------------------- the schedule
+
+constexpr int PLAN_THREADS = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
+    typedef Geo<D> G_;
+    extern __shared__ uint32_t tiles_before[];  // [B + 1]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ uint32_t red[32];
+    __shared__ uint32_t carry;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = A.a.B, G = A.a.Hq / A.a.Hkv;
+    const auto block_scan = [&](uint32_t v, uint32_t& all) {  // exclusive
+        const uint32_t own = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = add_units(v, t);
+        }
+        __syncthreads();
+        if (lane == 31) red[warp] = v;
+        __syncthreads();
+        uint32_t before = 0;
+        all = 0;
+        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+            if (w < warp) before = add_units(before, red[w]);
+            all = add_units(all, red[w]);
+        }
+        return add_units(before, v - own);
+    };
+    // tiles of query rows of each sequence
+    uint32_t at = 0;
+    for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
+        const int b = b0 + tid;
+        uint32_t n = 0, all;
+        if (b < B) n = (uint32_t)(((long long)seq_of<true>(A.a, b, true).n * G + G_::ROWS - 1) / G_::ROWS);
+        const uint32_t before = block_scan(n, all);
+        if (b < B) tiles_before[b] = at + before;
+        at = add_units(at, all);
+    }
+    if (tid == 0) tiles_before[B] = at;
+    __syncthreads();
+    const int jobs = (int)min(at, (uint32_t)A.most_jobs);
+    // a warp a job: what its rows see
+    for (int j = warp; j < jobs; j += PLAN_THREADS / 32) {
+        int b = 0, end = B;
+        while (end - b > 1) {
+            const int mid = (b + end) >> 1;
+            if (tiles_before[mid] <= (uint32_t)j) b = mid; else end = mid;
+        }
+        while (tiles_before[b + 1] <= (uint32_t)j) ++b;  // sequences without rows share a place
+        const Seq s = seq_of<true>(A.a, b, false);
+        TileJob J;
+        J.seq = b, J.mtile = j - (int)tiles_before[b], J.row0 = s.row0, J.p0 = s.ctx - s.n;
+        const int r0 = J.mtile * G_::ROWS;
+        J.rows = min(G_::ROWS, s.n * G - r0);
+        J.lo = J.full_hi = INT_MAX, J.hi = J.full_lo = 0;
+        int u0 = INT_MAX, u1 = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            J.k0[h] = J.k1[h] = 0;
+            const int ra = r0 + 128 * h, rb = r0 + min(J.rows, 128 * (h + 1));
+            if (h >= G_::HALVES || ra >= rb) continue;
+            int lo = INT_MAX, hi = 0, most = 0, least = INT_MAX;
+            for (int i = ra / G + lane; i <= (rb - 1) / G; i += 32) {
+                int p, l, e;
+                range_of(A, b, s.row0, J.p0, s.ctx, i, p, l, e);
+                if (l < e) lo = min(lo, l), hi = max(hi, e);
+                most = max(most, l), least = min(least, e);
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+            J.full_lo = max(J.full_lo, __reduce_max_sync(0xffffffffu, most));
+            J.full_hi = min(J.full_hi, __reduce_min_sync(0xffffffffu, least));
+            if (lo >= hi) continue;
+            J.lo = min(J.lo, lo), J.hi = max(J.hi, hi);
+            J.k0[h] = lo / G_::KV, J.k1[h] = (hi - 1) / G_::KV + 1;
+            u0 = min(u0, J.k0[h]), u1 = max(u1, J.k1[h]);
+        }
+        if (u1 == 0) u0 = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (J.k1[h] > 0) J.k0[h] -= u0, J.k1[h] -= u0;
+        J.unit0 = u0, J.units = max(u1 - u0, 1);  // a job without context still writes its rows
+        J.start = 0;
+        if (lane == 0) A.jobs[j] = J;
+    }
+    __syncthreads();
+    // their places in the schedule
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    for (int j0 = 0; j0 < jobs; j0 += PLAN_THREADS) {
+        const int j = j0 + tid;
+        uint32_t n = 0, all;
+        if (j < jobs) {
+            const unsigned long long u = (unsigned long long)A.jobs[j].units * A.a.Hkv;
+            n = u < MOST_UNITS ? (uint32_t)u : MOST_UNITS;
+        }
+        const uint32_t before = block_scan(n, all);
+        if (j < jobs) A.jobs[j].start = add_units(carry, before);
+        __syncthreads();
+        if (tid == 0) carry = add_units(carry, all);
+        __syncthreads();
+    }
+    uint32_t total = carry;
+    if (total >= MOST_UNITS || at > (uint32_t)A.most_jobs) {
+        if (tid == 0) set_status(A.a.st, E0_ST_BAD_LENGTH);
+        total = 0;
+    }
+    const uint32_t share = max((total + A.blocks - 1) / A.blocks, 1u);
+    if (tid == 0) *A.head = {total, share, jobs, 0};
+    for (int c = tid; c < A.blocks; c += PLAN_THREADS) {
+        const uint32_t u = c * share;
+        int4 to = make_int4(-1, 0, 0, 0);
+        if (u < total) {
+            int lo = 0, hi = jobs;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (A.jobs[mid].start <= u) lo = mid; else hi = mid;
+            }
+            const uint32_t rel = u - A.jobs[lo].start;
+            to = make_int4(lo, (int)(rel / A.jobs[lo].units), (int)(rel % A.jobs[lo].units), 0);
+        }
+        A.begin[c] = to;
+    }
+}
+
+// ---------------------------------------------------------------- a block's pieces of jobs
+
+struct Piece {
+    TileJob J;
+    int job, head, k0, k1;  // units k0..k1-1 of the job
+    E0_DEV bool has(int h, int k) const { return k >= J.k0[h] && k < J.k1[h]; }
+    E0_DEV int first(int h) const { return max(k0, J.k0[h]); }
+    E0_DEV int end(int h) const { return min(k1, J.k1[h]); }
+    E0_DEV bool whole() const { return k0 == 0 && k1 == J.units; }
+};
+
+struct Pieces {
+    const TileArgs& A;
+    uint32_t left;
+    int job, head, k;
+    E0_DEV Pieces(const TileArgs& args) : A(args), left(0), job(-1), head(0), k(0) {
+        const TileHead h = *A.head;
+        const uint32_t u = blockIdx.x * h.share;
+        if (u < h.total) {
+            const int4 b = A.begin[blockIdx.x];
+            job = b.x, head = b.y, k = b.z;
+            left = min(h.share, h.total - u);
+        }
+    }
+    E0_DEV bool next(Piece& p) {
+        if (left == 0) return false;
+        const int4* from = reinterpret_cast<const int4*>(A.jobs + job);
+        int4* to = reinterpret_cast<int4*>(&p.J);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(TileJob) / 16); ++i) to[i] = __ldcg(from + i);
+        p.job = job, p.head = head, p.k0 = k;
+        p.k1 = min(p.J.units, k + (int)left);
+        left -= p.k1 - p.k0;
+        k = 0;
+        if (++head == A.a.Hkv) head = 0, ++job;
+        return true;
+    }
+};
+static_assert(sizeof(TileJob) == 64, "four 16-byte loads");
+
+// ---------------------------------------------------------------- operands
+
+// Operand descriptor without swizzle: 8 x 16-byte blocks of 128 bytes, `lead` and `stride`
+// bytes apart.  K-major: lead from 8 elements of k to the next, stride from 8 rows to the
+// next; MN-major: lead from 8 elements of k to the next, stride from 8 elements of the other
+// side to the next.
+E0_DEV uint64_t sdesc_plain(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46;
+}
+constexpr uint32_t B_MN_MAJOR = 1u << 16;  // of the instruction descriptor
+
+E0_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+E0_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+template <int D>
+struct TileSmem {
+    uint8_t q[Geo<D>::Q_BYTES];
+    uint8_t k[Geo<D>::STAGES][Geo<D>::OPERAND];
+    uint8_t v[Geo<D>::STAGES][Geo<D>::OPERAND];
+    float4 sc[Geo<D>::STAGES][Geo<D>::KV / 16];  // of 16 tokens: keys' scale, values' log2 and inverse, seen (1) or not
+    uint64_t k_full[Geo<D>::STAGES], k_empty[Geo<D>::STAGES], v_full[Geo<D>::STAGES], v_empty[Geo<D>::STAGES];
+    uint64_t s_full[2], p_full[2], o_done[2], q_full[2], drained;
+    uint32_t tmem, abort;
+};
+
+// 16 codes as 16 fp16: two 16-byte chunks.
+E0_DEV void widen16(const uint4 c, uint4& a, uint4& b) {
+    a = make_uint4(e4m3x2_to_half2((uint16_t)c.x), e4m3x2_to_half2((uint16_t)(c.x >> 16)), e4m3x2_to_half2((uint16_t)c.y),
+                   e4m3x2_to_half2((uint16_t)(c.y >> 16)));
+    b = make_uint4(e4m3x2_to_half2((uint16_t)c.z), e4m3x2_to_half2((uint16_t)(c.z >> 16)), e4m3x2_to_half2((uint16_t)c.w),
+                   e4m3x2_to_half2((uint16_t)(c.w >> 16)));
+}
+
+template <int TY>
+E0_DEV void put_row4(const AttnArgs& a, bool vec, size_t tok, int col, float x, float y, float z, float w) {
+    if (a.raw) {
+        *reinterpret_cast<float4*>(a.raw + tok * ((size_t)a.Hq * a.D) + col) = make_float4(x, y, z, w);
+        return;
+    }
+    typedef typename Elem<TY>::T T;
+    T* to = reinterpret_cast<T*>(a.out) + tok * a.out_ld + col;
+    if (vec) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack16<TY>(x, y), pack16<TY>(z, w));
+    } else {
+        to[0] = Elem<TY>::put(x), to[1] = Elem<TY>::put(y), to[2] = Elem<TY>::put(z), to[3] = Elem<TY>::put(w);
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// TY: E0_F16 or E0_BF16.  RULES: scores are capped or lose with the distance.
+template <int D, int TY, bool RULES>
+__global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_constant__ TileArgs A) {
+    typedef Geo<D> G_;
+    typedef typename Elem<TY>::T T;
+    constexpr bool SPLIT = TY == E0_F16;
+    constexpr int KV = G_::KV, STAGES = G_::STAGES, HALVES = G_::HALVES;
+    extern __shared__ __align__(1024) char tile_sm[];
+    TileSmem<D>& S = *reinterpret_cast<TileSmem<D>*>(tile_sm);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = A.a.Hq / A.a.Hkv;
+    volatile uint32_t* abort = &S.abort;
+    const volatile uint32_t never = 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&S.k_full[s], 4), mbar_init(&S.v_full[s], 4);
+            mbar_init(&S.k_empty[s], 1), mbar_init(&S.v_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&S.s_full[s], 1), mbar_init(&S.o_done[s], 1);
+            mbar_init(&S.p_full[s], 4), mbar_init(&S.q_full[s], 4);
+        }
+        mbar_init(&S.drained, 1);
+        S.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == G_::SOFT + 4) tmem_alloc(&S.tmem, TILE_TMEM);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const auto give_up = [&]() {
+        *abort = 1;
+        set_status(A.a.st, E0_ST_TIMEOUT);
+    };
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the schedule is there
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Pieces pieces(A);
+
+    if (warp < G_::SOFT) {
+        // ---------------- softmax: a thread a row, half h of the tile
+        const int h = warp >> 2, t = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t o_at = tmem + lanes + G_::O_COL + h * D;
+        uint32_t n_s = 0;   // S of this half so far
+        uint32_t gk = 0;    // units of the block before this piece
+        bool ok = true;
+        // The second products of this half's n-th S are done.  (A warp may be two units ahead of
+        // another's P with one half: a barrier for even and one for odd units, so that a phase
+        // is never mistaken for the one before the last.)
+        const auto wait_o = [&](uint32_t n) {
+            return HALVES == 2 ? mbar_wait(&S.o_done[h], n & 1, abort, TILE_WAIT_NS)
+                               : mbar_wait(&S.o_done[n & 1], (n >> 1) & 1, abort, TILE_WAIT_NS);
+        };
+        Piece p;
+        TileCut begun = {0, 0, 0, 0}, went_on = {0, 0, 0, 0};
+        while (ok && pieces.next(p)) {
+            const TileJob& J = p.J;
+            const int r = J.mtile * G_::ROWS + 128 * h + t;  // row of the sequence: token, head of the group
+            const bool row_ok = 128 * h + t < J.rows;
+            const int i = r / G, head = p.head * G + r % G;
+            const size_t tok = (size_t)J.row0 + i;
+            const int kf = p.first(h), ke = p.end(h);
+            int pos = 0, lo = 0, hi = 0;
+            if (row_ok) range_of(A, J.seq, J.row0, J.p0, J.hi, i, pos, lo, hi);
+            float mx = -INFINITY, sum = 0.f, f = 0.f, slope = 0.f;
+            if (kf < ke) {
+                // ---- the row into shared memory
+                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(A.a.q) +
+                                                                  (row_ok ? tok * A.a.q_ld + (size_t)head * D : 0));
+                uint8_t* dst = S.q + (size_t)(128 * h + t) / 8 * (16 * D) + (t & 7) * 16;
+                if constexpr (TY == E0_F16) {
+                    uint32_t odd = 0;
+#pragma unroll 8
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (row_ok) u = __ldg(src + c);
+                        *reinterpret_cast<uint4*>(dst + c * 128) = u;
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) odd |= (w[k] & 0x7C007C00u) + 0x04000400u;  // exponent of all ones carries
+                    }
+                    f = odd & 0x80008000u ? __uint_as_float(0x7FC00000u) : A.a.scale * LOG2E;
+                } else {
+                    uint32_t m = 0;
+#pragma unroll 8
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (row_ok) u = __ldg(src + c);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+                    }
+                    m <<= 16;
+                    int e = (int)(m >> 23);
+                    e = e < 27 ? 27 : e > 253 ? 253 : e;
+                    const float down = m == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll 8
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (row_ok) u = __ldg(src + c);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 v = unpack16<E0_BF16>(w[k]);
+                            x[k] = half2_of(v.x * down, v.y * down);
+                        }
+                        *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    f = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)e << 23) * A.a.scale * LOG2E;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.q_full[h]);
+                if (RULES && A.a.slopes && row_ok) slope = A.a.slopes[head] * LOG2E;
+            }
+            // ---- units
+            for (int k = kf; k < ke; ++k, ++n_s) {
+                const uint32_t g = gk + (uint32_t)(k - p.k0), st = g % STAGES;
+                const uint32_t slot = HALVES == 2 ? h : n_s & 1, use = HALVES == 2 ? n_s : n_s >> 1;
+                const uint32_t s_at = tmem + lanes + slot * KV;
+                ok = mbar_wait(&S.s_full[slot], use & 1, abort, TILE_WAIT_NS) &&
+                     mbar_wait(&S.v_full[st], (g / STAGES) & 1, abort, TILE_WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const int at0 = (J.unit0 + k) * KV;
+                bool edge = at0 < lo || at0 + KV > hi;
+                if (lane < KV / 16) edge |= !(S.sc[st][lane].w > 0.f);
+                edge = __any_sync(0xffffffffu, edge);
+                const float away = (float)(pos - at0);
+                // t of 32 positions
+                const auto scores = [&](int c, float (&v)[32]) {
+                    uint32_t u[32];
+                    tmem_ld32(s_at + 32 * c, u);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float4 sc = S.sc[st][2 * c + q];
+                        const float fk = f * sc.x;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float s = __uint_as_float(u[16 * q + j]);
+                            if constexpr (RULES) {
+                                float x = s * fk;
+                                if (A.a.cap > 0.f) {
+                                    // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), a step of fp32 of cap off
+                                    const float e = exp2_of(fminf(x * A.a.inv_cap * (2.f * LOG2E), 126.f));
+                                    x = fmaf(-2.f * A.a.cap, __frcp_rn(1.f + e), A.a.cap);
+                                }
+                                x = fmaf(-slope, fabsf(away - (float)(32 * c + 16 * q + j)), x);
+                                v[16 * q + j] = x + sc.y;
+                            } else {
+                                v[16 * q + j] = fmaf(s, fk, sc.y);
+                            }
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const int at = at0 + 32 * c + 16 * q + j;
+                                if (at < lo || at >= hi || !(sc.w > 0.f)) v[16 * q + j] = -INFINITY;
+                            }
+                        }
+                    }
+                };
+                float top = mx;
+#pragma unroll 1
+                for (int c = 0; c < KV / 32; ++c) {
+                    float v[32];
+                    scores(c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+                }
+                const bool grows = top > mx + SLACK;
+                if (__any_sync(0xffffffffu, grows)) {
+                    if (!grows) top = mx;
+                    const float keep = mx == top ? 1.f : exp2_of(mx - top);
+                    mx = top;
+                    sum *= keep;
+                    if (k > kf) {  // O of the units before
+                        ok = wait_o(n_s - 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t u[32];
+                            tmem_ld32(o_at + 32 * c, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * keep);
+                            tmem_st32(o_at + 32 * c, u);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float base = (mx == -INFINITY ? 0.f : mx) - LIFT;
+#pragma unroll 1
+                for (int c = 0; c < KV / 32; ++c) {
+                    float v[32];
+                    scores(c, v);
+                    uint32_t hi16[16], lo16[SPLIT ? 16 : 1];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float iv = S.sc[st][2 * c + q].z;
+                        float part = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float a = exp2_of(v[16 * q + 2 * j] - base), b = exp2_of(v[16 * q + 2 * j + 1] - base);
+                            part += a + b;
+                            if constexpr (SPLIT)
+                                split_half(a, b, hi16[8 * q + j], lo16[8 * q + j]);
+                            else
+                                hi16[8 * q + j] = half2_of(a, b);
+                        }
+                        if (iv < INFINITY) sum = fmaf(part, iv, sum);
+                    }
+                    tmem_st16(s_at + 32 * c, hi16);
+                    if constexpr (SPLIT) tmem_st16(s_at + 32 * c + 16, lo16);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_full[slot]);
+            }
+            if (!ok) break;
+            gk += (uint32_t)(p.k1 - p.k0);
+            // ---- the row's result, or its part
+            const bool whole = p.whole();
+            const int part = 2 * blockIdx.x + (p.k0 == 0 ? 1 : 0);
+            if (kf < ke) {
+                ok = wait_o(n_s - 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const float inv = sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t u[32];
+                if (kf < ke) {
+                    tmem_ld32(o_at + 32 * c, u);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) u[j] = 0;
+                }
+                if (row_ok) {
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            put_row4<TY>(A.a, A.vec_out, tok, head * D + 32 * c + j, __uint_as_float(u[j]) * inv,
+                                         __uint_as_float(u[j + 1]) * inv, __uint_as_float(u[j + 2]) * inv,
+                                         __uint_as_float(u[j + 3]) * inv);
+                    } else {
+                        uint4* to = reinterpret_cast<uint4*>(A.part_o + ((size_t)part * G_::ROWS + 128 * h + t) * D + 32 * c);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) to[j / 4] = make_uint4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+                    }
+                }
+            }
+            tc_fence_before();  // O has been read before the next job's P is there
+            if (row_ok) {
+                if (!whole)
+                    A.part_ml[(size_t)part * G_::ROWS + 128 * h + t] = make_float2(mx, sum);
+                else if (A.a.lse)
+                    A.a.lse[tok * A.a.Hq + head] = lse_of(mx, sum);
+            }
+            if (!whole && threadIdx.x == 0) {
+                const uint32_t u0 = J.start + (uint32_t)p.head * J.units, share = A.head->share;
+                const int b0 = (int)(u0 / share), b1 = (int)((u0 + J.units - 1) / share);
+                (p.k0 == 0 ? begun : went_on) = {b1 - b0 + 1, b0, p.job, p.head};
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        if (threadIdx.x == 0) A.cuts[2 * blockIdx.x] = begun, A.cuts[2 * blockIdx.x + 1] = went_on;
+    } else if (warp < G_::SOFT + 4) {
+        // ---------------- codes into operands
+        const int cw = warp - G_::SOFT;
+        constexpr int L = G_::LOADS, PER = D / 64;  // loads; of 64 bytes a group of 8 tokens
+        Piece p;
+        bool more = pieces.next(p);
+        int k = more ? p.k0 : 0;
+        uint4 kr[L], vr[L];
+        // of the unit that is loaded: lane l < KV / 16 has the block of 16 tokens l
+        int id = -1;
+        float ks = 0.f, vs = 0.f;
+        bool edge = false;
+        const auto look_up = [&]() {
+            const TileJob& J = p.J;
+            const int at0 = (J.unit0 + k) * KV, at = at0 + 16 * lane;
+            id = -1;
+            if (lane < KV / 16 && at < J.hi && at + 16 > J.lo) {
+                id = A.a.table[(size_t)J.seq * A.a.max_blocks + (at >> A.a.shift)];
+                if (id >= 0 && id < A.a.n_blocks) {
+                    const size_t i = (size_t)id * A.a.Hkv + p.head;
+                    ks = A.a.ks[i], vs = A.a.vs[i];
+                } else {
+                    id = -1;
+                    set_status(A.a.st, E0_ST_BAD_BLOCK);
+                }
+            }
+            edge = at0 < J.full_lo || at0 + KV > J.full_hi;
+        };
+        const int bs = 1 << A.a.shift;
+        // load i: tokens 8 * group + lane % 8, 16 bytes of 64 of them
+        const auto load = [&](const uint8_t* from, uint4 (&to)[L]) {
+            const int at0 = (p.J.unit0 + k) * KV;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int n = 4 * i + cw, group = n / PER, part = n % PER;
+                const int token = 8 * group + (lane & 7), at = at0 + token;
+                const int b = __shfl_sync(0xffffffffu, id, group >> 1);
+                to[i] = make_uint4(0, 0, 0, 0);
+                if (b >= 0 && at < p.J.hi)
+                    to[i] = __ldg(reinterpret_cast<const uint4*>(
+                        from + ((((size_t)b * A.a.Hkv + p.head) << A.a.shift) + (at & (bs - 1))) * D + 64 * part + 16 * (lane >> 3)));
+            }
+        };
+        const auto store = [&](const uint4 (&from)[L], uint8_t* to, bool clean) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int n = 4 * i + cw, group = n / PER, part = n % PER;
+                uint8_t* dst = to + group * (16 * D) + (8 * part + 2 * (lane >> 3)) * 128 + (lane & 7) * 16;
+                uint4 c = from[i], a, b;
+                if (clean) c.x = without_nan(c.x), c.y = without_nan(c.y), c.z = without_nan(c.z), c.w = without_nan(c.w);
+                widen16(c, a, b);
+                *reinterpret_cast<uint4*>(dst) = a;
+                *reinterpret_cast<uint4*>(dst + 128) = b;
+            }
+        };
+        if (more) {
+            look_up();
+            load(A.a.k, kr);
+            load(A.a.v, vr);
+        }
+        bool ok = true;
+        for (uint32_t g = 0; more; ++g) {
+            const uint32_t st = g % STAGES, par = ((g / STAGES) + 1) & 1;
+            const bool clean = edge;
+            const float4 sc = id >= 0 ? make_float4(ks, log2f(fmaxf(vs, LEAST_SCALE)), SUM_UNIT / fmaxf(vs, LEAST_SCALE), 1.f)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (++k == p.k1) {
+                more = pieces.next(p);
+                k = p.k0;
+            }
+            if (more) look_up();
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.k_empty[st], par, abort, TILE_WAIT_NS));
+            if (!ok) break;
+            store(kr, S.k[st], false);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.k_full[st]);
+            if (more) load(A.a.k, kr);
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.v_empty[st], par, abort, TILE_WAIT_NS));
+            if (!ok) break;
+            if (cw == 0 && lane < KV / 16) S.sc[st][lane] = sc;
+            store(vr, S.v[st], clean);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.v_full[st]);
+            if (more) load(A.a.v, vr);
+        }
+        if (!ok && lane == 0) give_up();
+    } else {
+        // ---------------- products
+        if (lane == 0) {
+            const uint32_t q_at = smem_u32(S.q);
+            const uint32_t id_s = idesc_f16_f32(128, KV), id_o = idesc_f16_f32(128, D) | B_MN_MAJOR;
+            uint32_t n_s[2] = {0, 0}, n_q[2] = {0, 0}, gk = 0;
+            bool ok = true, issued = false;
+            Piece p;
+            // O of half h += P V of unit k (its number in the block: g)
+            const auto second = [&](int h, int k, uint32_t g, uint32_t n) {
+                const uint32_t st = g % STAGES, slot = HALVES == 2 ? h : n & 1, use = HALVES == 2 ? n : n >> 1;
+                if (!mbar_wait(&S.p_full[slot], use & 1, abort, TILE_WAIT_NS)) return false;
+                tc_fence_after();
+                const uint32_t v_at = smem_u32(S.v[st]), p_at = tmem + slot * KV, o_at = tmem + G_::O_COL + h * D;
+#pragma unroll
+                for (int s = 0; s < KV / 16; ++s) {
+                    const uint64_t b = sdesc_plain(v_at + s * 32 * D, 16 * D, 128);
+                    const uint32_t a = p_at + 32 * (s / 2) + 8 * (s % 2);
+                    umma_f16_ta(o_at, a, b, id_o, k > p.first(h) || s > 0);
+                    if constexpr (SPLIT) umma_f16_ta(o_at, a + 16, b, id_o, 1);
+                }
+                umma_commit(&S.o_done[slot]);
+                return true;
+            };
+            const auto wait_v = [&](uint32_t g) { return mbar_wait(&S.v_full[g % STAGES], (g / STAGES) & 1, abort, TILE_WAIT_NS); };
+            while (ok && pieces.next(p)) {
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+                    if (ok && p.first(h) < p.end(h)) ok = mbar_wait(&S.q_full[h], n_q[h]++ & 1, abort, TILE_WAIT_NS);
+                // one turn more than units: a unit's second products come with the next one's first
+                for (int k = p.k0; ok && k <= p.k1; ++k) {
+                    const uint32_t g = gk + (uint32_t)(k - p.k0), st = g % STAGES;
+                    const bool now = k < p.k1, before = k > p.k0;
+                    if (now) ok = mbar_wait(&S.k_full[st], (g / STAGES) & 1, abort, TILE_WAIT_NS);
+                    if (ok && before) ok = wait_v(g - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const auto first = [&](int h) {
+                        const uint32_t slot = HALVES == 2 ? h : n_s[h] & 1;
+                        const uint32_t k_at = smem_u32(S.k[st]), qh = q_at + h * 128 * D * 2;
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s)
+                            umma_f16(tmem + slot * KV, sdesc_plain(qh + s * 256, 128, 16 * D),
+                                     sdesc_plain(k_at + s * 256, 128, 16 * D), id_s, s > 0);
+                        umma_commit(&S.s_full[slot]);
+                        ++n_s[h];
+                    };
+                    if constexpr (HALVES == 2) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (ok && before && p.has(h, k - 1)) ok = second(h, k - 1, g - 1, n_s[h] - 1);
+                            if (ok && now && p.has(h, k)) first(h);
+                        }
+                    } else {
+                        const uint32_t n = n_s[0];
+                        if (now && p.has(0, k)) first(0);
+                        if (before && p.has(0, k - 1)) ok = second(0, k - 1, g - 1, n - 1);
+                    }
+                    issued = true;
+                    if (!ok) break;
+                    if (now) umma_commit(&S.k_empty[st]);
+                    if (before) umma_commit(&S.v_empty[(g - 1) % STAGES]);
+                }
+                gk += (uint32_t)(p.k1 - p.k0);
+            }
+            if (!ok) give_up();
+            if (issued) {  // the products have ended before tensor memory is freed
+                umma_commit(&S.drained);
+                mbar_wait(&S.drained, 0, &never, TILE_WAIT_NS);
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == G_::SOFT + 4) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TILE_TMEM);
+    }
+}
+
+// ---------------------------------------------------------------- jobs that several blocks have
+
+constexpr int TILE_JOIN_THREADS = 256;
+constexpr int TILE_JOIN_ROWS = 16;
+
+template <int D, int TY>
+__global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
+    typedef Geo<D> G_;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+    const TileCut cut = A.cuts[2 * blockIdx.x];
+    if (cut.parts == 0) return;
+    const TileJob J = A.jobs[cut.job];
+    const int G = A.a.Hq / A.a.Hkv, d4 = threadIdx.x % (D / 4) * 4;
+    const auto slot_of = [&](int r, int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * G_::ROWS + r; };
+    const int r0 = blockIdx.y * TILE_JOIN_ROWS, r1 = min(J.rows, r0 + TILE_JOIN_ROWS);
+    for (int r = r0 + threadIdx.x / (D / 4); r < r1; r += TILE_JOIN_THREADS / (D / 4)) {
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int BATCH = 4;
+        for (int i0 = 0; i0 < cut.parts; i0 += BATCH) {
+            float2 ml[BATCH];
+            float4 x[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < cut.parts) {
+                    ml[i] = A.part_ml[slot_of(r, i0 + i)];
+                    x[i] = *reinterpret_cast<const float4*>(A.part_o + slot_of(r, i0 + i) * D + d4);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) top = fmaxf(top, ml[i].x);
+            const float base = top == -INFINITY ? 0.f : top, keep = exp2_of(m - base);
+            m = top;
+            l *= keep;
+            o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const float w = exp2_of(ml[i].x - base);
+                l += w * ml[i].y;
+                o.x += w * x[i].x, o.y += w * x[i].y, o.z += w * x[i].z, o.w += w * x[i].w;
+            }
+        }
+        const float inv = l > 0.f || l != l ? SUM_UNIT / l : 0.f;
+        const int row = J.mtile * G_::ROWS + r, head = cut.head * G + row % G;
+        const size_t tok = (size_t)J.row0 + row / G;
+        put_row4<TY>(A.a, A.vec_out, tok, head * D + d4, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (A.a.lse && d4 == 0) A.a.lse[tok * A.a.Hq + head] = lse_of(m, l);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+inline int tile_blocks() { return num_sms(); }
+inline long long tile_jobs(int B, int max_q, int G, int D) {
+    const int rows = D == 256 ? 128 : 256;
+    return (long long)B * (((long long)max_q * G + rows - 1) / rows);
+}
+inline size_t tile_ws_bytes(int B, int max_q, int G, int D) {
+    const size_t rows = D == 256 ? 128 : 256, slots = 2 * (size_t)tile_blocks();
+    return up256(slots * rows * D * sizeof(float)) + up256(slots * rows * sizeof(float2)) + up256(slots * sizeof(TileCut)) +
+           up256((size_t)tile_jobs(B, max_q, G, D) * sizeof(TileJob)) + up256(tile_blocks() * sizeof(int4)) + 256;
+}
+
+template <int D, int TY, bool RULES>
+int tile_launch(const TileArgs& t, cudaStream_t s) {
+    static std::atomic<uint64_t> asked{0};
+    if (!allow_smem((const void*)k_attn_tile<D, TY, RULES>, sizeof(TileSmem<D>), asked)) return E0_ERR_CUDA;
+    k_tile_plan<D><<<1, PLAN_THREADS, (size_t)(t.a.B + 1) * sizeof(uint32_t), s>>>(t);
+    if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.stream = s;
+    cfg.gridDim = dim3(t.blocks);
+    cfg.blockDim = dim3(Geo<D>::THREADS);
+    cfg.dynamicSmemBytes = sizeof(TileSmem<D>);
+    if (cudaLaunchKernelEx(&cfg, k_attn_tile<D, TY, RULES>, t) != cudaSuccess) return E0_ERR_CUDA;
+    cfg.gridDim = dim3(t.blocks, Geo<D>::ROWS / TILE_JOIN_ROWS);
+    cfg.blockDim = dim3(TILE_JOIN_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_tile_join<D, TY>, t) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
+}
+
+template <int D>
+int tile_launch_d(const TileArgs& t, int dtype, cudaStream_t s) {
+    const bool rules = t.a.cap > 0.f || t.a.slopes;
+    if (dtype == E0_F16) return rules ? tile_launch<D, E0_F16, true>(t, s) : tile_launch<D, E0_F16, false>(t, s);
+    return rules ? tile_launch<D, E0_BF16, true>(t, s) : tile_launch<D, E0_BF16, false>(t, s);
+}
+
+// The arguments of the kernels above; `ws` of tile_ws_bytes.
+inline TileArgs tile_args(const AttnArgs& a, int dtype, void* ws) {
+    TileArgs t = {};
+    t.a = a;
+    t.a.unit = a.D == 256 ? 64 : 128;
+    t.blocks = tile_blocks();
+    t.most_jobs = (int)tile_jobs(a.B, a.max_q, a.Hq / a.Hkv, a.D);
+    const size_t rows = a.D == 256 ? 128 : 256, slots = 2 * (size_t)t.blocks;
+    char* p = reinterpret_cast<char*>(ws);
+    const auto take = [&](size_t n) {
+        char* at = p;
+        p += up256(n);
+        return at;
+    };
+    t.part_o = reinterpret_cast<float*>(take(slots * rows * a.D * sizeof(float)));
+    t.part_ml = reinterpret_cast<float2*>(take(slots * rows * sizeof(float2)));
+    t.cuts = reinterpret_cast<TileCut*>(take(slots * sizeof(TileCut)));
+    t.jobs = reinterpret_cast<TileJob*>(take((size_t)t.most_jobs * sizeof(TileJob)));
+    t.begin = reinterpret_cast<int4*>(take(t.blocks * sizeof(int4)));
+    t.head = reinterpret_cast<TileHead*>(take(sizeof(TileHead)));
+    t.vec_out = a.raw || (!((uintptr_t)a.out & 7) && (a.out_ld * type_size(dtype)) % 8 == 0);
+    return t;
+}
+
+}  // namespace
+}  // namespace e0

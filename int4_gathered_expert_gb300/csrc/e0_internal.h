@@ -66,6 +66,15 @@ size_t attn_ws_bytes(int D);
 int attn_decode(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu,
                 int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale, int window, void* out,
                 int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s);
+size_t attn_scored_ws_bytes(int B, int Hq, int Hkv, int D, int max_q);
+int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu, int B,
+                int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale, const e0_attn_rules* rules,
+                void* out, int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s);
+size_t attn_shared_ws_bytes(int B, int T, int Hq, int Hkv, int D, int max_q);
+int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_blocks, const int32_t* prefix_len,
+                const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu, int B, int T, int max_q,
+                const void* q, int dtype, int64_t q_ld, int Hq, float scale, const e0_attn_rules* rules, void* out,
+                int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s);
 int qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const e0_rope* r, const int32_t* pos,
             int64_t pos_ld, void* y, int64_t y_ld, uint32_t* st, cudaStream_t s);
 int sample(const void* x, int dtype, int64_t ld, int T, int V, const e0_sampling* r, const float* u, int32_t* token,

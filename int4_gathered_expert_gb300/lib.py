@@ -83,6 +83,10 @@ class KvState(C.Structure):
                 ("B", i32), ("max_blocks", i32), ("block_tokens", i32), ("n_blocks", i32)]
 
 
+class AttnRules(C.Structure):
+    _fields_ = [("cap", C.c_float), ("window", i32), ("slopes", vp), ("first", vp), ("open_len", vp)]
+
+
 class Rope(C.Structure):
     _fields_ = [("freq", vp), ("axis", vp), ("q_norm", vp), ("k_norm", vp), ("D", i32), ("rot", i32),
                 ("n_axes", i32), ("flags", i32), ("eps", C.c_float)]
@@ -146,6 +150,12 @@ def load() -> C.CDLL:
         "e0_attn_workspace_size": (sz, [C.c_int] * 5),
         "e0_attn_decode": (C.c_int, [P(KvCache), vp, C.c_int, vp, vp, C.c_int, C.c_int, vp, C.c_int, i64, C.c_int,
                                      C.c_float, C.c_int, vp, i64, vp, vp, sz, vp, vp]),
+        "e0_attn_scored_workspace_size": (sz, [C.c_int] * 5),
+        "e0_attn_scored": (C.c_int, [P(KvCache), vp, C.c_int, vp, vp, C.c_int, C.c_int, vp, C.c_int, i64, C.c_int,
+                                     C.c_float, P(AttnRules), vp, i64, vp, vp, sz, vp, vp]),
+        "e0_attn_shared_workspace_size": (sz, [C.c_int] * 6),
+        "e0_attn_shared": (C.c_int, [P(KvCache), vp, C.c_int, vp, vp, C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, vp,
+                                     C.c_int, i64, C.c_int, C.c_float, P(AttnRules), vp, i64, vp, vp, sz, vp, vp]),
         "e0_qk_rope": (C.c_int, [vp, C.c_int, i64, C.c_int, C.c_int, C.c_int, P(Rope), vp, i64, vp, i64, vp, vp]),
         "e0_sample": (C.c_int, [vp, C.c_int, i64, C.c_int, C.c_int, P(Sampling), vp, vp, vp, vp, vp, vp]),
         "e0_selftest_bounded_wait": (C.c_int, [vp, C.c_uint32, vp, vp]),
@@ -172,6 +182,7 @@ def exported_symbols():
             "e0_moe_prefill_forward",
             "e0_rmsnorm_q8", "e0_linear_bytes", "e0_pack_linear", "e0_linear_forward", "e0_kv_plan", "e0_kv_release",
             "e0_kv_append", "e0_attn_workspace_size", "e0_attn_decode",
+            "e0_attn_scored_workspace_size", "e0_attn_scored", "e0_attn_shared_workspace_size", "e0_attn_shared",
             "e0_qk_rope", "e0_sample",
             "e0_selftest_bounded_wait", "e0_read_status", "e0_status_string"]
 
@@ -436,6 +447,33 @@ def e0_attn_decode(cache: KvCache, block_table, max_blocks, ctx_len, cu_q, B, ma
                                ptr(q), dtype, q_ld, Hq, scale, window, ptr(out), out_ld, ptr(lse), ptr(ws), ws_bytes,
                                ptr(status), stream_handle(stream))
     return _check("e0_attn_decode", rc, raise_on_error)
+
+
+def e0_attn_scored_workspace_size(B, Hq, Hkv, D, max_q):
+    return load().e0_attn_scored_workspace_size(B, Hq, Hkv, D, max_q)
+
+
+def e0_attn_scored(cache: KvCache, block_table, max_blocks, ctx_len, cu_q, B, max_q, q, dtype, q_ld, Hq, scale,
+                   rules: Optional[AttnRules], out, out_ld, lse, ws, ws_bytes, status=None, stream=None,
+                   raise_on_error=True):
+    rc = load().e0_attn_scored(C.byref(cache), ptr(block_table), max_blocks, ptr(ctx_len), ptr(cu_q), B, max_q, ptr(q),
+                               dtype, q_ld, Hq, scale, C.byref(rules) if rules is not None else None, ptr(out), out_ld,
+                               ptr(lse), ptr(ws), ws_bytes, ptr(status), stream_handle(stream))
+    return _check("e0_attn_scored", rc, raise_on_error)
+
+
+def e0_attn_shared_workspace_size(B, T, Hq, Hkv, D, max_q):
+    return load().e0_attn_shared_workspace_size(B, T, Hq, Hkv, D, max_q)
+
+
+def e0_attn_shared(cache: KvCache, prefix_table, prefix_blocks, prefix_len, block_table, max_blocks, ctx_len, cu_q, B,
+                   T, max_q, q, dtype, q_ld, Hq, scale, rules: Optional[AttnRules], out, out_ld, lse, ws, ws_bytes,
+                   status=None, stream=None, raise_on_error=True):
+    rc = load().e0_attn_shared(C.byref(cache), ptr(prefix_table), prefix_blocks, ptr(prefix_len), ptr(block_table),
+                               max_blocks, ptr(ctx_len), ptr(cu_q), B, T, max_q, ptr(q), dtype, q_ld, Hq, scale,
+                               C.byref(rules) if rules is not None else None, ptr(out), out_ld, ptr(lse), ptr(ws),
+                               ws_bytes, ptr(status), stream_handle(stream))
+    return _check("e0_attn_shared", rc, raise_on_error)
 
 
 def e0_qk_rope(x, dtype, x_ld, T, Hq, Hk, rope: Rope, positions, pos_ld, y, y_ld, status=None, stream=None,
