@@ -36,7 +36,7 @@ struct Geo {
     static constexpr int STAGES = D == 64 ? 3 : 2;
     static constexpr int OPERAND = KV * D * 2;
     static constexpr int SOFT = 4 * HALVES;  // softmax warps
-    static constexpr int THREADS = (SOFT + 4 + 1) * 32;
+    static constexpr int THREADS = (SOFT + 4 + 4) * 32;  // and the converting ones; of the last four, one issues the products
     static constexpr int O_COL = 2 * KV;  // tensor memory: two S, then the halves' O
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int LOADS = KV * D / (4 * 512);  // 16-byte loads of a converting lane for one operand
@@ -68,8 +68,12 @@ struct TileArgs {
     int4* begin;              // [blocks]: job, head, unit
     TileHead* head;
     int blocks, most_jobs;
+    uint32_t by_group;        // n / G = n * by_group >> 31 + by_shift for n below 2^31
+    int by_shift;
     bool vec_out;
 };
+
+E0_DEV int div_group(const TileArgs& A, int n) { return (int)((unsigned long long)(uint32_t)n * A.by_group >> (31 + A.by_shift)); }
 
 // The range of positions that a token of a sequence sees.
 E0_DEV void range_of(const TileArgs& A, int seq, int row0, int p0, int ctx, int i, int& p, int& lo, int& hi) {
@@ -212,9 +216,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
 struct Piece {
     TileJob J;
     int job, head, k0, k1;  // units k0..k1-1 of the job
-    E0_DEV bool has(int h, int k) const { return k >= J.k0[h] && k < J.k1[h]; }
-    E0_DEV int first(int h) const { return max(k0, J.k0[h]); }
-    E0_DEV int end(int h) const { return min(k1, J.k1[h]); }
+    // the units of the piece that half h has (no index that is not a constant: J stays in registers)
+    E0_DEV int first(int h) const { return max(k0, h ? J.k0[1] : J.k0[0]); }
+    E0_DEV int end(int h) const { return min(k1, h ? J.k1[1] : J.k1[0]); }
     E0_DEV bool whole() const { return k0 == 0 && k1 == J.units; }
 };
 
@@ -234,9 +238,8 @@ struct Pieces {
     E0_DEV bool next(Piece& p) {
         if (left == 0) return false;
         const int4* from = reinterpret_cast<const int4*>(A.jobs + job);
-        int4* to = reinterpret_cast<int4*>(&p.J);
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(TileJob) / 16); ++i) to[i] = __ldcg(from + i);
+        const int4 a = __ldcg(from), b = __ldcg(from + 1), c = __ldcg(from + 2), d = __ldcg(from + 3);
+        p.J = {a.x, a.y, a.z, a.w, {b.x, b.y}, {b.z, b.w}, c.x, c.y, c.z, c.w, (uint32_t)d.x, d.y, d.z, d.w};
         p.job = job, p.head = head, p.k0 = k;
         p.k1 = min(p.J.units, k + (int)left);
         left -= p.k1 - p.k0;
@@ -252,9 +255,29 @@ static_assert(sizeof(TileJob) == 64, "four 16-byte loads");
 // Operand descriptor without swizzle: 8 x 16-byte blocks of 128 bytes, `lead` and `stride`
 // bytes apart.  K-major: lead from 8 elements of k to the next, stride from 8 rows to the
 // next; MN-major: lead from 8 elements of k to the next, stride from 8 elements of the other
-// side to the next.
-E0_DEV uint64_t sdesc_plain(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46;
+// side to the next.  Low word: address and lead in 16-byte units; high word: stride, version 1.
+E0_DEV uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; }
+constexpr uint32_t desc_high(uint32_t stride) { return (stride >> 4) | 1u << 14; }
+// umma_f16 and umma_f16_ta with descriptors by their words: what changes from one product to
+// the next is one 32-bit addition.
+E0_DEV void umma_lo(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+E0_DEV void umma_ta_lo(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+E0_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 constexpr uint32_t B_MN_MAJOR = 1u << 16;  // of the instruction descriptor
 
@@ -293,6 +316,64 @@ E0_DEV void widen16(const uint4 c, uint4& a, uint4& b) {
                    e4m3x2_to_half2((uint16_t)(c.y >> 16)));
     b = make_uint4(e4m3x2_to_half2((uint16_t)c.z), e4m3x2_to_half2((uint16_t)(c.z >> 16)), e4m3x2_to_half2((uint16_t)c.w),
                    e4m3x2_to_half2((uint16_t)(c.w >> 16)));
+}
+
+// (a0 * f + c, a1 * f + c) and (s0 + a, s1 + b), a pair an instruction.
+E0_DEV void fma2(float& r0, float& r1, float a0, float a1, float f, float c) {
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(f), "f"(c));
+}
+E0_DEV void add2(float& s0, float& s1, float a, float b) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "+f"(s0), "+f"(s1)
+        : "f"(a), "f"(b));
+}
+E0_DEV float inverse_of(float x) {  // a step of fp32 off
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Bits 0 .. n-1, n any number.
+E0_DEV uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
+
+// 16 columns of fp32 in tensor memory times `keep` of the row.
+E0_DEV void scale16(uint32_t at, float keep) {
+    float v[16];
+    uint32_t u[16];
+    tmem_ld16(at, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * keep);
+    tmem_st16(at, u);
+}
+// 64 positions' weights in tensor memory, fp16 pairs (and 32 columns on their rests), times
+// `keep`.
+template <bool SPLIT>
+E0_DEV void scale_p(uint32_t at, float keep) {
+    tmem_st_wait();  // they have just been written
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 16) {
+        float hi[16], lo[16];
+        uint32_t a[16], b[16];
+        tmem_ld16(at + c, hi);
+        if constexpr (SPLIT) tmem_ld16(at + 32 + c, lo);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float2 x = unpack16<E0_F16>(__float_as_uint(hi[j]));
+            if constexpr (SPLIT) {
+                const float2 y = unpack16<E0_F16>(__float_as_uint(lo[j]));
+                x.x += y.x, x.y += y.y;
+                split_half(x.x * keep, x.y * keep, a[j], b[j]);
+            } else {
+                a[j] = half2_of(x.x * keep, x.y * keep);
+            }
+        }
+        tmem_st16(at + c, a);
+        if constexpr (SPLIT) tmem_st16(at + 32 + c, b);
+    }
 }
 
 template <int TY>
@@ -351,13 +432,17 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Pieces pieces(A);
 
+    // 512 threads are launched with 128 registers each; a softmax thread wants more, the others
+    // less: 256 x 168 + 128 x 112 + 128 x 64 = 512 x 128.  (384 threads have 168 each.)
     if (warp < G_::SOFT) {
+        if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ---------------- softmax: a thread a row, half h of the tile
         const int h = warp >> 2, t = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_at = tmem + lanes + G_::O_COL + h * D;
-        uint32_t n_s = 0;   // S of this half so far
-        uint32_t gk = 0;    // units of the block before this piece
+        uint8_t* mine = S.q + (size_t)(128 * h + 32 * (warp & 3)) * (2 * D);  // the warp's 32 rows of Q; its outputs on their way
+        uint32_t n_s = 0;  // S of this half so far
+        uint32_t gk = 0;   // units of the block before this piece
         bool ok = true;
         // The second products of this half's n-th S are done.  (A warp may be two units ahead of
         // another's P with one half: a barrier for even and one for odd units, so that a phase
@@ -372,57 +457,72 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             const TileJob& J = p.J;
             const int r = J.mtile * G_::ROWS + 128 * h + t;  // row of the sequence: token, head of the group
             const bool row_ok = 128 * h + t < J.rows;
-            const int i = r / G, head = p.head * G + r % G;
+            const int i = div_group(A, r), head = p.head * G + r - i * G;
             const size_t tok = (size_t)J.row0 + i;
             const int kf = p.first(h), ke = p.end(h);
             int pos = 0, lo = 0, hi = 0;
             if (row_ok) range_of(A, J.seq, J.row0, J.p0, J.hi, i, pos, lo, hi);
             float mx = -INFINITY, sum = 0.f, f = 0.f, slope = 0.f;
             if (kf < ke) {
-                // ---- the row into shared memory
-                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(A.a.q) +
-                                                                  (row_ok ? tok * A.a.q_ld + (size_t)head * D : 0));
-                uint8_t* dst = S.q + (size_t)(128 * h + t) / 8 * (16 * D) + (t & 7) * 16;
-                if constexpr (TY == E0_F16) {
-                    uint32_t odd = 0;
-#pragma unroll 8
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (row_ok) u = __ldg(src + c);
-                        *reinterpret_cast<uint4*>(dst + c * 128) = u;
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                // ---- the warp's rows into shared memory, 8 at a time: a lane has 16 bytes of every 64
+                // of row lane % 8
+                constexpr int C = D / 32, GB = D == 256 ? 2 : 4;
+#pragma unroll 1
+                for (int g0 = 0; g0 < 4; g0 += GB) {
+                    uint4 u[GB][C];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) odd |= (w[k] & 0x7C007C00u) + 0x04000400u;  // exponent of all ones carries
-                    }
-                    f = odd & 0x80008000u ? __uint_as_float(0x7FC00000u) : A.a.scale * LOG2E;
-                } else {
-                    uint32_t m = 0;
-#pragma unroll 8
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (row_ok) u = __ldg(src + c);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    for (int y = 0; y < GB; ++y) {
+                        const int row = 128 * h + 32 * (warp & 3) + 8 * (g0 + y) + (lane & 7), rr = J.mtile * G_::ROWS + row;
+                        const int ii = div_group(A, rr);
+                        const bool have = row < J.rows;
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            reinterpret_cast<const T*>(A.a.q) +
+                            (have ? ((size_t)J.row0 + ii) * A.a.q_ld + (size_t)(p.head * G + rr - ii * G) * D : 0));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) m = max(m, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-                    }
-                    m <<= 16;
-                    int e = (int)(m >> 23);
-                    e = e < 27 ? 27 : e > 253 ? 253 : e;
-                    const float down = m == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll 8
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (row_ok) u = __ldg(src + c);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 v = unpack16<E0_BF16>(w[k]);
-                            x[k] = half2_of(v.x * down, v.y * down);
+                        for (int c = 0; c < C; ++c) {
+                            u[y][c] = make_uint4(0, 0, 0, 0);
+                            if (have) u[y][c] = __ldg(src + 4 * c + (lane >> 3));
                         }
-                        *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(x[0], x[1], x[2], x[3]);
                     }
-                    f = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)e << 23) * A.a.scale * LOG2E;
+#pragma unroll
+                    for (int y = 0; y < GB; ++y) {
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            const uint32_t w[4] = {u[y][c].x, u[y][c].y, u[y][c].z, u[y][c].w};
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) m = __vmaxu2(m, w[z] & 0x7FFF7FFFu);
+                        }
+                        m = max(m & 0xFFFFu, m >> 16);
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        float fr;
+                        if constexpr (TY == E0_F16) {
+                            fr = m >= 0x7C00u ? __uint_as_float(0x7FC00000u) : A.a.scale * LOG2E;
+                        } else {  // times a power of two that brings the largest near 1
+                            const uint32_t b = m << 16;
+                            int e = (int)(b >> 23);
+                            e = e < 27 ? 27 : e > 253 ? 253 : e;
+                            const float down = b == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
+                            fr = b >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                                  : __uint_as_float((uint32_t)e << 23) * A.a.scale * LOG2E;
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                const uint32_t w[4] = {u[y][c].x, u[y][c].y, u[y][c].z, u[y][c].w};
+                                uint32_t x[4];
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const float2 v = unpack16<E0_BF16>(w[z]);
+                                    x[z] = half2_of(v.x * down, v.y * down);
+                                }
+                                u[y][c] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                        if (lane >> 3 == g0 + y) f = fr;  // this thread's own row is one of these
+                        uint8_t* dst = mine + (g0 + y) * (16 * D) + (lane & 7) * 16;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) *reinterpret_cast<uint4*>(dst + (4 * c + (lane >> 3)) * 128) = u[y][c];
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -444,95 +544,105 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 if (lane < KV / 16) edge |= !(S.sc[st][lane].w > 0.f);
                 edge = __any_sync(0xffffffffu, edge);
                 const float away = (float)(pos - at0);
-                // t of 32 positions
-                const auto scores = [&](int c, float (&v)[32]) {
-                    uint32_t u[32];
-                    tmem_ld32(s_at + 32 * c, u);
+                float base = (mx == -INFINITY ? 0.f : mx) - LIFT;
+#pragma unroll 1
+                for (int c = 0; c < KV / 64; ++c) {
+                    uint32_t u[2][32];
+                    tmem_ld32(s_at + 64 * c, u[0]);
+                    tmem_ld32(s_at + 64 * c + 32, u[1]);
+                    // x = t - base of 64 positions
+                    float x[64], top[4];
+                    float iv[4];  // of 16 positions: values' inverse
+                    const float4* scales = &S.sc[st][4 * c];
                     tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float4 sc = S.sc[st][2 * c + q];
-                        const float fk = f * sc.x;
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 sc = scales[q];
+                        const float fk = f * sc.x, off = sc.y - base;
+                        iv[q] = sc.z;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float s = __uint_as_float(u[16 * q + j]);
+                        for (int j = 0; j < 16; j += 2) {
+                            const float s0 = __uint_as_float(u[q / 2][16 * (q & 1) + j]);
+                            const float s1 = __uint_as_float(u[q / 2][16 * (q & 1) + j + 1]);
                             if constexpr (RULES) {
-                                float x = s * fk;
-                                if (A.a.cap > 0.f) {
-                                    // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), a step of fp32 of cap off
-                                    const float e = exp2_of(fminf(x * A.a.inv_cap * (2.f * LOG2E), 126.f));
-                                    x = fmaf(-2.f * A.a.cap, __frcp_rn(1.f + e), A.a.cap);
+                                float y[2] = {s0 * fk, s1 * fk};
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    if (A.a.cap > 0.f) {
+                                        // cap tanh(y / cap) = cap - 2 cap / (1 + e^(2 y / cap)), two steps of fp32 of cap off
+                                        const float e = exp2_of(fminf(y[z] * A.a.inv_cap * (2.f * LOG2E), 126.f));
+                                        y[z] = fmaf(-2.f * A.a.cap, inverse_of(1.f + e), A.a.cap);
+                                    }
+                                    y[z] = fmaf(-slope, fabsf(away - (float)(64 * c) - (float)(16 * q + j + z)), y[z]);
+                                    x[16 * q + j + z] = y[z] + off;
                                 }
-                                x = fmaf(-slope, fabsf(away - (float)(32 * c + 16 * q + j)), x);
-                                v[16 * q + j] = x + sc.y;
                             } else {
-                                v[16 * q + j] = fmaf(s, fk, sc.y);
-                            }
-                        }
-                        if (edge) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const int at = at0 + 32 * c + 16 * q + j;
-                                if (at < lo || at >= hi || !(sc.w > 0.f)) v[16 * q + j] = -INFINITY;
+                                fma2(x[16 * q + j], x[16 * q + j + 1], s0, s1, fk, off);
                             }
                         }
                     }
-                };
-                float top = mx;
-#pragma unroll 1
-                for (int c = 0; c < KV / 32; ++c) {
-                    float v[32];
-                    scores(c, v);
+                    if (edge) {
+                        const int a = at0 + 64 * c;
+                        uint32_t see[2] = {bits_below(hi - a) & ~bits_below(lo - a), bits_below(hi - a - 32) & ~bits_below(lo - a - 32)};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-                }
-                const bool grows = top > mx + SLACK;
-                if (__any_sync(0xffffffffu, grows)) {
-                    if (!grows) top = mx;
-                    const float keep = mx == top ? 1.f : exp2_of(mx - top);
-                    mx = top;
-                    sum *= keep;
-                    if (k > kf) {  // O of the units before
-                        ok = wait_o(n_s - 1);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t u[32];
-                            tmem_ld32(o_at + 32 * c, u);
-                            tmem_ld_wait();
+                        for (int q = 0; q < 4; ++q)
+                            if (!(scales[q].w > 0.f)) see[q / 2] &= q & 1 ? 0xFFFFu : 0xFFFF0000u;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * keep);
-                            tmem_st32(o_at + 32 * c, u);
-                        }
-                        tmem_st_wait();
+                        for (int j = 0; j < 64; ++j)
+                            if (!(see[j / 32] & (1u << (j & 31)))) x[j] = -INFINITY;
                     }
-                }
-                const float base = (mx == -INFINITY ? 0.f : mx) - LIFT;
-#pragma unroll 1
-                for (int c = 0; c < KV / 32; ++c) {
-                    float v[32];
-                    scores(c, v);
-                    uint32_t hi16[16], lo16[SPLIT ? 16 : 1];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float iv = S.sc[st][2 * c + q].z;
-                        float part = 0.f;
+                    for (int y = 0; y < 4; ++y) {  // four chains of maxima, three operands each
+                        top[y] = fmaxf(x[y], x[4 + y]);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float a = exp2_of(v[16 * q + 2 * j] - base), b = exp2_of(v[16 * q + 2 * j + 1] - base);
-                            part += a + b;
-                            if constexpr (SPLIT)
-                                split_half(a, b, hi16[8 * q + j], lo16[8 * q + j]);
-                            else
-                                hi16[8 * q + j] = half2_of(a, b);
-                        }
-                        if (iv < INFINITY) sum = fmaf(part, iv, sum);
+                        for (int j = 8; j < 64; j += 8) top[y] = fmaxf(fmaxf(top[y], x[j + y]), x[j + 4 + y]);
                     }
-                    tmem_st16(s_at + 32 * c, hi16);
-                    if constexpr (SPLIT) tmem_st16(s_at + 32 * c + 16, lo16);
+                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    // m follows where t has grown by more than SLACK; the first one is any
+                    const bool grows = mx == -INFINITY ? most > -INFINITY : most > LIFT + SLACK;
+                    if (__any_sync(0xffffffffu, grows)) {
+                        const float now = grows ? most + base : mx, keep = mx == now ? 1.f : exp2_of(mx - now);
+                        const float base_now = (now == -INFINITY ? 0.f : now) - LIFT, shift = base - base_now;
+                        mx = now, base = base_now;
+                        sum *= keep;
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) x[j] += shift;
+                        if (k > kf) {  // O of the units before
+                            ok = wait_o(n_s - 1);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int y = 0; y < D / 16; ++y) scale16(o_at + 16 * y, keep);
+                        }
+                        if (c > 0) scale_p<SPLIT>(s_at, keep);  // P of the unit's first positions
+                    }
+                    float part[4];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t hi16[16], lo16[SPLIT ? 16 : 1];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float v = exp2_of(x[32 * b + 16 * q + 2 * j]), w = exp2_of(x[32 * b + 16 * q + 2 * j + 1]);
+                                add2(s0, s1, v, w);
+                                if constexpr (SPLIT)
+                                    split_half(v, w, hi16[8 * q + j], lo16[8 * q + j]);
+                                else
+                                    hi16[8 * q + j] = half2_of(v, w);
+                            }
+                            part[2 * b + q] = s0 + s1;
+                        }
+                        tmem_st16(s_at + 64 * c + 16 * b, hi16);
+                        if constexpr (SPLIT) tmem_st16(s_at + 64 * c + 32 + 16 * b, lo16);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (iv[q] < INFINITY) sum = fmaf(part[q], iv[q], sum);
                 }
+                if (!ok) break;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -540,7 +650,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             }
             if (!ok) break;
             gk += (uint32_t)(p.k1 - p.k0);
-            // ---- the row's result, or its part
+            // ---- the row's result, or its part: through shared memory, where Q was, COLS columns of
+            // fp32 at a time, so that rows are written whole
+            constexpr int COLS = D == 64 ? 32 : 64;
+            static_assert(32 * COLS * 4 <= 32 * 2 * D, "the warp's rows of Q");
             const bool whole = p.whole();
             const int part = 2 * blockIdx.x + (p.k0 == 0 ? 1 : 0);
             if (kf < ke) {
@@ -549,30 +662,41 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 if (!ok) break;
                 tc_fence_after();
             }
-            const float inv = sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
+            const float inv = !whole ? 1.f : sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t u[32];
-                if (kf < ke) {
-                    tmem_ld32(o_at + 32 * c, u);
-                    tmem_ld_wait();
-                } else {
+            for (int c = 0; c < D / COLS; ++c) {
+                float* to = reinterpret_cast<float*>(mine) + lane * COLS;
+                float v[COLS / 16][16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) u[j] = 0;
-                }
-                if (row_ok) {
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            put_row4<TY>(A.a, A.vec_out, tok, head * D + 32 * c + j, __uint_as_float(u[j]) * inv,
-                                         __uint_as_float(u[j + 1]) * inv, __uint_as_float(u[j + 2]) * inv,
-                                         __uint_as_float(u[j + 3]) * inv);
+                for (int y = 0; y < COLS / 16; ++y) {
+                    if (kf < ke) {
+                        tmem_ld16(o_at + COLS * c + 16 * y, v[y]);
                     } else {
-                        uint4* to = reinterpret_cast<uint4*>(A.part_o + ((size_t)part * G_::ROWS + 128 * h + t) * D + 32 * c);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) to[j / 4] = make_uint4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+                        for (int j = 0; j < 16; ++j) v[y][j] = 0.f;
                     }
                 }
+                tmem_ld_wait();
+#pragma unroll
+                for (int y = 0; y < COLS / 16; ++y)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4*>(to + 4 * ((4 * y + j) ^ (lane & 7))) = make_float4(
+                            v[y][4 * j] * inv, v[y][4 * j + 1] * inv, v[y][4 * j + 2] * inv, v[y][4 * j + 3] * inv);
+                __syncwarp();
+#pragma unroll 4
+                for (int y = 0; y < COLS / 4; ++y) {  // 128 / COLS rows at a time
+                    const int row = y * (128 / COLS) + lane / (COLS / 4), q4 = lane % (COLS / 4), in = 128 * h + 32 * (warp & 3) + row;
+                    if (in >= J.rows) continue;
+                    const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(mine) + row * COLS +
+                                                                      4 * (q4 ^ (row & 7)));
+                    const int rr = J.mtile * G_::ROWS + in, ii = div_group(A, rr), col = COLS * c + 4 * q4;
+                    if (!whole)
+                        *reinterpret_cast<float4*>(A.part_o + ((size_t)part * G_::ROWS + in) * D + col) = v;
+                    else
+                        put_row4<TY>(A.a, A.vec_out, (size_t)J.row0 + ii, (p.head * G + rr - ii * G) * D + col, v.x, v.y, v.z, v.w);
+                }
+                __syncwarp();
             }
             tc_fence_before();  // O has been read before the next job's P is there
             if (row_ok) {
@@ -590,46 +714,58 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         if (!ok && lane == 0) give_up();
         if (threadIdx.x == 0) A.cuts[2 * blockIdx.x] = begun, A.cuts[2 * blockIdx.x + 1] = went_on;
     } else if (warp < G_::SOFT + 4) {
-        // ---------------- codes into operands
-        const int cw = warp - G_::SOFT;
+        if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        // ---------------- codes into operands: block ids are read two units ahead, codes and
+        // scales one
+        const int cw = warp - G_::SOFT, bs = 1 << A.a.shift;
         constexpr int L = G_::LOADS, PER = D / 64;  // loads; of 64 bytes a group of 8 tokens
+        constexpr uint32_t NOWHERE = 0xFFFFFFFFu;
+        struct Unit {
+            int at0, head, hi;
+            int id;       // lane l < KV / 16: the block of its tokens 16 l ...
+            uint32_t at;  // ... and where they are, in 16 tokens; NOWHERE
+            bool edge;    // some row does not see all of it: codes may be anything
+        };
         Piece p;
         bool more = pieces.next(p);
         int k = more ? p.k0 : 0;
-        uint4 kr[L], vr[L];
-        // of the unit that is loaded: lane l < KV / 16 has the block of 16 tokens l
-        int id = -1;
-        float ks = 0.f, vs = 0.f;
-        bool edge = false;
-        const auto look_up = [&]() {
+        const auto look_up = [&](Unit& u) {  // the next unit, if there is one
+            if (!more) return false;
             const TileJob& J = p.J;
-            const int at0 = (J.unit0 + k) * KV, at = at0 + 16 * lane;
-            id = -1;
-            if (lane < KV / 16 && at < J.hi && at + 16 > J.lo) {
-                id = A.a.table[(size_t)J.seq * A.a.max_blocks + (at >> A.a.shift)];
-                if (id >= 0 && id < A.a.n_blocks) {
-                    const size_t i = (size_t)id * A.a.Hkv + p.head;
-                    ks = A.a.ks[i], vs = A.a.vs[i];
-                } else {
-                    id = -1;
-                    set_status(A.a.st, E0_ST_BAD_BLOCK);
-                }
+            u.at0 = (J.unit0 + k) * KV, u.head = p.head, u.hi = J.hi;
+            u.edge = u.at0 < J.full_lo || u.at0 + KV > J.full_hi;
+            const int at = u.at0 + 16 * lane;
+            u.id = -1;
+            if (lane < KV / 16 && at < J.hi && at + 16 > J.lo) u.id = A.a.table[(size_t)J.seq * A.a.max_blocks + (at >> A.a.shift)];
+            else if (lane < KV / 16) u.id = INT_MIN;  // not looked up
+            if (++k == p.k1) {
+                more = pieces.next(p);
+                k = p.k0;
             }
-            edge = at0 < J.full_lo || at0 + KV > J.full_hi;
+            return true;
         };
-        const int bs = 1 << A.a.shift;
+        // the id's bounds, its scales
+        const auto look_in = [&](Unit& u, float& ks, float& vs) {
+            if (lane < KV / 16 && u.id != INT_MIN && (u.id < 0 || u.id >= A.a.n_blocks)) set_status(A.a.st, E0_ST_BAD_BLOCK);
+            ks = vs = 0.f;
+            u.at = NOWHERE;
+            if (lane < KV / 16 && u.id >= 0 && u.id < A.a.n_blocks) {
+                const size_t i = (size_t)u.id * A.a.Hkv + u.head;
+                ks = A.a.ks[i], vs = A.a.vs[i];
+                u.at = (uint32_t)(((i << A.a.shift) + ((u.at0 + 16 * lane) & (bs - 1))) >> 4);
+            }
+        };
         // load i: tokens 8 * group + lane % 8, 16 bytes of 64 of them
-        const auto load = [&](const uint8_t* from, uint4 (&to)[L]) {
-            const int at0 = (p.J.unit0 + k) * KV;
+        const uint32_t in_group = (lane & 7) * D + 16 * (lane >> 3);
+        const auto load = [&](const Unit& u, const uint8_t* from, uint4 (&to)[L]) {
+            const int left = u.hi - u.at0 - (lane & 7);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 const int n = 4 * i + cw, group = n / PER, part = n % PER;
-                const int token = 8 * group + (lane & 7), at = at0 + token;
-                const int b = __shfl_sync(0xffffffffu, id, group >> 1);
+                const uint32_t b = __shfl_sync(0xffffffffu, u.at, group >> 1);
                 to[i] = make_uint4(0, 0, 0, 0);
-                if (b >= 0 && at < p.J.hi)
-                    to[i] = __ldg(reinterpret_cast<const uint4*>(
-                        from + ((((size_t)b * A.a.Hkv + p.head) << A.a.shift) + (at & (bs - 1))) * D + 64 * part + 16 * (lane >> 3)));
+                if (b != NOWHERE && 8 * group < left)
+                    to[i] = __ldg(reinterpret_cast<const uint4*>(from + (size_t)b * (16 * D) + ((group & 1) * (8 * D) + part * 64 + in_group)));
             }
         };
         const auto store = [&](const uint4 (&from)[L], uint8_t* to, bool clean) {
@@ -644,111 +780,124 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 *reinterpret_cast<uint4*>(dst + 128) = b;
             }
         };
-        if (more) {
-            look_up();
-            load(A.a.k, kr);
-            load(A.a.v, vr);
+        Unit now, next, after;
+        uint4 kr[L], vr[L];
+        float ks, vs, ks1, vs1;
+        bool have = look_up(now), have1 = look_up(next), ok = true;
+        if (have) {
+            look_in(now, ks, vs);
+            load(now, A.a.k, kr);
+            load(now, A.a.v, vr);
         }
-        bool ok = true;
-        for (uint32_t g = 0; more; ++g) {
+        for (uint32_t g = 0; have; ++g) {
             const uint32_t st = g % STAGES, par = ((g / STAGES) + 1) & 1;
-            const bool clean = edge;
-            const float4 sc = id >= 0 ? make_float4(ks, log2f(fmaxf(vs, LEAST_SCALE)), SUM_UNIT / fmaxf(vs, LEAST_SCALE), 1.f)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (++k == p.k1) {
-                more = pieces.next(p);
-                k = p.k0;
-            }
-            if (more) look_up();
+            const bool have2 = look_up(after);
+            if (have1) look_in(next, ks1, vs1);
             ok = __all_sync(0xffffffffu, mbar_wait(&S.k_empty[st], par, abort, TILE_WAIT_NS));
             if (!ok) break;
             store(kr, S.k[st], false);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.k_full[st]);
-            if (more) load(A.a.k, kr);
+            if (have1) load(next, A.a.k, kr);
             ok = __all_sync(0xffffffffu, mbar_wait(&S.v_empty[st], par, abort, TILE_WAIT_NS));
             if (!ok) break;
-            if (cw == 0 && lane < KV / 16) S.sc[st][lane] = sc;
-            store(vr, S.v[st], clean);
+            if (cw == 0 && lane < KV / 16) {
+                const float v = fmaxf(vs, LEAST_SCALE);
+                S.sc[st][lane] = now.at != NOWHERE ? make_float4(ks, log2f(v), SUM_UNIT / v, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            store(vr, S.v[st], now.edge);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.v_full[st]);
-            if (more) load(A.a.v, vr);
+            if (have1) load(next, A.a.v, vr);
+            now = next, next = after, ks = ks1, vs = vs1;
+            have = have1, have1 = have2;
         }
         if (!ok && lane == 0) give_up();
     } else {
-        // ---------------- products
-        if (lane == 0) {
-            const uint32_t q_at = smem_u32(S.q);
+        // ---------------- products: the warp follows the schedule together, one lane issues
+        if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == G_::SOFT + 4) {
             const uint32_t id_s = idesc_f16_f32(128, KV), id_o = idesc_f16_f32(128, D) | B_MN_MAJOR;
-            uint32_t n_s[2] = {0, 0}, n_q[2] = {0, 0}, gk = 0;
+            // the operands' addresses, the low words of their descriptors: 16-byte units
+            const uint32_t q_lo = desc_low(smem_u32(S.q), 128), k_lo = desc_low(smem_u32(S.k), 128), v_lo = desc_low(smem_u32(S.v), 16 * D);
+            constexpr uint32_t QK_HI = desc_high(16 * D), V_HI = desc_high(128);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const bool leader = elect_one();
+            uint32_t n_s0 = 0, n_s1 = 0, n_q0 = 0, n_q1 = 0, gk = 0;
             bool ok = true, issued = false;
             Piece p;
-            // O of half h += P V of unit k (its number in the block: g)
-            const auto second = [&](int h, int k, uint32_t g, uint32_t n) {
-                const uint32_t st = g % STAGES, slot = HALVES == 2 ? h : n & 1, use = HALVES == 2 ? n : n >> 1;
-                if (!mbar_wait(&S.p_full[slot], use & 1, abort, TILE_WAIT_NS)) return false;
-                tc_fence_after();
-                const uint32_t v_at = smem_u32(S.v[st]), p_at = tmem + slot * KV, o_at = tmem + G_::O_COL + h * D;
+            // S of half h, its n-th = Q K^T of the unit in stage st
+            const auto first = [&](int h, uint32_t st, uint32_t n) {
+                const uint32_t slot = HALVES == 2 ? h : n & 1, d = tm + slot * KV;
+                const uint32_t a = q_lo + h * 16 * D, b = k_lo + st * (uint32_t)(G_::OPERAND >> 4);
+                if (leader) {
 #pragma unroll
-                for (int s = 0; s < KV / 16; ++s) {
-                    const uint64_t b = sdesc_plain(v_at + s * 32 * D, 16 * D, 128);
-                    const uint32_t a = p_at + 32 * (s / 2) + 8 * (s % 2);
-                    umma_f16_ta(o_at, a, b, id_o, k > p.first(h) || s > 0);
-                    if constexpr (SPLIT) umma_f16_ta(o_at, a + 16, b, id_o, 1);
+                    for (int s = 0; s < D / 16; ++s) umma_lo(d, a + 16 * s, QK_HI, b + 16 * s, QK_HI, id_s, s > 0);
+                    umma_commit(&S.s_full[slot]);
                 }
-                umma_commit(&S.o_done[slot]);
+            };
+            // O of half h += P V of the unit in stage st, the half's n-th; `more`: not the piece's first
+            const auto second = [&](int h, uint32_t st, uint32_t n, uint32_t more) {
+                const uint32_t slot = HALVES == 2 ? h : n & 1, use = HALVES == 2 ? n : n >> 1;
+                if (!__all_sync(0xffffffffu, mbar_wait(&S.p_full[slot], use & 1, abort, TILE_WAIT_NS))) return false;
+                tc_fence_after();
+                const uint32_t p_at = tm + slot * KV, d = tm + G_::O_COL + h * D, b = v_lo + st * (uint32_t)(G_::OPERAND >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int s = 0; s < KV / 16; ++s) {
+                        const uint32_t a = p_at + 64 * (s / 4) + 8 * (s % 4);
+                        umma_ta_lo(d, a, b + s * 2 * D, V_HI, id_o, s > 0 ? 1 : more);
+                        if constexpr (SPLIT) umma_ta_lo(d, a + 32, b + s * 2 * D, V_HI, id_o, 1);
+                    }
+                    umma_commit(&S.o_done[slot]);
+                }
                 return true;
             };
-            const auto wait_v = [&](uint32_t g) { return mbar_wait(&S.v_full[g % STAGES], (g / STAGES) & 1, abort, TILE_WAIT_NS); };
             while (ok && pieces.next(p)) {
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h)
-                    if (ok && p.first(h) < p.end(h)) ok = mbar_wait(&S.q_full[h], n_q[h]++ & 1, abort, TILE_WAIT_NS);
+                const int f0 = p.first(0), e0 = p.end(0), f1 = p.first(1), e1 = p.end(1), k0 = p.k0, k1 = p.k1;
+                if (f0 < e0) ok = mbar_wait(&S.q_full[0], n_q0++ & 1, abort, TILE_WAIT_NS);
+                if (HALVES == 2 && ok && f1 < e1) ok = mbar_wait(&S.q_full[1], n_q1++ & 1, abort, TILE_WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
                 // one turn more than units: a unit's second products come with the next one's first
-                for (int k = p.k0; ok && k <= p.k1; ++k) {
-                    const uint32_t g = gk + (uint32_t)(k - p.k0), st = g % STAGES;
-                    const bool now = k < p.k1, before = k > p.k0;
+#pragma unroll 1
+                for (int k = k0; ok && k <= k1; ++k) {
+                    const uint32_t g = gk + (uint32_t)(k - k0), st = g % STAGES, last = (g - 1) % STAGES;
+                    const bool now = k < k1, before = k > k0;
                     if (now) ok = mbar_wait(&S.k_full[st], (g / STAGES) & 1, abort, TILE_WAIT_NS);
-                    if (ok && before) ok = wait_v(g - 1);
+                    if (ok && before) ok = mbar_wait(&S.v_full[last], ((g - 1) / STAGES) & 1, abort, TILE_WAIT_NS);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const auto first = [&](int h) {
-                        const uint32_t slot = HALVES == 2 ? h : n_s[h] & 1;
-                        const uint32_t k_at = smem_u32(S.k[st]), qh = q_at + h * 128 * D * 2;
-#pragma unroll
-                        for (int s = 0; s < D / 16; ++s)
-                            umma_f16(tmem + slot * KV, sdesc_plain(qh + s * 256, 128, 16 * D),
-                                     sdesc_plain(k_at + s * 256, 128, 16 * D), id_s, s > 0);
-                        umma_commit(&S.s_full[slot]);
-                        ++n_s[h];
-                    };
-                    if constexpr (HALVES == 2) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (ok && before && p.has(h, k - 1)) ok = second(h, k - 1, g - 1, n_s[h] - 1);
-                            if (ok && now && p.has(h, k)) first(h);
-                        }
-                    } else {
-                        const uint32_t n = n_s[0];
-                        if (now && p.has(0, k)) first(0);
-                        if (before && p.has(0, k - 1)) ok = second(0, k - 1, g - 1, n - 1);
-                    }
                     issued = true;
+                    const bool now0 = now && k >= f0 && k < e0, before0 = before && k - 1 >= f0 && k - 1 < e0;
+                    if constexpr (HALVES == 2) {
+                        const bool now1 = now && k >= f1 && k < e1, before1 = before && k - 1 >= f1 && k - 1 < e1;
+                        if (before0) ok = second(0, last, n_s0 - 1, k - 1 > f0);
+                        if (ok && now0) first(0, st, n_s0++);
+                        if (ok && before1) ok = second(1, last, n_s1 - 1, k - 1 > f1);
+                        if (ok && now1) first(1, st, n_s1++);
+                    } else {
+                        const uint32_t n = n_s0;
+                        if (now0) first(0, st, n_s0++);
+                        if (before0) ok = second(0, last, n - 1, k - 1 > f0);
+                    }
                     if (!ok) break;
-                    if (now) umma_commit(&S.k_empty[st]);
-                    if (before) umma_commit(&S.v_empty[(g - 1) % STAGES]);
+                    if (leader) {
+                        if (now) umma_commit(&S.k_empty[st]);
+                        if (before) umma_commit(&S.v_empty[last]);
+                    }
                 }
-                gk += (uint32_t)(p.k1 - p.k0);
+                gk += (uint32_t)(k1 - k0);
             }
-            if (!ok) give_up();
+            if (!ok && leader) give_up();
             if (issued) {  // the products have ended before tensor memory is freed
-                umma_commit(&S.drained);
+                if (leader) umma_commit(&S.drained);
                 mbar_wait(&S.drained, 0, &never, TILE_WAIT_NS);
             }
+            __syncwarp();
         }
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -859,6 +1008,9 @@ inline TileArgs tile_args(const AttnArgs& a, int dtype, void* ws) {
     TileArgs t = {};
     t.a = a;
     t.a.unit = a.D == 256 ? 64 : 128;
+    const int G = a.Hq / a.Hkv;
+    while ((1 << t.by_shift) < G) ++t.by_shift;
+    t.by_group = (uint32_t)(((1ull << (31 + t.by_shift)) + G - 1) / G);
     t.blocks = tile_blocks();
     t.most_jobs = (int)tile_jobs(a.B, a.max_q, a.Hq / a.Hkv, a.D);
     const size_t rows = a.D == 256 ? 128 : 256, slots = 2 * (size_t)t.blocks;
