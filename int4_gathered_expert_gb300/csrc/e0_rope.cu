@@ -69,14 +69,54 @@ struct Raw {
     uint4 v[N];  // 8 elements
 };
 
+// (a0, a1) * (b0, b1) + (c0, c1) and (a0, a1) * (b0, b1), a pair an instruction.
+E0_DEV void fma_pair(float& r0, float& r1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+E0_DEV void mul_pair(float& r0, float& r1, float a0, float a1, float b0, float b1) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+template <int TY>
+E0_DEV void to_fp32(const Raw<TY>& r, float (&v)[8]) {
+    if constexpr (TY == E0_F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(r.v[i].x), v[4 * i + 1] = __uint_as_float(r.v[i].y);
+            v[4 * i + 2] = __uint_as_float(r.v[i].z), v[4 * i + 3] = __uint_as_float(r.v[i].w);
+        }
+    } else {
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack16<TY>(w[i]);
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// A head's result is P x + Q x', x' the other element of the pair, with P = w cos and Q = -+ w' sin
+// (w' the other's weight): found once for the queries' heads and once for the keys', so that
+// a head is a sum of squares and three products a pair of elements.
 // VEC: D and twice the pairs that turn are multiples of 16 and every row starts on a 16-byte
-// boundary; otherwise elements come one by one.
-template <int TY, bool VEC>
-__global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
+// boundary; otherwise elements come one by one.  ADJACENT: pairs are neighbours.
+//
+// Measured (device time, GB300): 16384 rows of 36 heads of 128 bf16, three axes, norms (302 MB):
+// 64.9 us, 4.7 TB/s, 69 % of the measured copy rate, bound by instructions beside it; 87.7 with every lane
+// finding its sines, weights and rotation in turn and one value an instruction.  8 rows of 18
+// heads of 256: 3.5 us, a launch and two loads behind one another.
+template <int TY, bool VEC, bool ADJACENT>
+__global__ void __launch_bounds__(ROPE_WARPS * 32, VEC && TY != E0_F32 ? 3 : 2) k_qk_rope(RopeArgs A) {
     typedef typename Elem<TY>::T T;
     __shared__ unsigned long long turn[MOST_PAIRS];
     __shared__ uint8_t axis[MOST_PAIRS];
-    const int lane = threadIdx.x & 31;
+    __shared__ float2 turned[ROPE_WARPS][MOST_PAIRS];  // a warp's token: cosines and sines
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < A.half; i += ROPE_WARPS * 32) {
         // 1 / 2 pi in two parts, the first of 29 bits: its product with 24 is exact
         const double f = A.freq[i], t = f * 0.15915494272485375, rest = f * 3.6704158172530464e-10;
@@ -84,7 +124,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
         axis[i] = A.axis ? (uint8_t)min((int)A.axis[i], A.axes - 1) : (uint8_t)0;
     }
     __syncthreads();
-    const long long w = (long long)blockIdx.x * ROPE_WARPS + (threadIdx.x >> 5);
+    const long long w = (long long)blockIdx.x * ROPE_WARPS + warp;
     const int t = (int)(w / A.per_token);
     if (t >= A.T) return;
     if (A.pos[t] < 0) return;  // no token: the row stays as it is
@@ -92,23 +132,8 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
     const int first = (int)(w % A.per_token) * slots + lane / A.lanes, step = A.per_token * slots;
     const bool live = item < items;
     const Place at = place_of(A, item);
-    float cs[8], sn[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int p = 8 * item + i;
-        cs[i] = 1.f, sn[i] = 0.f;
-        if (p < A.half) {
-            const long long pos = A.pos[(size_t)axis[p] * A.pos_ld + t];
-            const unsigned long long a = (unsigned long long)pos * turn[p];
-            // the nearest turn taken off: -1/2 .. 1/2 of a turn, as half turns
-            sincospif((float)(int)(a >> 32) * 4.6566128730773926e-10f, &sn[i], &cs[i]);
-        }
-    }
     const T* x = reinterpret_cast<const T*>(A.x) + (size_t)t * A.x_ld;
     T* y = reinterpret_cast<T*>(A.y) + (size_t)t * A.y_ld;
-    bool bad = false;
-    float wt[16];
-    int have = 0;  // whose weights wt holds: 1 the queries', 2 the keys'
     const auto load = [&](int h, Raw<TY> (&r)[2]) {
         if constexpr (VEC) {
             if (h < A.heads && live) {
@@ -121,35 +146,50 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
     };
     Raw<TY> now[2], next[2];
     load(first, now);
+    // every angle once a warp
+    for (int p = lane; p < A.half; p += 32) {
+        const long long pos = A.pos[(size_t)axis[p] * A.pos_ld + t];
+        const unsigned long long a = (unsigned long long)pos * turn[p];
+        // the nearest turn taken off: -1/2 .. 1/2 of a turn, as half turns
+        float sn, cs;
+        sincospif((float)(int)(a >> 32) * 4.6566128730773926e-10f, &sn, &cs);
+        turned[warp][p] = make_float2(cs, sn);
+    }
+    __syncwarp();
+    float P[2][8], Q[2][8];
+    const auto factors = [&](const float* wp) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // the places of a lane's i-th elements, and of their pairs
+            float wa = 1.f, wb = 1.f;
+            int ea, eb;
+            pair_of(A, 8 * item + i, ea, eb);
+            const bool in = 8 * item + i < A.D / 2;
+            if (wp && in) wa = __ldg(wp + ea), wb = __ldg(wp + eb);
+            const float2 f = 8 * item + i < A.half ? turned[warp][8 * item + i] : make_float2(1.f, 0.f);
+            const float pa = wa * f.x, qa = -wb * f.y, pb = wb * f.x, qb = wa * f.y;
+            if (VEC && (ADJACENT || !at.turns)) {  // neighbours: pair i of 8 is elements 2i, 2i + 1 of 16
+                P[i / 4][2 * (i & 3)] = pa, Q[i / 4][2 * (i & 3)] = qa;
+                P[i / 4][2 * (i & 3) + 1] = pb, Q[i / 4][2 * (i & 3) + 1] = qb;
+            } else {
+                P[0][i] = pa, Q[0][i] = qa, P[1][i] = pb, Q[1][i] = qb;
+            }
+        }
+    };
+    bool bad = false;
+    int have = -1;  // whose factors these are: 0 the queries', 1 the keys'
     for (int h0 = 0; h0 < A.heads; h0 += step) {  // all lanes of a warp take every turn
         const int h = h0 + first;
         const bool mine = h < A.heads && live;
         load(h + step, next);
-        float a[8], b[8];  // pair i is (a[i], b[i])
+        const int kind = h < A.Hq ? 0 : 1;
+        if (mine && have != kind) {
+            factors(!A.norm ? nullptr : kind ? A.wk : A.wq);
+            have = kind;
+        }
+        float a[8], b[8];
         if constexpr (VEC) {
-            float u[8], v[8];
-            if constexpr (TY == E0_F32) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 p = now[0].v[i / 4], q = now[1].v[i / 4];
-                    u[i] = __uint_as_float(i % 4 == 0 ? p.x : i % 4 == 1 ? p.y : i % 4 == 2 ? p.z : p.w);
-                    v[i] = __uint_as_float(i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 p = now[0].v[0], q = now[1].v[0];
-                    const float2 f = unpack16<TY>(i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w);
-                    const float2 g = unpack16<TY>(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
-                    u[2 * i] = f.x, u[2 * i + 1] = f.y, v[2 * i] = g.x, v[2 * i + 1] = g.y;
-                }
-            }
-            const bool side = A.adjacent || !at.turns;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] = side ? (i < 4 ? u[2 * i] : v[2 * (i & 3)]) : u[i];
-                b[i] = side ? (i < 4 ? u[2 * i + 1] : v[2 * (i & 3) + 1]) : v[i];
-            }
+            to_fp32<TY>(now[0], a), to_fp32<TY>(now[1], b);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -161,57 +201,55 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
             }
         }
         if (A.norm) {
-            float ss = 0.f;
-            if (mine) {
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+            for (int i = 0; i < 8; i += 2) {
+                fma_pair(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
+                fma_pair(s0, s1, b[i], b[i + 1], b[i], b[i + 1], s0, s1);
             }
+            float ss = mine ? s0 + s1 : 0.f;
             for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float rstd = rsqrtf(fmaf(ss, A.inv_d, A.eps));
             bad |= mine && !(ss < INFINITY);
-            const float* wp = h < A.Hq ? A.wq : A.wk;
-            const int kind = h < A.Hq ? 1 : 2;
-            if (wp && mine && have != kind) {
-                have = kind;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    int ea, eb;
-                    pair_of(A, 8 * item + i, ea, eb);
-                    const bool in = 8 * item + i < A.D / 2;
-                    wt[i] = in ? __ldg(wp + ea) : 0.f;
-                    wt[8 + i] = in ? __ldg(wp + eb) : 0.f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] *= rstd, b[i] *= rstd;
-                if (wp) a[i] *= wt[i], b[i] *= wt[8 + i];
+            for (int i = 0; i < 8; i += 2) {
+                mul_pair(a[i], a[i + 1], a[i], a[i + 1], rstd, rstd);
+                mul_pair(b[i], b[i + 1], b[i], b[i + 1], rstd, rstd);
             }
         }
+        float u[8], v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = a[i], q = b[i];
-            a[i] = fmaf(p, cs[i], -q * sn[i]);
-            b[i] = fmaf(q, cs[i], p * sn[i]);
+        for (int i = 0; i < 8; i += 2) {
+            // a pair that does not turn has Q = 0, which must not meet an infinity of its partner
+            const bool turns = !VEC || at.turns;
+            float c0, c1, d0, d1;  // the partners
+            if (VEC && ADJACENT) {
+                c0 = a[i + 1], c1 = a[i], d0 = b[i + 1], d1 = b[i];
+            } else {
+                c0 = b[i], c1 = b[i + 1], d0 = a[i], d1 = a[i + 1];
+            }
+            if (turns) {
+                mul_pair(c0, c1, c0, c1, Q[0][i], Q[0][i + 1]);
+                mul_pair(d0, d1, d0, d1, Q[1][i], Q[1][i + 1]);
+            } else {
+                c0 = c1 = d0 = d1 = 0.f;
+            }
+            fma_pair(u[i], u[i + 1], a[i], a[i + 1], P[0][i], P[0][i + 1], c0, c1);
+            fma_pair(v[i], v[i + 1], b[i], b[i + 1], P[1][i], P[1][i + 1], d0, d1);
         }
         if (mine) {
             T* to = y + (size_t)h * A.D;
             if constexpr (VEC) {
-                float u[8], v[8];
-                const bool side = A.adjacent || !at.turns;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u[2 * i] = side ? a[i] : a[2 * i], u[2 * i + 1] = side ? b[i] : a[2 * i + 1];
-                    v[2 * i] = side ? a[4 + i] : b[2 * i], v[2 * i + 1] = side ? b[4 + i] : b[2 * i + 1];
-                }
                 store_vec<TY>(to + at.e0, u);
                 store_vec<TY>(to + at.e1, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     int ea, eb;
-                    pair_of(A, 8 * item + i, ea, eb);
-                    if (8 * item + i < A.D / 2) to[ea] = Elem<TY>::put(a[i]), to[eb] = Elem<TY>::put(b[i]);
+                    const int p = 8 * item + i;
+                    pair_of(A, p, ea, eb);
+                    if (p < A.half) to[ea] = Elem<TY>::put(u[i]), to[eb] = Elem<TY>::put(v[i]);
+                    else if (p < A.D / 2) to[ea] = Elem<TY>::put(a[i] * P[0][i]), to[eb] = Elem<TY>::put(b[i] * P[1][i]);
                 }
             }
         }
@@ -223,10 +261,11 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) k_qk_rope(RopeArgs A) {
 template <int TY>
 int launch(const RopeArgs& a, bool vec, cudaStream_t s) {
     const long long blocks = ((long long)a.T * a.per_token + ROPE_WARPS - 1) / ROPE_WARPS;
+    const auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, ROPE_WARPS * 32, 0, s>>>(a); };
     if (vec)
-        k_qk_rope<TY, true><<<(unsigned)blocks, ROPE_WARPS * 32, 0, s>>>(a);
+        a.adjacent ? go(k_qk_rope<TY, true, true>) : go(k_qk_rope<TY, true, false>);
     else
-        k_qk_rope<TY, false><<<(unsigned)blocks, ROPE_WARPS * 32, 0, s>>>(a);
+        a.adjacent ? go(k_qk_rope<TY, false, true>) : go(k_qk_rope<TY, false, false>);
     return cudaGetLastError() == cudaSuccess ? E0_OK : E0_ERR_CUDA;
 }
 

@@ -195,8 +195,9 @@ def row_ref(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     return who[at], math.log(w[at] / cum[-1]), n, near
 
 
-# weights are off by 2^-29 of themselves, sums as much: cuts and draws nearer than that to a border may go either way
-NEAR = 2.0 ** -28
+# weights are off by 2^-28 of themselves at most, so a running sum and the total that it is compared with by as much of
+# themselves, 2^-27 of the total together: cuts and draws nearer than that to a border may go either way
+NEAR = 2.0 ** -27
 
 
 def check_draw(L, x, u, dtype, **rules):  # noqa: F811
