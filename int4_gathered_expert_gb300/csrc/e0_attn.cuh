@@ -47,8 +47,21 @@ struct AttnArgs {
 
 // e0_attn_tile.cu: the same for many query rows of fp16 or bf16 (the workspace's size for at most
 // max_q queries of B sequences, G heads each).
+// prefix: `a` is of tokens that the rows of several sequences share (B is 1, max_q their most rows,
+// a.at = at, written here); `own` those sequences.  merge: o and lse are their own results, and the rows'
+// ends are written; otherwise a.raw gets the prefix' results.
+struct TilePrefix {
+    AttnArgs own;
+    int32_t* at;
+    const float* o;
+    const float* lse;
+    bool merge;
+};
 size_t attn_tile_ws_bytes(int B, int max_q, int G, int D);
-int attn_tile(const AttnArgs& a, int dtype, void* ws, cudaStream_t s);
+// Whether a prefix can be merged: no window, and no more jobs than blocks, so that a block has
+// one end of a job and one beginning at most.
+bool attn_tile_merges(const AttnArgs& a);
+int attn_tile(const AttnArgs& a, const TilePrefix* prefix, int dtype, void* ws, cudaStream_t s);
 
 namespace {
 
@@ -310,6 +323,17 @@ constexpr float LEAST_SCALE = 7.8886090522101181e-31f;  // 2^-100, the least tha
 constexpr float LIFT = 7.f, SLACK = 8.f;                // weights are 2^(t - m + LIFT), t at most m + SLACK
 constexpr float REST = 4096.f;                          // what the rests of the weights go in times
 constexpr float SUM_LIFT = -12.f, SUM_UNIT = 1.f / 4096.f;  // sums are times 2^SUM_LIFT
+
+// Two normed results with the lses x and y as one: their factors, its lse.
+struct Two {
+    float f1, f2, lse;
+};
+E0_DEV Two two_of(float x, float y) {
+    const float m = x != x || y != y ? __uint_as_float(0x7FC00000u) : fmaxf(x, y), base = m == -INFINITY ? 0.f : m;
+    const float u = exp2_of((x - base) * LOG2E), v = exp2_of((y - base) * LOG2E), sum = u + v;
+    if (!(sum > 0.f || sum != sum)) return {0.f, 0.f, -INFINITY};
+    return {u / sum, v / sum, base + log2f(sum) * LN2};
+}
 
 // ln of the softmax's sum from the running maximum and sum.
 E0_DEV float lse_of(float m, float l) {

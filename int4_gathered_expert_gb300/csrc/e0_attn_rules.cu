@@ -50,14 +50,11 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) k_shared_merge(AttnArgs a, c
     const Seq s = seq_of<true>(a, blockIdx.x, false);
     for (int item = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5); item < s.n * a.Hq; item += gridDim.y * MERGE_WARPS) {
         const size_t tok = (size_t)s.row0 + item / a.Hq, at = tok * a.Hq + item % a.Hq;
-        const float x = l1[at], y = l2[at];
-        const float m = x != x || y != y ? __uint_as_float(0x7FC00000u) : fmaxf(x, y), base = m == -INFINITY ? 0.f : m;
-        const float u = exp2_of((x - base) * LOG2E), v = exp2_of((y - base) * LOG2E), sum = u + v;
-        const float f1 = sum > 0.f || sum != sum ? u / sum : 0.f, f2 = sum > 0.f || sum != sum ? v / sum : 0.f;
+        const Two two = two_of(l1[at], l2[at]);
         T* to = reinterpret_cast<T*>(a.out) + tok * a.out_ld + (size_t)(item % a.Hq) * a.D;
         for (int d = lane; d < a.D; d += 32)
-            to[d] = Elem<TY>::put(fmaf(f1, o1[at * a.D + d], f2 * o2[at * a.D + d]));
-        if (a.lse && lane == 0) a.lse[at] = base + log2f(sum) * LN2;
+            to[d] = Elem<TY>::put(fmaf(two.f1, o1[at * a.D + d], two.f2 * o2[at * a.D + d]));
+        if (a.lse && lane == 0) a.lse[at] = two.lse;
     }
 }
 
@@ -77,14 +74,14 @@ int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
                 void* out, int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
     AttnArgs a = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, lse, ws, st);
     put_rules(a, rules);
-    if (by_tiles(dtype, (int64_t)max_q * (Hq / c->Hkv))) return attn_tile(a, dtype, ws, s);
+    if (by_tiles(dtype, (int64_t)max_q * (Hq / c->Hkv))) return attn_tile(a, nullptr, dtype, ws, s);
     return launch_t<true>(a, dtype, c->D, s);
 }
 
 size_t attn_shared_ws_bytes(int B, int T, int Hq, int Hkv, int D, int max_q) {
-    const size_t own = attn_ws_bytes(D), tiles = attn_tile_ws_bytes(1, T, Hq / Hkv, D);
-    const size_t both = by_tiles(E0_F16, (int64_t)T * (Hq / Hkv)) && tiles > own ? tiles : own;
-    return up256((size_t)T * sizeof(int32_t)) + 256 + 2 * parts_bytes(T, Hq, D) + both;
+    // the tiles' schedule is made while the sequences' own attention runs: a place for each
+    const size_t tiles = by_tiles(E0_F16, (int64_t)T * (Hq / Hkv)) ? attn_tile_ws_bytes(1, T, Hq / Hkv, D) : 0;
+    return up256((size_t)T * sizeof(int32_t)) + 256 + 2 * parts_bytes(T, Hq, D) + up256(attn_ws_bytes(D)) + tiles;
 }
 
 int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_blocks, const int32_t* prefix_len,
@@ -105,20 +102,32 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
         o[i] = reinterpret_cast<float*>(take((size_t)T * Hq * c->D * sizeof(float)));
         l[i] = reinterpret_cast<float*>(take((size_t)T * Hq * sizeof(float)));
     }
+    char* tiles = p + up256(attn_ws_bytes(c->D));
     AttnArgs mine = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, l[1], p, st);
     put_rules(mine, rules);
     mine.raw = o[1], mine.limit = T;
     mine.unit = 64;  // any: the kernels set their own
-    k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, prefix_len, at, cu2);
-    if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
     // the prefix, as one sequence whose queries are all rows
     AttnArgs front = args_of(c, prefix_table, prefix_blocks, prefix_len, cu2, 1, T, q, q_ld, Hq, scale, 0, out, out_ld, l[0], p, st);
     put_rules(front, rules);
-    front.raw = o[0], front.limit = T, front.at = at;
-    int rc = by_tiles(dtype, (int64_t)T * (Hq / c->Hkv)) ? attn_tile(front, dtype, p, s) : launch_t<true>(front, dtype, c->D, s);
+    front.limit = T, front.at = at;
+    // what the sequences have of their own comes first: the prefix' last kernel adds it where it can
+    int rc = launch_t<true>(mine, dtype, c->D, s);
     if (rc != E0_OK) return rc;
-    // what the sequences have of their own
-    rc = launch_t<true>(mine, dtype, c->D, s);
+    if (by_tiles(dtype, (int64_t)T * (Hq / c->Hkv))) {
+        const TilePrefix prefix = {mine, at, o[1], l[1], attn_tile_merges(front)};
+        if (prefix.merge) {
+            front.lse = lse;
+            return attn_tile(front, &prefix, dtype, tiles, s);
+        }
+        front.raw = o[0];
+        rc = attn_tile(front, &prefix, dtype, tiles, s);
+    } else {
+        k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, prefix_len, at, cu2);
+        if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
+        front.raw = o[0];
+        rc = launch_t<true>(front, dtype, c->D, s);
+    }
     if (rc != E0_OK) return rc;
     mine.lse = lse;
     const long long items = (long long)max_q * Hq;

@@ -61,6 +61,13 @@ struct TileHead {
 
 struct TileArgs {
     AttnArgs a;               // parts and cuts unused
+    // A prefix (own.B > 0): `own` are the sequences whose rows are the one job's; their positions
+    // behind the prefix go to own_at, -1 where a row is no sequence's.
+    AttnArgs own;
+    int32_t* own_at;
+    const float* own_o;       // merge: the sequences' own results, normed, and their lse
+    const float* own_lse;
+    bool merge;               // every piece of a job is a part; the join ends the rows with the own results
     float* part_o;            // [2 * blocks][ROWS][D]
     float2* part_ml;          // [2 * blocks][ROWS]
     TileCut* cuts;            // [blocks][2]
@@ -77,7 +84,7 @@ E0_DEV int div_group(const TileArgs& A, int n) { return (int)((unsigned long lon
 
 // The range of positions that a token of a sequence sees.
 E0_DEV void range_of(const TileArgs& A, int seq, int row0, int p0, int ctx, int i, int& p, int& lo, int& hi) {
-    p = A.a.at ? A.a.at[row0 + i] : p0 + i;
+    p = !A.a.at ? p0 + i : A.a.window > 0 || A.a.slopes ? A.a.at[row0 + i] : 0;  // needed there alone
     hi = A.a.at ? ctx : p + 1;
     if (A.a.open) hi = max(hi, A.a.open[seq]);
     hi = min(hi, ctx);
@@ -88,15 +95,19 @@ E0_DEV void range_of(const TileArgs& A, int seq, int row0, int p0, int ctx, int 
 // ---------------------------------------------------------------- the schedule
 
 constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_SHARED = 6144;  // jobs whose places are kept in shared memory
 
+// One block: with four sequences and 512 jobs 6 us beside the launch, chains of loads.
 template <int D>
 __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
     typedef Geo<D> G_;
-    extern __shared__ uint32_t tiles_before[];  // [B + 1]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ uint32_t tiles_before[];  // [B + 1], then the jobs' units and places
     __shared__ uint32_t red[32];
     __shared__ uint32_t carry;
+    __shared__ int all_rows;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = A.a.B, G = A.a.Hq / A.a.Hkv;
+    uint32_t* place = tiles_before + B + 1;
     const auto block_scan = [&](uint32_t v, uint32_t& all) {  // exclusive
         const uint32_t own = v;
 #pragma unroll
@@ -107,20 +118,44 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
         __syncthreads();
         if (lane == 31) red[warp] = v;
         __syncthreads();
-        uint32_t before = 0;
-        all = 0;
-        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-            if (w < warp) before = add_units(before, red[w]);
-            all = add_units(all, red[w]);
+        uint32_t w = red[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w = add_units(w, t);
         }
+        all = __shfl_sync(0xffffffffu, w, 31);
+        const uint32_t before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
         return add_units(before, v - own);
+    };
+    if (tid == 0) all_rows = 0, carry = 0;
+    if (A.own.B > 0) {
+        for (int t = tid; t < A.own.limit; t += PLAN_THREADS) A.own_at[t] = -1;
+        __syncthreads();
+        const int before = max(*A.a.ctx, 0);
+        for (int b = warp; b < A.own.B; b += PLAN_THREADS / 32) {
+            const Seq s = seq_of<true>(A.own, b, false);
+            for (int i = lane; i < s.n; i += 32) A.own_at[s.row0 + i] = before + s.ctx - s.n + i;
+            if (lane == 0 && s.n > 0) atomicMax(&all_rows, s.row0 + s.n);
+        }
+        __syncthreads();
+    }
+    const auto sequence = [&](int b, bool tell) {
+        if (A.own.B == 0) return seq_of<true>(A.a, b, tell);
+        Seq s;
+        s.row0 = 0, s.n = all_rows, s.ctx = *A.a.ctx;
+        if (s.ctx < 0 || (long long)s.ctx > ((long long)A.a.max_blocks << A.a.shift)) {
+            if (tell && tid == 0) set_status(A.a.st, E0_ST_BAD_LENGTH);
+            s.ctx = 0;
+        }
+        return s;
     };
     // tiles of query rows of each sequence
     uint32_t at = 0;
     for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
         const int b = b0 + tid;
         uint32_t n = 0, all;
-        if (b < B) n = (uint32_t)(((long long)seq_of<true>(A.a, b, true).n * G + G_::ROWS - 1) / G_::ROWS);
+        if (b < B) n = (uint32_t)(((long long)sequence(b, true).n * G + G_::ROWS - 1) / G_::ROWS);
         const uint32_t before = block_scan(n, all);
         if (b < B) tiles_before[b] = at + before;
         at = add_units(at, all);
@@ -136,7 +171,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
             if (tiles_before[mid] <= (uint32_t)j) b = mid; else end = mid;
         }
         while (tiles_before[b + 1] <= (uint32_t)j) ++b;  // sequences without rows share a place
-        const Seq s = seq_of<true>(A.a, b, false);
+        const Seq s = sequence(b, false);
         TileJob J;
         J.seq = b, J.mtile = j - (int)tiles_before[b], J.row0 = s.row0, J.p0 = s.ctx - s.n;
         const int r0 = J.mtile * G_::ROWS;
@@ -149,7 +184,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
             const int ra = r0 + 128 * h, rb = r0 + min(J.rows, 128 * (h + 1));
             if (h >= G_::HALVES || ra >= rb) continue;
             int lo = INT_MAX, hi = 0, most = 0, least = INT_MAX;
-            for (int i = ra / G + lane; i <= (rb - 1) / G; i += 32) {
+            for (int i = div_group(A, ra) + lane; i <= div_group(A, rb - 1); i += 32) {
                 int p, l, e;
                 range_of(A, b, s.row0, J.p0, s.ctx, i, p, l, e);
                 if (l < e) lo = min(lo, l), hi = max(hi, e);
@@ -169,21 +204,26 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
             if (J.k1[h] > 0) J.k0[h] -= u0, J.k1[h] -= u0;
         J.unit0 = u0, J.units = max(u1 - u0, 1);  // a job without context still writes its rows
         J.start = 0;
-        if (lane == 0) A.jobs[j] = J;
+        if (lane == 0) {
+            A.jobs[j] = J;
+            if (j < PLAN_SHARED) place[2 * j] = J.units;
+        }
     }
     __syncthreads();
     // their places in the schedule
-    if (tid == 0) carry = 0;
-    __syncthreads();
     for (int j0 = 0; j0 < jobs; j0 += PLAN_THREADS) {
         const int j = j0 + tid;
         uint32_t n = 0, all;
         if (j < jobs) {
-            const unsigned long long u = (unsigned long long)A.jobs[j].units * A.a.Hkv;
+            const unsigned long long u = (unsigned long long)(j < PLAN_SHARED ? (int)place[2 * j] : A.jobs[j].units) * A.a.Hkv;
             n = u < MOST_UNITS ? (uint32_t)u : MOST_UNITS;
         }
         const uint32_t before = block_scan(n, all);
-        if (j < jobs) A.jobs[j].start = add_units(carry, before);
+        if (j < jobs) {
+            const uint32_t start = add_units(carry, before);
+            A.jobs[j].start = start;
+            if (j < PLAN_SHARED) place[2 * j + 1] = start;
+        }
         __syncthreads();
         if (tid == 0) carry = add_units(carry, all);
         __syncthreads();
@@ -199,16 +239,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
         const uint32_t u = c * share;
         int4 to = make_int4(-1, 0, 0, 0);
         if (u < total) {
+            const auto start = [&](int j) { return j < PLAN_SHARED ? place[2 * j + 1] : A.jobs[j].start; };
             int lo = 0, hi = jobs;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (A.jobs[mid].start <= u) lo = mid; else hi = mid;
+                if (start(mid) <= u) lo = mid; else hi = mid;
             }
-            const uint32_t rel = u - A.jobs[lo].start;
-            to = make_int4(lo, (int)(rel / A.jobs[lo].units), (int)(rel % A.jobs[lo].units), 0);
+            const uint32_t rel = u - start(lo), units = lo < PLAN_SHARED ? place[2 * lo] : A.jobs[lo].units;
+            to = make_int4(lo, (int)(rel / units), (int)(rel % units), 0);
         }
         A.begin[c] = to;
     }
+    // what went before may still be running: the kernels after this one wait for it through here
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- a block's pieces of jobs
@@ -219,7 +262,7 @@ struct Piece {
     // the units of the piece that half h has (no index that is not a constant: J stays in registers)
     E0_DEV int first(int h) const { return max(k0, h ? J.k0[1] : J.k0[0]); }
     E0_DEV int end(int h) const { return min(k1, h ? J.k1[1] : J.k1[0]); }
-    E0_DEV bool whole() const { return k0 == 0 && k1 == J.units; }
+    E0_DEV bool all() const { return k0 == 0 && k1 == J.units; }
 };
 
 struct Pieces {
@@ -654,7 +697,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             // fp32 at a time, so that rows are written whole
             constexpr int COLS = D == 64 ? 32 : 64;
             static_assert(32 * COLS * 4 <= 32 * 2 * D, "the warp's rows of Q");
-            const bool whole = p.whole();
+            const bool whole = p.all() && !A.merge;
             const int part = 2 * blockIdx.x + (p.k0 == 0 ? 1 : 0);
             if (kf < ke) {
                 ok = wait_o(n_s - 1);
@@ -910,7 +953,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
 // ---------------------------------------------------------------- jobs that several blocks have
 
 constexpr int TILE_JOIN_THREADS = 256;
-constexpr int TILE_JOIN_ROWS = 16;
+template <int D>
+constexpr int TILE_JOIN_ROWS = TILE_JOIN_THREADS / (D / 4);  // four columns a thread
 
 template <int D, int TY>
 __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
@@ -918,46 +962,55 @@ __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
     const TileCut cut = A.cuts[2 * blockIdx.x];
     if (cut.parts == 0) return;
-    const TileJob J = A.jobs[cut.job];
-    const int G = A.a.Hq / A.a.Hkv, d4 = threadIdx.x % (D / 4) * 4;
-    const auto slot_of = [&](int r, int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * G_::ROWS + r; };
-    const int r0 = blockIdx.y * TILE_JOIN_ROWS, r1 = min(J.rows, r0 + TILE_JOIN_ROWS);
-    for (int r = r0 + threadIdx.x / (D / 4); r < r1; r += TILE_JOIN_THREADS / (D / 4)) {
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int BATCH = 4;
-        for (int i0 = 0; i0 < cut.parts; i0 += BATCH) {
-            float2 ml[BATCH];
-            float4 x[BATCH];
+    const int4* from = reinterpret_cast<const int4*>(A.jobs + cut.job);
+    const int mtile = from[0].y, row0 = from[3].y, rows = from[3].z;
+    const int G = A.a.Hq / A.a.Hkv, d4 = threadIdx.x % (D / 4) * 4, r = blockIdx.y * TILE_JOIN_ROWS<D> + threadIdx.x / (D / 4);
+    if (r >= rows) return;
+    const int row = mtile * G_::ROWS + r, i_tok = div_group(A, row), head = cut.head * G + row - i_tok * G;
+    const size_t tok = (size_t)row0 + i_tok, at = tok * A.a.Hq + head;
+    if (A.merge && A.own_at[tok] == -1) return;  // no sequence's row
+    const auto slot_of = [&](int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * G_::ROWS + r; };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int BATCH = 8;
+    for (int i0 = 0; i0 < cut.parts; i0 += BATCH) {
+        float2 ml[BATCH];
+        float4 x[BATCH];
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                ml[i] = make_float2(-INFINITY, 0.f);
-                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i0 + i < cut.parts) {
-                    ml[i] = A.part_ml[slot_of(r, i0 + i)];
-                    x[i] = *reinterpret_cast<const float4*>(A.part_o + slot_of(r, i0 + i) * D + d4);
-                }
-            }
-            float top = m;
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) top = fmaxf(top, ml[i].x);
-            const float base = top == -INFINITY ? 0.f : top, keep = exp2_of(m - base);
-            m = top;
-            l *= keep;
-            o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const float w = exp2_of(ml[i].x - base);
-                l += w * ml[i].y;
-                o.x += w * x[i].x, o.y += w * x[i].y, o.z += w * x[i].z, o.w += w * x[i].w;
+        for (int i = 0; i < BATCH; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + i < cut.parts) {
+                ml[i] = A.part_ml[slot_of(i0 + i)];
+                x[i] = *reinterpret_cast<const float4*>(A.part_o + slot_of(i0 + i) * D + d4);
             }
         }
-        const float inv = l > 0.f || l != l ? SUM_UNIT / l : 0.f;
-        const int row = J.mtile * G_::ROWS + r, head = cut.head * G + row % G;
-        const size_t tok = (size_t)J.row0 + row / G;
-        put_row4<TY>(A.a, A.vec_out, tok, head * D + d4, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (A.a.lse && d4 == 0) A.a.lse[tok * A.a.Hq + head] = lse_of(m, l);
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) top = fmaxf(top, ml[i].x);
+        const float base = top == -INFINITY ? 0.f : top, keep = exp2_of(m - base);
+        m = top;
+        l *= keep;
+        o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float w = exp2_of(ml[i].x - base);
+            l += w * ml[i].y;
+            o.x += w * x[i].x, o.y += w * x[i].y, o.z += w * x[i].z, o.w += w * x[i].w;
+        }
     }
+    const float inv = l > 0.f || l != l ? SUM_UNIT / l : 0.f;
+    float lse = lse_of(m, l);
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    if (A.merge) {
+        const float4 x = *reinterpret_cast<const float4*>(A.own_o + at * D + d4);
+        const Two two = two_of(lse, A.own_lse[at]);
+        o.x = fmaf(two.f1, o.x, two.f2 * x.x), o.y = fmaf(two.f1, o.y, two.f2 * x.y);
+        o.z = fmaf(two.f1, o.z, two.f2 * x.z), o.w = fmaf(two.f1, o.w, two.f2 * x.w);
+        lse = two.lse;
+    }
+    put_row4<TY>(A.a, A.vec_out, tok, head * D + d4, o.x, o.y, o.z, o.w);
+    if (A.a.lse && d4 == 0) A.a.lse[at] = lse;
 }
 
 // ---------------------------------------------------------------- host
@@ -977,20 +1030,29 @@ template <int D, int TY, bool RULES>
 int tile_launch(const TileArgs& t, cudaStream_t s) {
     static std::atomic<uint64_t> asked{0};
     if (!allow_smem((const void*)k_attn_tile<D, TY, RULES>, sizeof(TileSmem<D>), asked)) return E0_ERR_CUDA;
-    k_tile_plan<D><<<1, PLAN_THREADS, (size_t)(t.a.B + 1) * sizeof(uint32_t), s>>>(t);
-    if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    // The schedule beside the kernel before it where that one is this library's own results, which
+    // nothing here writes over; otherwise after all that went before.
+    cfg.numAttrs = t.merge ? 1 : 0;
     cfg.stream = s;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(PLAN_THREADS);
+    const int kept = t.most_jobs < PLAN_SHARED ? t.most_jobs : PLAN_SHARED;
+    cfg.dynamicSmemBytes = (size_t)(t.a.B + 1 + 2 * kept) * sizeof(uint32_t);
+    static std::atomic<uint64_t> asked_plan{0};
+    if (!allow_smem((const void*)k_tile_plan<D>, (size_t)(E0_MAX_SEQS + 1 + 2 * PLAN_SHARED) * sizeof(uint32_t), asked_plan))
+        return E0_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k_tile_plan<D>, t) != cudaSuccess) return E0_ERR_CUDA;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3(t.blocks);
     cfg.blockDim = dim3(Geo<D>::THREADS);
     cfg.dynamicSmemBytes = sizeof(TileSmem<D>);
     if (cudaLaunchKernelEx(&cfg, k_attn_tile<D, TY, RULES>, t) != cudaSuccess) return E0_ERR_CUDA;
-    cfg.gridDim = dim3(t.blocks, Geo<D>::ROWS / TILE_JOIN_ROWS);
+    cfg.gridDim = dim3(t.blocks, Geo<D>::ROWS / TILE_JOIN_ROWS<D>);
     cfg.blockDim = dim3(TILE_JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_tile_join<D, TY>, t) == cudaSuccess ? E0_OK : E0_ERR_CUDA;
@@ -1004,9 +1066,13 @@ int tile_launch_d(const TileArgs& t, int dtype, cudaStream_t s) {
 }
 
 // The arguments of the kernels above; `ws` of tile_ws_bytes.
-inline TileArgs tile_args(const AttnArgs& a, int dtype, void* ws) {
+inline TileArgs tile_args(const AttnArgs& a, const TilePrefix* prefix, int dtype, void* ws) {
     TileArgs t = {};
     t.a = a;
+    if (prefix) {
+        t.own = prefix->own, t.own_at = prefix->at, t.own_o = prefix->o, t.own_lse = prefix->lse, t.merge = prefix->merge;
+        t.own.unit = 64;  // any
+    }
     t.a.unit = a.D == 256 ? 64 : 128;
     const int G = a.Hq / a.Hkv;
     while ((1 << t.by_shift) < G) ++t.by_shift;
