@@ -77,7 +77,7 @@ struct TileArgs {
     int blocks, most_jobs;
     uint32_t by_group;        // n / G = n * by_group >> 31 + by_shift for n below 2^31
     int by_shift;
-    bool vec_out;
+    bool vec_out, out_16;     // rows of out start on 8 bytes, on 16
 };
 
 E0_DEV int div_group(const TileArgs& A, int n) { return (int)((unsigned long long)(uint32_t)n * A.by_group >> (31 + A.by_shift)); }
@@ -265,23 +265,34 @@ struct Piece {
     E0_DEV bool all() const { return k0 == 0 && k1 == J.units; }
 };
 
+// The first jobs of a block's are in shared memory from the start.
+constexpr int AT_HAND = 32;
+
 struct Pieces {
     const TileArgs& A;
+    const TileJob* near;
+    int near0;
     uint32_t left;
     int job, head, k;
-    E0_DEV Pieces(const TileArgs& args) : A(args), left(0), job(-1), head(0), k(0) {
+    E0_DEV Pieces(const TileArgs& args, const TileJob* at_hand) : A(args), near(at_hand), near0(0), left(0), job(-1), head(0), k(0) {
         const TileHead h = *A.head;
         const uint32_t u = blockIdx.x * h.share;
         if (u < h.total) {
             const int4 b = A.begin[blockIdx.x];
-            job = b.x, head = b.y, k = b.z;
+            job = near0 = b.x, head = b.y, k = b.z;
             left = min(h.share, h.total - u);
         }
     }
     E0_DEV bool next(Piece& p) {
         if (left == 0) return false;
-        const int4* from = reinterpret_cast<const int4*>(A.jobs + job);
-        const int4 a = __ldcg(from), b = __ldcg(from + 1), c = __ldcg(from + 2), d = __ldcg(from + 3);
+        int4 a, b, c, d;
+        if (job - near0 < AT_HAND) {
+            const int4* from = reinterpret_cast<const int4*>(near + (job - near0));
+            a = from[0], b = from[1], c = from[2], d = from[3];
+        } else {
+            const int4* from = reinterpret_cast<const int4*>(A.jobs + job);
+            a = __ldcg(from), b = __ldcg(from + 1), c = __ldcg(from + 2), d = __ldcg(from + 3);
+        }
         p.J = {a.x, a.y, a.z, a.w, {b.x, b.y}, {b.z, b.w}, c.x, c.y, c.z, c.w, (uint32_t)d.x, d.y, d.z, d.w};
         p.job = job, p.head = head, p.k0 = k;
         p.k1 = min(p.J.units, k + (int)left);
@@ -347,6 +358,7 @@ struct TileSmem {
     uint8_t q[Geo<D>::Q_BYTES];
     uint8_t k[Geo<D>::STAGES][Geo<D>::OPERAND];
     uint8_t v[Geo<D>::STAGES][Geo<D>::OPERAND];
+    TileJob jobs[AT_HAND];
     float4 sc[Geo<D>::STAGES][Geo<D>::KV / 16];  // of 16 tokens: keys' scale, values' log2 and inverse, seen (1) or not
     uint64_t k_full[Geo<D>::STAGES], k_empty[Geo<D>::STAGES], v_full[Geo<D>::STAGES], v_empty[Geo<D>::STAGES];
     uint64_t s_full[2], p_full[2], o_done[2], q_full[2], drained;
@@ -419,6 +431,12 @@ E0_DEV void scale_p(uint32_t at, float keep) {
     }
 }
 
+// Where element `col` (a multiple of four) of a part's row is.
+template <int D>
+E0_DEV size_t part_at(int slot, int row, int col) {
+    return (size_t)slot * Geo<D>::ROWS * D + (size_t)(row / 8) * (8 * D) + col * 8 + (row & 7) * 4;
+}
+
 template <int TY>
 E0_DEV void put_row4(const AttnArgs& a, bool vec, size_t tok, int col, float x, float y, float z, float w) {
     if (a.raw) {
@@ -473,7 +491,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
     };
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the schedule is there
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    Pieces pieces(A);
+    {
+        const int job0 = A.begin[blockIdx.x].x, i = threadIdx.x;  // -1: the block has nothing to do
+        if (i < AT_HAND * 4 && job0 >= 0 && job0 + i / 4 < A.head->jobs)
+            reinterpret_cast<int4*>(S.jobs)[i] = __ldcg(reinterpret_cast<const int4*>(A.jobs + job0) + i);
+        __syncthreads();
+    }
+    Pieces pieces(A, S.jobs);
 
     // 512 threads are launched with 128 registers each; a softmax thread wants more, the others
     // less: 256 x 168 + 128 x 112 + 128 x 64 = 512 x 128.  (384 threads have 168 each.)
@@ -705,39 +729,69 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 if (!ok) break;
                 tc_fence_after();
             }
-            const float inv = !whole ? 1.f : sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
+            const auto load_o = [&](int col, uint32_t (&u)[32]) {
+                if (kf < ke) {
+                    tmem_ld32(o_at + col, u);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) u[j] = 0;
+                }
+            };
+            if (!whole || A.a.raw) {
+                // fp32: a part's columns stand by fours, eight rows of each together (part_at), so that a warp
+                // writes whole lines
+                const float inv = !whole ? 1.f : sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
+                float* to = !whole ? A.part_o + part_at<D>(part, 128 * h + t, 0) : A.a.raw + (tok * A.a.Hq + head) * D;
+                const int step = !whole ? 32 : 4;
 #pragma unroll 1
-            for (int c = 0; c < D / COLS; ++c) {
-                float* to = reinterpret_cast<float*>(mine) + lane * COLS;
-                float v[COLS / 16][16];
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t u[32];
+                    load_o(32 * c, u);
+                    if (row_ok)
 #pragma unroll
-                for (int y = 0; y < COLS / 16; ++y) {
-                    if (kf < ke) {
-                        tmem_ld16(o_at + COLS * c + 16 * y, v[y]);
-                    } else {
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4*>(to + (8 * c + j) * step) =
+                                make_float4(__uint_as_float(u[4 * j]) * inv, __uint_as_float(u[4 * j + 1]) * inv,
+                                            __uint_as_float(u[4 * j + 2]) * inv, __uint_as_float(u[4 * j + 3]) * inv);
+                }
+            } else {
+                // through shared memory, where the warp's rows of Q were, so that rows are written whole
+                constexpr int CHUNKS = D / 8;  // of 16 bytes, lanes of a row
+                const float inv = sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t u[32];
+                    load_o(32 * c, u);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[y][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = pack16<TY>(__uint_as_float(u[8 * j + 2 * z]) * inv, __uint_as_float(u[8 * j + 2 * z + 1]) * inv);
+                        *reinterpret_cast<uint4*>(mine + lane * (2 * D) + (((4 * c + j) ^ (lane & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                tmem_ld_wait();
-#pragma unroll
-                for (int y = 0; y < COLS / 16; ++y)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4*>(to + 4 * ((4 * y + j) ^ (lane & 7))) = make_float4(
-                            v[y][4 * j] * inv, v[y][4 * j + 1] * inv, v[y][4 * j + 2] * inv, v[y][4 * j + 3] * inv);
                 __syncwarp();
+                const int c = lane % CHUNKS;
 #pragma unroll 4
-                for (int y = 0; y < COLS / 4; ++y) {  // 128 / COLS rows at a time
-                    const int row = y * (128 / COLS) + lane / (COLS / 4), q4 = lane % (COLS / 4), in = 128 * h + 32 * (warp & 3) + row;
+                for (int y = 0; y < CHUNKS; ++y) {
+                    const int row = y * (32 / CHUNKS) + lane / CHUNKS, in = 128 * h + 32 * (warp & 3) + row;
+                    const uint4 v = *reinterpret_cast<const uint4*>(mine + row * (2 * D) + ((c ^ (row & 7)) << 4));
+                    const int rr = J.mtile * G_::ROWS + in, ii = div_group(A, rr);
+                    T* to = reinterpret_cast<T*>(A.a.out) + ((size_t)J.row0 + ii) * A.a.out_ld + (p.head * G + rr - ii * G) * D + 8 * c;
                     if (in >= J.rows) continue;
-                    const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(mine) + row * COLS +
-                                                                      4 * (q4 ^ (row & 7)));
-                    const int rr = J.mtile * G_::ROWS + in, ii = div_group(A, rr), col = COLS * c + 4 * q4;
-                    if (!whole)
-                        *reinterpret_cast<float4*>(A.part_o + ((size_t)part * G_::ROWS + in) * D + col) = v;
-                    else
-                        put_row4<TY>(A.a, A.vec_out, (size_t)J.row0 + ii, (p.head * G + rr - ii * G) * D + col, v.x, v.y, v.z, v.w);
+                    if (A.out_16) {
+                        *reinterpret_cast<uint4*>(to) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            to[2 * z] = reinterpret_cast<const T*>(&w[z])[0];
+                            to[2 * z + 1] = reinterpret_cast<const T*>(&w[z])[1];
+                        }
+                    }
                 }
                 __syncwarp();
             }
@@ -871,6 +925,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             uint32_t n_s0 = 0, n_s1 = 0, n_q0 = 0, n_q1 = 0, gk = 0;
             bool ok = true, issued = false;
             Piece p;
+            const auto q_there = [&](int h, uint32_t n) {
+                const bool there = __all_sync(0xffffffffu, mbar_wait(&S.q_full[h], n & 1, abort, TILE_WAIT_NS));
+                tc_fence_after();
+                return there;
+            };
             // S of half h, its n-th = Q K^T of the unit in stage st
             const auto first = [&](int h, uint32_t st, uint32_t n) {
                 const uint32_t slot = HALVES == 2 ? h : n & 1, d = tm + slot * KV;
@@ -900,9 +959,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             };
             while (ok && pieces.next(p)) {
                 const int f0 = p.first(0), e0 = p.end(0), f1 = p.first(1), e1 = p.end(1), k0 = p.k0, k1 = p.k1;
-                if (f0 < e0) ok = mbar_wait(&S.q_full[0], n_q0++ & 1, abort, TILE_WAIT_NS);
-                if (HALVES == 2 && ok && f1 < e1) ok = mbar_wait(&S.q_full[1], n_q1++ & 1, abort, TILE_WAIT_NS);
-                ok = __all_sync(0xffffffffu, ok);
                 // one turn more than units: a unit's second products come with the next one's first
 #pragma unroll 1
                 for (int k = k0; ok && k <= k1; ++k) {
@@ -918,13 +974,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                     if constexpr (HALVES == 2) {
                         const bool now1 = now && k >= f1 && k < e1, before1 = before && k - 1 >= f1 && k - 1 < e1;
                         if (before0) ok = second(0, last, n_s0 - 1, k - 1 > f0);
+                        if (ok && now0 && k == f0) ok = q_there(0, n_q0++);  // a half's Q is waited for where it is wanted
                         if (ok && now0) first(0, st, n_s0++);
                         if (ok && before1) ok = second(1, last, n_s1 - 1, k - 1 > f1);
+                        if (ok && now1 && k == f1) ok = q_there(1, n_q1++);
                         if (ok && now1) first(1, st, n_s1++);
                     } else {
                         const uint32_t n = n_s0;
-                        if (now0) first(0, st, n_s0++);
-                        if (before0) ok = second(0, last, n - 1, k - 1 > f0);
+                        if (now0 && k == f0) ok = q_there(0, n_q0++);
+                        if (ok && now0) first(0, st, n_s0++);
+                        if (ok && before0) ok = second(0, last, n - 1, k - 1 > f0);
                     }
                     if (!ok) break;
                     if (leader) {
@@ -954,7 +1013,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
 
 constexpr int TILE_JOIN_THREADS = 256;
 template <int D>
-constexpr int TILE_JOIN_ROWS = TILE_JOIN_THREADS / (D / 4);  // four columns a thread
+constexpr int TILE_JOIN_ROWS = TILE_JOIN_THREADS / (D / 4);  // of a block, as many as four columns a thread make
 
 template <int D, int TY>
 __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
@@ -964,12 +1023,15 @@ __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
     if (cut.parts == 0) return;
     const int4* from = reinterpret_cast<const int4*>(A.jobs + cut.job);
     const int mtile = from[0].y, row0 = from[3].y, rows = from[3].z;
-    const int G = A.a.Hq / A.a.Hkv, d4 = threadIdx.x % (D / 4) * 4, r = blockIdx.y * TILE_JOIN_ROWS<D> + threadIdx.x / (D / 4);
+    // a warp: eight rows, 16 columns; a thread: four
+    constexpr int WIDE = D / 16;  // warps of eight rows
+    const int lane = threadIdx.x & 31, warp = (blockIdx.y * TILE_JOIN_THREADS + threadIdx.x) >> 5;
+    const int G = A.a.Hq / A.a.Hkv, d4 = 16 * (warp % WIDE) + 4 * (lane >> 3), r = 8 * (warp / WIDE) + (lane & 7);
     if (r >= rows) return;
     const int row = mtile * G_::ROWS + r, i_tok = div_group(A, row), head = cut.head * G + row - i_tok * G;
     const size_t tok = (size_t)row0 + i_tok, at = tok * A.a.Hq + head;
     if (A.merge && A.own_at[tok] == -1) return;  // no sequence's row
-    const auto slot_of = [&](int i) { return ((size_t)2 * (cut.block + i) + (i == 0)) * G_::ROWS + r; };
+    const auto slot_of = [&](int i) { return 2 * (cut.block + i) + (i == 0); };
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int BATCH = 8;
@@ -981,8 +1043,8 @@ __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
             ml[i] = make_float2(-INFINITY, 0.f);
             x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i0 + i < cut.parts) {
-                ml[i] = A.part_ml[slot_of(i0 + i)];
-                x[i] = *reinterpret_cast<const float4*>(A.part_o + slot_of(i0 + i) * D + d4);
+                ml[i] = A.part_ml[(size_t)slot_of(i0 + i) * G_::ROWS + r];
+                x[i] = *reinterpret_cast<const float4*>(A.part_o + part_at<D>(slot_of(i0 + i), r, d4));
             }
         }
         float top = m;
@@ -1092,6 +1154,7 @@ inline TileArgs tile_args(const AttnArgs& a, const TilePrefix* prefix, int dtype
     t.jobs = reinterpret_cast<TileJob*>(take((size_t)t.most_jobs * sizeof(TileJob)));
     t.begin = reinterpret_cast<int4*>(take(t.blocks * sizeof(int4)));
     t.head = reinterpret_cast<TileHead*>(take(sizeof(TileHead)));
+    t.out_16 = !((uintptr_t)a.out & 15) && (a.out_ld * type_size(dtype)) % 16 == 0;
     t.vec_out = a.raw || (!((uintptr_t)a.out & 7) && (a.out_ld * type_size(dtype)) % 8 == 0);
     return t;
 }
