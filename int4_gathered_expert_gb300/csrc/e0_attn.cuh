@@ -336,8 +336,8 @@ E0_DEV Two two_of(float x, float y) {
 }
 
 // ln of the softmax's sum from the running maximum and sum.
-E0_DEV float lse_of(float m, float l) {
-    return l > 0.f || l != l ? (m - (LIFT + SUM_LIFT) + log2f(l)) * LN2 : -INFINITY;
+E0_DEV float lse_of(float m, float l, float lift = LIFT) {
+    return l > 0.f || l != l ? (m - (lift + SUM_LIFT) + log2f(l)) * LN2 : -INFINITY;
 }
 
 template <int D>

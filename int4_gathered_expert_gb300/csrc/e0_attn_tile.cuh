@@ -38,9 +38,20 @@ struct Geo {
     static constexpr int SOFT = 4 * HALVES;  // softmax warps
     static constexpr int THREADS = (SOFT + 4 + 4) * 32;  // and the converting ones; of the last four, one issues the products
     static constexpr int O_COL = 2 * KV;  // tensor memory: two S, then the halves' O
-    static constexpr int Q_BYTES = ROWS * D * 2;
+    static constexpr int Q_BYTES = 128 * D * 2;             // of a half
+    static constexpr int Q_BUFS = D == 256 ? 1 : 3;         // halves' Q in shared memory
+    static constexpr int Q_WARPS = 3;                       // that bring it there
     static constexpr int LOADS = KV * D / (4 * 512);  // 16-byte loads of a converting lane for one operand
 };
+// Weights are 2^(t - m + TILE_LIFT) and m follows where t has grown by more than TILE_SLACK, so
+// that fp16's 2^15 is not passed: the rows of a warp seldom need O scaled after their first
+// scores, and every such time holds up both halves.  m's own weight is 2^3; what fp16 has no
+// steps for is 2^-28 of that.
+constexpr float TILE_LIFT = 3.f, TILE_SLACK = 12.f;
+// What a job costs beside its units (its rows of Q, its result, two halves that start and
+// stop), in units: 8 to 10 thousand cycles of four to five.  Dealt out by units alone the blocks with
+// the first rows of prompts, a unit a job, were twice as long as the others.
+constexpr uint32_t TILE_JOB_COST = 2;
 constexpr uint32_t TILE_TMEM = 512;
 constexpr uint64_t TILE_WAIT_NS = 2000000000ull;  // 2 s
 
@@ -215,7 +226,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
         const int j = j0 + tid;
         uint32_t n = 0, all;
         if (j < jobs) {
-            const unsigned long long u = (unsigned long long)(j < PLAN_SHARED ? (int)place[2 * j] : A.jobs[j].units) * A.a.Hkv;
+            const unsigned long long u = (unsigned long long)((j < PLAN_SHARED ? (int)place[2 * j] : A.jobs[j].units) + TILE_JOB_COST) * A.a.Hkv;
             n = u < MOST_UNITS ? (uint32_t)u : MOST_UNITS;
         }
         const uint32_t before = block_scan(n, all);
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
         if (tid == 0) set_status(A.a.st, E0_ST_BAD_LENGTH);
         total = 0;
     }
-    const uint32_t share = max((total + A.blocks - 1) / A.blocks, 1u);
+    const uint32_t share = max((total + A.blocks - 1) / A.blocks, TILE_JOB_COST + 1);
     if (tid == 0) *A.head = {total, share, jobs, 0};
     for (int c = tid; c < A.blocks; c += PLAN_THREADS) {
         const uint32_t u = c * share;
@@ -245,8 +256,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
                 const int mid = (lo + hi) >> 1;
                 if (start(mid) <= u) lo = mid; else hi = mid;
             }
-            const uint32_t rel = u - start(lo), units = lo < PLAN_SHARED ? place[2 * lo] : A.jobs[lo].units;
-            to = make_int4(lo, (int)(rel / units), (int)(rel % units), 0);
+            const uint32_t rel = u - start(lo), len = (lo < PLAN_SHARED ? place[2 * lo] : A.jobs[lo].units) + TILE_JOB_COST;
+            to = make_int4(lo, (int)(rel / len), (int)(rel % len), 0);
         }
         A.begin[c] = to;
     }
@@ -266,7 +277,7 @@ struct Piece {
 };
 
 // The first jobs of a block's are in shared memory from the start.
-constexpr int AT_HAND = 32;
+constexpr int AT_HAND = 12;
 
 struct Pieces {
     const TileArgs& A;
@@ -284,22 +295,27 @@ struct Pieces {
         }
     }
     E0_DEV bool next(Piece& p) {
-        if (left == 0) return false;
-        int4 a, b, c, d;
-        if (job - near0 < AT_HAND) {
-            const int4* from = reinterpret_cast<const int4*>(near + (job - near0));
-            a = from[0], b = from[1], c = from[2], d = from[3];
-        } else {
-            const int4* from = reinterpret_cast<const int4*>(A.jobs + job);
-            a = __ldcg(from), b = __ldcg(from + 1), c = __ldcg(from + 2), d = __ldcg(from + 3);
+        while (left > 0) {
+            int4 a, b, c, d;
+            if (job - near0 < AT_HAND) {
+                const int4* from = reinterpret_cast<const int4*>(near + (job - near0));
+                a = from[0], b = from[1], c = from[2], d = from[3];
+            } else {
+                const int4* from = reinterpret_cast<const int4*>(A.jobs + job);
+                a = __ldcg(from), b = __ldcg(from + 1), c = __ldcg(from + 2), d = __ldcg(from + 3);
+            }
+            p.J = {a.x, a.y, a.z, a.w, {b.x, b.y}, {b.z, b.w}, c.x, c.y, c.z, c.w, (uint32_t)d.x, d.y, d.z, d.w};
+            p.job = job, p.head = head;
+            // places k .. of the job: its cost, then its units
+            const int places = min(p.J.units + (int)TILE_JOB_COST - k, (int)left);
+            p.k0 = max(k - (int)TILE_JOB_COST, 0);
+            p.k1 = k + places - (int)TILE_JOB_COST;
+            left -= places;
+            k = 0;
+            if (++head == A.a.Hkv) head = 0, ++job;
+            if (p.k1 > p.k0) return true;  // otherwise a part of its cost: the units are the next block's
         }
-        p.J = {a.x, a.y, a.z, a.w, {b.x, b.y}, {b.z, b.w}, c.x, c.y, c.z, c.w, (uint32_t)d.x, d.y, d.z, d.w};
-        p.job = job, p.head = head, p.k0 = k;
-        p.k1 = min(p.J.units, k + (int)left);
-        left -= p.k1 - p.k0;
-        k = 0;
-        if (++head == A.a.Hkv) head = 0, ++job;
-        return true;
+        return false;
     }
 };
 static_assert(sizeof(TileJob) == 64, "four 16-byte loads");
@@ -355,15 +371,19 @@ E0_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
 
 template <int D>
 struct TileSmem {
-    uint8_t q[Geo<D>::Q_BYTES];
+    uint8_t q[Geo<D>::Q_BUFS][Geo<D>::Q_BYTES];
     uint8_t k[Geo<D>::STAGES][Geo<D>::OPERAND];
     uint8_t v[Geo<D>::STAGES][Geo<D>::OPERAND];
     TileJob jobs[AT_HAND];
     float4 sc[Geo<D>::STAGES][Geo<D>::KV / 16];  // of 16 tokens: keys' scale, values' log2 and inverse, seen (1) or not
     uint64_t k_full[Geo<D>::STAGES], k_empty[Geo<D>::STAGES], v_full[Geo<D>::STAGES], v_empty[Geo<D>::STAGES];
-    uint64_t s_full[2], p_full[2], o_done[2], q_full[2], drained;
+    float qf[Geo<D>::Q_BUFS][128];               // of a row of Q: what its scores want
+    uint64_t q_full[Geo<D>::Q_BUFS], q_empty[Geo<D>::Q_BUFS];
+    uint64_t s_full[2], p_full[2][2], o_half[2], o_done[2], drained;
     uint32_t tmem, abort;
 };
+
+static_assert(sizeof(TileSmem<64>) <= 232448 && sizeof(TileSmem<128>) <= 232448 && sizeof(TileSmem<256>) <= 232448, "227 KB");
 
 // 16 codes as 16 fp16: two 16-byte chunks.
 E0_DEV void widen16(const uint4 c, uint4& a, uint4& b) {
@@ -393,42 +413,14 @@ E0_DEV float inverse_of(float x) {  // a step of fp32 off
 // Bits 0 .. n-1, n any number.
 E0_DEV uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
 
-// 16 columns of fp32 in tensor memory times `keep` of the row.
-E0_DEV void scale16(uint32_t at, float keep) {
-    float v[16];
-    uint32_t u[16];
-    tmem_ld16(at, v);
+// 32 columns of fp32 in tensor memory times `keep` of the row.
+E0_DEV void scale32(uint32_t at, float keep) {
+    uint32_t u[32];
+    tmem_ld32(at, u);
     tmem_ld_wait();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * keep);
-    tmem_st16(at, u);
-}
-// 64 positions' weights in tensor memory, fp16 pairs (and 32 columns on their rests), times
-// `keep`.
-template <bool SPLIT>
-E0_DEV void scale_p(uint32_t at, float keep) {
-    tmem_st_wait();  // they have just been written
-#pragma unroll 1
-    for (int c = 0; c < 32; c += 16) {
-        float hi[16], lo[16];
-        uint32_t a[16], b[16];
-        tmem_ld16(at + c, hi);
-        if constexpr (SPLIT) tmem_ld16(at + 32 + c, lo);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            float2 x = unpack16<E0_F16>(__float_as_uint(hi[j]));
-            if constexpr (SPLIT) {
-                const float2 y = unpack16<E0_F16>(__float_as_uint(lo[j]));
-                x.x += y.x, x.y += y.y;
-                split_half(x.x * keep, x.y * keep, a[j], b[j]);
-            } else {
-                a[j] = half2_of(x.x * keep, x.y * keep);
-            }
-        }
-        tmem_st16(at + c, a);
-        if constexpr (SPLIT) tmem_st16(at + 32 + c, b);
-    }
+    for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * keep);
+    tmem_st32(at, u);
 }
 
 // Where element `col` (a multiple of four) of a part's row is.
@@ -452,6 +444,22 @@ E0_DEV void put_row4(const AttnArgs& a, bool vec, size_t tok, int col, float x, 
     }
 }
 
+// Wait for a barrier's phase, 2 s at most or until *abort.  The barrier's own test sleeps until the
+// phase ends or a while has passed; no sleep of a given length, which would go on after
+// the phase's end, and the clock only now and then: of 36 million instructions 17 had been waiting.
+E0_DEV bool arrived(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > TILE_WAIT_NS) return false;
+    }
+}
+
 // ---------------------------------------------------------------- the kernel
 
 // TY: E0_F16 or E0_BF16.  RULES: scores are capped or lose with the distance.
@@ -460,7 +468,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
     typedef Geo<D> G_;
     typedef typename Elem<TY>::T T;
     constexpr bool SPLIT = TY == E0_F16;
-    constexpr int KV = G_::KV, STAGES = G_::STAGES, HALVES = G_::HALVES;
+    constexpr int KV = G_::KV, STAGES = G_::STAGES, HALVES = G_::HALVES, CHUNKS = KV / 64;
     extern __shared__ __align__(1024) char tile_sm[];
     TileSmem<D>& S = *reinterpret_cast<TileSmem<D>*>(tile_sm);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = A.a.Hq / A.a.Hkv;
@@ -474,8 +482,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&S.s_full[s], 1), mbar_init(&S.o_done[s], 1);
-            mbar_init(&S.p_full[s], 4), mbar_init(&S.q_full[s], 4);
+            mbar_init(&S.p_full[s][0], 4), mbar_init(&S.p_full[s][1], 4), mbar_init(&S.o_half[s], 1);
         }
+        for (int s = 0; s < G_::Q_BUFS; ++s) mbar_init(&S.q_full[s], G_::Q_WARPS), mbar_init(&S.q_empty[s], 4);
         mbar_init(&S.drained, 1);
         S.abort = 0;
         mbar_fence_init();
@@ -507,16 +516,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         const int h = warp >> 2, t = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_at = tmem + lanes + G_::O_COL + h * D;
-        uint8_t* mine = S.q + (size_t)(128 * h + 32 * (warp & 3)) * (2 * D);  // the warp's 32 rows of Q; its outputs on their way
         uint32_t n_s = 0;  // S of this half so far
         uint32_t gk = 0;   // units of the block before this piece
+        uint32_t n_q = 0;  // halves with units before this piece
         bool ok = true;
         // The second products of this half's n-th S are done.  (A warp may be two units ahead of
         // another's P with one half: a barrier for even and one for odd units, so that a phase
         // is never mistaken for the one before the last.)
         const auto wait_o = [&](uint32_t n) {
-            return HALVES == 2 ? mbar_wait(&S.o_done[h], n & 1, abort, TILE_WAIT_NS)
-                               : mbar_wait(&S.o_done[n & 1], (n >> 1) & 1, abort, TILE_WAIT_NS);
+            return HALVES == 2 ? arrived(&S.o_done[h], n & 1, abort)
+                               : arrived(&S.o_done[n & 1], (n >> 1) & 1, abort);
         };
         Piece p;
         TileCut begun = {0, 0, 0, 0}, went_on = {0, 0, 0, 0};
@@ -530,70 +539,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             int pos = 0, lo = 0, hi = 0;
             if (row_ok) range_of(A, J.seq, J.row0, J.p0, J.hi, i, pos, lo, hi);
             float mx = -INFINITY, sum = 0.f, f = 0.f, slope = 0.f;
+            // the number of this half's Q, of all that the block has had
+            const uint32_t nq = n_q + (h && p.first(0) < p.end(0)), qb = nq % G_::Q_BUFS;
+            n_q += (p.first(0) < p.end(0)) + (HALVES == 2 && p.first(1) < p.end(1));
             if (kf < ke) {
-                // ---- the warp's rows into shared memory, 8 at a time: a lane has 16 bytes of every 64
-                // of row lane % 8
-                constexpr int C = D / 32, GB = D == 256 ? 2 : 4;
-#pragma unroll 1
-                for (int g0 = 0; g0 < 4; g0 += GB) {
-                    uint4 u[GB][C];
-#pragma unroll
-                    for (int y = 0; y < GB; ++y) {
-                        const int row = 128 * h + 32 * (warp & 3) + 8 * (g0 + y) + (lane & 7), rr = J.mtile * G_::ROWS + row;
-                        const int ii = div_group(A, rr);
-                        const bool have = row < J.rows;
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            reinterpret_cast<const T*>(A.a.q) +
-                            (have ? ((size_t)J.row0 + ii) * A.a.q_ld + (size_t)(p.head * G + rr - ii * G) * D : 0));
-#pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            u[y][c] = make_uint4(0, 0, 0, 0);
-                            if (have) u[y][c] = __ldg(src + 4 * c + (lane >> 3));
-                        }
-                    }
-#pragma unroll
-                    for (int y = 0; y < GB; ++y) {
-                        uint32_t m = 0;
-#pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            const uint32_t w[4] = {u[y][c].x, u[y][c].y, u[y][c].z, u[y][c].w};
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) m = __vmaxu2(m, w[z] & 0x7FFF7FFFu);
-                        }
-                        m = max(m & 0xFFFFu, m >> 16);
-                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        float fr;
-                        if constexpr (TY == E0_F16) {
-                            fr = m >= 0x7C00u ? __uint_as_float(0x7FC00000u) : A.a.scale * LOG2E;
-                        } else {  // times a power of two that brings the largest near 1
-                            const uint32_t b = m << 16;
-                            int e = (int)(b >> 23);
-                            e = e < 27 ? 27 : e > 253 ? 253 : e;
-                            const float down = b == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
-                            fr = b >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                                                  : __uint_as_float((uint32_t)e << 23) * A.a.scale * LOG2E;
-#pragma unroll
-                            for (int c = 0; c < C; ++c) {
-                                const uint32_t w[4] = {u[y][c].x, u[y][c].y, u[y][c].z, u[y][c].w};
-                                uint32_t x[4];
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const float2 v = unpack16<E0_BF16>(w[z]);
-                                    x[z] = half2_of(v.x * down, v.y * down);
-                                }
-                                u[y][c] = make_uint4(x[0], x[1], x[2], x[3]);
-                            }
-                        }
-                        if (lane >> 3 == g0 + y) f = fr;  // this thread's own row is one of these
-                        uint8_t* dst = mine + (g0 + y) * (16 * D) + (lane & 7) * 16;
-#pragma unroll
-                        for (int c = 0; c < C; ++c) *reinterpret_cast<uint4*>(dst + (4 * c + (lane >> 3)) * 128) = u[y][c];
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.q_full[h]);
+                ok = arrived(&S.q_full[qb], (nq / G_::Q_BUFS) & 1, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                f = S.qf[qb][t];
                 if (RULES && A.a.slopes && row_ok) slope = A.a.slopes[head] * LOG2E;
             }
             // ---- units
@@ -601,8 +554,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 const uint32_t g = gk + (uint32_t)(k - p.k0), st = g % STAGES;
                 const uint32_t slot = HALVES == 2 ? h : n_s & 1, use = HALVES == 2 ? n_s : n_s >> 1;
                 const uint32_t s_at = tmem + lanes + slot * KV;
-                ok = mbar_wait(&S.s_full[slot], use & 1, abort, TILE_WAIT_NS) &&
-                     mbar_wait(&S.v_full[st], (g / STAGES) & 1, abort, TILE_WAIT_NS);
+                ok = arrived(&S.s_full[slot], use & 1, abort) &&
+                     arrived(&S.v_full[st], (g / STAGES) & 1, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -611,9 +564,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 if (lane < KV / 16) edge |= !(S.sc[st][lane].w > 0.f);
                 edge = __any_sync(0xffffffffu, edge);
                 const float away = (float)(pos - at0);
-                float base = (mx == -INFINITY ? 0.f : mx) - LIFT;
+                float base = (mx == -INFINITY ? 0.f : mx) - TILE_LIFT;
 #pragma unroll 1
-                for (int c = 0; c < KV / 64; ++c) {
+                for (int c = 0; c < CHUNKS; ++c) {
                     uint32_t u[2][32];
                     tmem_ld32(s_at + 64 * c, u[0]);
                     tmem_ld32(s_at + 64 * c + 32, u[1]);
@@ -665,24 +618,23 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                         for (int j = 8; j < 64; j += 8) top[y] = fmaxf(fmaxf(top[y], x[j + y]), x[j + 4 + y]);
                     }
                     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    // m follows where t has grown by more than SLACK; the first one is any
-                    const bool grows = mx == -INFINITY ? most > -INFINITY : most > LIFT + SLACK;
+                    // m follows where t has grown by more than TILE_SLACK; the first one is any
+                    const bool grows = mx == -INFINITY ? most > -INFINITY : most > TILE_LIFT + TILE_SLACK;
                     if (__any_sync(0xffffffffu, grows)) {
                         const float now = grows ? most + base : mx, keep = mx == now ? 1.f : exp2_of(mx - now);
-                        const float base_now = (now == -INFINITY ? 0.f : now) - LIFT, shift = base - base_now;
+                        const float base_now = (now == -INFINITY ? 0.f : now) - TILE_LIFT, shift = base - base_now;
                         mx = now, base = base_now;
                         sum *= keep;
 #pragma unroll
                         for (int j = 0; j < 64; ++j) x[j] += shift;
-                        if (k > kf) {  // O of the units before
-                            ok = wait_o(n_s - 1);
+                        if (k > kf || c > 0) {  // O of the units, or the positions, before
+                            ok = c > 0 ? arrived(&S.o_half[h], n_s & 1, abort) : wait_o(n_s - 1);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int y = 0; y < D / 16; ++y) scale16(o_at + 16 * y, keep);
+                            for (int y = 0; y < D / 32; ++y) scale32(o_at + 32 * y, keep);
                         }
-                        if (c > 0) scale_p<SPLIT>(s_at, keep);  // P of the unit's first positions
                     }
                     float part[4];
 #pragma unroll
@@ -708,12 +660,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (iv[q] < INFINITY) sum = fmaf(part[q], iv[q], sum);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.p_full[slot][c]);
                 }
                 if (!ok) break;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_full[slot]);
             }
             if (!ok) break;
             gk += (uint32_t)(p.k1 - p.k0);
@@ -729,16 +681,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 if (!ok) break;
                 tc_fence_after();
             }
-            const auto load_o = [&](int col, uint32_t (&u)[32]) {
-                if (kf < ke) {
-                    tmem_ld32(o_at + col, u);
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) u[j] = 0;
-                }
-            };
-            if (!whole || A.a.raw) {
+            if (kf >= ke) {  // nobody sees anything
+                if (row_ok && whole)
+                    for (int c = 0; c < D; c += 4) put_row4<TY>(A.a, A.vec_out, tok, head * D + c, 0.f, 0.f, 0.f, 0.f);
+                if (row_ok && !whole)
+                    for (int c = 0; c < D; c += 4)
+                        *reinterpret_cast<float4*>(A.part_o + part_at<D>(part, 128 * h + t, c)) = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else if (!whole || A.a.raw) {
                 // fp32: a part's columns stand by fours, eight rows of each together (part_at), so that a warp
                 // writes whole lines
                 const float inv = !whole ? 1.f : sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
@@ -747,7 +696,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t u[32];
-                    load_o(32 * c, u);
+                    tmem_ld32(o_at + 32 * c, u);
+                    tmem_ld_wait();
                     if (row_ok)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -757,12 +707,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 }
             } else {
                 // through shared memory, where the warp's rows of Q were, so that rows are written whole
-                constexpr int CHUNKS = D / 8;  // of 16 bytes, lanes of a row
+                constexpr int ROW = D / 8;  // chunks of 16 bytes, lanes of a row
+                uint8_t* mine = S.q[qb] + 32 * (warp & 3) * (2 * D);
                 const float inv = sum > 0.f || sum != sum ? SUM_UNIT / sum : 0.f;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t u[32];
-                    load_o(32 * c, u);
+                    tmem_ld32(o_at + 32 * c, u);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
@@ -774,10 +726,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                     }
                 }
                 __syncwarp();
-                const int c = lane % CHUNKS;
+                const int c = lane % ROW;
 #pragma unroll 4
-                for (int y = 0; y < CHUNKS; ++y) {
-                    const int row = y * (32 / CHUNKS) + lane / CHUNKS, in = 128 * h + 32 * (warp & 3) + row;
+                for (int y = 0; y < ROW; ++y) {
+                    const int row = y * (32 / ROW) + lane / ROW, in = 128 * h + 32 * (warp & 3) + row;
                     const uint4 v = *reinterpret_cast<const uint4*>(mine + row * (2 * D) + ((c ^ (row & 7)) << 4));
                     const int rr = J.mtile * G_::ROWS + in, ii = div_group(A, rr);
                     T* to = reinterpret_cast<T*>(A.a.out) + ((size_t)J.row0 + ii) * A.a.out_ld + (p.head * G + rr - ii * G) * D + 8 * c;
@@ -796,14 +748,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 __syncwarp();
             }
             tc_fence_before();  // O has been read before the next job's P is there
+            __syncwarp();
+            if (kf < ke && lane == 0) mbar_arrive(&S.q_empty[qb]);
             if (row_ok) {
                 if (!whole)
                     A.part_ml[(size_t)part * G_::ROWS + 128 * h + t] = make_float2(mx, sum);
                 else if (A.a.lse)
-                    A.a.lse[tok * A.a.Hq + head] = lse_of(mx, sum);
+                    A.a.lse[tok * A.a.Hq + head] = lse_of(mx, sum, TILE_LIFT);
             }
             if (!whole && threadIdx.x == 0) {
-                const uint32_t u0 = J.start + (uint32_t)p.head * J.units, share = A.head->share;
+                const uint32_t u0 = J.start + (uint32_t)p.head * (J.units + TILE_JOB_COST) + TILE_JOB_COST, share = A.head->share;
                 const int b0 = (int)(u0 / share), b1 = (int)((u0 + J.units - 1) / share);
                 (p.k0 == 0 ? begun : went_on) = {b1 - b0 + 1, b0, p.job, p.head};
             }
@@ -890,14 +844,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             const uint32_t st = g % STAGES, par = ((g / STAGES) + 1) & 1;
             const bool have2 = look_up(after);
             if (have1) look_in(next, ks1, vs1);
-            ok = __all_sync(0xffffffffu, mbar_wait(&S.k_empty[st], par, abort, TILE_WAIT_NS));
+            ok = __all_sync(0xffffffffu, arrived(&S.k_empty[st], par, abort));
             if (!ok) break;
             store(kr, S.k[st], false);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.k_full[st]);
             if (have1) load(next, A.a.k, kr);
-            ok = __all_sync(0xffffffffu, mbar_wait(&S.v_empty[st], par, abort, TILE_WAIT_NS));
+            ok = __all_sync(0xffffffffu, arrived(&S.v_empty[st], par, abort));
             if (!ok) break;
             if (cw == 0 && lane < KV / 16) {
                 const float v = fmaxf(vs, LEAST_SCALE);
@@ -922,18 +876,18 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             constexpr uint32_t QK_HI = desc_high(16 * D), V_HI = desc_high(128);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const bool leader = elect_one();
-            uint32_t n_s0 = 0, n_s1 = 0, n_q0 = 0, n_q1 = 0, gk = 0;
+            uint32_t n_s0 = 0, n_s1 = 0, n_q = 0, gk = 0;
             bool ok = true, issued = false;
             Piece p;
-            const auto q_there = [&](int h, uint32_t n) {
-                const bool there = __all_sync(0xffffffffu, mbar_wait(&S.q_full[h], n & 1, abort, TILE_WAIT_NS));
+            const auto q_there = [&](uint32_t n) {
+                const bool there = __all_sync(0xffffffffu, arrived(&S.q_full[n % G_::Q_BUFS], (n / G_::Q_BUFS) & 1, abort));
                 tc_fence_after();
                 return there;
             };
             // S of half h, its n-th = Q K^T of the unit in stage st
-            const auto first = [&](int h, uint32_t st, uint32_t n) {
+            const auto first = [&](int h, uint32_t st, uint32_t n, uint32_t nq) {
                 const uint32_t slot = HALVES == 2 ? h : n & 1, d = tm + slot * KV;
-                const uint32_t a = q_lo + h * 16 * D, b = k_lo + st * (uint32_t)(G_::OPERAND >> 4);
+                const uint32_t a = q_lo + nq % G_::Q_BUFS * (uint32_t)(G_::Q_BYTES >> 4), b = k_lo + st * (uint32_t)(G_::OPERAND >> 4);
                 if (leader) {
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) umma_lo(d, a + 16 * s, QK_HI, b + 16 * s, QK_HI, id_s, s > 0);
@@ -943,29 +897,34 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             // O of half h += P V of the unit in stage st, the half's n-th; `more`: not the piece's first
             const auto second = [&](int h, uint32_t st, uint32_t n, uint32_t more) {
                 const uint32_t slot = HALVES == 2 ? h : n & 1, use = HALVES == 2 ? n : n >> 1;
-                if (!__all_sync(0xffffffffu, mbar_wait(&S.p_full[slot], use & 1, abort, TILE_WAIT_NS))) return false;
-                tc_fence_after();
                 const uint32_t p_at = tm + slot * KV, d = tm + G_::O_COL + h * D, b = v_lo + st * (uint32_t)(G_::OPERAND >> 4);
-                if (leader) {
 #pragma unroll
-                    for (int s = 0; s < KV / 16; ++s) {
-                        const uint32_t a = p_at + 64 * (s / 4) + 8 * (s % 4);
-                        umma_ta_lo(d, a, b + s * 2 * D, V_HI, id_o, s > 0 ? 1 : more);
-                        if constexpr (SPLIT) umma_ta_lo(d, a + 32, b + s * 2 * D, V_HI, id_o, 1);
+                for (int c = 0; c < CHUNKS; ++c) {  // the first positions' products run under the last ones' exponentials
+                    if (!__all_sync(0xffffffffu, arrived(&S.p_full[slot][c], use & 1, abort))) return false;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int s = 4 * c; s < 4 * c + 4; ++s) {
+                            const uint32_t a = p_at + 64 * c + 8 * (s % 4);
+                            umma_ta_lo(d, a, b + s * 2 * D, V_HI, id_o, s > 0 ? 1 : more);
+                            if constexpr (SPLIT) umma_ta_lo(d, a + 32, b + s * 2 * D, V_HI, id_o, 1);
+                        }
+                        umma_commit(c + 1 < CHUNKS ? &S.o_half[h] : &S.o_done[slot]);
                     }
-                    umma_commit(&S.o_done[slot]);
                 }
                 return true;
             };
             while (ok && pieces.next(p)) {
                 const int f0 = p.first(0), e0 = p.end(0), f1 = p.first(1), e1 = p.end(1), k0 = p.k0, k1 = p.k1;
+                const uint32_t nq0 = n_q, nq1 = n_q + (f0 < e0);
+                n_q = nq1 + (HALVES == 2 && f1 < e1);
                 // one turn more than units: a unit's second products come with the next one's first
 #pragma unroll 1
                 for (int k = k0; ok && k <= k1; ++k) {
                     const uint32_t g = gk + (uint32_t)(k - k0), st = g % STAGES, last = (g - 1) % STAGES;
                     const bool now = k < k1, before = k > k0;
-                    if (now) ok = mbar_wait(&S.k_full[st], (g / STAGES) & 1, abort, TILE_WAIT_NS);
-                    if (ok && before) ok = mbar_wait(&S.v_full[last], ((g - 1) / STAGES) & 1, abort, TILE_WAIT_NS);
+                    if (now) ok = arrived(&S.k_full[st], (g / STAGES) & 1, abort);
+                    if (ok && before) ok = arrived(&S.v_full[last], ((g - 1) / STAGES) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -974,15 +933,15 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                     if constexpr (HALVES == 2) {
                         const bool now1 = now && k >= f1 && k < e1, before1 = before && k - 1 >= f1 && k - 1 < e1;
                         if (before0) ok = second(0, last, n_s0 - 1, k - 1 > f0);
-                        if (ok && now0 && k == f0) ok = q_there(0, n_q0++);  // a half's Q is waited for where it is wanted
-                        if (ok && now0) first(0, st, n_s0++);
+                        if (ok && now0 && k == f0) ok = q_there(nq0);  // a half's Q is waited for where it is wanted
+                        if (ok && now0) first(0, st, n_s0++, nq0);
                         if (ok && before1) ok = second(1, last, n_s1 - 1, k - 1 > f1);
-                        if (ok && now1 && k == f1) ok = q_there(1, n_q1++);
-                        if (ok && now1) first(1, st, n_s1++);
+                        if (ok && now1 && k == f1) ok = q_there(nq1);
+                        if (ok && now1) first(1, st, n_s1++, nq1);
                     } else {
                         const uint32_t n = n_s0;
-                        if (now0 && k == f0) ok = q_there(0, n_q0++);
-                        if (ok && now0) first(0, st, n_s0++);
+                        if (now0 && k == f0) ok = q_there(nq0);
+                        if (ok && now0) first(0, st, n_s0++, nq0);
                         if (ok && before0) ok = second(0, last, n - 1, k - 1 > f0);
                     }
                     if (!ok) break;
@@ -996,9 +955,86 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             if (!ok && leader) give_up();
             if (issued) {  // the products have ended before tensor memory is freed
                 if (leader) umma_commit(&S.drained);
-                mbar_wait(&S.drained, 0, &never, TILE_WAIT_NS);
+                arrived(&S.drained, 0, &never);
             }
             __syncwarp();
+        } else {
+            // ---------------- Q: a warp eight rows at a time, a lane 16 bytes of every 64 of row lane % 8
+            const int g0 = warp - G_::SOFT - 5;
+            uint32_t nq = 0;
+            bool ok = true;
+            Piece p;
+            while (ok && pieces.next(p)) {
+                const TileJob& J = p.J;
+#pragma unroll 1
+                for (int h = 0; h < HALVES; ++h) {
+                    if (p.first(h) >= p.end(h)) continue;
+                    const uint32_t qb = nq % G_::Q_BUFS;
+                    constexpr int C = D / 32;
+                    uint4 u[C], next[C];
+                    const auto load_q = [&](int g8, uint4 (&to)[C]) {
+                        const int row = 128 * h + 8 * g8 + (lane & 7), rr = J.mtile * G_::ROWS + row;
+                        const int ii = div_group(A, rr);
+                        const bool have = row < J.rows;
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            reinterpret_cast<const T*>(A.a.q) +
+                            (have ? ((size_t)J.row0 + ii) * A.a.q_ld + (size_t)(p.head * G + rr - ii * G) * D : 0));
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            to[c] = make_uint4(0, 0, 0, 0);
+                            if (have) to[c] = __ldg(src + 4 * c + (lane >> 3));
+                        }
+                    };
+                    load_q(g0, next);
+                    ok = __all_sync(0xffffffffu, arrived(&S.q_empty[qb], ((nq / G_::Q_BUFS) + 1) & 1, abort));
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int g8 = g0; g8 < 16; g8 += G_::Q_WARPS) {
+#pragma unroll
+                        for (int c = 0; c < C; ++c) u[c] = next[c];
+                        if (g8 + G_::Q_WARPS < 16) load_q(g8 + G_::Q_WARPS, next);
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int c = 0; c < C; ++c)
+                            m = __vmaxu2(__vmaxu2(__vmaxu2(m, u[c].x & 0x7FFF7FFFu), u[c].y & 0x7FFF7FFFu),
+                                         __vmaxu2(u[c].z & 0x7FFF7FFFu, u[c].w & 0x7FFF7FFFu));
+                        m = max(m & 0xFFFFu, m >> 16);
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        float fr;
+                        if constexpr (TY == E0_F16) {
+                            fr = m >= 0x7C00u ? __uint_as_float(0x7FC00000u) : A.a.scale * LOG2E;
+                        } else {  // times a power of two that brings the largest near 1
+                            const uint32_t b = m << 16;
+                            int e = (int)(b >> 23);
+                            e = e < 27 ? 27 : e > 253 ? 253 : e;
+                            const float down = b == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);
+                            fr = b >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                                  : __uint_as_float((uint32_t)e << 23) * A.a.scale * LOG2E;
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+                                uint32_t x[4];
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const float2 v = unpack16<E0_BF16>(w[z]);
+                                    x[z] = half2_of(v.x * down, v.y * down);
+                                }
+                                u[c] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                        if (lane < 8) S.qf[qb][8 * g8 + lane] = fr;
+                        uint8_t* dst = S.q[qb] + g8 * (16 * D) + (lane & 7) * 16;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) *reinterpret_cast<uint4*>(dst + (4 * c + (lane >> 3)) * 128) = u[c];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.q_full[qb]);
+                    ++nq;
+                }
+            }
+            if (!ok && lane == 0) give_up();
         }
     }
     tc_fence_before();
@@ -1062,7 +1098,7 @@ __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
         }
     }
     const float inv = l > 0.f || l != l ? SUM_UNIT / l : 0.f;
-    float lse = lse_of(m, l);
+    float lse = lse_of(m, l, TILE_LIFT);
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
     if (A.merge) {
         const float4 x = *reinterpret_cast<const float4*>(A.own_o + at * D + d4);
