@@ -290,6 +290,27 @@ E0_DEV float exp2_of(float x) {  // 2 ulp; results below 2^-126 are 0
     return r;
 }
 
+// tanh(u) / u for u^2 = v up to 1: the polynomial of least largest error (1.7e-9; 1.4e-7 of itself
+// in fp32), fitted to 40 digits' values.  Scores are hardly ever beyond their cap, and the
+// exponential and the inverse that tanh takes there are what these kernels have least of.
+E0_DEV constexpr float tanh_of(int i) {  // the factor of v^i
+    return i == 0   ? 1.0f
+           : i == 1 ? -0.3333318531513214f
+           : i == 2 ? 0.1333116590976715f
+           : i == 3 ? -0.05382394418120384f
+           : i == 4 ? 0.02135070599615574f
+           : i == 5 ? -0.007768805138766766f
+           : i == 6 ? 0.0021835514344274998f
+                    : -0.00032712501706555486f;
+}
+E0_DEV float tanh_below_1(float u) {
+    const float v = u * u;
+    float p = tanh_of(7);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) p = fmaf(p, v, tanh_of(i));
+    return p * u;
+}
+
 E0_DEV void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -668,12 +689,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 #pragma unroll
                     for (int w = 0; w < RW; ++w)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float x = WIDE ? s[h][2 * w + i] * (f[w] * sc[h / 2].x) : (s[h][i] + s[h][2 + i]) * fk;
-                            if (A.cap > 0.f) x = A.cap * tanhf(x * A.inv_cap);
-                            if (A.slopes) x = fmaf(-slope[w], fabsf((float)(place[w] - (pos + 8 * h + 2 * t4 + i))), x);
-                            p[w][h][i] = x + sc[h / 2].y;
-                        }
+                        for (int i = 0; i < 2; ++i)  // the score alone, for now
+                            p[w][h][i] = WIDE ? s[h][2 * w + i] * (f[w] * sc[h / 2].x) : (s[h][i] + s[h][2 + i]) * fk;
                 } else if constexpr (WIDE) {
                     const float fk1 = f[RW - 1] * sc[h / 2].x;
                     p[0][h][0] = fmaf(s[h][0], fk, sc[h / 2].y), p[0][h][1] = fmaf(s[h][1], fk, sc[h / 2].y);
@@ -682,6 +699,25 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     p[0][h][0] = fmaf(s[h][0] + s[h][2], fk, sc[h / 2].y);
                     p[0][h][1] = fmaf(s[h][1] + s[h][3], fk, sc[h / 2].y);
                 }
+            }
+            if (RULES && (A.cap > 0.f || A.slopes)) {
+                float most = 0.f;
+#pragma unroll
+                for (int w = 0; w < RW; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2 * SUBS; ++h) most = fmaxf(most, fmaxf(fabsf(p[w][h][0]), fabsf(p[w][h][1])));
+                const bool small = !__any_sync(0xffffffffu, !(most <= A.cap));
+#pragma unroll
+                for (int w = 0; w < RW; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2 * SUBS; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = p[w][h][i];
+                            if (A.cap > 0.f) x = A.cap * (small ? tanh_below_1(x * A.inv_cap) : tanhf(x * A.inv_cap));
+                            if (A.slopes) x = fmaf(-slope[w], fabsf((float)(place[w] - (pos + 8 * h + 2 * t4 + i))), x);
+                            p[w][h][i] = x + sc[h / 2].y;
+                        }
             }
             if (edge) {
 #pragma unroll

@@ -405,10 +405,51 @@ E0_DEV void add2(float& s0, float& s1, float a, float b) {
         : "+f"(s0), "+f"(s1)
         : "f"(a), "f"(b));
 }
+E0_DEV void mul2(float& r0, float& r1, float a0, float a1, float f) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(f));
+}
+// (a0 * b0 + c, a1 * b1 + c)
+E0_DEV void fma2_by(float& r0, float& r1, float a0, float a1, float b0, float b1, float c) {
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %6};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c));
+}
 E0_DEV float inverse_of(float x) {  // a step of fp32 off
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// x = cap tanh(x / cap) of 64 scores: a polynomial where none of the warp's is beyond the cap,
+// otherwise cap - 2 cap / (1 + e^(2 x / cap)), two steps of fp32 of cap off.
+E0_DEV void cap_scores(float (&x)[64], float cap, float inv_cap) {
+    float top[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        top[y] = fmaxf(fabsf(x[y]), fabsf(x[4 + y]));
+#pragma unroll
+        for (int j = 8; j < 64; j += 8) top[y] = fmaxf(fmaxf(top[y], fabsf(x[j + y])), fabsf(x[j + 4 + y]));
+    }
+    if (!__any_sync(0xffffffffu, !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= cap))) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+            float u0, u1, v0, v1, p0, p1;
+            mul2(u0, u1, x[j], x[j + 1], inv_cap);
+            fma2_by(v0, v1, u0, u1, u0, u1, 0.f);
+            fma2(p0, p1, v0, v1, tanh_of(7), tanh_of(6));
+#pragma unroll
+            for (int i = 5; i >= 0; --i) fma2_by(p0, p1, p0, p1, v0, v1, tanh_of(i));
+            fma2_by(x[j], x[j + 1], x[j], x[j + 1], p0, p1, 0.f);  // cap (x / cap) p
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            const float e = exp2_of(fminf(x[j] * inv_cap * (2.f * LOG2E), 126.f));
+            x[j] = fmaf(-2.f * cap, inverse_of(1.f + e), cap);
+        }
+    }
 }
 // Bits 0 .. n-1, n any number.
 E0_DEV uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
@@ -584,21 +625,24 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                         for (int j = 0; j < 16; j += 2) {
                             const float s0 = __uint_as_float(u[q / 2][16 * (q & 1) + j]);
                             const float s1 = __uint_as_float(u[q / 2][16 * (q & 1) + j + 1]);
-                            if constexpr (RULES) {
-                                float y[2] = {s0 * fk, s1 * fk};
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) {
-                                    if (A.a.cap > 0.f) {
-                                        // cap tanh(y / cap) = cap - 2 cap / (1 + e^(2 y / cap)), two steps of fp32 of cap off
-                                        const float e = exp2_of(fminf(y[z] * A.a.inv_cap * (2.f * LOG2E), 126.f));
-                                        y[z] = fmaf(-2.f * A.a.cap, inverse_of(1.f + e), A.a.cap);
-                                    }
-                                    y[z] = fmaf(-slope, fabsf(away - (float)(64 * c) - (float)(16 * q + j + z)), y[z]);
-                                    x[16 * q + j + z] = y[z] + off;
-                                }
-                            } else {
+                            if constexpr (RULES)
+                                mul2(x[16 * q + j], x[16 * q + j + 1], s0, s1, fk);
+                            else
                                 fma2(x[16 * q + j], x[16 * q + j + 1], s0, s1, fk, off);
-                            }
+                        }
+                    }
+                    if constexpr (RULES) {
+                        if (A.a.cap > 0.f) cap_scores(x, A.a.cap, A.a.inv_cap);
+                        if (A.a.slopes) {
+                            const float from = away - (float)(64 * c);
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) x[j] = fmaf(-slope, fabsf(from - (float)j), x[j]);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float off = scales[q].y - base;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[16 * q + j] += off;
                         }
                     }
                     if (edge) {
@@ -623,11 +667,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                     if (__any_sync(0xffffffffu, grows)) {
                         const float now = grows ? most + base : mx, keep = mx == now ? 1.f : exp2_of(mx - now);
                         const float base_now = (now == -INFINITY ? 0.f : now) - TILE_LIFT, shift = base - base_now;
+                        const bool had = grows && mx > -INFINITY;
                         mx = now, base = base_now;
                         sum *= keep;
 #pragma unroll
                         for (int j = 0; j < 64; ++j) x[j] += shift;
-                        if (k > kf || c > 0) {  // O of the units, or the positions, before
+                        // O of the units, or the positions, before, where a row had seen any (otherwise it is 0)
+                        if ((k > kf || c > 0) && __any_sync(0xffffffffu, had)) {
                             ok = c > 0 ? arrived(&S.o_half[h], n_s & 1, abort) : wait_o(n_s - 1);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
