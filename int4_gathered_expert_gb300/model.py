@@ -357,6 +357,12 @@ class KvCacheDev:
         self.free_count = torch.full((1,), n_blocks, dtype=torch.int32, device=device)
         self.state = L.KvState(self.table.data_ptr(), self.ctx.data_ptr(), self.free.data_ptr(),
                                self.free_count.data_ptr(), B, max_blocks, block_tokens, n_blocks)
+        # what all sequences begin with (share), as a sequence of its own of the same pool
+        self.prefix_table = torch.full((1, max_blocks), -1, dtype=torch.int32, device=device)
+        self.prefix_len = torch.zeros(1, dtype=torch.int32, device=device)
+        self.prefix_state = L.KvState(self.prefix_table.data_ptr(), self.prefix_len.data_ptr(), self.free.data_ptr(),
+                                      self.free_count.data_ptr(), 1, max_blocks, block_tokens, n_blocks)
+        self._all = torch.ones(1, dtype=torch.uint8, device=device)
         torch.cuda.synchronize()  # any stream may use it from here on
 
     def plan(self, new_len, T_cap, cu_q, slots, positions=None, seq_ids=None, status=None, stream=None):
@@ -367,6 +373,91 @@ class KvCacheDev:
     def release(self, mask, status=None, stream=None):
         """Empty the sequences whose mask byte is set; their blocks are free again."""
         L.e0_kv_release(self.state, mask, self.ctx, self.free_count, status, stream=stream)
+
+    def share(self, b: int, stream=None):
+        """Sequence b's tokens become the prefix of every sequence (decoders made with
+        prefix=True), and b is empty.  The others' tokens then stand behind them, so they are
+        empty, too, when this is called; a prefix there was is given back first (unshare)."""
+        if not 0 <= b < self.B:
+            raise ValueError("b is one of the %d sequences" % self.B)
+        with _on(stream):
+            self.prefix_table[0].copy_(self.table[b])
+            self.prefix_len.copy_(self.ctx[b:b + 1])
+            self.table[b].fill_(-1)
+            self.ctx[b].fill_(0)
+
+    def unshare(self, status=None, stream=None):
+        """The prefix' blocks are free again; there is none."""
+        L.e0_kv_release(self.prefix_state, self._all, self.prefix_len, self.free_count, status, stream=stream)
+
+
+class QkRope:
+    """Norms of queries and keys and their rotation by position (e0_qk_rope), as the edit of a
+    BatchDecoder: called with the layer, qkv fp16 [T, (Hq + 2 Hkv) D], changed in place, and
+    positions int32 [T], or [axes, T] where pairs turn by several.  freq: radians a
+    position for each of rot / 2 pairs; axis: which axis a pair turns by; q_norm,
+    k_norm: a weight fp32 [D] a layer, or None for norms without one; norm=False: none."""
+
+    def __init__(self, shape, freq: np.ndarray, n_layers: int = 1, axis: Optional[np.ndarray] = None, n_axes: int = 1,
+                 norm: bool = True, q_norm: Optional[List[np.ndarray]] = None, k_norm: Optional[List[np.ndarray]] = None,
+                 adjacent: bool = False, eps: float = 1e-6, device="cuda"):
+        def weights(w):
+            if w is not None and (len(w) != n_layers or any(v.shape != (shape.D,) for v in w)):
+                raise ValueError("a norm's weight is one [%d] a layer" % shape.D)
+            return [None] * n_layers if w is None else [_dev(v.astype(np.float32), device) for v in w]
+
+        if axis is not None and (axis.shape != freq.shape or int(axis.max(initial=0)) >= n_axes):
+            raise ValueError("an axis below n_axes for each of the pairs")
+        self.shape, self.n_axes = shape, n_axes
+        self.freq = _dev(freq.astype(np.float32), device)
+        self.axis = None if axis is None else _dev(axis.astype(np.uint8), device)
+        self.q_norm, self.k_norm = weights(q_norm), weights(k_norm)
+        flags = (L.E0_ROPE_ADJACENT if adjacent else 0) | (L.E0_QK_NORM if norm else 0)
+        self.descs = [L.Rope(self.freq.data_ptr(), L.ptr(self.axis), L.ptr(q), L.ptr(k), shape.D, 2 * len(freq), n_axes,
+                             flags, eps) for q, k in zip(self.q_norm, self.k_norm)]
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.synchronize()
+
+    def __call__(self, layer: int, qkv: torch.Tensor, positions: torch.Tensor):
+        a = self.shape
+        row = (a.Hq + 2 * a.Hkv) * a.D
+        if qkv.dtype != torch.float16 or qkv.dim() != 2 or qkv.shape[1] != row or qkv.stride(1) != 1:
+            raise ValueError("qkv is fp16 rows of %d" % row)
+        T = len(qkv)
+        if positions.dtype != torch.int32 or positions.numel() != self.n_axes * T or not positions.is_contiguous():
+            raise ValueError("positions are contiguous int32 [%d, %d]" % (self.n_axes, T))
+        L.e0_qk_rope(qkv, L.E0_F16, qkv.stride(0), T, a.Hq, a.Hkv, self.descs[layer], positions, T, qkv, qkv.stride(0),
+                     self.status)
+
+
+class Sampler:
+    """The next tokens of T rows of logits over V tokens (e0_sample).  The rules are tensors of
+    T values on the device, to be changed between calls, or None for no such rule; the results
+    are the sampler's own buffers: the next call writes over them."""
+
+    def __init__(self, T: int, V: int, temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                 top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None, device="cuda"):
+        for t, dtype in ((temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32), (min_p, torch.float32)):
+            if t is not None and (t.dtype != dtype or t.shape != (T,) or not t.is_cuda or not t.is_contiguous()):
+                raise ValueError("a rule is contiguous %s [%d] on the device" % (str(dtype)[6:], T))
+        self.T, self.V = T, V
+        self.keep = (temperature, top_k, top_p, min_p)
+        self.rules = L.Sampling(L.ptr(temperature), L.ptr(top_k), L.ptr(top_p), L.ptr(min_p))
+        self.tokens = torch.zeros(T, dtype=torch.int32, device=device)
+        self.logp = torch.zeros(T, device=device)
+        self.kept = torch.zeros(T, dtype=torch.int32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.synchronize()
+
+    def __call__(self, logits: torch.Tensor, u: torch.Tensor, stream=None) -> torch.Tensor:
+        code = {torch.float32: L.E0_F32, torch.float16: L.E0_F16, torch.bfloat16: L.E0_BF16}.get(logits.dtype)
+        if code is None or logits.shape != (self.T, self.V) or not logits.is_cuda or logits.stride(1) != 1:
+            raise ValueError("logits are rows [%d, %d] of fp32, fp16 or bf16 on the device" % (self.T, self.V))
+        if u.dtype != torch.float32 or u.shape != (self.T,) or not u.is_cuda or not u.is_contiguous():
+            raise ValueError("u is contiguous fp32 [%d] on the device" % self.T)
+        L.e0_sample(logits, code, logits.stride(0), self.T, self.V, self.rules, u, self.tokens, self.logp, self.kept,
+                    self.status, stream=stream)
+        return self.tokens
 
 
 class BatchDecoder:
@@ -383,11 +474,19 @@ class BatchDecoder:
     edit: what a model does to queries and keys before they meet (rotary embeddings,
     norms), or None: called on the step's stream with the layer, qkv fp16 [T, (Hq + 2
     Hkv) D] (queries, keys, values; to be changed in place) and the rows' positions
-    int32 [T], -1 after the last new token.  All of a step's work is on one stream and
+    int32 [T], -1 after the last new token (QkRope is one).
+    cap, slopes: scores are capped, or lose slopes[head] a token of distance.  prefix: the
+    sequences stand behind the cache's prefix (KvCacheDev.share; positions count it).
+    All of a step's work is on one stream and
     allocates nothing but what edit does, so a step can be captured into a CUDA graph."""
 
     def __init__(self, sd: StackDev, attn: List[dict], shape, cache: KvCacheDev, T: int, device="cuda",
-                 edit: Optional[Callable[[int, torch.Tensor, torch.Tensor], None]] = None):
+                 edit: Optional[Callable[[int, torch.Tensor, torch.Tensor], None]] = None, cap: float = 0.0,
+                 slopes: Optional[np.ndarray] = None, prefix: bool = False):
+        if not 0 <= cap < float("inf"):
+            raise ValueError("cap is 0 (none) or a positive number")
+        if slopes is not None and slopes.shape != (shape.Hq,):
+            raise ValueError("a slope a query head")
         if len(attn) != sd.L:
             raise ValueError("one attention half a layer")
         if not 1 <= T <= L.E0_MAX_T_DECODE:
@@ -418,7 +517,15 @@ class BatchDecoder:
         self.inds, self.w = buf(T, sd.K, dtype=torch.int32), buf(T, sd.K)
         self.ws_bytes = L.e0_workspace_size(0, T, sd.H, sd.I, sd.E, sd.K)
         self.ws = buf(self.ws_bytes, dtype=torch.uint8)
-        self.aws_bytes = L.e0_attn_workspace_size(cache.B, a.Hq, a.Hkv, a.D, T)
+        self.cap, self.prefix = cap, prefix
+        self.slopes = None if slopes is None else _dev(slopes.astype(np.float32), device)
+        self.at, self.real = buf(T, dtype=torch.int32), buf(T, dtype=torch.bool)
+        if prefix:
+            self.aws_bytes = L.e0_attn_shared_workspace_size(cache.B, T, a.Hq, a.Hkv, a.D, T)
+        elif cap or slopes is not None:
+            self.aws_bytes = L.e0_attn_scored_workspace_size(cache.B, a.Hq, a.Hkv, a.D, T)
+        else:
+            self.aws_bytes = L.e0_attn_workspace_size(cache.B, a.Hq, a.Hkv, a.D, T)
         self.aws = buf(self.aws_bytes, dtype=torch.uint8)
         self.status = buf(1, dtype=torch.int32)
         self.r_out = buf(T, H)
@@ -438,6 +545,12 @@ class BatchDecoder:
         c.plan(new_len, T, self.cu_q, self.slots, self.positions, status=self.status, **kw)
         with _on(stream):
             self.o.zero_()  # attention leaves the rows after the last new token, which an earlier step may have used
+            positions = self.positions
+            if self.prefix:  # behind the prefix; -1 where there is no token
+                torch.ge(self.positions, 0, out=self.real)
+                torch.mul(self.real, c.prefix_len, out=self.at)
+                positions = self.at.add_(self.positions)
+        rules = L.AttnRules(self.cap, window, L.ptr(self.slopes), None, None)
         src, delta = x, None
         for l in range(sd.L):
             L.e0_rmsnorm_q8(src, delta, self.norm[l], T, H, L.E0_F32, 1e-6, H, H, self.r, None, self.q8, self.q8_scale,
@@ -447,13 +560,22 @@ class BatchDecoder:
                                 self.row, **kw)
             if self.edit is not None:
                 with _on(stream):
-                    self.edit(l, self.x_qkv, self.positions)
+                    self.edit(l, self.x_qkv, positions)
             k = self.x_qkv.data_ptr() + 2 * a.Hq * a.D
             v = k + 2 * a.Hkv * a.D
             L.e0_kv_append(c.descs[l], k, v, L.E0_F16, self.row, self.row, self.slots, T, self.status, **kw)
-            L.e0_attn_decode(c.descs[l], c.table, c.max_blocks, c.ctx, self.cu_q, c.B, T, self.x_qkv, L.E0_F16, self.row,
-                             a.Hq, a.D ** -0.5, window, self.o, a.Hq * a.D, None, self.aws, self.aws_bytes, self.status,
-                             **kw)
+            if self.prefix:
+                L.e0_attn_shared(c.descs[l], c.prefix_table, c.max_blocks, c.prefix_len, c.table, c.max_blocks, c.ctx,
+                                 self.cu_q, c.B, T, T, self.x_qkv, L.E0_F16, self.row, a.Hq, a.D ** -0.5, rules, self.o,
+                                 a.Hq * a.D, None, self.aws, self.aws_bytes, self.status, **kw)
+            elif self.cap or self.slopes is not None:
+                L.e0_attn_scored(c.descs[l], c.table, c.max_blocks, c.ctx, self.cu_q, c.B, T, self.x_qkv, L.E0_F16,
+                                 self.row, a.Hq, a.D ** -0.5, rules, self.o, a.Hq * a.D, None, self.aws, self.aws_bytes,
+                                 self.status, **kw)
+            else:
+                L.e0_attn_decode(c.descs[l], c.table, c.max_blocks, c.ctx, self.cu_q, c.B, T, self.x_qkv, L.E0_F16,
+                                 self.row, a.Hq, a.D ** -0.5, window, self.o, a.Hq * a.D, None, self.aws, self.aws_bytes,
+                                 self.status, **kw)
             p = self.out[l]
             L.e0_linear_forward(p.data, p.N, p.K, self.o, L.E0_F16, a.Hq * a.D, None, T, self.r, H, self.r, L.E0_F32, H,
                                 **kw)
