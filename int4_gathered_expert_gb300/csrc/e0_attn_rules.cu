@@ -5,9 +5,29 @@
 namespace e0 {
 namespace {
 
-// Whether many rows of a KV head go through the tensor cores' tiles (their products in fp16
-// are not enough for fp32 outputs) or through the kernel that is made for few.
-bool by_tiles(int dtype, int64_t rows) { return dtype != E0_F32 && rows >= 64; }
+// Whether the rows can go through the tensor cores' tiles: enough of a KV head to fill a part of
+// one (their products in fp16 are not enough for fp32 outputs).
+bool has_tiles(int dtype, int64_t rows) { return dtype != E0_F32 && rows >= 64; }
+
+// Whether they do: the tiles' kernels take 17 to 25 us before a first product counts, the one
+// for few rows 8 us and then 1 us for every 160 thousand pairs of a row and a position in fp16 with
+// heads of 128 (a half of that with heads of 256, one and a half times as many in bf16).  Measured with 8
+// heads on 2 (us, few rows / tiles; fp16, heads of 128): 200 queries behind 1000 tokens 14.8 / 29.6, 600
+// queries alone 31.2 / 31.7, four times 600 85 / 36, 1500 behind 500 153 / 40.  The host knows what a
+// sequence can hold, not what it does: no more than 8192 positions are counted on.
+bool by_tiles(const AttnArgs& a, int dtype, int64_t rows, int64_t queries, int64_t pairs_worth) {
+    if (!has_tiles(dtype, rows)) return false;
+    int64_t seen = (int64_t)a.max_blocks << a.shift;
+    if (a.window > 0 && !a.at) seen = seen < (int64_t)a.window + a.max_q ? seen : (int64_t)a.window + a.max_q;
+    return queries * a.Hq * (seen < 8192 ? seen : 8192) >= pairs_worth;
+}
+
+int64_t prompt_pairs(int dtype, int D) {
+    const int64_t n = dtype == E0_BF16 ? 4500000 : 3000000;
+    return D == 256 ? n * 6 / 10 : n;
+}
+// (32 sequences behind 8000 tokens, 8 heads of 128 on 2, 2 million pairs: 37.1 / 34.8 us; behind 2000: 26.9 / 31.2.)
+constexpr int64_t PREFIX_PAIRS = 1000000;
 
 void put_rules(AttnArgs& a, const e0_attn_rules* r) {
     if (!r) return;
@@ -66,7 +86,7 @@ size_t parts_bytes(int T, int Hq, int D) {  // a normed fp32 result and its lse
 
 size_t attn_scored_ws_bytes(int B, int Hq, int Hkv, int D, int max_q) {
     const size_t few = attn_ws_bytes(D), many = attn_tile_ws_bytes(B, max_q, Hq / Hkv, D);
-    return by_tiles(E0_F16, (int64_t)max_q * (Hq / Hkv)) && many > few ? many : few;
+    return has_tiles(E0_F16, (int64_t)max_q * (Hq / Hkv)) && many > few ? many : few;
 }
 
 int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu, int B,
@@ -74,13 +94,14 @@ int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
                 void* out, int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
     AttnArgs a = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, lse, ws, st);
     put_rules(a, rules);
-    if (by_tiles(dtype, (int64_t)max_q * (Hq / c->Hkv))) return attn_tile(a, nullptr, dtype, ws, s);
+    if (by_tiles(a, dtype, (int64_t)max_q * (Hq / c->Hkv), (int64_t)B * max_q, prompt_pairs(dtype, c->D)))
+        return attn_tile(a, nullptr, dtype, ws, s);
     return launch_t<true>(a, dtype, c->D, s);
 }
 
 size_t attn_shared_ws_bytes(int B, int T, int Hq, int Hkv, int D, int max_q) {
     // the tiles' schedule is made while the sequences' own attention runs: a place for each
-    const size_t tiles = by_tiles(E0_F16, (int64_t)T * (Hq / Hkv)) ? attn_tile_ws_bytes(1, T, Hq / Hkv, D) : 0;
+    const size_t tiles = has_tiles(E0_F16, (int64_t)T * (Hq / Hkv)) ? attn_tile_ws_bytes(1, T, Hq / Hkv, D) : 0;
     return up256((size_t)T * sizeof(int32_t)) + 256 + 2 * parts_bytes(T, Hq, D) + up256(attn_ws_bytes(D)) + tiles;
 }
 
@@ -114,7 +135,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
     // what the sequences have of their own comes first: the prefix' last kernel adds it where it can
     int rc = launch_t<true>(mine, dtype, c->D, s);
     if (rc != E0_OK) return rc;
-    if (by_tiles(dtype, (int64_t)T * (Hq / c->Hkv))) {
+    if (by_tiles(front, dtype, (int64_t)T * (Hq / c->Hkv), T, PREFIX_PAIRS)) {
         const TilePrefix prefix = {mine, at, o[1], l[1], attn_tile_merges(front)};
         if (prefix.merge) {
             front.lse = lse;

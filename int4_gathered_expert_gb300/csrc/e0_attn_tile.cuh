@@ -417,6 +417,12 @@ E0_DEV void fma2_by(float& r0, float& r1, float a0, float a1, float b0, float b1
         : "=f"(r0), "=f"(r1)
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c));
 }
+// 16 bytes on their way to shared memory, zeros where there are none.
+E0_DEV void copy16_or_zero(uint8_t* dst, const void* src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(have ? 16 : 0)
+                 : "memory");
+}
 E0_DEV float inverse_of(float x) {  // a step of fp32 off
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -1005,8 +1011,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             }
             __syncwarp();
         } else {
-            // ---------------- Q: a warp eight rows at a time, a lane 16 bytes of every 64 of row lane % 8
+            // ---------------- Q: a warp eight rows at a time, a lane 16 bytes of every 64 of row lane % 8.
+            // All of a warp's rows are copied to their places first, so that one latency is waited for, then
+            // looked at and, bf16, turned into fp16 there.
             const int g0 = warp - G_::SOFT - 5;
+            constexpr int C = D / 32;
             uint32_t nq = 0;
             bool ok = true;
             Piece p;
@@ -1016,34 +1025,30 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 for (int h = 0; h < HALVES; ++h) {
                     if (p.first(h) >= p.end(h)) continue;
                     const uint32_t qb = nq % G_::Q_BUFS;
-                    constexpr int C = D / 32;
-                    uint4 u[C], next[C];
-                    const auto load_q = [&](int g8, uint4 (&to)[C]) {
-                        const int row = 128 * h + 8 * g8 + (lane & 7), rr = J.mtile * G_::ROWS + row;
-                        const int ii = div_group(A, rr);
-                        const bool have = row < J.rows;
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            reinterpret_cast<const T*>(A.a.q) +
-                            (have ? ((size_t)J.row0 + ii) * A.a.q_ld + (size_t)(p.head * G + rr - ii * G) * D : 0));
-#pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            to[c] = make_uint4(0, 0, 0, 0);
-                            if (have) to[c] = __ldg(src + 4 * c + (lane >> 3));
-                        }
-                    };
-                    load_q(g0, next);
                     ok = __all_sync(0xffffffffu, arrived(&S.q_empty[qb], ((nq / G_::Q_BUFS) + 1) & 1, abort));
                     if (!ok) break;
+                    uint8_t* mine = S.q[qb] + (lane & 7) * 16 + (lane >> 3) * 128;
 #pragma unroll 1
                     for (int g8 = g0; g8 < 16; g8 += G_::Q_WARPS) {
+                        const int row = 128 * h + 8 * g8 + (lane & 7), rr = J.mtile * G_::ROWS + row, ii = div_group(A, rr);
+                        const bool have = row < J.rows;
+                        const T* src = reinterpret_cast<const T*>(A.a.q) + 8 * (lane >> 3) +
+                                       (have ? ((size_t)J.row0 + ii) * A.a.q_ld + (size_t)(p.head * G + rr - ii * G) * D : 0);
 #pragma unroll
-                        for (int c = 0; c < C; ++c) u[c] = next[c];
-                        if (g8 + G_::Q_WARPS < 16) load_q(g8 + G_::Q_WARPS, next);
+                        for (int c = 0; c < C; ++c) copy16_or_zero(mine + g8 * (16 * D) + c * 512, src + 32 * c, have);
+                    }
+                    copy_commit();
+                    copy_wait<0>();
+#pragma unroll 1
+                    for (int g8 = g0; g8 < 16; g8 += G_::Q_WARPS) {
+                        uint4 u[C];
                         uint32_t m = 0;
 #pragma unroll
-                        for (int c = 0; c < C; ++c)
+                        for (int c = 0; c < C; ++c) {
+                            u[c] = *reinterpret_cast<const uint4*>(mine + g8 * (16 * D) + c * 512);
                             m = __vmaxu2(__vmaxu2(__vmaxu2(m, u[c].x & 0x7FFF7FFFu), u[c].y & 0x7FFF7FFFu),
                                          __vmaxu2(u[c].z & 0x7FFF7FFFu, u[c].w & 0x7FFF7FFFu));
+                        }
                         m = max(m & 0xFFFFu, m >> 16);
                         m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -1066,13 +1071,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                                     const float2 v = unpack16<E0_BF16>(w[z]);
                                     x[z] = half2_of(v.x * down, v.y * down);
                                 }
-                                u[c] = make_uint4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<uint4*>(mine + g8 * (16 * D) + c * 512) = make_uint4(x[0], x[1], x[2], x[3]);
                             }
                         }
                         if (lane < 8) S.qf[qb][8 * g8 + lane] = fr;
-                        uint8_t* dst = S.q[qb] + g8 * (16 * D) + (lane & 7) * 16;
-#pragma unroll
-                        for (int c = 0; c < C; ++c) *reinterpret_cast<uint4*>(dst + (4 * c + (lane >> 3)) * 128) = u[c];
                     }
                     fence_proxy_async_smem();
                     __syncwarp();

@@ -13,7 +13,27 @@ from tests.test_layer_ops import (BF16, DT, EPS, F16, F32, H, TINY16, L, attend,
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-TILE_ROWS = 64  # rows of a KV head from which 16-bit queries go through the tiles
+TILE_ROWS = 64  # rows of a KV head from which 16-bit queries can go through the tiles
+ROOM = 8192     # positions: with tables of as many, calls of some hundred rows do
+WORTH = 5_000_000  # pairs of rows and positions from which all do
+
+
+class Tables:
+    """Tables as long as what the cache holds, or with room for more, where calls of few rows go another way."""
+    room = False
+
+    @classmethod
+    def widen(cls, table, bs):
+        table = np.atleast_2d(np.asarray(table, np.int32))
+        n = ROOM // bs - table.shape[1] if cls.room else 0
+        return np.pad(table, ((0, 0), (0, max(n, 0))), constant_values=-1)
+
+
+@pytest.fixture(params=[False, True], ids=["held", "room"])
+def room(request):
+    Tables.room = request.param
+    yield request.param
+    Tables.room = False
 
 
 def rules_ref(q, k, v, scale, p, seen, cap=0.0, slopes=None, weight_err=0.0, quantum=0.0):
@@ -85,7 +105,13 @@ def scored(L, desc, Hkv, table, ctx, cu, q, dtype, window=0, cap=0.0, slopes=Non
     T, Hq, D = q.shape
     B = len(ctx)
     n = np.diff(cu)
-    max_q = max(1, int(n.max())) if max_q is None else max_q
+    if max_q is None:
+        max_q = max(1, int(n.max()))
+        if Tables.room and B * Hq < WORTH:
+            max_q = max(max_q, TILE_ROWS)
+            while B * max_q * Hq * min(ROOM, window + max_q if window else ROOM) < WORTH:
+                max_q *= 2
+    table = Tables.widen(table, desc.block_tokens)
     if out is None:
         out = torch.full((T + pad, Hq, D), -7.0, dtype=DT[dtype], device="cuda")
     ls = torch.full((T + pad, Hq), -7.0, device="cuda") if lse else None
@@ -95,7 +121,7 @@ def scored(L, desc, Hkv, table, ctx, cu, q, dtype, window=0, cap=0.0, slopes=Non
     wsb = L.e0_attn_scored_workspace_size(B, Hq, Hkv, D, max_q)
     ws = torch.full((wsb,), 255, dtype=torch.uint8, device="cuda")
     st = status()
-    L.e0_attn_scored(desc, dev(np.asarray(table, np.int32)), np.asarray(table).shape[1], dev(np.asarray(ctx, np.int32)),
+    L.e0_attn_scored(desc, dev(table), table.shape[1], dev(np.asarray(ctx, np.int32)),
                      dev(np.asarray(cu, np.int32)), B, max_q, q, dtype, q.stride(0), Hq, scale or 1 / np.sqrt(D), rules, out,
                      out.stride(0), ls, ws, wsb, st, stream=stream)
     return out, ls, L.e0_read_status(st)
@@ -107,7 +133,7 @@ def check_scored(c, table, ctx, cu, q, out, lse, dtype, window=0, cap=0.0, slope
     slopes = None if slopes is None else np.asarray(slopes, np.float32).astype(np.float64)
     got, gl, qv = f64(out), f64(lse) if lse is not None else None, f64(q)
     rows = int(np.diff(cu).max()) * (Hq // c.H)
-    tiles = dtype != F32 and rows >= TILE_ROWS
+    tiles = dtype != F32 and (rows >= TILE_ROWS or Tables.room)
     werr, quantum = weights_of(dtype, tiles, dtype == BF16 and rows > 8, c.vs)
     for b in range(len(ctx)):
         at = slice(cu[b], cu[b + 1])
@@ -135,6 +161,7 @@ ALIBI = lambda Hq: 2.0 ** (-8.0 * np.arange(1, Hq + 1) / Hq)  # noqa: E731
 # ------------------------------------------------------------------ tiles: the plain case first
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("D", [128, 64, 256])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_prompt_of_one_tile(L, D, dtype):  # noqa: F811
@@ -147,6 +174,7 @@ def test_prompt_of_one_tile(L, D, dtype):  # noqa: F811
     check_scored(c, table, ctx, cu, q, out, lse, dtype)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("bs", [16, 128])
@@ -164,6 +192,7 @@ def test_prompts_of_many_lengths(L, D, dtype, bs):  # noqa: F811
     check_scored(c, table, ctx, cu, q, out, lse, dtype)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (4, 1), (24, 3), (20, 1), (7, 1), (40, 2)])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("window", [0, 1, 90])
@@ -181,6 +210,7 @@ def test_prompts_heads_and_windows(L, Hq, Hkv, dtype, window):  # noqa: F811
 # ------------------------------------------------------------------ rules, for single tokens and for prompts
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("new", [[1, 1, 1, 1, 1], [3, 0, 2, 1, 4], [40, 1, 130, 66, 0]])
@@ -197,6 +227,7 @@ def test_capped_and_biased_scores(L, D, dtype, new, rule):  # noqa: F811
     check_scored(c, table, ctx, cu, q, out, lse, dtype, **kw)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("long", [False, True])
@@ -222,6 +253,7 @@ def test_documents_and_open_prefixes(L, D, dtype, long):  # noqa: F811
         check_scored(c, table, ctx, cu, q, out, lse, dtype, **kw)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 1), (64, 4, 2), (256, 2, 1)])
 def test_long_contexts_cut_among_blocks(L, D, Hq, Hkv, dtype):  # noqa: F811
@@ -250,6 +282,7 @@ def test_no_rules_is_plain_attention(L):  # noqa: F811
         assert st == 0 and torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_tiles_of_far_scales_and_large_scores(L, dtype):  # noqa: F811
     """Value scales 2^40 apart, scores of hundreds that grow along the context, queries of any size."""
@@ -266,6 +299,7 @@ def test_tiles_of_far_scales_and_large_scores(L, dtype):  # noqa: F811
     check_scored(c, table, ctx, [0, n], q, out, lse, dtype)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [1, 90])
 def test_non_finite_queries_and_codes_that_nobody_sees(L, n):  # noqa: F811
     """A query's NaN stays in its row; NaN codes behind a row's position or before its document do not reach it."""
@@ -290,6 +324,7 @@ def test_non_finite_queries_and_codes_that_nobody_sees(L, n):  # noqa: F811
     assert torch.equal(out[:n][keep], ref[:n][keep]) and torch.equal(lse[:n][keep], rl[:n][keep])
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [2, 100])
 def test_bad_lengths_and_blocks(L, n):  # noqa: F811
     rng = np.random.default_rng(4)
@@ -313,6 +348,7 @@ def test_bad_lengths_and_blocks(L, n):  # noqa: F811
     check_scored(c, table, ctx[:1], cu[:2], q[:n], out[:n], lse[:n], F16)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_strided_queries_and_unaligned_outputs(L, D):  # noqa: F811
     """Queries inside a projection's rows, outputs at odd addresses and strides, no lse."""
@@ -332,6 +368,7 @@ def test_strided_queries_and_unaligned_outputs(L, D):  # noqa: F811
         assert (buf[mask] == -7).all()
 
 
+@pytest.mark.usefixtures("room")
 def test_many_sequences_of_prompts(L):  # noqa: F811
     rng = np.random.default_rng(6)
     B = 1100
@@ -364,7 +401,8 @@ def shared(L, desc, Hkv, ptable, P, table, ctx, cu, q, dtype, window=0, cap=0.0,
     ws = torch.full((wsb,), 255, dtype=torch.uint8, device="cuda")
     st = status()
     pl = dev(np.array([P], np.int32)) if plen is None else plen
-    L.e0_attn_shared(desc, dev(np.asarray(ptable, np.int32)), len(ptable), pl, dev(np.asarray(table, np.int32)),
+    ptable = Tables.widen(ptable, desc.block_tokens)[0]
+    L.e0_attn_shared(desc, dev(ptable), len(ptable), pl, dev(np.asarray(table, np.int32)),
                      np.asarray(table).shape[1], dev(np.asarray(ctx, np.int32)), dev(np.asarray(cu, np.int32)), B, T, max_q, q,
                      dtype, Hq * D, Hq, scale or 1 / np.sqrt(D), rules, out, Hq * D, ls, ws, wsb, st, stream=stream)
     return out, ls, L.e0_read_status(st)
@@ -404,6 +442,7 @@ def with_prefix(L, P, ctx, bs, Hkv, D, rng):  # noqa: F811
     return c, t, desc, np.maximum(front, -1), table[:-1]
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("D", [128, 64, 256])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("P", [1, 16, 100, 128, 129, 700])
@@ -422,6 +461,7 @@ def test_shared_prefix(L, D, dtype, P):  # noqa: F811
         check_shared(c, front, P, table, ctx, cu, q, out, lse, dtype)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("window", [0, 1, 40, 600])
 def test_shared_prefix_rules(L, dtype, window):  # noqa: F811
@@ -440,6 +480,7 @@ def test_shared_prefix_rules(L, dtype, window):  # noqa: F811
         check_shared(c, front, P, table, ctx, cu, q, out, lse, dtype, **kw)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_shared_long_prefix_and_equal_bits(L, dtype):  # noqa: F811
     rng = np.random.default_rng(7)
@@ -455,9 +496,10 @@ def test_shared_long_prefix_and_equal_bits(L, dtype):  # noqa: F811
     assert torch.equal(out, again) and torch.equal(lse, l2)
 
 
+@pytest.mark.usefixtures("room")
 def test_shared_prefix_of_nothing_and_bad_lengths(L):  # noqa: F811
     rng = np.random.default_rng(8)
-    B, Hq, Hkv, D, P = 20, 4, 1, 64, 50
+    B, Hq, Hkv, D, P = 40, 4, 1, 64, 50
     ctx = [int(x) for x in rng.integers(1, 60, B)]
     cu = np.arange(B + 1)
     c, t, desc, front, table = with_prefix(L, P, ctx, 16, Hkv, D, rng)
@@ -466,7 +508,7 @@ def test_shared_prefix_of_nothing_and_bad_lengths(L):  # noqa: F811
         none, lse, st = shared(L, desc, Hkv, front, 0, table, ctx, cu, q, dtype)
         assert st == 0
         check_shared(c, front, 0, table, ctx, cu, q, none, lse, dtype)
-        for bad in (-1, len(front) * 16 + 1, 2 ** 31 - 1):
+        for bad in (-1, len(Tables.widen(front, 16)[0]) * 16 + 1, 2 ** 31 - 1):
             out, lse, st = shared(L, desc, Hkv, front, bad, table, ctx, cu, q, dtype)
             assert st == L.E0_ST_BAD_LENGTH and torch.equal(out, none)
         holes = front.copy()
