@@ -21,7 +21,13 @@ namespace {
 //     their logits; a bin of very many members is divided by all blocks.  What is left are
 //     some tokens, or equal ones, whose order is that of the tokens.
 // The draw then needs no order: the first token, by number, whose running sum of kept
-// weights exceeds u times their total.
+// weights exceeds u times their total.  Each block's sum is in its histogram already unless
+// min-p takes from it, and only the block of the draw looks for its place (all blocks adding up
+// once more: 92 us for 85 below).
+// 64 rows of 131071 fp32 logits, top-p 0.9: 85 us, two turns of 38 clusters of 13 us for the
+// histogram (three additions in shared memory a token), 5 for the reading (of the 5 us in which
+// memory alone could be read), 12 for meetings and searches, 8 for the draw.  Read from the L2
+// cache in each pass instead of held, all rows would run at once, and take 98 us.
 //
 // A draw over V tokens has V borders, and an error in the sums moves all of them: with fp32
 // exponentials one row in a hundred would get another token than the definition gives.
@@ -73,8 +79,9 @@ struct SampleSmem {
     uint32_t count[BINS], low[BINS], high[BINS];  // of this block's share of the row; a sum of weights is high : low
     u64 few[FEW];                                 // order : token of the last bin's members (the first block's)
     u64 few_w[FEW];
+    u64 mine[FEW];                                // this block's own of them
     int2 steps[STEPS_OF_ONE];
-    uint32_t n_few;
+    uint32_t n_few, n_mine, mine_at;
     uint32_t sub, sub_count;
     u64 sub_mass;
     uint32_t n_sub;
@@ -139,7 +146,6 @@ struct Scale {
 
 // y of a logit (>= 0) as fp32, monotone in the logit; and the exact one's rest.
 E0_DEV float y_of(const Scale& s, float x) { return (s.most - x) * s.ch; }
-
 
 // 2^(-i / STEPS_OF_ONE), times 2^30, from the power series at compile time.
 struct Steps {
@@ -246,6 +252,10 @@ struct Row {
     uint32_t rank, blocks;
     Scale sc;
     float per_unit;  // bins of a unit of y: the first 16 units of y are looked at alone, or all of them
+    // this block's share of what `find` found, where its histogram of weights says it
+    bool known;
+    uint32_t own_count, own_members;
+    u64 own_mass;
 
     // Counts, and sums where they are wanted, of this block's tokens by bin (`bin_of` gives
     // BINS for none).  told[1]: every block's tokens in bins, and the sum of their weights, or of
@@ -377,21 +387,30 @@ struct Row {
         meet();
     }
 
-    // The tokens with `in(logit)` go to the first block, in any order.
+    // The tokens with `in(logit)`, FEW in all at most, go to the first block, in any order: each block's
+    // together, for an addition in another block's memory takes a microsecond to answer.  n_few and
+    // n_mine are 0.  Returns how many are this block's, in S.mine.
     template <typename F>
-    E0_DEV void gather(F in) {
-        if (threadIdx.x == 0) S.n_few = 0;
-        meet();
+    E0_DEV uint32_t gather(F in) {
 #pragma unroll 4
         for (int i = threadIdx.x; i < n; i += SM_THREADS)
             if (in(x[i])) {
-                const uint32_t at = add_to(of_block(&S.n_few, 0), 1u);
-                if (at < FEW) {
-                    put(of_block(&S.few[at], 0), ((u64)order_of(x[i]) << 32) | (uint32_t)~(from + i));  // larger is earlier
-                    put(of_block(&S.few_w[at], 0), weight_of(sc, x[i]));
-                }
+                const uint32_t at = atomicAdd(&S.n_mine, 1u);
+                if (at < FEW) S.mine[at] = ((u64)order_of(x[i]) << 32) | (uint32_t)~(from + i);  // larger is earlier
             }
+        __syncthreads();
+        const uint32_t m = min(S.n_mine, (uint32_t)FEW);
+        if (threadIdx.x == 0) S.mine_at = m ? add_to(of_block(&S.n_few, 0), m) : 0;
+        __syncthreads();
+        if (threadIdx.x == 0) S.n_mine = 0;
+        const uint32_t at = S.mine_at + threadIdx.x;
+        if (threadIdx.x < m && at < FEW) {
+            const u64 me = S.mine[threadIdx.x];
+            put(of_block(&S.few[at], 0), me);
+            put(of_block(&S.few_w[at], 0), weight_of(sc, logit_of((uint32_t)(me >> 32))));
+        }
         meet();
+        return m;
     }
 
     // The first block: of the m tokens in S.few, after count0 others of sum mass0, the one with
@@ -466,8 +485,11 @@ struct Row {
     // the one with which the count reaches want_n or the sum want_w.  One block takes them.
     template <typename F>
     E0_DEV End among_few(F in, bool by_count, uint32_t want_n, u64 want_w, uint32_t count0, u64 mass0) {
-        gather(in);
-        if (rank == 0) pick(min((int)S.n_few, FEW), by_count, want_n, want_w, count0, mass0);
+        own_members = gather(in);
+        if (rank == 0) {
+            pick(min((int)S.n_few, FEW), by_count, want_n, want_w, count0, mass0);
+            if (threadIdx.x == 0) S.n_few = 0;
+        }
         meet();
         return {S.told.key, S.told.index, S.told.count_through, S.told.mass_through};
     }
@@ -500,13 +522,28 @@ struct Row {
 
     // The end of the kept tokens: the token with which their count reaches want_n, or
     // their sum want_w (> 0, at most the row's).  find_bin has found its bin by weight.
-    E0_DEV End find(bool by_count, uint32_t want_n, u64 want_w) {
+    E0_DEV End find(bool by_count, uint32_t want_n, u64 want_w, bool sums) {
         uint32_t bin = S.told.bin, members = S.told.members, count0 = S.told.count_before;
         u64 mass0 = S.told.mass_before;
         const Scale s = sc;
         const float per = per_unit;
         const auto in_first = [s, per, bin](float v) { return weight_bin(s, per, v) == bin; };
-        if (members <= FEW) return among_few(in_first, by_count, want_n, want_w, count0, mass0);
+        known = sums && members <= FEW;
+        if (members <= FEW) {
+            // the bins before, and the bin's own members up to the end
+            uint32_t c = 0;
+            u64 m = 0;
+            for (int b = threadIdx.x; known && b < (int)bin; b += SM_THREADS) c += S.count[b], m += ((u64)S.high[b] << 32) + S.low[b];
+            const End end = among_few(in_first, by_count, want_n, want_w, count0, mass0);
+            if (!known) return end;
+            if (threadIdx.x < own_members) {
+                const u64 me = S.mine[threadIdx.x];
+                if (end.holds((uint32_t)(me >> 32), ~(uint32_t)me)) ++c, m += weight_of(sc, logit_of((uint32_t)(me >> 32)));
+            }
+            const Before own = block_before(S, c, m);
+            own_count = own.all_count, own_mass = own.all_sum;
+            return end;
+        }
         // many: by the bits of their orders
         uint32_t lo = 0xFFFFFFFFu, hi = 0;
         for (int i = threadIdx.x; i < n; i += SM_THREADS)
@@ -569,7 +606,7 @@ E0_DEV void put_token(const SampleArgs& A, int row, int token, uint32_t kept, u6
 }
 
 template <int TY>
-__global__ void __launch_bounds__(SM_THREADS) k_sample(SampleArgs A) {
+__global__ void __launch_bounds__(SM_THREADS, 2) k_sample(SampleArgs A) {
     typedef typename Elem<TY>::T T;
     extern __shared__ __align__(16) char sample_sm[];
     SampleSmem& S = *reinterpret_cast<SampleSmem*>(sample_sm);
@@ -587,6 +624,7 @@ __global__ void __launch_bounds__(SM_THREADS) k_sample(SampleArgs A) {
         S.ch = (float)c, S.cl = (float)(c - (double)S.ch);
         S.least = min_p > 0.f ? (u64)((double)fminf(min_p, 1.f) * 17592186044416.0) : 0;  // 2^44
     }
+    if (tid == 0) S.n_few = S.n_mine = 0;
     if (tid < STEPS_OF_ONE) S.steps[tid] = make_int2(STEPS.at[tid], __float_as_int((float)STEPS.at[tid]));
     for (int i = tid; i < BINS; i += SM_THREADS) S.count[i] = S.low[i] = S.high[i] = 0;  // for the first histogram
     // ---- the row's share, its largest logit
@@ -647,7 +685,7 @@ __global__ void __launch_bounds__(SM_THREADS) k_sample(SampleArgs A) {
         }
         return;  // every block of the row leaves here, and none reads another's memory after the meeting
     }
-    Row R = {S, x, n, from, rank, blocks, {most, S.ch, S.cl, S.steps}, Row::NEAR};
+    Row R = {S, x, n, from, rank, blocks, {most, S.ch, S.cl, S.steps}, Row::NEAR, false, 0, 0, 0};
     // ---- the end of what top-k and top-p keep
     End end = {0, 0xFFFFFFFFu, 0, 0};
     const bool by_k = top_k > 0 && top_k < A.V, by_p = top_p < 1.f;
@@ -714,22 +752,22 @@ __global__ void __launch_bounds__(SM_THREADS) k_sample(SampleArgs A) {
             if (run <= want && want < run + w) put_token(A, row, (int)id, count, w, total);
             return;
         }
-        if (cut) {
-            end = R.find(true, top_k, 0);
+        // of top-k, then of top-p within these
+#pragma unroll 1
+        for (bool by_count = cut; by_count || by_p;) {
+            end = R.find(by_count, top_k, wanted(m), !by_count && S.least == 0);
+            if (!by_count || !by_p) break;
+            by_count = false;
             m = end.mass;
-            if (by_p) {
-                // within these; their sum may end in another bin
-                R.per_unit = Row::NEAR;
+            R.per_unit = Row::NEAR;
+            R.histogram(bin_of, true, false);
+            R.find_bin(false, 0, wanted(m), 0, 0);
+            if (S.told.members == 0) {  // their sum ends in another bin
+                R.per_unit = Row::FAR;
                 R.histogram(bin_of, true, false);
                 R.find_bin(false, 0, wanted(m), 0, 0);
-                if (S.told.members == 0) {
-                    R.per_unit = Row::FAR;
-                    R.histogram(bin_of, true, false);
-                    R.find_bin(false, 0, wanted(m), 0, 0);
-                }
             }
         }
-        if (by_p) end = R.find(false, 0, wanted(m));
     }
     // ---- sums of the kept tokens' weights: a warp has consecutive tokens
     const int per = (n + SM_THREADS - 1) / SM_THREADS * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
@@ -743,47 +781,52 @@ __global__ void __launch_bounds__(SM_THREADS) k_sample(SampleArgs A) {
         w = weight_of(R.sc, v);
         return w >= least;
     };
-    u64 sum = 0;
-    uint32_t count = 0;
-    for (int ib = i0; ib < i1; ib += BATCH * 32) {
-        float v[BATCH];
-        bool in[BATCH], any = false;
+    u64 all = R.own_mass, before = 0, total = 0, want = 0;
+    uint32_t total_count = R.own_count;
+    // Where the histogram has said what the block has of them, only the block of the draw adds them up.
+#pragma unroll 1
+    for (bool here = false;;) {
+        if (here || !R.known) {
+            u64 sum = 0;
+            uint32_t count = 0;
+            for (int ib = i0; ib < i1; ib += BATCH * 32) {
+                float v[BATCH];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int i = ib + 32 * k + lane;
-            v[k] = i < i1 ? x[i] : -INFINITY;
-            in[k] = v[k] >= lowest && end.holds(order_of(v[k]), from + i);
-            any |= in[k];
-        }
-        if (!__any_sync(0xffffffffu, any)) continue;
+                for (int k = 0; k < BATCH; ++k) {
+                    const int i = ib + 32 * k + lane;
+                    v[k] = i < i1 ? x[i] : -INFINITY;
+                }
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const u64 w = weight_of(R.sc, v[k]);
-            if (in[k] && w >= least) sum += w, ++count;
+                for (int k = 0; k < BATCH; ++k) {
+                    if (!__any_sync(0xffffffffu, v[k] >= lowest)) continue;
+                    const u64 w = weight_of(R.sc, v[k]);
+                    if (v[k] >= lowest && end.holds(order_of(v[k]), from + ib + 32 * k + lane) && w >= least) sum += w, ++count;
+                }
+            }
+            sum = warp_total(sum), count = warp_total(count);
+            __syncthreads();
+            if (lane == 0) S.wsum[warp] = sum, S.wcount[warp] = count;
+            __syncthreads();
+            if (here) break;
+            for (int w = 0; w < SM_WARPS; ++w) all += S.wsum[w], total_count += S.wcount[w];
         }
+        if (tid < blocks) {
+            put(of_block(&S.told.mass[0][rank], tid), all);
+            put(of_block(&S.told.count[0][rank], tid), total_count);
+        }
+        meet();  // the last one: each block goes on with its own memory
+        total_count = 0;
+        for (uint32_t r = 0; r < blocks; ++r) {
+            if (r == rank) before = total;
+            total += S.told.mass[0][r], total_count += S.told.count[0][r];
+        }
+        // the first token whose running sum exceeds u * total
+        want = u < 1.f ? __umul64hi(fraction_of(u), total) : total;
+        if (want >= total) want = total - 1;
+        if (want < before || want >= before + all) return;
+        if (!R.known) break;
+        here = true;
     }
-    sum = warp_total(sum), count = warp_total(count);
-    __syncthreads();
-    if (lane == 0) S.wsum[warp] = sum, S.wcount[warp] = count;
-    __syncthreads();
-    u64 all = 0, before = 0;
-    uint32_t total_count = 0;
-    for (int w = 0; w < SM_WARPS; ++w) all += S.wsum[w], total_count += S.wcount[w];
-    if (tid < blocks) {
-        put(of_block(&S.told.mass[0][rank], tid), all);
-        put(of_block(&S.told.count[0][rank], tid), total_count);
-    }
-    meet();  // the last one: each block goes on with its own memory
-    u64 total = 0;
-    total_count = 0;
-    for (uint32_t r = 0; r < blocks; ++r) {
-        if (r == rank) before = total;
-        total += S.told.mass[0][r], total_count += S.told.count[0][r];
-    }
-    // the first token whose running sum exceeds u * total
-    u64 want = u < 1.f ? __umul64hi(fraction_of(u), total) : total;
-    if (want >= total) want = total - 1;
-    if (want < before || want >= before + all) return;
     int at = 0;  // the warp whose tokens it is among
     while (want >= before + S.wsum[at]) before += S.wsum[at++];
     // the block shares that warp's tokens, consecutive ones a thread
@@ -818,8 +861,7 @@ int launch(SampleArgs a, int T, cudaStream_t s) {
     const size_t most = sizeof(SampleSmem) + (size_t)(E0_MAX_VOCAB / MOST_BLOCKS) * sizeof(float);
     if (!allow_smem((const void*)k_sample<TY>, most, asked)) return E0_ERR_CUDA;
     // Blocks of a row: shares of 2048 tokens and less while there are more blocks to have (one row
-    // of 32000: 13.7 us with eight, 15.5 with four, 23 with two, 32 with one; 64 of 131071: 92 with
-    // eight, 102 with four).
+    // of 32000: 13.6 us with eight, 15.5 with four, 23 with two, 32 with one).
     int blocks = 1;
     while (blocks < MOST_BLOCKS && (a.V + blocks - 1) / blocks > 2048) blocks *= 2;
     a.slice = ((a.V + blocks - 1) / blocks + 7) / 8 * 8;

@@ -231,6 +231,7 @@ def test_draws_by_all_rules(L, V, dtype):  # noqa: F811
     check_draw(L, x, u, dtype, top_k=rng.integers(-1, 60, T))
     check_draw(L, x, u, dtype, top_p=rng.random(T) * 1.1)
     check_draw(L, x, u, dtype, min_p=rng.random(T) * 0.2 - 0.02)
+    check_draw(L, x, u, dtype, top_k=rng.integers(1, max(2, V), T), top_p=0.3 + 0.69 * rng.random(T))
     got, kept = check_draw(L, x, u, dtype, temperature=0.5 + rng.random(T), top_k=rng.integers(1, max(2, V), T),
                            top_p=0.5 + 0.5 * rng.random(T), min_p=rng.random(T) ** 3 * 0.1)
     assert (got >= 0).all() and (got < V).all() and (kept >= 1).all()
