@@ -36,7 +36,16 @@ struct Geo {
     static constexpr int STAGES = D == 64 ? 3 : 2;
     static constexpr int OPERAND = KV * D * 2;
     static constexpr int SOFT = 4 * HALVES;  // softmax warps
-    static constexpr int THREADS = (SOFT + 4 + 4) * 32;  // and the converting ones; of the last four, one issues the products
+    static constexpr int OPS = HALVES == 2 ? 2 : 1;  // operands of a converting warp: keys and values, or one of them
+    static constexpr int TURN = 8 / OPS;             // converting warps
+    static constexpr int THREADS = (SOFT + TURN + 4) * 32;  // of the last four, one issues the products
+    // Registers of a softmax, a converting and another thread: together what was launched, 512 x 128.
+    // With heads of 256, whose softmax has four warps, there is room for eight converting ones (20
+    // times two queries over 6000 positions: 56 us with four, 52 with eight); with others it would be
+    // 640 threads of 96, and softmax's and the operands' registers in local memory (4096 tokens of
+    // documents: 113 us with four, 126 with eight).
+    static constexpr int SOFT_REGS = HALVES == 2 ? 168 : 208, TURN_REGS = HALVES == 2 ? 112 : 88, OTHER_REGS = HALVES == 2 ? 64 : 128;
+    static_assert(32 * (SOFT * SOFT_REGS + TURN * TURN_REGS + 4 * OTHER_REGS) == THREADS * 128 && THREADS == 512, "all of them come");
     static constexpr int O_COL = 2 * KV;  // tensor memory: two S, then the halves' O
     static constexpr int Q_BYTES = 128 * D * 2;             // of a half
     static constexpr int Q_BUFS = D == 256 ? 1 : 3;         // halves' Q in shared memory
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         S.abort = 0;
         mbar_fence_init();
     }
-    if (warp == G_::SOFT + 4) tmem_alloc(&S.tmem, TILE_TMEM);
+    if (warp == G_::SOFT + G_::TURN) tmem_alloc(&S.tmem, TILE_TMEM);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -555,10 +564,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
     }
     Pieces pieces(A, S.jobs);
 
-    // 512 threads are launched with 128 registers each; a softmax thread wants more, the others
-    // less: 256 x 168 + 128 x 112 + 128 x 64 = 512 x 128.  (384 threads have 168 each.)
     if (warp < G_::SOFT) {
-        if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G_::SOFT_REGS));
         // ---------------- softmax: a thread a row, half h of the tile
         const int h = warp >> 2, t = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -816,11 +823,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         }
         if (!ok && lane == 0) give_up();
         if (threadIdx.x == 0) A.cuts[2 * blockIdx.x] = begun, A.cuts[2 * blockIdx.x + 1] = went_on;
-    } else if (warp < G_::SOFT + 4) {
-        if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-        // ---------------- codes into operands: block ids are read two units ahead, codes and
-        // scales one
-        const int cw = warp - G_::SOFT, bs = 1 << A.a.shift;
+    } else if (warp < G_::SOFT + G_::TURN) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G_::TURN_REGS));
+        // ---------------- codes into operands, four warps an operand: block ids are read two units
+        // ahead, codes and scales one
+        const int cw = (warp - G_::SOFT) & 3, bs = 1 << A.a.shift;
+        constexpr int OPS = G_::OPS;
+        const int op0 = OPS == 2 ? 0 : (warp - G_::SOFT) >> 2;  // 0: keys (first), 1: values
         constexpr int L = G_::LOADS, PER = D / 64;  // loads; of 64 bytes a group of 8 tokens
         constexpr uint32_t NOWHERE = 0xFFFFFFFFu;
         struct Unit {
@@ -884,44 +893,42 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             }
         };
         Unit now, next, after;
-        uint4 kr[L], vr[L];
+        uint4 r[OPS][L];
         float ks, vs, ks1, vs1;
         bool have = look_up(now), have1 = look_up(next), ok = true;
         if (have) {
             look_in(now, ks, vs);
-            load(now, A.a.k, kr);
-            load(now, A.a.v, vr);
+#pragma unroll
+            for (int o = 0; o < OPS; ++o) load(now, op0 + o ? A.a.v : A.a.k, r[o]);
         }
         for (uint32_t g = 0; have; ++g) {
             const uint32_t st = g % STAGES, par = ((g / STAGES) + 1) & 1;
             const bool have2 = look_up(after);
             if (have1) look_in(next, ks1, vs1);
-            ok = __all_sync(0xffffffffu, arrived(&S.k_empty[st], par, abort));
-            if (!ok) break;
-            store(kr, S.k[st], false);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.k_full[st]);
-            if (have1) load(next, A.a.k, kr);
-            ok = __all_sync(0xffffffffu, arrived(&S.v_empty[st], par, abort));
-            if (!ok) break;
-            if (cw == 0 && lane < KV / 16) {
-                const float v = fmaxf(vs, LEAST_SCALE);
-                S.sc[st][lane] = now.at != NOWHERE ? make_float4(ks, log2f(v), SUM_UNIT / v, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int o = 0; o < OPS; ++o) {
+                const bool values = op0 + o > 0;
+                ok = __all_sync(0xffffffffu, arrived(values ? &S.v_empty[st] : &S.k_empty[st], par, abort));
+                if (!ok) break;
+                if (values && cw == 0 && lane < KV / 16) {
+                    const float v = fmaxf(vs, LEAST_SCALE);
+                    S.sc[st][lane] = now.at != NOWHERE ? make_float4(ks, log2f(v), SUM_UNIT / v, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                store(r[o], values ? S.v[st] : S.k[st], values && now.edge);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(values ? &S.v_full[st] : &S.k_full[st]);
+                if (have1) load(next, values ? A.a.v : A.a.k, r[o]);
             }
-            store(vr, S.v[st], now.edge);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.v_full[st]);
-            if (have1) load(next, A.a.v, vr);
+            if (!ok) break;
             now = next, next = after, ks = ks1, vs = vs1;
             have = have1, have1 = have2;
         }
         if (!ok && lane == 0) give_up();
     } else {
         // ---------------- products: the warp follows the schedule together, one lane issues
-        if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == G_::SOFT + 4) {
+        if constexpr (G_::OTHER_REGS < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G_::OTHER_REGS));
+        if (warp == G_::SOFT + G_::TURN) {
             const uint32_t id_s = idesc_f16_f32(128, KV), id_o = idesc_f16_f32(128, D) | B_MN_MAJOR;
             // the operands' addresses, the low words of their descriptors: 16-byte units
             const uint32_t q_lo = desc_low(smem_u32(S.q), 128), k_lo = desc_low(smem_u32(S.k), 128), v_lo = desc_low(smem_u32(S.v), 16 * D);
@@ -1014,7 +1021,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             // ---------------- Q: a warp eight rows at a time, a lane 16 bytes of every 64 of row lane % 8.
             // All of a warp's rows are copied to their places first, so that one latency is waited for, then
             // looked at and, bf16, turned into fp16 there.
-            const int g0 = warp - G_::SOFT - 5;
+            const int g0 = warp - G_::SOFT - G_::TURN - 1;
             constexpr int C = D / 32;
             uint32_t nq = 0;
             bool ok = true;
@@ -1087,7 +1094,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == G_::SOFT + 4) {
+    if (warp == G_::SOFT + G_::TURN) {
         tc_fence_after();
         tmem_dealloc(tmem, TILE_TMEM);
     }
