@@ -5,9 +5,13 @@
 namespace e0 {
 namespace {
 
-// Whether the rows can go through the tensor cores' tiles: enough of a KV head to fill a part of
-// one (their products in fp16 are not enough for fp32 outputs).
-bool has_tiles(int dtype, int64_t rows) { return dtype != E0_F32 && rows >= 64; }
+// Whether B times max_q queries of D can go through the tensor cores' tiles: enough rows of a KV head to
+// fill a part of one (their products in fp16 are not enough for fp32 outputs), and a list of the
+// tiles that might be that takes 256 MB at most.
+bool has_tiles(int dtype, int64_t B, int64_t max_q, int64_t G, int D) {
+    const int64_t rows = max_q * G, tile = D == 256 ? 128 : 256;
+    return dtype != E0_F32 && rows >= 64 && B * ((rows + tile - 1) / tile) <= 1 << 22;
+}
 
 // Whether they do: the tiles' kernels take 17 to 25 us before a first product counts, the one
 // for few rows 8 us and then 1 us for every 160 thousand pairs of a row and a position in fp16 with
@@ -15,11 +19,11 @@ bool has_tiles(int dtype, int64_t rows) { return dtype != E0_F32 && rows >= 64; 
 // heads on 2 (us, few rows / tiles; fp16, heads of 128): 200 queries behind 1000 tokens 14.8 / 29.6, 600
 // queries alone 31.2 / 31.7, four times 600 85 / 36, 1500 behind 500 153 / 40.  The host knows what a
 // sequence can hold, not what it does: no more than 8192 positions are counted on.
-bool by_tiles(const AttnArgs& a, int dtype, int64_t rows, int64_t queries, int64_t pairs_worth) {
-    if (!has_tiles(dtype, rows)) return false;
+bool by_tiles(const AttnArgs& a, int dtype, int64_t pairs_worth) {
+    if (!has_tiles(dtype, a.B, a.max_q, a.Hq / a.Hkv, a.D)) return false;
     int64_t seen = (int64_t)a.max_blocks << a.shift;
     if (a.window > 0 && !a.at) seen = seen < (int64_t)a.window + a.max_q ? seen : (int64_t)a.window + a.max_q;
-    return queries * a.Hq * (seen < 8192 ? seen : 8192) >= pairs_worth;
+    return (int64_t)a.B * a.max_q * a.Hq * (seen < 8192 ? seen : 8192) >= pairs_worth;
 }
 
 int64_t prompt_pairs(int dtype, int D) {
@@ -33,7 +37,9 @@ void put_rules(AttnArgs& a, const e0_attn_rules* r) {
     if (!r) return;
     a.window = r->window, a.slopes = r->slopes, a.first = r->first, a.open = r->open_len;
     if (r->cap > 0.f) {
-        a.cap = r->cap * LOG2E;
+        // between 2^-120 and 2^120 neither the cap nor its inverse leaves fp32's range; beyond, no score that fp32
+        // holds beside others knows the difference
+        a.cap = fminf(fmaxf(r->cap, 0x1p-120f), 0x1p120f) * LOG2E;
         a.inv_cap = 1.f / a.cap;
     }
 }
@@ -86,7 +92,7 @@ size_t parts_bytes(int T, int Hq, int D) {  // a normed fp32 result and its lse
 
 size_t attn_scored_ws_bytes(int B, int Hq, int Hkv, int D, int max_q) {
     const size_t few = attn_ws_bytes(D), many = attn_tile_ws_bytes(B, max_q, Hq / Hkv, D);
-    return has_tiles(E0_F16, (int64_t)max_q * (Hq / Hkv)) && many > few ? many : few;
+    return has_tiles(E0_F16, B, max_q, Hq / Hkv, D) && many > few ? many : few;
 }
 
 int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, const int32_t* ctx, const int32_t* cu, int B,
@@ -94,14 +100,13 @@ int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
                 void* out, int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
     AttnArgs a = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, lse, ws, st);
     put_rules(a, rules);
-    if (by_tiles(a, dtype, (int64_t)max_q * (Hq / c->Hkv), (int64_t)B * max_q, prompt_pairs(dtype, c->D)))
-        return attn_tile(a, nullptr, dtype, ws, s);
+    if (by_tiles(a, dtype, prompt_pairs(dtype, c->D))) return attn_tile(a, nullptr, dtype, ws, s);
     return launch_t<true>(a, dtype, c->D, s);
 }
 
 size_t attn_shared_ws_bytes(int B, int T, int Hq, int Hkv, int D, int max_q) {
     // the tiles' schedule is made while the sequences' own attention runs: a place for each
-    const size_t tiles = has_tiles(E0_F16, (int64_t)T * (Hq / Hkv)) ? attn_tile_ws_bytes(1, T, Hq / Hkv, D) : 0;
+    const size_t tiles = has_tiles(E0_F16, 1, T, Hq / Hkv, D) ? attn_tile_ws_bytes(1, T, Hq / Hkv, D) : 0;
     return up256((size_t)T * sizeof(int32_t)) + 256 + 2 * parts_bytes(T, Hq, D) + up256(attn_ws_bytes(D)) + tiles;
 }
 
@@ -135,7 +140,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
     // what the sequences have of their own comes first: the prefix' last kernel adds it where it can
     int rc = launch_t<true>(mine, dtype, c->D, s);
     if (rc != E0_OK) return rc;
-    if (by_tiles(front, dtype, (int64_t)T * (Hq / c->Hkv), T, PREFIX_PAIRS)) {
+    if (by_tiles(front, dtype, PREFIX_PAIRS)) {
         const TilePrefix prefix = {mine, at, o[1], l[1], attn_tile_merges(front)};
         if (prefix.merge) {
             front.lse = lse;

@@ -596,23 +596,21 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             // the number of this half's Q, of all that the block has had
             const uint32_t nq = n_q + (h && p.first(0) < p.end(0)), qb = nq % G_::Q_BUFS;
             n_q += (p.first(0) < p.end(0)) + (HALVES == 2 && p.first(1) < p.end(1));
-            if (kf < ke) {
-                ok = arrived(&S.q_full[qb], (nq / G_::Q_BUFS) & 1, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                f = S.qf[qb][t];
-                if (RULES && A.a.slopes && row_ok) slope = A.a.slopes[head] * LOG2E;
-            }
+            if (RULES && kf < ke && A.a.slopes && row_ok) slope = A.a.slopes[head] * LOG2E;
             // ---- units
             for (int k = kf; k < ke; ++k, ++n_s) {
                 const uint32_t g = gk + (uint32_t)(k - p.k0), st = g % STAGES;
                 const uint32_t slot = HALVES == 2 ? h : n_s & 1, use = HALVES == 2 ? n_s : n_s >> 1;
                 const uint32_t s_at = tmem + lanes + slot * KV;
+                // S first: a half without units in some pieces comes here well before the other, and
+                // its S alone says that the other barriers are in the phases that are asked for
                 ok = arrived(&S.s_full[slot], use & 1, abort) &&
-                     arrived(&S.v_full[st], (g / STAGES) & 1, abort);
+                     arrived(&S.v_full[st], (g / STAGES) & 1, abort) &&
+                     (k > kf || arrived(&S.q_full[qb], (nq / G_::Q_BUFS) & 1, abort));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
+                if (k == kf) f = S.qf[qb][t];
                 const int at0 = (J.unit0 + k) * KV;
                 bool edge = at0 < lo || at0 + KV > hi;
                 if (lane < KV / 16) edge |= !(S.sc[st][lane].w > 0.f);

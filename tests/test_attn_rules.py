@@ -36,9 +36,9 @@ def room(request):
     Tables.room = False
 
 
-def rules_ref(q, k, v, scale, p, seen, cap=0.0, slopes=None, weight_err=0.0, quantum=0.0):
+def rules_ref(q, k, v, scale, p, seen, cap=0.0, slopes=None, weight_err=0.0, quantum=0.0, more=0.0):
     """q [n][Hq][D] at the positions p, k and v [S][Hkv][D] (NaN: not there), seen [n][S].  Returns out, lse and what
-    they may be off by."""
+    they may be off by; `more`: of a score, beside its own."""
     n, Hq, D = q.shape
     G = Hq // k.shape[1]
     j = np.arange(len(k))
@@ -56,7 +56,7 @@ def rules_ref(q, k, v, scale, p, seen, cap=0.0, slopes=None, weight_err=0.0, qua
         s = q[:, h] @ kk.T * scale
         mag = np.abs(q[:, h]) @ np.abs(kk).T * abs(scale)
         # a score: D products of operands of 22 bits and more, summed in fp32, and factors of three roundings
-        off = (D + 16) * EPS * mag + 4 * EPS * np.abs(s)
+        off = (D + 16) * EPS * mag + (4 * EPS + more) * np.abs(s)
         if cap:
             s = cap * np.tanh(s / cap)
             off = off + 4 * EPS * cap  # the cap's own steps: an exponential, a division, two products
@@ -127,7 +127,8 @@ def scored(L, desc, Hkv, table, ctx, cu, q, dtype, window=0, cap=0.0, slopes=Non
     return out, ls, L.e0_read_status(st)
 
 
-def check_scored(c, table, ctx, cu, q, out, lse, dtype, window=0, cap=0.0, slopes=None, first=None, opens=None, scale=None):
+def check_scored(c, table, ctx, cu, q, out, lse, dtype, window=0, cap=0.0, slopes=None, first=None, opens=None, scale=None,
+                 more=0.0):
     T, Hq, D = q.shape
     scale = float(np.float32(scale or 1 / np.sqrt(D)))
     slopes = None if slopes is None else np.asarray(slopes, np.float32).astype(np.float64)
@@ -149,7 +150,7 @@ def check_scored(c, table, ctx, cu, q, out, lse, dtype, window=0, cap=0.0, slope
             seen = seen & (j[None, :] >= np.asarray(first)[at][:, None])
         if window:
             seen = seen & (j[None, :] > p[:, None] - window)
-        want = rules_ref(qv[at], k, v, scale, p, seen, cap, slopes, werr, quantum)
+        want = rules_ref(qv[at], k, v, scale, p, seen, cap, slopes, werr, quantum, more)
         compare(got[at], None if gl is None else gl[at], want, dtype, (b, n, ctx[b]))
     end = cu[-1]
     assert (got[end:] == -7).all() and (gl is None or (gl[end:] == -7).all())
@@ -271,6 +272,26 @@ def test_long_contexts_cut_among_blocks(L, D, Hq, Hkv, dtype):  # noqa: F811
         assert torch.equal(out, again)
 
 
+@pytest.mark.usefixtures("room")
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_caps_of_any_size(L, dtype):  # noqa: F811
+    """A cap that makes all scores alike, below fp32's normal numbers too, and one that no score comes near."""
+    rng = np.random.default_rng(11)
+    ctx, cu = [300, 90], np.array([0, 70, 140])
+    c, t, desc, table = filled_cache(L, 2, 16, 2, 64, ctx, rng)
+    q = dev(rng.standard_normal((140, 4, 64)) * 2, DT[dtype])
+    q[3] = 0
+    for cap in (1e-42, 1e-38, 1e-20):  # scores of that size: their weights are equal to 2^-60
+        out, lse, st = scored(L, desc, 2, table, ctx, cu, q, dtype, cap=cap)
+        assert st == 0
+        check_scored(c, table, ctx, cu, torch.zeros_like(q), out, lse, dtype)
+    for cap in (1e20, 3e38):  # s^3 / (3 cap^2) is less than 2^-100 of s = 1000
+        out, lse, st = scored(L, desc, 2, table, ctx, cu, q, dtype, cap=cap)
+        assert st == 0
+        # the score through the cap and back: a product with its inverse, the tangent's factor, a product with it
+        check_scored(c, table, ctx, cu, q, out, lse, dtype, more=4 * EPS)
+
+
 def test_no_rules_is_plain_attention(L):  # noqa: F811
     rng = np.random.default_rng(1)
     ctx, cu = [100, 1, 2000], [0, 1, 2, 3]
@@ -366,6 +387,30 @@ def test_strided_queries_and_unaligned_outputs(L, D):  # noqa: F811
         mask = torch.ones_like(buf, dtype=torch.bool)
         torch.as_strided(mask, (n, Hq, D), (Hq * D + 3, D, 1), 1).fill_(False)
         assert (buf[mask] == -7).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 16, 4), (64, 8, 2)])
+@pytest.mark.parametrize("open_part", [False, True])
+def test_short_last_tiles_between_long_prompts(L, D, Hq, Hkv, dtype, open_part):  # noqa: F811
+    """Tiles of which only the first half has rows, several heads of them before tiles of two halves: whoever works on
+    the second half is there early, and has to wait for its own queries."""
+    rng = np.random.default_rng(D + open_part)
+    new = [714, 33, 70, 1500, 10, 17, 918, 30, 800, 95, 954]
+    held = [774, 100, 0, 585, 745, 3, 632, 175, 0, 40, 859]
+    ctx = [a + b for a, b in zip(new, held)]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    c, t, desc, table = filled_cache(L, len(new), 32, Hkv, D, ctx, rng)
+    # queries of many sizes: each row's own factor counts
+    q = dev(rng.standard_normal((int(cu[-1]), Hq, D)) * 2.0 ** rng.integers(-6, 2, (int(cu[-1]), 1, 1)), DT[dtype])
+    kw = dict(opens=[int(0.4 * x) for x in ctx], cap=30.0) if open_part else {}
+    for _ in range(4):
+        out, lse, st = scored(L, desc, Hkv, table, ctx, cu, q, dtype, **kw)
+        assert st == 0
+        if _ == 0:
+            check_scored(c, table, ctx, cu, q, out, lse, dtype, **kw)
+            first = out, lse
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
 @pytest.mark.usefixtures("room")
