@@ -706,7 +706,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                 for (int w = 0; w < RW; ++w)
 #pragma unroll
                     for (int h = 0; h < 2 * SUBS; ++h) most = fmaxf(most, fmaxf(fabsf(p[w][h][0]), fabsf(p[w][h][1])));
-                const bool small = !__any_sync(0xffffffffu, !(most <= A.cap));
+                // (a score takes the form that its own size asks for, whatever stands beside it)
+                const bool some = __any_sync(0xffffffffu, most > A.cap);
 #pragma unroll
                 for (int w = 0; w < RW; ++w)
 #pragma unroll
@@ -714,7 +715,11 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float x = p[w][h][i];
-                            if (A.cap > 0.f) x = A.cap * (small ? tanh_below_1(x * A.inv_cap) : tanhf(x * A.inv_cap));
+                            if (A.cap > 0.f) {
+                                float th = tanh_below_1(x * A.inv_cap);
+                                if (some && fabsf(x) > A.cap) th = tanhf(x * A.inv_cap);
+                                x = A.cap * th;
+                            }
                             if (A.slopes) x = fmaf(-slope[w], fabsf((float)(place[w] - (pos + 8 * h + 2 * t4 + i))), x);
                             p[w][h][i] = x + sc[h / 2].y;
                         }

@@ -346,6 +346,44 @@ def test_non_finite_queries_and_codes_that_nobody_sees(L, n):  # noqa: F811
 
 
 @pytest.mark.usefixtures("room")
+@pytest.mark.parametrize("n", [1, 3, 90])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_capped_scores_know_nothing_of_one_another(L, n, dtype):  # noqa: F811
+    """Scores far beyond the cap in places that a row does not see, or in other rows, leave no trace in its bits; a
+    query's NaN stays NaN beside scores beyond the cap."""
+    rng = np.random.default_rng(n)
+    D, ctx, Hq = 64, [n + 50], 4
+    c, t, desc, table = filled_cache(L, 1, 16, 2, D, ctx, rng)
+    c.k[:] = R.encode(rng.standard_normal(c.k.shape) * 0.1)
+    c.ks[np.isnan(c.ks)] = c.vs[np.isnan(c.vs)] = 1.0
+    c.ks[:] = 1.0
+    t, desc = cache_dev(L, c)
+    q = dev(rng.standard_normal((n, Hq, D)), DT[dtype])
+    first = np.full(n, 20)
+    kw = dict(cap=4.0, first=first)
+    a, la, st = scored(L, desc, 2, table, ctx, [0, n], q, dtype, **kw)
+    assert st == 0
+    check_scored(c, table, ctx, [0, n], q, a, la, dtype, **kw)
+    blk, last = table[0, 1], table[0, (ctx[0] - 1) // 16]
+    c.k[blk, :, :4] = 0x7E  # positions 16 to 19: 448
+    if ctx[0] % 16:
+        c.k[last, :, ctx[0] % 16:] = 0x7E  # behind the last one
+    t2, desc2 = cache_dev(L, c)
+    b, lb, _ = scored(L, desc2, 2, table, ctx, [0, n], q, dtype, **kw)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    large = q.clone()
+    large[0, 1] *= 100  # its own scores are beyond the cap
+    b, lb, _ = scored(L, desc2, 2, table, ctx, [0, n], large, dtype, **kw)
+    keep = torch.ones((n, Hq), dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    assert torch.equal(a[:n][keep], b[:n][keep]) and torch.equal(la[:n][keep], lb[:n][keep])
+    large[0, 1, 3] = float("nan")
+    large[0, 0] *= 100
+    b, lb, _ = scored(L, desc2, 2, table, ctx, [0, n], large, dtype, **kw)
+    assert b[0, 1].isnan().all() and lb[0, 1].isnan() and b[0, 0].isfinite().all()
+
+
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("n", [2, 100])
 def test_bad_lengths_and_blocks(L, n):  # noqa: F811
     rng = np.random.default_rng(4)
