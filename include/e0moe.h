@@ -731,6 +731,8 @@ typedef struct e0_attn_rules {
                                 query sees (where its document begins)                      */
     const int32_t* open_len; /* device [B] or NULL: positions below it are seen by all
                                 queries of the sequence, earlier ones too (an open prefix)  */
+    int32_t rows;            /* > 0: cu_q gives no more rows than these in all; 0: B * max_q
+                                (says which kernel a call is worth, nothing else)           */
 } e0_attn_rules;
 
 /* Workspace of e0_attn_scored, as e0_attn_workspace_size's. */
@@ -743,12 +745,12 @@ size_t e0_attn_scored_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * arguments, queries that see nothing, rows after the last sequence's, conditions found on the
  * device, equal calls' bits.  A negative first[t] counts as 0, an open_len beyond the cached
  * tokens as all of them.  Where q is fp16 or bf16, max_q queries have 64 rows of a KV head and
- * more, and B, max_q, Hq and the table (with the window) leave room for some millions of scores,
- * the products run in tiles of 128 or 256 rows on the tensor cores: the weights are then rounded to
- * 11 bits (bf16) or 22 (fp16).  What max_q and max_blocks allow beyond the lengths thus has a say in
- * an output's last bits.  All else takes the path for few rows (every 8 of a KV head, 16 of bf16, read
- * the sequence once more).  rules NULL: none.  Errors as
- * e0_attn_decode's; cap negative or not finite, window < 0, or a pointer of the rules that
+ * more, an average sequence has 64 of the rows in all, and these, Hq and the table (with the
+ * window) leave room for some millions of scores, the products run in tiles of 128 or 256 rows on the
+ * tensor cores: the weights are then rounded to 11 bits (bf16) or 22 (fp16).  What max_q, max_blocks
+ * and rows allow beyond the lengths thus has a say in an output's last bits.  All else takes the path
+ * for few rows (every 8 of a KV head, 16 of bf16, read the sequence once more).  rules NULL: none.  Errors as
+ * e0_attn_decode's; cap negative or not finite, window < 0, rows < 0, or a pointer of the rules that
  * is not aligned to 4 bytes -> E0_ERR_ARG. */
 int e0_attn_scored(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
                    const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,

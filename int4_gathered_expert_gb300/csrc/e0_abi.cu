@@ -107,7 +107,7 @@ int check_attn(const e0_kv_cache* cache, const int32_t* block_table, int max_blo
 
 int check_rules(const e0_attn_rules* r) {
     if (!r) return E0_OK;
-    if (!(r->cap >= 0.f && r->cap <= FLT_MAX)) return E0_ERR_ARG;
+    if (!(r->cap >= 0.f && r->cap <= FLT_MAX) || r->rows < 0) return E0_ERR_ARG;
     return aligned(4, r->slopes, r->first, r->open_len) ? E0_OK : E0_ERR_ARG;
 }
 

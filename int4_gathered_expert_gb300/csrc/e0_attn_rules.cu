@@ -18,12 +18,14 @@ bool has_tiles(int dtype, int64_t B, int64_t max_q, int64_t G, int D) {
 // heads of 128 (a half of that with heads of 256, one and a half times as many in bf16).  Measured with 8
 // heads on 2 (us, few rows / tiles; fp16, heads of 128): 200 queries behind 1000 tokens 14.8 / 29.6, 600
 // queries alone 31.2 / 31.7, four times 600 85 / 36, 1500 behind 500 153 / 40.  The host knows what a
-// sequence can hold, not what it does: no more than 8192 positions are counted on.
-bool by_tiles(const AttnArgs& a, int dtype, int64_t pairs_worth) {
-    if (!has_tiles(dtype, a.B, a.max_q, a.Hq / a.Hkv, a.D)) return false;
+// sequence can hold, not what it does: no more than 8192 positions are counted on.  `rows`: of q in all,
+// at most (0: any); a decode step of a batch, where any one sequence might have all of them, is not for tiles.
+bool by_tiles(const AttnArgs& a, int dtype, int64_t pairs_worth, int64_t rows) {
+    const int64_t G = a.Hq / a.Hkv, all = (int64_t)a.B * a.max_q, queries = rows > 0 && rows < all ? rows : all;
+    if (!has_tiles(dtype, a.B, a.max_q, G, a.D) || queries * G < 64 * (int64_t)a.B) return false;
     int64_t seen = (int64_t)a.max_blocks << a.shift;
     if (a.window > 0 && !a.at) seen = seen < (int64_t)a.window + a.max_q ? seen : (int64_t)a.window + a.max_q;
-    return (int64_t)a.B * a.max_q * a.Hq * (seen < 8192 ? seen : 8192) >= pairs_worth;
+    return queries * a.Hq * (seen < 8192 ? seen : 8192) >= pairs_worth;
 }
 
 int64_t prompt_pairs(int dtype, int D) {
@@ -100,7 +102,7 @@ int attn_scored(const e0_kv_cache* c, const int32_t* table, int max_blocks, cons
                 void* out, int64_t out_ld, float* lse, void* ws, uint32_t* st, cudaStream_t s) {
     AttnArgs a = args_of(c, table, max_blocks, ctx, cu, B, max_q, q, q_ld, Hq, scale, 0, out, out_ld, lse, ws, st);
     put_rules(a, rules);
-    if (by_tiles(a, dtype, prompt_pairs(dtype, c->D))) return attn_tile(a, nullptr, dtype, ws, s);
+    if (by_tiles(a, dtype, prompt_pairs(dtype, c->D), rules ? rules->rows : 0)) return attn_tile(a, nullptr, dtype, ws, s);
     return launch_t<true>(a, dtype, c->D, s);
 }
 
@@ -140,7 +142,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
     // what the sequences have of their own comes first: the prefix' last kernel adds it where it can
     int rc = launch_t<true>(mine, dtype, c->D, s);
     if (rc != E0_OK) return rc;
-    if (by_tiles(front, dtype, PREFIX_PAIRS)) {
+    if (by_tiles(front, dtype, PREFIX_PAIRS, 0)) {
         const TilePrefix prefix = {mine, at, o[1], l[1], attn_tile_merges(front)};
         if (prefix.merge) {
             front.lse = lse;

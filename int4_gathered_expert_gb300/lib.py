@@ -84,7 +84,7 @@ class KvState(C.Structure):
 
 
 class AttnRules(C.Structure):
-    _fields_ = [("cap", C.c_float), ("window", i32), ("slopes", vp), ("first", vp), ("open_len", vp)]
+    _fields_ = [("cap", C.c_float), ("window", i32), ("slopes", vp), ("first", vp), ("open_len", vp), ("rows", i32)]
 
 
 class Rope(C.Structure):

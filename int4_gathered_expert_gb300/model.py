@@ -377,9 +377,10 @@ class KvCacheDev:
     def share(self, b: int, stream=None):
         """Sequence b's tokens become the prefix of every sequence (decoders made with
         prefix=True), and b is empty.  The others' tokens then stand behind them, so they are
-        empty, too, when this is called; a prefix there was is given back first (unshare)."""
+        empty, too, when this is called.  The blocks of a prefix there was are free again."""
         if not 0 <= b < self.B:
             raise ValueError("b is one of the %d sequences" % self.B)
+        self.unshare(stream=stream)
         with _on(stream):
             self.prefix_table[0].copy_(self.table[b])
             self.prefix_len.copy_(self.ctx[b:b + 1])
@@ -550,7 +551,7 @@ class BatchDecoder:
                 torch.ge(self.positions, 0, out=self.real)
                 torch.mul(self.real, c.prefix_len, out=self.at)
                 positions = self.at.add_(self.positions)
-        rules = L.AttnRules(self.cap, window, L.ptr(self.slopes), None, None)
+        rules = L.AttnRules(self.cap, window, L.ptr(self.slopes), None, None, T)
         src, delta = x, None
         for l in range(sd.L):
             L.e0_rmsnorm_q8(src, delta, self.norm[l], T, H, L.E0_F32, 1e-6, H, H, self.r, None, self.q8, self.q8_scale,

@@ -101,7 +101,7 @@ def compare(got, gl, want, dtype, where=""):
 
 
 def scored(L, desc, Hkv, table, ctx, cu, q, dtype, window=0, cap=0.0, slopes=None, first=None, opens=None,  # noqa: F811
-           scale=None, out=None, lse=True, pad=2, max_q=None, stream=None):
+           scale=None, out=None, lse=True, pad=2, max_q=None, stream=None, rows=0):
     T, Hq, D = q.shape
     B = len(ctx)
     n = np.diff(cu)
@@ -117,7 +117,7 @@ def scored(L, desc, Hkv, table, ctx, cu, q, dtype, window=0, cap=0.0, slopes=Non
     ls = torch.full((T + pad, Hq), -7.0, device="cuda") if lse else None
     keep = [None if x is None else dev(np.asarray(x, t)) for x, t in
             ((slopes, np.float32), (first, np.int32), (opens, np.int32))]
-    rules = L.AttnRules(cap, window, *[L.ptr(x) for x in keep])
+    rules = L.AttnRules(cap, window, *[L.ptr(x) for x in keep], rows)
     wsb = L.e0_attn_scored_workspace_size(B, Hq, Hkv, D, max_q)
     ws = torch.full((wsb,), 255, dtype=torch.uint8, device="cuda")
     st = status()
@@ -128,13 +128,13 @@ def scored(L, desc, Hkv, table, ctx, cu, q, dtype, window=0, cap=0.0, slopes=Non
 
 
 def check_scored(c, table, ctx, cu, q, out, lse, dtype, window=0, cap=0.0, slopes=None, first=None, opens=None, scale=None,
-                 more=0.0):
+                 more=0.0, tiles=None):
     T, Hq, D = q.shape
     scale = float(np.float32(scale or 1 / np.sqrt(D)))
     slopes = None if slopes is None else np.asarray(slopes, np.float32).astype(np.float64)
     got, gl, qv = f64(out), f64(lse) if lse is not None else None, f64(q)
     rows = int(np.diff(cu).max()) * (Hq // c.H)
-    tiles = dtype != F32 and (rows >= TILE_ROWS or Tables.room)
+    tiles = dtype != F32 and (rows >= TILE_ROWS or Tables.room) if tiles is None else tiles
     werr, quantum = weights_of(dtype, tiles, dtype == BF16 and rows > 8, c.vs)
     for b in range(len(ctx)):
         at = slice(cu[b], cu[b + 1])
@@ -290,6 +290,22 @@ def test_caps_of_any_size(L, dtype):  # noqa: F811
         assert st == 0
         # the score through the cap and back: a product with its inverse, the tangent's factor, a product with it
         check_scored(c, table, ctx, cu, q, out, lse, dtype, more=4 * EPS)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_few_rows_in_all(L, dtype):  # noqa: F811
+    """Where the rows in all are told, a step of single tokens takes the path for few rows, whatever max_q is."""
+    rng = np.random.default_rng(12)
+    ctx, cu = [int(x) for x in rng.integers(1, 900, 20)], np.arange(21)
+    c, t, desc, table = filled_cache(L, 20, 32, 2, 128, ctx, rng)
+    q = dev(rng.standard_normal((20, 8, 128)), DT[dtype])
+    wide = np.pad(table, ((0, 0), (0, 256 - table.shape[1])), constant_values=-1)
+    a, la, _ = attend(L, c, desc, wide, ctx, cu, q, dtype, max_q=512)  # that path by itself; bf16's bits know max_q there, too
+    b, lb, st = scored(L, desc, 2, wide, ctx, cu, q, dtype, max_q=512, rows=20)
+    assert st == 0 and torch.equal(a, b) and torch.equal(la, lb)
+    b, lb, st = scored(L, desc, 2, wide, ctx, cu, q, dtype, max_q=512)
+    assert st == 0
+    check_scored(c, table, ctx, cu, q, b, lb, dtype, tiles=dtype != F32)
 
 
 def test_no_rules_is_plain_attention(L):  # noqa: F811

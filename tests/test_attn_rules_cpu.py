@@ -45,7 +45,7 @@ def test_shared_refusals(L, change, code):  # noqa: F811
 
 @pytest.mark.parametrize("field,value,scored,shared", [
     ("cap", -1.0, "ARG", "ARG"), ("cap", float("nan"), "ARG", "ARG"), ("cap", float("inf"), "ARG", "ARG"),
-    ("window", -1, "ARG", "ARG"), ("slopes", P + 2, "ARG", "ARG"), ("first", P + 1, "ARG", "ARG"), ("open_len", P + 1, "ARG", "ARG"),
+    ("window", -1, "ARG", "ARG"), ("rows", -1, "ARG", "ARG"), ("slopes", P + 2, "ARG", "ARG"), ("first", P + 1, "ARG", "ARG"), ("open_len", P + 1, "ARG", "ARG"),
     ("first", P, None, "UNSUPPORTED"), ("open_len", P, None, "UNSUPPORTED")])
 def test_rules_refusals(L, field, value, scored, shared):  # noqa: F811
     rules = L.AttnRules(**{field: value})

@@ -102,6 +102,11 @@ def test_steps_behind_a_prefix(L, prefix_tokens, rules):  # noqa: F811
             tol = tol + 16 * EPS * np.abs(w_l)[:, :, None] * np.abs(v).max()
             compare(o[cu[b]:cu[b + 1]], None, (w_o, w_l, tol, ltol), F16, (b, new))
         assert (o[n:] == 0).all()
+    # another prefix in the place of this one, whose blocks are free again
+    cache.release(torch.ones(B, dtype=torch.uint8, device="cuda"), bd.status)
+    bd.step(x(), lens([0, 17, 0, 0]))
+    cache.share(1)
+    assert cache.prefix_len.tolist() == [17] and cache.free_count.tolist() == [38] and cache.ctx.tolist() == [0] * B
     # everything goes back
     cache.release(torch.ones(B, dtype=torch.uint8, device="cuda"), bd.status)
     cache.unshare(bd.status)
