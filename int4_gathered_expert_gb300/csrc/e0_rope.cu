@@ -107,9 +107,10 @@ E0_DEV void to_fp32(const Raw<TY>& r, float (&v)[8]) {
 // boundary; otherwise elements come one by one.  ADJACENT: pairs are neighbours.
 //
 // Measured (device time, GB300): 16384 rows of 36 heads of 128 bf16, three axes, norms (302 MB):
-// 64.9 us, 4.7 TB/s, 69 % of the measured copy rate, bound by instructions beside it; 87.7 with every lane
+// 59.7 us, 5.1 TB/s, 75 % of the measured copy rate, bound by instructions beside it; 64.7 with a block for
+// every eight rows, each making the table of turns and the last wave half empty, 87.7 with every lane
 // finding its sines, weights and rotation in turn and one value an instruction.  8 rows of 18
-// heads of 256: 3.5 us, a launch and two loads behind one another.
+// heads of 256: 3.9 us, a launch and two loads behind one another.
 template <int TY, bool VEC, bool ADJACENT>
 __global__ void __launch_bounds__(ROPE_WARPS * 32, VEC && TY != E0_F32 ? 3 : 2) k_qk_rope(RopeArgs A) {
     typedef typename Elem<TY>::T T;
@@ -124,136 +125,139 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, VEC && TY != E0_F32 ? 3 : 2) 
         axis[i] = A.axis ? (uint8_t)min((int)A.axis[i], A.axes - 1) : (uint8_t)0;
     }
     __syncthreads();
-    const long long w = (long long)blockIdx.x * ROPE_WARPS + warp;
-    const int t = (int)(w / A.per_token);
-    if (t >= A.T) return;
-    if (A.pos[t] < 0) return;  // no token: the row stays as it is
-    const int slots = 32 / A.lanes, item = lane & (A.lanes - 1), items = (A.D + 15) / 16;
-    const int first = (int)(w % A.per_token) * slots + lane / A.lanes, step = A.per_token * slots;
+    const int slots = 32 / A.lanes, item = lane & (A.lanes - 1), items = (A.D + 15) / 16, step = A.per_token * slots;
     const bool live = item < items;
     const Place at = place_of(A, item);
-    const T* x = reinterpret_cast<const T*>(A.x) + (size_t)t * A.x_ld;
-    T* y = reinterpret_cast<T*>(A.y) + (size_t)t * A.y_ld;
-    const auto load = [&](int h, Raw<TY> (&r)[2]) {
-        if constexpr (VEC) {
-            if (h < A.heads && live) {
-                const uint4* a = reinterpret_cast<const uint4*>(x + (size_t)h * A.D + at.e0);
-                const uint4* b = reinterpret_cast<const uint4*>(x + (size_t)h * A.D + at.e1);
-#pragma unroll
-                for (int i = 0; i < Raw<TY>::N; ++i) r[0].v[i] = a[i], r[1].v[i] = b[i];
-            }
-        }
-    };
-    Raw<TY> now[2], next[2];
-    load(first, now);
-    // every angle once a warp
-    for (int p = lane; p < A.half; p += 32) {
-        const long long pos = A.pos[(size_t)axis[p] * A.pos_ld + t];
-        const unsigned long long a = (unsigned long long)pos * turn[p];
-        // the nearest turn taken off: -1/2 .. 1/2 of a turn, as half turns
-        float sn, cs;
-        sincospif((float)(int)(a >> 32) * 4.6566128730773926e-10f, &sn, &cs);
-        turned[warp][p] = make_float2(cs, sn);
-    }
-    __syncwarp();
-    float P[2][8], Q[2][8];
-    const auto factors = [&](const float* wp) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // the places of a lane's i-th elements, and of their pairs
-            float wa = 1.f, wb = 1.f;
-            int ea, eb;
-            pair_of(A, 8 * item + i, ea, eb);
-            const bool in = 8 * item + i < A.D / 2;
-            if (wp && in) wa = __ldg(wp + ea), wb = __ldg(wp + eb);
-            const float2 f = 8 * item + i < A.half ? turned[warp][8 * item + i] : make_float2(1.f, 0.f);
-            const float pa = wa * f.x, qa = -wb * f.y, pb = wb * f.x, qb = wa * f.y;
-            if (VEC && (ADJACENT || !at.turns)) {  // neighbours: pair i of 8 is elements 2i, 2i + 1 of 16
-                P[i / 4][2 * (i & 3)] = pa, Q[i / 4][2 * (i & 3)] = qa;
-                P[i / 4][2 * (i & 3) + 1] = pb, Q[i / 4][2 * (i & 3) + 1] = qb;
-            } else {
-                P[0][i] = pa, Q[0][i] = qa, P[1][i] = pb, Q[1][i] = qb;
-            }
-        }
-    };
     bool bad = false;
-    int have = -1;  // whose factors these are: 0 the queries', 1 the keys'
-    for (int h0 = 0; h0 < A.heads; h0 += step) {  // all lanes of a warp take every turn
-        const int h = h0 + first;
-        const bool mine = h < A.heads && live;
-        load(h + step, next);
-        const int kind = h < A.Hq ? 0 : 1;
-        if (mine && have != kind) {
-            factors(!A.norm ? nullptr : kind ? A.wk : A.wq);
-            have = kind;
+    // (per_token is more than 1 only where T is small: 2^30 at most)
+    const int all = A.T * A.per_token;
+    for (int w = blockIdx.x * ROPE_WARPS + warp; w < all; w += gridDim.x * ROPE_WARPS) {
+        const int t = w / A.per_token;
+        if (A.pos[t] < 0) continue;  // no token: the row stays as it is
+        const int first = w % A.per_token * slots + lane / A.lanes;
+        const T* x = reinterpret_cast<const T*>(A.x) + (size_t)t * A.x_ld;
+        T* y = reinterpret_cast<T*>(A.y) + (size_t)t * A.y_ld;
+        const auto load = [&](int h, Raw<TY> (&r)[2]) {
+            if constexpr (VEC) {
+                if (h < A.heads && live) {
+                    const uint4* a = reinterpret_cast<const uint4*>(x + (size_t)h * A.D + at.e0);
+                    const uint4* b = reinterpret_cast<const uint4*>(x + (size_t)h * A.D + at.e1);
+#pragma unroll
+                    for (int i = 0; i < Raw<TY>::N; ++i) r[0].v[i] = a[i], r[1].v[i] = b[i];
+                }
+            }
+        };
+        Raw<TY> now[2], next[2];
+        load(first, now);
+        // every angle once a warp
+        __syncwarp();
+        for (int p = lane; p < A.half; p += 32) {
+            const long long pos = A.pos[(size_t)axis[p] * A.pos_ld + t];
+            const unsigned long long a = (unsigned long long)pos * turn[p];
+            // the nearest turn taken off: -1/2 .. 1/2 of a turn, as half turns
+            float sn, cs;
+            sincospif((float)(int)(a >> 32) * 4.6566128730773926e-10f, &sn, &cs);
+            turned[warp][p] = make_float2(cs, sn);
         }
-        float a[8], b[8];
-        if constexpr (VEC) {
-            to_fp32<TY>(now[0], a), to_fp32<TY>(now[1], b);
-        } else {
+        __syncwarp();
+        float P[2][8], Q[2][8];
+        const auto factors = [&](const float* wp) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                // the places of a lane's i-th elements, and of their pairs
+                float wa = 1.f, wb = 1.f;
                 int ea, eb;
                 pair_of(A, 8 * item + i, ea, eb);
-                const bool in = mine && 8 * item + i < A.D / 2;
-                a[i] = in ? Elem<TY>::get(x[(size_t)h * A.D + ea]) : 0.f;
-                b[i] = in ? Elem<TY>::get(x[(size_t)h * A.D + eb]) : 0.f;
+                const bool in = 8 * item + i < A.D / 2;
+                if (wp && in) wa = __ldg(wp + ea), wb = __ldg(wp + eb);
+                const float2 f = 8 * item + i < A.half ? turned[warp][8 * item + i] : make_float2(1.f, 0.f);
+                const float pa = wa * f.x, qa = -wb * f.y, pb = wb * f.x, qb = wa * f.y;
+                if (VEC && (ADJACENT || !at.turns)) {  // neighbours: pair i of 8 is elements 2i, 2i + 1 of 16
+                    P[i / 4][2 * (i & 3)] = pa, Q[i / 4][2 * (i & 3)] = qa;
+                    P[i / 4][2 * (i & 3) + 1] = pb, Q[i / 4][2 * (i & 3) + 1] = qb;
+                } else {
+                    P[0][i] = pa, Q[0][i] = qa, P[1][i] = pb, Q[1][i] = qb;
+                }
             }
-        }
-        if (A.norm) {
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                fma_pair(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
-                fma_pair(s0, s1, b[i], b[i + 1], b[i], b[i + 1], s0, s1);
+        };
+        int have = -1;  // whose factors these are: 0 the queries', 1 the keys'
+        for (int h0 = 0; h0 < A.heads; h0 += step) {  // all lanes of a warp take every turn
+            const int h = h0 + first;
+            const bool mine = h < A.heads && live;
+            load(h + step, next);
+            const int kind = h < A.Hq ? 0 : 1;
+            if (mine && have != kind) {
+                factors(!A.norm ? nullptr : kind ? A.wk : A.wq);
+                have = kind;
             }
-            float ss = mine ? s0 + s1 : 0.f;
-            for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rstd = rsqrtf(fmaf(ss, A.inv_d, A.eps));
-            bad |= mine && !(ss < INFINITY);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                mul_pair(a[i], a[i + 1], a[i], a[i + 1], rstd, rstd);
-                mul_pair(b[i], b[i + 1], b[i], b[i + 1], rstd, rstd);
-            }
-        }
-        float u[8], v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            // a pair that does not turn has Q = 0, which must not meet an infinity of its partner
-            const bool turns = !VEC || at.turns;
-            float c0, c1, d0, d1;  // the partners
-            if (VEC && ADJACENT) {
-                c0 = a[i + 1], c1 = a[i], d0 = b[i + 1], d1 = b[i];
-            } else {
-                c0 = b[i], c1 = b[i + 1], d0 = a[i], d1 = a[i + 1];
-            }
-            if (turns) {
-                mul_pair(c0, c1, c0, c1, Q[0][i], Q[0][i + 1]);
-                mul_pair(d0, d1, d0, d1, Q[1][i], Q[1][i + 1]);
-            } else {
-                c0 = c1 = d0 = d1 = 0.f;
-            }
-            fma_pair(u[i], u[i + 1], a[i], a[i + 1], P[0][i], P[0][i + 1], c0, c1);
-            fma_pair(v[i], v[i + 1], b[i], b[i + 1], P[1][i], P[1][i + 1], d0, d1);
-        }
-        if (mine) {
-            T* to = y + (size_t)h * A.D;
+            float a[8], b[8];
             if constexpr (VEC) {
-                store_vec<TY>(to + at.e0, u);
-                store_vec<TY>(to + at.e1, v);
+                to_fp32<TY>(now[0], a), to_fp32<TY>(now[1], b);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     int ea, eb;
-                    const int p = 8 * item + i;
-                    pair_of(A, p, ea, eb);
-                    if (p < A.half) to[ea] = Elem<TY>::put(u[i]), to[eb] = Elem<TY>::put(v[i]);
-                    else if (p < A.D / 2) to[ea] = Elem<TY>::put(a[i] * P[0][i]), to[eb] = Elem<TY>::put(b[i] * P[1][i]);
+                    pair_of(A, 8 * item + i, ea, eb);
+                    const bool in = mine && 8 * item + i < A.D / 2;
+                    a[i] = in ? Elem<TY>::get(x[(size_t)h * A.D + ea]) : 0.f;
+                    b[i] = in ? Elem<TY>::get(x[(size_t)h * A.D + eb]) : 0.f;
                 }
             }
+            if (A.norm) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    fma_pair(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
+                    fma_pair(s0, s1, b[i], b[i + 1], b[i], b[i + 1], s0, s1);
+                }
+                float ss = mine ? s0 + s1 : 0.f;
+                for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float rstd = rsqrtf(fmaf(ss, A.inv_d, A.eps));
+                bad |= mine && !(ss < INFINITY);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    mul_pair(a[i], a[i + 1], a[i], a[i + 1], rstd, rstd);
+                    mul_pair(b[i], b[i + 1], b[i], b[i + 1], rstd, rstd);
+                }
+            }
+            float u[8], v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                // a pair that does not turn has Q = 0, which must not meet an infinity of its partner
+                const bool turns = !VEC || at.turns;
+                float c0, c1, d0, d1;  // the partners
+                if (VEC && ADJACENT) {
+                    c0 = a[i + 1], c1 = a[i], d0 = b[i + 1], d1 = b[i];
+                } else {
+                    c0 = b[i], c1 = b[i + 1], d0 = a[i], d1 = a[i + 1];
+                }
+                if (turns) {
+                    mul_pair(c0, c1, c0, c1, Q[0][i], Q[0][i + 1]);
+                    mul_pair(d0, d1, d0, d1, Q[1][i], Q[1][i + 1]);
+                } else {
+                    c0 = c1 = d0 = d1 = 0.f;
+                }
+                fma_pair(u[i], u[i + 1], a[i], a[i + 1], P[0][i], P[0][i + 1], c0, c1);
+                fma_pair(v[i], v[i + 1], b[i], b[i + 1], P[1][i], P[1][i + 1], d0, d1);
+            }
+            if (mine) {
+                T* to = y + (size_t)h * A.D;
+                if constexpr (VEC) {
+                    store_vec<TY>(to + at.e0, u);
+                    store_vec<TY>(to + at.e1, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        int ea, eb;
+                        const int p = 8 * item + i;
+                        pair_of(A, p, ea, eb);
+                        if (p < A.half) to[ea] = Elem<TY>::put(u[i]), to[eb] = Elem<TY>::put(v[i]);
+                        else if (p < A.D / 2) to[ea] = Elem<TY>::put(a[i] * P[0][i]), to[eb] = Elem<TY>::put(b[i] * P[1][i]);
+                    }
+                }
+            }
+            now[0] = next[0], now[1] = next[1];
         }
-        now[0] = next[0], now[1] = next[1];
     }
     if (bad && item == 0) set_status(A.st, E0_ST_NONFINITE);
 }
@@ -261,7 +265,8 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, VEC && TY != E0_F32 ? 3 : 2) 
 template <int TY>
 int launch(const RopeArgs& a, bool vec, cudaStream_t s) {
     const long long blocks = ((long long)a.T * a.per_token + ROPE_WARPS - 1) / ROPE_WARPS;
-    const auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, ROPE_WARPS * 32, 0, s>>>(a); };
+    const long long most = (long long)num_sms() * (vec && TY != E0_F32 ? 3 : 2);
+    const auto go = [&](auto kernel) { kernel<<<(unsigned)(blocks < most ? blocks : most), ROPE_WARPS * 32, 0, s>>>(a); };
     if (vec)
         a.adjacent ? go(k_qk_rope<TY, true, true>) : go(k_qk_rope<TY, true, false>);
     else
