@@ -747,8 +747,9 @@ size_t e0_attn_scored_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * tokens as all of them.  Where q is fp16 or bf16, max_q queries have 64 rows of a KV head and
  * more, an average sequence has 64 of the rows in all, and these, Hq and the table (with the
  * window) leave room for some millions of scores, the products run in tiles of 128 or 256 rows on the
- * tensor cores: the weights are then rounded to 11 bits (bf16) or 22 (fp16).  What max_q, max_blocks
- * and rows allow beyond the lengths thus has a say in an output's last bits.  All else takes the path
+ * tensor cores, the weights in 22 bits.  What max_q, max_blocks and rows allow beyond the lengths thus has a
+ * say in an output's last bits (fp32 sums in another order; on the path for few rows bf16 outputs of more than
+ * 8 rows of a KV head have weights of 11 bits, as e0_attn_decode's).  All else takes the path
  * for few rows (every 8 of a KV head, 16 of bf16, read the sequence once more).  rules NULL: none.  Errors as
  * e0_attn_decode's; cap negative or not finite, window < 0, rows < 0, or a pointer of the rules that
  * is not aligned to 4 bytes -> E0_ERR_ARG. */

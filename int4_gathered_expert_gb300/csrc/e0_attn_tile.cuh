@@ -25,9 +25,11 @@ namespace {
 // exponentials, and both read the same operands; with D = 256 tensor memory holds one half
 // and two S.
 // fp16 operands: codes widen exactly; bf16 queries go in times a power of two of the
-// row, fp16 ones as they are; the weights 2^(t - m + TILE_LIFT), at most 2^15, are rounded to fp16,
-// for bf16 outputs an eighth of what the output's rounding is; fp16 outputs get the weights'
-// rests, too, in a second product (SPLIT).
+// row, fp16 ones as they are; the weights 2^(t - m + TILE_LIFT), at most 2^15, go in as an fp16 part and
+// their rests, a product each: 22 bits for outputs of either type, as in e0_attn.cuh for up to 8 rows, so
+// that a call's bits do not depend on its path beyond what fp32 sums in another order do.  (bf16 outputs
+// without the rests: 116 us a call for 129, the documents below, and 61 for 66 behind a prefix of 16000, but
+// one output in 25 rounded to the other side of a step.)
 //
 // Products are issued by one thread and done in its order: a unit's first products go where the
 // weights of the unit before were as soon as that one's second products have been issued.
@@ -546,7 +548,6 @@ template <int D, int TY, bool RULES>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_constant__ TileArgs A) {
     typedef Geo<D> G_;
     typedef typename Elem<TY>::T T;
-    constexpr bool SPLIT = TY == E0_F16;
     constexpr int KV = G_::KV, STAGES = G_::STAGES, HALVES = G_::HALVES, CHUNKS = KV / 64;
     extern __shared__ __align__(1024) char tile_sm[];
     TileSmem<D>& S = *reinterpret_cast<TileSmem<D>*>(tile_sm);
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                     float part[4];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        uint32_t hi16[16], lo16[SPLIT ? 16 : 1];
+                        uint32_t hi16[16], lo16[16];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             float s0 = 0.f, s1 = 0.f;
@@ -727,15 +728,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                             for (int j = 0; j < 8; ++j) {
                                 const float v = exp2_of(x[32 * b + 16 * q + 2 * j]), w = exp2_of(x[32 * b + 16 * q + 2 * j + 1]);
                                 add2(s0, s1, v, w);
-                                if constexpr (SPLIT)
-                                    split_half(v, w, hi16[8 * q + j], lo16[8 * q + j]);
-                                else
-                                    hi16[8 * q + j] = half2_of(v, w);
+                                split_half(v, w, hi16[8 * q + j], lo16[8 * q + j]);
                             }
                             part[2 * b + q] = s0 + s1;
                         }
                         tmem_st16(s_at + 64 * c + 16 * b, hi16);
-                        if constexpr (SPLIT) tmem_st16(s_at + 64 * c + 32 + 16 * b, lo16);
+                        tmem_st16(s_at + 64 * c + 32 + 16 * b, lo16);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -987,7 +985,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                         for (int s = 4 * c; s < 4 * c + 4; ++s) {
                             const uint32_t a = p_at + 64 * c + 8 * (s % 4);
                             umma_ta_lo(d, a, b + s * 2 * D, V_HI, id_o, s > 0 ? 1 : more);
-                            if constexpr (SPLIT) umma_ta_lo(d, a + 32, b + s * 2 * D, V_HI, id_o, 1);
+                            umma_ta_lo(d, a + 32, b + s * 2 * D, V_HI, id_o, 1);
                         }
                         umma_commit(c + 1 < CHUNKS ? &S.o_half[h] : &S.o_done[slot]);
                     }
