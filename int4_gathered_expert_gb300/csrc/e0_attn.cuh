@@ -172,6 +172,13 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     return s;
 }
 
+// The tokens of a prefix of length `given`: none where that is negative or more than its table (of `a`, the prefix')
+// has room for.  Rows' positions are counted from it, too: from 2^31 - 1 they would pass 32 bits, and
+// with them a window's first position.
+E0_DEV int prefix_of(const AttnArgs& a, int given) {
+    return given < 0 || (long long)given > ((long long)a.max_blocks << a.shift) ? 0 : given;
+}
+
 // A schedule longer than this is not run (it would read for seconds).
 constexpr uint32_t MOST_UNITS = 0x7FFFFFFFu;
 

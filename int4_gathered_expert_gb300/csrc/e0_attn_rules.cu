@@ -49,15 +49,15 @@ void put_rules(AttnArgs& a, const e0_attn_rules* r) {
 // ---------------------------------------------------------------- the shared prefix
 
 // For each row its position behind the prefix, and {0, rows} as the bounds of one sequence
-// of them all.  `a` is of the sequences' own tokens.
+// of them all.  `a` is of the sequences' own tokens, `front` of the prefix.
 constexpr int ROWS_THREADS = 1024;
-__global__ void __launch_bounds__(ROWS_THREADS) k_shared_rows(AttnArgs a, const int32_t* prefix_len, int32_t* at, int32_t* cu) {
+__global__ void __launch_bounds__(ROWS_THREADS) k_shared_rows(AttnArgs a, AttnArgs front, int32_t* at, int32_t* cu) {
     __shared__ int rows;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) rows = 0;
     for (int t = threadIdx.x; t < a.limit; t += ROWS_THREADS) at[t] = 0;
     __syncthreads();
-    const int before = max(*prefix_len, 0);
+    const int before = prefix_of(front, *front.ctx);
     for (int b = threadIdx.x >> 5; b < a.B; b += ROWS_THREADS / 32) {
         const Seq s = seq_of<true>(a, b, false);
         for (int i = lane; i < s.n; i += 32) at[s.row0 + i] = before + s.ctx - s.n + i;
@@ -151,7 +151,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
         front.raw = o[0];
         rc = attn_tile(front, &prefix, dtype, tiles, s);
     } else {
-        k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, prefix_len, at, cu2);
+        k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, front, at, cu2);
         if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
         front.raw = o[0];
         rc = launch_t<true>(front, dtype, c->D, s);

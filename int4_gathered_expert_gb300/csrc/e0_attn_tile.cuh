@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
     if (A.own.B > 0) {
         for (int t = tid; t < A.own.limit; t += PLAN_THREADS) A.own_at[t] = -1;
         __syncthreads();
-        const int before = max(*A.a.ctx, 0);
+        const int before = prefix_of(A.a, *A.a.ctx);
         for (int b = warp; b < A.own.B; b += PLAN_THREADS / 32) {
             const Seq s = seq_of<true>(A.own, b, false);
             for (int i = lane; i < s.n; i += 32) A.own_at[s.row0 + i] = before + s.ctx - s.n + i;
@@ -176,11 +176,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
     const auto sequence = [&](int b, bool tell) {
         if (A.own.B == 0) return seq_of<true>(A.a, b, tell);
         Seq s;
-        s.row0 = 0, s.n = all_rows, s.ctx = *A.a.ctx;
-        if (s.ctx < 0 || (long long)s.ctx > ((long long)A.a.max_blocks << A.a.shift)) {
-            if (tell && tid == 0) set_status(A.a.st, E0_ST_BAD_LENGTH);
-            s.ctx = 0;
-        }
+        const int given = *A.a.ctx;
+        s.row0 = 0, s.n = all_rows, s.ctx = prefix_of(A.a, given);
+        if (s.ctx != given && tell && tid == 0) set_status(A.a.st, E0_ST_BAD_LENGTH);
         return s;
     };
     // tiles of query rows of each sequence
