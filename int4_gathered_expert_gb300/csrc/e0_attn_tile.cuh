@@ -92,10 +92,13 @@ struct TileHead {
     int jobs, pad;
 };
 
+// No position: those of queries are -2^30 and more (a sequence may have more queries than tokens).
+constexpr int NO_ROW = INT_MIN;
+
 struct TileArgs {
     AttnArgs a;               // parts and cuts unused
     // A prefix (own.B > 0): `own` are the sequences whose rows are the one job's; their positions
-    // behind the prefix go to own_at, -1 where a row is no sequence's.
+    // behind the prefix go to own_at, NO_ROW where a row is no sequence's.
     AttnArgs own;
     int32_t* own_at;
     const float* own_o;       // merge: the sequences' own results, normed, and their lse
@@ -117,7 +120,8 @@ E0_DEV int div_group(const TileArgs& A, int n) { return (int)((unsigned long lon
 
 // The range of positions that a token of a sequence sees.
 E0_DEV void range_of(const TileArgs& A, int seq, int row0, int p0, int ctx, int i, int& p, int& lo, int& hi) {
-    p = !A.a.at ? p0 + i : A.a.window > 0 || A.a.slopes ? A.a.at[row0 + i] : 0;  // needed there alone
+    // (needed there alone; no distance from it passes 32 bits)
+    p = !A.a.at ? p0 + i : A.a.window > 0 || A.a.slopes ? max(A.a.at[row0 + i], -(1 << 30)) : 0;
     hi = A.a.at ? ctx : p + 1;
     if (A.a.open) hi = max(hi, A.a.open[seq]);
     hi = min(hi, ctx);
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
     };
     if (tid == 0) all_rows = 0, carry = 0;
     if (A.own.B > 0) {
-        for (int t = tid; t < A.own.limit; t += PLAN_THREADS) A.own_at[t] = -1;
+        for (int t = tid; t < A.own.limit; t += PLAN_THREADS) A.own_at[t] = NO_ROW;
         __syncthreads();
         const int before = prefix_of(A.a, *A.a.ctx);
         for (int b = warp; b < A.own.B; b += PLAN_THREADS / 32) {
@@ -1138,7 +1142,7 @@ __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
     if (r >= rows) return;
     const int row = mtile * G_::ROWS + r, i_tok = div_group(A, row), head = cut.head * G + row - i_tok * G;
     const size_t tok = (size_t)row0 + i_tok, at = tok * A.a.Hq + head;
-    if (A.merge && A.own_at[tok] == -1) return;  // no sequence's row
+    if (A.merge && A.own_at[tok] == NO_ROW) return;  // no sequence's row
     const auto slot_of = [&](int i) { return 2 * (cut.block + i) + (i == 0); };
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
