@@ -110,6 +110,10 @@ E0_DEV uint32_t cluster_blocks() {
 E0_DEV void meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Only once all the row's blocks have begun may one write to another's memory: each says so as its first
+// act and waits for the others before its first such write, the reading of the row between the two.
+E0_DEV void say_begun() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+E0_DEV void all_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // A variable of block r's shared memory.
 template <typename P>
 E0_DEV uint32_t of_block(P* p, uint32_t r) {
@@ -613,6 +617,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) k_sample(SampleArgs A) {
     float* x = reinterpret_cast<float*>(sample_sm + sizeof(SampleSmem));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), blocks = cluster_blocks();
+    say_begun();
     const int row = blockIdx.x / blocks;
     const int from = min(A.V, (int)rank * A.slice), n = min(A.V, from + A.slice) - from;
     const float temp = A.temperature ? A.temperature[row] : 1.f;
@@ -663,6 +668,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) k_sample(SampleArgs A) {
     odd = __any_sync(0xffffffffu, odd);
     if (lane == 0) S.wsum[warp] = best, S.wcount[warp] = odd;
     __syncthreads();
+    all_begun();
     if (tid < blocks) {
         uint32_t some = 0;
         for (int w = 0; w < SM_WARPS; ++w) best = max(best, S.wsum[w]), some |= S.wcount[w];
