@@ -585,8 +585,9 @@ typedef struct e0_sampling {
  * but one at least.  token [T] is the first kept token, by number, whose running sum of
  * kept weights exceeds u[t] times their total (u = 1: the last).  Optional outputs (or
  * NULL): logp [T] = ln(w / total), kept [T] = n.  u: device fp32 [T] in [0, 1], the caller's
- * random numbers.  Weights are integers, 2^44 w, off by 2^-28 of themselves at most, and their sums exact:
- * equal calls give equal tokens; a weight below 2^-44 is never drawn.  A row that holds
+ * random numbers.  Weights are integers, 2^44 w, off by 2^-28 of themselves or by 2^-44, whichever is more (min_p
+ * is compared with these), and their sums exact: equal calls give equal tokens; a weight below 2^-44 is never
+ * drawn.  logp comes from the token's own logit and is off by 4 steps of fp32 and V 2^-44 at most.  A row that holds
  * NaN or +infinity or nothing but -infinity, or whose temperature is negative, infinite or
  * NaN, whose u is outside [0, 1], or top_p or min_p NaN, gets token -1, logp -infinity and
  * kept 0, and raises E0_ST_NONFINITE.  rules NULL: all defaults.  Errors: NULL x, u or

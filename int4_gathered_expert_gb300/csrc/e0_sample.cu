@@ -32,7 +32,7 @@ namespace {
 // A draw over V tokens has V borders, and an error in the sums moves all of them: with fp32
 // exponentials one row in a hundred would get another token than the definition gives.
 // So a weight 2^-y, y = (largest - logit) log2 e / temperature, is a 64-bit integer, 2^44
-// times its value, good to 2^-28 of itself: y comes from a difference and a product that
+// times its value, good to 2^-28 of itself or to one, whichever is more: y comes from a difference and a product that
 // carry their rounding errors along (Dekker, Numer. Math. 18, 1971), its power of two from a
 // table of 128 and the series of what is left.  Sums of integers are exact in any order, so
 // equal calls give equal tokens.  Weights below 2^-44 of the largest count as nothing.
@@ -188,6 +188,13 @@ E0_DEV u64 weight_of(const Scale& s, float x) {
     const float t = f * fmaf(f, fmaf(f, L3, L2), L1);
     const int g = step.x + (__float_as_int(fmaf(__int_as_float(step.y), t, WHOLE)) - __float_as_int(WHOLE));
     return ((u64)(uint32_t)g << (WEIGHT_BITS - 30)) >> (k / STEPS_OF_ONE);
+}
+
+// ln of a token's weight, from its logit: the whole number of a rare token has few bits.  Three steps of
+// fp32 (the constant's, the product's, the sum's).
+E0_DEV float ln_weight_of(const Scale& s, float x) {
+    const float d = s.most - x, p = __fmul_rn(d, s.ch);
+    return -0.6931471805599453f * (p + (fmaf(d, s.ch, -p) + d * s.cl));
 }
 
 // v of [0, 1) times 2^64, rounded down.
@@ -599,13 +606,13 @@ struct Row {
 
 // ---------------------------------------------------------------- the kernel
 
-E0_DEV void put_token(const SampleArgs& A, int row, int token, uint32_t kept, u64 w, u64 total) {
+E0_DEV void put_token(const SampleArgs& A, const Scale& s, int row, int token, float x, uint32_t kept, u64 w, u64 total) {
     A.token[row] = token;
     if (A.kept) A.kept[row] = (int32_t)kept;
     if (A.logp) {
-        // ln(w / total), by what is left of 1 where that is small
+        // ln(w / total), by what is left of 1 where that is small (w has 43 bits and more then)
         const float rest = (float)(total - w) / (float)total;
-        A.logp[row] = rest < 0.5f ? log1pf(-rest) : logf((float)w / (float)total);
+        A.logp[row] = rest < 0.5f ? log1pf(-rest) : ln_weight_of(s, x) - logf((float)total * 0x1p-44f);
     }
 }
 
@@ -755,7 +762,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) k_sample(SampleArgs A) {
             u64 run = 0;
             for (int j = 0; j < all; ++j)
                 if ((uint32_t)S.few[j] < id) run += S.few_w[j];
-            if (run <= want && want < run + w) put_token(A, row, (int)id, count, w, total);
+            if (run <= want && want < run + w) put_token(A, R.sc, row, (int)id, logit_of((uint32_t)(me >> 32)), count, w, total);
             return;
         }
         // of top-k, then of top-p within these
@@ -854,7 +861,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) k_sample(SampleArgs A) {
         u64 w;
         if (!kept(i, w)) continue;
         if (want < before + w) {
-            put_token(A, row, from + i, total_count, w, total);
+            put_token(A, R.sc, row, from + i, x[i], total_count, w, total);
             return;
         }
         before += w;

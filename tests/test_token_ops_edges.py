@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests.test_layer_ops import BF16, DT, F16, F32, L  # noqa: F401
+from tests.test_layer_ops import BF16, DT, EPS, F16, F32, L, dev, f64  # noqa: F401
 from tests.test_token_ops import draw, rules_of
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +24,38 @@ def test_the_largest_of_many_short_rows(L, V, dtype):  # noqa: F811
     for rules in (dict(top_k=np.ones(T)), dict(top_k=np.full(T, 2), top_p=np.full(T, 0.5))):
         got, logp, kept, st = draw(L, x, np.full(T, 0.4), dtype, rules_of(L, **rules))
         assert st == 0 and np.array_equal(got, at) and (kept == 1).all() and (logp == 0).all()
+
+
+@pytest.mark.parametrize("V", [3, 200, 3000, 40000])
+@pytest.mark.parametrize("temp", [1.0, 0.37, 60.0])
+@pytest.mark.parametrize("rules", ["none", "top_k", "top_p"])
+def test_the_probability_of_rare_tokens(L, V, temp, rules):  # noqa: F811
+    """The last token, drawn by u = 1, has a weight of 2^-1 to 2^-43.9: ln p is its logit's, not that of the few bits that
+    its weight has as a whole number of 2^-44."""
+    rng = np.random.default_rng(V)
+    y = np.concatenate([np.linspace(1, 43.9, 60), [30, 35.5, 40.5, 41.9, 42.9, 43.5]])
+    T = len(y)
+    temp = float(np.float32(temp))
+    x = np.minimum(rng.standard_normal((T, V)), 2.9) * 2 * temp
+    if rules != "none":  # few tokens that come before it, so that the first block ends the row
+        x = x - 200 * temp
+    x[:, 0] = 6 * temp
+    x[:, V - 1] = 6 * temp - y * np.log(2) * temp
+    x = dev(x, torch.float32)
+    kw = dict(temperature=np.full(T, temp))
+    if rules == "top_k":
+        kw["top_k"] = np.full(T, 2)
+    if rules == "top_p":
+        kw["top_p"] = np.full(T, 1 - 2.0 ** -24)  # the last token is needed up to a weight of 2^-24
+    got, logp, kept, st = draw(L, x, np.ones(T), F32, rules_of(L, **kw))
+    assert st == 0
+    xv = f64(x)
+    for t in range(T):
+        if rules == "top_p" and y[t] > 23:
+            continue
+        assert got[t] == V - 1, (t, y[t])
+        d = (xv[t] - xv[t].max()) / temp
+        w = np.exp(d if rules == "none" else d[[0, V - 1]])
+        want = d[V - 1] - np.log(w.sum())
+        # 4 steps of fp32, of which the test's own 64 bits take none; weights are whole numbers of 2^-44
+        assert abs(logp[t] - want) <= 4 * EPS * abs(want) + V * 2.0 ** -44, (t, y[t], logp[t], want)
