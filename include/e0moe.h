@@ -569,7 +569,8 @@ int e0_qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, co
 
 /* A row's rules: device arrays of T values, each NULL for its default in all rows. */
 typedef struct e0_sampling {
-    const float* temperature; /* 1; 0 (or less than 2^-100): the largest logit's token   */
+    const float* temperature; /* 1; 0 (or less than 2^-100): the largest logit's token;
+                                 more than 2^116 counts as 2^116                          */
     const int32_t* top_k;     /* 0 and less: no limit                                    */
     const float* top_p;       /* 1 and more: no limit; 0 and less: the first token alone */
     const float* min_p;       /* 0 and less: no limit; more than 1 counts as 1           */

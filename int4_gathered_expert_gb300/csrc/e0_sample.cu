@@ -632,7 +632,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) k_sample(SampleArgs A) {
     const float top_p = A.top_p ? A.top_p[row] : 1.f, min_p = A.min_p ? A.min_p[row] : 0.f;
     const int top_k = A.top_k ? A.top_k[row] : 0;
     if (tid == 0) {
-        const double c = 1.4426950408889634 / (double)temp;
+        // (beyond 2^116 the factor would lose bits below fp32's normal numbers, and differences that count pass its range)
+        const double c = 1.4426950408889634 / (double)fminf(temp, 0x1p116f);
         S.ch = (float)c, S.cl = (float)(c - (double)S.ch);
         S.least = min_p > 0.f ? (u64)((double)fminf(min_p, 1.f) * 17592186044416.0) : 0;  // 2^44
     }

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from tests.test_layer_ops import BF16, DT, EPS, F16, F32, L, dev, f64  # noqa: F401
-from tests.test_token_ops import draw, rules_of
+from tests.test_token_ops import NEAR, draw, row_ref, rules_of
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -59,3 +59,26 @@ def test_the_probability_of_rare_tokens(L, V, temp, rules):  # noqa: F811
         want = d[V - 1] - np.log(w.sum())
         # 4 steps of fp32, of which the test's own 64 bits take none; weights are whole numbers of 2^-44
         assert abs(logp[t] - want) <= 4 * EPS * abs(want) + V * 2.0 ** -44, (t, y[t], logp[t], want)
+
+
+@pytest.mark.parametrize("temp", [2.0 ** 100, 1e31, 2.0 ** 116, 1e37, 1.3e38, 3.4e38])
+@pytest.mark.parametrize("size", [1.0, 1e31, 3e35, 3e38])
+def test_the_hottest_temperatures(L, temp, size):  # noqa: F811
+    """Temperatures beyond 2^116 count as that: the weights keep their bits, and logits whose differences pass fp32's range
+    are told apart."""
+    rng = np.random.default_rng(int(np.log2(temp)))
+    V, T = 3000, 60
+    x = rng.uniform(-1, 1, (T, V)) * size
+    x = dev(x.astype(np.float32))
+    u = rng.random(T).astype(np.float32) * 0.999
+    got, logp, kept, st = draw(L, x, u, F32, rules_of(L, temperature=np.full(T, temp), top_p=np.full(T, 0.7)))
+    assert st == 0
+    xv, sure = f64(x), 0
+    for t in range(T):
+        tok, want, n, near = row_ref(xv[t], float(u[t]), min(float(np.float32(temp)), 2.0 ** 116), 0, float(np.float32(0.7)))
+        if near < NEAR + V * 2.0 ** -44:
+            continue
+        sure += 1
+        assert got[t] == tok and kept[t] == n
+        assert abs(logp[t] - want) <= 4 * EPS * abs(want) + V * 2.0 ** -44
+    assert sure >= T - 3
