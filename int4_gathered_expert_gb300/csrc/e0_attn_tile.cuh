@@ -106,7 +106,7 @@ struct TileArgs {
     bool merge;               // every piece of a job is a part; the join ends the rows with the own results
     float* part_o;            // [2 * blocks][ROWS][D]
     float2* part_ml;          // [2 * blocks][ROWS]
-    TileCut* cuts;            // [blocks][2]
+    TileCut* cuts;            // [blocks]: the job that the block began and left unfinished
     TileJob* jobs;
     int4* begin;              // [blocks]: job, head, unit
     TileHead* head;
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                                : arrived(&S.o_done[n & 1], (n >> 1) & 1, abort);
         };
         Piece p;
-        TileCut begun = {0, 0, 0, 0}, went_on = {0, 0, 0, 0};
+        TileCut begun = {0, 0, 0, 0};
         while (ok && pieces.next(p)) {
             const TileJob& J = p.J;
             const int r = J.mtile * G_::ROWS + 128 * h + t;  // row of the sequence: token, head of the group
@@ -836,14 +836,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
                 else if (A.a.lse)
                     A.a.lse[tok * A.a.Hq + head] = lse_of(mx, sum, TILE_LIFT);
             }
-            if (!whole && threadIdx.x == 0) {
+            if (!whole && p.k0 == 0 && threadIdx.x == 0) {
                 const uint32_t u0 = J.start + (uint32_t)p.head * (J.units + TILE_JOB_COST) + TILE_JOB_COST, share = A.head->share;
                 const int b0 = (int)(u0 / share), b1 = (int)((u0 + J.units - 1) / share);
-                (p.k0 == 0 ? begun : went_on) = {b1 - b0 + 1, b0, p.job, p.head};
+                begun = {b1 - b0 + 1, b0, p.job, p.head};
             }
         }
         if (!ok && lane == 0) give_up();
-        if (threadIdx.x == 0) A.cuts[2 * blockIdx.x] = begun, A.cuts[2 * blockIdx.x + 1] = went_on;
+        if (threadIdx.x == 0) A.cuts[blockIdx.x] = begun;
     } else if (warp < G_::SOFT + G_::TURN) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G_::TURN_REGS));
         // ---------------- codes into operands, four warps an operand: block ids are read two units
@@ -1131,7 +1131,7 @@ template <int D, int TY>
 __global__ void __launch_bounds__(TILE_JOIN_THREADS) k_tile_join(TileArgs A) {
     typedef Geo<D> G_;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
-    const TileCut cut = A.cuts[2 * blockIdx.x];
+    const TileCut cut = A.cuts[blockIdx.x];
     if (cut.parts == 0) return;
     const int4* from = reinterpret_cast<const int4*>(A.jobs + cut.job);
     const int mtile = from[0].y, row0 = from[3].y, rows = from[3].z;
@@ -1196,7 +1196,7 @@ inline long long tile_jobs(int B, int max_q, int G, int D) {
 }
 inline size_t tile_ws_bytes(int B, int max_q, int G, int D) {
     const size_t rows = D == 256 ? 128 : 256, slots = 2 * (size_t)tile_blocks();
-    return up256(slots * rows * D * sizeof(float)) + up256(slots * rows * sizeof(float2)) + up256(slots * sizeof(TileCut)) +
+    return up256(slots * rows * D * sizeof(float)) + up256(slots * rows * sizeof(float2)) + up256(tile_blocks() * sizeof(TileCut)) +
            up256((size_t)tile_jobs(B, max_q, G, D) * sizeof(TileJob)) + up256(tile_blocks() * sizeof(int4)) + 256;
 }
 
@@ -1262,7 +1262,7 @@ inline TileArgs tile_args(const AttnArgs& a, const TilePrefix* prefix, int dtype
     };
     t.part_o = reinterpret_cast<float*>(take(slots * rows * a.D * sizeof(float)));
     t.part_ml = reinterpret_cast<float2*>(take(slots * rows * sizeof(float2)));
-    t.cuts = reinterpret_cast<TileCut*>(take(slots * sizeof(TileCut)));
+    t.cuts = reinterpret_cast<TileCut*>(take(t.blocks * sizeof(TileCut)));
     t.jobs = reinterpret_cast<TileJob*>(take((size_t)t.most_jobs * sizeof(TileJob)));
     t.begin = reinterpret_cast<int4*>(take(t.blocks * sizeof(int4)));
     t.head = reinterpret_cast<TileHead*>(take(sizeof(TileHead)));
