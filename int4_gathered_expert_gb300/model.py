@@ -407,8 +407,9 @@ class QkRope:
                 raise ValueError("a norm's weight is one [%d] a layer" % shape.D)
             return [None] * n_layers if w is None else [_dev(v.astype(np.float32), device) for v in w]
 
-        if axis is not None and (axis.shape != freq.shape or int(axis.max(initial=0)) >= n_axes):
-            raise ValueError("an axis below n_axes for each of the pairs")
+        if axis is not None and (axis.dtype.kind not in "iu" or axis.shape != freq.shape or int(axis.min(initial=0)) < 0 or
+                                 int(axis.max(initial=0)) >= n_axes):
+            raise ValueError("an axis from 0 and below n_axes for each of the pairs")
         self.shape, self.n_axes = shape, n_axes
         self.freq = _dev(freq.astype(np.float32), device)
         self.axis = None if axis is None else _dev(axis.astype(np.uint8), device)
@@ -422,11 +423,15 @@ class QkRope:
     def __call__(self, layer: int, qkv: torch.Tensor, positions: torch.Tensor):
         a = self.shape
         row = (a.Hq + 2 * a.Hkv) * a.D
+        at = self.freq.device
         if qkv.dtype != torch.float16 or qkv.dim() != 2 or qkv.shape[1] != row or qkv.stride(1) != 1:
             raise ValueError("qkv is fp16 rows of %d" % row)
         T = len(qkv)
-        if positions.dtype != torch.int32 or positions.numel() != self.n_axes * T or not positions.is_contiguous():
+        fits = positions.shape == (self.n_axes, T) or (self.n_axes == 1 and positions.shape == (T,))
+        if positions.dtype != torch.int32 or not fits or not positions.is_contiguous():
             raise ValueError("positions are contiguous int32 [%d, %d]" % (self.n_axes, T))
+        if not at.type == qkv.device.type == positions.device.type == "cuda" or not at == qkv.device == positions.device:
+            raise ValueError("qkv and positions are on the device that the rotation's tables are on")
         L.e0_qk_rope(qkv, L.E0_F16, qkv.stride(0), T, a.Hq, a.Hkv, self.descs[layer], positions, T, qkv, qkv.stride(0),
                      self.status)
 
