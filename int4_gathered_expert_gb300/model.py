@@ -374,18 +374,26 @@ class KvCacheDev:
         """Empty the sequences whose mask byte is set; their blocks are free again."""
         L.e0_kv_release(self.state, mask, self.ctx, self.free_count, status, stream=stream)
 
-    def share(self, b: int, stream=None):
+    def share(self, b: int, stream=None, status=None):
         """Sequence b's tokens become the prefix of every sequence (decoders made with
-        prefix=True), and b is empty.  The others' tokens then stand behind them, so they are
-        empty, too, when this is called.  The blocks of a prefix there was are free again."""
+        prefix=True; others do not see it), and b is empty.  The others' tokens would then stand behind them:
+        where one has any, nothing changes and status, if given, gets E0_ST_BAD_LENGTH.  The blocks of a prefix
+        there was are free again; b's tokens start at position 0, so they come from steps without one."""
         if not 0 <= b < self.B:
             raise ValueError("b is one of the %d sequences" % self.B)
-        self.unshare(stream=stream)
         with _on(stream):
-            self.prefix_table[0].copy_(self.table[b])
-            self.prefix_len.copy_(self.ctx[b:b + 1])
-            self.table[b].fill_(-1)
-            self.ctx[b].fill_(0)
+            full = self.ctx.ne(0)
+            full[b:b + 1].zero_()
+            alone = full.any().logical_not()
+            mask = alone.to(torch.uint8).view(1)
+        L.e0_kv_release(self.prefix_state, mask, self.prefix_len, self.free_count, status, stream=stream)
+        with _on(stream):
+            self.prefix_table[0].copy_(torch.where(alone, self.table[b], self.prefix_table[0]))
+            self.prefix_len.copy_(torch.where(alone, self.ctx[b:b + 1], self.prefix_len))
+            self.table[b].masked_fill_(alone, -1)
+            self.ctx[b:b + 1].masked_fill_(alone, 0)
+            if status is not None:
+                status.bitwise_or_(alone.logical_not().to(status.dtype) * L.E0_ST_BAD_LENGTH)
 
     def unshare(self, status=None, stream=None):
         """The prefix' blocks are free again; there is none."""

@@ -52,3 +52,55 @@ def test_steps_on_several_axes(L, axes):  # noqa: F811
         assert torch.equal(qkv[:, 8 * 64:], was[:, 8 * 64:]) and torch.equal(qkv[n:], was[n:])
     with pytest.raises(ValueError):  # the row's positions alone do not say where it is on the others
         rope(0, torch.zeros((T, 640), dtype=torch.float16, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_prefix_is_shared_where_the_others_are_empty(L, captured):  # noqa: F811
+    """Tokens that another sequence has would silently stand behind it: the cache, and a prefix there was, stay as they are."""
+    from int4_gathered_expert_gb300.model import BatchDecoder, KvCacheDev
+    a = synth.AttnShape(Hq=4, Hkv=2, D=64, block_tokens=16)
+    B, T = 3, 40
+    sd, attn = parts(1, a)
+    cache = KvCacheDev(1, B, 20, 4, a.Hkv, a.D, 16)
+    first, bd = BatchDecoder(sd, attn, a, cache, T), BatchDecoder(sd, attn, a, cache, T, prefix=True)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph, side = None, torch.cuda.Stream()
+
+    def share():
+        if graph:
+            graph.replay()
+        else:
+            cache.share(1, status=st)
+
+    def all_of():
+        return [t.clone() for t in (cache.table, cache.ctx, cache.prefix_table, cache.prefix_len, cache.free_count)]
+
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cache.share(1, status=st)
+        assert cache.prefix_len.tolist() == [0] and L.e0_read_status(st) == 0
+    x = torch.randn((T, synth.TINY.H), generator=torch.Generator().manual_seed(1)).cuda()
+    first.step(x, lens([0, 17, 0]))
+    row = cache.table[1].clone()
+    share()
+    assert L.e0_read_status(st) == 0 and cache.prefix_len.tolist() == [17] and cache.ctx.tolist() == [0] * B
+    assert torch.equal(cache.prefix_table[0], row) and (cache.table == -1).all()
+    bd.step(x, lens([1, 0, 1]))
+    for new in ([0, 0, 0], [0, 18, 0]):  # an empty sequence as another prefix; one with tokens
+        if sum(new):
+            bd.step(x, lens(new))
+        was = all_of()
+        share()
+        assert L.e0_read_status(st) == L.E0_ST_BAD_LENGTH and all(torch.equal(p, q) for p, q in zip(was, all_of()))
+        st.zero_()
+    cache.release(torch.tensor([1, 0, 1], dtype=torch.uint8, device="cuda"), st)
+    share()  # the others are empty now
+    assert cache.prefix_len.tolist() == [18] and cache.free_count.tolist() == [18] and cache.ctx.tolist() == [0] * B
+    torch.cuda.synchronize()
+    cache.share(0, stream=side)  # nothing as the prefix, on a stream of its own
+    cache.share(0, stream=side.cuda_stream)
+    side.synchronize()
+    assert L.e0_read_status(st) == 0 and cache.prefix_len.tolist() == [0] and sorted(cache.free.tolist()) == list(range(20))
+    assert cache.free_count.tolist() == [20]
