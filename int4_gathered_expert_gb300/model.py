@@ -497,8 +497,8 @@ class BatchDecoder:
     def __init__(self, sd: StackDev, attn: List[dict], shape, cache: KvCacheDev, T: int, device="cuda",
                  edit: Optional[Callable[[int, torch.Tensor, torch.Tensor], None]] = None, cap: float = 0.0,
                  slopes: Optional[np.ndarray] = None, prefix: bool = False):
-        if not 0 <= cap < float("inf"):
-            raise ValueError("cap is 0 (none) or a positive number")
+        if not 0 <= np.float32(cap) < np.inf or (cap and not np.float32(cap)):
+            raise ValueError("cap is 0 (none) or a positive number in fp32's range")
         if slopes is not None and slopes.shape != (shape.Hq,):
             raise ValueError("a slope a query head")
         if len(attn) != sd.L:
@@ -507,6 +507,8 @@ class BatchDecoder:
             raise ValueError("T is 1..%d" % L.E0_MAX_T_DECODE)
         if len(cache.descs) < sd.L or any(c.Hkv != shape.Hkv or c.D != shape.D for c in cache.descs):
             raise ValueError("the cache has other layers or heads than the attention")
+        if prefix and 2 * cache.max_blocks * cache.block_tokens > L.E0_MAX_CONTEXT:
+            raise ValueError("a prefix and a sequence of the cache's max_blocks each have more than %d positions" % L.E0_MAX_CONTEXT)
         row, back = (shape.Hq + 2 * shape.Hkv) * shape.D, shape.Hq * shape.D
         for w in attn:
             n, k = w["qkv"]["codes"].shape, w["out"]["codes"].shape
