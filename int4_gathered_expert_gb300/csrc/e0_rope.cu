@@ -23,6 +23,9 @@ namespace {
 // block, which handles many heads.
 constexpr int ROPE_WARPS = 8;
 constexpr int MOST_PAIRS = E0_MAX_ROPE_D / 2;
+// From here on eps hides what the squares of 256 values lose below fp32's normal numbers (2^-142).  With a smaller one
+// the kernel that takes elements one by one looks after them (it has the registers, and nobody's models have such an eps).
+constexpr float LEAST_EPS = 0x1p-100f;
 
 struct RopeArgs {
     const void* x;
@@ -103,8 +106,8 @@ E0_DEV void to_fp32(const Raw<TY>& r, float (&v)[8]) {
 // A head's result is P x + Q x', x' the other element of the pair, with P = w cos and Q = -+ w' sin
 // (w' the other's weight): found once for the queries' heads and once for the keys', so that
 // a head is a sum of squares and three products a pair of elements.
-// VEC: D and twice the pairs that turn are multiples of 16 and every row starts on a 16-byte
-// boundary; otherwise elements come one by one.  ADJACENT: pairs are neighbours.
+// VEC: D and twice the pairs that turn are multiples of 16, every row starts on a 16-byte
+// boundary, and a norm has an eps of LEAST_EPS or more; otherwise elements come one by one.  ADJACENT: pairs are neighbours.
 //
 // Measured (device time, GB300): 16384 rows of 36 heads of 128 bf16, three axes, norms (302 MB):
 // 59.7 us, 5.1 TB/s, 75 % of the measured copy rate, bound by instructions beside it; 64.7 with a block for
@@ -204,15 +207,25 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, VEC && TY != E0_F32 ? 3 : 2) 
                 }
             }
             if (A.norm) {
-                float s0 = 0.f, s1 = 0.f;
+                const auto squares = [&]() {
+                    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    fma_pair(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
-                    fma_pair(s0, s1, b[i], b[i + 1], b[i], b[i + 1], s0, s1);
+                    for (int i = 0; i < 8; i += 2) {
+                        fma_pair(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
+                        fma_pair(s0, s1, b[i], b[i + 1], b[i], b[i + 1], s0, s1);
+                    }
+                    float ss = mine ? s0 + s1 : 0.f;
+                    for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    return ss;
+                };
+                float ss = squares(), eps = A.eps;
+                if (!VEC && eps < LEAST_EPS) {  // the squares alone count, and they may be below fp32's normal numbers
+                    const float up = ss < 0x1p-100f ? 0x1p100f : 1.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a[i] *= up, b[i] *= up;
+                    ss = squares(), eps *= up, eps *= up;
                 }
-                float ss = mine ? s0 + s1 : 0.f;
-                for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float rstd = rsqrtf(fmaf(ss, A.inv_d, A.eps));
+                const float rstd = rsqrtf(fmaf(ss, A.inv_d, eps));
                 bad |= mine && !(ss < INFINITY);
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
@@ -292,7 +305,7 @@ int qk_rope(const void* x, int dtype, int64_t x_ld, int T, int Hq, int Hk, const
     if (a.per_token > most) a.per_token = most;
     const int sz = type_size(dtype);
     const uintptr_t bits = (uintptr_t)x | (uintptr_t)y | (uintptr_t)(x_ld * sz) | (uintptr_t)(y_ld * sz);
-    const bool vec = r->D % 16 == 0 && r->rot % 16 == 0 && !(bits & 15);
+    const bool vec = r->D % 16 == 0 && r->rot % 16 == 0 && !(bits & 15) && !(a.norm && a.eps < LEAST_EPS);
     switch (dtype) {
         case E0_F32: return launch<E0_F32>(a, vec, s);
         case E0_F16: return launch<E0_F16>(a, vec, s);

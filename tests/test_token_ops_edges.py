@@ -2,8 +2,8 @@
 import numpy as np
 import pytest
 
-from tests.test_layer_ops import BF16, DT, EPS, F16, F32, L, dev, f64  # noqa: F401
-from tests.test_token_ops import NEAR, draw, row_ref, rules_of
+from tests.test_layer_ops import BF16, DT, EPS, F16, F32, H, L, dev, f64, status  # noqa: F401
+from tests.test_token_ops import NEAR, draw, rope_of, rope_ref, row_ref, rules_of
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -82,3 +82,27 @@ def test_the_hottest_temperatures(L, temp, size):  # noqa: F811
         assert got[t] == tok and kept[t] == n
         assert abs(logp[t] - want) <= 4 * EPS * abs(want) + V * 2.0 ** -44
     assert sure >= T - 3
+
+
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 1e-38, 2.0 ** -100, 1e-12])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 80])
+def test_norms_of_the_smallest_heads(L, eps, dtype, D):  # noqa: F811
+    """Heads whose squares are below fp32's normal numbers, with an eps that does not hide them."""
+    rng = np.random.default_rng(D)
+    size = 2.0 ** np.array([0, -20, -49.5, -50, -51, -60, -66, -70, -75, -90, -110, -120, -130])  # (bf16 and fp32 alike)
+    T = len(size)
+    x = dev(rng.uniform(0.5, 1, (T, 3, D)) * rng.choice([-1, 1], (T, 3, D)) * size[:, None, None], DT[dtype])
+    x[0, 0] = 0
+    eps = float(np.float32(eps))
+    freq = (1e4 ** (-np.arange(D // 2) / (D // 2))).astype(np.float32)
+    pos = np.arange(T, dtype=np.int32)[None] * 100
+    y, st = torch.full_like(x, 7.0), status()
+    L.e0_qk_rope(x, dtype, 3 * D, T, 2, 1, rope_of(L, D, D, dev(freq), norm=True, eps=eps), dev(pos), T, y, 3 * D, st)
+    assert L.e0_read_status(st) == 0
+    want, tol = rope_ref(f64(x), 2, pos, freq, np.zeros(D // 2, int), D, False, True, None, None, eps if eps else 1e-300)
+    got = f64(y)
+    if not eps:  # 0 / 0
+        assert np.isnan(got[0, 0]).all()
+        got[0, 0] = want[0, 0] = tol[0, 0] = 0
+    assert (np.abs(got - want) <= tol + H[dtype] * np.abs(want) * 1.0001 + 2.0 ** -126).all()
