@@ -3,9 +3,9 @@ GPU against 64-bit references; tolerances as in test_attn_rules."""
 import numpy as np
 import pytest
 
-from tests.test_attn_rules import (ALIBI, Tables, check_shared, compare, rules_ref, shared, weights_of,
-                                   with_prefix)
-from tests.test_layer_ops import BF16, DT, EPS, F16, F32, L, dev, f64  # noqa: F401
+from tests.test_attn_rules import (ALIBI, Tables, check_scored, check_shared, compare, rules_ref, scored, shared,
+                                   weights_of, with_prefix)
+from tests.test_layer_ops import BF16, DT, EPS, F16, F32, L, dev, f64, filled_cache, status  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -73,3 +73,84 @@ def test_queries_before_the_first_position(L, D, dtype, P):  # noqa: F811
         want = rules_ref(f64(q[rows]), pk, pv, float(np.float32(D ** -0.5)), np.zeros(new[b]), np.ones((new[b], P), bool),
                          weight_err=werr + 32 * EPS, quantum=quantum)
         compare(f64(out[rows]), f64(lse[rows]), (*want[:3], want[3] + 32 * EPS * (1 + np.abs(want[1]))), dtype, b)
+
+
+@pytest.mark.usefixtures("room")
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("kw", [{}, dict(window=333), dict(cap=6.0, biased=True)])
+def test_prompts_behind_a_prefix(L, dtype, kw):  # noqa: F811
+    """Sequences whose own new tokens are hundreds, some of them behind cached ones."""
+    rng = np.random.default_rng(17)
+    kw = dict(kw)
+    new, held = [400, 1, 130, 0, 257], [0, 90, 300, 4, 1]
+    ctx = [n + h for n, h in zip(new, held)]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    Hq, Hkv, D, P = 4, 2, 64, 300
+    if kw.pop("biased", False):
+        kw["slopes"] = ALIBI(Hq) * 0.1
+    c, t, desc, front, table = with_prefix(L, P, ctx, 32, Hkv, D, rng)
+    q = dev(rng.standard_normal((int(cu[-1]), Hq, D)), DT[dtype])
+    out, lse, st = shared(L, desc, Hkv, front, P, table, ctx, cu, q, dtype, **kw)
+    assert st == 0
+    check_shared(c, front, P, table, ctx, cu, q, out, lse, dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("P", [0, 1, 300])
+def test_more_tiles_than_blocks_behind_a_prefix(L, D, dtype, P):  # noqa: F811
+    """So many rows that a block has several tiles: the results come together in a kernel of their own, without a window."""
+    rng = np.random.default_rng(D + P)
+    B, Hq, Hkv = 40, 32, 8
+    new = rng.integers(20, 45, B)
+    ctx = [int(x) for x in new + rng.integers(0, 30, B)]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    c, t, desc, front, table = with_prefix(L, P, ctx, 64, Hkv, D, rng)
+    q = dev(rng.standard_normal((int(cu[-1]), Hq, D)), DT[dtype])
+    Tables.room = True
+    try:
+        out, lse, st = shared(L, desc, Hkv, front, P, table, ctx, cu, q, dtype)
+    finally:
+        Tables.room = False
+    assert st == 0
+    check_shared(c, front, P, table, ctx, cu, q, out, lse, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("Hq,Hkv,D", [(64, 1, 64), (200, 1, 128), (300, 1, 64), (130, 2, 256), (513, 1, 64)])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+def test_many_heads_of_a_kv_head(L, Hq, Hkv, D, dtype, cap):  # noqa: F811
+    """Single tokens whose heads alone fill a tile, or do not divide one; cu_q may be NULL then."""
+    rng = np.random.default_rng(Hq)
+    B = 9
+    ctx = [int(x) for x in rng.integers(1, 700, B)]
+    ctx[3] = 1
+    c, t, desc, table = filled_cache(L, B, 16, Hkv, D, ctx, rng)
+    q = dev(rng.standard_normal((B, Hq, D)), DT[dtype])
+    room = np.pad(table, ((0, 0), (0, 512 - table.shape[1])), constant_values=-1)  # for 8192 positions
+    out, ls = torch.full((B + 1, Hq, D), -7.0, dtype=DT[dtype], device="cuda"), torch.full((B + 1, Hq), -7.0, device="cuda")
+    wsb = L.e0_attn_scored_workspace_size(B, Hq, Hkv, D, 1)
+    ws, st = torch.full((wsb,), 255, dtype=torch.uint8, device="cuda"), status()
+    L.e0_attn_scored(desc, dev(room), 512, dev(np.asarray(ctx, np.int32)), None, B, 1, q, dtype, Hq * D, Hq, D ** -0.5,
+                     L.AttnRules(cap), out, Hq * D, ls, ws, wsb, st)
+    assert L.e0_read_status(st) == 0
+    check_scored(c, table, ctx, np.arange(B + 1), q, out, ls, dtype, cap=cap, tiles=dtype != F32)
+
+
+@pytest.mark.usefixtures("room")
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_first_and_open_at_their_types_ends(L, dtype):  # noqa: F811
+    """Any 32-bit number may stand in first and open_len, and the largest window."""
+    rng = np.random.default_rng(23)
+    new, ctx = [70, 1, 100], [300, 40, 100]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    c, t, desc, table = filled_cache(L, 3, 16, 1, 64, ctx, rng)
+    q = dev(rng.standard_normal((int(cu[-1]), 4, 64)), DT[dtype])
+    ends = np.array([-2 ** 31, -1, 0, 1, 50, 2 ** 31 - 1, 2 ** 31 - 64, 299])
+    first = ends[rng.integers(0, len(ends), int(cu[-1]))]
+    for opens in ([-2 ** 31, 2 ** 31 - 1, 60], [2 ** 31 - 1, -1, 2 ** 30]):
+        for window in (0, 37, 2 ** 31 - 1):
+            kw = dict(first=first, opens=opens, window=window)
+            out, lse, st = scored(L, desc, 1, table, ctx, cu, q, dtype, **kw)
+            assert st == 0
+            check_scored(c, table, ctx, cu, q, out, lse, dtype, **kw)
