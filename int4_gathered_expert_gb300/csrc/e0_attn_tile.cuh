@@ -853,9 +853,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         const int op0 = OPS == 2 ? 0 : (warp - G_::SOFT) >> 2;  // 0: keys (first), 1: values
         constexpr int L = G_::LOADS, PER = D / 64;  // loads; of 64 bytes a group of 8 tokens
         constexpr uint32_t NOWHERE = 0xFFFFFFFFu;
+        constexpr int NOT_LOOKED_UP = INT_MIN;
         struct Unit {
             int at0, head, hi;
-            int id;       // lane l < KV / 16: the block of its tokens 16 l ...
+            int id;       // lane l < KV / 16: the block of its tokens 16 l ..., -1 for what is none; NOT_LOOKED_UP
             uint32_t at;  // ... and where they are, in 16 tokens; NOWHERE
             bool edge;    // some row does not see all of it: codes may be anything
         };
@@ -869,8 +870,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
             u.edge = u.at0 < J.full_lo || u.at0 + KV > J.full_hi;
             const int at = u.at0 + 16 * lane;
             u.id = -1;
-            if (lane < KV / 16 && at < J.hi && at + 16 > J.lo) u.id = A.a.table[(size_t)J.seq * A.a.max_blocks + (at >> A.a.shift)];
-            else if (lane < KV / 16) u.id = INT_MIN;  // not looked up
+            if (lane < KV / 16 && at < J.hi && at + 16 > J.lo) u.id = max(A.a.table[(size_t)J.seq * A.a.max_blocks + (at >> A.a.shift)], -1);
+            else if (lane < KV / 16) u.id = NOT_LOOKED_UP;
             if (++k == p.k1) {
                 more = pieces.next(p);
                 k = p.k0;
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) k_attn_tile(const __grid_c
         };
         // the id's bounds, its scales
         const auto look_in = [&](Unit& u, float& ks, float& vs) {
-            if (lane < KV / 16 && u.id != INT_MIN && (u.id < 0 || u.id >= A.a.n_blocks)) set_status(A.a.st, E0_ST_BAD_BLOCK);
+            if (lane < KV / 16 && u.id != NOT_LOOKED_UP && (u.id < 0 || u.id >= A.a.n_blocks)) set_status(A.a.st, E0_ST_BAD_BLOCK);
             ks = vs = 0.f;
             u.at = NOWHERE;
             if (lane < KV / 16 && u.id >= 0 && u.id < A.a.n_blocks) {

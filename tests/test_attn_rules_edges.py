@@ -154,3 +154,23 @@ def test_first_and_open_at_their_types_ends(L, dtype):  # noqa: F811
             out, lse, st = scored(L, desc, 1, table, ctx, cu, q, dtype, **kw)
             assert st == 0
             check_scored(c, table, ctx, cu, q, out, lse, dtype, **kw)
+
+
+@pytest.mark.usefixtures("room")
+@pytest.mark.parametrize("bad", [-2 ** 31, -2 ** 31 + 1, -1, 2 ** 31 - 1])
+def test_any_block_id_that_is_none(L, bad):  # noqa: F811
+    """Every 32-bit number that is no block's is reported, in a sequence's table and in a prefix'."""
+    rng = np.random.default_rng(31)
+    n, ctx, P = 90, [90], 60
+    c, t, desc, front, table = with_prefix(L, P, ctx, 16, 1, 64, rng)
+    q = dev(rng.standard_normal((n, 4, 64)), torch.float16)
+    hole = table.copy()
+    hole[0, 2] = bad
+    out, lse, st = scored(L, desc, 1, hole, ctx, [0, n], q, F16)
+    assert st == L.E0_ST_BAD_BLOCK
+    check_scored(c, np.where((hole < 0) | (hole >= c.n), -1, hole), ctx, [0, n], q, out, lse, F16)
+    hole = front.copy()
+    hole[1] = bad
+    out, lse, st = shared(L, desc, 1, hole, P, table, ctx, [0, n], q, F16)
+    assert st == L.E0_ST_BAD_BLOCK
+    check_shared(c, np.where((hole < 0) | (hole >= c.n), -1, hole), P, table, ctx, [0, n], q, out, lse, F16)
