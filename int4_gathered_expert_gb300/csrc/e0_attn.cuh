@@ -40,6 +40,7 @@ struct AttnArgs {
     const int32_t* first;  // [rows of q] or NULL: the first position that a row sees
     const int32_t* open;   // [B] or NULL: all rows see the positions below
     const int32_t* at;     // [rows of q] or NULL: rows' positions, where they see all of the context but for windows
+    const int32_t* at_least;  // with at: the least of them (not of a sequence's row: any)
     float* raw;            // fp32 [rows][Hq][D] to be written in place of out, or NULL
     int limit;             // rows of q
     float cap, inv_cap;    // in units of log2; 0: none
@@ -140,8 +141,8 @@ struct Seq {
     int low;                  // the first position that the first query sees
 };
 
-// Where a sequence has more queries than this, its beginning is not looked for among the
-// rows' first positions (the masks keep it out; long prompts have kernels of their own).
+// Where a sequence has more queries than this, its beginning is not looked for among all the
+// rows' first positions, but among those of a tile (long prompts have kernels of their own).
 constexpr int MOST_FIRST = 16;
 
 template <bool RULES>
@@ -157,7 +158,7 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
     s.low = A.window > 0 ? max(s.ctx - s.n + 1 - A.window, 0) : 0;
     if constexpr (RULES) {
-        if (A.at) s.low = 0;
+        if (A.at) s.low = A.window > 0 ? min(max(*A.at_least - A.window + 1, 0), s.ctx) : 0;
         if (A.first && s.n <= MOST_FIRST && s.n > 0) {
             int least = INT_MAX;
             for (int i = 0; i < s.n; ++i) least = min(least, A.first[s.row0 + i]);
@@ -449,7 +450,16 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
         while (u < u1) {
             j = span_at<RULES>(A, plan, first, u, u1);
             u = j.end;
-            if (j.c1 > j.c0) return true;
+            if (j.c1 <= j.c0) continue;
+            if constexpr (RULES) {
+                if (A.first && j.s.n > MOST_FIRST) {  // blocks that no row of the tile sees are not looked up
+                    int least = INT_MAX;
+                    for (int i = j.tile * ROWS / G; i <= min(j.tile * ROWS + ROWS - 1, j.s.n * G - 1) / G; ++i)
+                        least = min(least, A.first[j.s.row0 + i]);
+                    j.s.low = max(j.s.low, min(least, j.s.ctx));
+                }
+            }
+            return true;
         }
         return false;
     };

@@ -49,22 +49,22 @@ void put_rules(AttnArgs& a, const e0_attn_rules* r) {
 // ---------------------------------------------------------------- the shared prefix
 
 // For each row its position behind the prefix, and {0, rows} as the bounds of one sequence
-// of them all.  `a` is of the sequences' own tokens, `front` of the prefix.
+// of them all, then the least position.  `a` is of the sequences' own tokens, `front` of the prefix.
 constexpr int ROWS_THREADS = 1024;
 __global__ void __launch_bounds__(ROWS_THREADS) k_shared_rows(AttnArgs a, AttnArgs front, int32_t* at, int32_t* cu) {
-    __shared__ int rows;
+    __shared__ int rows, least;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) rows = 0;
+    if (threadIdx.x == 0) rows = 0, least = INT_MAX;
     for (int t = threadIdx.x; t < a.limit; t += ROWS_THREADS) at[t] = 0;
     __syncthreads();
     const int before = prefix_of(front, *front.ctx);
     for (int b = threadIdx.x >> 5; b < a.B; b += ROWS_THREADS / 32) {
         const Seq s = seq_of<true>(a, b, false);
         for (int i = lane; i < s.n; i += 32) at[s.row0 + i] = before + s.ctx - s.n + i;
-        if (lane == 0 && s.n > 0) atomicMax(&rows, s.row0 + s.n);
+        if (lane == 0 && s.n > 0) atomicMax(&rows, s.row0 + s.n), atomicMin(&least, before + s.ctx - s.n);
     }
     __syncthreads();
-    if (threadIdx.x == 0) cu[0] = 0, cu[1] = rows;
+    if (threadIdx.x == 0) cu[0] = 0, cu[1] = rows, cu[2] = least;
 }
 
 // out = (e^(l1 - m) o1 + e^(l2 - m) o2) / (e^(l1 - m) + e^(l2 - m)) of two normed results
@@ -123,7 +123,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
         return at;
     };
     int32_t* at = reinterpret_cast<int32_t*>(take((size_t)T * sizeof(int32_t)));
-    int32_t* cu2 = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+    int32_t* cu2 = reinterpret_cast<int32_t*>(take(3 * sizeof(int32_t)));
     float* o[2];
     float* l[2];
     for (int i = 0; i < 2; ++i) {
@@ -138,7 +138,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
     // the prefix, as one sequence whose queries are all rows
     AttnArgs front = args_of(c, prefix_table, prefix_blocks, prefix_len, cu2, 1, T, q, q_ld, Hq, scale, 0, out, out_ld, l[0], p, st);
     put_rules(front, rules);
-    front.limit = T, front.at = at;
+    front.limit = T, front.at = at, front.at_least = cu2 + 2;
     // what the sequences have of their own comes first: the prefix' last kernel adds it where it can
     int rc = launch_t<true>(mine, dtype, c->D, s);
     if (rc != E0_OK) return rc;

@@ -174,3 +174,32 @@ def test_any_block_id_that_is_none(L, bad):  # noqa: F811
     out, lse, st = shared(L, desc, 1, hole, P, table, ctx, [0, n], q, F16)
     assert st == L.E0_ST_BAD_BLOCK
     check_shared(c, np.where((hole < 0) | (hole >= c.n), -1, hole), P, table, ctx, [0, n], q, out, lse, F16)
+
+
+@pytest.mark.usefixtures("room")
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_blocks_that_nobody_sees_may_be_gone(L, dtype):  # noqa: F811
+    """Prefix blocks before every window, and blocks before every document: their ids are not looked at."""
+    rng = np.random.default_rng(37)
+    B, Hq, D, P, window = 40, 4, 64, 400, 100
+    new = rng.integers(1, 4, B)
+    ctx = [int(x) for x in new + rng.integers(0, 20, B)]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    c, t, desc, front, table = with_prefix(L, P, ctx, 16, 1, D, rng)
+    q = dev(rng.standard_normal((int(cu[-1]), Hq, D)), DT[dtype])
+    least = P + min(x - n for x, n in zip(ctx, new)) - window + 1
+    gone = front.copy()
+    gone[:least // 16] = -1
+    assert least // 16 > 15
+    out, lse, st = shared(L, desc, 1, gone, P, table, ctx, cu, q, dtype, window)
+    assert st == 0
+    check_shared(c, front, P, table, ctx, cu, q, out, lse, dtype, window)
+    n, ctx = 60, [500]
+    c, t, desc, table = filled_cache(L, 1, 16, 1, D, ctx, rng)
+    q = dev(rng.standard_normal((n, Hq, D)), DT[dtype])
+    first = rng.integers(300, 440, n)
+    gone = table.copy()
+    gone[0, :first.min() // 16] = -1
+    out, lse, st = scored(L, desc, 1, gone, ctx, [0, n], q, dtype, first=first)
+    assert st == 0
+    check_scored(c, table, ctx, [0, n], q, out, lse, dtype, first=first)
