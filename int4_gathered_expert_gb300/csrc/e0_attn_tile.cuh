@@ -120,9 +120,9 @@ E0_DEV int div_group(const TileArgs& A, int n) { return (int)((unsigned long lon
 
 // The range of positions that a token of a sequence sees.
 E0_DEV void range_of(const TileArgs& A, int seq, int row0, int p0, int ctx, int i, int& p, int& lo, int& hi) {
-    // (needed there alone; no distance from it passes 32 bits)
-    p = !A.a.at ? p0 + i : A.a.window > 0 || A.a.slopes ? max(A.a.at[row0 + i], -(1 << 30)) : 0;
-    hi = A.a.at ? ctx : p + 1;
+    p = !A.a.at ? p0 + i : A.a.window > 0 || A.a.slopes ? A.a.at[row0 + i] : 0;  // needed there alone
+    hi = !A.a.at ? p + 1 : p == NO_ROW ? 0 : ctx;
+    p = max(p, -(1 << 30));  // no distance from NO_ROW passes 32 bits
     if (A.a.open) hi = max(hi, A.a.open[seq]);
     hi = min(hi, ctx);
     lo = A.a.window > 0 ? max(p - A.a.window + 1, 0) : 0;

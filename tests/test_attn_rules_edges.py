@@ -194,6 +194,10 @@ def test_blocks_that_nobody_sees_may_be_gone(L, dtype):  # noqa: F811
     out, lse, st = shared(L, desc, 1, gone, P, table, ctx, cu, q, dtype, window)
     assert st == 0
     check_shared(c, front, P, table, ctx, cu, q, out, lse, dtype, window)
+    q = torch.cat([q[:7], q])  # rows of no sequence see nothing either
+    out, lse, st = shared(L, desc, 1, gone, P, table, ctx, 7 + cu, q, dtype, window)
+    assert st == 0 and (out[:7] == -7).all()
+    check_shared(c, front, P, table, ctx, 7 + cu, q, out, lse, dtype, window)
     n, ctx = 60, [500]
     c, t, desc, table = filled_cache(L, 1, 16, 1, D, ctx, rng)
     q = dev(rng.standard_normal((n, Hq, D)), DT[dtype])
