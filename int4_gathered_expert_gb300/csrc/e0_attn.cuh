@@ -145,6 +145,9 @@ struct Seq {
 // rows' first positions, but among those of a tile (long prompts have kernels of their own).
 constexpr int MOST_FIRST = 16;
 
+// `low` as the first position that is seen of ctx: where that is none of them, beyond the last piece of 16.
+E0_DEV int low_in(int ctx, int low) { return low < ctx ? low : ctx + 15; }
+
 template <bool RULES>
 E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     Seq s;
@@ -158,11 +161,11 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
     s.low = A.window > 0 ? max(s.ctx - s.n + 1 - A.window, 0) : 0;
     if constexpr (RULES) {
-        if (A.at) s.low = A.window > 0 ? min(max(*A.at_least - A.window + 1, 0), s.ctx) : 0;
+        if (A.at) s.low = A.window > 0 ? low_in(s.ctx, max(*A.at_least - A.window + 1, 0)) : 0;
         if (A.first && s.n <= MOST_FIRST && s.n > 0) {
             int least = INT_MAX;
             for (int i = 0; i < s.n; ++i) least = min(least, A.first[s.row0 + i]);
-            s.low = max(s.low, min(least, s.ctx));
+            s.low = max(s.low, low_in(s.ctx, least));
         }
     }
     s.first = s.low / A.unit;
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
                     int least = INT_MAX;
                     for (int i = j.tile * ROWS / G; i <= min(j.tile * ROWS + ROWS - 1, j.s.n * G - 1) / G; ++i)
                         least = min(least, A.first[j.s.row0 + i]);
-                    j.s.low = max(j.s.low, min(least, j.s.ctx));
+                    j.s.low = max(j.s.low, low_in(j.s.ctx, least));
                 }
             }
             return true;

@@ -207,3 +207,12 @@ def test_blocks_that_nobody_sees_may_be_gone(L, dtype):  # noqa: F811
     out, lse, st = scored(L, desc, 1, gone, ctx, [0, n], q, dtype, first=first)
     assert st == 0
     check_scored(c, table, ctx, [0, n], q, out, lse, dtype, first=first)
+    for m in (1, 3, n):  # documents that begin behind everything there is
+        first = np.full(m, 501)
+        out, lse, st = scored(L, desc, 1, np.full_like(table, -1), ctx, [0, m], q[:m], dtype, first=first)
+        assert st == 0 and (out[:m] == 0).all() and torch.isneginf(lse[:m]).all()
+    # windows that end before their prefix' last block does
+    c, t, desc, front, table = with_prefix(L, 390, [20], 16, 1, D, rng)
+    out, lse, st = shared(L, desc, 1, np.full_like(front, -1), 390, table, [20], [0, 1], q[:1], dtype, 20)
+    assert st == 0
+    check_shared(c, front, 390, table, [20], [0, 1], q[:1], out, lse, dtype, 20)
