@@ -40,7 +40,7 @@ struct AttnArgs {
     const int32_t* first;  // [rows of q] or NULL: the first position that a row sees
     const int32_t* open;   // [B] or NULL: all rows see the positions below
     const int32_t* at;     // [rows of q] or NULL: rows' positions, where they see all of the context but for windows
-    const int32_t* at_least;  // with at: the least of them (not of a sequence's row: any)
+    const int32_t* at_low;    // with at and a window: the first position that one of the rows sees
     float* raw;            // fp32 [rows][Hq][D] to be written in place of out, or NULL
     int limit;             // rows of q
     float cap, inv_cap;    // in units of log2; 0: none
@@ -161,7 +161,7 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     if (bad && tell) set_status(A.st, E0_ST_BAD_LENGTH);
     s.low = A.window > 0 ? max(s.ctx - s.n + 1 - A.window, 0) : 0;
     if constexpr (RULES) {
-        if (A.at) s.low = A.window > 0 ? low_in(s.ctx, max(*A.at_least - A.window + 1, 0)) : 0;
+        if (A.at) s.low = A.at_low ? *A.at_low : 0;
         if (A.first && s.n <= MOST_FIRST && s.n > 0) {
             int least = INT_MAX;
             for (int i = 0; i < s.n; ++i) least = min(least, A.first[s.row0 + i]);
@@ -176,11 +176,11 @@ E0_DEV Seq seq_of(const AttnArgs& A, int b, bool tell) {
     return s;
 }
 
-// The tokens of a prefix of length `given`: none where that is negative or more than its table (of `a`, the prefix')
+// The tokens of a prefix of length `given`: none where that is negative or more than its table of max_blocks
 // has room for.  Rows' positions are counted from it, too: from 2^31 - 1 they would pass 32 bits, and
 // with them a window's first position.
-E0_DEV int prefix_of(const AttnArgs& a, int given) {
-    return given < 0 || (long long)given > ((long long)a.max_blocks << a.shift) ? 0 : given;
+E0_DEV int prefix_of(int given, int max_blocks, int shift) {
+    return given < 0 || (long long)given > ((long long)max_blocks << shift) ? 0 : given;
 }
 
 // A schedule longer than this is not run (it would read for seconds).
@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(AT_WARPS * 32) k_attn(AttnArgs A) {
             if (j.c1 <= j.c0) continue;
             if constexpr (RULES) {
                 if (A.first && j.s.n > MOST_FIRST) {  // blocks that no row of the tile sees are not looked up
-                    int least = INT_MAX;
-                    for (int i = j.tile * ROWS / G; i <= min(j.tile * ROWS + ROWS - 1, j.s.n * G - 1) / G; ++i)
-                        least = min(least, A.first[j.s.row0 + i]);
+                    const int i = j.tile * ROWS / G + lane;  // of its tokens, ROWS at most
+                    const bool in = i < j.s.n && i * G < (j.tile + 1) * ROWS;
+                    const int least = __reduce_min_sync(0xffffffffu, in ? A.first[j.s.row0 + i] : INT_MAX);
                     j.s.low = max(j.s.low, low_in(j.s.ctx, least));
                 }
             }

@@ -49,22 +49,30 @@ void put_rules(AttnArgs& a, const e0_attn_rules* r) {
 // ---------------------------------------------------------------- the shared prefix
 
 // For each row its position behind the prefix, and {0, rows} as the bounds of one sequence
-// of them all, then the least position.  `a` is of the sequences' own tokens, `front` of the prefix.
+// of them all; under a window then the first position that one of them sees.  `a` is of the sequences' own tokens,
+// prefix_blocks of the prefix.
 constexpr int ROWS_THREADS = 1024;
-__global__ void __launch_bounds__(ROWS_THREADS) k_shared_rows(AttnArgs a, AttnArgs front, int32_t* at, int32_t* cu) {
+__global__ void __launch_bounds__(ROWS_THREADS) k_shared_rows(AttnArgs a, const int32_t* prefix_len, int prefix_blocks, int32_t* at,
+                                                              int32_t* cu) {
     __shared__ int rows, least;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) rows = 0, least = INT_MAX;
     for (int t = threadIdx.x; t < a.limit; t += ROWS_THREADS) at[t] = 0;
     __syncthreads();
-    const int before = prefix_of(front, *front.ctx);
+    const int before = prefix_of(*prefix_len, prefix_blocks, a.shift);
     for (int b = threadIdx.x >> 5; b < a.B; b += ROWS_THREADS / 32) {
         const Seq s = seq_of<true>(a, b, false);
         for (int i = lane; i < s.n; i += 32) at[s.row0 + i] = before + s.ctx - s.n + i;
-        if (lane == 0 && s.n > 0) atomicMax(&rows, s.row0 + s.n), atomicMin(&least, before + s.ctx - s.n);
+        if (lane == 0 && s.n > 0) {
+            atomicMax(&rows, s.row0 + s.n);
+            if (a.window > 0) atomicMin(&least, before + s.ctx - s.n);
+        }
     }
     __syncthreads();
-    if (threadIdx.x == 0) cu[0] = 0, cu[1] = rows, cu[2] = least;
+    if (threadIdx.x == 0) {
+        cu[0] = 0, cu[1] = rows;
+        if (a.window > 0) cu[2] = low_in(before, max(least - a.window + 1, 0));
+    }
 }
 
 // out = (e^(l1 - m) o1 + e^(l2 - m) o2) / (e^(l1 - m) + e^(l2 - m)) of two normed results
@@ -138,7 +146,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
     // the prefix, as one sequence whose queries are all rows
     AttnArgs front = args_of(c, prefix_table, prefix_blocks, prefix_len, cu2, 1, T, q, q_ld, Hq, scale, 0, out, out_ld, l[0], p, st);
     put_rules(front, rules);
-    front.limit = T, front.at = at, front.at_least = cu2 + 2;
+    front.limit = T, front.at = at, front.at_low = front.window > 0 ? cu2 + 2 : nullptr;
     // what the sequences have of their own comes first: the prefix' last kernel adds it where it can
     int rc = launch_t<true>(mine, dtype, c->D, s);
     if (rc != E0_OK) return rc;
@@ -151,7 +159,7 @@ int attn_shared(const e0_kv_cache* c, const int32_t* prefix_table, int prefix_bl
         front.raw = o[0];
         rc = attn_tile(front, &prefix, dtype, tiles, s);
     } else {
-        k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, front, at, cu2);
+        k_shared_rows<<<1, ROWS_THREADS, 0, s>>>(mine, prefix_len, prefix_blocks, at, cu2);
         if (cudaGetLastError() != cudaSuccess) return E0_ERR_CUDA;
         front.raw = o[0];
         rc = launch_t<true>(front, dtype, c->D, s);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
     if (A.own.B > 0) {
         for (int t = tid; t < A.own.limit; t += PLAN_THREADS) A.own_at[t] = NO_ROW;
         __syncthreads();
-        const int before = prefix_of(A.a, *A.a.ctx);
+        const int before = prefix_of(*A.a.ctx, A.a.max_blocks, A.a.shift);
         for (int b = warp; b < A.own.B; b += PLAN_THREADS / 32) {
             const Seq s = seq_of<true>(A.own, b, false);
             for (int i = lane; i < s.n; i += 32) A.own_at[s.row0 + i] = before + s.ctx - s.n + i;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tile_plan(TileArgs A) {
         if (A.own.B == 0) return seq_of<true>(A.a, b, tell);
         Seq s;
         const int given = *A.a.ctx;
-        s.row0 = 0, s.n = all_rows, s.ctx = prefix_of(A.a, given);
+        s.row0 = 0, s.n = all_rows, s.ctx = prefix_of(given, A.a.max_blocks, A.a.shift);
         if (s.ctx != given && tell && tid == 0) set_status(A.a.st, E0_ST_BAD_LENGTH);
         return s;
     };
