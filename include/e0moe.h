@@ -752,8 +752,10 @@ size_t e0_attn_scored_workspace_size(int B, int Hq, int Hkv, int D, int max_q);
  * tensor cores, the weights in 22 bits.  What max_q, max_blocks and rows allow beyond the lengths thus has a
  * say in an output's last bits (fp32 sums in another order; on the path for few rows bf16 outputs of more than
  * 8 rows of a KV head have weights of 11 bits, as e0_attn_decode's).  All else takes the path
- * for few rows (every 8 of a KV head, 16 of bf16, read the sequence once more).  rules NULL: none.  Errors as
- * e0_attn_decode's; cap negative or not finite, window < 0, rows < 0, or a pointer of the rules that
+ * for few rows (every 8 of a KV head, 16 of bf16, read the sequence once more).  Waits inside the tiles give
+ * up after 2 s with E0_ST_TIMEOUT, which many rows that see more than 2^25 positions each may come to.  Blocks
+ * that no query sees, before all windows and documents, may be gone: their ids are not looked at.  rules NULL:
+ * none.  Errors as e0_attn_decode's; cap negative or not finite, window < 0, rows < 0, or a pointer of the rules that
  * is not aligned to 4 bytes -> E0_ERR_ARG. */
 int e0_attn_scored(const e0_kv_cache* cache, const int32_t* block_table, int max_blocks, const int32_t* ctx_len,
                    const int32_t* cu_q, int B, int max_q, const void* q, int dtype, int64_t q_ld, int Hq, float scale,
@@ -765,14 +767,17 @@ size_t e0_attn_shared_workspace_size(int B, int T, int Hq, int Hkv, int D, int m
 
 /* Attention of a batch whose sequences begin alike: positions 0 .. P-1, P = *prefix_len
  * (device), are tokens that all of them share, in the blocks prefix_table[0 ..
- * prefix_blocks-1] (device) of the same cache, and are read once for the batch, not once a
- * sequence.  block_table, ctx_len and cu_q are as e0_attn_decode's and say what each
+ * prefix_blocks-1] (device) of the same cache, and are read for all rows together, not for each
+ * sequence: in tiles once for every 128 or 256 rows of a KV head (as e0_attn_scored's, where rows and
+ * prefix_blocks leave room for a million scores), otherwise once for every 8, or 16 in bf16 (fp32
+ * queries with 8 heads and more of a KV head thus gain nothing by it).  block_table, ctx_len and cu_q are as e0_attn_decode's and say what each
  * sequence has of its own, from position P on (ctx_len without the prefix; own tokens start in a
  * block of their own, whatever P is); cu_q gives at most T rows.  A query sees the
  * prefix and its own sequence up to itself, within the window.  rules: cap, window and slopes
  * as e0_attn_scored's, or NULL; first and open_len -> E0_ERR_UNSUPPORTED.  A P that is
  * negative or needs more than prefix_blocks blocks raises E0_ST_BAD_LENGTH, and nobody sees the
- * prefix; a cu_q that gives more than T rows raises it, and that sequence's rows are left as they
+ * prefix; a query of a sequence with fewer tokens than queries, or of a bad length, sees what the window
+ * leaves of it; a cu_q that gives more than T rows raises it, and that sequence's rows are left as they
  * were.  All else is e0_attn_scored's.  Errors: as e0_attn_scored's, and NULL prefix_table or
  * prefix_len -> E0_ERR_NULL; T < 1 or prefix_blocks < 1 -> E0_ERR_ARG; (prefix_blocks +
  * max_blocks) * block_tokens > E0_MAX_CONTEXT, T * Hq > 2^30 -> E0_ERR_UNSUPPORTED. */

@@ -34,13 +34,13 @@ namespace {
 // Products are issued by one thread and done in its order: a unit's first products go where the
 // weights of the unit before were as soon as that one's second products have been issued.
 //
-// Measured (device time, GB300; heads of 128, 32 on 4, bf16): 4096 tokens of five documents 113 us, 307 TFLOP/s of
-// what is seen; the same tokens as one document 243 us, 564 TFLOP/s.  What bounds it, in cycles a unit of
-// 128 positions and 256 rows (4.2 thousand): a half's exponentials, 2.7 thousand of a thread's own
-// instructions (0.8 for scores and maximum, 1 for weights and their sum), behind which its products, 0.8, have to wait,
-// for there is room for one S a half; the operands' warps, 3.6 thousand busy, are next.
-// The products by themselves would be 1.5 thousand (shared memory's rate).  Around the units a piece of a
-// job costs 8 to 10 thousand, the schedule 6 us, the join 8.
+// Measured (device time, GB300; heads of 128, 32 on 4, bf16): 4096 tokens of five documents 126 us, 276 TFLOP/s of
+// what is seen; the same tokens as one document 229 us, 600 TFLOP/s.  What bounds it, by the clock in a copy, in cycles
+// a unit of 128 positions and 256 rows (5.9 thousand with one document, 6.8 with five): a half's softmax, 3.4 thousand
+// of a thread's own instructions and their latencies, behind which its products have to wait, 2.5 thousand (3.2 with
+// five), for there is room for one S a half.  The products by themselves would be 3.1 thousand, three of 1024 (S, O
+// by the weights, O by their rests) at 8192 a cycle.  The end of a piece of a job costs 5 to 6 thousand, its start
+// as much; of the documents' 126 us the schedule takes about 6 beside its launch, the join 8.
 template <int D>
 struct Geo {
     static constexpr int HALVES = D == 256 ? 1 : 2;
@@ -56,7 +56,7 @@ struct Geo {
     // With heads of 256, whose softmax has four warps, there is room for eight converting ones (20
     // times two queries over 6000 positions: 56 us with four, 52 with eight); with others it would be
     // 640 threads of 96, and softmax's and the operands' registers in local memory (4096 tokens of
-    // documents: 113 us with four, 126 with eight).
+    // documents, weights without rests: 113 us with four, 126 with eight).
     static constexpr int SOFT_REGS = HALVES == 2 ? 168 : 208, TURN_REGS = HALVES == 2 ? 112 : 88, OTHER_REGS = HALVES == 2 ? 64 : 128;
     static_assert(32 * (SOFT * SOFT_REGS + TURN * TURN_REGS + 4 * OTHER_REGS) == THREADS * 128 && THREADS == 512, "all of them come");
     static constexpr int O_COL = 2 * KV;  // tensor memory: two S, then the halves' O
@@ -71,7 +71,7 @@ struct Geo {
 // steps for is 2^-28 of that.
 constexpr float TILE_LIFT = 3.f, TILE_SLACK = 12.f;
 // What a job costs beside its units (its rows of Q, its result, two halves that start and
-// stop), in units: 8 to 10 thousand cycles of four to five.  Dealt out by units alone the blocks with
+// stop), in units: 10 to 12 thousand cycles of about six.  Dealt out by units alone the blocks with
 // the first rows of prompts, a unit a job, were twice as long as the others.
 constexpr uint32_t TILE_JOB_COST = 2;
 constexpr uint32_t TILE_TMEM = 512;

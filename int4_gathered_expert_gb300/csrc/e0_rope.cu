@@ -107,10 +107,12 @@ E0_DEV void to_fp32(const Raw<TY>& r, float (&v)[8]) {
 // (w' the other's weight): found once for the queries' heads and once for the keys', so that
 // a head is a sum of squares and three products a pair of elements.
 // VEC: D and twice the pairs that turn are multiples of 16, every row starts on a 16-byte
-// boundary, and a norm has an eps of LEAST_EPS or more; otherwise elements come one by one.  ADJACENT: pairs are neighbours.
+// boundary, and a norm has an eps of LEAST_EPS or more; otherwise elements come one by one.
+// ADJACENT: pairs are neighbours.
 //
 // Measured (device time, GB300): 16384 rows of 36 heads of 128 bf16, three axes, norms (302 MB):
-// 59.7 us, 5.1 TB/s, 75 % of the measured copy rate, bound by instructions beside it; 64.7 with a block for
+// 59.1 us, 5.1 TB/s, 75 % of the measured copy rate; what is missing are loads in flight, 24 warps an SM with one head
+// ahead each (2.7 of a scheduler's 5.6 warps wait for memory, no pipe is half busy); 64.7 with a block for
 // every eight rows, each making the table of turns and the last wave half empty, 87.7 with every lane
 // finding its sines, weights and rotation in turn and one value an instruction.  8 rows of 18
 // heads of 256: 3.9 us, a launch and two loads behind one another.

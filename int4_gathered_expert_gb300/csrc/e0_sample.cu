@@ -27,13 +27,14 @@ namespace {
 // 64 rows of 131071 fp32 logits, top-p 0.9: 85 us, two turns of 38 clusters of 13 us for the
 // histogram (three additions in shared memory a token), 5 for the reading (of the 5 us in which
 // memory alone could be read), 12 for meetings and searches, 8 for the draw.  Read from the L2
-// cache in each pass instead of held, all rows would run at once, and take 98 us.
+// cache in each pass instead of held, all rows would run at once, and take 98 us.  (Up to 149888
+// tokens an SM has room for two blocks, beyond for one: 24 rows of 151936, not truncated, 23 us in two turns.)
 //
 // A draw over V tokens has V borders, and an error in the sums moves all of them: with fp32
 // exponentials one row in a hundred would get another token than the definition gives.
 // So a weight 2^-y, y = (largest - logit) log2 e / temperature, is a 64-bit integer, 2^44
-// times its value, good to 2^-28 of itself or to one, whichever is more: y comes from a difference and a product that
-// carry their rounding errors along (Dekker, Numer. Math. 18, 1971), its power of two from a
+// times its value, good to 2^-28 of itself or to one, whichever is more: y comes from a difference and
+// a product that carry their rounding errors along (Dekker, Numer. Math. 18, 1971), its power of two from a
 // table of 128 and the series of what is left.  Sums of integers are exact in any order, so
 // equal calls give equal tokens.  Weights below 2^-44 of the largest count as nothing.
 constexpr int SM_THREADS = 512, SM_WARPS = SM_THREADS / 32;

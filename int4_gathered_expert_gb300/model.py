@@ -488,10 +488,11 @@ class BatchDecoder:
     edit: what a model does to queries and keys before they meet (rotary embeddings,
     norms), or None: called on the step's stream with the layer, qkv fp16 [T, (Hq + 2
     Hkv) D] (queries, keys, values; to be changed in place) and the rows' positions
-    int32 [T], -1 after the last new token (QkRope is one).
+    int32 [T], -1 after the last new token (QkRope is one; with several axes, a function
+    that adds the other axes' positions and calls it).
     cap, slopes: scores are capped, or lose slopes[head] a token of distance.  prefix: the
-    sequences stand behind the cache's prefix (KvCacheDev.share; positions count it).
-    All of a step's work is on one stream and
+    sequences stand behind the cache's prefix (KvCacheDev.share; positions count it), which
+    decoders without it do not see.  All of a step's work is on one stream and
     allocates nothing but what edit does, so a step can be captured into a CUDA graph."""
 
     def __init__(self, sd: StackDev, attn: List[dict], shape, cache: KvCacheDev, T: int, device="cuda",
