@@ -6,8 +6,8 @@ namespace e0 {
 namespace {
 
 // Whether B times max_q queries of D can go through the tensor cores' tiles: enough rows of a KV head to
-// fill a part of one (their products in fp16 are not enough for fp32 outputs), and a list of the
-// tiles that might be that takes 256 MB at most.
+// fill a part of one (they hold one fp16 operand of Q, and fp32 queries need their rests, too), and a list
+// of the tiles that might be that takes 256 MB at most.
 bool has_tiles(int dtype, int64_t B, int64_t max_q, int64_t G, int D) {
     const int64_t rows = max_q * G, tile = D == 256 ? 128 : 256;
     return dtype != E0_F32 && rows >= 64 && B * ((rows + tile - 1) / tile) <= 1 << 22;
